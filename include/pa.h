@@ -500,6 +500,198 @@ pa_status pa_gather_kv(const void* k_blocks, const void* v_blocks, void* k_out, 
                        int64_t num_blocks, int32_t max_blocks_per_seq, pa_dtype kv_dtype,
                        cudaStream_t stream);
 
+/* ---- speculative decoding over the cache --------------------------------------------------
+ *
+ * A drafted step of a sequence: a tree of candidate tokens is cached behind its context
+ * (pa_rope_and_cache), the tree attends to the context and to each node's ancestors
+ * (pa_tree_attention), and the accepted path's rows are moved together (pa_tree_commit).  The
+ * pages of forked, growing and ended sequences are kept by pa_fork_sequences, pa_grow_sequences
+ * and pa_free_sequences, whose block copies pa_copy_blocks makes in every layer's pools.
+ */
+
+/* Long-context scalings of the rotary frequencies (pa_rope_frequencies). */
+enum {
+  PA_ROPE_PLAIN = 0,  /* f_i = base^(-2 i / rotary_dim) */
+  PA_ROPE_LINEAR = 1, /* f_i / factor */
+  PA_ROPE_NTK = 2,    /* base times factor^(rotary_dim / (rotary_dim - 2)) */
+  PA_ROPE_YARN = 3,   /* f_i / factor for the slow pairs, f_i for the fast ones, a ramp over the
+                         pair index between those that turn beta_slow and beta_fast times over
+                         original_max_position; attention factor 0.1 ln(factor) + 1 */
+  PA_ROPE_BANDS = 4   /* the same two ends, with a ramp over the turns f_i * original_max_position
+                         / (2 pi) between low_freq_factor and high_freq_factor */
+};
+typedef struct {
+  int32_t kind;   /* PA_ROPE_* */
+  double factor;  /* >= 1; every kind but PA_ROPE_PLAIN */
+  double original_max_position;              /* PA_ROPE_YARN, PA_ROPE_BANDS */
+  double beta_fast, beta_slow;               /* PA_ROPE_YARN, usually 32 and 1 */
+  double low_freq_factor, high_freq_factor;  /* PA_ROPE_BANDS, usually 1 and 4 */
+} pa_rope_scaling;
+
+/*
+ * pa_rope_frequencies -- the rotary frequencies (radians per position) of the rotary_dim / 2
+ * pairs, in fp64, for pa_rope_and_cache.  A host function: inv_freq and attn_factor (may be
+ * NULL) are HOST pointers, scaling (NULL: plain) too.  rotary_dim positive and even (PA_ESHAPE),
+ * base > 1, factor >= 1, original_max_position > 0, beta_fast > beta_slow > 0, high_freq_factor >
+ * low_freq_factor > 0 where the kind uses them (PA_EINVAL).
+ */
+pa_status pa_rope_frequencies(int32_t rotary_dim, double base, const pa_rope_scaling* scaling,
+                              double* inv_freq, float* attn_factor);
+
+/*
+ * pa_rope_and_cache -- rotary positions for the new tokens' queries and keys, and the scatter of
+ * their keys and values into the pools, in one pass.
+ *   q, q_out  [num_tokens, num_heads, head_dim] of src_dtype (both NULL: keys and values only);
+ *             k, v [num_tokens, num_kv_heads, head_dim] of src_dtype.  Consecutive tokens lie
+ *             *_stride elements apart (at least a token's row; e.g. views of one fused q/k/v
+ *             product), a token's heads are contiguous.  q_out may be q with the same stride;
+ *             otherwise the outputs overlap no input.
+ *   positions [num_tokens] any int32, inv_freq [rotary_dim / 2] fp64 DEVICE (finite radians per
+ *             position).  Pair i of a head's first rotary_dim elements, (x_i, x_(i + rotary_dim/2))
+ *             or (x_2i, x_(2i+1)) when interleaved, becomes
+ *               attn_factor * (a cos t - b sin t, a sin t + b cos t),  t = position * inv_freq[i];
+ *             elements from rotary_dim on are unchanged.  The angle is exact to 2^-25 half turns
+ *             at any position (fp32 products lose it at far positions); arithmetic in fp32.
+ *   pools     as in pa_reshape_and_cache_ex: K stored as rotated value / scale, V as value / scale,
+ *             rounded once to kv_dtype (e4m3 saturates), into row slot_mapping[t].  The scales are
+ *             k_scale / v_scale, or k_scales / v_scales [num_kv_heads] DEVICE (NULL: the scalars;
+ *             given, the scalar has to be 1).  Every slot is checked before anything is written
+ *             (q_out included); a slot outside the pool, or a per-head scale that is not finite
+ *             and positive, records PA_EINVAL.  Duplicate slots are undefined.
+ * rotary_dim even, at most head_dim (PA_ESHAPE) and 256 (PA_EUNSUPPORTED); interleaved pairs need
+ * an even head_dim (PA_EUNSUPPORTED).
+ */
+pa_status pa_rope_and_cache(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                            const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            void* k_blocks, void* v_blocks, const int32_t* positions,
+                            const int32_t* slot_mapping, const double* inv_freq,
+                            int32_t rotary_dim, int32_t interleaved, float attn_factor,
+                            int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                            int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                            pa_dtype src_dtype, pa_dtype kv_dtype, float k_scale, float v_scale,
+                            const float* k_scales, const float* v_scales, cudaStream_t stream);
+
+/* pa_tree_attention_workspace_size -- bytes of device workspace pa_tree_attention needs for these
+ * sizes (the plan of the call and the partial states of split items). */
+size_t pa_tree_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads,
+                                        int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t max_blocks_per_seq, int32_t block_size);
+
+/*
+ * pa_tree_attention -- attention of trees of drafted tokens over the paged cache.  Sequence s has
+ * n = query_start_loc[s + 1] - query_start_loc[s] nodes, cached as its LAST n positions: node i
+ * (token query_start_loc[s] + i) lies at position seq_lens[s] - n + i of the cache, behind a
+ * context of seq_lens[s] - n positions.  positions[t] is the token's logical position (its
+ * context length plus its depth, usually).  Token t of sequence s attends to
+ *     every context position j, and every node i whose bit (i % 32) of
+ *     tree_mask[t * mask_words + i / 32] is set (its ancestors and itself),
+ * of which a sliding_window w > 0 leaves the keys with logical position > positions[t] - w (j for
+ * a context position, positions[] of a node).  out = softmax(scale * q . K) V over those keys; a
+ * token that sees no key gets 0 and lse -inf.  Bits of nodes >= n are ignored.  positions are
+ * read only when there is a window.
+ * Types, sinks, lse, k_scale / v_scale and k_scales / v_scales as in pa_varlen_forward_ex and
+ * pa_varlen_forward_per_head (a per-head array needs a scalar of 1); kv_dtype PA_FP8_E4M3 reads
+ * the codes' values times the scales.  Every cached V row of the sequences has to be finite (a
+ * masked node's V enters the products with weight zero); K rows of masked keys, and rows at or
+ * past seq_lens[s], may hold anything.
+ * Validation, on the device before anything is written: query_start_loc starts at 0, never
+ * decreases and ends at num_tokens; for a sequence with nodes n <= 32 * mask_words, n <=
+ * seq_lens[s], its table covers seq_lens[s] positions with ids in [0, num_blocks), positions >= 0
+ * when there is a window; per-head scales finite and positive.  Failures record PA_EINVAL and
+ * leave out and lse untouched.  mask_words > 64 is PA_EUNSUPPORTED.  A call without tokens does
+ * nothing.
+ * workspace: pa_tree_attention_workspace_size(...) bytes, 256-byte aligned, scratch of the caller
+ * that calls which overlap on the device must not share.  The results of a call depend on its
+ * inputs alone (no atomics on values); how a context is split, and so the last bits of a row,
+ * depend on the lengths of the whole batch.
+ */
+pa_status pa_tree_attention(const void* q, const void* k_blocks, const void* v_blocks, void* out,
+                            const int32_t* query_start_loc, const int32_t* seq_lens,
+                            const int32_t* positions, const int32_t* tree_mask,
+                            const int32_t* block_tables, int32_t num_seqs, int64_t num_tokens,
+                            int32_t mask_words, int32_t num_heads, int32_t num_kv_heads,
+                            int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                            int32_t max_blocks_per_seq, pa_dtype q_dtype, pa_dtype kv_dtype,
+                            float scale, int32_t sliding_window, const float* sinks, float* lse,
+                            float k_scale, float v_scale, const float* k_scales,
+                            const float* v_scales, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+
+/*
+ * pa_tree_commit -- keep the accepted path of each sequence's tree: position context_lens[s] + i
+ * gets the K and V rows of position context_lens[s] + accepted[s * max_accepted + i], for i <
+ * num_accepted[s], as if all rows were read before any is written.  Bit-exact copies (pools of any
+ * kv_dtype; with per-block dequantisation factors only where the blocks' factors agree).  The
+ * accepted nodes of a sequence strictly increase (a path's nodes do, parents being numbered before
+ * their children).  0 <= num_accepted[s] <= max_accepted, nodes >= 0 and strictly increasing, the
+ * positions inside the table and their ids in [0, num_blocks): otherwise PA_EINVAL is recorded and
+ * nothing is written.  Entries past num_accepted[s] are ignored.  A block that is written belongs
+ * to one sequence only (pa_fork_sequences gives every child its own last block).
+ */
+pa_status pa_tree_commit(void* k_blocks, void* v_blocks, const int32_t* block_tables,
+                         const int32_t* context_lens, const int32_t* accepted,
+                         const int32_t* num_accepted, int32_t num_seqs, int32_t max_accepted,
+                         int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                         int64_t num_blocks, int32_t max_blocks_per_seq, pa_dtype kv_dtype,
+                         cudaStream_t stream);
+
+/*
+ * pa_copy_blocks -- copy whole pool blocks: for every pair (src, dst) of block_pairs
+ * [num_pairs, 2] (DEVICE, 8-byte aligned), block dst of each pool gets block src; (-1, -1) pairs
+ * are skipped.  A source may repeat; destinations are distinct and no destination is a source:
+ * this and the ids' range are checked before anything is written (PA_EINVAL recorded).  v_blocks
+ * may be NULL.  Per-block dequantisation factors [num_blocks, num_kv_heads] move with the same
+ * call, as f32 pools of block size 1 and head size 1.  More than 256 pairs need num_blocks <=
+ * 2^23 (PA_EUNSUPPORTED).
+ */
+pa_status pa_copy_blocks(void* k_blocks, void* v_blocks, const int32_t* block_pairs,
+                         int64_t num_pairs, int32_t num_kv_heads, int32_t head_dim,
+                         int32_t block_size, int64_t num_blocks, pa_dtype kv_dtype,
+                         cudaStream_t stream);
+
+/*
+ * Page bookkeeping, on the device and in the stream's order:
+ *   block_tables [num_rows, max_blocks_per_seq], seq_lens [num_rows]: row r's first
+ *                ceil(seq_lens[r] / block_size) entries are the blocks it holds;
+ *   ref_counts   [num_blocks]: rows that hold each block;
+ *   free_list    [num_blocks], free_count [1]: the ids of the blocks that nobody holds are
+ *                free_list[0 .. *free_count - 1], each once (the caller sets this up).
+ * Blocks are taken from the end of the free list.  Each call checks everything before it writes:
+ * a row outside [0, num_rows), a written row listed twice, a length that is negative or beyond
+ * the table, an id outside the pool, a held block without a reference, a free block with one, too
+ * few free blocks, or a count outside [0, num_blocks] records PA_EINVAL and leaves every array as
+ * it was.  num_rows <= 65536, num_blocks <= 2^23 and num_rows * max_blocks_per_seq < 2^31, else
+ * PA_EUNSUPPORTED.  Calls on the same arrays must not overlap on the device.
+ *
+ * pa_fork_sequences -- fork f makes row children[f] a copy of row parents[f]: whole blocks are
+ * shared (their counts rise by one), a partly filled last block is replaced by a new one, for
+ * which block_pairs[f] = (parent's block, new block); (-1, -1) when there is none.  Forks take
+ * their blocks in list order.  A row may be the parent of several forks, but children are
+ * distinct and none is a parent; what a child's row held before is forgotten, not freed.  Give
+ * block_pairs [num_forks, 2] to pa_copy_blocks for every layer's pools.
+ */
+pa_status pa_fork_sequences(int32_t* block_tables, int32_t* seq_lens, const int32_t* parents,
+                            const int32_t* children, int32_t num_forks, int32_t num_rows,
+                            int32_t max_blocks_per_seq, int32_t block_size, int32_t* ref_counts,
+                            int32_t* free_list, int32_t* free_count, int64_t num_blocks,
+                            int32_t* block_pairs, cudaStream_t stream);
+
+/* pa_grow_sequences -- lengthen row sequences[i] to new_lens[i] >= its length, taking the blocks
+ * this needs (in list order, ascending position) and writing them behind the row's blocks. */
+pa_status pa_grow_sequences(int32_t* block_tables, int32_t* seq_lens, const int32_t* sequences,
+                            const int32_t* new_lens, int32_t num_sequences, int32_t num_rows,
+                            int32_t max_blocks_per_seq, int32_t block_size, int32_t* ref_counts,
+                            int32_t* free_list, int32_t* free_count, int64_t num_blocks,
+                            cudaStream_t stream);
+
+/* pa_free_sequences -- end the rows in `sequences` (distinct): every block they hold loses a
+ * reference for each row that holds it, blocks without references are appended to the free list
+ * in ascending order, and the rows' lengths become 0 (their table entries stay). */
+pa_status pa_free_sequences(int32_t* block_tables, int32_t* seq_lens, const int32_t* sequences,
+                            int32_t num_sequences, int32_t num_rows, int32_t max_blocks_per_seq,
+                            int32_t block_size, int32_t* ref_counts, int32_t* free_list,
+                            int32_t* free_count, int64_t num_blocks, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

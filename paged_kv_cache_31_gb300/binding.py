@@ -89,6 +89,24 @@ _SIGS = {
                               _vp], ctypes.c_int),
     "pa_gather_kv": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _i64, _i32,
                       ctypes.c_int, _vp], ctypes.c_int),
+    "pa_rope_frequencies": ([_i32, ctypes.c_double, _vp, _vp, _vp], ctypes.c_int),
+    "pa_rope_and_cache": ([_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
+                           _i32, _i32, _f32, _i64, _i32, _i32, _i32, _i32, _i64, ctypes.c_int,
+                           ctypes.c_int, _f32, _f32, _vp, _vp, _vp], ctypes.c_int),
+    "pa_tree_attention_workspace_size": ([_i32, _i64, _i32, _i32, _i32, _i32, _i32], _sz),
+    "pa_tree_attention": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32,
+                           _i32, _i32, _i32, _i64, _i32, ctypes.c_int, ctypes.c_int, _f32, _i32,
+                           _vp, _vp, _f32, _f32, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "pa_tree_commit": ([_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i64, _i32,
+                        ctypes.c_int, _vp], ctypes.c_int),
+    "pa_copy_blocks": ([_vp, _vp, _vp, _i64, _i32, _i32, _i32, _i64, ctypes.c_int, _vp],
+                       ctypes.c_int),
+    "pa_fork_sequences": ([_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _vp,
+                           _vp], ctypes.c_int),
+    "pa_grow_sequences": ([_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _vp],
+                          ctypes.c_int),
+    "pa_free_sequences": ([_vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _vp],
+                          ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -503,3 +521,240 @@ def pa_gather_kv(k_blocks, v_blocks, k_out, v_out, cu_seq_lens, block_tables, se
                              _p(seq_starts), _p(block_tables), cu_seq_lens.numel() - 1,
                              k_out.shape[0], Hkv, D, bs, NB, block_tables.shape[1],
                              _DT[k_blocks.dtype], _stream(stream)), "pa_gather_kv")
+
+
+# ---- speculative decoding over the cache ----------------------------------------------------
+
+PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_NTK, PA_ROPE_YARN, PA_ROPE_BANDS = range(5)
+_ROPE_KINDS = {None: PA_ROPE_PLAIN, "linear": PA_ROPE_LINEAR, "ntk": PA_ROPE_NTK,
+               "yarn": PA_ROPE_YARN, "bands": PA_ROPE_BANDS}
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", _i32)] + [(n, ctypes.c_double) for n in (
+        "factor", "original_max_position", "beta_fast", "beta_slow", "low_freq_factor",
+        "high_freq_factor")]
+
+
+def _same_device(*ts):
+    devices = {t.device for t in ts if t is not None}
+    if len(devices) > 1:
+        raise ValueError("tensors must live on one device")
+    if devices and devices.pop().index != torch.cuda.current_device():
+        raise ValueError("tensors must live on the current CUDA device")
+
+
+def pa_rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0,
+                        original_max_position=0, beta_fast=32.0, beta_slow=1.0,
+                        low_freq_factor=1.0, high_freq_factor=4.0, device="cuda"):
+    """The rotary frequencies (fp64 [rotary_dim / 2] on `device`, radians per position) and the
+    attention factor for pa_rope_and_cache.  scaling: None, "linear", "ntk", "yarn" or "bands"
+    (the kinds PA_ROPE_* of pa.h), with the values it uses."""
+    if scaling not in _ROPE_KINDS:
+        raise ValueError(f"scaling must be one of {sorted(k for k in _ROPE_KINDS if k)} or None")
+    sc = _RopeScaling(_ROPE_KINDS[scaling], factor, original_max_position, beta_fast, beta_slow,
+                      low_freq_factor, high_freq_factor)
+    f = torch.empty(max(int(rotary_dim) // 2, 0), dtype=torch.float64)
+    af = _f32()
+    _check(_lib.pa_rope_frequencies(int(rotary_dim), float(base), ctypes.byref(sc), _p(f),
+                                    ctypes.byref(af)), "pa_rope_frequencies")
+    return f.to(device), af.value
+
+
+def _token_rows(t, what):
+    """Elements between the tokens of [T, N, D] rows whose heads are contiguous."""
+    T, N, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (N > 1 and t.stride(1) != D):
+        raise ValueError(f"{what}: a token's heads must be contiguous")
+    return t.stride(0) if T > 1 else N * D
+
+
+def pa_rope_and_cache(q, k, v, q_out, k_blocks, v_blocks, positions, slot_mapping, inv_freq,
+                      interleaved=False, attn_factor=1.0, k_scale=1.0, v_scale=1.0, k_scales=None,
+                      v_scales=None, stream=None):
+    """Rotary positions for q [T, H, D] (into q_out, which may be q; both None: no queries) and k
+    [T, Hkv, D], and the scatter of k and v into the pools at slot_mapping.  The tokens of q, k, v
+    and q_out may be strided (views of one fused product).  inv_freq: fp64 [rotary_dim / 2]
+    (pa_rope_frequencies); scales as in pa_reshape_and_cache."""
+    for t in (q, k, v, q_out):
+        if t is not None and (not t.is_cuda or t.dim() != 3):
+            raise ValueError("q, k, v and q_out must be [T, heads, D] CUDA tensors")
+    _dev(k_blocks, v_blocks, positions, slot_mapping, inv_freq)
+    _i32t(positions, slot_mapping)
+    _same_device(q, k, v, q_out, k_blocks, v_blocks, positions, slot_mapping, inv_freq, k_scales,
+                 v_scales)
+    if k.shape != v.shape or k_blocks.dim() != 4 or k_blocks.shape != v_blocks.shape:
+        raise ValueError("k, v must be [T, Hkv, D]; pools [NB, b, Hkv, D]")
+    if k.dtype != v.dtype or k_blocks.dtype != v_blocks.dtype:
+        raise ValueError("k and v (and the two pools) must share one dtype")
+    T, Hkv, D = k.shape
+    NB, bs, Hkv2, D2 = k_blocks.shape
+    if (Hkv, D) != (Hkv2, D2):
+        raise ValueError("kv heads / head size differ between rows and pool")
+    if positions.numel() != T or slot_mapping.numel() != T:
+        raise ValueError("positions and slot_mapping must be [T]")
+    if (q is None) != (q_out is None):
+        raise ValueError("give both q and q_out or neither")
+    H = 0
+    if q is not None:
+        H = q.shape[1]
+        if q.shape != (T, H, D) or q_out.shape != q.shape or not q.dtype == q_out.dtype == k.dtype:
+            raise ValueError("q and q_out must be [T, H, D] of the rows' dtype")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be fp64 [rotary_dim / 2]")
+    _head_scales(Hkv, k_scales, v_scales)
+    _check(_lib.pa_rope_and_cache(
+        _p(q), 0 if q is None else _token_rows(q, "q"),
+        _p(q_out), 0 if q is None else _token_rows(q_out, "q_out"), _p(k), _token_rows(k, "k"),
+        _p(v), _token_rows(v, "v"), _p(k_blocks), _p(v_blocks), _p(positions), _p(slot_mapping),
+        _p(inv_freq), 2 * inv_freq.numel(), int(bool(interleaved)), float(attn_factor), T, H, Hkv,
+        D, bs, NB, _DT[k.dtype], _DT[k_blocks.dtype], float(k_scale), float(v_scale), _p(k_scales),
+        _p(v_scales), _stream(stream)), "pa_rope_and_cache")
+    return q_out
+
+
+def pa_tree_attention_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                                     max_blocks_per_seq, block_size) -> int:
+    return int(_lib.pa_tree_attention_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads,
+                                                     head_dim, max_blocks_per_seq, block_size))
+
+
+def pa_tree_attention(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, positions, tree_mask,
+                      block_tables, scale, sliding_window=0, workspace=None, stream=None,
+                      sinks=None, lse=None, k_scale=1.0, v_scale=1.0, k_scales=None,
+                      v_scales=None):
+    """Attention of each sequence's drafted nodes (its last query_start_loc[s + 1] -
+    query_start_loc[s] cached positions) over its context and the nodes of their tree_mask rows:
+    int32 [T, mask_words], bit i of a row = node i of the token's sequence.  sinks, lse and scales
+    as in pa_varlen_forward."""
+    _dev(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, positions, tree_mask, block_tables,
+         workspace, sinks, lse)
+    _i32t(query_start_loc, seq_lens, positions, tree_mask, block_tables)
+    _same_device(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, positions, tree_mask,
+                 block_tables, workspace, sinks, lse, k_scales, v_scales)
+    if q.dim() != 3 or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("q and out must be [T, H, D] of one dtype")
+    if k_blocks.shape != v_blocks.shape or k_blocks.dtype != v_blocks.dtype:
+        raise ValueError("k_blocks and v_blocks must match")
+    T, H, D = q.shape
+    NB, bs, Hkv, D2 = k_blocks.shape
+    S = query_start_loc.numel() - 1
+    if D2 != D:
+        raise ValueError("head size differs between q and the pool")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != T or positions.numel() != T:
+        raise ValueError("tree_mask must be [T, mask_words] and positions [T]")
+    if seq_lens.numel() != S or block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("seq_lens must be [S] and block_tables [S, max_blocks]")
+    if sinks is not None and (sinks.dtype != torch.float32 or sinks.shape != (H,)):
+        raise ValueError("sinks must be a contiguous fp32 [num_heads] tensor")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (H, T)):
+        raise ValueError("lse must be a contiguous fp32 [num_heads, num_tokens] tensor")
+    _head_scales(Hkv, k_scales, v_scales)
+    if workspace is None:
+        n = pa_tree_attention_workspace_size(S, T, H, Hkv, D, block_tables.shape[1], bs)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    _check(_lib.pa_tree_attention(
+        _p(q), _p(k_blocks), _p(v_blocks), _p(out), _p(query_start_loc), _p(seq_lens),
+        _p(positions), _p(tree_mask), _p(block_tables), S, T, tree_mask.shape[1], H, Hkv, D, bs, NB,
+        block_tables.shape[1], _DT[q.dtype], _DT[k_blocks.dtype], float(scale),
+        int(sliding_window), _p(sinks), _p(lse), float(k_scale), float(v_scale), _p(k_scales),
+        _p(v_scales), _p(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)), "pa_tree_attention")
+    return out
+
+
+def _pools(k_blocks, v_blocks):
+    if k_blocks.dim() != 4 or k_blocks.dtype not in _DT:
+        raise ValueError("pools must be [NB, b, Hkv, D]")
+    if v_blocks is not None and (k_blocks.shape != v_blocks.shape
+                                 or k_blocks.dtype != v_blocks.dtype):
+        raise ValueError("k_blocks and v_blocks must match")
+    return k_blocks.shape
+
+
+def pa_tree_commit(k_blocks, v_blocks, block_tables, context_lens, accepted, num_accepted,
+                   stream=None):
+    """Move the K and V rows of the accepted nodes (accepted [S, max_accepted], the first
+    num_accepted[s] of a row, strictly increasing) of each sequence's tree, which begins at
+    position context_lens[s], to its first positions."""
+    _dev(k_blocks, v_blocks, block_tables, context_lens, accepted, num_accepted)
+    _i32t(block_tables, context_lens, accepted, num_accepted)
+    _same_device(k_blocks, v_blocks, block_tables, context_lens, accepted, num_accepted)
+    NB, bs, Hkv, D = _pools(k_blocks, v_blocks)
+    if accepted.dim() != 2 or block_tables.dim() != 2:
+        raise ValueError("accepted must be [S, max_accepted], block_tables [S, max_blocks]")
+    S, A = accepted.shape
+    if context_lens.numel() != S or num_accepted.numel() != S or block_tables.shape[0] != S:
+        raise ValueError("context_lens and num_accepted must be [S]")
+    _check(_lib.pa_tree_commit(_p(k_blocks), _p(v_blocks), _p(block_tables), _p(context_lens),
+                               _p(accepted), _p(num_accepted), S, A, Hkv, D, bs, NB,
+                               block_tables.shape[1], _DT[k_blocks.dtype], _stream(stream)),
+           "pa_tree_commit")
+
+
+def pa_copy_blocks(k_blocks, v_blocks, block_pairs, stream=None):
+    """Copy whole blocks of both pools (v_blocks may be None) for every (src, dst) of block_pairs
+    [n, 2]; (-1, -1) is skipped."""
+    _dev(k_blocks, v_blocks, block_pairs)
+    _i32t(block_pairs)
+    _same_device(k_blocks, v_blocks, block_pairs)
+    NB, bs, Hkv, D = _pools(k_blocks, v_blocks)
+    if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
+        raise ValueError("block_pairs must be [n, 2]")
+    _check(_lib.pa_copy_blocks(_p(k_blocks), _p(v_blocks), _p(block_pairs), block_pairs.shape[0],
+                               Hkv, D, bs, NB, _DT[k_blocks.dtype], _stream(stream)),
+           "pa_copy_blocks")
+
+
+def _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, *lists):
+    _dev(block_tables, seq_lens, ref_counts, free_list, free_count, *lists)
+    _i32t(block_tables, seq_lens, ref_counts, free_list, free_count, *lists)
+    _same_device(block_tables, seq_lens, ref_counts, free_list, free_count, *lists)
+    if block_tables.dim() != 2 or seq_lens.numel() != block_tables.shape[0]:
+        raise ValueError("block_tables must be [rows, max_blocks] and seq_lens [rows]")
+    if free_list.numel() != ref_counts.numel() or free_count.numel() != 1:
+        raise ValueError("ref_counts and free_list must be [num_blocks], free_count [1]")
+    if any(x.numel() != lists[0].numel() for x in lists):
+        raise ValueError("the lists must have one length")
+
+
+def pa_fork_sequences(block_tables, seq_lens, parents, children, ref_counts, free_list, free_count,
+                      block_size, block_pairs=None, stream=None):
+    """Make row children[f] a copy of row parents[f] that shares its whole blocks; returns
+    block_pairs [n, 2], the partly filled blocks to copy with pa_copy_blocks."""
+    _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, parents, children)
+    n = parents.numel()
+    if block_pairs is None:
+        block_pairs = torch.empty(n, 2, dtype=torch.int32, device=block_tables.device)
+    _dev(block_pairs)
+    _i32t(block_pairs)
+    _same_device(block_tables, block_pairs)
+    if block_pairs.shape != (n, 2):
+        raise ValueError("block_pairs must be [n, 2]")
+    _check(_lib.pa_fork_sequences(_p(block_tables), _p(seq_lens), _p(parents), _p(children), n,
+                                  block_tables.shape[0], block_tables.shape[1], int(block_size),
+                                  _p(ref_counts), _p(free_list), _p(free_count),
+                                  ref_counts.numel(), _p(block_pairs), _stream(stream)),
+           "pa_fork_sequences")
+    return block_pairs
+
+
+def pa_grow_sequences(block_tables, seq_lens, sequences, new_lens, ref_counts, free_list,
+                      free_count, block_size, stream=None):
+    """Lengthen the rows `sequences` to new_lens, taking the blocks they need."""
+    _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, sequences, new_lens)
+    _check(_lib.pa_grow_sequences(_p(block_tables), _p(seq_lens), _p(sequences), _p(new_lens),
+                                  sequences.numel(), block_tables.shape[0], block_tables.shape[1],
+                                  int(block_size), _p(ref_counts), _p(free_list), _p(free_count),
+                                  ref_counts.numel(), _stream(stream)), "pa_grow_sequences")
+
+
+def pa_free_sequences(block_tables, seq_lens, sequences, ref_counts, free_list, free_count,
+                      block_size, stream=None):
+    """End the rows `sequences`: their blocks lose a reference each, and those without any go
+    back to the free list in ascending order."""
+    _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, sequences)
+    _check(_lib.pa_free_sequences(_p(block_tables), _p(seq_lens), _p(sequences),
+                                  sequences.numel(), block_tables.shape[0], block_tables.shape[1],
+                                  int(block_size), _p(ref_counts), _p(free_list), _p(free_count),
+                                  ref_counts.numel(), _stream(stream)), "pa_free_sequences")

@@ -14,33 +14,6 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
-// Exclusive prefix sum of one int per thread across the block; *total receives the sum.
-__device__ int block_exclusive_scan(int v, int* s_warp, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    int y = __shfl_up_sync(kFull, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) s_warp[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int w = lane < nwarps ? s_warp[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      int y = __shfl_up_sync(kFull, w, o);
-      if (lane >= o) w += y;
-    }
-    s_warp[lane] = w;
-  }
-  __syncthreads();
-  const int before = warp ? s_warp[warp - 1] : 0;
-  *total = s_warp[nwarps - 1];
-  __syncthreads();
-  return before + x - v;
-}
-
 __device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
@@ -1169,7 +1142,6 @@ cudaError_t gather_as(const void* kb, const void* vb, void* ko, void* vo, const 
   return cudaGetLastError();
 }
 
-bool aligned(const void* p, size_t a) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace
 
@@ -1363,6 +1335,14 @@ cudaError_t launch_gather_kv(const void* k_blocks, const void* v_blocks, void* k
                             row_bytes, block_size, max_blocks, status, stream);
 }
 
+
+cudaError_t launch_validate_slots(const int32_t* slots, int64_t num_tokens, int64_t num_slots,
+                                  int* status, cudaStream_t stream) {
+  const int64_t grid = std::min<int64_t>((num_tokens + 255) / 256, 1024);
+  return launch_pdl(k_validate_slots, dim3((unsigned)grid), dim3(256), 0, stream, slots,
+                    num_tokens, num_slots, (const float*)nullptr, (const float*)nullptr, 1, 0,
+                    status);
+}
 
 cudaError_t launch_validate_scales(const float* k_scales, const float* v_scales,
                                    int32_t num_kv_heads, int* status, cudaStream_t stream) {

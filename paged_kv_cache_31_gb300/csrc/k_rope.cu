@@ -1,0 +1,304 @@
+// k_rope.cu -- rotary positions applied to the new tokens' queries and keys, with the keys and
+// values scattered into the paged pools in the same pass.
+//
+// Math.  Pair i of a head's first R = rotary_dim elements is (x_i, x_{R/2+i}) in the half
+// layout and (x_{2i}, x_{2i+1}) interleaved; at position p it is turned by the angle
+// p * inv_freq[i] and multiplied by the attention factor f (long-context scalings):
+//   y_a = f (x_a cos - x_b sin),  y_b = f (x_a sin + x_b cos)
+// and elements past R are copied.  Everything is computed in fp32 and rounded once.
+//
+// Angles.  In fp32 the product p * inv_freq is off by up to 2^-24 p radians: 0.06 at a million
+// positions.  Here each frequency becomes the fraction of a turn per position as a 64-bit
+// fixed-point number, once per CTA and in fp64 (fp64 is slow on this GPU: R / 2 values of five
+// operations), and a position's angle is one 64-bit integer product that wraps at whole turns,
+// exactly.  Its top 32 bits go to sincospif as a signed fraction of half a turn (off by at
+// most 2^-25 half turns).
+//
+// What bounds it: memory.  Every element of q, k and v is read once and written once, 16 bytes
+// at a time; a rotated half-layout unit is the two 16-byte chunks of its pairs, so a thread
+// has both sides of each pair in registers.  A CTA takes TOK tokens; their angles are computed
+// once into shared memory and serve all H + Hkv heads.  The items of the CTA's tokens (rotated
+// units, copied chunks and value chunks) are dealt to the threads in memory order, with four
+// items' loads in flight per thread.
+#include <algorithm>
+
+#include "pa_internal.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kCheckedTokens = 2048;  // up to here every CTA checks all slots itself
+constexpr int kMaxHalf = 128;         // rotary_dim / 2, at most
+
+// Division of 0 <= n < 2^31 by a fixed d >= 1: with l = ceil(log2 d) and
+// m = ceil(2^(31 + l) / d) < 2^32, floor(n m / 2^(31 + l)) is the quotient (the error of m adds
+// less than n / 2^(31 + l) < 2^-l <= 1 / d).
+struct FastDiv {
+  uint32_t d, m, l;
+  explicit FastDiv(uint32_t x) : d(x), m(0), l(0) {
+    while ((1ull << l) < x) ++l;
+    m = (uint32_t)(((1ull << (31 + l)) + x - 1) / x);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return (uint32_t)(((uint64_t)n * m) >> (31 + l));
+  }
+};
+
+struct Geometry {
+  FastDiv per_token;  // items of one token
+  FastDiv per_head;   // items of a rotated head: rotated units, then copied chunks
+  FastDiv per_v;      // value chunks of a kv head
+  int rot_units;      // rotated units of a head
+};
+
+// one chunk of VE elements as fp32
+template <typename TS, int VE>
+__device__ __forceinline__ void load_chunk(const TS* p, float (&x)[VE]) {
+  if constexpr (sizeof(TS) * VE == 16) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const TS* e = reinterpret_cast<const TS*>(&w);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) x[i] = to_f32(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VE; ++i) x[i] = to_f32(p[i]);
+  }
+}
+
+// VE fp32 values in pool type DST (a pa_dtype), rounded to nearest even
+template <int DST, int VE>
+__device__ __forceinline__ void store_chunk(void* base, int64_t at, const float (&x)[VE]) {
+  if constexpr (DST == PA_FP8_E4M3) {
+    uint8_t* p = static_cast<uint8_t*>(base) + at;
+    if constexpr (VE % 4 == 0) {
+      uint32_t w[VE / 4];
+#pragma unroll
+      for (int i = 0; i < VE / 4; ++i)
+        w[i] = f32x2_to_e4m3x2(x[4 * i], x[4 * i + 1]) |
+               ((uint32_t)f32x2_to_e4m3x2(x[4 * i + 2], x[4 * i + 3]) << 16);
+      if constexpr (VE == 8)
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+      else
+        *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) p[i] = (uint8_t)(f32x2_to_e4m3x2(x[i], 0.f) & 0xffu);
+    }
+  } else if constexpr (DST == PA_BF16) {
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + at;
+    if constexpr (VE == 8) {
+      *reinterpret_cast<uint4*>(p) =
+          make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                     pack_bf16x2(x[6], x[7]));
+    } else if constexpr (VE == 4) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) p[i] = __float2bfloat16_rn(x[i]);
+    }
+  } else {
+    float* p = static_cast<float*>(base) + at;
+    if constexpr (VE % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < VE; i += 4)
+        *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) p[i] = x[i];
+    }
+  }
+}
+
+// TS: type of q, k, v; DST: the pools' pa_dtype; VE: elements per chunk (16 bytes of TS, or 1 /
+// 2 when shapes, strides or addresses do not allow that); IL: interleaved pairs; CHECKED: this
+// kernel checks the slots (else k_validate_slots ran before).
+template <typename TS, int DST, int VE, bool IL, bool CHECKED>
+__global__ void __launch_bounds__(kThreads)
+    k_rope_and_cache(const RopeParams p, const Geometry g, const int tok_per_cta) {
+  static_assert(!IL || VE % 2 == 0, "interleaved pairs stay inside a chunk");
+  __shared__ int s_skip;
+  __shared__ uint64_t s_turn[kMaxHalf];
+  extern __shared__ __align__(16) float s_trig[];  // [tok][half] cos, then sin
+  pdl_wait();
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) s_skip = status_set(p.status) ? 1 : 0;
+  const int half = p.rotary_dim >> 1;
+  for (int i = threadIdx.x; i < half; i += kThreads) {
+    const double f = p.inv_freq[i] * 0.15915494309189533577;  // turns per position
+    s_turn[i] = (uint64_t)__double2ll_rn((f - rint(f)) * 18446744073709551616.0);
+  }
+  __syncthreads();
+  if (s_skip) return;
+  if constexpr (CHECKED) {
+    bool bad = false;
+    for (int64_t t = threadIdx.x; t < p.num_tokens; t += kThreads) {
+      const int32_t s = p.slots[t];
+      bad |= s < 0 || (int64_t)s >= p.num_slots;
+    }
+    if (__syncthreads_or(bad)) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) record_error(p.status, PA_EINVAL);
+      return;
+    }
+  }
+  const int64_t t0 = (int64_t)blockIdx.x * tok_per_cta;
+  const int ntok = (int)min((int64_t)tok_per_cta, p.num_tokens - t0);
+  float* s_cos = s_trig;
+  float* s_sin = s_trig + tok_per_cta * half;
+  for (int a = threadIdx.x; a < ntok * half; a += kThreads) {
+    const int tk = a / half, i = a - tk * half;
+    const uint64_t turn = (uint64_t)(int64_t)p.positions[t0 + tk] * s_turn[i];
+    float sn, cs;
+    sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &sn, &cs);
+    s_cos[a] = cs * p.attn_factor;
+    s_sin[a] = sn * p.attn_factor;
+  }
+  __syncthreads();
+
+  const int H = p.q ? p.num_heads : 0, D = p.head_dim, R = p.rotary_dim;
+  const int rot_items = (H + p.num_kv_heads) * (int)g.per_head.d;
+  const TS* q = static_cast<const TS*>(p.q);
+  const TS* k = static_cast<const TS*>(p.k);
+  const TS* v = static_cast<const TS*>(p.v);
+  const int total = ntok * (int)g.per_token.d;
+  constexpr int U = VE == 1 || VE == 2 ? 2 : 4;  // items in flight
+  for (int it0 = threadIdx.x; it0 < total; it0 += U * kThreads) {
+    float a[U][VE], b[U][VE];
+    int tk[U], head[U], off[U];  // head: 0 .. H - 1 q, then k, then v heads
+    bool rot[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int it = it0 + u * kThreads;
+      tk[u] = -1;
+      rot[u] = false;
+      if (it >= total) continue;
+      tk[u] = (int)g.per_token.div((uint32_t)it);
+      const int r = it - tk[u] * (int)g.per_token.d;
+      const int64_t t = t0 + tk[u];
+      const TS* src;
+      if (r < rot_items) {
+        head[u] = (int)g.per_head.div((uint32_t)r);
+        const int e = r - head[u] * (int)g.per_head.d;
+        rot[u] = e < g.rot_units;
+        off[u] = rot[u] ? e * VE : R + (e - g.rot_units) * VE;
+        src = head[u] < H ? q + t * p.q_stride + (int64_t)head[u] * D
+                          : k + t * p.k_stride + (int64_t)(head[u] - H) * D;
+      } else {
+        const int hv = (int)g.per_v.div((uint32_t)(r - rot_items));
+        off[u] = (r - rot_items - hv * (int)g.per_v.d) * VE;
+        src = v + t * p.v_stride + (int64_t)hv * D;
+        head[u] = H + p.num_kv_heads + hv;
+      }
+      load_chunk<TS, VE>(src + off[u], a[u]);
+      if (!IL && rot[u]) load_chunk<TS, VE>(src + off[u] + half, b[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (tk[u] < 0) continue;
+      if (rot[u]) {
+        const float* cs = s_cos + tk[u] * half + (IL ? off[u] / 2 : off[u]);
+        const float* sn = s_sin + tk[u] * half + (IL ? off[u] / 2 : off[u]);
+        if constexpr (IL) {
+#pragma unroll
+          for (int i = 0; i < VE / 2; ++i) {
+            const float x = a[u][2 * i], y = a[u][2 * i + 1];
+            a[u][2 * i] = x * cs[i] - y * sn[i];
+            a[u][2 * i + 1] = x * sn[i] + y * cs[i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < VE; ++i) {
+            const float x = a[u][i], y = b[u][i];
+            a[u][i] = x * cs[i] - y * sn[i];
+            b[u][i] = x * sn[i] + y * cs[i];
+          }
+        }
+      }
+      const int64_t t = t0 + tk[u];
+      const bool two = !IL && rot[u];
+      if (head[u] < H) {
+        constexpr int SRC = sizeof(TS) == 2 ? PA_BF16 : PA_F32;
+        const int64_t at = t * p.q_out_stride + (int64_t)head[u] * D + off[u];
+        store_chunk<SRC, VE>(p.q_out, at, a[u]);
+        if (two) store_chunk<SRC, VE>(p.q_out, at + half, b[u]);
+        continue;
+      }
+      const bool is_v = head[u] >= H + p.num_kv_heads;
+      const int hk = head[u] - H - (is_v ? p.num_kv_heads : 0);
+      const float* scales = is_v ? p.v_scales : p.k_scales;
+      const float sc = scales ? __ldg(scales + hk) : is_v ? p.v_scale : p.k_scale;
+      if (sc != 1.f) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          a[u][i] = __fdiv_rn(a[u][i], sc);
+          if (two) b[u][i] = __fdiv_rn(b[u][i], sc);
+        }
+      }
+      const int64_t at = ((int64_t)p.slots[t] * p.num_kv_heads + hk) * D + off[u];
+      void* pool = is_v ? p.v_blocks : p.k_blocks;
+      store_chunk<DST, VE>(pool, at, a[u]);
+      if (two) store_chunk<DST, VE>(pool, at + half, b[u]);
+    }
+  }
+}
+
+template <typename TS, int DST, int VE, bool IL>
+cudaError_t launch_as(const RopeParams& p, int num_sms, cudaStream_t stream) {
+  const int D = p.head_dim, R = p.rotary_dim;
+  const int rot_units = R / (IL ? VE : 2 * VE), per_head = rot_units + (D - R) / VE;
+  const int heads = (p.q ? p.num_heads : 0) + p.num_kv_heads;
+  const int64_t per_token = (int64_t)heads * per_head + (int64_t)p.num_kv_heads * (D / VE);
+  // several tokens to a CTA once every SM has a few CTAs (their angles and checks are shared
+  // work); a CTA's items stay below 2^31 whatever the row's length
+  int tok = 4;
+  while (tok > 1 && (p.num_tokens < (int64_t)tok * 4 * num_sms || per_token > (1 << 24))) tok >>= 1;
+  if (per_token > (1 << 30)) return cudaErrorInvalidValue;
+  const Geometry g{FastDiv((uint32_t)per_token), FastDiv((uint32_t)std::max(1, per_head)),
+                   FastDiv((uint32_t)(D / VE)), rot_units};
+  const dim3 grid((unsigned)((p.num_tokens + tok - 1) / tok));
+  const size_t smem = (size_t)tok * R * 4;
+  if (p.num_tokens <= kCheckedTokens)
+    return launch_pdl(k_rope_and_cache<TS, DST, VE, IL, true>, grid, dim3(kThreads), smem, stream,
+                      p, g, tok);
+  const cudaError_t e = launch_validate_slots(p.slots, p.num_tokens, p.num_slots, p.status, stream);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_rope_and_cache<TS, DST, VE, IL, false>, grid, dim3(kThreads), smem, stream,
+                    p, g, tok);
+}
+
+template <typename TS, int DST>
+cudaError_t launch_types(const RopeParams& p, int num_sms, cudaStream_t stream) {
+  constexpr int VE = 16 / (int)sizeof(TS);
+  constexpr size_t kDst = DST == PA_FP8_E4M3 ? 1 : DST == PA_BF16 ? 2 : 4;
+  const int D = p.head_dim, R = p.rotary_dim;
+  // 16-byte chunks: whole chunks on both sides of every pair and in the copied rest, rows and
+  // tensors aligned for the loads and for the pools' stores
+  const bool vec = D % VE == 0 && R % (p.interleaved ? VE : 2 * VE) == 0 &&
+                   (p.q == nullptr || (p.q_stride % VE == 0 && p.q_out_stride % VE == 0 &&
+                                       aligned(p.q, 16) && aligned(p.q_out, 16))) &&
+                   p.k_stride % VE == 0 && p.v_stride % VE == 0 && aligned(p.k, 16) &&
+                   aligned(p.v, 16) && aligned(p.k_blocks, std::min<size_t>(16, VE * kDst)) &&
+                   aligned(p.v_blocks, std::min<size_t>(16, VE * kDst));
+  if (p.interleaved) {
+    if (vec) return launch_as<TS, DST, VE, true>(p, num_sms, stream);
+    return D % 2 == 0 ? launch_as<TS, DST, 2, true>(p, num_sms, stream) : cudaErrorInvalidValue;
+  }
+  return vec ? launch_as<TS, DST, VE, false>(p, num_sms, stream)
+             : launch_as<TS, DST, 1, false>(p, num_sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_and_cache(const RopeParams& p, pa_dtype src_dtype, pa_dtype kv_dtype,
+                                  int num_sms, cudaStream_t stream) {
+  if (src_dtype == PA_BF16) {
+    if (kv_dtype == PA_BF16) return launch_types<__nv_bfloat16, PA_BF16>(p, num_sms, stream);
+    if (kv_dtype == PA_FP8_E4M3) return launch_types<__nv_bfloat16, PA_FP8_E4M3>(p, num_sms, stream);
+    return launch_types<__nv_bfloat16, PA_F32>(p, num_sms, stream);
+  }
+  if (kv_dtype == PA_BF16) return launch_types<float, PA_BF16>(p, num_sms, stream);
+  if (kv_dtype == PA_FP8_E4M3) return launch_types<float, PA_FP8_E4M3>(p, num_sms, stream);
+  return launch_types<float, PA_F32>(p, num_sms, stream);
+}
+
+}  // namespace pa

@@ -1,0 +1,495 @@
+// k_tree.cu -- attention of a tree of drafted tokens over the paged cache: the planning kernel,
+// the general kernel (any types, head size and block size) and the merge of split items.
+//
+// Math.  Sequence s has n nodes (its query tokens), cached as its last n positions behind a
+// context of c = seq_len - n positions.  Node t attends to the context and to the nodes whose
+// bit is set in its mask row (its ancestors and itself, in a tree).  A key's logical position is
+// j for context position j and positions[node] for a node; with a sliding window w a key is
+// visible when its logical position is greater than positions[t] - w.  The visible scores go
+// through one softmax, online over key tiles: m' = max(m, .), l = 2^(m - m') l + sum p,
+// O = 2^(m - m') O + P V.
+//
+// Why split: a drafted step has few query rows and long contexts, so (sequence, kv head) items
+// alone do not fill the GPU evenly.  All items' key tiles are laid end to end and every CTA
+// takes an equal, contiguous share; the pieces of an item are merged afterwards in key order.
+// How a batch is cut depends on its lengths alone, so equal inputs give equal bits.
+#include <algorithm>
+
+#include "k_tree.cuh"
+
+namespace pa {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kPlanThreads = 1024;
+constexpr int kCumShared = 2048;  // sequences whose prefix weights the planner keeps in smem
+
+__device__ __forceinline__ int64_t block_sum_scan(int64_t v, int64_t* s_warp, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(kFull, w, o);
+      if (lane >= o) w += y;
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  const int64_t before = warp ? s_warp[warp - 1] : 0;
+  *total = s_warp[31];
+  __syncthreads();
+  return before + x - v;
+}
+
+// Block 0 plans; blocks 1 .. check the table entries of the sequences, one warp per 256 entries.
+// Everything is read after the wait for the kernels ahead, and nothing is written by the
+// attention kernel before this whole launch is done, so an error leaves the outputs untouched.
+__global__ void __launch_bounds__(kPlanThreads) k_tree_plan(const TreeParams p) {
+  __shared__ int64_t s_warp[32];
+  __shared__ int64_t s_cum[kCumShared + 1];
+  __shared__ int s_first[kPlanThreads], s_nodes[kPlanThreads], s_low[kPlanThreads];
+  const VarlenMeta& m = p.m;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+  bool bad = false;
+  if (blockIdx.x > 0) {
+    const int warps = (gridDim.x - 1) * (kPlanThreads / 32);
+    const int me = (blockIdx.x - 1) * (kPlanThreads / 32) + warp;
+    const int per = (m.max_blocks + 255) / 256;  // chunks of a table row
+    const int64_t chunks = (int64_t)m.num_seqs * per;
+    for (int64_t c = me; c < chunks; c += warps) {
+      const int s = (int)(c / per), e0 = (int)(c % per) * 256;
+      const int n = m.seq_lens[s];
+      if (m.query_start_loc[s + 1] <= m.query_start_loc[s] || n < 1) continue;
+      const int64_t need = ((int64_t)n + m.block_size - 1) / m.block_size;
+      const int lim = (int)min(need, (int64_t)m.max_blocks);
+      const int32_t* row = m.block_tables + (int64_t)s * m.max_blocks;
+      int id[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int e = e0 + lane + 32 * u;
+        id[u] = e < lim ? row[e] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) bad |= id[u] < 0 || (int64_t)id[u] >= m.num_blocks;
+    }
+    if (__any_sync(kFull, bad) && lane == 0) record_error(p.status, PA_EINVAL);
+    return;
+  }
+
+  // per-head scales (each array may be missing)
+  for (int g = tid; g < m.num_kv_heads; g += kPlanThreads) {
+    const float a = m.k_scales ? m.k_scales[g] : 1.f, b = m.v_scales ? m.v_scales[g] : 1.f;
+    bad |= !(a > 0.f && a <= 3.402823466e38f) || !(b > 0.f && b <= 3.402823466e38f);
+  }
+  int64_t base = 0;
+  for (int s0 = 0; s0 < m.num_seqs; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    int qs = 0, nodes = 0, n = 0;
+    if (s < m.num_seqs) {
+      qs = m.query_start_loc[s];
+      const int qe = m.query_start_loc[s + 1];
+      bad |= qs < 0 || qe < qs || (int64_t)qe > m.num_tokens || (s == 0 && qs != 0) ||
+             (s == m.num_seqs - 1 && (int64_t)qe != m.num_tokens);
+      if (qs >= 0 && qe > qs && (int64_t)qe <= m.num_tokens) {
+        nodes = qe - qs;
+        n = m.seq_lens[s];
+        if (n < nodes || nodes > 32 * (int64_t)p.mask_words ||
+            ((int64_t)n + m.block_size - 1) / m.block_size > m.max_blocks) {
+          bad = true;
+          nodes = 0;
+        }
+      }
+    }
+    // with a window: the lowest position of each sequence's nodes decides the first key it reads
+    if (m.window > 0) {
+      s_first[tid] = qs;
+      s_nodes[tid] = nodes;
+      __syncthreads();
+      const int here = min(kPlanThreads, m.num_seqs - s0);
+      for (int i = warp; i < here; i += kPlanThreads / 32) {
+        int lo = INT_MAX;
+        for (int t = lane; t < s_nodes[i]; t += 32) lo = min(lo, m.positions[s_first[i] + t]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) lo = min(lo, __shfl_xor_sync(kFull, lo, o));
+        if (lane == 0) s_low[i] = lo;
+      }
+      __syncthreads();
+    }
+    int64_t weight = 0;
+    if (nodes > 0) {
+      int kv0 = 0;
+      if (m.window > 0) {
+        bad |= s_low[tid] < 0;
+        kv0 = min(max(s_low[tid] - m.window + 1, 0), n - nodes);
+      }
+      kv0 -= kv0 % m.block_size;
+      const int tiles = (n - kv0 + p.key_tile - 1) / p.key_tile;
+      p.seqs[s] = make_int4(qs, nodes, n, kv0);
+      const int64_t rows = (int64_t)nodes * m.group;
+      const int64_t full = rows / p.rows_per_item;
+      const int rest = (int)(rows % p.rows_per_item);
+      weight = (full * tree_weight(p.rows_per_item) + (rest ? tree_weight(rest) : 0)) *
+               m.num_kv_heads * tiles;
+    } else if (s < m.num_seqs) {
+      p.seqs[s] = make_int4(0, 0, 0, 0);
+    }
+    int64_t total;
+    const int64_t at = base + block_sum_scan(weight, s_warp, &total);
+    if (s < m.num_seqs) {
+      p.cum[s] = at;
+      if (s < kCumShared) s_cum[s] = at;
+    }
+    base += total;
+  }
+  if (tid == 0) {
+    p.cum[m.num_seqs] = base;
+    if (m.num_seqs <= kCumShared) s_cum[m.num_seqs] = base;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad) {
+    if (tid == 0) record_error(p.status, PA_EINVAL);
+    return;
+  }
+  // where each CTA's share begins
+  const bool shared = m.num_seqs <= kCumShared;
+  for (int c = tid; c <= p.grid; c += kPlanThreads) {
+    int4 st = make_int4(m.num_seqs, 0, 0, 0);
+    if (c < p.grid && base > 0) {
+      const int64_t x = base / p.grid * c + base % p.grid * c / p.grid;  // floor(base c / grid)
+      int lo = 0, hi = m.num_seqs;  // the last sequence with cum <= x
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((shared ? s_cum[mid] : p.cum[mid]) <= x) lo = mid; else hi = mid;
+      }
+      const int64_t rem = x - (shared ? s_cum[lo] : p.cum[lo]);
+      const int4 q = p.seqs[lo];
+      const TreeGeometry g(p, q);
+      const int64_t per_head = g.weight_before(g.items) * g.tiles;
+      const int kvh = (int)(rem / per_head);
+      const int64_t r = rem % per_head;
+      const int full_w = tree_weight(p.rows_per_item);
+      const int it = min((int)(r / ((int64_t)full_w * g.tiles)), g.items - 1);
+      const int64_t in = r - (int64_t)it * full_w * g.tiles;
+      const int w = tree_weight(g.rows_of(p, it));
+      st = make_int4(lo, kvh * g.items + it, min((int)(in / w), g.tiles - 1), 0);
+    }
+    p.starts[c] = st;
+  }
+}
+
+// ---- the general kernel -----------------------------------------------------------------------
+// 32 query rows x 32 keys per step in fp32 on the FMA pipes: thread (row = tid / 4, c = tid % 4)
+// computes the scores of keys c, c + 4, ... of its row and dims 4c + 16i .. of its output row.
+// Rows are padded by four floats, so the quads' 16-byte reads of different rows hit different
+// banks.  It is bound by shared-memory reads (9 of them for 32 FMAs on both products).
+
+constexpr int kBM = kTreeGenericRows, kBN = kTreeGenericKeys;
+
+template <typename TKV>
+__device__ __forceinline__ float4 load4(const TKV* p) {
+  if constexpr (sizeof(TKV) == 4) {
+    return *reinterpret_cast<const float4*>(p);
+  } else if constexpr (sizeof(TKV) == 2) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
+    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+  } else {
+    uint32_t lo, hi;
+    e4m3x4_to_f16(*reinterpret_cast<const uint32_t*>(p), lo, hi);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+}
+
+template <int DP>
+constexpr size_t generic_smem() {
+  return (size_t)(3 * 32 * (DP + 4) + 32 * 33) * 4;
+}
+
+// DP: head size padded to 64, 128 or 256; vec: rows can be read four elements at a time
+template <typename TQ, typename TKV, int DP>
+__global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const bool vec) {
+  constexpr int LD = DP + 4;
+  extern __shared__ __align__(16) float s_mem[];
+  float* sq = s_mem;
+  float* sk = sq + kBM * LD;
+  float* sv = sk + kBN * LD;
+  float* sp = sv + kBN * LD;  // [32][33]
+  __shared__ int s_skip;
+  const VarlenMeta& m = p.m;
+  const int tid = threadIdx.x, row = tid >> 2, c = tid & 3;
+  const int D = m.head_dim, G = m.group;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (tid == 0) s_skip = status_set(p.status) ? 1 : 0;
+  __syncthreads();
+  if (s_skip) return;
+  const TQ* q = static_cast<const TQ*>(p.q);
+  const TKV* kb = static_cast<const TKV*>(p.k_blocks);
+  const TKV* vb = static_cast<const TKV*>(p.v_blocks);
+
+  TreeWalk walk(p, blockIdx.x);
+  TreeSegment sg;
+  while (walk.next(p, sg)) {
+    const int rows = sg.rows;
+    const int r = sg.row0 + row;  // row of the sequence's nodes x group
+    const bool valid = row < rows;
+    const int tok = sg.qs + (valid ? r / G : 0);
+    const int pos = m.window > 0 ? m.positions[tok] : 0;
+    const float sl = head_scale(m.k_scales, sg.kvh, p.scale) * kLog2e;
+    __syncthreads();  // the buffers of the segment before are free
+    for (int i = tid; i < kBM * DP; i += 128) {
+      const int rr = i / DP, d = i % DP;
+      float x = 0.f;
+      if (rr < rows && d < D) {
+        const int R = sg.row0 + rr;
+        x = to_f32(q[((int64_t)(sg.qs + R / G) * m.num_heads + sg.kvh * G + R % G) * D + d]);
+      }
+      sq[rr * LD + d] = x;
+    }
+    float mx = -INFINITY, l = 0.f;
+    float o[DP / 4];
+#pragma unroll
+    for (int i = 0; i < DP / 4; ++i) o[i] = 0.f;
+    const int32_t* trow = m.block_tables + (int64_t)sg.s * m.max_blocks;
+    for (int j = sg.t0; j < sg.t1; ++j) {
+      const int key0 = sg.kv0 + j * kBN;
+      __syncthreads();  // the tile before has been used
+      for (int i = tid; i < kBN * (DP / 4); i += 128) {
+        const int kk = i / (DP / 4), d = (i % (DP / 4)) * 4, key = key0 + kk;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+        if (key < sg.n && d < D) {
+          const int64_t at = (((int64_t)trow[key / m.block_size] * m.block_size +
+                               key % m.block_size) * m.num_kv_heads + sg.kvh) * D + d;
+          if (vec) {
+            a = load4<TKV>(kb + at);
+            b = load4<TKV>(vb + at);
+          } else {
+            float x[4] = {}, y[4] = {};
+            for (int e = 0; e < 4 && d + e < D; ++e) {
+              x[e] = to_f32(kb[at + e]);
+              y[e] = to_f32(vb[at + e]);
+            }
+            a = make_float4(x[0], x[1], x[2], x[3]);
+            b = make_float4(y[0], y[1], y[2], y[3]);
+          }
+        }
+        *reinterpret_cast<float4*>(sk + kk * LD + d) = a;
+        *reinterpret_cast<float4*>(sv + kk * LD + d) = b;
+      }
+      __syncthreads();
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+      for (int d = 0; d < DP; d += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(sq + row * LD + d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 b = *reinterpret_cast<const float4*>(sk + (c + 4 * i) * LD + d);
+          x[i] += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+        }
+      }
+      float mt = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = valid && tree_visible(p, sg, tok, pos, key0 + c + 4 * i) ? x[i] * sl : -INFINITY;
+        mt = fmaxf(mt, x[i]);
+      }
+      mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 1));
+      mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 2));
+      const float mn = fmaxf(mx, mt), b0 = mn == -INFINITY ? 0.f : mn;
+      const float alpha = exp2f(mx - b0);
+      float ls = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = exp2f(x[i] - b0);
+        ls += x[i];
+        sp[row * 33 + c + 4 * i] = x[i];
+      }
+      mx = mn;
+      l = l * alpha + ls;  // this thread's eight keys; the quad is summed at the end
+#pragma unroll
+      for (int i = 0; i < DP / 4; ++i) o[i] *= alpha;
+      __syncwarp();  // the row's weights come from this warp's own quad
+#pragma unroll 4
+      for (int kk = 0; kk < kBN; ++kk) {
+        const float w = sp[row * 33 + kk];
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) {
+          const float4 b = *reinterpret_cast<const float4*>(sv + kk * LD + 4 * c + 16 * i);
+          o[4 * i] += w * b.x;
+          o[4 * i + 1] += w * b.y;
+          o[4 * i + 2] += w * b.z;
+          o[4 * i + 3] += w * b.w;
+        }
+      }
+    }
+    l += __shfl_xor_sync(kFull, l, 1);
+    l += __shfl_xor_sync(kFull, l, 2);
+    if (!valid) continue;
+    if (sg.slot >= 0) {
+      const int64_t at = (int64_t)sg.slot * p.rows_per_item + row;
+      if (c == 0) p.part_ml[at] = make_float2(mx, l);
+#pragma unroll
+      for (int i = 0; i < DP / 4; ++i) {
+        const int d = 4 * c + 16 * (i >> 2) + (i & 3);
+        if (d < D) p.part_o[at * D + d] = o[i];
+      }
+      continue;
+    }
+    const int h = sg.kvh * G + r % G;
+    const float inv = tree_finish(p, sg.kvh, h, tok, mx, l, c == 0);
+    TQ* out = static_cast<TQ*>(p.out) + ((int64_t)tok * m.num_heads + h) * D;
+#pragma unroll
+    for (int i = 0; i < DP / 4; ++i) {
+      const int d = 4 * c + 16 * (i >> 2) + (i & 3);
+      if (d < D) out[d] = from_f32<TQ>(o[i] * inv);
+    }
+  }
+}
+
+// ---- merge ------------------------------------------------------------------------------------
+// Block (b, y): the item that the boundary between CTA b and b + 1 cuts, when that is the item's
+// first cut; a warp per row.  out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the
+// item's pieces in key order.
+template <typename TQ>
+__global__ void __launch_bounds__(256) k_tree_merge(const TreeParams p) {
+  __shared__ int s_skip;
+  const VarlenMeta& m = p.m;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) s_skip = status_set(p.status) ? 1 : 0;
+  __syncthreads();
+  if (s_skip) return;
+  const int b = blockIdx.x;
+  const int4 cut = p.starts[b + 1], from = p.starts[b];
+  if (cut.x >= m.num_seqs || cut.z == 0) return;
+  const bool same = from.x == cut.x && from.y == cut.y;
+  if (same && from.z > 0) return;  // a later cut of the item
+  const int4 q = p.seqs[cut.x];
+  const TreeGeometry g(p, q);
+  const int kvh = cut.y / g.items, it = cut.y % g.items;
+  const int rows = g.rows_of(p, it);
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int D = m.head_dim, G = m.group;
+  // pieces: CTA b's (its first segment when the item begins its share, else its last), then the
+  // CTAs behind it while their share begins inside the item
+  float M = -INFINITY, L = 0.f;
+  float acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  int slot = same ? 2 * b : 2 * b + 1;
+  for (int c = b;;) {
+    const int64_t at = (int64_t)slot * p.rows_per_item + row;
+    const float2 ml = p.part_ml[at];
+    const float mn = fmaxf(M, ml.x), base = mn == -INFINITY ? 0.f : mn;
+    const float a = exp2f(M - base), w = exp2f(ml.x - base);
+    M = mn;
+    L = L * a + ml.y * w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int d = lane + 32 * i;
+      if (d < D) acc[i] = acc[i] * a + p.part_o[at * D + d] * w;
+    }
+    bool more = false;  // the next CTA with work that begins inside the item
+    for (++c; c < p.grid; ++c) {
+      const int4 s0 = p.starts[c], s1 = p.starts[c + 1];
+      if (s0.x != cut.x || s0.y != cut.y) break;
+      if (s1.x != s0.x || s1.y != s0.y || s1.z != s0.z) {
+        more = true;
+        break;
+      }
+    }
+    if (!more) break;
+    slot = 2 * c;
+  }
+  const int r = it * p.rows_per_item + row;
+  const int tok = q.x + r / G, h = kvh * G + r % G;
+  const float inv = tree_finish(p, kvh, h, tok, M, L, lane == 0);
+  TQ* out = static_cast<TQ*>(p.out) + ((int64_t)tok * m.num_heads + h) * D;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int d = lane + 32 * i;
+    if (d < D) out[d] = from_f32<TQ>(acc[i] * inv);
+  }
+}
+
+template <typename TQ, typename TKV, int DP>
+cudaError_t generic_as(const TreeParams& p, bool vec, cudaStream_t stream) {
+  auto kern = k_tree_generic<TQ, TKV, DP>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)generic_smem<DP>());
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(p.grid), dim3(128), generic_smem<DP>(), stream, p, vec);
+}
+
+template <typename TQ, typename TKV>
+cudaError_t generic_dims(const TreeParams& p, cudaStream_t stream) {
+  const int D = p.m.head_dim;
+  const bool vec = D % 4 == 0 && aligned(p.k_blocks, 4 * sizeof(TKV)) &&
+                   aligned(p.v_blocks, 4 * sizeof(TKV));
+  if (D <= 64) return generic_as<TQ, TKV, 64>(p, vec, stream);
+  if (D <= 128) return generic_as<TQ, TKV, 128>(p, vec, stream);
+  return generic_as<TQ, TKV, 256>(p, vec, stream);
+}
+
+}  // namespace
+
+TreeLayout tree_layout(int32_t num_seqs, int64_t num_tokens, int32_t group, int32_t num_kv_heads,
+                       int32_t head_dim, int64_t max_keys, int32_t rows_per_item,
+                       int32_t key_tile, int32_t max_grid) {
+  auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  TreeLayout L;
+  // no more CTAs than there can be (item, key tile) pairs
+  const int64_t items = (num_tokens * group / rows_per_item + num_seqs) * num_kv_heads;
+  const int64_t tiles = max_keys / key_tile + 2;
+  L.grid = (int32_t)std::max<int64_t>(1, std::min<int64_t>(max_grid, std::min<int64_t>(items, max_grid) * tiles));
+  L.cum_off = up(16 * (int64_t)num_seqs);
+  L.starts_off = L.cum_off + up(8 * ((int64_t)num_seqs + 1));
+  L.ml_off = L.starts_off + up(16 * ((int64_t)L.grid + 1));
+  L.o_off = L.ml_off + up(2 * (int64_t)L.grid * rows_per_item * 8);
+  L.bytes = L.o_off + up(2 * (int64_t)L.grid * rows_per_item * head_dim * 4);
+  return L;
+}
+
+cudaError_t launch_tree_plan(const TreeParams& p, cudaStream_t stream) {
+  // table checks beside the planner: a warp per 256 entries, at most 64 blocks
+  const int64_t chunks = (int64_t)p.m.num_seqs * ((p.m.max_blocks + 255) / 256);
+  const int blocks = (int)std::min<int64_t>((chunks + 31) / 32, 64);
+  return launch_pdl(k_tree_plan, dim3(1 + blocks), dim3(kPlanThreads), 0, stream, p);
+}
+
+cudaError_t launch_tree_generic(const TreeParams& p, pa_dtype kv, cudaStream_t stream) {
+  if (p.q_bf16) {
+    if (kv == PA_BF16) return generic_dims<__nv_bfloat16, __nv_bfloat16>(p, stream);
+    if (kv == PA_F32) return generic_dims<__nv_bfloat16, float>(p, stream);
+    return generic_dims<__nv_bfloat16, e4m3_t>(p, stream);
+  }
+  if (kv == PA_BF16) return generic_dims<float, __nv_bfloat16>(p, stream);
+  if (kv == PA_F32) return generic_dims<float, float>(p, stream);
+  return generic_dims<float, e4m3_t>(p, stream);
+}
+
+cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t stream) {
+  if (p.grid < 2) return cudaSuccess;
+  const dim3 grid((unsigned)(p.grid - 1), (unsigned)((p.rows_per_item + 7) / 8));
+  if (p.q_bf16) return launch_pdl(k_tree_merge<__nv_bfloat16>, grid, dim3(256), 0, stream, p);
+  return launch_pdl(k_tree_merge<float>, grid, dim3(256), 0, stream, p);
+}
+
+}  // namespace pa

@@ -37,14 +37,10 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceState {
-  void* ctx = nullptr;  // the context the address below was looked up in
-  int* status = nullptr;
-  int sms = 0;
-};
-
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
+
+}  // namespace
 
 // Status-word address and SM count of the current device, looked up with that device
 // current, and again whenever the current context is not the one of the last lookup (after
@@ -69,6 +65,8 @@ const DeviceState* device_state() {
   }
   return &d;
 }
+
+namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -179,15 +177,6 @@ void stall_hook(uint64_t& limit, uint32_t& stall) {
   }
 }
 void mma_waits(Mma16Params& p) { stall_hook(p.wait_limit_ns, p.debug_stall); }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-bool dtype_ok(pa_dtype t) { return t == PA_F32 || t == PA_BF16; }  // q, out, new rows
-bool pool_dtype_ok(pa_dtype t) { return dtype_ok(t) || t == PA_FP8_E4M3; }
-int esize(pa_dtype t) { return t == PA_FP8_E4M3 ? 1 : t == PA_BF16 ? 2 : 4; }
-// dequantisation scales: finite and positive
-bool scale_ok(float s) { return s > 0.f && s <= 3.402823466e38f; }
-
-pa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ECUDA; }
 
 // Fast path of the attention kernels: bf16 q and pool, head size 64 or 128, 16-position
 // blocks, TMA-compatible pool addresses.

@@ -37,6 +37,36 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 }
 
 // ------------------------------------------------------------------------------------------
+// block-wide helpers
+
+// Exclusive prefix sum of one int per thread across the block; *total receives the sum.
+__device__ __forceinline__ int block_exclusive_scan(int v, int* s_warp, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int w = lane < nwarps ? s_warp[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  const int before = warp ? s_warp[warp - 1] : 0;
+  *total = s_warp[nwarps - 1];
+  __syncthreads();
+  return before + x - v;
+}
+
+// ------------------------------------------------------------------------------------------
 // shared memory, mbarriers, TMA
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -458,6 +488,9 @@ cudaError_t launch_reshape_and_cache_convert(const void* k, const void* v, void*
                                              int32_t head_dim, int* status, cudaStream_t stream,
                                              const float* k_bscales = nullptr,
                                              const float* v_bscales = nullptr);
+// Records PA_EINVAL when a slot lies outside [0, num_slots).
+cudaError_t launch_validate_slots(const int32_t* slots, int64_t num_tokens, int64_t num_slots,
+                                  int* status, cudaStream_t stream);
 // Records PA_EINVAL when a per-head scale (either array may be null) is not finite and > 0.
 cudaError_t launch_validate_scales(const float* k_scales, const float* v_scales,
                                    int32_t num_kv_heads, int* status, cudaStream_t stream);
@@ -486,6 +519,119 @@ cudaError_t launch_merge_attn_states(void* out, float* out_lse, const void* pref
                                      const float* suffix_lse, int64_t num_tokens,
                                      int32_t num_heads, int32_t head_dim, int64_t prefix_tokens,
                                      int bf16, int* status, cudaStream_t stream);
+
+// ---- speculative decoding: rotary caching, tree attention, pages ---------------------------
+
+struct RopeParams {
+  const void* q;  // [T, H, D], tokens q_stride elements apart; null: keys and values only
+  void* q_out;
+  const void* k;
+  const void* v;
+  void* k_blocks;
+  void* v_blocks;
+  int64_t q_stride, q_out_stride, k_stride, v_stride;  // elements between tokens
+  const int32_t* positions;
+  const int32_t* slots;
+  const double* inv_freq;  // [rotary_dim / 2] radians per position
+  int32_t rotary_dim, interleaved;
+  float attn_factor;
+  int64_t num_tokens, num_slots;
+  int32_t num_heads, num_kv_heads, head_dim;
+  float k_scale, v_scale;
+  const float* k_scales;  // per kv head, or null
+  const float* v_scales;
+  int* status;
+};
+cudaError_t launch_rope_and_cache(const RopeParams& p, pa_dtype src_dtype, pa_dtype kv_dtype,
+                                  int num_sms, cudaStream_t stream);
+
+// page bookkeeping: block tables, per-block reference counts, the stack of free block ids
+struct PagesParams {
+  int32_t* block_tables;  // [num_rows, max_blocks]
+  int32_t* seq_lens;      // [num_rows]
+  const int32_t* rows;    // fork: parents; grow, free: the sequences
+  const int32_t* other;   // fork: children; grow: new lengths
+  int32_t* block_pairs;   // fork: [count, 2] out
+  int32_t* ref_counts;    // [num_blocks]
+  int32_t* free_list;     // [num_blocks]
+  int32_t* free_count;    // [1]
+  int32_t count, num_rows, max_blocks, block_size;
+  int64_t num_blocks;
+  int* status;
+};
+enum { PAGES_FORK = 0, PAGES_GROW = 1, PAGES_FREE = 2 };
+constexpr int32_t kMaxPageRows = 65536;        // rows of a block table these calls take
+constexpr int64_t kMaxTrackedBlocks = 1 << 23;  // blocks their bitmaps cover
+cudaError_t launch_pages(int what, const PagesParams& p, cudaStream_t stream);
+// Copy blocks src -> dst of both pools (v_blocks may be null).
+constexpr int64_t kFusedPairs = 256;  // lists up to this long are checked by the copy itself
+cudaError_t launch_copy_blocks(void* k_blocks, void* v_blocks, const int32_t* pairs,
+                               int64_t num_pairs, int64_t block_bytes, int64_t num_blocks,
+                               int* status, int num_sms, cudaStream_t stream);
+cudaError_t launch_tree_commit(void* k_blocks, void* v_blocks, const int32_t* block_tables,
+                               const int32_t* context_lens, const int32_t* accepted,
+                               const int32_t* num_accepted, int32_t num_seqs,
+                               int32_t max_accepted, int32_t max_blocks, int64_t row_bytes,
+                               int32_t block_size, int64_t num_blocks, int* status,
+                               cudaStream_t stream);
+
+// Tree attention.  A work item is (sequence, kv head, up to rows_per_item consecutive query rows;
+// a row is (node, head of the group), node-major) over the sequence's key tiles.  The items'
+// tiles, laid end to end in the order (sequence, kv head, rows), are cut into equal weights, one
+// contiguous range per CTA; an item cut between CTAs leaves a partial softmax state per piece,
+// which the merge kernel joins in key order.
+struct TreeParams {
+  const void* q;
+  const void* k_blocks;
+  const void* v_blocks;
+  void* out;
+  VarlenMeta m;
+  const int32_t* mask;  // [T, mask_words] bit i: node i of the token's sequence is visible
+  int32_t mask_words;
+  float scale;  // softmax scale, k_scale included
+  int32_t rows_per_item, key_tile;
+  int32_t grid;     // CTAs the work is cut for
+  int4* seqs;       // [num_seqs] (first token, nodes, seq_len, first key); nodes 0: no work
+  int64_t* cum;     // [num_seqs + 1] weight before the sequence
+  int4* starts;     // [grid + 1] (sequence, item, key tile, 0) where each CTA's range begins
+  float2* part_ml;  // [2 * grid, rows_per_item] running max (log2 units) and exp-sum
+  float* part_o;    // [2 * grid, rows_per_item, head_dim] unnormalised outputs
+  int* status;
+  int32_t q_bf16, out_vec;
+};
+// One 128-row tile of an item costs two units of weight a key tile, two such tiles three (they
+// share the keys' copies).
+constexpr int kTreeTileRows = 128;
+__host__ __device__ inline int tree_weight(int rows) { return rows > kTreeTileRows ? 3 : 2; }
+struct TreeLayout {
+  int64_t cum_off, starts_off, ml_off, o_off, bytes;
+  int32_t grid;
+};
+TreeLayout tree_layout(int32_t num_seqs, int64_t num_tokens, int32_t group, int32_t num_kv_heads,
+                       int32_t head_dim, int64_t max_keys, int32_t rows_per_item,
+                       int32_t key_tile, int32_t max_grid);
+constexpr int32_t kTreeMaxMaskWords = 64;  // 2048 nodes to a tree
+constexpr int32_t kTreeGenericRows = 32, kTreeGenericKeys = 32, kTreeGenericGrid = 608;
+cudaError_t launch_tree_plan(const TreeParams& p, cudaStream_t stream);
+cudaError_t launch_tree_generic(const TreeParams& p, pa_dtype kv_dtype, cudaStream_t stream);
+cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t stream);
+
+// Status word and SM count of the current device, cached per context; null on a CUDA error.
+struct DeviceState {
+  void* ctx = nullptr;  // the context the address below was looked up in
+  int* status = nullptr;
+  int sms = 0;
+};
+const DeviceState* device_state();
+
+// argument checks shared by the entry points
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline bool dtype_ok(pa_dtype t) { return t == PA_F32 || t == PA_BF16; }  // q, out, new rows
+inline bool pool_dtype_ok(pa_dtype t) { return dtype_ok(t) || t == PA_FP8_E4M3; }
+inline int esize(pa_dtype t) { return t == PA_FP8_E4M3 ? 1 : t == PA_BF16 ? 2 : 4; }
+// dequantisation scales: finite and positive
+inline bool scale_ok(float s) { return s > 0.f && s <= 3.402823466e38f; }
+inline pa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ECUDA; }
 
 int num_sms();  // SM count of the current device (cached)
 void* current_context();  // the calling thread's current driver context (CUcontext), or null
