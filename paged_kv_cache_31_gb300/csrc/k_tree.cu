@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(const TreeParams p) 
       const int64_t rows = (int64_t)nodes * m.group;
       const int64_t full = rows / p.rows_per_item;
       const int rest = (int)(rows % p.rows_per_item);
-      weight = (full * tree_weight(p.rows_per_item) + (rest ? tree_weight(rest) : 0)) *
+      weight = (full * tree_weight(p, p.rows_per_item) + (rest ? tree_weight(p, rest) : 0)) *
                m.num_kv_heads * tiles;
     } else if (s < m.num_seqs) {
       p.seqs[s] = make_int4(0, 0, 0, 0);
@@ -178,10 +178,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(const TreeParams p) 
       const int64_t per_head = g.weight_before(g.items) * g.tiles;
       const int kvh = (int)(rem / per_head);
       const int64_t r = rem % per_head;
-      const int full_w = tree_weight(p.rows_per_item);
+      const int full_w = tree_weight(p, p.rows_per_item);
       const int it = min((int)(r / ((int64_t)full_w * g.tiles)), g.items - 1);
       const int64_t in = r - (int64_t)it * full_w * g.tiles;
-      const int w = tree_weight(g.rows_of(p, it));
+      const int w = tree_weight(p, g.rows_of(p, it));
       st = make_int4(lo, kvh * g.items + it, min((int)(in / w), g.tiles - 1), 0);
     }
     p.starts[c] = st;

@@ -16,8 +16,8 @@ struct TreeGeometry {
     rows = q.y * p.m.group;
     items = (rows + p.rows_per_item - 1) / p.rows_per_item;
     tiles = (q.z - q.w + p.key_tile - 1) / p.key_tile;
-    full_w = tree_weight(p.rows_per_item);
-    rest_w = items ? tree_weight(rows - (items - 1) * p.rows_per_item) : 0;
+    full_w = tree_weight(p, p.rows_per_item);
+    rest_w = items ? tree_weight(p, rows - (items - 1) * p.rows_per_item) : 0;
   }
   __device__ __forceinline__ int rows_of(const TreeParams& p, int item) const {
     return min(p.rows_per_item, rows - item * p.rows_per_item);

@@ -82,6 +82,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 // TMA descriptor of a bf16 pool [num_blocks, 16, Hkv, D] seen as the 3-D tensor
 // (D, Hkv, num_blocks * 16) with a 64 x 1 x 16 box and the 128-byte swizzle.
 bool pool_map(CUtensorMap* map, const void* base, int64_t num_blocks, int block_size, int hkv,
@@ -115,6 +117,8 @@ bool pool_map_fp8(CUtensorMap* map, const void* base, int64_t num_blocks, int bl
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+namespace {
+
 // The same byte tensor with a 64 x 1 x 16 box and no swizzle: the 64 dims of one half of a
 // head size of 128 for one (block, kv head), 1 KB of plain 64-byte rows (the tcgen05 prefill
 // kernel's V part of a CTA).
@@ -132,15 +136,18 @@ bool pool_map_fp8_half(CUtensorMap* map, const void* base, int64_t num_blocks, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// TMA descriptor of q [T, H, D] bf16 seen as the 3-D tensor (D, H, T): a 64 x G x 128/G box
-// is the 64-dim half of a 128-row query tile whose rows are the G heads of one kv head for
-// 128/G consecutive tokens.
-bool query_map(CUtensorMap* map, const void* q, int64_t num_tokens, int h, int d, int group) {
+}  // namespace
+
+// TMA descriptor of q [T, H, D] bf16 seen as the 3-D tensor (D, H, T): a 64 x G x `tokens` box
+// is the 64-dim half of a query tile whose rows are the G heads of one kv head for `tokens`
+// consecutive tokens.
+bool query_map(CUtensorMap* map, const void* q, int64_t num_tokens, int h, int d, int group,
+               int tokens) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)h, (cuuint64_t)num_tokens};
   cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)h * d * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)};
+  cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tokens};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -176,6 +183,9 @@ void stall_hook(uint64_t& limit, uint32_t& stall) {
     }
   }
 }
+
+namespace {
+
 void mma_waits(Mma16Params& p) { stall_hook(p.wait_limit_ns, p.debug_stall); }
 
 // Fast path of the attention kernels: bf16 q and pool, head size 64 or 128, 16-position
@@ -534,7 +544,7 @@ static pa_status varlen_impl(const void* q, const void* k_blocks, const void* v_
     mma_waits(p);
     if (L.use_tc) {
       CUtensorMap tq, tv_half;
-      if (!query_map(&tq, q, num_tokens, num_heads, head_dim, m.group) ||
+      if (!query_map(&tq, q, num_tokens, num_heads, head_dim, m.group, 128 / m.group) ||
           !pool_map_fp8_half(&tv_half, v_blocks, num_blocks, block_size, num_kv_heads, head_dim))
         return PA_ECUDA;
       TcParams tp;
@@ -580,7 +590,7 @@ static pa_status varlen_impl(const void* q, const void* k_blocks, const void* v_
       // SMs the tcgen05 kernel leaves free; after that kernel it recomputes the items the
       // tcgen05 kernel marked (V outside f16's range)
       CUtensorMap tq;
-      if (!query_map(&tq, q, num_tokens, num_heads, head_dim, m.group)) return PA_ECUDA;
+      if (!query_map(&tq, q, num_tokens, num_heads, head_dim, m.group, 128 / m.group)) return PA_ECUDA;
       TcParams tp;
       std::memset(&tp, 0, sizeof tp);
       tp.out = out;

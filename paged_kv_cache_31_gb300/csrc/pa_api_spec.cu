@@ -120,6 +120,18 @@ pa_status pa_rope_and_cache(const void* q, int64_t q_stride, void* q_out, int64_
   return from_cuda(launch_rope_and_cache(p, src_dtype, kv_dtype, d->sms, stream));
 }
 
+// Rows of one row tile of the tensor-core kernel: whole nodes, at most 128 rows.
+static int32_t tree_tile_rows(int32_t group) { return 128 / group * group; }
+
+// Layout of a call on the tensor-core kernel: items of one row tile when no sequence can have
+// more rows (mask_words bounds a tree), else of two.
+static TreeLayout tree_tc_layout(int32_t num_seqs, int64_t num_tokens, int32_t group,
+                                 int32_t num_kv_heads, int32_t head_dim, int64_t max_keys,
+                                 int32_t rows_per_item) {
+  return tree_layout(num_seqs, num_tokens, group, num_kv_heads, head_dim, max_keys, rows_per_item,
+                     kTreeTcKeys, kTreeTcGrid);
+}
+
 size_t pa_tree_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads,
                                         int32_t num_kv_heads, int32_t head_dim,
                                         int32_t max_blocks_per_seq, int32_t block_size) {
@@ -129,7 +141,15 @@ size_t pa_tree_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, in
   const TreeLayout L = tree_layout(num_seqs, num_tokens, num_heads / num_kv_heads, num_kv_heads,
                                    head_dim, (int64_t)max_blocks_per_seq * block_size,
                                    kTreeGenericRows, kTreeGenericKeys, kTreeGenericGrid);
-  return (size_t)L.bytes;
+  int64_t bytes = L.bytes;
+  const int32_t group = num_heads / num_kv_heads;
+  if (group <= 128 && (head_dim == 64 || head_dim == 128))  // the tensor-core kernel may run
+    for (int tiles = 1; tiles <= 2; ++tiles)
+      bytes = std::max(bytes, tree_tc_layout(num_seqs, num_tokens, group, num_kv_heads, head_dim,
+                                             (int64_t)max_blocks_per_seq * block_size,
+                                             tiles * tree_tile_rows(group))
+                                  .bytes);
+  return (size_t)bytes;
 }
 
 pa_status pa_tree_attention(const void* q, const void* k_blocks, const void* v_blocks, void* out,
@@ -200,11 +220,31 @@ pa_status pa_tree_attention(const void* q, const void* k_blocks, const void* v_b
   p.scale = scale * k_scale;
   p.status = d->status;
   p.q_bf16 = q_dtype == PA_BF16;
-  p.rows_per_item = kTreeGenericRows;
-  p.key_tile = kTreeGenericKeys;
-  const TreeLayout L = tree_layout(num_seqs, num_tokens, m.group, num_kv_heads, head_dim,
-                                   (int64_t)max_blocks_per_seq * block_size, p.rows_per_item,
-                                   p.key_tile, kTreeGenericGrid);
+  const int64_t max_keys = (int64_t)max_blocks_per_seq * block_size;
+  const bool fp8 = kv_dtype == PA_FP8_E4M3;
+  // the tensor-core kernel: bf16 q over bf16 or e4m3 pools of 16-position blocks, a group that
+  // fits a row tile, tensors aligned for TMA, and a positive scale (its row maxima are taken
+  // before the scale)
+  const bool tc = q_dtype == PA_BF16 && block_size == 16 && m.group <= 128 &&
+                  (fp8 ? head_dim == 128
+                       : kv_dtype == PA_BF16 && (head_dim == 64 || head_dim == 128)) &&
+                  aligned(q, 16) && aligned(out, 16) && aligned(k_blocks, 16) &&
+                  aligned(v_blocks, 16) && p.scale > 0.f && num_blocks > 0 && tc_enabled();
+  TreeLayout L;
+  if (tc) {
+    p.tile_rows = tree_tile_rows(m.group);
+    const int64_t most = std::min<int64_t>(32 * (int64_t)mask_words, num_tokens) * m.group;
+    p.rows_per_item = most > p.tile_rows ? 2 * p.tile_rows : p.tile_rows;
+    p.key_tile = kTreeTcKeys;
+    L = tree_tc_layout(num_seqs, num_tokens, m.group, num_kv_heads, head_dim, max_keys,
+                       p.rows_per_item);
+    L.grid = std::min(L.grid, d->sms);  // (a smaller grid uses less of each part of the workspace)
+  } else {
+    p.tile_rows = p.rows_per_item = kTreeGenericRows;
+    p.key_tile = kTreeGenericKeys;
+    L = tree_layout(num_seqs, num_tokens, m.group, num_kv_heads, head_dim, max_keys,
+                    p.rows_per_item, p.key_tile, kTreeGenericGrid);
+  }
   p.grid = L.grid;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.seqs = reinterpret_cast<int4*>(ws);
@@ -212,8 +252,25 @@ pa_status pa_tree_attention(const void* q, const void* k_blocks, const void* v_b
   p.starts = reinterpret_cast<int4*>(ws + L.starts_off);
   p.part_ml = reinterpret_cast<float2*>(ws + L.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + L.o_off);
+  CUtensorMap tq, tk, tv;
+  if (tc) {
+    const bool ok =
+        query_map(&tq, q, num_tokens, num_heads, head_dim, m.group, p.tile_rows / m.group) &&
+        (fp8 ? pool_map_fp8(&tk, k_blocks, num_blocks, 16, num_kv_heads, head_dim) &&
+                   pool_map_fp8(&tv, v_blocks, num_blocks, 16, num_kv_heads, head_dim)
+             : pool_map(&tk, k_blocks, num_blocks, 16, num_kv_heads, head_dim) &&
+                   pool_map(&tv, v_blocks, num_blocks, 16, num_kv_heads, head_dim));
+    if (!ok) return PA_ECUDA;
+  }
   if (launch_tree_plan(p, stream) != cudaSuccess) return PA_ECUDA;
-  if (launch_tree_generic(p, kv_dtype, stream) != cudaSuccess) return PA_ECUDA;
+  if (tc) {
+    uint64_t limit;
+    uint32_t stall;
+    stall_hook(limit, stall);
+    if (launch_tree_tc(tq, tk, tv, p, fp8, limit, stall, stream) != cudaSuccess) return PA_ECUDA;
+  } else if (launch_tree_generic(p, kv_dtype, stream) != cudaSuccess) {
+    return PA_ECUDA;
+  }
   return from_cuda(launch_tree_merge(p, stream));
 }
 

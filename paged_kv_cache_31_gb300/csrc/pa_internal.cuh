@@ -590,6 +590,7 @@ struct TreeParams {
   int32_t mask_words;
   float scale;  // softmax scale, k_scale included
   int32_t rows_per_item, key_tile;
+  int32_t tile_rows;  // rows of one row tile (whole nodes); an item is one tile or two
   int32_t grid;     // CTAs the work is cut for
   int4* seqs;       // [num_seqs] (first token, nodes, seq_len, first key); nodes 0: no work
   int64_t* cum;     // [num_seqs + 1] weight before the sequence
@@ -599,10 +600,11 @@ struct TreeParams {
   int* status;
   int32_t q_bf16, out_vec;
 };
-// One 128-row tile of an item costs two units of weight a key tile, two such tiles three (they
-// share the keys' copies).
-constexpr int kTreeTileRows = 128;
-__host__ __device__ inline int tree_weight(int rows) { return rows > kTreeTileRows ? 3 : 2; }
+// An item of one row tile costs two units of weight a key tile, one of two tiles three (they share
+// the keys' copies).
+__host__ __device__ inline int tree_weight(const TreeParams& p, int rows) {
+  return rows > p.tile_rows ? 3 : 2;
+}
 struct TreeLayout {
   int64_t cum_off, starts_off, ml_off, o_off, bytes;
   int32_t grid;
@@ -614,6 +616,11 @@ constexpr int32_t kTreeMaxMaskWords = 64;  // 2048 nodes to a tree
 constexpr int32_t kTreeGenericRows = 32, kTreeGenericKeys = 32, kTreeGenericGrid = 608;
 cudaError_t launch_tree_plan(const TreeParams& p, cudaStream_t stream);
 cudaError_t launch_tree_generic(const TreeParams& p, pa_dtype kv_dtype, cudaStream_t stream);
+constexpr int32_t kTreeTcKeys = 128, kTreeTcGrid = 152;
+// tq: box 64 x group x tile_rows / group of q; tk, tv: the pools' block boxes
+cudaError_t launch_tree_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           const TreeParams& p, bool fp8, uint64_t wait_limit, uint32_t stall,
+                           cudaStream_t stream);
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t stream);
 
 // Status word and SM count of the current device, cached per context; null on a CUDA error.
@@ -623,6 +630,16 @@ struct DeviceState {
   int sms = 0;
 };
 const DeviceState* device_state();
+
+// tensor maps (false: the driver refused), waits and paths of the attention kernels; see pa_api.cu
+bool pool_map(CUtensorMap* map, const void* base, int64_t num_blocks, int block_size, int hkv,
+              int d);
+bool pool_map_fp8(CUtensorMap* map, const void* base, int64_t num_blocks, int block_size,
+                  int hkv, int d);
+bool query_map(CUtensorMap* map, const void* q, int64_t num_tokens, int h, int d, int group,
+               int tokens);
+void stall_hook(uint64_t& limit, uint32_t& stall);
+bool tc_enabled();
 
 // argument checks shared by the entry points
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
