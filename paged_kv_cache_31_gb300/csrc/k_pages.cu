@@ -7,9 +7,10 @@
 //
 // Bookkeeping (k_pages).  A few hundred to some 10^5 integers: bound by the latency of its
 // dependent loads, not by bandwidth, so one cluster of eight CTAs does a whole call in one
-// launch.  Its phases (check everything, then write) are separated by cluster barriers, so an
-// error leaves every array as it was, and no workspace is needed: the set of blocks whose last
-// reference goes away is a bitmap spread over the eight CTAs' shared memory.  The blocks a
+// launch.  Its phases are separated by cluster barriers: everything is checked, and the reference
+// counts are changed, before anything else is written; an error then takes the changes of the
+// counts back, so it leaves every array as it was.  No workspace is needed: the set of blocks
+// whose last reference goes away is a bitmap spread over the CTAs' shared memory.  The blocks a
 // call takes or gives back are numbered by prefix sums, never by the order in which atomics
 // arrive, so equal inputs give equal tables and free lists.  Only the reference counts are
 // changed by atomics (integer additions, whose order does not matter).
@@ -198,7 +199,7 @@ __device__ __forceinline__ bool accepted_ok(const int32_t* tables, const int32_t
   return x >= 0 && (int64_t)x < num_blocks && y >= 0 && (int64_t)y < num_blocks;
 }
 
-constexpr int kFusedAccepted = 2048;  // lists up to this many entries: every CTA checks them all
+constexpr int kFusedAccepted = 256;  // lists up to this many entries: every CTA checks them all
 
 __global__ void __launch_bounds__(256)
     k_check_accepted(const int32_t* tables, const int32_t* ctx, const int32_t* accepted,
@@ -301,17 +302,20 @@ constexpr int kChunk = 256;  // table entries a warp takes at a time, eight per 
 struct PagesShared {
   int bad;      // CTA 0's: any CTA found an error
   int scan[32];
-  int total;    // blocks taken (fork, grow) / freed by this CTA (free)
+  int total;    // blocks freed by this CTA (free)
   int off[kPagesThreads + 1];  // chunk offsets of this round's items
   int entries[kPagesThreads];  // table entries of the item that are walked
   int from[kPagesThreads];     // table row that is read
-  int to[kPagesThreads];       // fork: table row that is written
+  int to[kPagesThreads];       // fork: table row that is written; grow: the first new entry
   int taken[kPagesThreads];    // fork, grow: blocks taken before the item
+  int refs[kPagesThreads];     // fork: the round's forks of this parent, at its first fork (else 0)
   uint32_t rows[kMaxPageRows / 32];
 };
 
 // WHAT: PAGES_FORK, PAGES_GROW or PAGES_FREE.  Items (forks, or sequences) go in rounds of up to
 // 1024; a round's table entries are cut into chunks of 256, dealt to all warps of the cluster.
+// Reference counts are the scattered accesses (a sector each), which is what a large call takes
+// its time for; a parent's are read and raised once per round, whatever its number of forks.
 template <int WHAT>
 __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, uint32_t words) {
   extern __shared__ __align__(16) uint8_t s_raw[];
@@ -324,36 +328,41 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
   // (one thread of the cluster reads the status word: another stream's call may set it meanwhile)
   if (tid == 0) sh.bad = rank == 0 && status_set(p.status) ? 2 : 0;
   if (WHAT == PAGES_FREE) gone.clear();
-  for (int i = tid; i < (p.num_rows + 31) / 32; i += kPagesThreads) sh.rows[i] = 0;
+  if (rank == 0)
+    for (int i = tid; i < (p.num_rows + 31) / 32; i += kPagesThreads) sh.rows[i] = 0;
   const int have_free = *p.free_count;
   cluster_sync();
   const uint32_t flag = peer_addr(&sh.bad, 0);
+  if (peer_load(flag)) {  // an earlier error: nothing is done
+    cluster_sync();       // (CTA 0 stays until every CTA has read its flag)
+    return;
+  }
   bool bad = have_free < 0 || (int64_t)have_free > p.num_blocks;
 
   auto blocks_of = [&](int n) { return (int)(((int64_t)n + b - 1) / b); };
   auto in_pool = [&](int id) { return id >= 0 && (int64_t)id < p.num_blocks; };
   // Items r0 .. r0 + K - 1 into shared memory; returns the chunks to walk.  `taken` counts on
   // from `base` (blocks taken in earlier rounds), which is advanced.
-  auto load_round = [&](int r0, int& base) {
+  auto load_round = [&](int r0, int& base, bool group = false) {
     const int K = min(kPagesThreads, p.count - r0);
-    int entries = 0, take = 0, row = 0, to = 0;
+    int entries = 0, take = 0, row = -1, to = 0;
     if (tid < K) {
       row = p.rows[r0 + tid];
+      if (WHAT != PAGES_FREE) to = p.other[r0 + tid];
       if (row >= 0 && row < p.num_rows) {
         const int n = p.seq_lens[row];
         if (n < 0 || blocks_of(n) > p.max_blocks) {
           bad = true;
         } else if (WHAT == PAGES_FORK) {
-          to = p.other[r0 + tid];
           entries = blocks_of(n);
           take = n % b != 0;
         } else if (WHAT == PAGES_GROW) {
-          const int want = p.other[r0 + tid];
+          const int want = to;
           if (want < n || blocks_of(want) > p.max_blocks) {
             bad = true;
           } else {
             entries = take = blocks_of(want) - blocks_of(n);
-            to = blocks_of(n);  // the first new entry
+            to = blocks_of(n);
           }
         } else {
           entries = blocks_of(n);
@@ -373,6 +382,18 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
     if (tid == 0) sh.off[kPagesThreads] = chunks;
     base += took;
     __syncthreads();
+    if (WHAT == PAGES_FORK && group) {  // forks of this parent in the round, told to the first of them
+      int same = 0;
+      bool first = true;
+      if (tid < K)
+        for (int i = 0; i < K; ++i) {
+          const bool e = sh.from[i] == row;
+          same += e;
+          first = first && !(e && i < tid);
+        }
+      sh.refs[tid] = first ? same : 0;
+      __syncthreads();
+    }
     return chunks;
   };
   // f(item, first entry, entries) for this warp's chunks of the round
@@ -387,8 +408,47 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
     }
     __syncthreads();  // the next round reuses the arrays
   };
+  // Adds sign (-1: takes back) times the call's change to the reference counts of the table
+  // entries it holds on to (fork: all but a partly filled last one) or lets go; `bad` when an entry
+  // is not an id or its count cannot be right.
+  auto change_refs = [&](int sign) {
+    int none = 0;
+    for (int r0 = 0; r0 < p.count; r0 += kPagesThreads) {
+      const int K = min(kPagesThreads, p.count - r0);
+      const int chunks = load_round(r0, none, true);
+      walk(chunks, K, [&](int it, int e0, int n) {
+        const int by = WHAT == PAGES_FORK ? sh.refs[it] : -1;
+        if (by == 0) return;  // the parent's first fork does it
+        const bool part = WHAT == PAGES_FORK && p.seq_lens[sh.from[it]] % b != 0;
+        const int32_t* row = p.block_tables + (int64_t)sh.from[it] * p.max_blocks;
+        int id[8], old[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int e = e0 + lane + 32 * u;
+          id[u] = e < n ? row[e] : -1;
+          if (e < n && !in_pool(id[u])) bad = true;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          old[u] = 1;
+          if (!in_pool(id[u])) continue;
+          if (part && e0 + lane + 32 * u == n - 1)
+            old[u] = p.ref_counts[id[u]];
+          else
+            old[u] = atomicAdd(p.ref_counts + id[u], sign * by);
+        }
+        if (sign < 0) return;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          bad |= old[u] < 1;  // held without a reference, or freed more often than it is held
+          if (WHAT == PAGES_FREE && old[u] == 1 && in_pool(id[u])) gone.insert((uint32_t)id[u]);
+        }
+      });
+    }
+    return none;
+  };
 
-  // ---- check: rows distinct (CTA 0), then lengths, table entries and the blocks to take
+  // ---- rows distinct (CTA 0), lengths, table entries and their counts, the blocks to take
   if (rank == 0) {
     const int32_t* written = WHAT == PAGES_FORK ? p.other : p.rows;
     for (int i = tid; i < p.count; i += kPagesThreads) {
@@ -406,137 +466,95 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
       }
   }
   int taken = 0;
-  for (int r0 = 0; r0 < p.count; r0 += kPagesThreads) {
-    const int K = min(kPagesThreads, p.count - r0);
-    const int chunks = load_round(r0, taken);
-    walk(chunks, K, [&](int it, int e0, int n) {
-      int id[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int e = e0 + lane + 32 * u;
-        id[u] = 0;
-        if (e >= n) continue;
-        if (WHAT == PAGES_GROW) {
-          const int at = have_free - 1 - sh.taken[it] - e;
-          id[u] = at >= 0 && (int64_t)at < p.num_blocks ? p.free_list[at] : -1;
-        } else {
-          id[u] = p.block_tables[(int64_t)sh.from[it] * p.max_blocks + e];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        if (e0 + lane + 32 * u >= n) continue;
-        if (!in_pool(id[u]))
-          bad = true;
-        else if (WHAT == PAGES_FORK)
-          bad |= p.ref_counts[id[u]] < 1;
-        else if (WHAT == PAGES_GROW)
-          bad |= p.ref_counts[id[u]] != 0;
-      }
-    });
+  if (WHAT == PAGES_GROW) {
+    for (int r0 = 0; r0 < p.count; r0 += kPagesThreads) load_round(r0, taken);
+  } else {
+    taken = change_refs(1);
   }
-  if (WHAT != PAGES_FREE) bad |= taken > have_free;
-  if (WHAT == PAGES_FORK)  // the new pages of partly filled last blocks
+  if (WHAT != PAGES_FREE) {
+    bad |= taken > have_free;
     for (int i = rank * kPagesThreads + tid; i < taken; i += kCluster * kPagesThreads) {
       const int at = have_free - 1 - i;
       const int id = at >= 0 && (int64_t)at < p.num_blocks ? p.free_list[at] : -1;
       bad |= !in_pool(id) || p.ref_counts[id] != 0;
     }
+  }
   if (__syncthreads_or(bad) && tid == 0) peer_or(flag, 1u);
-  cluster_sync();
-  if (peer_load(flag)) {  // (an earlier error stays the recorded one)
-    if (rank == 0 && tid == 0) record_error(p.status, PA_EINVAL);
-    cluster_sync();  // CTA 0 stays until every CTA has read its flag
-    return;
-  }
-
-  // ---- write
-  taken = 0;
-  bad = false;
-  for (int r0 = 0; r0 < p.count; r0 += kPagesThreads) {
-    const int K = min(kPagesThreads, p.count - r0);
-    const int chunks = load_round(r0, taken);
-    // (with several rounds the lengths are written after the last of them: a parent's is read
-    // in every round)
-    walk(chunks, K, [&](int it, int e0, int n) {
-      const int64_t row = (int64_t)sh.from[it] * p.max_blocks;
-      int id[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int e = e0 + lane + 32 * u;
-        if (e >= n) continue;
-        id[u] = WHAT == PAGES_GROW ? p.free_list[have_free - 1 - sh.taken[it] - e]
-                                   : p.block_tables[row + e];
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int e = e0 + lane + 32 * u;
-        if (e >= n) continue;
-        if (WHAT == PAGES_GROW) {
-          p.block_tables[row + sh.to[it] + e] = id[u];
-          p.ref_counts[id[u]] = 1;
-        } else if (WHAT == PAGES_FORK) {
-          int32_t* child = p.block_tables + (int64_t)sh.to[it] * p.max_blocks + e;
-          if (e + 1 == n && p.seq_lens[sh.from[it]] % b != 0) {  // partly filled: a new page
-            const int page = p.free_list[have_free - 1 - sh.taken[it]];
-            *child = page;
-            p.ref_counts[page] = 1;
-            p.block_pairs[2 * (r0 + it)] = id[u];
-            p.block_pairs[2 * (r0 + it) + 1] = page;
-          } else {
-            *child = id[u];
-            atomicAdd(p.ref_counts + id[u], 1);
-          }
-        } else {
-          const int old = atomicSub(p.ref_counts + id[u], 1);
-          if (old == 1) gone.insert((uint32_t)id[u]);
-          bad |= old < 1;  // freed more often than it is held
-        }
-      }
-    });
-  }
-  if (WHAT == PAGES_FORK)  // forks of whole blocks copy nothing
-    for (int i = rank * kPagesThreads + tid; i < p.count; i += kCluster * kPagesThreads)
-      if (p.seq_lens[p.rows[i]] % b == 0) p.block_pairs[2 * i] = p.block_pairs[2 * i + 1] = -1;
-
+  cluster_sync();  // (free: every reference is dropped and the set complete)
+  bool undo = peer_load(flag) != 0;
+  int at = 0;
+  const uint32_t per = (words + kPagesThreads - 1) / kPagesThreads;
+  const uint32_t w0 = min(tid * per, words), w1 = min(w0 + per, words);
   if (WHAT == PAGES_FREE) {
-    if (__syncthreads_or(bad) && tid == 0) peer_or(flag, 1u);
-    cluster_sync();  // every reference is dropped, the set is complete
     // freed ids in ascending order: this CTA's words, a contiguous run per thread
-    const uint32_t per = (words + kPagesThreads - 1) / kPagesThreads;
-    const uint32_t w0 = min(tid * per, words), w1 = min(w0 + per, words);
     int mine = 0;
     for (uint32_t w = w0; w < w1; ++w) mine += __popc(gone.mine[w]);
     int total;
-    int at = block_exclusive_scan(mine, sh.scan, &total);
+    at = block_exclusive_scan(mine, sh.scan, &total);
     if (tid == 0) sh.total = total;
     cluster_sync();
     int before = 0, all = 0;
+#pragma unroll
     for (int r = 0; r < kCluster; ++r) {
       const int t = (int)peer_load(peer_addr(&sh.total, r));
       if (r < rank) before += t;
       all += t;
     }
-    const bool undo = peer_load(flag) != 0 || (int64_t)have_free + all > p.num_blocks;
-    if (undo) {  // nothing else has been written yet: put the references back
-      int none = 0;
-      for (int r0 = 0; r0 < p.count; r0 += kPagesThreads) {
-        const int K = min(kPagesThreads, p.count - r0);
-        const int chunks = load_round(r0, none);
-        walk(chunks, K, [&](int it, int e0, int n) {
-          for (int e = e0 + lane; e < min(n, e0 + kChunk); e += 32)
-            atomicAdd(p.ref_counts + p.block_tables[(int64_t)sh.from[it] * p.max_blocks + e], 1);
-        });
-      }
-      if (rank == 0 && tid == 0) record_error(p.status, PA_EINVAL);
-      cluster_sync();
-      return;
-    }
     at += have_free + before;
+    taken = -all;
+    undo |= (int64_t)have_free + all > p.num_blocks;
+  }
+  if (undo) {
+    if (WHAT != PAGES_GROW) change_refs(-1);
+    if (rank == 0 && tid == 0) record_error(p.status, PA_EINVAL);
+    cluster_sync();  // no CTA leaves while another may read its shared memory
+    return;
+  }
+
+  // ---- write
+  if (WHAT == PAGES_FREE) {
     for (uint32_t w = w0; w < w1; ++w)
       for (uint32_t m = gone.mine[w]; m; m &= m - 1)
         p.free_list[at++] = (int)(((uint32_t)rank * words + w) * 32 + __ffs(m) - 1);
-    taken = -all;
+  } else {
+    int base = 0;
+    for (int r0 = 0; r0 < p.count; r0 += kPagesThreads) {
+      const int K = min(kPagesThreads, p.count - r0);
+      const int chunks = load_round(r0, base);
+      walk(chunks, K, [&](int it, int e0, int n) {
+        const int64_t row = (int64_t)sh.from[it] * p.max_blocks;
+        const bool part = WHAT == PAGES_FORK && p.seq_lens[sh.from[it]] % b != 0;
+        int id[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int e = e0 + lane + 32 * u;
+          if (e >= n) continue;
+          id[u] = WHAT == PAGES_GROW ? p.free_list[have_free - 1 - sh.taken[it] - e]
+                                     : p.block_tables[row + e];
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int e = e0 + lane + 32 * u;
+          if (e >= n) continue;
+          if (WHAT == PAGES_GROW) {
+            p.block_tables[row + sh.to[it] + e] = id[u];
+            p.ref_counts[id[u]] = 1;
+          } else {
+            int page = id[u];
+            if (part && e == n - 1) {  // partly filled: a new page
+              page = p.free_list[have_free - 1 - sh.taken[it]];
+              p.ref_counts[page] = 1;
+              p.block_pairs[2 * (r0 + it)] = id[u];
+              p.block_pairs[2 * (r0 + it) + 1] = page;
+            }
+            p.block_tables[(int64_t)sh.to[it] * p.max_blocks + e] = page;
+          }
+        }
+      });
+    }
+    if (WHAT == PAGES_FORK)  // forks of whole blocks copy nothing
+      for (int i = rank * kPagesThreads + tid; i < p.count; i += kCluster * kPagesThreads)
+        if (p.seq_lens[p.rows[i]] % b == 0) p.block_pairs[2 * i] = p.block_pairs[2 * i + 1] = -1;
   }
   cluster_sync();  // every CTA has read the lengths and the count
   for (int i = rank * kPagesThreads + tid; i < p.count; i += kCluster * kPagesThreads) {

@@ -17,9 +17,9 @@
 // What bounds it: memory.  Every element of q, k and v is read once and written once, 16 bytes
 // at a time; a rotated half-layout unit is the two 16-byte chunks of its pairs, so a thread
 // has both sides of each pair in registers.  A CTA takes TOK tokens; their angles are computed
-// once into shared memory and serve all H + Hkv heads.  The items of the CTA's tokens (rotated
-// units, copied chunks and value chunks) are dealt to the threads in memory order, with four
-// items' loads in flight per thread.
+// once into shared memory and serve all H + Hkv heads.  The items of a token (rotated units, copied
+// chunks and value chunks) are dealt to the threads in memory order; a thread takes its item through
+// the CTA's tokens, four in flight.
 #include <algorithm>
 
 #include "pa_internal.cuh"
@@ -46,7 +46,7 @@ struct FastDiv {
 };
 
 struct Geometry {
-  FastDiv per_token;  // items of one token
+  uint32_t per_token;  // items of one token
   FastDiv per_head;   // items of a rotated head: rotated units, then copied chunks
   FastDiv per_v;      // value chunks of a kv head
   int rot_units;      // rotated units of a head
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads)
       bad |= s < 0 || (int64_t)s >= p.num_slots;
     }
     if (__syncthreads_or(bad)) {
-      if (blockIdx.x == 0 && threadIdx.x == 0) record_error(p.status, PA_EINVAL);
+      if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_error(p.status, PA_EINVAL);
       return;
     }
   }
@@ -155,89 +155,102 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
 
+  // an item's place in a token's rows is the same for all tokens of the CTA: worked out once, then
+  // the tokens go through it U at a time
   const int H = p.q ? p.num_heads : 0, D = p.head_dim, R = p.rotary_dim;
   const int rot_items = (H + p.num_kv_heads) * (int)g.per_head.d;
-  const TS* q = static_cast<const TS*>(p.q);
-  const TS* k = static_cast<const TS*>(p.k);
-  const TS* v = static_cast<const TS*>(p.v);
-  const int total = ntok * (int)g.per_token.d;
-  constexpr int U = VE == 1 || VE == 2 ? 2 : 4;  // items in flight
-  for (int it0 = threadIdx.x; it0 < total; it0 += U * kThreads) {
-    float a[U][VE], b[U][VE];
-    int tk[U], head[U], off[U];  // head: 0 .. H - 1 q, then k, then v heads
-    bool rot[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int it = it0 + u * kThreads;
-      tk[u] = -1;
-      rot[u] = false;
-      if (it >= total) continue;
-      tk[u] = (int)g.per_token.div((uint32_t)it);
-      const int r = it - tk[u] * (int)g.per_token.d;
-      const int64_t t = t0 + tk[u];
-      const TS* src;
-      if (r < rot_items) {
-        head[u] = (int)g.per_head.div((uint32_t)r);
-        const int e = r - head[u] * (int)g.per_head.d;
-        rot[u] = e < g.rot_units;
-        off[u] = rot[u] ? e * VE : R + (e - g.rot_units) * VE;
-        src = head[u] < H ? q + t * p.q_stride + (int64_t)head[u] * D
-                          : k + t * p.k_stride + (int64_t)(head[u] - H) * D;
-      } else {
-        const int hv = (int)g.per_v.div((uint32_t)(r - rot_items));
-        off[u] = (r - rot_items - hv * (int)g.per_v.d) * VE;
-        src = v + t * p.v_stride + (int64_t)hv * D;
-        head[u] = H + p.num_kv_heads + hv;
-      }
-      load_chunk<TS, VE>(src + off[u], a[u]);
-      if (!IL && rot[u]) load_chunk<TS, VE>(src + off[u] + half, b[u]);
+  constexpr int U = 4;
+  for (int it = blockIdx.y * kThreads + threadIdx.x; it < (int)g.per_token;
+       it += gridDim.y * kThreads) {
+    int head, off;
+    bool rot = false;
+    const TS* src;
+    int64_t stride;
+    if (it < rot_items) {
+      head = (int)g.per_head.div((uint32_t)it);
+      const int e = it - head * (int)g.per_head.d;
+      rot = e < g.rot_units;
+      off = rot ? e * VE : R + (e - g.rot_units) * VE;
+      const bool is_q = head < H;
+      src = is_q ? static_cast<const TS*>(p.q) + (int64_t)head * D
+                 : static_cast<const TS*>(p.k) + (int64_t)(head - H) * D;
+      stride = is_q ? p.q_stride : p.k_stride;
+    } else {
+      const int hv = (int)g.per_v.div((uint32_t)(it - rot_items));
+      off = (it - rot_items - hv * (int)g.per_v.d) * VE;
+      src = static_cast<const TS*>(p.v) + (int64_t)hv * D;
+      stride = p.v_stride;
+      head = H + p.num_kv_heads + hv;
     }
+    src += off + t0 * stride;
+    const bool two = !IL && rot;
+    const bool to_q = head < H, is_v = head >= H + p.num_kv_heads;
+    const int hk = head - H - (is_v ? p.num_kv_heads : 0);
+    float sc = 1.f, inv = 1.f;
+    bool divide = false;
+    if (!to_q) {
+      const float* scales = is_v ? p.v_scales : p.k_scales;
+      sc = scales ? __ldg(scales + hk) : is_v ? p.v_scale : p.k_scale;
+      // dividing by a power of two is multiplying by its inverse, to the bit
+      divide = (__float_as_uint(sc) & 0x7fffffu) != 0 || sc < 2.3283064e-10f || sc > 4294967296.f;
+      inv = divide ? 1.f : 1.f / sc;
+    }
+    for (int k0 = 0; k0 < ntok; k0 += U) {
+      float a[U][VE], b[U][VE];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (tk[u] < 0) continue;
-      if (rot[u]) {
-        const float* cs = s_cos + tk[u] * half + (IL ? off[u] / 2 : off[u]);
-        const float* sn = s_sin + tk[u] * half + (IL ? off[u] / 2 : off[u]);
-        if constexpr (IL) {
+      for (int u = 0; u < U; ++u) {
+        if (k0 + u >= ntok) break;
+        load_chunk<TS, VE>(src + (k0 + u) * stride, a[u]);
+        if (two) load_chunk<TS, VE>(src + (k0 + u) * stride + half, b[u]);
+      }
 #pragma unroll
-          for (int i = 0; i < VE / 2; ++i) {
-            const float x = a[u][2 * i], y = a[u][2 * i + 1];
-            a[u][2 * i] = x * cs[i] - y * sn[i];
-            a[u][2 * i + 1] = x * sn[i] + y * cs[i];
+      for (int u = 0; u < U; ++u) {
+        const int tk = k0 + u;
+        if (tk >= ntok) break;
+        if (rot) {
+          const float* cs = s_cos + tk * half + (IL ? off / 2 : off);
+          const float* sn = s_sin + tk * half + (IL ? off / 2 : off);
+          if constexpr (IL) {
+#pragma unroll
+            for (int i = 0; i < VE / 2; ++i) {
+              const float x = a[u][2 * i], y = a[u][2 * i + 1];
+              a[u][2 * i] = x * cs[i] - y * sn[i];
+              a[u][2 * i + 1] = x * sn[i] + y * cs[i];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+              const float x = a[u][i], y = b[u][i];
+              a[u][i] = x * cs[i] - y * sn[i];
+              b[u][i] = x * sn[i] + y * cs[i];
+            }
+          }
+        }
+        if (to_q) {
+          constexpr int SRC = sizeof(TS) == 2 ? PA_BF16 : PA_F32;
+          const int64_t at = (t0 + tk) * p.q_out_stride + (int64_t)head * D + off;
+          store_chunk<SRC, VE>(p.q_out, at, a[u]);
+          if (two) store_chunk<SRC, VE>(p.q_out, at + half, b[u]);
+          continue;
+        }
+        if (divide) {
+#pragma unroll
+          for (int i = 0; i < VE; ++i) {
+            a[u][i] = __fdiv_rn(a[u][i], sc);
+            if (two) b[u][i] = __fdiv_rn(b[u][i], sc);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < VE; ++i) {
-            const float x = a[u][i], y = b[u][i];
-            a[u][i] = x * cs[i] - y * sn[i];
-            b[u][i] = x * sn[i] + y * cs[i];
+            a[u][i] *= inv;
+            if (two) b[u][i] *= inv;
           }
         }
+        const int64_t at = ((int64_t)p.slots[t0 + tk] * p.num_kv_heads + hk) * D + off;
+        void* pool = is_v ? p.v_blocks : p.k_blocks;
+        store_chunk<DST, VE>(pool, at, a[u]);
+        if (two) store_chunk<DST, VE>(pool, at + half, b[u]);
       }
-      const int64_t t = t0 + tk[u];
-      const bool two = !IL && rot[u];
-      if (head[u] < H) {
-        constexpr int SRC = sizeof(TS) == 2 ? PA_BF16 : PA_F32;
-        const int64_t at = t * p.q_out_stride + (int64_t)head[u] * D + off[u];
-        store_chunk<SRC, VE>(p.q_out, at, a[u]);
-        if (two) store_chunk<SRC, VE>(p.q_out, at + half, b[u]);
-        continue;
-      }
-      const bool is_v = head[u] >= H + p.num_kv_heads;
-      const int hk = head[u] - H - (is_v ? p.num_kv_heads : 0);
-      const float* scales = is_v ? p.v_scales : p.k_scales;
-      const float sc = scales ? __ldg(scales + hk) : is_v ? p.v_scale : p.k_scale;
-      if (sc != 1.f) {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          a[u][i] = __fdiv_rn(a[u][i], sc);
-          if (two) b[u][i] = __fdiv_rn(b[u][i], sc);
-        }
-      }
-      const int64_t at = ((int64_t)p.slots[t] * p.num_kv_heads + hk) * D + off[u];
-      void* pool = is_v ? p.v_blocks : p.k_blocks;
-      store_chunk<DST, VE>(pool, at, a[u]);
-      if (two) store_chunk<DST, VE>(pool, at + half, b[u]);
     }
   }
 }
@@ -248,14 +261,16 @@ cudaError_t launch_as(const RopeParams& p, int num_sms, cudaStream_t stream) {
   const int rot_units = R / (IL ? VE : 2 * VE), per_head = rot_units + (D - R) / VE;
   const int heads = (p.q ? p.num_heads : 0) + p.num_kv_heads;
   const int64_t per_token = (int64_t)heads * per_head + (int64_t)p.num_kv_heads * (D / VE);
-  // several tokens to a CTA once every SM has a few CTAs (their angles and checks are shared
-  // work); a CTA's items stay below 2^31 whatever the row's length
-  int tok = 4;
-  while (tok > 1 && (p.num_tokens < (int64_t)tok * 4 * num_sms || per_token > (1 << 24))) tok >>= 1;
-  if (per_token > (1 << 30)) return cudaErrorInvalidValue;
-  const Geometry g{FastDiv((uint32_t)per_token), FastDiv((uint32_t)std::max(1, per_head)),
+  if (per_token > (1 << 28)) return cudaErrorInvalidValue;
+  // eight tokens to a CTA when that still gives every SM four CTAs, fewer for smaller batches;
+  // with one, its items are spread over several CTAs
+  int tok = 8;
+  while (tok > 1 && p.num_tokens < (int64_t)tok * 4 * num_sms) tok >>= 1;
+  const int64_t most = (per_token + kThreads - 1) / kThreads;
+  const int64_t parts = tok > 1 ? 1 : std::min<int64_t>(most, std::max<int64_t>(1, 2 * num_sms / p.num_tokens));
+  const Geometry g{(uint32_t)per_token, FastDiv((uint32_t)std::max(1, per_head)),
                    FastDiv((uint32_t)(D / VE)), rot_units};
-  const dim3 grid((unsigned)((p.num_tokens + tok - 1) / tok));
+  const dim3 grid((unsigned)((p.num_tokens + tok - 1) / tok), (unsigned)std::min<int64_t>(parts, 65535));
   const size_t smem = (size_t)tok * R * 4;
   if (p.num_tokens <= kCheckedTokens)
     return launch_pdl(k_rope_and_cache<TS, DST, VE, IL, true>, grid, dim3(kThreads), smem, stream,

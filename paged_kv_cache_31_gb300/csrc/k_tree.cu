@@ -139,8 +139,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(const TreeParams p) 
       const int64_t rows = (int64_t)nodes * m.group;
       const int64_t full = rows / p.rows_per_item;
       const int rest = (int)(rows % p.rows_per_item);
-      weight = (full * tree_weight(p, p.rows_per_item) + (rest ? tree_weight(p, rest) : 0)) *
-               m.num_kv_heads * tiles;
+      weight = ((full * tree_weight(p, p.rows_per_item) + (rest ? tree_weight(p, rest) : 0)) * tiles +
+                (full + (rest > 0)) * kTreeItemWeight) *
+               m.num_kv_heads;
     } else if (s < m.num_seqs) {
       p.seqs[s] = make_int4(0, 0, 0, 0);
     }
@@ -175,12 +176,14 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(const TreeParams p) 
       const int64_t rem = x - (shared ? s_cum[lo] : p.cum[lo]);
       const int4 q = p.seqs[lo];
       const TreeGeometry g(p, q);
-      const int64_t per_head = g.weight_before(g.items) * g.tiles;
+      const int64_t per_head =
+          g.weight_before(g.items) * g.tiles + (int64_t)g.items * kTreeItemWeight;
       const int kvh = (int)(rem / per_head);
       const int64_t r = rem % per_head;
-      const int full_w = tree_weight(p, p.rows_per_item);
-      const int it = min((int)(r / ((int64_t)full_w * g.tiles)), g.items - 1);
-      const int64_t in = r - (int64_t)it * full_w * g.tiles;
+      const int64_t item_w =
+          (int64_t)tree_weight(p, p.rows_per_item) * g.tiles + kTreeItemWeight;
+      const int it = (int)min(r / item_w, (int64_t)g.items - 1);
+      const int64_t in = max(r - it * item_w - kTreeItemWeight, (int64_t)0);
       const int w = tree_weight(p, g.rows_of(p, it));
       st = make_int4(lo, kvh * g.items + it, min((int)(in / w), g.tiles - 1), 0);
     }
@@ -364,59 +367,90 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
 // ---- merge ------------------------------------------------------------------------------------
 // Block (b, y): the item that the boundary between CTA b and b + 1 cuts, when that is the item's
 // first cut; a warp per row.  out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the
-// item's pieces in key order.
-template <typename TQ>
+// item's pieces in key order: CTA b's piece (its first segment when the item begins its share,
+// else its last), then those of the CTAs behind it whose shares begin inside the item.  Bound by
+// the latency of its loads, so 32 pieces' states are read at once, a lane each, and four pieces'
+// outputs at a time.
+// VEC: rows of whole float4s (head sizes that are multiples of 4)
+template <typename TQ, bool VEC>
 __global__ void __launch_bounds__(256) k_tree_merge(const TreeParams p) {
-  __shared__ int s_skip;
   const VarlenMeta& m = p.m;
   pdl_wait();
   pdl_launch_dependents();
-  if (threadIdx.x == 0) s_skip = status_set(p.status) ? 1 : 0;
-  __syncthreads();
-  if (s_skip) return;
-  const int b = blockIdx.x;
+  const int b = blockIdx.x, lane = threadIdx.x & 31;
+  const int skip = status_set(p.status);
   const int4 cut = p.starts[b + 1], from = p.starts[b];
+  if (__syncthreads_or(skip)) return;  // (one answer for the whole CTA)
   if (cut.x >= m.num_seqs || cut.z == 0) return;
   const bool same = from.x == cut.x && from.y == cut.y;
   if (same && from.z > 0) return;  // a later cut of the item
   const int4 q = p.seqs[cut.x];
   const TreeGeometry g(p, q);
   const int kvh = cut.y / g.items, it = cut.y % g.items;
-  const int rows = g.rows_of(p, it);
-  const int lane = threadIdx.x & 31;
   const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (row >= rows) return;
+  if (row >= g.rows_of(p, it)) return;
   const int D = m.head_dim, G = m.group;
-  // pieces: CTA b's (its first segment when the item begins its share, else its last), then the
-  // CTAs behind it while their share begins inside the item
   float M = -INFINITY, L = 0.f;
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  int slot = same ? 2 * b : 2 * b + 1;
-  for (int c = b;;) {
-    const int64_t at = (int64_t)slot * p.rows_per_item + row;
-    const float2 ml = p.part_ml[at];
-    const float mn = fmaxf(M, ml.x), base = mn == -INFINITY ? 0.f : mn;
-    const float a = exp2f(M - base), w = exp2f(ml.x - base);
-    M = mn;
-    L = L * a + ml.y * w;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int d = lane + 32 * i;
-      if (d < D) acc[i] = acc[i] * a + p.part_o[at * D + d] * w;
-    }
-    bool more = false;  // the next CTA with work that begins inside the item
-    for (++c; c < p.grid; ++c) {
+  for (int c0 = b;; c0 += 32) {  // pieces of CTAs c0 .. c0 + 31, one per lane
+    const int c = c0 + lane;
+    bool in = c == b;
+    int slot = same ? 2 * b : 2 * b + 1;
+    if (c > b && c < p.grid) {
       const int4 s0 = p.starts[c], s1 = p.starts[c + 1];
-      if (s0.x != cut.x || s0.y != cut.y) break;
-      if (s1.x != s0.x || s1.y != s0.y || s1.z != s0.z) {
-        more = true;
-        break;
-      }
+      in = s0.x == cut.x && s0.y == cut.y;
+      // (a CTA whose share is empty left nothing)
+      slot = in && (s1.x != s0.x || s1.y != s0.y || s1.z != s0.z) ? 2 * c : -1;
     }
-    if (!more) break;
-    slot = 2 * c;
+    const unsigned run = __ballot_sync(kFull, in);  // contiguous from lane 0
+    const int64_t at = in && slot >= 0 ? (int64_t)slot * p.rows_per_item + row : -1;
+    const float2 ml = at >= 0 ? p.part_ml[at] : make_float2(-INFINITY, 0.f);
+    float mx = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    const float mn = fmaxf(M, mx), base = mn == -INFINITY ? 0.f : mn;
+    const float a = exp2f(M - base), w = at >= 0 ? exp2f(ml.x - base) : 0.f;
+    float l = w * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+    M = mn;
+    L = L * a + l;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] *= a;
+    const int n = __popc(run);
+    for (int j0 = 0; j0 < n; j0 += 4) {
+      float x[4][8], wj[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = min(j0 + u, 31);
+        wj[u] = j0 + u < n ? __shfl_sync(kFull, w, j) : 0.f;
+        const int64_t aj = __shfl_sync(kFull, at, j);
+        const bool have = j0 + u < n && aj >= 0;
+        const float* src = p.part_o + aj * D;
+        if constexpr (VEC) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int d = 128 * k + 4 * lane;
+            const float4 v = have && d < D ? *reinterpret_cast<const float4*>(src + d)
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[u][4 * k] = v.x;
+            x[u][4 * k + 1] = v.y;
+            x[u][4 * k + 2] = v.z;
+            x[u][4 * k + 3] = v.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[u][i] = have && lane + 32 * i < D ? src[lane + 32 * i] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += wj[u] * x[u][i];
+    }
+    if (n < 32) break;
   }
   const int r = it * p.rows_per_item + row;
   const int tok = q.x + r / G, h = kvh * G + r % G;
@@ -424,7 +458,7 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeParams p) {
   TQ* out = static_cast<TQ*>(p.out) + ((int64_t)tok * m.num_heads + h) * D;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int d = lane + 32 * i;
+    const int d = VEC ? 128 * (i >> 2) + 4 * lane + (i & 3) : lane + 32 * i;
     if (d < D) out[d] = from_f32<TQ>(acc[i] * inv);
   }
 }
@@ -487,9 +521,13 @@ cudaError_t launch_tree_generic(const TreeParams& p, pa_dtype kv, cudaStream_t s
 
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t stream) {
   if (p.grid < 2) return cudaSuccess;
-  const dim3 grid((unsigned)(p.grid - 1), (unsigned)((p.rows_per_item + 7) / 8));
-  if (p.q_bf16) return launch_pdl(k_tree_merge<__nv_bfloat16>, grid, dim3(256), 0, stream, p);
-  return launch_pdl(k_tree_merge<float>, grid, dim3(256), 0, stream, p);
+  const int64_t rows = std::min<int64_t>(p.rows_per_item, p.m.num_tokens * p.m.group);
+  const dim3 grid((unsigned)(p.grid - 1), (unsigned)((rows + 7) / 8)), block(256);
+  if (p.m.head_dim % 4 == 0)
+    return p.q_bf16 ? launch_pdl(k_tree_merge<__nv_bfloat16, true>, grid, block, 0, stream, p)
+                    : launch_pdl(k_tree_merge<float, true>, grid, block, 0, stream, p);
+  return p.q_bf16 ? launch_pdl(k_tree_merge<__nv_bfloat16, false>, grid, block, 0, stream, p)
+                  : launch_pdl(k_tree_merge<float, false>, grid, block, 0, stream, p);
 }
 
 }  // namespace pa

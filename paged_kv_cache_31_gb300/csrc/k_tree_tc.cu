@@ -10,8 +10,9 @@
 // Two streams.  A softmax warpgroup (one thread per row, so no exchange between threads) and an
 // S / P buffer and O accumulator in tensor memory make a stream; there are two.  An item with two
 // row tiles gives each stream one, and both use the same key tiles: each K / V byte that reaches
-// shared memory serves 256 rows.  An item with one row tile gives its even key tiles to stream 0
-// and its odd ones to stream 1, whose states (m, l, O) are joined at the end.  Either way one
+// shared memory serves 256 rows.  An item with one row tile gives its key tiles to the
+// streams in turn; the stream that takes the last one joins their states (m, l, O), while the
+// other goes on with the next item.  Either way one
 // stream's MMAs run while the other's exponentials do.
 //
 // Per key tile of a stream:  S = Q K^T (M 128, N 128, K = head size);  mask, running max (moved,
@@ -20,10 +21,10 @@
 // 2^-16); over e4m3 pools it is one f16 value (2^-11), with q, K and V widened to f16 (exactly,
 // for the codes) in shared memory.  Row sums add the fp32 weights.
 //
-// Roles.  warp 0: TMA of K and V through a ring of five 128-key stages, K and V alternating;
-// warp 1: tensor-memory owner, issues S = Q K^T; warp 2: issues O += P V, and zeroes the V rows
-// past the sequence's end (they may hold anything; K's are masked); warp 3: TMA of Q, a ring of
-// two row tiles; warps 4..7 and 8..11: the streams' softmax and epilogue; warps 12..15 (e4m3
+// Roles.  warp 0: TMA of K, warp 3: of Q (a ring of two row tiles) and V; K and V alternate in a
+// ring of five 128-key stages; warp 1: tensor-memory owner, issues S = Q K^T; warp 2: issues
+// O += P V, and zeroes the V rows past the sequence's end (they may hold anything; K's are
+// masked); warps 4..7 and 8..11: the streams' softmax and epilogue; warps 12..15 (e4m3
 // pools): widen Q, K and V in shared memory.
 //
 // What bounds it: up to 128 rows per kv head, the K / V bytes (a tile is 64 KB of bf16, 1.5 us of
@@ -31,8 +32,8 @@
 // tiles, the tensor cores (2.0 us a tile).
 //
 // Every mbarrier wait is bounded; one that runs out records PA_ETIMEOUT and raises an abort flag
-// that ends the other roles' waits.  The softmax warps meet at a named barrier at the end of each
-// segment, where they agree on leaving; the TMA issuers wait (bounded) for their copies in flight
+// that ends the other roles' waits.  A softmax warp whose wait fails goes through the rest of its
+// share without waiting or writing, so that no warp is left at the named barriers; the TMA issuers wait (bounded) for their copies in flight
 // and the MMA issuers for their MMAs before the CTA gives its tensor memory back.
 #include <algorithm>
 
@@ -53,12 +54,16 @@ struct Shape {
   static constexpr int kTileBytes = kHalves * kHalfBytes;  // a 128-row tile of 16-bit values
   static constexpr int kLoadBytes = FP8 ? kTileBytes / 2 : kTileBytes;
   static constexpr int kThreads = FP8 ? 512 : 384;
+  // K / V stages over bf16 pools: 8-row groups of (dim half, 8 rows of 128 bytes), as the 5-D
+  // boxes write them; widened e4m3 stages and Q: dim half by dim half
+  static constexpr int kRowGroup = FP8 ? 1024 : 1024 * kHalves;  // between 8-row groups
+  static constexpr int kDimHalf = FP8 ? kHalfBytes : 1024;       // between dim halves
   static constexpr int kOffKV = 2 * kTileBytes;
-  static constexpr int kOffX = kOffKV + kStages * kTileBytes;  // [2][128] float2: stream 1's m, l
-  static constexpr int kOffBad = kOffX + 2 * 128 * 8;          // [2][8] failed-wait flags
-  static constexpr int kOffBar = kOffBad + 2 * 8 * 4;
+  static constexpr int kOffX = kOffKV + kStages * kTileBytes;  // [2][128] float2: a stream's m, l
+  static constexpr int kOffBad = kOffX + 2 * 128 * 8;          // [2][4] its warps' failed waits
+  static constexpr int kOffBar = kOffBad + 2 * 4 * 4;
   static constexpr int kOffMisc = kOffBar + 40 * 8;
-  static constexpr int kSmem = kOffMisc + 16;
+  static constexpr int kSmem = kOffMisc + 32;  // tensor-memory base, flags, stages sent
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
@@ -84,23 +89,22 @@ constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t col_s(int x) { return (uint32_t)x * 128; }
 __device__ __forceinline__ uint32_t col_o(int x) { return 256 + (uint32_t)x * 128; }
 
-// One CTA's MMAs (cta_group::1), issued by lane 0 of a warp in uniform control flow.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
+// One CTA's MMAs (cta_group::1), issued by the one lane with `elect` of a warp in uniform control
+// flow.
+__device__ __forceinline__ void mma_ss(uint32_t elect, uint32_t d, uint64_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .u32 l;\n\t.reg .pred e, p;\n\tmov.u32 l, %%laneid;\n\tsetp.eq.u32 e, l, 0;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred e, p;\n\tsetp.ne.u32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elect)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t elect, uint32_t d, uint32_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .u32 l;\n\t.reg .pred e, p;\n\tmov.u32 l, %%laneid;\n\tsetp.eq.u32 e, l, 0;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred e, p;\n\tsetp.ne.u32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elect)
       : "memory");
 }
 // Arrive on `bar` once this thread's MMAs so far are done.
@@ -117,131 +121,144 @@ struct Ctx {
   uint64_t* bar;
   volatile int* abort;
   int* status;
+  uint32_t* issued;  // [2] stages that the K and V producers have sent
   uint64_t limit;
   bool work;  // false: an earlier error, nothing is done
 };
 
 __device__ __forceinline__ bool wait_bar(const Ctx& c, int idx, uint32_t parity) {
   uint64_t* b = c.bar + idx;
-  if (mbar_try_wait(b, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(b, parity)) return true;
-    if ((i & 31u) == 0) {
-      if (*c.abort) return false;
-      if (globaltimer_ns() - t0 > c.limit) {
-        record_error(c.status, PA_ETIMEOUT);
-        *c.abort = 1;
-        return false;
-      }
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; !mbar_try_wait(b, parity); ++i) {
+    if ((i & 63u) != 63u) continue;
+    const uint64_t now = globaltimer_ns();
+    t0 = t0 ? t0 : now;
+    const bool late = now - t0 > c.limit;
+    if (late) {
+      record_error(c.status, PA_ETIMEOUT);
+      *c.abort = 1;
     }
+    if (late || *c.abort) return false;
   }
+  return true;
 }
 __device__ __forceinline__ bool wait_all(const Ctx& c, int idx, uint32_t parity) {
   return __all_sync(kFull, wait_bar(c, idx, parity));
 }
 
-// Position in the K / V ring.
+// The K / V ring.  The copies of a CTA's tiles 0, 1, 2, ... are numbered in the order in which
+// they are needed: K0 V0 K1 V1 ... where every item may have two row tiles, and K0 K1 V0 K2 V1 ...
+// (`ahead`) where none has: the streams then work on two tiles at once, and tile t's V is needed
+// after tile t + 1's K.  Copy n uses stage n % kStages.
+__device__ __forceinline__ bool ring_ahead(const TreeParams& p) {
+  return p.rows_per_item == p.tile_rows;
+}
 struct Ring {
-  uint32_t st = 0, par = 0;
-  __device__ __forceinline__ void next() {
-    if (++st == kStages) {
-      st = 0;
+  uint32_t st, par;
+  bool ahead, first;
+  __device__ __forceinline__ Ring(const TreeParams& p, int kv) {
+    ahead = ring_ahead(p);
+    first = ahead && kv == 0;
+    st = kv ? (ahead ? 2 : 1) : 0;
+    par = 0;
+  }
+  __device__ __forceinline__ void next() {  // the next tile's copy of the same operand
+    st += first ? 1 : 2;
+    first = false;
+    if (st >= kStages) {
+      st -= kStages;
       par ^= 1;
     }
   }
 };
 
-// Tiles of stream x in a segment of nt key tiles: both streams all of them (two row tiles), or
-// the even and the odd ones.
+// Both streams take all key tiles of a segment with two row tiles.  With one row tile the streams
+// alternate, over segments too: the stream that does not take a segment's last tile begins the
+// next one, while the other finishes this one.
 __device__ __forceinline__ bool two_tiles(const TreeParams& p, const TreeSegment& g) {
   return g.rows > p.tile_rows;
 }
 
 // ---- roles --------------------------------------------------------------------------------------
 
+// Warp 0 brings K (kv = 0), warp 3 Q and V (kv = 1); both walk the whole share.  A block is one
+// box, issued by a lane of its own: a warp's TMA instructions go out one lane after the other,
+// and one warp issuing 32 half-size boxes per key tile was what bound this kernel.
 template <int D, bool FP8>
-__device__ void kv_producer(const Ctx& c, const TreeParams& p, const CUtensorMap* tk,
-                            const CUtensorMap* tv) {
+__device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* tkv,
+                         const CUtensorMap* tq, int kv) {
   using S = Shape<D, FP8>;
   const int lane = threadIdx.x & 31;
-  constexpr int kBoxes = FP8 ? 8 : 8 * S::kHalves;  // one box per lane
-  const int blk = lane & 7, half = lane >> 3;
-  Ring r;
-  uint32_t issued = 0;
+  Ring r(p, kv);
+  uint32_t issued = 0, nq = 0;  // this warp's stages; row tiles of Q (tile n uses buffer n % 2)
   bool ok = c.work;
   TreeWalk walk(p, blockIdx.x);
   TreeSegment g;
   while (ok && walk.next(p, g)) {
     const int32_t* row = p.m.block_tables + (int64_t)g.s * p.m.max_blocks;
     const int blocks = (g.n + 15) / 16;
-    const int b0 = g.kv0 / 16 + 8 * g.t0 + blk;
-    int next = b0 < blocks ? row[b0] : -1;
-    for (int j = g.t0; ok && j < g.t1; ++j) {
-      const int id = next;
-      const int nb = b0 + 8 * (j + 1 - g.t0);
-      if (j + 1 < g.t1) next = nb < blocks ? row[nb] : -1;
-      const int coord = id >= 0 ? id * 16 : -16;  // past the end: rows outside the pool, zeros
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        if (lane == 0) {
-          ok = wait_bar(c, B_EMPTY + r.st, r.par ^ 1);
-          if (ok) mbar_arrive_expect_tx(c.bar + B_FULL + r.st, S::kLoadBytes);
-        }
-        ok = __shfl_sync(kFull, (int)ok, 0);
-        if (!ok) break;
-        if (lane < kBoxes) {
-          uint8_t* dst = c.sm + S::kOffKV + r.st * S::kTileBytes;
-          if constexpr (FP8)  // the codes go where the second dim half's rows will be
-            tma_load_3d(dst + S::kHalfBytes + blk * 2048, kv ? tv : tk, 0, g.kvh, coord,
-                        c.bar + B_FULL + r.st);
-          else
-            tma_load_3d(dst + half * S::kHalfBytes + blk * 2048, kv ? tv : tk, 64 * half, g.kvh,
-                        coord, c.bar + B_FULL + r.st);
-        }
-        ++issued;
-        r.next();
-      }
-    }
-  }
-  // the copies still in flight (after an abort; otherwise all have been consumed)
-  if (lane == 0)
-    for (uint32_t k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
-      mbar_wait(c.bar + B_FULL + k % kStages, (k / kStages) & 1u, c.limit);
-  __syncwarp();
-}
-
-template <int D, bool FP8>
-__device__ void q_producer(const Ctx& c, const TreeParams& p, const CUtensorMap* tq) {
-  using S = Shape<D, FP8>;
-  const int lane = threadIdx.x & 31;
-  uint32_t n = 0;  // row tiles loaded; tile n uses buffer n % 2
-  bool ok = c.work;
-  TreeWalk walk(p, blockIdx.x);
-  TreeSegment g;
-  while (ok && walk.next(p, g)) {
-    const int tiles = two_tiles(p, g) ? 2 : 1;
+    const int b0 = g.kv0 / 16 + 8 * g.t0 + lane;
+    int next = lane < 8 && b0 < blocks ? row[b0] : -1;
+    const int tiles = kv ? (two_tiles(p, g) ? 2 : 1) : 0;
     for (int x = 0; ok && x < tiles; ++x) {
       if (lane == 0) {
-        ok = wait_bar(c, B_QEMPTY + (n & 1), ((n >> 1) & 1) ^ 1);
+        ok = wait_bar(c, B_QEMPTY + (nq & 1), ((nq >> 1) & 1) ^ 1);
         if (ok) {
-          uint64_t* bar = c.bar + B_QFULL + (n & 1);
+          uint64_t* bar = c.bar + B_QFULL + (nq & 1);
           mbar_arrive_expect_tx(bar, (uint32_t)p.tile_rows * 128 * S::kHalves);
           const int tok = g.qs + (g.row0 + x * p.tile_rows) / p.m.group;
 #pragma unroll
           for (int h = 0; h < S::kHalves; ++h)
-            tma_load_3d(c.sm + (n & 1) * S::kTileBytes + h * S::kHalfBytes, tq, 64 * h,
+            tma_load_3d(c.sm + (nq & 1) * S::kTileBytes + h * S::kHalfBytes, tq, 64 * h,
                         g.kvh * p.m.group, tok, bar);
         }
       }
       ok = __shfl_sync(kFull, (int)ok, 0);
-      if (ok) ++n;
+      if (ok) ++nq;
+    }
+    for (int j = g.t0; ok && j < g.t1; ++j) {
+      const int id = next;
+      const int nb = b0 + 8 * (j + 1 - g.t0);
+      if (j + 1 < g.t1) next = lane < 8 && nb < blocks ? row[nb] : -1;
+      if (lane == 0) {
+        ok = wait_bar(c, B_EMPTY + r.st, r.par ^ 1);
+        if (ok) mbar_arrive_expect_tx(c.bar + B_FULL + r.st, S::kLoadBytes);
+      }
+      ok = __shfl_sync(kFull, (int)ok, 0);
+      if (!ok) break;
+      if (lane < 8) {  // a block past the end: rows outside the pool, which TMA fills with zeros
+        uint8_t* dst = c.sm + S::kOffKV + r.st * S::kTileBytes;
+        if constexpr (FP8)  // the codes go where the second dim half's rows will be
+          tma_load_3d(dst + S::kHalfBytes + lane * 2048, tkv, 0, g.kvh, id >= 0 ? id * 16 : -16,
+                      c.bar + B_FULL + r.st);
+        else
+          tma_load_5d(dst + lane * (S::kTileBytes / 8), tkv, 0, 0, 0, id >= 0 ? id * 2 : -2, g.kvh,
+                      c.bar + B_FULL + r.st);
+      }
+      ++issued;
+      r.next();
     }
   }
+  if (lane == 0) c.issued[kv] = issued;
+  // Q's copies still in flight (after an abort; otherwise all have been consumed)
   if (lane == 0)
-    for (uint32_t k = n > 2 ? n - 2 : 0; k < n; ++k)
+    for (uint32_t k = nq > 2 ? nq - 2 : 0; k < nq; ++k)
       mbar_wait(c.bar + B_QFULL + (k & 1), (k >> 1) & 1u, c.limit);
   __syncwarp();
+}
+
+// The same for K and V, by one thread once both producers are done: each stage's last copy (an
+// earlier one's phase may have been followed by two others, whose parity it shares).
+__device__ void drain_kv(const Ctx& c, bool ahead) {
+  const uint32_t nk = c.issued[0], nv = c.issued[1];
+  auto sent = [&](uint32_t n) {
+    if (ahead) return n == 0 ? nk > 0 : n & 1 ? (n + 1) / 2 < nk : (n - 2) / 2 < nv;
+    return n & 1 ? n / 2 < nv : n / 2 < nk;
+  };
+  const uint32_t end = 2 * max(nk, nv) + 3;
+  for (uint32_t n = end > 4 * kStages ? end - 4 * kStages : 0; n < end; ++n)
+    if (sent(n) && !sent(n + kStages))
+      mbar_wait(c.bar + B_FULL + n % kStages, (n / kStages) & 1u, c.limit);
 }
 
 template <int D, bool FP8>
@@ -249,9 +266,10 @@ __device__ void s_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   using S = Shape<D, FP8>;
   constexpr uint32_t kIdesc = idesc_f16kind(128, kBN, 0, FP8 ? 0 : 1);
   constexpr int kQ = FP8 ? B_QCONV : B_QFULL, kKV = FP8 ? B_CONV : B_FULL;
-  const uint32_t sm = smem_u32(c.sm);
-  Ring r;
+  const uint32_t sm = smem_u32(c.sm), elect = (threadIdx.x & 31) == 0;
+  Ring r(p, 0);
   uint32_t nq = 0, cnt[2] = {0, 0};  // row tiles used; tiles of each stream
+  int turn = 0;                      // the stream whose turn it is
   if (!c.work) return;
   TreeWalk walk(p, blockIdx.x);
   TreeSegment g;
@@ -260,28 +278,32 @@ __device__ void s_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
     for (int j = g.t0; j < g.t1; ++j) {
       if (!wait_all(c, kKV + r.st, r.par)) return;
       const uint32_t kb = sm + S::kOffKV + r.st * S::kTileBytes;
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int x = two ? y : (j - g.t0) & 1;  // the stream
-        if (!two && y) break;
+#pragma unroll 1
+      for (int y = 0; y < (two ? 2 : 1); ++y) {
+        const int x = two ? y : turn;  // the stream
         const uint32_t q = nq + (two ? y : 0);
         if (j == g.t0 && !wait_all(c, kQ + (q & 1), (q >> 1) & 1)) return;
         const uint32_t n = x ? cnt[1] : cnt[0];
         if (!wait_all(c, B_PVDONE + x, (n & 1) ^ 1)) return;  // the buffer's last P is used up
         tc_fence_after();
         const uint32_t qb = sm + (q & 1) * S::kTileBytes;
+        // (addresses of a descriptor advance in units of 16 bytes)
+        uint64_t qd = sdesc(qb, 16, 1024), kd = sdesc(kb, 16, S::kRowGroup);
+#pragma unroll 1
+        for (int h = 0; h < S::kHalves; ++h) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + col_s(x), sdesc(qb + (kk >> 2) * S::kHalfBytes + (kk & 3) * 32, 16, 1024),
-                 sdesc(kb + (kk >> 2) * S::kHalfBytes + (kk & 3) * 32, 16, 1024), kIdesc,
-                 kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss(elect, tmem + col_s(x), qd + 2 * kk, kd + 2 * kk, kIdesc, (h | kk) ? 1u : 0u);
+          qd += S::kHalfBytes / 16;
+          kd += S::kDimHalf / 16;
+        }
         mma_commit(c.bar + B_SFULL + x);
         if (x) ++cnt[1]; else ++cnt[0];
       }
+      if (!two) turn ^= 1;
       mma_commit(c.bar + B_EMPTY + r.st);
       __syncwarp();
       r.next();
-      r.next();  // V's stage
     }
     for (int y = 0; y < (two ? 2 : 1); ++y) mma_commit(c.bar + B_QEMPTY + ((nq + y) & 1));
     nq += two ? 2 : 1;
@@ -294,52 +316,59 @@ __device__ void pv_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   constexpr uint32_t kIdesc = idesc_f16kind(128, D, 1, FP8 ? 0 : 1);
   constexpr int kKV = FP8 ? B_CONV : B_FULL;
   const int lane = threadIdx.x & 31;
-  const uint32_t sm = smem_u32(c.sm);
-  Ring r;
+  const uint32_t elect = lane == 0;
+  Ring r(p, 1);
   uint32_t cnt[2] = {0, 0}, seg = 0;
+  int turn = 0;
   if (!c.work) return;
   TreeWalk walk(p, blockIdx.x);
   TreeSegment g;
   for (; walk.next(p, g); ++seg) {
     const bool two = two_tiles(p, g);
     for (int j = g.t0; j < g.t1; ++j) {
-      r.next();  // K's stage
       if (!wait_all(c, kKV + r.st, r.par)) return;
       uint8_t* v = c.sm + S::kOffKV + r.st * S::kTileBytes;
       if constexpr (!FP8) {  // (the converters do it over e4m3 pools)
         // rows of the last block past the sequence's end: zeros (whole blocks past it are)
         const int lim = g.n - (g.kv0 + j * kBN);
         if (lim < kBN && (lim & 15)) {
-          const int rows = 16 - (lim & 15);
-          for (int i = lane; i < rows * 8 * S::kHalves; i += 32) {
-            const int h = i / (rows * 8), e = i % (rows * 8);
-            *reinterpret_cast<uint4*>(v + h * S::kHalfBytes + lim * 128 + e * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+          for (int i = lane; i < (16 - (lim & 15)) * 8 * S::kHalves; i += 32) {
+            const int row = lim + i / (8 * S::kHalves), h = (i >> 3) % S::kHalves;
+            *reinterpret_cast<uint4*>(v + (row >> 3) * S::kRowGroup + h * S::kDimHalf +
+                                      (row & 7) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
           __syncwarp();
         }
       }
       const uint32_t vb = smem_u32(v);
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int x = two ? y : (j - g.t0) & 1;
-        if (!two && y) break;
+#pragma unroll 1
+      for (int y = 0; y < (two ? 2 : 1); ++y) {
+        const int x = two ? y : turn;
         const bool first = two ? j == g.t0 : j - g.t0 < 2;
         if (first && !wait_all(c, B_OFREE + x, (seg & 1) ^ 1)) return;
         const uint32_t n = x ? cnt[1] : cnt[0];
         if (!wait_all(c, B_PFULL + x, n & 1)) return;
         tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk) {
-          const uint64_t vd = sdesc(vb + kk * 2048, S::kHalfBytes, 1024);
-          mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, vd, kIdesc,
-                 (!first || kk > 0) ? 1u : 0u);
-          if constexpr (!FP8) mma_ts(tmem + col_o(x), tmem + col_s(x) + 64 + kk * 8, vd, kIdesc, 1u);
+        uint64_t vd = sdesc(vb, S::kDimHalf, S::kRowGroup);
+        uint32_t pc = tmem + col_s(x), acc = first ? 0u : 1u;
+        constexpr uint64_t kStep = 2 * S::kRowGroup / 16;  // 16 keys
+#pragma unroll 1
+        for (int kk = 0; kk < kBN / 32; ++kk) {  // 32 keys: hi, hi and lo, lo
+          mma_ts(elect, tmem + col_o(x), pc, vd, kIdesc, acc);
+          mma_ts(elect, tmem + col_o(x), pc + 8, vd + kStep, kIdesc, 1u);
+          if constexpr (!FP8) {
+            mma_ts(elect, tmem + col_o(x), pc + 16, vd, kIdesc, 1u);
+            mma_ts(elect, tmem + col_o(x), pc + 24, vd + kStep, kIdesc, 1u);
+          }
+          vd += 2 * kStep;
+          pc += 32;
+          acc = 1;
         }
         mma_commit(c.bar + B_PVDONE + x);
         if (x) ++cnt[1]; else ++cnt[0];
       }
+      if (!two) turn ^= 1;
       mma_commit(c.bar + B_EMPTY + r.st);
       __syncwarp();
       r.next();
@@ -348,49 +377,50 @@ __device__ void pv_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
 }
 
 // Widen a staged tile of 128 x 128 codes to f16, in place: the codes lie in the second dim half's
-// 16 KB, in rows of 128 bytes with the 128-byte swizzle; warp w takes blocks 2w and 2w + 1.  A
-// round's stores overwrite only codes of its own four rows, loaded by all lanes before.  Rows at
-// or past `lim` become zeros.
-__device__ __forceinline__ void widen_tile(uint8_t* tile, int w, int lane, int lim) {
+// 16 KB, in rows of 128 bytes with the 128-byte swizzle.  A warp takes rows 32 w .. 32 w + 31 and has
+// loaded all their codes before it stores over them.  Rows at or past `lim` become zeros.
+__device__ __forceinline__ void widen_rows(uint8_t* tile, int w, int lane, int lim) {
   constexpr int kHalf = 128 * 128;
-#pragma unroll 2
+  uint4 src[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    src[i] = *reinterpret_cast<const uint4*>(tile + kHalf + w * 4096 + (lane + 32 * i) * 16);
+  __syncwarp();
+#pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int b = 2 * w + (i >> 2), ch = lane + 32 * (i & 3);
-    const uint4 src = *reinterpret_cast<const uint4*>(tile + kHalf + b * 2048 + ch * 16);
-    __syncwarp();
-    const int rr = ch >> 3, L = (ch & 7) ^ (rr & 7);  // row of the block, dims 16 L .. 16 L + 15
+    const int ch = lane + 32 * i, rr = ch >> 3;       // row of the warp's 32
+    const int L = (ch & 7) ^ (rr & 7);                // dims 16 L .. 16 L + 15
     const int h = L >> 2, c0 = 2 * (L & 3);           // dim half, first output chunk
     uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-    if (b * 16 + rr < lim) {
-      widen4(src.x, lo.x, lo.y);
-      widen4(src.y, lo.z, lo.w);
-      widen4(src.z, hi.x, hi.y);
-      widen4(src.w, hi.z, hi.w);
+    if (w * 32 + rr < lim) {
+      widen4(src[i].x, lo.x, lo.y);
+      widen4(src[i].y, lo.z, lo.w);
+      widen4(src[i].z, hi.x, hi.y);
+      widen4(src[i].w, hi.z, hi.w);
     }
-    uint8_t* row = tile + h * kHalf + b * 2048 + rr * 128;
+    uint8_t* row = tile + h * kHalf + w * 4096 + rr * 128;
     *reinterpret_cast<uint4*>(row + ((c0 ^ (rr & 7)) << 4)) = lo;
     *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (rr & 7)) << 4)) = hi;
   }
-  fence_proxy_async_smem();
-  __syncwarp();
 }
 
+// Warps 12 and 13 widen Q and K, 14 and 15 V: each half of every tile, in the order of the copies.
 template <int D>
 __device__ void converter(const Ctx& c, const TreeParams& p) {
   using S = Shape<D, true>;
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 12;
-  Ring r;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 1, kv = ((threadIdx.x >> 5) - 12) >> 1;
+  Ring r(p, kv);
   uint32_t nq = 0;
   if (!c.work) return;
   TreeWalk walk(p, blockIdx.x);
   TreeSegment g;
   while (walk.next(p, g)) {
-    const int tiles = two_tiles(p, g) ? 2 : 1;
+    const int tiles = kv ? 0 : two_tiles(p, g) ? 2 : 1;
     for (int x = 0; x < tiles; ++x, ++nq) {
       if (!wait_all(c, B_QFULL + (nq & 1), (nq >> 1) & 1)) return;
-      uint4* q = reinterpret_cast<uint4*>(c.sm + (nq & 1) * S::kTileBytes) + w * (S::kTileBytes / 64);
+      uint4* q = reinterpret_cast<uint4*>(c.sm + (nq & 1) * S::kTileBytes) + w * (S::kTileBytes / 32);
 #pragma unroll 4
-      for (int i = 0; i < S::kTileBytes / 64 / 32; ++i) {
+      for (int i = 0; i < S::kTileBytes / 32 / 32; ++i) {
         uint4 v = q[lane + 32 * i];
         v.x = bf16x2_to_f16x2(v.x);
         v.y = bf16x2_to_f16x2(v.y);
@@ -404,12 +434,14 @@ __device__ void converter(const Ctx& c, const TreeParams& p) {
     }
     for (int j = g.t0; j < g.t1; ++j) {
       const int lim = g.n - (g.kv0 + j * kBN);
-      for (int kv = 0; kv < 2; ++kv) {
-        if (!wait_all(c, B_FULL + r.st, r.par)) return;
-        widen_tile(c.sm + S::kOffKV + r.st * S::kTileBytes, w, lane, lim);
-        if (lane == 0) mbar_arrive(c.bar + B_CONV + r.st);
-        r.next();
-      }
+      if (!wait_all(c, B_FULL + r.st, r.par)) return;
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i)
+        widen_rows(c.sm + S::kOffKV + r.st * S::kTileBytes, 2 * w + i, lane, lim);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c.bar + B_CONV + r.st);
+      r.next();
     }
   }
 }
@@ -440,18 +472,58 @@ __device__ __forceinline__ uint32_t visible_word(const TreeParams& p, const Tree
     }
     const int end = g.nodes - node0;  // bits from there on are past the tree
     if (end < 32) t &= (1u << end) - 1u;
-    if (p.m.window > 0)
+    // Nodes too far behind pos, one by one, unless none can be: positions are not negative, and a
+    // first key kv0 > 0 says that the sequence's lowest one is at least kv0 + window - 1.
+    const int far = pos - p.m.window;
+    if (p.m.window > 0 && far >= 0 && !(g.kv0 > 0 && g.kv0 + p.m.window - 1 > far))
       for (uint32_t m = t; m; m &= m - 1) {
         const int i = __ffs(m) - 1;
-        if (p.m.positions[g.qs + node0 + i] <= pos - p.m.window) t &= ~(1u << i);
+        if (p.m.positions[g.qs + node0 + i] <= far) t &= ~(1u << i);
       }
     w |= t;
   }
   return w;
 }
 
-__device__ __forceinline__ void softmax_sync() {
-  asm volatile("bar.sync 1, 256;" ::: "memory");
+// The weights p = 2^(s * sl + nb) of 32 keys (packed pairs), added to `sum` and written to
+// tensor memory for the product with V: bf16 hi in columns 0 .. 15 and lo in 16 .. 31, or f16 in
+// columns 0 .. 15.
+template <bool FP8>
+__device__ __forceinline__ void weights32(uint32_t taddr, const uint32_t (&s)[32], uint64_t sl,
+                                          uint64_t nb, uint64_t (&sum)[2]) {
+  uint32_t w[FP8 ? 16 : 32];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float a, b;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sl, nb), a,
+              b);
+    a = fast_exp2(a);
+    b = fast_exp2(b);
+    const uint64_t ab = f2_pack(a, b);
+    sum[e & 1] = f2_add(sum[e & 1], ab);
+    if constexpr (FP8) {
+      w[e] = pack_f16x2(a, b);
+    } else {
+      w[e] = pack_bf16x2(a, b);
+      // (a - hi is exact: hi is within half a bf16 step of a)
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u)),
+                       f2_pack(-1.f, -1.f), ab), a, b);
+      w[16 + e] = pack_bf16x2(a, b);
+    }
+  }
+  if constexpr (FP8)
+    tmem_st16(taddr, w);
+  else
+    tmem_st32(taddr, w);
+}
+
+// Handing a stream's state over at a segment's end: the warpgroup that finishes first arrives and
+// goes on, the other waits for it.  Two barriers in turn.
+__device__ __forceinline__ void state_given(int par) {
+  asm volatile("bar.arrive %0, 256;" ::"r"(1 + par) : "memory");
+}
+__device__ __forceinline__ void state_taken(int par) {
+  asm volatile("bar.sync %0, 256;" ::"r"(1 + par) : "memory");
 }
 
 // The streams' threads: warpgroup x (warps 4 + 4x ..), thread = row = tensor-memory lane.
@@ -467,6 +539,7 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
   int* bads = reinterpret_cast<int*>(c.sm + S::kOffBad);
   uint32_t cnt[2] = {0, 0};  // tiles of both streams so far
   uint32_t seg = 0;
+  int turn = 0;  // the stream whose turn it is
   bool bad = false;
   if (!c.work) return;
   TreeWalk walk(p, blockIdx.x);
@@ -474,8 +547,9 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
   for (; walk.next(p, g); ++seg) {
     const bool two = two_tiles(p, g);
     const int nt = g.t1 - g.t0;
-    const int mine = two ? nt : (nt + 1 - x) >> 1;       // this stream's tiles
-    const int other = two ? nt : (nt + x) >> 1;
+    const int skip = two ? 0 : x ^ turn;                  // this stream's first tile
+    const int mine = two ? nt : (nt + 1 - skip) >> 1;    // its tiles
+    const int other = two ? nt : (nt + skip) >> 1;
     const int tile_row0 = two ? x * p.tile_rows : 0;     // of the item's rows
     const int rows = two ? (x ? g.rows - p.tile_rows : p.tile_rows) : g.rows;
     const bool valid = r < rows;
@@ -490,42 +564,45 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
     float m_ref = -INFINITY, l = 0.f;
     uint32_t n = x ? cnt[1] : cnt[0];
     for (int i = 0; i < mine; ++i, ++n) {
-      const int key0 = g.kv0 + (g.t0 + (two ? i : 2 * i + x)) * kBN;
+      const int key0 = g.kv0 + (g.t0 + (two ? i : 2 * i + skip)) * kBN;
       const uint32_t sb = lanes + col_s(x);
+      // a tile that hides keys from some row: which ones, while S is still being computed
+      const bool hides = !__all_sync(kFull, key0 >= free_lo && key0 + kBN <= ctx) && !idle;
+      uint32_t see[4] = {0, 0, 0, 0};
+      if (hides) {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t w = visible_word(p, g, tok, pos, key0 + 32 * q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) see[e] = e == q ? w : see[e];
+        }
+      }
       if (!bad)
         bad = !wait_all(c, stall ? B_NEVER : B_SFULL + x, stall ? 0u : n & 1);
       if (!idle && !bad) {
         tc_fence_after();
-        float v[kBN];
-        {
-          uint32_t a[64], b[64];
-          tmem_ld64(sb, a);
-          tmem_ld64(sb + 64, b);
-          tmem_wait_ld64(a);
-          tmem_wait_ld64(b);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          uint32_t v[64];
+          tmem_ld64(sb + 64 * q, v);
+          tmem_wait_ld64(v);
+          if (hides) {  // hidden keys' scores become -inf in place
+            const uint32_t w0 = q ? see[2] : see[0], w1 = q ? see[3] : see[1];
+            uint32_t u[32];
 #pragma unroll
-          for (int e = 0; e < 64; ++e) {
-            v[e] = __uint_as_float(a[e]);
-            v[64 + e] = __uint_as_float(b[e]);
+            for (int e = 0; e < 32; ++e) u[e] = v[e] = (w0 >> e) & 1u ? v[e] : 0xff800000u;
+            tmem_st32(sb + 64 * q, u);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) u[e] = v[32 + e] = (w1 >> e) & 1u ? v[32 + e] : 0xff800000u;
+            tmem_st32(sb + 64 * q + 32, u);
           }
-        }
-        if (!__all_sync(kFull, key0 >= free_lo && key0 + kBN <= ctx)) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t w = visible_word(p, g, tok, pos, key0 + 32 * q);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              v[32 * q + e] = (w >> e) & 1u ? v[32 * q + e] : -INFINITY;
-          }
+          for (int e = 0; e < 64; e += 2)
+            mx[(e >> 1) & 3] =
+                fmaxf(mx[(e >> 1) & 3], fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
         }
-        float mx[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-        for (int e = 4; e < kBN; e += 4) {
-          mx[0] = fmaxf(mx[0], v[e]);
-          mx[1] = fmaxf(mx[1], v[e + 1]);
-          mx[2] = fmaxf(mx[2], v[e + 2]);
-          mx[3] = fmaxf(mx[3], v[e + 3]);
-        }
+        if (hides) tmem_wait_st();
         // (the scale is positive on this path, so it commutes with the max)
         const float m_new = fmaxf(m_ref, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl);
         const bool resc = m_new > m_ref + 8.f;
@@ -538,27 +615,16 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
         const float nb = m_ref == -INFINITY ? 0.f : -m_ref;
         const uint64_t sl2 = f2_pack(sl, sl), nb2 = f2_pack(nb, nb);
         uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {  // 64 keys at a time: P over their S columns
-          uint32_t ph[32], pl[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int k = 64 * part + 2 * e;
-            float a, b;
-            f2_unpack(f2_fma(f2_pack(v[k], v[k + 1]), sl2, nb2), a, b);
-            a = fast_exp2(a);
-            b = fast_exp2(b);
-            sum[e & 1] = f2_add(sum[e & 1], f2_pack(a, b));
-            if constexpr (FP8) {
-              ph[e] = pack_f16x2(a, b);
-            } else {
-              ph[e] = pack_bf16x2(a, b);
-              pl[e] = pack_bf16x2(a - __uint_as_float(ph[e] << 16),
-                                  b - __uint_as_float(ph[e] & 0xffff0000u));
-            }
+        // P over the S columns it came from, 32 keys at a time (a loop: straight-line code for
+        // all 128 keys ran out of the instruction cache and took 1.9 times as long)
+        {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t s0[32];
+            tmem_ld32(sb + 32 * q, s0);
+            tmem_wait_ld(s0);
+            weights32<FP8>(sb + 32 * q, s0, sl2, nb2, sum);
           }
-          tmem_st32(sb + 32 * part, ph);
-          if constexpr (!FP8) tmem_st32(sb + 64 + 32 * part, pl);
         }
         {
           float a, b, d, e;
@@ -570,7 +636,7 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
         if (i > 0 && __any_sync(kFull, resc)) {
           if (!bad) bad = !wait_all(c, B_PVDONE + x, (n - 1) & 1);
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < D / 32; ++q) {
             uint32_t o[32];
             tmem_ld32(lanes + col_o(x) + 32 * q, o);
@@ -591,23 +657,31 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
 
     // ---- the segment's end
     const int par = seg & 1;
-    // both streams' last P V, as far as this warpgroup reads their O
-    if (!bad && mine) bad = !wait_all(c, B_PVDONE + x, (n - 1) & 1);
-    if (!two && x == 0 && other) {
-      if (!bad) bad = !wait_all(c, B_PVDONE + 1, (cnt[1] - 1) & 1);
+    if (!two) turn = (turn + nt) & 1;
+    if (!two && x == turn) {  // the other stream has the last tile: it gets this one's state
+      if (mine) {
+        xchg[par * 128 + r] = make_float2(m_ref, l);
+        if (lane == 0) bads[par * 4 + quad] = bad ? 1 : 0;
+        // (after a failed wait nothing holds this warp back: it must not come round to the same
+        // barrier before the other stream has passed it)
+        if (bad)
+          state_taken(par);
+        else
+          state_given(par);
+      }
+      continue;
     }
-    if (!two && x == 1) xchg[par * 128 + r] = make_float2(m_ref, l);
-    if (lane == 0) bads[par * 8 + warp] = bad ? 1 : 0;
-    softmax_sync();
-    int any = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) any |= bads[par * 8 + e];
-    if (any) return;  // all eight warps alike, before anything is written
-    if (two || x == 0) {
+    if (!bad && mine) bad = !wait_all(c, B_PVDONE + x, (n - 1) & 1);
+    const bool join = !two && other > 0;
+    if (join) {
+      if (!bad) bad = !wait_all(c, B_PVDONE + (x ^ 1), ((x ? cnt[0] : cnt[1]) - 1) & 1);
+      state_taken(par);
+      bad |= bads[par * 4 + quad] != 0;  // (uniform across the warp)
+    }
+    if (!bad && *c.abort == 0) {  // (a failed role's rows must not be written)
       tc_fence_after();
       float a0 = 1.f, a1 = 0.f;
-      const bool join = !two && other > 0;
-      if (join) {  // stream 1's state
+      if (join) {
         const float2 o = xchg[par * 128 + r];
         const float mn = fmaxf(m_ref, o.x), base = mn == -INFINITY ? 0.f : mn;
         a0 = fast_exp2(m_ref - base);
@@ -632,7 +706,7 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
       a0 *= scale;
       a1 *= scale;
       if (!idle) {
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
           tmem_ld32(lanes + col_o(x) + 32 * q, o);
@@ -641,7 +715,7 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
 #pragma unroll
           for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * a0;
           if (join) {
-            tmem_ld32(lanes + col_o(1) + 32 * q, o);
+            tmem_ld32(lanes + col_o(x ^ 1) + 32 * q, o);
             tmem_wait_ld(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) f[e] += __uint_as_float(o[e]) * a1;
@@ -662,9 +736,9 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
       tc_fence_before();
     }
     __syncwarp();
-    if (lane == 0) {  // (a stream's next O waits for all eight warps, whoever read it)
-      mbar_arrive(c.bar + B_OFREE);
-      mbar_arrive(c.bar + B_OFREE + 1);
+    if (lane == 0) {
+      mbar_arrive(c.bar + B_OFREE + x);
+      if (!two) mbar_arrive(c.bar + B_OFREE + (x ^ 1));
     }
   }
 }
@@ -684,9 +758,9 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     flags[1] = 0;
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
-      if ((i >= B_QCONV && i < B_QCONV + 2) || (i >= B_CONV && i < B_CONV + kStages)) n = 4;
+      if ((i >= B_QCONV && i < B_QCONV + 2) || (i >= B_CONV && i < B_CONV + kStages)) n = 2;
       if (i >= B_PFULL && i < B_PFULL + 2) n = 4;
-      if (i >= B_OFREE && i < B_OFREE + 2) n = 8;
+      if (i >= B_OFREE && i < B_OFREE + 2) n = 4;
       mbar_init(bar + i, n);
     }
     prefetch_tmap(&tq);
@@ -715,8 +789,8 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
   }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
-  const Ctx c{sm, bar, reinterpret_cast<volatile int*>(flags + 1), p.status, wait_limit,
-              flags[0] == 0};
+  const Ctx c{sm, bar, reinterpret_cast<volatile int*>(flags + 1), p.status,
+              reinterpret_cast<uint32_t*>(sm + S::kOffMisc + 12), wait_limit, flags[0] == 0};
 
   // register shares: bf16 4 x 72 + 8 x 216, e4m3 4 x 64 + 8 x 184 + 4 x 80 warps' worth
   static_assert(4 * 72 + 8 * 216 <= 12 * 168 && 4 * 64 + 8 * 184 + 4 * 80 <= 16 * 128, "registers");
@@ -730,9 +804,9 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
     if (warp == 0) {
-      kv_producer<D, FP8>(c, p, &tk, &tv);
+      producer<D, FP8>(c, p, &tk, &tq, 0);
     } else if (warp == 3) {
-      q_producer<D, FP8>(c, p, &tq);
+      producer<D, FP8>(c, p, &tv, &tq, 1);
     } else {
       if (warp == 1)
         s_issuer<D, FP8>(c, p, tmem);
@@ -746,6 +820,7 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) drain_kv(c, ring_ahead(p));
     if (warp == 1) {
       tc_fence_after();
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),

@@ -82,8 +82,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-}  // namespace
-
 // TMA descriptor of a bf16 pool [num_blocks, 16, Hkv, D] seen as the 3-D tensor
 // (D, Hkv, num_blocks * 16) with a 64 x 1 x 16 box and the 128-byte swizzle.
 bool pool_map(CUtensorMap* map, const void* base, int64_t num_blocks, int block_size, int hkv,
@@ -95,6 +93,25 @@ bool pool_map(CUtensorMap* map, const void* base, int64_t num_blocks, int block_
   cuuint32_t box[3] = {64, 1, 16};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+// TMA descriptor of a bf16 pool [num_blocks, 16, Hkv, D] seen as the 5-D tensor (64 dims of a half,
+// 8 rows, D / 64 halves, num_blocks * 2 groups of 8 rows, Hkv): a 64 x 8 x D/64 x 2 x 1 box is a
+// whole K (or V) block of one kv head, as 8-row groups of 1 KB per dim half (128-byte swizzle).
+bool pool_map_rows(CUtensorMap* map, const void* base, int64_t num_blocks, int hkv, int d) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = (cuuint64_t)hkv * d * 2;
+  cuuint64_t dims[5] = {64, 8, (cuuint64_t)(d / 64), (cuuint64_t)num_blocks * 2, (cuuint64_t)hkv};
+  cuuint64_t strides[4] = {row, 128, 8 * row, (cuuint64_t)d * 2};
+  cuuint32_t box[5] = {64, 8, (cuuint32_t)(d / 64), 2, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -258,8 +258,8 @@ pa_status pa_tree_attention(const void* q, const void* k_blocks, const void* v_b
         query_map(&tq, q, num_tokens, num_heads, head_dim, m.group, p.tile_rows / m.group) &&
         (fp8 ? pool_map_fp8(&tk, k_blocks, num_blocks, 16, num_kv_heads, head_dim) &&
                    pool_map_fp8(&tv, v_blocks, num_blocks, 16, num_kv_heads, head_dim)
-             : pool_map(&tk, k_blocks, num_blocks, 16, num_kv_heads, head_dim) &&
-                   pool_map(&tv, v_blocks, num_blocks, 16, num_kv_heads, head_dim));
+             : pool_map_rows(&tk, k_blocks, num_blocks, num_kv_heads, head_dim) &&
+                   pool_map_rows(&tv, v_blocks, num_blocks, num_kv_heads, head_dim));
     if (!ok) return PA_ECUDA;
   }
   if (launch_tree_plan(p, stream) != cudaSuccess) return PA_ECUDA;

@@ -158,6 +158,17 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_5d(void* smem_dst, const CUtensorMap* map, int32_t c0,
+                                            int32_t c1, int32_t c2, int32_t c3, int32_t c4,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -600,10 +611,15 @@ struct TreeParams {
   int* status;
   int32_t q_bf16, out_vec;
 };
-// An item of one row tile costs two units of weight a key tile, one of two tiles three (they share
-// the keys' copies).
+// The work of an item, in about hundredths of a microsecond (only the balance between the CTAs
+// depends on it): a key tile of one row tile of w warps' rows takes 1.35 us and 0.1 us for each
+// warp (measured 1.45 to 1.75 us: the copies bound the small ones, the exponentials the large),
+// of two row tiles 2.8 us; every item about 3 us for its beginning and end.
+constexpr int kTreeItemWeight = 300;
 __host__ __device__ inline int tree_weight(const TreeParams& p, int rows) {
-  return rows > p.tile_rows ? 3 : 2;
+  if (p.key_tile < 64) return 300;  // the general kernel's key tiles are alike
+  const int warps = (rows + 31) / 32;
+  return rows > p.tile_rows ? 250 + 4 * warps : 135 + 10 * warps;
 }
 struct TreeLayout {
   int64_t cum_off, starts_off, ml_off, o_off, bytes;
@@ -632,8 +648,7 @@ struct DeviceState {
 const DeviceState* device_state();
 
 // tensor maps (false: the driver refused), waits and paths of the attention kernels; see pa_api.cu
-bool pool_map(CUtensorMap* map, const void* base, int64_t num_blocks, int block_size, int hkv,
-              int d);
+bool pool_map_rows(CUtensorMap* map, const void* base, int64_t num_blocks, int hkv, int d);
 bool pool_map_fp8(CUtensorMap* map, const void* base, int64_t num_blocks, int block_size,
                   int hkv, int d);
 bool query_map(CUtensorMap* map, const void* q, int64_t num_tokens, int h, int d, int group,
