@@ -27,6 +27,7 @@ PA_F32, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
 PA_FLAG_BITWISE = 1
 _DT = {torch.float32: PA_F32, torch.bfloat16: PA_BF16, torch.float8_e4m3fn: PA_FP8_E4M3}
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
 _vp, _i32, _i64, _f32, _sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                               ctypes.c_size_t)
 _SIGS = {
@@ -536,12 +537,35 @@ class _RopeScaling(ctypes.Structure):
         "high_freq_factor")]
 
 
-def _same_device(*ts):
-    devices = {t.device for t in ts if t is not None}
-    if len(devices) > 1:
-        raise ValueError("tensors must live on one device")
-    if devices and devices.pop().index != torch.cuda.current_device():
-        raise ValueError("tensors must live on the current CUDA device")
+def _arrays(dev, *ts):
+    """Contiguous tensors (or None) on CUDA device `dev`."""
+    for t in ts:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous and live on the current CUDA device")
+
+
+def _ints(dev, *ts):
+    """Contiguous int32 tensors on CUDA device `dev`."""
+    for t in ts:
+        if t.get_device() != dev or t.dtype is not torch.int32 or not t.is_contiguous():
+            raise ValueError("metadata tensors must be contiguous int32 tensors on the current "
+                             "CUDA device")
+
+
+def _a(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on(dev, stream):
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _scratch(nbytes, dev, stream):
+    """Workspace of one call; it stays with the call's stream when that is not the current one."""
+    w = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", dev))
+    if stream is not None:
+        w.record_stream(stream)
+    return w
 
 
 def pa_rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0,
@@ -576,13 +600,13 @@ def pa_rope_and_cache(q, k, v, q_out, k_blocks, v_blocks, positions, slot_mappin
     [T, Hkv, D], and the scatter of k and v into the pools at slot_mapping.  The tokens of q, k, v
     and q_out may be strided (views of one fused product).  inv_freq: fp64 [rotary_dim / 2]
     (pa_rope_frequencies); scales as in pa_reshape_and_cache."""
+    dev = torch.cuda.current_device()
     for t in (q, k, v, q_out):
-        if t is not None and (not t.is_cuda or t.dim() != 3):
-            raise ValueError("q, k, v and q_out must be [T, heads, D] CUDA tensors")
-    _dev(k_blocks, v_blocks, positions, slot_mapping, inv_freq)
-    _i32t(positions, slot_mapping)
-    _same_device(q, k, v, q_out, k_blocks, v_blocks, positions, slot_mapping, inv_freq, k_scales,
-                 v_scales)
+        if t is not None and (t.get_device() != dev or t.dim() != 3):
+            raise ValueError("q, k, v and q_out must be [T, heads, D] tensors on the current CUDA "
+                             "device")
+    _arrays(dev, k_blocks, v_blocks, inv_freq, k_scales, v_scales)
+    _ints(dev, positions, slot_mapping)
     if k.shape != v.shape or k_blocks.dim() != 4 or k_blocks.shape != v_blocks.shape:
         raise ValueError("k, v must be [T, Hkv, D]; pools [NB, b, Hkv, D]")
     if k.dtype != v.dtype or k_blocks.dtype != v_blocks.dtype:
@@ -604,12 +628,12 @@ def pa_rope_and_cache(q, k, v, q_out, k_blocks, v_blocks, positions, slot_mappin
         raise ValueError("inv_freq must be fp64 [rotary_dim / 2]")
     _head_scales(Hkv, k_scales, v_scales)
     _check(_lib.pa_rope_and_cache(
-        _p(q), 0 if q is None else _token_rows(q, "q"),
-        _p(q_out), 0 if q is None else _token_rows(q_out, "q_out"), _p(k), _token_rows(k, "k"),
-        _p(v), _token_rows(v, "v"), _p(k_blocks), _p(v_blocks), _p(positions), _p(slot_mapping),
-        _p(inv_freq), 2 * inv_freq.numel(), int(bool(interleaved)), float(attn_factor), T, H, Hkv,
-        D, bs, NB, _DT[k.dtype], _DT[k_blocks.dtype], float(k_scale), float(v_scale), _p(k_scales),
-        _p(v_scales), _stream(stream)), "pa_rope_and_cache")
+        _a(q), 0 if q is None else _token_rows(q, "q"),
+        _a(q_out), 0 if q is None else _token_rows(q_out, "q_out"), _a(k), _token_rows(k, "k"),
+        _a(v), _token_rows(v, "v"), _a(k_blocks), _a(v_blocks), _a(positions), _a(slot_mapping),
+        _a(inv_freq), 2 * inv_freq.numel(), int(bool(interleaved)), float(attn_factor), T, H, Hkv,
+        D, bs, NB, _DT[k.dtype], _DT[k_blocks.dtype], float(k_scale), float(v_scale), _a(k_scales),
+        _a(v_scales), _on(dev, stream)), "pa_rope_and_cache")
     return q_out
 
 
@@ -627,11 +651,9 @@ def pa_tree_attention(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, pos
     query_start_loc[s] cached positions) over its context and the nodes of their tree_mask rows:
     int32 [T, mask_words], bit i of a row = node i of the token's sequence.  sinks, lse and scales
     as in pa_varlen_forward."""
-    _dev(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, positions, tree_mask, block_tables,
-         workspace, sinks, lse)
-    _i32t(query_start_loc, seq_lens, positions, tree_mask, block_tables)
-    _same_device(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, positions, tree_mask,
-                 block_tables, workspace, sinks, lse, k_scales, v_scales)
+    dev = torch.cuda.current_device()
+    _arrays(dev, q, k_blocks, v_blocks, out, workspace, sinks, lse, k_scales, v_scales)
+    _ints(dev, query_start_loc, seq_lens, positions, tree_mask, block_tables)
     if q.dim() != 3 or out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("q and out must be [T, H, D] of one dtype")
     if k_blocks.shape != v_blocks.shape or k_blocks.dtype != v_blocks.dtype:
@@ -652,14 +674,14 @@ def pa_tree_attention(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, pos
     _head_scales(Hkv, k_scales, v_scales)
     if workspace is None:
         n = pa_tree_attention_workspace_size(S, T, H, Hkv, D, block_tables.shape[1], bs)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(n, dev, stream)
     _check(_lib.pa_tree_attention(
-        _p(q), _p(k_blocks), _p(v_blocks), _p(out), _p(query_start_loc), _p(seq_lens),
-        _p(positions), _p(tree_mask), _p(block_tables), S, T, tree_mask.shape[1], H, Hkv, D, bs, NB,
+        _a(q), _a(k_blocks), _a(v_blocks), _a(out), _a(query_start_loc), _a(seq_lens),
+        _a(positions), _a(tree_mask), _a(block_tables), S, T, tree_mask.shape[1], H, Hkv, D, bs, NB,
         block_tables.shape[1], _DT[q.dtype], _DT[k_blocks.dtype], float(scale),
-        int(sliding_window), _p(sinks), _p(lse), float(k_scale), float(v_scale), _p(k_scales),
-        _p(v_scales), _p(workspace), workspace.numel() * workspace.element_size(),
-        _stream(stream)), "pa_tree_attention")
+        int(sliding_window), _a(sinks), _a(lse), float(k_scale), float(v_scale), _a(k_scales),
+        _a(v_scales), _a(workspace), workspace.numel() * workspace.element_size(),
+        _on(dev, stream)), "pa_tree_attention")
     return out
 
 
@@ -677,64 +699,62 @@ def pa_tree_commit(k_blocks, v_blocks, block_tables, context_lens, accepted, num
     """Move the K and V rows of the accepted nodes (accepted [S, max_accepted], the first
     num_accepted[s] of a row, strictly increasing) of each sequence's tree, which begins at
     position context_lens[s], to its first positions."""
-    _dev(k_blocks, v_blocks, block_tables, context_lens, accepted, num_accepted)
-    _i32t(block_tables, context_lens, accepted, num_accepted)
-    _same_device(k_blocks, v_blocks, block_tables, context_lens, accepted, num_accepted)
+    dev = torch.cuda.current_device()
+    _arrays(dev, k_blocks, v_blocks)
+    _ints(dev, block_tables, context_lens, accepted, num_accepted)
     NB, bs, Hkv, D = _pools(k_blocks, v_blocks)
     if accepted.dim() != 2 or block_tables.dim() != 2:
         raise ValueError("accepted must be [S, max_accepted], block_tables [S, max_blocks]")
     S, A = accepted.shape
     if context_lens.numel() != S or num_accepted.numel() != S or block_tables.shape[0] != S:
         raise ValueError("context_lens and num_accepted must be [S]")
-    _check(_lib.pa_tree_commit(_p(k_blocks), _p(v_blocks), _p(block_tables), _p(context_lens),
-                               _p(accepted), _p(num_accepted), S, A, Hkv, D, bs, NB,
-                               block_tables.shape[1], _DT[k_blocks.dtype], _stream(stream)),
+    _check(_lib.pa_tree_commit(_a(k_blocks), _a(v_blocks), _a(block_tables), _a(context_lens),
+                               _a(accepted), _a(num_accepted), S, A, Hkv, D, bs, NB,
+                               block_tables.shape[1], _DT[k_blocks.dtype], _on(dev, stream)),
            "pa_tree_commit")
 
 
 def pa_copy_blocks(k_blocks, v_blocks, block_pairs, stream=None):
     """Copy whole blocks of both pools (v_blocks may be None) for every (src, dst) of block_pairs
     [n, 2]; (-1, -1) is skipped."""
-    _dev(k_blocks, v_blocks, block_pairs)
-    _i32t(block_pairs)
-    _same_device(k_blocks, v_blocks, block_pairs)
+    dev = torch.cuda.current_device()
+    _arrays(dev, k_blocks, v_blocks)
+    _ints(dev, block_pairs)
     NB, bs, Hkv, D = _pools(k_blocks, v_blocks)
     if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
         raise ValueError("block_pairs must be [n, 2]")
-    _check(_lib.pa_copy_blocks(_p(k_blocks), _p(v_blocks), _p(block_pairs), block_pairs.shape[0],
-                               Hkv, D, bs, NB, _DT[k_blocks.dtype], _stream(stream)),
+    _check(_lib.pa_copy_blocks(_a(k_blocks), _a(v_blocks), _a(block_pairs), block_pairs.shape[0],
+                               Hkv, D, bs, NB, _DT[k_blocks.dtype], _on(dev, stream)),
            "pa_copy_blocks")
 
 
 def _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, *lists):
-    _dev(block_tables, seq_lens, ref_counts, free_list, free_count, *lists)
-    _i32t(block_tables, seq_lens, ref_counts, free_list, free_count, *lists)
-    _same_device(block_tables, seq_lens, ref_counts, free_list, free_count, *lists)
+    dev = torch.cuda.current_device()
+    _ints(dev, block_tables, seq_lens, ref_counts, free_list, free_count, *lists)
     if block_tables.dim() != 2 or seq_lens.numel() != block_tables.shape[0]:
         raise ValueError("block_tables must be [rows, max_blocks] and seq_lens [rows]")
     if free_list.numel() != ref_counts.numel() or free_count.numel() != 1:
         raise ValueError("ref_counts and free_list must be [num_blocks], free_count [1]")
     if any(x.numel() != lists[0].numel() for x in lists):
         raise ValueError("the lists must have one length")
+    return dev
 
 
 def pa_fork_sequences(block_tables, seq_lens, parents, children, ref_counts, free_list, free_count,
                       block_size, block_pairs=None, stream=None):
     """Make row children[f] a copy of row parents[f] that shares its whole blocks; returns
     block_pairs [n, 2], the partly filled blocks to copy with pa_copy_blocks."""
-    _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, parents, children)
+    dev = _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, parents, children)
     n = parents.numel()
     if block_pairs is None:
         block_pairs = torch.empty(n, 2, dtype=torch.int32, device=block_tables.device)
-    _dev(block_pairs)
-    _i32t(block_pairs)
-    _same_device(block_tables, block_pairs)
+    _ints(dev, block_pairs)
     if block_pairs.shape != (n, 2):
         raise ValueError("block_pairs must be [n, 2]")
-    _check(_lib.pa_fork_sequences(_p(block_tables), _p(seq_lens), _p(parents), _p(children), n,
+    _check(_lib.pa_fork_sequences(_a(block_tables), _a(seq_lens), _a(parents), _a(children), n,
                                   block_tables.shape[0], block_tables.shape[1], int(block_size),
-                                  _p(ref_counts), _p(free_list), _p(free_count),
-                                  ref_counts.numel(), _p(block_pairs), _stream(stream)),
+                                  _a(ref_counts), _a(free_list), _a(free_count),
+                                  ref_counts.numel(), _a(block_pairs), _on(dev, stream)),
            "pa_fork_sequences")
     return block_pairs
 
@@ -742,19 +762,20 @@ def pa_fork_sequences(block_tables, seq_lens, parents, children, ref_counts, fre
 def pa_grow_sequences(block_tables, seq_lens, sequences, new_lens, ref_counts, free_list,
                       free_count, block_size, stream=None):
     """Lengthen the rows `sequences` to new_lens, taking the blocks they need."""
-    _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, sequences, new_lens)
-    _check(_lib.pa_grow_sequences(_p(block_tables), _p(seq_lens), _p(sequences), _p(new_lens),
+    dev = _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, sequences,
+                       new_lens)
+    _check(_lib.pa_grow_sequences(_a(block_tables), _a(seq_lens), _a(sequences), _a(new_lens),
                                   sequences.numel(), block_tables.shape[0], block_tables.shape[1],
-                                  int(block_size), _p(ref_counts), _p(free_list), _p(free_count),
-                                  ref_counts.numel(), _stream(stream)), "pa_grow_sequences")
+                                  int(block_size), _a(ref_counts), _a(free_list), _a(free_count),
+                                  ref_counts.numel(), _on(dev, stream)), "pa_grow_sequences")
 
 
 def pa_free_sequences(block_tables, seq_lens, sequences, ref_counts, free_list, free_count,
                       block_size, stream=None):
     """End the rows `sequences`: their blocks lose a reference each, and those without any go
     back to the free list in ascending order."""
-    _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, sequences)
-    _check(_lib.pa_free_sequences(_p(block_tables), _p(seq_lens), _p(sequences),
+    dev = _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, sequences)
+    _check(_lib.pa_free_sequences(_a(block_tables), _a(seq_lens), _a(sequences),
                                   sequences.numel(), block_tables.shape[0], block_tables.shape[1],
-                                  int(block_size), _p(ref_counts), _p(free_list), _p(free_count),
-                                  ref_counts.numel(), _stream(stream)), "pa_free_sequences")
+                                  int(block_size), _a(ref_counts), _a(free_list), _a(free_count),
+                                  ref_counts.numel(), _on(dev, stream)), "pa_free_sequences")

@@ -612,14 +612,13 @@ struct TreeParams {
   int32_t q_bf16, out_vec;
 };
 // The work of an item, in about hundredths of a microsecond (only the balance between the CTAs
-// depends on it): a key tile of one row tile of w warps' rows takes 1.35 us and 0.1 us for each
-// warp (measured 1.45 to 1.75 us: the copies bound the small ones, the exponentials the large),
-// of two row tiles 2.8 us; every item about 3 us for its beginning and end.
-constexpr int kTreeItemWeight = 300;
+// depends on it): a key tile of one row tile takes about 1.5 us, a little more the more warps its
+// rows fill, of two row tiles 2.3 us; every item 2 us for its beginning and end.
+constexpr int kTreeItemWeight = 200;
 __host__ __device__ inline int tree_weight(const TreeParams& p, int rows) {
-  if (p.key_tile < 64) return 300;  // the general kernel's key tiles are alike
+  if (p.key_tile < 64) return 100;  // the general kernel's key tiles are alike
   const int warps = (rows + 31) / 32;
-  return rows > p.tile_rows ? 250 + 4 * warps : 135 + 10 * warps;
+  return rows > p.tile_rows ? 206 + 3 * warps : 140 + 4 * warps;
 }
 struct TreeLayout {
   int64_t cum_off, starts_off, ml_off, o_off, bytes;
