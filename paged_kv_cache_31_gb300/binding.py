@@ -562,7 +562,7 @@ def _on(dev, stream):
 
 def _scratch(nbytes, dev, stream):
     """Workspace of one call; it stays with the call's stream when that is not the current one."""
-    w = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", dev))
+    w = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
     if stream is not None:
         w.record_stream(stream)
     return w
@@ -585,12 +585,12 @@ def pa_rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0,
     return f.to(device), af.value
 
 
-def _token_rows(t, what):
+def _token_rows(t, N, D, what):
     """Elements between the tokens of [T, N, D] rows whose heads are contiguous."""
-    T, N, D = t.shape
-    if (D > 1 and t.stride(2) != 1) or (N > 1 and t.stride(1) != D):
+    a, b, c = t.stride()
+    if (c != 1 and D > 1) or (b != D and N > 1):
         raise ValueError(f"{what}: a token's heads must be contiguous")
-    return t.stride(0) if T > 1 else N * D
+    return a if len(t) > 1 else N * D
 
 
 def pa_rope_and_cache(q, k, v, q_out, k_blocks, v_blocks, positions, slot_mapping, inv_freq,
@@ -601,39 +601,45 @@ def pa_rope_and_cache(q, k, v, q_out, k_blocks, v_blocks, positions, slot_mappin
     and q_out may be strided (views of one fused product).  inv_freq: fp64 [rotary_dim / 2]
     (pa_rope_frequencies); scales as in pa_reshape_and_cache."""
     dev = torch.cuda.current_device()
-    for t in (q, k, v, q_out):
-        if t is not None and (t.get_device() != dev or t.dim() != 3):
+    if (q is None) != (q_out is None):
+        raise ValueError("give both q and q_out or neither")
+    for t in (k, v) if q is None else (q, k, v, q_out):
+        if t.get_device() != dev or t.dim() != 3:
             raise ValueError("q, k, v and q_out must be [T, heads, D] tensors on the current CUDA "
                              "device")
-    _arrays(dev, k_blocks, v_blocks, inv_freq, k_scales, v_scales)
+    _arrays(dev, k_blocks, v_blocks, inv_freq)
     _ints(dev, positions, slot_mapping)
-    if k.shape != v.shape or k_blocks.dim() != 4 or k_blocks.shape != v_blocks.shape:
+    kv_shape, pool_shape, src, kv = k.shape, k_blocks.shape, k.dtype, k_blocks.dtype
+    if v.shape != kv_shape or len(pool_shape) != 4 or v_blocks.shape != pool_shape:
         raise ValueError("k, v must be [T, Hkv, D]; pools [NB, b, Hkv, D]")
-    if k.dtype != v.dtype or k_blocks.dtype != v_blocks.dtype:
+    if v.dtype != src or v_blocks.dtype != kv:
         raise ValueError("k and v (and the two pools) must share one dtype")
-    T, Hkv, D = k.shape
-    NB, bs, Hkv2, D2 = k_blocks.shape
-    if (Hkv, D) != (Hkv2, D2):
+    T, Hkv, D = kv_shape
+    NB, bs, Hkv2, D2 = pool_shape
+    if Hkv != Hkv2 or D != D2:
         raise ValueError("kv heads / head size differ between rows and pool")
     if positions.numel() != T or slot_mapping.numel() != T:
         raise ValueError("positions and slot_mapping must be [T]")
-    if (q is None) != (q_out is None):
-        raise ValueError("give both q and q_out or neither")
-    H = 0
+    H = q_ptr = out_ptr = q_rows = out_rows = 0
     if q is not None:
-        H = q.shape[1]
-        if q.shape != (T, H, D) or q_out.shape != q.shape or not q.dtype == q_out.dtype == k.dtype:
+        q_shape = q.shape
+        if q_shape[0] != T or q_shape[2] != D or q_out.shape != q_shape or q.dtype != src \
+                or q_out.dtype != src:
             raise ValueError("q and q_out must be [T, H, D] of the rows' dtype")
+        H = q_shape[1]
+        q_ptr, q_rows = q.data_ptr(), _token_rows(q, H, D, "q")
+        out_ptr, out_rows = q_out.data_ptr(), _token_rows(q_out, H, D, "q_out")
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
         raise ValueError("inv_freq must be fp64 [rotary_dim / 2]")
-    _head_scales(Hkv, k_scales, v_scales)
+    if k_scales is not None or v_scales is not None:
+        _arrays(dev, k_scales, v_scales)
+        _head_scales(Hkv, k_scales, v_scales)
     _check(_lib.pa_rope_and_cache(
-        _a(q), 0 if q is None else _token_rows(q, "q"),
-        _a(q_out), 0 if q is None else _token_rows(q_out, "q_out"), _a(k), _token_rows(k, "k"),
-        _a(v), _token_rows(v, "v"), _a(k_blocks), _a(v_blocks), _a(positions), _a(slot_mapping),
-        _a(inv_freq), 2 * inv_freq.numel(), int(bool(interleaved)), float(attn_factor), T, H, Hkv,
-        D, bs, NB, _DT[k.dtype], _DT[k_blocks.dtype], float(k_scale), float(v_scale), _a(k_scales),
-        _a(v_scales), _on(dev, stream)), "pa_rope_and_cache")
+        q_ptr, q_rows, out_ptr, out_rows, k.data_ptr(), _token_rows(k, Hkv, D, "k"), v.data_ptr(),
+        _token_rows(v, Hkv, D, "v"), k_blocks.data_ptr(), v_blocks.data_ptr(),
+        positions.data_ptr(), slot_mapping.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel(),
+        bool(interleaved), attn_factor, T, H, Hkv, D, bs, NB, _DT[src], _DT[kv], k_scale, v_scale,
+        _a(k_scales), _a(v_scales), _on(dev, stream)), "pa_rope_and_cache")
     return q_out
 
 
@@ -652,36 +658,42 @@ def pa_tree_attention(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, pos
     int32 [T, mask_words], bit i of a row = node i of the token's sequence.  sinks, lse and scales
     as in pa_varlen_forward."""
     dev = torch.cuda.current_device()
-    _arrays(dev, q, k_blocks, v_blocks, out, workspace, sinks, lse, k_scales, v_scales)
+    _arrays(dev, q, k_blocks, v_blocks, out, workspace, sinks, lse)
     _ints(dev, query_start_loc, seq_lens, positions, tree_mask, block_tables)
-    if q.dim() != 3 or out.shape != q.shape or out.dtype != q.dtype:
+    q_shape, pool_shape, src, kv = q.shape, k_blocks.shape, q.dtype, k_blocks.dtype
+    if len(q_shape) != 3 or out.shape != q_shape or out.dtype != src:
         raise ValueError("q and out must be [T, H, D] of one dtype")
-    if k_blocks.shape != v_blocks.shape or k_blocks.dtype != v_blocks.dtype:
+    if len(pool_shape) != 4 or v_blocks.shape != pool_shape or v_blocks.dtype != kv:
         raise ValueError("k_blocks and v_blocks must match")
-    T, H, D = q.shape
-    NB, bs, Hkv, D2 = k_blocks.shape
+    T, H, D = q_shape
+    NB, bs, Hkv, D2 = pool_shape
     S = query_start_loc.numel() - 1
+    mask_shape, table_shape = tree_mask.shape, block_tables.shape
     if D2 != D:
         raise ValueError("head size differs between q and the pool")
-    if tree_mask.dim() != 2 or tree_mask.shape[0] != T or positions.numel() != T:
+    if len(mask_shape) != 2 or mask_shape[0] != T or positions.numel() != T:
         raise ValueError("tree_mask must be [T, mask_words] and positions [T]")
-    if seq_lens.numel() != S or block_tables.dim() != 2 or block_tables.shape[0] != S:
+    if seq_lens.numel() != S or len(table_shape) != 2 or table_shape[0] != S:
         raise ValueError("seq_lens must be [S] and block_tables [S, max_blocks]")
     if sinks is not None and (sinks.dtype != torch.float32 or sinks.shape != (H,)):
         raise ValueError("sinks must be a contiguous fp32 [num_heads] tensor")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (H, T)):
         raise ValueError("lse must be a contiguous fp32 [num_heads, num_tokens] tensor")
-    _head_scales(Hkv, k_scales, v_scales)
+    if k_scales is not None or v_scales is not None:
+        _arrays(dev, k_scales, v_scales)
+        _head_scales(Hkv, k_scales, v_scales)
     if workspace is None:
-        n = pa_tree_attention_workspace_size(S, T, H, Hkv, D, block_tables.shape[1], bs)
-        workspace = _scratch(n, dev, stream)
+        nbytes = _lib.pa_tree_attention_workspace_size(S, T, H, Hkv, D, table_shape[1], bs)
+        workspace = _scratch(nbytes, dev, stream)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
     _check(_lib.pa_tree_attention(
-        _a(q), _a(k_blocks), _a(v_blocks), _a(out), _a(query_start_loc), _a(seq_lens),
-        _a(positions), _a(tree_mask), _a(block_tables), S, T, tree_mask.shape[1], H, Hkv, D, bs, NB,
-        block_tables.shape[1], _DT[q.dtype], _DT[k_blocks.dtype], float(scale),
-        int(sliding_window), _a(sinks), _a(lse), float(k_scale), float(v_scale), _a(k_scales),
-        _a(v_scales), _a(workspace), workspace.numel() * workspace.element_size(),
-        _on(dev, stream)), "pa_tree_attention")
+        q.data_ptr(), k_blocks.data_ptr(), v_blocks.data_ptr(), out.data_ptr(),
+        query_start_loc.data_ptr(), seq_lens.data_ptr(), positions.data_ptr(),
+        tree_mask.data_ptr(), block_tables.data_ptr(), S, T, mask_shape[1], H, Hkv, D, bs, NB,
+        table_shape[1], _DT[src], _DT[kv], scale, int(sliding_window), _a(sinks), _a(lse), k_scale,
+        v_scale, _a(k_scales), _a(v_scales), workspace.data_ptr(), nbytes, _on(dev, stream)),
+        "pa_tree_attention")
     return out
 
 

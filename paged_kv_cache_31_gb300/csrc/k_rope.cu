@@ -30,6 +30,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kCheckedTokens = 2048;  // up to here every CTA checks all slots itself
 constexpr int kMaxHalf = 128;         // rotary_dim / 2, at most
+constexpr int kMaxTokens = 8;         // tokens of a CTA, at most
 
 // Division of 0 <= n < 2^31 by a fixed d >= 1: with l = ceil(log2 d) and
 // m = ceil(2^(31 + l) / d) < 2^32, floor(n m / 2^(31 + l)) is the quotient (the error of m adds
@@ -52,19 +53,33 @@ struct Geometry {
   int rot_units;      // rotated units of a head
 };
 
-// one chunk of VE elements as fp32
+// one chunk of VE elements: as it lies in memory, and its values in fp32
 template <typename TS, int VE>
-__device__ __forceinline__ void load_chunk(const TS* p, float (&x)[VE]) {
-  if constexpr (sizeof(TS) * VE == 16) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const TS* e = reinterpret_cast<const TS*>(&w);
+struct Chunk {
+  static constexpr bool kWide = sizeof(TS) * VE == 16;
+  uint32_t w[kWide ? 4 : VE];
+  __device__ __forceinline__ void load(const TS* p) {
+    if constexpr (kWide) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < VE; ++i) x[i] = to_f32(e[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VE; ++i) x[i] = to_f32(p[i]);
+      for (int i = 0; i < VE; ++i) w[i] = __float_as_uint(to_f32(p[i]));
+    }
   }
-}
+  __device__ __forceinline__ void values(float (&x)[VE]) const {
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      if constexpr (kWide && sizeof(TS) == 2)
+        x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+      else
+        x[i] = __uint_as_float(w[i]);
+    }
+  }
+};
 
 // VE fp32 values in pool type DST (a pa_dtype), rounded to nearest even
 template <int DST, int VE>
@@ -119,6 +134,7 @@ __global__ void __launch_bounds__(kThreads)
   static_assert(!IL || VE % 2 == 0, "interleaved pairs stay inside a chunk");
   __shared__ int s_skip;
   __shared__ uint64_t s_turn[kMaxHalf];
+  __shared__ int32_t s_slot[kMaxTokens];
   extern __shared__ __align__(16) float s_trig[];  // [tok][half] cos, then sin
   pdl_wait();
   pdl_launch_dependents();
@@ -143,6 +159,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   const int64_t t0 = (int64_t)blockIdx.x * tok_per_cta;
   const int ntok = (int)min((int64_t)tok_per_cta, p.num_tokens - t0);
+  if ((int)threadIdx.x < ntok) s_slot[threadIdx.x] = p.slots[t0 + threadIdx.x];
   float* s_cos = s_trig;
   float* s_sin = s_trig + tok_per_cta * half;
   for (int a = threadIdx.x; a < ntok * half; a += kThreads) {
@@ -196,60 +213,63 @@ __global__ void __launch_bounds__(kThreads)
       inv = divide ? 1.f : 1.f / sc;
     }
     for (int k0 = 0; k0 < ntok; k0 += U) {
-      float a[U][VE], b[U][VE];
+      Chunk<TS, VE> ra[U], rb[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (k0 + u >= ntok) break;
-        load_chunk<TS, VE>(src + (k0 + u) * stride, a[u]);
-        if (two) load_chunk<TS, VE>(src + (k0 + u) * stride + half, b[u]);
+        ra[u].load(src + (k0 + u) * stride);
+        if (two) rb[u].load(src + (k0 + u) * stride + half);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int tk = k0 + u;
         if (tk >= ntok) break;
+        float a[VE], b[VE];
+        ra[u].values(a);
+        if (two) rb[u].values(b);
         if (rot) {
           const float* cs = s_cos + tk * half + (IL ? off / 2 : off);
           const float* sn = s_sin + tk * half + (IL ? off / 2 : off);
           if constexpr (IL) {
 #pragma unroll
             for (int i = 0; i < VE / 2; ++i) {
-              const float x = a[u][2 * i], y = a[u][2 * i + 1];
-              a[u][2 * i] = x * cs[i] - y * sn[i];
-              a[u][2 * i + 1] = x * sn[i] + y * cs[i];
+              const float x = a[2 * i], y = a[2 * i + 1];
+              a[2 * i] = x * cs[i] - y * sn[i];
+              a[2 * i + 1] = x * sn[i] + y * cs[i];
             }
           } else {
 #pragma unroll
             for (int i = 0; i < VE; ++i) {
-              const float x = a[u][i], y = b[u][i];
-              a[u][i] = x * cs[i] - y * sn[i];
-              b[u][i] = x * sn[i] + y * cs[i];
+              const float x = a[i], y = b[i];
+              a[i] = x * cs[i] - y * sn[i];
+              b[i] = x * sn[i] + y * cs[i];
             }
           }
         }
         if (to_q) {
           constexpr int SRC = sizeof(TS) == 2 ? PA_BF16 : PA_F32;
           const int64_t at = (t0 + tk) * p.q_out_stride + (int64_t)head * D + off;
-          store_chunk<SRC, VE>(p.q_out, at, a[u]);
-          if (two) store_chunk<SRC, VE>(p.q_out, at + half, b[u]);
+          store_chunk<SRC, VE>(p.q_out, at, a);
+          if (two) store_chunk<SRC, VE>(p.q_out, at + half, b);
           continue;
         }
         if (divide) {
 #pragma unroll
           for (int i = 0; i < VE; ++i) {
-            a[u][i] = __fdiv_rn(a[u][i], sc);
-            if (two) b[u][i] = __fdiv_rn(b[u][i], sc);
+            a[i] = __fdiv_rn(a[i], sc);
+            if (two) b[i] = __fdiv_rn(b[i], sc);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < VE; ++i) {
-            a[u][i] *= inv;
-            if (two) b[u][i] *= inv;
+            a[i] *= inv;
+            if (two) b[i] *= inv;
           }
         }
-        const int64_t at = ((int64_t)p.slots[t0 + tk] * p.num_kv_heads + hk) * D + off;
+        const int64_t at = ((int64_t)s_slot[tk] * p.num_kv_heads + hk) * D + off;
         void* pool = is_v ? p.v_blocks : p.k_blocks;
-        store_chunk<DST, VE>(pool, at, a[u]);
-        if (two) store_chunk<DST, VE>(pool, at + half, b[u]);
+        store_chunk<DST, VE>(pool, at, a);
+        if (two) store_chunk<DST, VE>(pool, at + half, b);
       }
     }
   }
@@ -264,7 +284,7 @@ cudaError_t launch_as(const RopeParams& p, int num_sms, cudaStream_t stream) {
   if (per_token > (1 << 28)) return cudaErrorInvalidValue;
   // eight tokens to a CTA when that still gives every SM four CTAs, fewer for smaller batches;
   // with one, its items are spread over several CTAs
-  int tok = 8;
+  int tok = kMaxTokens;
   while (tok > 1 && p.num_tokens < (int64_t)tok * 4 * num_sms) tok >>= 1;
   const int64_t most = (per_token + kThreads - 1) / kThreads;
   const int64_t parts = tok > 1 ? 1 : std::min<int64_t>(most, std::max<int64_t>(1, 2 * num_sms / p.num_tokens));

@@ -18,8 +18,10 @@
 // Per key tile of a stream:  S = Q K^T (M 128, N 128, K = head size);  mask, running max (moved,
 // with O rescaled, only when it grows by more than 2^8), p = 2^(s - m);  P written over S;
 // O += P V.  Over bf16 pools P is a bf16 pair hi + lo (two products with V, weights good to
-// 2^-16); over e4m3 pools it is one f16 value (2^-11), with q, K and V widened to f16 (exactly,
-// for the codes) in shared memory.  Row sums add the fp32 weights.
+// 2^-16); over e4m3 pools it is one f16 value (2^-11), with V widened to f16 (exactly) in shared
+// memory, while K's codes are used as they are: q is split into two e4m3 terms, hi + lo, with one
+// power of two per row (exact down to 2^-9 of the row's largest element), two products for S.
+// (Widening K too made the conversions bound the kernel.)  Row sums add the fp32 weights.
 //
 // Roles.  warp 0: TMA of K, warp 3: of Q (a ring of two row tiles) and V; K and V alternate in a
 // ring of five 128-key stages; warp 1: tensor-memory owner, issues S = Q K^T; warp 2: issues
@@ -63,7 +65,9 @@ struct Shape {
   static constexpr int kOffBad = kOffX + 2 * 128 * 8;          // [2][4] its warps' failed waits
   static constexpr int kOffBar = kOffBad + 2 * 4 * 4;
   static constexpr int kOffMisc = kOffBar + 40 * 8;
-  static constexpr int kSmem = kOffMisc + 32;  // tensor-memory base, flags, stages sent
+  // tensor-memory base, flags, stages sent; e4m3: the rows' scale exponents of four Q tiles
+  static constexpr int kOffExp = kOffMisc + 32;
+  static constexpr int kSmem = kOffExp + (FP8 ? 4 * 128 : 0);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
@@ -71,10 +75,10 @@ struct Shape {
 enum : int {
   B_QFULL = 0,                     // Q buffer landed
   B_QEMPTY = B_QFULL + 2,          // its last S = Q K^T is done
-  B_QCONV = B_QEMPTY + 2,          // e4m3: its f16 form is ready
+  B_QCONV = B_QEMPTY + 2,          // e4m3: it has been split
   B_FULL = B_QCONV + 2,            // K / V stage landed
   B_EMPTY = B_FULL + kStages,
-  B_CONV = B_EMPTY + kStages,      // e4m3: the stage's f16 form is ready
+  B_CONV = B_EMPTY + kStages,      // e4m3: the stage's V is ready as f16 (V's copies only)
   B_SFULL = B_CONV + kStages,      // per stream: S is ready
   B_PFULL = B_SFULL + 2,           // P is written
   B_PVDONE = B_PFULL + 2,          // P V is done: O is current, the S / P buffer is free
@@ -96,6 +100,15 @@ __device__ __forceinline__ void mma_ss(uint32_t elect, uint32_t d, uint64_t a, u
   asm volatile(
       "{\n\t.reg .pred e, p;\n\tsetp.ne.u32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elect)
+      : "memory");
+}
+// The same over e4m3 operands (K = 32).
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t elect, uint32_t d, uint64_t a, uint64_t b,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\tsetp.ne.u32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elect)
       : "memory");
 }
@@ -154,13 +167,16 @@ __device__ __forceinline__ bool ring_ahead(const TreeParams& p) {
   return p.rows_per_item == p.tile_rows;
 }
 struct Ring {
-  uint32_t st, par;
-  bool ahead, first;
+  uint32_t st, par;  // stage of this operand's current copy, phase parity of its barriers
+  // the same for barriers that only this operand's copies complete: its stages come round every
+  // kStages copies, as kStages is odd
+  uint32_t turn, par_own;
+  bool first;
   __device__ __forceinline__ Ring(const TreeParams& p, int kv) {
-    ahead = ring_ahead(p);
+    const bool ahead = ring_ahead(p);
     first = ahead && kv == 0;
     st = kv ? (ahead ? 2 : 1) : 0;
-    par = 0;
+    par = turn = par_own = 0;
   }
   __device__ __forceinline__ void next() {  // the next tile's copy of the same operand
     st += first ? 1 : 2;
@@ -169,8 +185,13 @@ struct Ring {
       st -= kStages;
       par ^= 1;
     }
+    if (++turn == kStages) {
+      turn = 0;
+      par_own ^= 1;
+    }
   }
 };
+static_assert(kStages % 2 == 1, "an operand's copies visit every stage");
 
 // Both streams take all key tiles of a segment with two row tiles.  With one row tile the streams
 // alternate, over segments too: the stream that does not take a segment's last tile begins the
@@ -228,9 +249,9 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
       if (!ok) break;
       if (lane < 8) {  // a block past the end: rows outside the pool, which TMA fills with zeros
         uint8_t* dst = c.sm + S::kOffKV + r.st * S::kTileBytes;
-        if constexpr (FP8)  // the codes go where the second dim half's rows will be
-          tma_load_3d(dst + S::kHalfBytes + lane * 2048, tkv, 0, g.kvh, id >= 0 ? id * 16 : -16,
-                      c.bar + B_FULL + r.st);
+        if constexpr (FP8)  // V's codes go where its second dim half's rows will be
+          tma_load_3d(dst + (kv ? S::kHalfBytes : 0) + lane * 2048, tkv, 0, g.kvh,
+                      id >= 0 ? id * 16 : -16, c.bar + B_FULL + r.st);
         else
           tma_load_5d(dst + lane * (S::kTileBytes / 8), tkv, 0, 0, 0, id >= 0 ? id * 2 : -2, g.kvh,
                       c.bar + B_FULL + r.st);
@@ -264,8 +285,9 @@ __device__ void drain_kv(const Ctx& c, bool ahead) {
 template <int D, bool FP8>
 __device__ void s_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   using S = Shape<D, FP8>;
+  // (f8f6f4's descriptor has zeros where e4m3 operands are named)
   constexpr uint32_t kIdesc = idesc_f16kind(128, kBN, 0, FP8 ? 0 : 1);
-  constexpr int kQ = FP8 ? B_QCONV : B_QFULL, kKV = FP8 ? B_CONV : B_FULL;
+  constexpr int kQ = FP8 ? B_QCONV : B_QFULL;
   const uint32_t sm = smem_u32(c.sm), elect = (threadIdx.x & 31) == 0;
   Ring r(p, 0);
   uint32_t nq = 0, cnt[2] = {0, 0};  // row tiles used; tiles of each stream
@@ -276,7 +298,7 @@ __device__ void s_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   while (walk.next(p, g)) {
     const bool two = two_tiles(p, g);
     for (int j = g.t0; j < g.t1; ++j) {
-      if (!wait_all(c, kKV + r.st, r.par)) return;
+      if (!wait_all(c, B_FULL + r.st, r.par)) return;
       const uint32_t kb = sm + S::kOffKV + r.st * S::kTileBytes;
 #pragma unroll 1
       for (int y = 0; y < (two ? 2 : 1); ++y) {
@@ -292,10 +314,15 @@ __device__ void s_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
 #pragma unroll 1
         for (int h = 0; h < S::kHalves; ++h) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ss(elect, tmem + col_s(x), qd + 2 * kk, kd + 2 * kk, kIdesc, (h | kk) ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk) {
+            if constexpr (FP8)  // q's high codes, then its low ones, over all 128 dims of K
+              mma_ss_e4m3(elect, tmem + col_s(x), qd + 2 * kk, kd + 2 * kk, kIdesc,
+                          (h | kk) ? 1u : 0u);
+            else
+              mma_ss(elect, tmem + col_s(x), qd + 2 * kk, kd + 2 * kk, kIdesc, (h | kk) ? 1u : 0u);
+          }
           qd += S::kHalfBytes / 16;
-          kd += S::kDimHalf / 16;
+          if constexpr (!FP8) kd += S::kDimHalf / 16;
         }
         mma_commit(c.bar + B_SFULL + x);
         if (x) ++cnt[1]; else ++cnt[0];
@@ -314,7 +341,6 @@ template <int D, bool FP8>
 __device__ void pv_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   using S = Shape<D, FP8>;
   constexpr uint32_t kIdesc = idesc_f16kind(128, D, 1, FP8 ? 0 : 1);
-  constexpr int kKV = FP8 ? B_CONV : B_FULL;
   const int lane = threadIdx.x & 31;
   const uint32_t elect = lane == 0;
   Ring r(p, 1);
@@ -326,7 +352,7 @@ __device__ void pv_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   for (; walk.next(p, g); ++seg) {
     const bool two = two_tiles(p, g);
     for (int j = g.t0; j < g.t1; ++j) {
-      if (!wait_all(c, kKV + r.st, r.par)) return;
+      if (!wait_all(c, (FP8 ? B_CONV : B_FULL) + r.st, FP8 ? r.par_own : r.par)) return;
       uint8_t* v = c.sm + S::kOffKV + r.st * S::kTileBytes;
       if constexpr (!FP8) {  // (the converters do it over e4m3 pools)
         // rows of the last block past the sequence's end: zeros (whole blocks past it are)
@@ -404,40 +430,84 @@ __device__ __forceinline__ void widen_rows(uint8_t* tile, int w, int lane, int l
   }
 }
 
-// Warps 12 and 13 widen Q and K, 14 and 15 V: each half of every tile, in the order of the copies.
+// Split the warp's 32 rows of a Q tile (bf16, dim half by dim half) into e4m3 codes, in place: hi
+// in the first half's rows, lo in the second's (rows of 128 bytes, swizzled as they were).  With the
+// row times 2^s, its largest magnitude in [128, 256), hi is the nearest code and lo the rest: eight
+// significant bits in two of four, exactly, for elements down to 2^-9 of the row's largest (and to
+// 2^-17 of it below that).  Two lanes share a row, a dim half each.
+__device__ __forceinline__ void split_q(uint8_t* tile, int8_t* exps, int w, int lane) {
+  constexpr int kHalf = 128 * 128;
+#pragma unroll 1
+  for (int it = 0; it < 2; ++it) {
+    const int r = 32 * w + 16 * it + (lane >> 1), h = lane & 1, sw = r & 7;
+    uint4 v[8];
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // (chunk i of the row; the lanes start at different banks)
+      v[i] = *reinterpret_cast<const uint4*>(tile + h * kHalf + r * 128 + ((i ^ sw) << 4));
+      const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[e] << 16)),
+                           fabsf(__uint_as_float(x[e] & 0xffff0000u))));
+    }
+    m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+    const int exp = min(max(134 - (int)(__float_as_uint(m) >> 23), -120), 120);
+    const float up = __uint_as_float((uint32_t)(127 + exp) << 23);
+    __syncwarp();  // both lanes of every row have loaded it
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t hw = 0, lw = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float a = __uint_as_float(x[2 * e + k] << 16) * up;
+          const float b = __uint_as_float(x[2 * e + k] & 0xffff0000u) * up;
+          const uint32_t c = f32x2_to_e4m3x2(a, b);
+          const uint32_t f = e4m3x2_to_f16x2((uint16_t)c);
+          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&f));
+          hw |= c << (16 * k);
+          lw |= (uint32_t)f32x2_to_e4m3x2(a - back.x, b - back.y) << (16 * k);
+        }
+        hi[e] = hw;
+        lo[e] = lw;
+      }
+      // dims 64 h + 8 i ..: 8 bytes of 16-byte chunk 4 h + i / 2
+      uint8_t* to = tile + r * 128 + (((4 * h + (i >> 1)) ^ sw) << 4) + 8 * (i & 1);
+      *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(to + kHalf) = make_uint2(lo[0], lo[1]);
+    }
+    if (h == 0) exps[r] = (int8_t)exp;
+  }
+}
+
+// Warps 12 to 15 split Q and widen V, a quarter of every tile each.  K is used as it is.
 template <int D>
 __device__ void converter(const Ctx& c, const TreeParams& p) {
   using S = Shape<D, true>;
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 1, kv = ((threadIdx.x >> 5) - 12) >> 1;
-  Ring r(p, kv);
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 12;
+  Ring r(p, 1);
   uint32_t nq = 0;
   if (!c.work) return;
   TreeWalk walk(p, blockIdx.x);
   TreeSegment g;
   while (walk.next(p, g)) {
-    const int tiles = kv ? 0 : two_tiles(p, g) ? 2 : 1;
+    const int tiles = two_tiles(p, g) ? 2 : 1;
+#pragma unroll 1
     for (int x = 0; x < tiles; ++x, ++nq) {
       if (!wait_all(c, B_QFULL + (nq & 1), (nq >> 1) & 1)) return;
-      uint4* q = reinterpret_cast<uint4*>(c.sm + (nq & 1) * S::kTileBytes) + w * (S::kTileBytes / 32);
-#pragma unroll 4
-      for (int i = 0; i < S::kTileBytes / 32 / 32; ++i) {
-        uint4 v = q[lane + 32 * i];
-        v.x = bf16x2_to_f16x2(v.x);
-        v.y = bf16x2_to_f16x2(v.y);
-        v.z = bf16x2_to_f16x2(v.z);
-        v.w = bf16x2_to_f16x2(v.w);
-        q[lane + 32 * i] = v;
-      }
+      split_q(c.sm + (nq & 1) * S::kTileBytes,
+              reinterpret_cast<int8_t*>(c.sm + S::kOffExp) + (nq & 3) * 128, w, lane);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(c.bar + B_QCONV + (nq & 1));
     }
     for (int j = g.t0; j < g.t1; ++j) {
-      const int lim = g.n - (g.kv0 + j * kBN);
       if (!wait_all(c, B_FULL + r.st, r.par)) return;
-#pragma unroll 1
-      for (int i = 0; i < 2; ++i)
-        widen_rows(c.sm + S::kOffKV + r.st * S::kTileBytes, 2 * w + i, lane, lim);
+      widen_rows(c.sm + S::kOffKV + r.st * S::kTileBytes, w, lane, g.n - (g.kv0 + j * kBN));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(c.bar + B_CONV + r.st);
@@ -538,7 +608,7 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
   float2* xchg = reinterpret_cast<float2*>(c.sm + S::kOffX);
   int* bads = reinterpret_cast<int*>(c.sm + S::kOffBad);
   uint32_t cnt[2] = {0, 0};  // tiles of both streams so far
-  uint32_t seg = 0;
+  uint32_t seg = 0, nq = 0;  // nq: row tiles of Q before this segment
   int turn = 0;  // the stream whose turn it is
   bool bad = false;
   if (!c.work) return;
@@ -557,7 +627,10 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
     const int R = g.row0 + tile_row0 + (valid ? r : 0);
     const int tok = g.qs + R / m.group, h = g.kvh * m.group + R % m.group;
     const int pos = m.window > 0 ? m.positions[tok] : 0;
-    const float sl = head_scale(m.k_scales, g.kvh, p.scale) * kLog2e;
+    float sl = head_scale(m.k_scales, g.kvh, p.scale) * kLog2e;
+    const int8_t* exps = reinterpret_cast<const int8_t*>(c.sm + S::kOffExp) +
+                         ((nq + (two ? x : 0)) & 3) * 128 + r;
+    nq += two ? 2 : 1;
     const int ctx = g.n - g.nodes;
     // keys [free_lo, ctx) are visible to this row whatever its mask says
     const int free_lo = m.window > 0 ? pos - m.window + 1 : 0;
@@ -579,6 +652,8 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
       }
       if (!bad)
         bad = !wait_all(c, stall ? B_NEVER : B_SFULL + x, stall ? 0u : n & 1);
+      // the row of q was multiplied by 2^exp when it was split (known once its first S is)
+      if (FP8 && i == 0) sl *= __uint_as_float((uint32_t)(127 - *exps) << 23);
       if (!idle && !bad) {
         tc_fence_after();
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -758,7 +833,7 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     flags[1] = 0;
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
-      if ((i >= B_QCONV && i < B_QCONV + 2) || (i >= B_CONV && i < B_CONV + kStages)) n = 2;
+      if ((i >= B_QCONV && i < B_QCONV + 2) || (i >= B_CONV && i < B_CONV + kStages)) n = 4;
       if (i >= B_PFULL && i < B_PFULL + 2) n = 4;
       if (i >= B_OFREE && i < B_OFREE + 2) n = 4;
       mbar_init(bar + i, n);

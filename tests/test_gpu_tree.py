@@ -135,6 +135,15 @@ def test_long_context_many_pieces(pa):
     Batch([7], [3001], 4, 1, 64, src=F32, kv=F32, seed=4).check(pa)
 
 
+@pytest.mark.parametrize("kv", [BF16, E4M3])
+@pytest.mark.parametrize("n", [7, 30, 45])
+def test_many_tiles_to_a_cta(pa, n, kv):
+    """Shares of dozens of key tiles over several items: the copies' ring goes round many times."""
+    ctx = [700, 9000, 1, 4000, 129, 2500, 6000, 900]
+    Batch([n, 1, n, 3, n, 2, n, n], [c * 4 for c in ctx], 16, 4, 128, kv=kv, seed=n).check(
+        pa, k_scale=0.25, v_scale=0.5)
+
+
 def test_many_sequences(pa):
     rng = random.Random(7)
     n = [rng.randint(0, 12) for _ in range(300)]
