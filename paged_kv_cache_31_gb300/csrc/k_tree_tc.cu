@@ -65,8 +65,8 @@ struct Shape {
   static constexpr int kOffBad = kOffX + 2 * 128 * 8;          // [2][4] its warps' failed waits
   static constexpr int kOffBar = kOffBad + 2 * 4 * 4;
   static constexpr int kOffMisc = kOffBar + 40 * 8;
-  // tensor-memory base, flags, stages sent; e4m3: the rows' scale exponents of four Q tiles
-  static constexpr int kOffExp = kOffMisc + 32;
+  // tensor-memory base, flags; e4m3: the rows' scale exponents of four Q tiles
+  static constexpr int kOffExp = kOffMisc + 16;
   static constexpr int kSmem = kOffExp + (FP8 ? 4 * 128 : 0);
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
@@ -76,8 +76,8 @@ enum : int {
   B_QFULL = 0,                     // Q buffer landed
   B_QEMPTY = B_QFULL + 2,          // its last S = Q K^T is done
   B_QCONV = B_QEMPTY + 2,          // e4m3: it has been split
-  B_FULL = B_QCONV + 2,            // K / V stage landed
-  B_EMPTY = B_FULL + kStages,
+  B_FULL = B_QCONV + 2,            // stage landed: K's copies, then V's (B_FULL + kStages + stage)
+  B_EMPTY = B_FULL + 2 * kStages,  // its copy has been used up
   B_CONV = B_EMPTY + kStages,      // e4m3: the stage's V is ready as f16 (V's copies only)
   B_SFULL = B_CONV + kStages,      // per stream: S is ready
   B_PFULL = B_SFULL + 2,           // P is written
@@ -134,7 +134,6 @@ struct Ctx {
   uint64_t* bar;
   volatile int* abort;
   int* status;
-  uint32_t* issued;  // [2] stages that the K and V producers have sent
   uint64_t limit;
   bool work;  // false: an earlier error, nothing is done
 };
@@ -160,27 +159,31 @@ __device__ __forceinline__ bool wait_all(const Ctx& c, int idx, uint32_t parity)
 }
 
 // The K / V ring.  The copies of a CTA's tiles 0, 1, 2, ... are numbered in the order in which
-// they are needed: K0 V0 K1 V1 ... where every item may have two row tiles, and K0 K1 V0 K2 V1 ...
-// (`ahead`) where none has: the streams then work on two tiles at once, and tile t's V is needed
-// after tile t + 1's K.  Copy n uses stage n % kStages.
+// they are needed: K0 V0 K1 V1 ... (K_t 2t, V_t 2t + 1) where an item may have two row tiles, and
+// K0 - K1 V0 K2 V1 K3 ... (K_t 2t, V_t 2t + 3; `ahead`) where none has: the streams then work on two
+// tiles at once, and tile t's V is needed after tile t + 1's K.  Copy n uses stage n % kStages, so
+// K and V take turns in a stage, and an operand's copies come to the same stage every kStages
+// tiles.  A parity tells neighbouring phases of a barrier apart, no more, so each barrier has to
+// be waited for in every phase, or be known to be near:
+//   - "landed" and "ready" barriers are one set per operand, whose consumers wait for each phase;
+//   - a stage's "empty" barrier is completed by K's and V's consumers in turn and waited for by
+//     the other operand's producer.  A producer that waits for copy n + 5's consumption has sent
+//     copy n + 8 of its own, after copy n + 3 was used up, and that was after copy n was: QK of
+//     tile t + 3 follows PV of tile t + 1 (n V_t), and PV of tile t its QK (n K_t).  So the barrier
+//     has passed copy n's phase.
+// Where copy 1 does not exist its "empty" phase is completed at the start.
 __device__ __forceinline__ bool ring_ahead(const TreeParams& p) {
   return p.rows_per_item == p.tile_rows;
 }
 struct Ring {
-  uint32_t st, par;  // stage of this operand's current copy, phase parity of its barriers
-  // the same for barriers that only this operand's copies complete: its stages come round every
-  // kStages copies, as kStages is odd
-  uint32_t turn, par_own;
-  bool first;
+  uint32_t st, par;        // stage of this operand's current copy, parity of n / kStages
+  uint32_t turn, par_own;  // tile t % kStages, parity of t / kStages: its visits to the stage
   __device__ __forceinline__ Ring(const TreeParams& p, int kv) {
-    const bool ahead = ring_ahead(p);
-    first = ahead && kv == 0;
-    st = kv ? (ahead ? 2 : 1) : 0;
+    st = kv ? (ring_ahead(p) ? 3 : 1) : 0;
     par = turn = par_own = 0;
   }
   __device__ __forceinline__ void next() {  // the next tile's copy of the same operand
-    st += first ? 1 : 2;
-    first = false;
+    st += 2;
     if (st >= kStages) {
       st -= kStages;
       par ^= 1;
@@ -191,7 +194,7 @@ struct Ring {
     }
   }
 };
-static_assert(kStages % 2 == 1, "an operand's copies visit every stage");
+static_assert(kStages == 5, "the reasoning above");
 
 // Both streams take all key tiles of a segment with two row tiles.  With one row tile the streams
 // alternate, over segments too: the stream that does not take a segment's last tile begins the
@@ -210,6 +213,7 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
                          const CUtensorMap* tq, int kv) {
   using S = Shape<D, FP8>;
   const int lane = threadIdx.x & 31;
+  uint64_t* full = c.bar + B_FULL + kv * kStages;
   Ring r(p, kv);
   uint32_t issued = 0, nq = 0;  // this warp's stages; row tiles of Q (tile n uses buffer n % 2)
   bool ok = c.work;
@@ -243,7 +247,7 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
       if (j + 1 < g.t1) next = lane < 8 && nb < blocks ? row[nb] : -1;
       if (lane == 0) {
         ok = wait_bar(c, B_EMPTY + r.st, r.par ^ 1);
-        if (ok) mbar_arrive_expect_tx(c.bar + B_FULL + r.st, S::kLoadBytes);
+        if (ok) mbar_arrive_expect_tx(full + r.st, S::kLoadBytes);
       }
       ok = __shfl_sync(kFull, (int)ok, 0);
       if (!ok) break;
@@ -251,35 +255,25 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
         uint8_t* dst = c.sm + S::kOffKV + r.st * S::kTileBytes;
         if constexpr (FP8)  // V's codes go where its second dim half's rows will be
           tma_load_3d(dst + (kv ? S::kHalfBytes : 0) + lane * 2048, tkv, 0, g.kvh,
-                      id >= 0 ? id * 16 : -16, c.bar + B_FULL + r.st);
+                      id >= 0 ? id * 16 : -16, full + r.st);
         else
           tma_load_5d(dst + lane * (S::kTileBytes / 8), tkv, 0, 0, 0, id >= 0 ? id * 2 : -2, g.kvh,
-                      c.bar + B_FULL + r.st);
+                      full + r.st);
       }
       ++issued;
       r.next();
     }
   }
-  if (lane == 0) c.issued[kv] = issued;
-  // Q's copies still in flight (after an abort; otherwise all have been consumed)
-  if (lane == 0)
+  // the copies still in flight (after an abort; otherwise all have been consumed): the last ones
+  // are the last of their barriers
+  if (lane == 0) {
+    Ring d(p, kv);
+    for (uint32_t k = 0; k < issued; ++k, d.next())
+      if (k + kStages >= issued) mbar_wait(full + d.st, d.par_own, c.limit);
     for (uint32_t k = nq > 2 ? nq - 2 : 0; k < nq; ++k)
       mbar_wait(c.bar + B_QFULL + (k & 1), (k >> 1) & 1u, c.limit);
+  }
   __syncwarp();
-}
-
-// The same for K and V, by one thread once both producers are done: each stage's last copy (an
-// earlier one's phase may have been followed by two others, whose parity it shares).
-__device__ void drain_kv(const Ctx& c, bool ahead) {
-  const uint32_t nk = c.issued[0], nv = c.issued[1];
-  auto sent = [&](uint32_t n) {
-    if (ahead) return n == 0 ? nk > 0 : n & 1 ? (n + 1) / 2 < nk : (n - 2) / 2 < nv;
-    return n & 1 ? n / 2 < nv : n / 2 < nk;
-  };
-  const uint32_t end = 2 * max(nk, nv) + 3;
-  for (uint32_t n = end > 4 * kStages ? end - 4 * kStages : 0; n < end; ++n)
-    if (sent(n) && !sent(n + kStages))
-      mbar_wait(c.bar + B_FULL + n % kStages, (n / kStages) & 1u, c.limit);
 }
 
 template <int D, bool FP8>
@@ -298,7 +292,7 @@ __device__ void s_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   while (walk.next(p, g)) {
     const bool two = two_tiles(p, g);
     for (int j = g.t0; j < g.t1; ++j) {
-      if (!wait_all(c, B_FULL + r.st, r.par)) return;
+      if (!wait_all(c, B_FULL + r.st, r.par_own)) return;
       const uint32_t kb = sm + S::kOffKV + r.st * S::kTileBytes;
 #pragma unroll 1
       for (int y = 0; y < (two ? 2 : 1); ++y) {
@@ -352,7 +346,7 @@ __device__ void pv_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   for (; walk.next(p, g); ++seg) {
     const bool two = two_tiles(p, g);
     for (int j = g.t0; j < g.t1; ++j) {
-      if (!wait_all(c, (FP8 ? B_CONV : B_FULL) + r.st, FP8 ? r.par_own : r.par)) return;
+      if (!wait_all(c, (FP8 ? B_CONV : B_FULL + kStages) + r.st, r.par_own)) return;
       uint8_t* v = c.sm + S::kOffKV + r.st * S::kTileBytes;
       if constexpr (!FP8) {  // (the converters do it over e4m3 pools)
         // rows of the last block past the sequence's end: zeros (whole blocks past it are)
@@ -403,30 +397,33 @@ __device__ void pv_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
 }
 
 // Widen a staged tile of 128 x 128 codes to f16, in place: the codes lie in the second dim half's
-// 16 KB, in rows of 128 bytes with the 128-byte swizzle.  A warp takes rows 32 w .. 32 w + 31 and has
-// loaded all their codes before it stores over them.  Rows at or past `lim` become zeros.
+// 16 KB, in rows of 128 bytes with the 128-byte swizzle.  A warp takes rows 32 w .. 32 w + 31, 16 at a
+// time, and has loaded their codes before it stores over them.  Rows at or past `lim` become zeros.
 __device__ __forceinline__ void widen_rows(uint8_t* tile, int w, int lane, int lim) {
   constexpr int kHalf = 128 * 128;
-  uint4 src[8];
+#pragma unroll 1
+  for (int r0 = 32 * w; r0 < 32 * w + 32; r0 += 16) {
+    uint4 src[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    src[i] = *reinterpret_cast<const uint4*>(tile + kHalf + w * 4096 + (lane + 32 * i) * 16);
-  __syncwarp();
+    for (int i = 0; i < 4; ++i)
+      src[i] = *reinterpret_cast<const uint4*>(tile + kHalf + r0 * 128 + (lane + 32 * i) * 16);
+    __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int ch = lane + 32 * i, rr = ch >> 3;       // row of the warp's 32
-    const int L = (ch & 7) ^ (rr & 7);                // dims 16 L .. 16 L + 15
-    const int h = L >> 2, c0 = 2 * (L & 3);           // dim half, first output chunk
-    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-    if (w * 32 + rr < lim) {
-      widen4(src[i].x, lo.x, lo.y);
-      widen4(src[i].y, lo.z, lo.w);
-      widen4(src[i].z, hi.x, hi.y);
-      widen4(src[i].w, hi.z, hi.w);
+    for (int i = 0; i < 4; ++i) {
+      const int ch = lane + 32 * i, r = r0 + (ch >> 3), sw = r & 7;
+      const int L = (ch & 7) ^ sw;             // dims 16 L .. 16 L + 15
+      const int h = L >> 2, c0 = 2 * (L & 3);  // dim half, first output chunk
+      uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+      if (r < lim) {
+        widen4(src[i].x, lo.x, lo.y);
+        widen4(src[i].y, lo.z, lo.w);
+        widen4(src[i].z, hi.x, hi.y);
+        widen4(src[i].w, hi.z, hi.w);
+      }
+      uint8_t* row = tile + h * kHalf + r * 128;
+      *reinterpret_cast<uint4*>(row + ((c0 ^ sw) << 4)) = lo;
+      *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ sw) << 4)) = hi;
     }
-    uint8_t* row = tile + h * kHalf + w * 4096 + rr * 128;
-    *reinterpret_cast<uint4*>(row + ((c0 ^ (rr & 7)) << 4)) = lo;
-    *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (rr & 7)) << 4)) = hi;
   }
 }
 
@@ -506,7 +503,7 @@ __device__ void converter(const Ctx& c, const TreeParams& p) {
       if (lane == 0) mbar_arrive(c.bar + B_QCONV + (nq & 1));
     }
     for (int j = g.t0; j < g.t1; ++j) {
-      if (!wait_all(c, B_FULL + r.st, r.par)) return;
+      if (!wait_all(c, B_FULL + kStages + r.st, r.par_own)) return;
       widen_rows(c.sm + S::kOffKV + r.st * S::kTileBytes, w, lane, g.n - (g.kv0 + j * kBN));
       fence_proxy_async_smem();
       __syncwarp();
@@ -838,6 +835,7 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
       if (i >= B_OFREE && i < B_OFREE + 2) n = 4;
       mbar_init(bar + i, n);
     }
+    if (ring_ahead(p)) mbar_arrive(bar + B_EMPTY + 1);
     prefetch_tmap(&tq);
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
@@ -865,19 +863,16 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
   const Ctx c{sm, bar, reinterpret_cast<volatile int*>(flags + 1), p.status,
-              reinterpret_cast<uint32_t*>(sm + S::kOffMisc + 12), wait_limit, flags[0] == 0};
+              wait_limit, flags[0] == 0};
 
-  // register shares: bf16 4 x 72 + 8 x 216, e4m3 4 x 64 + 8 x 184 + 4 x 80 warps' worth
-  static_assert(4 * 72 + 8 * 216 <= 12 * 168 && 4 * 64 + 8 * 184 + 4 * 80 <= 16 * 128, "registers");
+  // register shares of the warps: bf16 4 x 72 + 8 x 216, e4m3 4 x 72 + 8 x 176 + 4 x 88
+  static_assert(4 * 72 + 8 * 216 <= 12 * 168 && 4 * 72 + 8 * 176 + 4 * 88 <= 16 * 128, "registers");
   if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
     if constexpr (FP8) converter<D>(c, p);
     __syncthreads();
   } else if (warp < 4) {
-    if constexpr (FP8)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
     if (warp == 0) {
       producer<D, FP8>(c, p, &tk, &tq, 0);
     } else if (warp == 3) {
@@ -895,7 +890,6 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0) drain_kv(c, ring_ahead(p));
     if (warp == 1) {
       tc_fence_after();
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
@@ -904,7 +898,7 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     }
   } else {
     if constexpr (FP8)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;" ::: "memory");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 176;" ::: "memory");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
     softmax_role<D, FP8>(c, p, tmem, stall);
