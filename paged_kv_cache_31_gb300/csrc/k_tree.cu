@@ -50,6 +50,10 @@ __device__ __forceinline__ int64_t block_sum_scan(int64_t v, int64_t* s_warp, in
   return before + x - v;
 }
 
+__device__ __forceinline__ int64_t item_weight(const TreeParams& p, int tiles, int rows) {
+  return (int64_t)tree_weight(p, rows) * tiles + kTreeItemWeight;
+}
+
 // Block 0 plans; blocks 1 .. check the table entries of the sequences, one warp per 256 entries.
 // Everything is read after the wait for the kernels ahead, and nothing is written by the
 // attention kernel before this whole launch is done, so an error leaves the outputs untouched.
@@ -135,15 +139,14 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(const TreeParams p) 
       }
       kv0 -= kv0 % m.block_size;
       const int tiles = (n - kv0 + p.key_tile - 1) / p.key_tile;
-      p.seqs[s] = make_int4(qs, nodes, n, kv0);
-      const int64_t rows = (int64_t)nodes * m.group;
-      const int64_t full = rows / p.rows_per_item;
-      const int rest = (int)(rows % p.rows_per_item);
-      weight = ((full * tree_weight(p, p.rows_per_item) + (rest ? tree_weight(p, rest) : 0)) * tiles +
-                (full + (rest > 0)) * kTreeItemWeight) *
-               m.num_kv_heads;
+      const int rows = nodes * m.group, items = (rows + p.rows_per_item - 1) / p.rows_per_item;
+      p.seqs[2 * s] = make_int4(qs, nodes, n, kv0);
+      p.seqs[2 * s + 1] = make_int4(items, tiles, rows, 0);
+      weight = item_weight(p, tiles, p.rows_per_item) * (items - 1) +
+               item_weight(p, tiles, rows - (items - 1) * p.rows_per_item);
+      weight *= m.num_kv_heads;
     } else if (s < m.num_seqs) {
-      p.seqs[s] = make_int4(0, 0, 0, 0);
+      p.seqs[2 * s] = p.seqs[2 * s + 1] = make_int4(0, 0, 0, 0);
     }
     int64_t total;
     const int64_t at = base + block_sum_scan(weight, s_warp, &total);
@@ -174,18 +177,16 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(const TreeParams p) 
         if ((shared ? s_cum[mid] : p.cum[mid]) <= x) lo = mid; else hi = mid;
       }
       const int64_t rem = x - (shared ? s_cum[lo] : p.cum[lo]);
-      const int4 q = p.seqs[lo];
-      const TreeGeometry g(p, q);
-      const int64_t per_head =
-          g.weight_before(g.items) * g.tiles + (int64_t)g.items * kTreeItemWeight;
+      const int4 w = p.seqs[2 * lo + 1];
+      const int last_rows = w.z - (w.x - 1) * p.rows_per_item;
+      const int64_t full = item_weight(p, w.y, p.rows_per_item);
+      const int64_t per_head = full * (w.x - 1) + item_weight(p, w.y, last_rows);
       const int kvh = (int)(rem / per_head);
       const int64_t r = rem % per_head;
-      const int64_t item_w =
-          (int64_t)tree_weight(p, p.rows_per_item) * g.tiles + kTreeItemWeight;
-      const int it = (int)min(r / item_w, (int64_t)g.items - 1);
-      const int64_t in = max(r - it * item_w - kTreeItemWeight, (int64_t)0);
-      const int w = tree_weight(p, g.rows_of(p, it));
-      st = make_int4(lo, kvh * g.items + it, min((int)(in / w), g.tiles - 1), 0);
+      const int it = (int)min(r / full, (int64_t)w.x - 1);
+      const int64_t in = max(r - it * full - kTreeItemWeight, (int64_t)0);
+      const int tw = tree_weight(p, it == w.x - 1 ? last_rows : p.rows_per_item);
+      st = make_int4(lo, kvh, it, (int)min(in / tw, (int64_t)w.y - 1));
     }
     p.starts[c] = st;
   }
@@ -366,14 +367,16 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
 
 // ---- merge ------------------------------------------------------------------------------------
 // Block (b, y): the item that the boundary between CTA b and b + 1 cuts, when that is the item's
-// first cut; a warp per row.  out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the
-// item's pieces in key order: CTA b's piece (its first segment when the item begins its share,
+// first cut; a warp for R rows.  out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over
+// the item's pieces in key order: CTA b's piece (its first segment when the item begins its share,
 // else its last), then those of the CTAs behind it whose shares begin inside the item.  Bound by
-// the latency of its loads, so 32 pieces' states are read at once, a lane each, and four pieces'
-// outputs at a time.
-// VEC: rows of whole float4s (head sizes that are multiples of 4)
-template <typename TQ, bool VEC>
+// the latency of its loads: 32 pieces' states are read at once, a lane each, and the outputs of
+// two pieces for all of the warp's rows.  A warp takes one row, or as many more as keep the whole
+// grid resident at once (151 cuts of 128 rows: 12.5 us with one row, in two waves of CTAs).
+// VEC: rows of whole float4s (head sizes that are multiples of 4); DK: 128-dim parts of a row
+template <typename TQ, bool VEC, int DK, int R>
 __global__ void __launch_bounds__(256) k_tree_merge(const TreeParams p) {
+  constexpr int E = 4 * DK;  // a lane's values of a row
   const VarlenMeta& m = p.m;
   pdl_wait();
   pdl_launch_dependents();
@@ -381,86 +384,125 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeParams p) {
   const int skip = status_set(p.status);
   const int4 cut = p.starts[b + 1], from = p.starts[b];
   if (__syncthreads_or(skip)) return;  // (one answer for the whole CTA)
-  if (cut.x >= m.num_seqs || cut.z == 0) return;
-  const bool same = from.x == cut.x && from.y == cut.y;
-  if (same && from.z > 0) return;  // a later cut of the item
-  const int4 q = p.seqs[cut.x];
-  const TreeGeometry g(p, q);
-  const int kvh = cut.y / g.items, it = cut.y % g.items;
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (row >= g.rows_of(p, it)) return;
+  if (cut.x >= m.num_seqs || cut.w == 0) return;
+  const bool same = from.x == cut.x && from.y == cut.y && from.z == cut.z;
+  if (same && from.w > 0) return;  // a later cut of the item
+  const int4 q = p.seqs[2 * cut.x];
+  const int kvh = cut.y, row0 = cut.z * p.rows_per_item;
+  const int rows = min(p.rows_per_item, q.y * m.group - row0);
+  const int row = (blockIdx.y * 8 + (threadIdx.x >> 5)) * R;
+  if (row >= rows) return;
   const int D = m.head_dim, G = m.group;
-  float M = -INFINITY, L = 0.f;
-  float acc[8];
+  float M[R], L[R], acc[R][E];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  for (int k = 0; k < R; ++k) {
+    M[k] = -INFINITY;
+    L[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[k][i] = 0.f;
+  }
   for (int c0 = b;; c0 += 32) {  // pieces of CTAs c0 .. c0 + 31, one per lane
     const int c = c0 + lane;
     bool in = c == b;
     int slot = same ? 2 * b : 2 * b + 1;
     if (c > b && c < p.grid) {
       const int4 s0 = p.starts[c], s1 = p.starts[c + 1];
-      in = s0.x == cut.x && s0.y == cut.y;
+      in = s0.x == cut.x && s0.y == cut.y && s0.z == cut.z;
       // (a CTA whose share is empty left nothing)
-      slot = in && (s1.x != s0.x || s1.y != s0.y || s1.z != s0.z) ? 2 * c : -1;
+      slot = in && (s1.x != s0.x || s1.y != s0.y || s1.z != s0.z || s1.w != s0.w) ? 2 * c : -1;
     }
-    const unsigned run = __ballot_sync(kFull, in);  // contiguous from lane 0
-    const int64_t at = in && slot >= 0 ? (int64_t)slot * p.rows_per_item + row : -1;
-    const float2 ml = at >= 0 ? p.part_ml[at] : make_float2(-INFINITY, 0.f);
-    float mx = ml.x;
+    const int n = __popc(__ballot_sync(kFull, in));  // contiguous from lane 0
+    const bool have = in && slot >= 0;
+    float w[R];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-    const float mn = fmaxf(M, mx), base = mn == -INFINITY ? 0.f : mn;
-    const float a = exp2f(M - base), w = at >= 0 ? exp2f(ml.x - base) : 0.f;
-    float l = w * ml.y;
+    for (int k = 0; k < R; ++k) {
+      const float2 ml = have && row + k < rows
+                            ? p.part_ml[(int64_t)slot * p.rows_per_item + row + k]
+                            : make_float2(-INFINITY, 0.f);
+      float mx = ml.x;  // (over the lanes of the n pieces: their group of a power of two)
+      for (int o = 1; o < n; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+      mx = __shfl_sync(kFull, mx, 0);
+      const float mn = fmaxf(M[k], mx), base = mn == -INFINITY ? 0.f : mn;
+      const float a = exp2f(M[k] - base);
+      w[k] = have ? exp2f(ml.x - base) : 0.f;
+      float l = w[k] * ml.y;
+      for (int o = 1; o < n; o <<= 1) l += __shfl_xor_sync(kFull, l, o);
+      l = __shfl_sync(kFull, l, 0);
+      M[k] = mn;
+      L[k] = L[k] * a + l;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
-    M = mn;
-    L = L * a + l;
+      for (int i = 0; i < E; ++i) acc[k][i] *= a;
+    }
+    for (int j0 = 0; j0 < n; j0 += 2) {
+      float x[2][R][E];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] *= a;
-    const int n = __popc(run);
-    for (int j0 = 0; j0 < n; j0 += 4) {
-      float x[4][8], wj[4];
+      for (int u = 0; u < 2; ++u) {
+        const int sj = __shfl_sync(kFull, have ? slot : -1, min(j0 + u, 31));
+        const bool ok = j0 + u < n && sj >= 0;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int j = min(j0 + u, 31);
-        wj[u] = j0 + u < n ? __shfl_sync(kFull, w, j) : 0.f;
-        const int64_t aj = __shfl_sync(kFull, at, j);
-        const bool have = j0 + u < n && aj >= 0;
-        const float* src = p.part_o + aj * D;
-        if constexpr (VEC) {
+        for (int k = 0; k < R; ++k) {
+          const float* src = p.part_o + ((int64_t)sj * p.rows_per_item + row + k) * D;
+          const bool get = ok && row + k < rows;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int d = 128 * k + 4 * lane;
-            const float4 v = have && d < D ? *reinterpret_cast<const float4*>(src + d)
-                                           : make_float4(0.f, 0.f, 0.f, 0.f);
-            x[u][4 * k] = v.x;
-            x[u][4 * k + 1] = v.y;
-            x[u][4 * k + 2] = v.z;
-            x[u][4 * k + 3] = v.w;
+          for (int i = 0; i < DK; ++i) {
+            if constexpr (VEC) {
+              const int d = 128 * i + 4 * lane;
+              const float4 v = get && d < D ? *reinterpret_cast<const float4*>(src + d)
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+              x[u][k][4 * i] = v.x;
+              x[u][k][4 * i + 1] = v.y;
+              x[u][k][4 * i + 2] = v.z;
+              x[u][k][4 * i + 3] = v.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int d = 128 * i + 32 * e + lane;
+                x[u][k][4 * i + e] = get && d < D ? src[d] : 0.f;
+              }
+            }
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[u][i] = have && lane + 32 * i < D ? src[lane + 32 * i] : 0.f;
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += wj[u] * x[u][i];
+        for (int k = 0; k < R; ++k) {
+          const float wj = __shfl_sync(kFull, w[k], min(j0 + u, 31));
+#pragma unroll
+          for (int i = 0; i < E; ++i) acc[k][i] += (j0 + u < n ? wj : 0.f) * x[u][k][i];
+        }
     }
     if (n < 32) break;
   }
-  const int r = it * p.rows_per_item + row;
-  const int tok = q.x + r / G, h = kvh * G + r % G;
-  const float inv = tree_finish(p, kvh, h, tok, M, L, lane == 0);
-  TQ* out = static_cast<TQ*>(p.out) + ((int64_t)tok * m.num_heads + h) * D;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int d = VEC ? 128 * (i >> 2) + 4 * lane + (i & 3) : lane + 32 * i;
-    if (d < D) out[d] = from_f32<TQ>(acc[i] * inv);
+  for (int k = 0; k < R; ++k) {
+    if (row + k >= rows) break;
+    const int r = row0 + row + k;
+    const int tok = q.x + r / G, h = kvh * G + r % G;
+    const float inv = tree_finish(p, kvh, h, tok, M[k], L[k], lane == 0);
+    TQ* out = static_cast<TQ*>(p.out) + ((int64_t)tok * m.num_heads + h) * D;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int d = VEC ? 128 * (i >> 2) + 4 * lane + (i & 3) : 128 * (i >> 2) + 32 * (i & 3) + lane;
+      if (d < D) out[d] = from_f32<TQ>(acc[k][i] * inv);
+    }
   }
+}
+
+template <typename TQ, bool VEC, int R>
+cudaError_t merge_rows(const TreeParams& p, int64_t rows, cudaStream_t stream) {
+  const dim3 grid((unsigned)(p.grid - 1), (unsigned)((rows + 8 * R - 1) / (8 * R)));
+  if (p.m.head_dim <= 128)
+    return launch_pdl(k_tree_merge<TQ, VEC, 1, R>, grid, dim3(256), 0, stream, p);
+  return launch_pdl(k_tree_merge<TQ, VEC, 2, R>, grid, dim3(256), 0, stream, p);
+}
+template <typename TQ, bool VEC>
+cudaError_t merge_as(const TreeParams& p, cudaStream_t stream) {
+  const int64_t rows = std::min<int64_t>(p.rows_per_item, p.m.num_tokens * p.m.group);
+  const int64_t warps = (p.grid - 1) * ((rows + 7) / 8 * 8), resident = 48 * (int64_t)num_sms();
+  if (warps <= resident) return merge_rows<TQ, VEC, 1>(p, rows, stream);
+  if (warps <= 2 * resident) return merge_rows<TQ, VEC, 2>(p, rows, stream);
+  return merge_rows<TQ, VEC, 4>(p, rows, stream);
 }
 
 template <typename TQ, typename TKV, int DP>
@@ -493,7 +535,7 @@ TreeLayout tree_layout(int32_t num_seqs, int64_t num_tokens, int32_t group, int3
   const int64_t items = (num_tokens * group / rows_per_item + num_seqs) * num_kv_heads;
   const int64_t tiles = max_keys / key_tile + 2;
   L.grid = (int32_t)std::max<int64_t>(1, std::min<int64_t>(max_grid, std::min<int64_t>(items, max_grid) * tiles));
-  L.cum_off = up(16 * (int64_t)num_seqs);
+  L.cum_off = up(32 * (int64_t)num_seqs);
   L.starts_off = L.cum_off + up(8 * ((int64_t)num_seqs + 1));
   L.ml_off = L.starts_off + up(16 * ((int64_t)L.grid + 1));
   L.o_off = L.ml_off + up(2 * (int64_t)L.grid * rows_per_item * 8);
@@ -521,13 +563,9 @@ cudaError_t launch_tree_generic(const TreeParams& p, pa_dtype kv, cudaStream_t s
 
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t stream) {
   if (p.grid < 2) return cudaSuccess;
-  const int64_t rows = std::min<int64_t>(p.rows_per_item, p.m.num_tokens * p.m.group);
-  const dim3 grid((unsigned)(p.grid - 1), (unsigned)((rows + 7) / 8)), block(256);
   if (p.m.head_dim % 4 == 0)
-    return p.q_bf16 ? launch_pdl(k_tree_merge<__nv_bfloat16, true>, grid, block, 0, stream, p)
-                    : launch_pdl(k_tree_merge<float, true>, grid, block, 0, stream, p);
-  return p.q_bf16 ? launch_pdl(k_tree_merge<__nv_bfloat16, false>, grid, block, 0, stream, p)
-                  : launch_pdl(k_tree_merge<float, false>, grid, block, 0, stream, p);
+    return p.q_bf16 ? merge_as<__nv_bfloat16, true>(p, stream) : merge_as<float, true>(p, stream);
+  return p.q_bf16 ? merge_as<__nv_bfloat16, false>(p, stream) : merge_as<float, false>(p, stream);
 }
 
 }  // namespace pa

@@ -8,81 +8,57 @@
 
 namespace pa {
 
-// Items of one kv head of a sequence (plan record q: first token, nodes, seq_len, first key).
-struct TreeGeometry {
-  int rows, items, tiles;
-  int full_w, rest_w;
-  __device__ __forceinline__ TreeGeometry(const TreeParams& p, int4 q) {
-    rows = q.y * p.m.group;
-    items = (rows + p.rows_per_item - 1) / p.rows_per_item;
-    tiles = (q.z - q.w + p.key_tile - 1) / p.key_tile;
-    full_w = tree_weight(p, p.rows_per_item);
-    rest_w = items ? tree_weight(p, rows - (items - 1) * p.rows_per_item) : 0;
-  }
-  __device__ __forceinline__ int rows_of(const TreeParams& p, int item) const {
-    return min(p.rows_per_item, rows - item * p.rows_per_item);
-  }
-  // weight of one key tile of the first `i` items (i == items: of all of them)
-  __device__ __forceinline__ int64_t weight_before(int i) const {
-    return i < items ? (int64_t)i * full_w : (int64_t)(items - 1) * full_w + rest_w;
-  }
-};
-
-// One CTA's share of one item: key tiles [t0, t1) of `tiles`.
+// One CTA's share of one item: key tiles [t0, t1).
 struct TreeSegment {
   int s, kvh, row0, rows;  // rows row0 .. of the sequence's (node, head of the group) rows
+  int item;                // row0 / rows_per_item
   int qs, nodes, n, kv0;
-  int t0, t1, tiles;
+  int t0, t1;
   int slot;  // partial state it writes, or -1: the item is whole and goes to the output
 };
 
+// The segments of a CTA's share, in order.  (No division: this code is part of every role.)
 struct TreeWalk {
-  int s, item, tile;        // where the next segment begins
-  int es, eitem, etile;     // where the share ends
-  int first_slot;
-  bool first;
+  int4 at, end;  // (sequence, kv head, item, key tile) where the next segment begins, the share ends
+  int slot;      // of a partial segment
   __device__ __forceinline__ TreeWalk(const TreeParams& p, int cta) {
-    const int4 a = p.starts[cta], e = p.starts[cta + 1];
-    s = a.x;
-    item = a.y;
-    tile = a.z;
-    es = e.x;
-    eitem = e.y;
-    etile = e.z;
-    first_slot = 2 * cta;
-    first = true;
+    at = p.starts[cta];
+    end = p.starts[cta + 1];
+    slot = 2 * cta;
   }
   __device__ __forceinline__ bool next(const TreeParams& p, TreeSegment& g) {
-    if (s >= p.m.num_seqs) return false;
-    int4 q = p.seqs[s];
+    if (at.x >= p.m.num_seqs) return false;
+    int4 q = p.seqs[2 * at.x];
     while (q.y == 0) {  // sequences without nodes
-      if (++s >= p.m.num_seqs) return false;
-      q = p.seqs[s];
+      if (++at.x >= p.m.num_seqs) return false;
+      q = p.seqs[2 * at.x];
     }
-    const TreeGeometry ge(p, q);
-    const bool last = s == es && item == eitem;
-    const int t1 = last ? etile : ge.tiles;
-    if (s > es || (s == es && item > eitem) || t1 <= tile) return false;
-    g.s = s;
-    g.kvh = item / ge.items;
-    const int it = item % ge.items;
-    g.row0 = it * p.rows_per_item;
-    g.rows = ge.rows_of(p, it);
+    const int4 w = p.seqs[2 * at.x + 1];  // (items, key tiles, rows)
+    const bool last = at.x == end.x && at.y == end.y && at.z == end.z;
+    const int t1 = last ? end.w : w.y;
+    if (t1 <= at.w) return false;
+    g.s = at.x;
+    g.kvh = at.y;
+    g.item = at.z;
+    g.row0 = at.z * p.rows_per_item;
+    g.rows = min(p.rows_per_item, w.z - g.row0);
     g.qs = q.x;
     g.nodes = q.y;
     g.n = q.z;
     g.kv0 = q.w;
-    g.t0 = tile;
+    g.t0 = at.w;
     g.t1 = t1;
-    g.tiles = ge.tiles;
-    g.slot = tile > 0 || t1 < ge.tiles ? first_slot + (first ? 0 : 1) : -1;
-    first = false;
-    tile = 0;
+    g.slot = at.w > 0 || t1 < w.y ? slot : -1;
+    slot |= 1;  // a share's first segment has the even slot
+    at.w = 0;
     if (last) {
-      s = p.m.num_seqs;  // the share is used up
-    } else if (++item == ge.items * p.m.num_kv_heads) {
-      item = 0;
-      ++s;
+      at.x = p.m.num_seqs;  // the share is used up
+    } else if (++at.z == w.x) {
+      at.z = 0;
+      if (++at.y == p.m.num_kv_heads) {
+        at.y = 0;
+        ++at.x;
+      }
     }
     return true;
   }

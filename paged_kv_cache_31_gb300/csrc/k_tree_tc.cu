@@ -231,7 +231,8 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
         if (ok) {
           uint64_t* bar = c.bar + B_QFULL + (nq & 1);
           mbar_arrive_expect_tx(bar, (uint32_t)p.tile_rows * 128 * S::kHalves);
-          const int tok = g.qs + (g.row0 + x * p.tile_rows) / p.m.group;
+          // (an item's rows are those of whole row tiles)
+          const int tok = g.qs + (ring_ahead(p) ? g.item : 2 * g.item + x) * p.tile_tokens;
 #pragma unroll
           for (int h = 0; h < S::kHalves; ++h)
             tma_load_3d(c.sm + (nq & 1) * S::kTileBytes + h * S::kHalfBytes, tq, 64 * h,
@@ -873,10 +874,8 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     __syncthreads();
   } else if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
-    if (warp == 0) {
-      producer<D, FP8>(c, p, &tk, &tq, 0);
-    } else if (warp == 3) {
-      producer<D, FP8>(c, p, &tv, &tq, 1);
+    if (warp == 0 || warp == 3) {
+      producer<D, FP8>(c, p, warp ? &tv : &tk, &tq, warp ? 1 : 0);
     } else {
       if (warp == 1)
         s_issuer<D, FP8>(c, p, tmem);

@@ -233,6 +233,7 @@ pa_status pa_tree_attention(const void* q, const void* k_blocks, const void* v_b
   TreeLayout L;
   if (tc) {
     p.tile_rows = tree_tile_rows(m.group);
+    p.tile_tokens = p.tile_rows / m.group;
     const int64_t most = std::min<int64_t>(32 * (int64_t)mask_words, num_tokens) * m.group;
     p.rows_per_item = most > p.tile_rows ? 2 * p.tile_rows : p.tile_rows;
     p.key_tile = kTreeTcKeys;
@@ -255,7 +256,7 @@ pa_status pa_tree_attention(const void* q, const void* k_blocks, const void* v_b
   CUtensorMap tq, tk, tv;
   if (tc) {
     const bool ok =
-        query_map(&tq, q, num_tokens, num_heads, head_dim, m.group, p.tile_rows / m.group) &&
+        query_map(&tq, q, num_tokens, num_heads, head_dim, m.group, p.tile_tokens) &&
         (fp8 ? pool_map_fp8(&tk, k_blocks, num_blocks, 16, num_kv_heads, head_dim) &&
                    pool_map_fp8(&tv, v_blocks, num_blocks, 16, num_kv_heads, head_dim)
              : pool_map_rows(&tk, k_blocks, num_blocks, num_kv_heads, head_dim) &&

@@ -602,10 +602,12 @@ struct TreeParams {
   float scale;  // softmax scale, k_scale included
   int32_t rows_per_item, key_tile;
   int32_t tile_rows;  // rows of one row tile (whole nodes); an item is one tile or two
+  int32_t tile_tokens;  // tile_rows / group
   int32_t grid;     // CTAs the work is cut for
-  int4* seqs;       // [num_seqs] (first token, nodes, seq_len, first key); nodes 0: no work
+  int4* seqs;       // [num_seqs, 2] (first token, nodes, seq_len, first key; nodes 0: no work),
+                    // (items of a kv head, key tiles, rows, 0)
   int64_t* cum;     // [num_seqs + 1] weight before the sequence
-  int4* starts;     // [grid + 1] (sequence, item, key tile, 0) where each CTA's range begins
+  int4* starts;     // [grid + 1] (sequence, kv head, item, key tile) where each CTA's share begins
   float2* part_ml;  // [2 * grid, rows_per_item] running max (log2 units) and exp-sum
   float* part_o;    // [2 * grid, rows_per_item, head_dim] unnormalised outputs
   int* status;
