@@ -505,8 +505,9 @@ pa_status pa_gather_kv(const void* k_blocks, const void* v_blocks, void* k_out, 
  * A drafted step of a sequence: a tree of candidate tokens is cached behind its context
  * (pa_rope_and_cache), the tree attends to the context and to each node's ancestors
  * (pa_tree_attention), and the accepted path's rows are moved together (pa_tree_commit).  The
- * pages of forked, growing and ended sequences are kept by pa_fork_sequences, pa_grow_sequences
- * and pa_free_sequences, whose block copies pa_copy_blocks makes in every layer's pools.
+ * pages of forked, growing, shortened and ended sequences are kept by pa_fork_sequences,
+ * pa_grow_sequences, pa_trim_sequences and pa_free_sequences; pa_copy_blocks makes the copies
+ * that forks ask for, in every layer's pools.
  */
 
 /* Long-context scalings of the rotary frequencies (pa_rope_frequencies). */
@@ -679,6 +680,17 @@ pa_status pa_fork_sequences(int32_t* block_tables, int32_t* seq_lens, const int3
 /* pa_grow_sequences -- lengthen row sequences[i] to new_lens[i] >= its length, taking the blocks
  * this needs (in list order, ascending position) and writing them behind the row's blocks. */
 pa_status pa_grow_sequences(int32_t* block_tables, int32_t* seq_lens, const int32_t* sequences,
+                            const int32_t* new_lens, int32_t num_sequences, int32_t num_rows,
+                            int32_t max_blocks_per_seq, int32_t block_size, int32_t* ref_counts,
+                            int32_t* free_list, int32_t* free_count, int64_t num_blocks,
+                            cudaStream_t stream);
+
+/* pa_trim_sequences -- shorten row sequences[i] to new_lens[i], 0 <= new_lens[i] <= its length
+ * (after a drafted step: to the context and the accepted tokens).  The blocks behind
+ * ceil(new_lens[i] / block_size) are let go as in pa_free_sequences.  A last block that stays
+ * partly filled is not replaced: a row cut inside a block that other rows hold, too, shares that
+ * block with them, so fork the row before anything is written behind its end. */
+pa_status pa_trim_sequences(int32_t* block_tables, int32_t* seq_lens, const int32_t* sequences,
                             const int32_t* new_lens, int32_t num_sequences, int32_t num_rows,
                             int32_t max_blocks_per_seq, int32_t block_size, int32_t* ref_counts,
                             int32_t* free_list, int32_t* free_count, int64_t num_blocks,

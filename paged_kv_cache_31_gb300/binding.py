@@ -106,6 +106,8 @@ _SIGS = {
                            _vp], ctypes.c_int),
     "pa_grow_sequences": ([_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _vp],
                           ctypes.c_int),
+    "pa_trim_sequences": ([_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _vp],
+                          ctypes.c_int),
     "pa_free_sequences": ([_vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _vp],
                           ctypes.c_int),
 }
@@ -561,11 +563,12 @@ def _on(dev, stream):
 
 
 def _scratch(nbytes, dev, stream):
-    """Workspace of one call; it stays with the call's stream when that is not the current one."""
-    w = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
-    if stream is not None:
-        w.record_stream(stream)
-    return w
+    """Memory of one call, from the pool of the stream that the call goes to: memory of another
+    stream's pool may still be in use by what that stream has queued."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
 
 
 def pa_rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0,
@@ -759,7 +762,7 @@ def pa_fork_sequences(block_tables, seq_lens, parents, children, ref_counts, fre
     dev = _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, parents, children)
     n = parents.numel()
     if block_pairs is None:
-        block_pairs = torch.empty(n, 2, dtype=torch.int32, device=block_tables.device)
+        block_pairs = _scratch(8 * n, dev, stream).view(torch.int32).view(n, 2)
     _ints(dev, block_pairs)
     if block_pairs.shape != (n, 2):
         raise ValueError("block_pairs must be [n, 2]")
@@ -780,6 +783,17 @@ def pa_grow_sequences(block_tables, seq_lens, sequences, new_lens, ref_counts, f
                                   sequences.numel(), block_tables.shape[0], block_tables.shape[1],
                                   int(block_size), _a(ref_counts), _a(free_list), _a(free_count),
                                   ref_counts.numel(), _on(dev, stream)), "pa_grow_sequences")
+
+
+def pa_trim_sequences(block_tables, seq_lens, sequences, new_lens, ref_counts, free_list,
+                      free_count, block_size, stream=None):
+    """Shorten the rows `sequences` to new_lens, giving back the blocks behind."""
+    dev = _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, sequences,
+                       new_lens)
+    _check(_lib.pa_trim_sequences(_a(block_tables), _a(seq_lens), _a(sequences), _a(new_lens),
+                                  sequences.numel(), block_tables.shape[0], block_tables.shape[1],
+                                  int(block_size), _a(ref_counts), _a(free_list), _a(free_count),
+                                  ref_counts.numel(), _on(dev, stream)), "pa_trim_sequences")
 
 
 def pa_free_sequences(block_tables, seq_lens, sequences, ref_counts, free_list, free_count,

@@ -34,11 +34,16 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile(
-      "barrier.cluster.arrive.release.aligned;\n\t"
-      "barrier.cluster.wait.acquire.aligned;" ::
-          : "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 // Address, in the cluster's shared window, of p's counterpart in CTA `rank`.
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
@@ -58,6 +63,9 @@ __device__ __forceinline__ uint32_t peer_load(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void peer_store(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // A set of block ids, `words` 32-bit words of it in each CTA of the cluster.
@@ -300,13 +308,14 @@ constexpr int kWarps = kPagesThreads / 32;
 constexpr int kChunk = 256;  // table entries a warp takes at a time, eight per lane
 
 struct PagesShared {
-  int bad;      // CTA 0's: any CTA found an error
+  int bad;                     // some CTA found an error (told to all)
+  int totals[kCluster];        // free: blocks freed by each CTA (told to all)
   int scan[32];
-  int total;    // blocks freed by this CTA (free)
   int off[kPagesThreads + 1];  // chunk offsets of this round's items
   int entries[kPagesThreads];  // table entries of the item that are walked
+  int len[kPagesThreads];      // length of the row that is read
   int from[kPagesThreads];     // table row that is read
-  int to[kPagesThreads];       // fork: table row that is written; grow: the first new entry
+  int to[kPagesThreads];       // fork: table row that is written; else the first entry walked
   int taken[kPagesThreads];    // fork, grow: blocks taken before the item
   int refs[kPagesThreads];     // fork: the round's forks of this parent, at its first fork (else 0)
   uint32_t rows[kMaxPageRows / 32];
@@ -314,6 +323,8 @@ struct PagesShared {
 
 // WHAT: PAGES_FORK, PAGES_GROW or PAGES_FREE.  Items (forks, or sequences) go in rounds of up to
 // 1024; a round's table entries are cut into chunks of 256, dealt to all warps of the cluster.
+// What a CTA learns that all have to know is written into every CTA's shared memory before a
+// cluster barrier, so no CTA reads another's and none has to wait for the others to leave.
 // Reference counts are the scattered accesses (a sector each), which is what a large call takes
 // its time for; a parent's are read and raised once per round, whatever its number of forks.
 template <int WHAT>
@@ -324,20 +335,17 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster_rank();
   const int b = p.block_size;
-  pdl_wait();
-  // (one thread of the cluster reads the status word: another stream's call may set it meanwhile)
-  if (tid == 0) sh.bad = rank == 0 && status_set(p.status) ? 2 : 0;
+  const bool single = p.count <= kPagesThreads;  // one round: it stays in shared memory
+  if (tid == 0) sh.bad = 0;
   if (WHAT == PAGES_FREE) gone.clear();
   if (rank == 0)
     for (int i = tid; i < (p.num_rows + 31) / 32; i += kPagesThreads) sh.rows[i] = 0;
+  cluster_arrive();  // (waited for before the first access to another CTA's shared memory)
+  pdl_wait();
   const int have_free = *p.free_count;
-  cluster_sync();
-  const uint32_t flag = peer_addr(&sh.bad, 0);
-  if (peer_load(flag)) {  // an earlier error: nothing is done
-    cluster_sync();       // (CTA 0 stays until every CTA has read its flag)
-    return;
-  }
   bool bad = have_free < 0 || (int64_t)have_free > p.num_blocks;
+  // (one thread of the cluster reads the status word: another stream's call may set it meanwhile)
+  if (rank == 0 && tid == 0) bad |= status_set(p.status);
 
   auto blocks_of = [&](int n) { return (int)(((int64_t)n + b - 1) / b); };
   auto in_pool = [&](int id) { return id >= 0 && (int64_t)id < p.num_blocks; };
@@ -345,12 +353,12 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
   // from `base` (blocks taken in earlier rounds), which is advanced.
   auto load_round = [&](int r0, int& base, bool group = false) {
     const int K = min(kPagesThreads, p.count - r0);
-    int entries = 0, take = 0, row = -1, to = 0;
+    int entries = 0, take = 0, row = -1, to = 0, n = 0;
     if (tid < K) {
       row = p.rows[r0 + tid];
-      if (WHAT != PAGES_FREE) to = p.other[r0 + tid];
+      if (WHAT != PAGES_FREE || p.other) to = p.other[r0 + tid];
       if (row >= 0 && row < p.num_rows) {
-        const int n = p.seq_lens[row];
+        n = p.seq_lens[row];
         if (n < 0 || blocks_of(n) > p.max_blocks) {
           bad = true;
         } else if (WHAT == PAGES_FORK) {
@@ -364,18 +372,22 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
             entries = take = blocks_of(want) - blocks_of(n);
             to = blocks_of(n);
           }
+        } else if (to < 0 || to > n) {
+          bad = true;
         } else {
-          entries = blocks_of(n);
+          entries = blocks_of(n) - blocks_of(to);
+          to = blocks_of(to);
         }
       } else {
         bad = true;
       }
     }
-    int chunks, took;
+    int chunks, took = 0, before = 0;
     const int off = block_exclusive_scan((entries + kChunk - 1) / kChunk, sh.scan, &chunks);
-    const int before = block_exclusive_scan(take, sh.scan, &took);
+    if (WHAT != PAGES_FREE) before = block_exclusive_scan(take, sh.scan, &took);
     sh.off[tid] = off;
     sh.entries[tid] = entries;
+    sh.len[tid] = n;
     sh.from[tid] = row;
     sh.to[tid] = to;
     sh.taken[tid] = base + before;
@@ -410,17 +422,21 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
   };
   // Adds sign (-1: takes back) times the call's change to the reference counts of the table
   // entries it holds on to (fork: all but a partly filled last one) or lets go; `bad` when an entry
-  // is not an id or its count cannot be right.
+  // is not an id or its count cannot be right.  Returns the blocks that the call takes; `chunks`
+  // is the last round's.
+  int chunks = 0;
   auto change_refs = [&](int sign) {
-    int none = 0;
+    int take = 0;
     for (int r0 = 0; r0 < p.count; r0 += kPagesThreads) {
       const int K = min(kPagesThreads, p.count - r0);
-      const int chunks = load_round(r0, none, true);
+      chunks = load_round(r0, take, true);
+      if (r0 == 0 && sign > 0) cluster_wait();
       walk(chunks, K, [&](int it, int e0, int n) {
         const int by = WHAT == PAGES_FORK ? sh.refs[it] : -1;
         if (by == 0) return;  // the parent's first fork does it
-        const bool part = WHAT == PAGES_FORK && p.seq_lens[sh.from[it]] % b != 0;
-        const int32_t* row = p.block_tables + (int64_t)sh.from[it] * p.max_blocks;
+        const bool part = WHAT == PAGES_FORK && sh.len[it] % b != 0;
+        const int32_t* row = p.block_tables + (int64_t)sh.from[it] * p.max_blocks +
+                             (WHAT == PAGES_FREE ? sh.to[it] : 0);
         int id[8], old[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -445,11 +461,12 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
         }
       });
     }
-    return none;
+    return take;
   };
 
   // ---- rows distinct (CTA 0), lengths, table entries and their counts, the blocks to take
   if (rank == 0) {
+    __syncthreads();  // the bitmap is clear
     const int32_t* written = WHAT == PAGES_FORK ? p.other : p.rows;
     for (int i = tid; i < p.count; i += kPagesThreads) {
       const int row = written[i];
@@ -458,16 +475,18 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
       else
         bad |= (atomicOr(&sh.rows[row >> 5], 1u << (row & 31)) >> (row & 31)) & 1u;
     }
-    __syncthreads();
-    if (WHAT == PAGES_FORK)
+    if (WHAT == PAGES_FORK) {
+      __syncthreads();
       for (int i = tid; i < p.count; i += kPagesThreads) {
         const int row = p.rows[i];
         if (row >= 0 && row < p.num_rows) bad |= (sh.rows[row >> 5] >> (row & 31)) & 1u;
       }
+    }
   }
   int taken = 0;
   if (WHAT == PAGES_GROW) {
-    for (int r0 = 0; r0 < p.count; r0 += kPagesThreads) load_round(r0, taken);
+    for (int r0 = 0; r0 < p.count; r0 += kPagesThreads) chunks = load_round(r0, taken);
+    cluster_wait();
   } else {
     taken = change_refs(1);
   }
@@ -479,9 +498,9 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
       bad |= !in_pool(id) || p.ref_counts[id] != 0;
     }
   }
-  if (__syncthreads_or(bad) && tid == 0) peer_or(flag, 1u);
+  if (__syncthreads_or(bad) && tid < kCluster) peer_or(peer_addr(&sh.bad, tid), 1u);
   cluster_sync();  // (free: every reference is dropped and the set complete)
-  bool undo = peer_load(flag) != 0;
+  bool undo = *reinterpret_cast<volatile int*>(&sh.bad) != 0;
   int at = 0;
   const uint32_t per = (words + kPagesThreads - 1) / kPagesThreads;
   const uint32_t w0 = min(tid * per, words), w1 = min(w0 + per, words);
@@ -491,12 +510,12 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
     for (uint32_t w = w0; w < w1; ++w) mine += __popc(gone.mine[w]);
     int total;
     at = block_exclusive_scan(mine, sh.scan, &total);
-    if (tid == 0) sh.total = total;
+    if (tid < kCluster) peer_store(peer_addr(&sh.totals[rank], tid), (uint32_t)total);
     cluster_sync();
     int before = 0, all = 0;
 #pragma unroll
     for (int r = 0; r < kCluster; ++r) {
-      const int t = (int)peer_load(peer_addr(&sh.total, r));
+      const int t = *reinterpret_cast<volatile int*>(&sh.totals[r]);
       if (r < rank) before += t;
       all += t;
     }
@@ -506,8 +525,8 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
   }
   if (undo) {
     if (WHAT != PAGES_GROW) change_refs(-1);
+    // (an earlier error stays the recorded one)
     if (rank == 0 && tid == 0) record_error(p.status, PA_EINVAL);
-    cluster_sync();  // no CTA leaves while another may read its shared memory
     return;
   }
 
@@ -520,10 +539,10 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
     int base = 0;
     for (int r0 = 0; r0 < p.count; r0 += kPagesThreads) {
       const int K = min(kPagesThreads, p.count - r0);
-      const int chunks = load_round(r0, base);
+      if (!single) chunks = load_round(r0, base);
       walk(chunks, K, [&](int it, int e0, int n) {
         const int64_t row = (int64_t)sh.from[it] * p.max_blocks;
-        const bool part = WHAT == PAGES_FORK && p.seq_lens[sh.from[it]] % b != 0;
+        const bool part = WHAT == PAGES_FORK && sh.len[it] % b != 0;
         int id[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -552,15 +571,17 @@ __global__ void __launch_bounds__(kPagesThreads) k_pages(const PagesParams p, ui
         }
       });
     }
-    if (WHAT == PAGES_FORK)  // forks of whole blocks copy nothing
-      for (int i = rank * kPagesThreads + tid; i < p.count; i += kCluster * kPagesThreads)
-        if (p.seq_lens[p.rows[i]] % b == 0) p.block_pairs[2 * i] = p.block_pairs[2 * i + 1] = -1;
+    if (!single) cluster_sync();  // every CTA has read the lengths
   }
-  cluster_sync();  // every CTA has read the lengths and the count
+  // lengths, and pairs of forks of whole blocks (which copy nothing)
   for (int i = rank * kPagesThreads + tid; i < p.count; i += kCluster * kPagesThreads) {
-    if (WHAT == PAGES_FORK) p.seq_lens[p.other[i]] = p.seq_lens[p.rows[i]];
+    if (WHAT == PAGES_FORK) {
+      const int n = single ? sh.len[i] : p.seq_lens[p.rows[i]];
+      if (n % b == 0) p.block_pairs[2 * i] = p.block_pairs[2 * i + 1] = -1;
+      p.seq_lens[p.other[i]] = n;
+    }
     if (WHAT == PAGES_GROW) p.seq_lens[p.rows[i]] = p.other[i];
-    if (WHAT == PAGES_FREE) p.seq_lens[p.rows[i]] = 0;
+    if (WHAT == PAGES_FREE) p.seq_lens[p.rows[i]] = p.other ? p.other[i] : 0;
   }
   if (rank == 0 && tid == 0) *p.free_count = have_free - taken;
 }

@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
   float* sk = sq + kBM * LD;
   float* sv = sk + kBN * LD;
   float* sp = sv + kBN * LD;  // [32][33]
+  __shared__ int64_t s_row[kBN];  // pool rows (position, kv head) of the tile's keys, or -1
   __shared__ int s_skip;
   const VarlenMeta& m = p.m;
   const int tid = threadIdx.x, row = tid >> 2, c = tid & 3;
@@ -271,28 +272,42 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
     const int32_t* trow = m.block_tables + (int64_t)sg.s * m.max_blocks;
     for (int j = sg.t0; j < sg.t1; ++j) {
       const int key0 = sg.kv0 + j * kBN;
-      __syncthreads();  // the tile before has been used
-      for (int i = tid; i < kBN * (DP / 4); i += 128) {
-        const int kk = i / (DP / 4), d = (i % (DP / 4)) * 4, key = key0 + kk;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        if (key < sg.n && d < D) {
-          const int64_t at = (((int64_t)trow[key / m.block_size] * m.block_size +
-                               key % m.block_size) * m.num_kv_heads + sg.kvh) * D + d;
+      if (tid < kBN) {
+        const int key = key0 + tid;
+        s_row[tid] = key < sg.n ? ((int64_t)trow[key / m.block_size] * m.block_size +
+                                   key % m.block_size) * m.num_kv_heads + sg.kvh
+                                : -1;
+      }
+      __syncthreads();  // (the tile before has been used, too)
+      // a thread's column is the same in all its rows; four rows are in flight at a time
+      constexpr int kCols = DP / 4, kStep = 128 / kCols;
+      const int d = tid % kCols * 4;
+      for (int k0 = tid / kCols; k0 < kBN; k0 += 4 * kStep) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          a[u] = b[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          const int64_t at = s_row[k0 + u * kStep] * D + d;
+          if (at < 0 || d >= D) continue;
           if (vec) {
-            a = load4<TKV>(kb + at);
-            b = load4<TKV>(vb + at);
+            a[u] = load4<TKV>(kb + at);
+            b[u] = load4<TKV>(vb + at);
           } else {
             float x[4] = {}, y[4] = {};
             for (int e = 0; e < 4 && d + e < D; ++e) {
               x[e] = to_f32(kb[at + e]);
               y[e] = to_f32(vb[at + e]);
             }
-            a = make_float4(x[0], x[1], x[2], x[3]);
-            b = make_float4(y[0], y[1], y[2], y[3]);
+            a[u] = make_float4(x[0], x[1], x[2], x[3]);
+            b[u] = make_float4(y[0], y[1], y[2], y[3]);
           }
         }
-        *reinterpret_cast<float4*>(sk + kk * LD + d) = a;
-        *reinterpret_cast<float4*>(sv + kk * LD + d) = b;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int kk = k0 + u * kStep;
+          *reinterpret_cast<float4*>(sk + kk * LD + d) = a[u];
+          *reinterpret_cast<float4*>(sv + kk * LD + d) = b[u];
+        }
       }
       __syncthreads();
       float x[8];

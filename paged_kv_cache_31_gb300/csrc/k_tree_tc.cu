@@ -35,8 +35,9 @@
 //
 // Every mbarrier wait is bounded; one that runs out records PA_ETIMEOUT and raises an abort flag
 // that ends the other roles' waits.  A softmax warp whose wait fails goes through the rest of its
-// share without waiting or writing, so that no warp is left at the named barriers; the TMA issuers wait (bounded) for their copies in flight
-// and the MMA issuers for their MMAs before the CTA gives its tensor memory back.
+// share without waiting or writing, so that no warp is left at the named barriers; the TMA
+// issuers wait (bounded) for their copies in flight and the MMA issuers for their MMAs before the
+// CTA gives its tensor memory back.
 #include <algorithm>
 
 #include "k_tree.cuh"
@@ -652,6 +653,8 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
         bad = !wait_all(c, stall ? B_NEVER : B_SFULL + x, stall ? 0u : n & 1);
       // the row of q was multiplied by 2^exp when it was split (known once its first S is)
       if (FP8 && i == 0) sl *= __uint_as_float((uint32_t)(127 - *exps) << 23);
+      // (a product that came to zero would make the hidden keys' -inf a NaN)
+      if (i == 0) sl = fmaxf(sl, 1.17549435e-38f);
       if (!idle && !bad) {
         tc_fence_after();
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -751,7 +754,8 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
       state_taken(par);
       bad |= bads[par * 4 + quad] != 0;  // (uniform across the warp)
     }
-    if (!bad && *c.abort == 0) {  // (a failed role's rows must not be written)
+    // (a failed role's rows must not be written)
+    if (!bad && __all_sync(kFull, *c.abort == 0)) {
       tc_fence_after();
       float a0 = 1.f, a1 = 0.f;
       if (join) {

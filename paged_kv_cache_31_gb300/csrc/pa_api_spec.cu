@@ -394,4 +394,24 @@ pa_status pa_free_sequences(int32_t* block_tables, int32_t* seq_lens, const int3
   return pages_call(PAGES_FREE, p, sequences, nullptr, stream);
 }
 
+pa_status pa_trim_sequences(int32_t* block_tables, int32_t* seq_lens, const int32_t* sequences,
+                            const int32_t* new_lens, int32_t num_sequences, int32_t num_rows,
+                            int32_t max_blocks_per_seq, int32_t block_size, int32_t* ref_counts,
+                            int32_t* free_list, int32_t* free_count, int64_t num_blocks,
+                            cudaStream_t stream) {
+  PagesParams p{};
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.ref_counts = ref_counts;
+  p.free_list = free_list;
+  p.free_count = free_count;
+  p.count = num_sequences;
+  p.num_rows = num_rows;
+  p.max_blocks = max_blocks_per_seq;
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  if (num_sequences > 0 && !new_lens) return PA_EINVAL;
+  return pages_call(PAGES_FREE, p, sequences, new_lens, stream);
+}
+
 }  // extern "C"

@@ -561,7 +561,7 @@ struct PagesParams {
   int32_t* block_tables;  // [num_rows, max_blocks]
   int32_t* seq_lens;      // [num_rows]
   const int32_t* rows;    // fork: parents; grow, free: the sequences
-  const int32_t* other;   // fork: children; grow: new lengths
+  const int32_t* other;   // fork: children; grow, free: new lengths (free: null for none)
   int32_t* block_pairs;   // fork: [count, 2] out
   int32_t* ref_counts;    // [num_blocks]
   int32_t* free_list;     // [num_blocks]

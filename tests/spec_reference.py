@@ -65,11 +65,13 @@ def unpack_mask(mask, nodes):
 
 
 def tree_attention(q, kb, vb, qsl, lens, positions, mask, tables, scale, window=0, sinks=None,
-                   k_scales=None, v_scales=None, weight_u=2.0 ** -16):
+                   k_scales=None, v_scales=None, weight_u=2.0 ** -16, q_u=0.0):
     """(out [T, H, D], lse [H, T], bound of out before its own rounding, bound of lse), 64 bits.
 
     k_scales, v_scales: per kv head (or None).  weight_u: the softmax weights' rounding where they
-    enter the product with V (a bf16 pair 2^-16, f16 2^-11, fp32 less than either)."""
+    enter the product with V (a bf16 pair 2^-16, f16 2^-11, fp32 less than either).  q_u: what q's
+    elements may be off by, relative to their row's largest (0: q is used as it is; a pair of
+    e4m3 terms 2^-17: half of e4m3's smallest step, 2^-10, where the largest is at least 2^7)."""
     T, H, D = q.shape
     NB, bs, Hkv, _ = kb.shape
     G = H // Hkv
@@ -101,6 +103,9 @@ def tree_attention(q, kb, vb, qsl, lens, positions, mask, tables, scale, window=
             # an fp32 dot product of D terms: (D + 2) u of the terms' magnitudes, scale included
             d = ((qd[a:b, h].abs() @ torch.nan_to_num(K).abs().t()) * abs(scale))
             d = torch.where(see, d, 0.0).amax(1, keepdim=True) * (D + 4) * U32
+            if q_u:
+                e = torch.where(see, torch.nan_to_num(K).abs().sum(1), 0.0).amax(1, keepdim=True)
+                d = d + q_u * qd[a:b, h].abs().amax(1, keepdim=True) * e * abs(scale)
             x = torch.where(see, x, -math.inf)
             if sinks is not None:
                 x = torch.cat([x, values(sinks)[h].expand(n, 1)], 1)
@@ -179,12 +184,13 @@ class Pages:
                 self.tables[r][i] = page
             self.lens[r] = n
 
-    def end(self, rows):
+    def end(self, rows, new=None):
         gone = []
-        for r in rows:
-            for b in self.tables[r][:self._blocks(self.lens[r])]:
+        for i, r in enumerate(rows):
+            n = new[i] if new else 0
+            for b in self.tables[r][self._blocks(n):self._blocks(self.lens[r])]:
                 self.refs[b] -= 1
                 if self.refs[b] == 0:
                     gone.append(b)
-            self.lens[r] = 0
+            self.lens[r] = n
         self.free += sorted(gone)

@@ -251,6 +251,31 @@ def test_fork_grow_free(pa, lens, forks, block):
     assert not any(st.p.refs) and len(st.p.free) == len(st.p.refs)
 
 
+@pytest.mark.parametrize("block", [16, 1, 5])
+def test_trim(pa, block):
+    """Rows cut to nothing, inside a block, at a block's end, not at all; shared and own blocks."""
+    rng = random.Random(block)
+    lens = [40, 16, 0, 1, 333, 80, 7]
+    st = _state(9, 70 if block > 1 else 340, lens, block, 9, 120)
+    pairs = pa.pa_fork_sequences(st.tables, st.lens, _i32([4, 0]), _i32([7, 8]), *st.args())
+    assert [tuple(x) for x in pairs.tolist()] == st.p.fork([4, 0], [7, 8])
+    rows = [4, 0, 1, 2, 3, 7, 8, 5]
+    for new in ([330, 40, 16, 0, 0, 321, 1, 75], [0, 39, 0, 0, 0, 320, 0, 16]):
+        order = rng.sample(range(len(rows)), len(rows))
+        r, n = [rows[i] for i in order], [min(new[i], st.p.lens[rows[i]]) for i in order]
+        pa.pa_trim_sequences(st.tables, st.lens, _i32(r), _i32(n), *st.args())
+        st.p.end(r, n)
+        st.same()
+    old = [st.p.lens[r] for r in (0, 5)]
+    for r, n in (([0], [old[0] + 1]), ([0], [-1]), ([0, 0], [0, 0]), ([9], [0]), ([5, 0], [0, 100])):
+        _refused(pa, st, lambda: pa.pa_trim_sequences(st.tables, st.lens, _i32(r), _i32(n),  # noqa: B023
+                                                      *st.args()))
+    pa.pa_free_sequences(st.tables, st.lens, _i32(list(range(9))), *st.args())
+    st.p.end(range(9))
+    st.same()
+    assert pa.pa_device_status() == pa.PA_OK and not any(st.p.refs)
+
+
 def test_more_rows_than_one_round(pa):
     """Lists longer than the 1024 rows that the kernel takes at a time."""
     lens = [33, 16, 5]
@@ -264,6 +289,10 @@ def test_more_rows_than_one_round(pa):
     new = [min(64, st.p.lens[k] + k % 20) for k in kids]
     pa.pa_grow_sequences(st.tables, st.lens, _i32(kids), _i32(new), *st.args())
     st.p.grow(kids, new)
+    st.same()
+    new = [n // 3 for n in new]
+    pa.pa_trim_sequences(st.tables, st.lens, _i32(kids), _i32(new), *st.args())
+    st.p.end(kids, new)
     st.same()
     pa.pa_free_sequences(st.tables, st.lens, _i32(kids[::-1]), *st.args())
     st.p.end(kids)

@@ -76,7 +76,8 @@ class Batch:
         u = 2.0 ** -11 if self.kb.dtype == E4M3 else 2.0 ** -16
         want, wl, ob, lb = tree_attention(self.q, self.kb, self.vb, self.qsl, self.lens, self.pos,
                                           self.mask, self.tables, self.scale, window, sinks, ks,
-                                          vs, weight_u=u)
+                                          vs, weight_u=u,
+                                          q_u=2.0 ** -17 if self.kb.dtype == E4M3 else 0.0)
         assert_within(out, want, ob + (want.abs() + ob) * OUT_U[self.q.dtype] + 2.0 ** -126, "out")
         assert_within(lse, wl, lb, "lse")
         out2, _ = self.call(pa, window=window, lse=False, sinks=sinks, k_scale=k_scale,
@@ -175,6 +176,22 @@ def test_sharp_and_negative_scales(pa):
     b.check(pa)
     b.scale = 0.0
     b.check(pa)
+
+
+def test_uneven_queries_over_e4m3_pools(pa):
+    """Rows of q with one large element, tiny rows, rows of zeros; scales at both ends."""
+    b = Batch([30, 5], [300, 90], 8, 2, 128, kv=E4M3, seed=27)
+    b.q *= 2.0 ** -9
+    b.q[::2, ::3, 5] = 40.0
+    b.q[3], b.q[7] = 0.0, b.q[7] * 2.0 ** -100
+    b.check(pa)
+    b.q[11] *= 2.0 ** 90
+    b.check(pa, k_scale=2.0 ** -90, v_scale=2.0 ** 20)
+    b.q[11] = 0.0
+    b.scale = 2.0 ** -40
+    b.check(pa, k_scale=2.0 ** -40)
+    b.mask[9] = 0
+    b.check(pa, window=3)
 
 
 def test_rows_that_see_nothing(pa):

@@ -183,7 +183,11 @@ def test_page_refusals(b):
              NB=8):
         return L.pa_free_sequences(tab, lens, seqs, n, rows, MB, bs, refs, fl, fc, NB, None)
 
-    for f in (fork, grow, free):
+    def trim(tab=FAKE, lens=FAKE, seqs=FAKE, new=FAKE, n=2, rows=4, MB=3, bs=16, refs=FAKE, fl=FAKE,
+             fc=FAKE, NB=8):
+        return L.pa_trim_sequences(tab, lens, seqs, new, n, rows, MB, bs, refs, fl, fc, NB, None)
+
+    for f in (fork, grow, trim, free):
         assert f(bs=0) == S
         assert f(rows=65537) == f(NB=(1 << 23) + 1) == f(MB=1 << 30) == U
         for kw in (dict(n=5), dict(n=-1), dict(rows=-1), dict(MB=-1), dict(NB=-1), dict(tab=None),
@@ -192,3 +196,4 @@ def test_page_refusals(b):
         assert f(n=0, tab=None) == b.PA_OK
     assert fork(par=None) == fork(kid=None) == fork(pairs=None) == E
     assert grow(seqs=None) == grow(new=None) == free(seqs=None) == E
+    assert trim(seqs=None) == trim(new=None) == E
