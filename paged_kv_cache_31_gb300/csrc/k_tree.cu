@@ -193,10 +193,13 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(const TreeParams p) 
 }
 
 // ---- the general kernel -----------------------------------------------------------------------
-// 32 query rows x 32 keys per step in fp32 on the FMA pipes: thread (row = tid / 4, c = tid % 4)
-// computes the scores of keys c, c + 4, ... of its row and dims 4c + 16i .. of its output row.
-// Rows are padded by four floats, so the quads' 16-byte reads of different rows hit different
-// banks.  It is bound by shared-memory reads (9 of them for 32 FMAs on both products).
+// 32 query rows x 32 keys per step in fp32 on the FMA pipes: thread (rg = tid / 16, c = tid % 16)
+// computes the scores of rows 4 rg .. 4 rg + 3 and keys c and c + 16, and dims 4c + 64i .. of the
+// same rows' outputs.  It is bound by shared-memory reads (a 16-byte read takes as long as 16 of
+// a warp's FMAs): 9 of them for the 64 FMAs per thread of four dims of Q K^T and one key of P V at
+// head size 128, against 18 when a thread had one row, eight keys and a quarter of the dims.
+// Rows of the tiles are padded by four floats, so 16-byte reads of different rows hit different
+// banks.
 
 constexpr int kBM = kTreeGenericRows, kBN = kTreeGenericKeys;
 
@@ -218,24 +221,27 @@ __device__ __forceinline__ float4 load4(const TKV* p) {
   }
 }
 
+constexpr int kLDP = kBM + 4;  // row length of the transposed weights
+
 template <int DP>
 constexpr size_t generic_smem() {
-  return (size_t)(3 * 32 * (DP + 4) + 32 * 33) * 4;
+  return (size_t)((kBM + 2 * kBN) * (DP + 4) + kBN * kLDP) * 4;
 }
 
 // DP: head size padded to 64, 128 or 256; vec: rows can be read four elements at a time
 template <typename TQ, typename TKV, int DP>
 __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const bool vec) {
   constexpr int LD = DP + 4;
+  constexpr int kDI = DP / 64;  // float4s of a thread's output row
   extern __shared__ __align__(16) float s_mem[];
   float* sq = s_mem;
   float* sk = sq + kBM * LD;
   float* sv = sk + kBN * LD;
-  float* sp = sv + kBN * LD;  // [32][33]
+  float* sp = sv + kBN * LD;      // [key][row]
   __shared__ int64_t s_row[kBN];  // pool rows (position, kv head) of the tile's keys, or -1
   __shared__ int s_skip;
   const VarlenMeta& m = p.m;
-  const int tid = threadIdx.x, row = tid >> 2, c = tid & 3;
+  const int tid = threadIdx.x, rg = 4 * (tid >> 4), c = tid & 15;
   const int D = m.head_dim, G = m.group;
   pdl_wait();
   pdl_launch_dependents();
@@ -250,10 +256,12 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
   TreeSegment sg;
   while (walk.next(p, sg)) {
     const int rows = sg.rows;
-    const int r = sg.row0 + row;  // row of the sequence's nodes x group
-    const bool valid = row < rows;
-    const int tok = sg.qs + (valid ? r / G : 0);
-    const int pos = m.window > 0 ? m.positions[tok] : 0;
+    int tok[4], pos[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      tok[k] = sg.qs + (rg + k < rows ? (sg.row0 + rg + k) / G : 0);
+      pos[k] = m.window > 0 ? m.positions[tok[k]] : 0;
+    }
     const float sl = head_scale(m.k_scales, sg.kvh, p.scale) * kLog2e;
     __syncthreads();  // the buffers of the segment before are free
     for (int i = tid; i < kBM * DP; i += 128) {
@@ -265,10 +273,15 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
       }
       sq[rr * LD + d] = x;
     }
-    float mx = -INFINITY, l = 0.f;
-    float o[DP / 4];
+    float mx[4], l[4];
+    float4 o[4][kDI];
 #pragma unroll
-    for (int i = 0; i < DP / 4; ++i) o[i] = 0.f;
+    for (int k = 0; k < 4; ++k) {
+      mx[k] = -INFINITY;
+      l[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kDI; ++i) o[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     const int32_t* trow = m.block_tables + (int64_t)sg.s * m.max_blocks;
     for (int j = sg.t0; j < sg.t1; ++j) {
       const int key0 = sg.kv0 + j * kBN;
@@ -310,72 +323,95 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
         }
       }
       __syncthreads();
-      float x[8];
+      float x[4][2] = {};
+#pragma unroll 2
+      for (int d4 = 0; d4 < DP; d4 += 4) {
+        float4 b[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-      for (int d = 0; d < DP; d += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(sq + row * LD + d);
+        for (int i = 0; i < 2; ++i)
+          b[i] = *reinterpret_cast<const float4*>(sk + (c + 16 * i) * LD + d4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 b = *reinterpret_cast<const float4*>(sk + (c + 4 * i) * LD + d);
-          x[i] += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+        for (int k = 0; k < 4; ++k) {
+          const float4 a = *reinterpret_cast<const float4*>(sq + (rg + k) * LD + d4);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            x[k][i] += a.x * b[i].x + a.y * b[i].y + a.z * b[i].z + a.w * b[i].w;
         }
       }
-      float mt = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = valid && tree_visible(p, sg, tok, pos, key0 + c + 4 * i) ? x[i] * sl : -INFINITY;
-        mt = fmaxf(mt, x[i]);
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          x[k][i] = rg + k < rows && tree_visible(p, sg, tok[k], pos[k], key0 + c + 16 * i)
+                        ? x[k][i] * sl
+                        : -INFINITY;
+        float mt = fmaxf(x[k][0], x[k][1]);
+#pragma unroll
+        for (int s = 8; s > 0; s >>= 1) mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, s));
+        const float mn = fmaxf(mx[k], mt), b0 = mn == -INFINITY ? 0.f : mn;
+        const float alpha = exp2f(mx[k] - b0);
+        x[k][0] = exp2f(x[k][0] - b0);
+        x[k][1] = exp2f(x[k][1] - b0);
+        mx[k] = mn;
+        l[k] = l[k] * alpha + (x[k][0] + x[k][1]);  // this thread's keys; summed at the end
+#pragma unroll
+        for (int i = 0; i < kDI; ++i) {
+          o[k][i].x *= alpha;
+          o[k][i].y *= alpha;
+          o[k][i].z *= alpha;
+          o[k][i].w *= alpha;
+        }
       }
-      mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 1));
-      mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 2));
-      const float mn = fmaxf(mx, mt), b0 = mn == -INFINITY ? 0.f : mn;
-      const float alpha = exp2f(mx - b0);
-      float ls = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = exp2f(x[i] - b0);
-        ls += x[i];
-        sp[row * 33 + c + 4 * i] = x[i];
-      }
-      mx = mn;
-      l = l * alpha + ls;  // this thread's eight keys; the quad is summed at the end
-#pragma unroll
-      for (int i = 0; i < DP / 4; ++i) o[i] *= alpha;
-      __syncwarp();  // the row's weights come from this warp's own quad
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<float4*>(sp + (c + 16 * i) * kLDP + rg) =
+            make_float4(x[0][i], x[1][i], x[2][i], x[3][i]);
+      __syncwarp();  // a row's weights come from its own warp
 #pragma unroll 4
       for (int kk = 0; kk < kBN; ++kk) {
-        const float w = sp[row * 33 + kk];
+        const float4 w4 = *reinterpret_cast<const float4*>(sp + kk * kLDP + rg);
+        const float w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-        for (int i = 0; i < DP / 16; ++i) {
-          const float4 b = *reinterpret_cast<const float4*>(sv + kk * LD + 4 * c + 16 * i);
-          o[4 * i] += w * b.x;
-          o[4 * i + 1] += w * b.y;
-          o[4 * i + 2] += w * b.z;
-          o[4 * i + 3] += w * b.w;
+        for (int i = 0; i < kDI; ++i) {
+          const float4 b = *reinterpret_cast<const float4*>(sv + kk * LD + 4 * c + 64 * i);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            o[k][i].x += w[k] * b.x;
+            o[k][i].y += w[k] * b.y;
+            o[k][i].z += w[k] * b.z;
+            o[k][i].w += w[k] * b.w;
+          }
         }
       }
     }
-    l += __shfl_xor_sync(kFull, l, 1);
-    l += __shfl_xor_sync(kFull, l, 2);
-    if (!valid) continue;
-    if (sg.slot >= 0) {
-      const int64_t at = (int64_t)sg.slot * p.rows_per_item + row;
-      if (c == 0) p.part_ml[at] = make_float2(mx, l);
 #pragma unroll
-      for (int i = 0; i < DP / 4; ++i) {
-        const int d = 4 * c + 16 * (i >> 2) + (i & 3);
-        if (d < D) p.part_o[at * D + d] = o[i];
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int s = 8; s > 0; s >>= 1) l[k] += __shfl_xor_sync(kFull, l[k], s);
+      const int r = rg + k;
+      if (r >= rows) continue;  // (the same for all sixteen threads of a row)
+      const bool part = sg.slot >= 0;
+      const int64_t at = (int64_t)sg.slot * p.rows_per_item + r;
+      const int R = sg.row0 + r, h = sg.kvh * G + R % G;
+      float f = 1.f;
+      if (!part)
+        f = tree_finish(p, sg.kvh, h, tok[k], mx[k], l[k], c == 0);
+      else if (c == 0)
+        p.part_ml[at] = make_float2(mx[k], l[k]);
+      TQ* out = static_cast<TQ*>(p.out) + ((int64_t)tok[k] * m.num_heads + h) * D;
+#pragma unroll
+      for (int i = 0; i < kDI; ++i) {
+        const float v[4] = {o[k][i].x, o[k][i].y, o[k][i].z, o[k][i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int d = 4 * c + 64 * i + e;
+          if (d >= D) continue;
+          if (part)
+            p.part_o[at * D + d] = v[e];
+          else
+            out[d] = from_f32<TQ>(v[e] * f);
+        }
       }
-      continue;
-    }
-    const int h = sg.kvh * G + r % G;
-    const float inv = tree_finish(p, sg.kvh, h, tok, mx, l, c == 0);
-    TQ* out = static_cast<TQ*>(p.out) + ((int64_t)tok * m.num_heads + h) * D;
-#pragma unroll
-    for (int i = 0; i < DP / 4; ++i) {
-      const int d = 4 * c + 16 * (i >> 2) + (i & 3);
-      if (d < D) out[d] = from_f32<TQ>(o[i] * inv);
     }
   }
 }
