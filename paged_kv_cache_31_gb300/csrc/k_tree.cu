@@ -221,6 +221,17 @@ __device__ __forceinline__ float4 load4(const TKV* p) {
   }
 }
 
+// Up to four of the n values that a row has left at p.
+template <typename T>
+__device__ __forceinline__ float4 row4(const T* p, int n, bool vec) {
+  if (vec) return load4<T>(p);
+  float x[4] = {};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < n) x[e] = to_f32(p[e]);
+  return make_float4(x[0], x[1], x[2], x[3]);
+}
+
 constexpr int kLDP = kBM + 4;  // row length of the transposed weights
 
 template <int DP>
@@ -233,6 +244,8 @@ template <typename TQ, typename TKV, int DP>
 __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const bool vec) {
   constexpr int LD = DP + 4;
   constexpr int kDI = DP / 64;  // float4s of a thread's output row
+  // when a tile is read, a thread's four columns are the same in all its rows, kStep apart
+  constexpr int kCols = DP / 4, kStep = 128 / kCols;
   extern __shared__ __align__(16) float s_mem[];
   float* sq = s_mem;
   float* sk = sq + kBM * LD;
@@ -242,6 +255,7 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
   __shared__ int s_skip;
   const VarlenMeta& m = p.m;
   const int tid = threadIdx.x, rg = 4 * (tid >> 4), c = tid & 15;
+  const int col = tid % kCols * 4;
   const int D = m.head_dim, G = m.group;
   pdl_wait();
   pdl_launch_dependents();
@@ -264,14 +278,19 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
     }
     const float sl = head_scale(m.k_scales, sg.kvh, p.scale) * kLog2e;
     __syncthreads();  // the buffers of the segment before are free
-    for (int i = tid; i < kBM * DP; i += 128) {
-      const int rr = i / DP, d = i % DP;
-      float x = 0.f;
-      if (rr < rows && d < D) {
-        const int R = sg.row0 + rr;
-        x = to_f32(q[((int64_t)(sg.qs + R / G) * m.num_heads + sg.kvh * G + R % G) * D + d]);
+    for (int r0 = tid / kCols; r0 < kBM; r0 += 4 * kStep) {
+      float4 a[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int rr = r0 + u * kStep, R = sg.row0 + rr;
+        a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (rr < rows && col < D)
+          a[u] = row4<TQ>(q + ((int64_t)(sg.qs + R / G) * m.num_heads + sg.kvh * G + R % G) * D + col,
+                          D - col, vec);
       }
-      sq[rr * LD + d] = x;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<float4*>(sq + (r0 + u * kStep) * LD + col) = a[u];
     }
     float mx[4], l[4];
     float4 o[4][kDI];
@@ -292,34 +311,21 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
                                 : -1;
       }
       __syncthreads();  // (the tile before has been used, too)
-      // a thread's column is the same in all its rows; four rows are in flight at a time
-      constexpr int kCols = DP / 4, kStep = 128 / kCols;
-      const int d = tid % kCols * 4;
       for (int k0 = tid / kCols; k0 < kBN; k0 += 4 * kStep) {
         float4 a[4], b[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 4; ++u) {  // (four rows in flight)
           a[u] = b[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          const int64_t at = s_row[k0 + u * kStep] * D + d;
-          if (at < 0 || d >= D) continue;
-          if (vec) {
-            a[u] = load4<TKV>(kb + at);
-            b[u] = load4<TKV>(vb + at);
-          } else {
-            float x[4] = {}, y[4] = {};
-            for (int e = 0; e < 4 && d + e < D; ++e) {
-              x[e] = to_f32(kb[at + e]);
-              y[e] = to_f32(vb[at + e]);
-            }
-            a[u] = make_float4(x[0], x[1], x[2], x[3]);
-            b[u] = make_float4(y[0], y[1], y[2], y[3]);
-          }
+          const int64_t at = s_row[k0 + u * kStep] * D + col;
+          if (at < 0 || col >= D) continue;
+          a[u] = row4<TKV>(kb + at, D - col, vec);
+          b[u] = row4<TKV>(vb + at, D - col, vec);
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int kk = k0 + u * kStep;
-          *reinterpret_cast<float4*>(sk + kk * LD + d) = a[u];
-          *reinterpret_cast<float4*>(sv + kk * LD + d) = b[u];
+          *reinterpret_cast<float4*>(sk + kk * LD + col) = a[u];
+          *reinterpret_cast<float4*>(sv + kk * LD + col) = b[u];
         }
       }
       __syncthreads();
@@ -568,7 +574,7 @@ cudaError_t generic_as(const TreeParams& p, bool vec, cudaStream_t stream) {
 template <typename TQ, typename TKV>
 cudaError_t generic_dims(const TreeParams& p, cudaStream_t stream) {
   const int D = p.m.head_dim;
-  const bool vec = D % 4 == 0 && aligned(p.k_blocks, 4 * sizeof(TKV)) &&
+  const bool vec = D % 4 == 0 && aligned(p.q, 4 * sizeof(TQ)) && aligned(p.k_blocks, 4 * sizeof(TKV)) &&
                    aligned(p.v_blocks, 4 * sizeof(TKV));
   if (D <= 64) return generic_as<TQ, TKV, 64>(p, vec, stream);
   if (D <= 128) return generic_as<TQ, TKV, 128>(p, vec, stream);
