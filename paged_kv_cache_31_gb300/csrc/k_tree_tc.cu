@@ -48,21 +48,24 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBN = 128;      // keys per tile
-constexpr int kStages = 5;    // K / V ring
+constexpr int kStages = 5;    // K / V ring (bf16 pools)
+constexpr int kCodeStages = 3;  // e4m3 pools: a ring of codes for K, one for V
 
 template <int D, bool FP8>
 struct Shape {
   static constexpr int kHalves = D / 64;            // 64-dim halves of a tile: rows of 128 bytes
   static constexpr int kHalfBytes = 128 * 128;
   static constexpr int kTileBytes = kHalves * kHalfBytes;  // a 128-row tile of 16-bit values
-  static constexpr int kLoadBytes = FP8 ? kTileBytes / 2 : kTileBytes;
+  static constexpr int kStageBytes = FP8 ? kTileBytes / 2 : kTileBytes;  // a tile as it is loaded
   static constexpr int kThreads = FP8 ? 512 : 384;
   // K / V stages over bf16 pools: 8-row groups of (dim half, 8 rows of 128 bytes), as the 5-D
-  // boxes write them; widened e4m3 stages and Q: dim half by dim half
+  // boxes write them; widened V and Q: dim half by dim half
   static constexpr int kRowGroup = FP8 ? 1024 : 1024 * kHalves;  // between 8-row groups
   static constexpr int kDimHalf = FP8 ? kHalfBytes : 1024;       // between dim halves
   static constexpr int kOffKV = 2 * kTileBytes;
-  static constexpr int kOffX = kOffKV + kStages * kTileBytes;  // [2][128] float2: a stream's m, l
+  static constexpr int kOffWide = kOffKV + 2 * kCodeStages * kStageBytes;  // e4m3: two tiles of V
+  // [2][128] float2: a stream's m, l
+  static constexpr int kOffX = FP8 ? kOffWide + 2 * kTileBytes : kOffKV + kStages * kTileBytes;
   static constexpr int kOffBad = kOffX + 2 * 128 * 8;          // [2][4] its warps' failed waits
   static constexpr int kOffBar = kOffBad + 2 * 4 * 4;
   static constexpr int kOffMisc = kOffBar + 40 * 8;
@@ -72,15 +75,19 @@ struct Shape {
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
+constexpr int kMostStages = 2 * kCodeStages;
+static_assert(kMostStages >= kStages, "stage barriers");
+
 // barriers (indices of consecutive 8-byte words)
 enum : int {
   B_QFULL = 0,                     // Q buffer landed
   B_QEMPTY = B_QFULL + 2,          // its last S = Q K^T is done
   B_QCONV = B_QEMPTY + 2,          // e4m3: it has been split
-  B_FULL = B_QCONV + 2,            // stage landed: K's copies, then V's (B_FULL + kStages + stage)
-  B_EMPTY = B_FULL + 2 * kStages,  // its copy has been used up
-  B_CONV = B_EMPTY + kStages,      // e4m3: the stage's V is ready as f16 (V's copies only)
-  B_SFULL = B_CONV + kStages,      // per stream: S is ready
+  B_FULL = B_QCONV + 2,            // stage landed: K's copies, then V's (B_FULL + kMostStages + ..)
+  B_EMPTY = B_FULL + 2 * kMostStages,  // its copy has been used up
+  B_WIDE = B_EMPTY + kMostStages,  // e4m3: a V tile is ready as f16
+  B_WFREE = B_WIDE + 2,            // e4m3: its P V is done
+  B_SFULL = B_WFREE + 2,           // per stream: S is ready
   B_PFULL = B_SFULL + 2,           // P is written
   B_PVDONE = B_PFULL + 2,          // P V is done: O is current, the S / P buffer is free
   B_OFREE = B_PVDONE + 2,          // the segment's O has been read
@@ -159,39 +166,57 @@ __device__ __forceinline__ bool wait_all(const Ctx& c, int idx, uint32_t parity)
   return __all_sync(kFull, wait_bar(c, idx, parity));
 }
 
-// The K / V ring.  The copies of a CTA's tiles 0, 1, 2, ... are numbered in the order in which
-// they are needed: K0 V0 K1 V1 ... (K_t 2t, V_t 2t + 1) where an item may have two row tiles, and
-// K0 - K1 V0 K2 V1 K3 ... (K_t 2t, V_t 2t + 3; `ahead`) where none has: the streams then work on two
-// tiles at once, and tile t's V is needed after tile t + 1's K.  Copy n uses stage n % kStages, so
-// K and V take turns in a stage, and an operand's copies come to the same stage every kStages
-// tiles.  A parity tells neighbouring phases of a barrier apart, no more, so each barrier has to
-// be waited for in every phase, or be known to be near:
-//   - "landed" and "ready" barriers are one set per operand, whose consumers wait for each phase;
+// Over bf16 pools K and V share a ring.  The copies of a CTA's tiles 0, 1, 2, ... are numbered in
+// the order in which they are needed: K0 V0 K1 V1 ... (K_t 2t, V_t 2t + 1) where an item may have
+// two row tiles, and K0 - K1 V0 K2 V1 K3 ... (K_t 2t, V_t 2t + 3; `ahead`) where none has: the
+// streams then work on two tiles at once, and tile t's V is needed after tile t + 1's K.  Copy n
+// uses stage n % kStages, so K and V take turns in a stage, and an operand's copies come to the
+// same stage every kStages tiles.  A parity tells neighbouring phases of a barrier apart, no more,
+// so each barrier has to be waited for in every phase, or be known to be near:
+//   - "landed" barriers are one set per operand, whose consumers wait for each phase;
 //   - a stage's "empty" barrier is completed by K's and V's consumers in turn and waited for by
 //     the other operand's producer.  A producer that waits for copy n + 5's consumption has sent
 //     copy n + 8 of its own, after copy n + 3 was used up, and that was after copy n was: QK of
 //     tile t + 3 follows PV of tile t + 1 (n V_t), and PV of tile t its QK (n K_t).  So the barrier
 //     has passed copy n's phase.
 // Where copy 1 does not exist its "empty" phase is completed at the start.
+//
+// Over e4m3 pools each operand has a ring of code stages of its own (0 .. 2 K, 3 .. 5 V), half as
+// large.  V's codes are widened into one of two f16 tiles, and their stage is free as soon as they
+// have been read: more bytes are on their way than when a stage held its V until P V was done.
 __device__ __forceinline__ bool ring_ahead(const TreeParams& p) {
   return p.rows_per_item == p.tile_rows;
 }
+template <bool FP8>
 struct Ring {
-  uint32_t st, par;        // stage of this operand's current copy, parity of n / kStages
-  uint32_t turn, par_own;  // tile t % kStages, parity of t / kStages: its visits to the stage
+  uint32_t st, par;        // stage of this operand's current copy; the parity of its "empty" phase
+  uint32_t turn, par_own;  // tile t % kStages; the parity of its "landed" phase
   __device__ __forceinline__ Ring(const TreeParams& p, int kv) {
-    st = kv ? (ring_ahead(p) ? 3 : 1) : 0;
+    if constexpr (FP8)
+      st = kv ? kCodeStages : 0;
+    else
+      st = kv ? (ring_ahead(p) ? 3 : 1) : 0;
     par = turn = par_own = 0;
   }
   __device__ __forceinline__ void next() {  // the next tile's copy of the same operand
-    st += 2;
-    if (st >= kStages) {
-      st -= kStages;
-      par ^= 1;
-    }
-    if (++turn == kStages) {
-      turn = 0;
-      par_own ^= 1;
+    if constexpr (FP8) {
+      ++st;
+      if (++turn == kCodeStages) {
+        st -= kCodeStages;
+        turn = 0;
+        par ^= 1;
+        par_own ^= 1;
+      }
+    } else {
+      st += 2;
+      if (st >= kStages) {
+        st -= kStages;
+        par ^= 1;
+      }
+      if (++turn == kStages) {
+        turn = 0;
+        par_own ^= 1;
+      }
     }
   }
 };
@@ -214,8 +239,8 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
                          const CUtensorMap* tq, int kv) {
   using S = Shape<D, FP8>;
   const int lane = threadIdx.x & 31;
-  uint64_t* full = c.bar + B_FULL + kv * kStages;
-  Ring r(p, kv);
+  uint64_t* full = c.bar + B_FULL + kv * kMostStages;
+  Ring<FP8> r(p, kv);
   uint32_t issued = 0, nq = 0;  // this warp's stages; row tiles of Q (tile n uses buffer n % 2)
   bool ok = c.work;
   TreeWalk walk(p, blockIdx.x);
@@ -249,18 +274,16 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
       if (j + 1 < g.t1) next = lane < 8 && nb < blocks ? row[nb] : -1;
       if (lane == 0) {
         ok = wait_bar(c, B_EMPTY + r.st, r.par ^ 1);
-        if (ok) mbar_arrive_expect_tx(full + r.st, S::kLoadBytes);
+        if (ok) mbar_arrive_expect_tx(full + r.st, S::kStageBytes);
       }
       ok = __shfl_sync(kFull, (int)ok, 0);
       if (!ok) break;
       if (lane < 8) {  // a block past the end: rows outside the pool, which TMA fills with zeros
-        uint8_t* dst = c.sm + S::kOffKV + r.st * S::kTileBytes;
-        if constexpr (FP8)  // V's codes go where its second dim half's rows will be
-          tma_load_3d(dst + (kv ? S::kHalfBytes : 0) + lane * 2048, tkv, 0, g.kvh,
-                      id >= 0 ? id * 16 : -16, full + r.st);
+        uint8_t* dst = c.sm + S::kOffKV + r.st * S::kStageBytes + lane * (S::kStageBytes / 8);
+        if constexpr (FP8)
+          tma_load_3d(dst, tkv, 0, g.kvh, id >= 0 ? id * 16 : -16, full + r.st);
         else
-          tma_load_5d(dst + lane * (S::kTileBytes / 8), tkv, 0, 0, 0, id >= 0 ? id * 2 : -2, g.kvh,
-                      full + r.st);
+          tma_load_5d(dst, tkv, 0, 0, 0, id >= 0 ? id * 2 : -2, g.kvh, full + r.st);
       }
       ++issued;
       r.next();
@@ -269,9 +292,9 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
   // the copies still in flight (after an abort; otherwise all have been consumed): the last ones
   // are the last of their barriers
   if (lane == 0) {
-    Ring d(p, kv);
+    Ring<FP8> d(p, kv);
     for (uint32_t k = 0; k < issued; ++k, d.next())
-      if (k + kStages >= issued) mbar_wait(full + d.st, d.par_own, c.limit);
+      if (k + (FP8 ? kCodeStages : kStages) >= issued) mbar_wait(full + d.st, d.par_own, c.limit);
     for (uint32_t k = nq > 2 ? nq - 2 : 0; k < nq; ++k)
       mbar_wait(c.bar + B_QFULL + (k & 1), (k >> 1) & 1u, c.limit);
   }
@@ -285,7 +308,7 @@ __device__ void s_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   constexpr uint32_t kIdesc = idesc_f16kind(128, kBN, 0, FP8 ? 0 : 1);
   constexpr int kQ = FP8 ? B_QCONV : B_QFULL;
   const uint32_t sm = smem_u32(c.sm), elect = (threadIdx.x & 31) == 0;
-  Ring r(p, 0);
+  Ring<FP8> r(p, 0);
   uint32_t nq = 0, cnt[2] = {0, 0};  // row tiles used; tiles of each stream
   int turn = 0;                      // the stream whose turn it is
   if (!c.work) return;
@@ -295,7 +318,7 @@ __device__ void s_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
     const bool two = two_tiles(p, g);
     for (int j = g.t0; j < g.t1; ++j) {
       if (!wait_all(c, B_FULL + r.st, r.par_own)) return;
-      const uint32_t kb = sm + S::kOffKV + r.st * S::kTileBytes;
+      const uint32_t kb = sm + S::kOffKV + r.st * S::kStageBytes;
 #pragma unroll 1
       for (int y = 0; y < (two ? 2 : 1); ++y) {
         const int x = two ? y : turn;  // the stream
@@ -339,7 +362,8 @@ __device__ void pv_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   constexpr uint32_t kIdesc = idesc_f16kind(128, D, 1, FP8 ? 0 : 1);
   const int lane = threadIdx.x & 31;
   const uint32_t elect = lane == 0;
-  Ring r(p, 1);
+  Ring<FP8> r(p, 1);
+  uint32_t wide = 0;  // e4m3: V tiles so far
   uint32_t cnt[2] = {0, 0}, seg = 0;
   int turn = 0;
   if (!c.work) return;
@@ -348,8 +372,11 @@ __device__ void pv_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   for (; walk.next(p, g); ++seg) {
     const bool two = two_tiles(p, g);
     for (int j = g.t0; j < g.t1; ++j) {
-      if (!wait_all(c, (FP8 ? B_CONV : B_FULL + kStages) + r.st, r.par_own)) return;
-      uint8_t* v = c.sm + S::kOffKV + r.st * S::kTileBytes;
+      if (!(FP8 ? wait_all(c, B_WIDE + (wide & 1), (wide >> 1) & 1)
+                : wait_all(c, B_FULL + kMostStages + r.st, r.par_own)))
+        return;
+      uint8_t* v = c.sm + (FP8 ? S::kOffWide + (wide & 1) * S::kTileBytes
+                               : S::kOffKV + r.st * S::kStageBytes);
       if constexpr (!FP8) {  // (the converters do it over e4m3 pools)
         // rows of the last block past the sequence's end: zeros (whole blocks past it are)
         const int lim = g.n - (g.kv0 + j * kBN);
@@ -391,25 +418,28 @@ __device__ void pv_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
         if (x) ++cnt[1]; else ++cnt[0];
       }
       if (!two) turn ^= 1;
-      mma_commit(c.bar + B_EMPTY + r.st);
+      mma_commit(c.bar + (FP8 ? B_WFREE + (wide & 1) : B_EMPTY + r.st));
       __syncwarp();
-      r.next();
+      if constexpr (FP8)
+        ++wide;
+      else
+        r.next();
     }
   }
 }
 
-// Widen a staged tile of 128 x 128 codes to f16, in place: the codes lie in the second dim half's
-// 16 KB, in rows of 128 bytes with the 128-byte swizzle.  A warp takes rows 32 w .. 32 w + 31, 16 at a
-// time, and has loaded their codes before it stores over them.  Rows at or past `lim` become zeros.
-__device__ __forceinline__ void widen_rows(uint8_t* tile, int w, int lane, int lim) {
+// Widen a staged tile of 128 x 128 codes (rows of 128 bytes with the 128-byte swizzle) to f16, dim
+// half by dim half.  A warp takes rows 32 w .. 32 w + 31, 16 at a time.  Rows at or past `lim`
+// become zeros.
+__device__ __forceinline__ void widen_rows(const uint8_t* codes, uint8_t* tile, int w, int lane,
+                                           int lim) {
   constexpr int kHalf = 128 * 128;
 #pragma unroll 1
   for (int r0 = 32 * w; r0 < 32 * w + 32; r0 += 16) {
     uint4 src[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      src[i] = *reinterpret_cast<const uint4*>(tile + kHalf + r0 * 128 + (lane + 32 * i) * 16);
-    __syncwarp();
+      src[i] = *reinterpret_cast<const uint4*>(codes + r0 * 128 + (lane + 32 * i) * 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int ch = lane + 32 * i, r = r0 + (ch >> 3), sw = r & 7;
@@ -488,8 +518,8 @@ template <int D>
 __device__ void converter(const Ctx& c, const TreeParams& p) {
   using S = Shape<D, true>;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 12;
-  Ring r(p, 1);
-  uint32_t nq = 0;
+  Ring<true> r(p, 1);
+  uint32_t nq = 0, wide = 0;
   if (!c.work) return;
   TreeWalk walk(p, blockIdx.x);
   TreeSegment g;
@@ -505,11 +535,18 @@ __device__ void converter(const Ctx& c, const TreeParams& p) {
       if (lane == 0) mbar_arrive(c.bar + B_QCONV + (nq & 1));
     }
     for (int j = g.t0; j < g.t1; ++j) {
-      if (!wait_all(c, B_FULL + kStages + r.st, r.par_own)) return;
-      widen_rows(c.sm + S::kOffKV + r.st * S::kTileBytes, w, lane, g.n - (g.kv0 + j * kBN));
+      const uint32_t x = wide & 1;
+      if (!wait_all(c, B_WFREE + x, ((wide >> 1) & 1) ^ 1)) return;
+      if (!wait_all(c, B_FULL + kMostStages + r.st, r.par_own)) return;
+      widen_rows(c.sm + S::kOffKV + r.st * S::kStageBytes, c.sm + S::kOffWide + x * S::kTileBytes, w,
+                 lane, g.n - (g.kv0 + j * kBN));
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(c.bar + B_CONV + r.st);
+      if (lane == 0) {
+        mbar_arrive(c.bar + B_EMPTY + r.st);
+        mbar_arrive(c.bar + B_WIDE + x);
+      }
+      ++wide;
       r.next();
     }
   }
@@ -835,12 +872,14 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     flags[1] = 0;
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
-      if ((i >= B_QCONV && i < B_QCONV + 2) || (i >= B_CONV && i < B_CONV + kStages)) n = 4;
+      if ((i >= B_QCONV && i < B_QCONV + 2) || (i >= B_WIDE && i < B_WIDE + 2)) n = 4;
+      // e4m3: four warps read V's codes
+      if (FP8 && i >= B_EMPTY + kCodeStages && i < B_EMPTY + 2 * kCodeStages) n = 4;
       if (i >= B_PFULL && i < B_PFULL + 2) n = 4;
       if (i >= B_OFREE && i < B_OFREE + 2) n = 4;
       mbar_init(bar + i, n);
     }
-    if (ring_ahead(p)) mbar_arrive(bar + B_EMPTY + 1);
+    if (!FP8 && ring_ahead(p)) mbar_arrive(bar + B_EMPTY + 1);
     prefetch_tmap(&tq);
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
