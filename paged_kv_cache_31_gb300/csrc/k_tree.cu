@@ -435,16 +435,19 @@ template <typename TQ, bool VEC, int DK, int R>
 __global__ void __launch_bounds__(256) k_tree_merge(const TreeParams p) {
   constexpr int E = 4 * DK;  // a lane's values of a row
   const VarlenMeta& m = p.m;
+  const int b = blockIdx.x, lane = threadIdx.x & 31;
+  // The plan is read before the wait: the attention kernel let this one start only after the
+  // planning kernel's end.  (After a failed plan there is anything in it: it is not used as an
+  // index before the status is known.)
+  const int4 cut = __ldcg(&p.starts[b + 1]), from = __ldcg(&p.starts[b]);
+  const bool in = cut.x >= 0 && cut.x < m.num_seqs;
+  const int4 q = in ? __ldcg(&p.seqs[2 * cut.x]) : make_int4(0, 0, 0, 0);
   pdl_wait();
   pdl_launch_dependents();
-  const int b = blockIdx.x, lane = threadIdx.x & 31;
-  const int skip = status_set(p.status);
-  const int4 cut = p.starts[b + 1], from = p.starts[b];
-  if (__syncthreads_or(skip)) return;  // (one answer for the whole CTA)
-  if (cut.x >= m.num_seqs || cut.w == 0) return;
+  if (__syncthreads_or(status_set(p.status))) return;  // (one answer for the whole CTA)
+  if (!in || cut.w == 0) return;
   const bool same = from.x == cut.x && from.y == cut.y && from.z == cut.z;
   if (same && from.w > 0) return;  // a later cut of the item
-  const int4 q = p.seqs[2 * cut.x];
   const int kvh = cut.y, row0 = cut.z * p.rows_per_item;
   const int rows = min(p.rows_per_item, q.y * m.group - row0);
   const int row = (blockIdx.y * 8 + (threadIdx.x >> 5)) * R;
