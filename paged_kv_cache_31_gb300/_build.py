@@ -4,6 +4,8 @@ Each translation unit under csrc/ is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a`` and linked into
 ``paged_kv_cache_31_gb300/libpa.so`` (static CUDA runtime; the driver's tensor-map
 encoder is reached through cudaGetDriverEntryPointByVersion, so libcuda is not linked).
+csrc/pa_calls.cpp (host code over torch's C++ headers) becomes the Python module ``_calls.so``
+next to it, which is linked to libpa.so.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpa.so")
+CALLS = os.path.join(PKG, "_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]
@@ -36,15 +40,45 @@ def sources():
 
 
 def _deps():
-    return sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
+    return sources() + [os.path.join(CSRC, "pa_calls.cpp")] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
         os.path.join(INCLUDE, "pa.h")]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _compile_calls(nvcc: str) -> str:
+    import torch
+
+    obj = os.path.join(BUILD, "pa_calls.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    inside = os.path.join(os.path.dirname(torch.__file__), "include")
+    inc = [sysconfig.get_paths()["include"], inside, cuda]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, *(f for i in inc for f in ("-isystem", i)),
+           "-c", os.path.join(CSRC, "pa_calls.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on pa_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    import torch
+
+    tmp = CALLS + f".tmp{os.getpid()}"
+    libs = ["-L", os.path.join(os.path.dirname(torch.__file__), "lib")]
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libpa.so", "-Wl,-rpath,$ORIGIN", *libs,
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -64,14 +98,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    workers = max(1, min(len(srcs) + 1, os.cpu_count() or 4))
+    with concurrent.futures.ThreadPoolExecutor(max_workers=workers) as ex:
+        calls = ex.submit(_compile_calls, nvcc)
         objs = list(ex.map(compile_one, srcs))
+        calls = calls.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_calls(calls)
     return LIB
 
 

@@ -4,6 +4,8 @@ Each ``pa_*`` function takes torch tensors that live on the current CUDA device,
 checks their shapes / dtypes / contiguity, passes raw pointers and the current
 stream to the library, and raises ``PaError`` on a non-OK status.  It does no
 arithmetic of its own: every step of the path runs in the library's kernels.
+The speculative-decoding calls have their checks in the compiled module ``_calls``
+(csrc/pa_calls.cpp), as ctypes took longer than their kernels.
 Importing this module loads the library and raises if it has not been built
 (``python -c "import __graft_entry__ as g; g.build()"``); there is no fallback.
 """
@@ -22,12 +24,13 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
+from . import _calls  # noqa: E402  (linked to libpa.so)
+
 PA_OK, PA_EINVAL, PA_ESHAPE, PA_EUNSUPPORTED, PA_ECUDA, PA_ETIMEOUT = range(6)
 PA_F32, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
 PA_FLAG_BITWISE = 1
 _DT = {torch.float32: PA_F32, torch.bfloat16: PA_BF16, torch.float8_e4m3fn: PA_FP8_E4M3}
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
 _vp, _i32, _i64, _f32, _sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                               ctypes.c_size_t)
 _SIGS = {
@@ -539,38 +542,6 @@ class _RopeScaling(ctypes.Structure):
         "high_freq_factor")]
 
 
-def _arrays(dev, *ts):
-    """Contiguous tensors (or None) on CUDA device `dev`."""
-    for t in ts:
-        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
-            raise ValueError("tensors must be contiguous and live on the current CUDA device")
-
-
-def _ints(dev, *ts):
-    """Contiguous int32 tensors on CUDA device `dev`."""
-    for t in ts:
-        if t.get_device() != dev or t.dtype is not torch.int32 or not t.is_contiguous():
-            raise ValueError("metadata tensors must be contiguous int32 tensors on the current "
-                             "CUDA device")
-
-
-def _a(t):
-    return None if t is None else t.data_ptr()
-
-
-def _on(dev, stream):
-    return _raw_stream(dev) if stream is None else stream.cuda_stream
-
-
-def _scratch(nbytes, dev, stream):
-    """Memory of one call, from the pool of the stream that the call goes to: memory of another
-    stream's pool may still be in use by what that stream has queued."""
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
-
-
 def pa_rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0,
                         original_max_position=0, beta_fast=32.0, beta_slow=1.0,
                         low_freq_factor=1.0, high_freq_factor=4.0, device="cuda"):
@@ -588,14 +559,6 @@ def pa_rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0,
     return f.to(device), af.value
 
 
-def _token_rows(t, N, D, what):
-    """Elements between the tokens of [T, N, D] rows whose heads are contiguous."""
-    a, b, c = t.stride()
-    if (c != 1 and D > 1) or (b != D and N > 1):
-        raise ValueError(f"{what}: a token's heads must be contiguous")
-    return a if len(t) > 1 else N * D
-
-
 def pa_rope_and_cache(q, k, v, q_out, k_blocks, v_blocks, positions, slot_mapping, inv_freq,
                       interleaved=False, attn_factor=1.0, k_scale=1.0, v_scale=1.0, k_scales=None,
                       v_scales=None, stream=None):
@@ -603,46 +566,9 @@ def pa_rope_and_cache(q, k, v, q_out, k_blocks, v_blocks, positions, slot_mappin
     [T, Hkv, D], and the scatter of k and v into the pools at slot_mapping.  The tokens of q, k, v
     and q_out may be strided (views of one fused product).  inv_freq: fp64 [rotary_dim / 2]
     (pa_rope_frequencies); scales as in pa_reshape_and_cache."""
-    dev = torch.cuda.current_device()
-    if (q is None) != (q_out is None):
-        raise ValueError("give both q and q_out or neither")
-    for t in (k, v) if q is None else (q, k, v, q_out):
-        if t.get_device() != dev or t.dim() != 3:
-            raise ValueError("q, k, v and q_out must be [T, heads, D] tensors on the current CUDA "
-                             "device")
-    _arrays(dev, k_blocks, v_blocks, inv_freq)
-    _ints(dev, positions, slot_mapping)
-    kv_shape, pool_shape, src, kv = k.shape, k_blocks.shape, k.dtype, k_blocks.dtype
-    if v.shape != kv_shape or len(pool_shape) != 4 or v_blocks.shape != pool_shape:
-        raise ValueError("k, v must be [T, Hkv, D]; pools [NB, b, Hkv, D]")
-    if v.dtype != src or v_blocks.dtype != kv:
-        raise ValueError("k and v (and the two pools) must share one dtype")
-    T, Hkv, D = kv_shape
-    NB, bs, Hkv2, D2 = pool_shape
-    if Hkv != Hkv2 or D != D2:
-        raise ValueError("kv heads / head size differ between rows and pool")
-    if positions.numel() != T or slot_mapping.numel() != T:
-        raise ValueError("positions and slot_mapping must be [T]")
-    H = q_ptr = out_ptr = q_rows = out_rows = 0
-    if q is not None:
-        q_shape = q.shape
-        if q_shape[0] != T or q_shape[2] != D or q_out.shape != q_shape or q.dtype != src \
-                or q_out.dtype != src:
-            raise ValueError("q and q_out must be [T, H, D] of the rows' dtype")
-        H = q_shape[1]
-        q_ptr, q_rows = q.data_ptr(), _token_rows(q, H, D, "q")
-        out_ptr, out_rows = q_out.data_ptr(), _token_rows(q_out, H, D, "q_out")
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be fp64 [rotary_dim / 2]")
-    if k_scales is not None or v_scales is not None:
-        _arrays(dev, k_scales, v_scales)
-        _head_scales(Hkv, k_scales, v_scales)
-    _check(_lib.pa_rope_and_cache(
-        q_ptr, q_rows, out_ptr, out_rows, k.data_ptr(), _token_rows(k, Hkv, D, "k"), v.data_ptr(),
-        _token_rows(v, Hkv, D, "v"), k_blocks.data_ptr(), v_blocks.data_ptr(),
-        positions.data_ptr(), slot_mapping.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel(),
-        bool(interleaved), attn_factor, T, H, Hkv, D, bs, NB, _DT[src], _DT[kv], k_scale, v_scale,
-        _a(k_scales), _a(v_scales), _on(dev, stream)), "pa_rope_and_cache")
+    _check(_calls.rope_and_cache(q, k, v, q_out, k_blocks, v_blocks, positions, slot_mapping, inv_freq,
+                                 interleaved, attn_factor, k_scale, v_scale, k_scales, v_scales,
+                                 stream), "pa_rope_and_cache")
     return q_out
 
 
@@ -660,53 +586,11 @@ def pa_tree_attention(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, pos
     query_start_loc[s] cached positions) over its context and the nodes of their tree_mask rows:
     int32 [T, mask_words], bit i of a row = node i of the token's sequence.  sinks, lse and scales
     as in pa_varlen_forward."""
-    dev = torch.cuda.current_device()
-    _arrays(dev, q, k_blocks, v_blocks, out, workspace, sinks, lse)
-    _ints(dev, query_start_loc, seq_lens, positions, tree_mask, block_tables)
-    q_shape, pool_shape, src, kv = q.shape, k_blocks.shape, q.dtype, k_blocks.dtype
-    if len(q_shape) != 3 or out.shape != q_shape or out.dtype != src:
-        raise ValueError("q and out must be [T, H, D] of one dtype")
-    if len(pool_shape) != 4 or v_blocks.shape != pool_shape or v_blocks.dtype != kv:
-        raise ValueError("k_blocks and v_blocks must match")
-    T, H, D = q_shape
-    NB, bs, Hkv, D2 = pool_shape
-    S = query_start_loc.numel() - 1
-    mask_shape, table_shape = tree_mask.shape, block_tables.shape
-    if D2 != D:
-        raise ValueError("head size differs between q and the pool")
-    if len(mask_shape) != 2 or mask_shape[0] != T or positions.numel() != T:
-        raise ValueError("tree_mask must be [T, mask_words] and positions [T]")
-    if seq_lens.numel() != S or len(table_shape) != 2 or table_shape[0] != S:
-        raise ValueError("seq_lens must be [S] and block_tables [S, max_blocks]")
-    if sinks is not None and (sinks.dtype != torch.float32 or sinks.shape != (H,)):
-        raise ValueError("sinks must be a contiguous fp32 [num_heads] tensor")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (H, T)):
-        raise ValueError("lse must be a contiguous fp32 [num_heads, num_tokens] tensor")
-    if k_scales is not None or v_scales is not None:
-        _arrays(dev, k_scales, v_scales)
-        _head_scales(Hkv, k_scales, v_scales)
-    if workspace is None:
-        nbytes = _lib.pa_tree_attention_workspace_size(S, T, H, Hkv, D, table_shape[1], bs)
-        workspace = _scratch(nbytes, dev, stream)
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
-    _check(_lib.pa_tree_attention(
-        q.data_ptr(), k_blocks.data_ptr(), v_blocks.data_ptr(), out.data_ptr(),
-        query_start_loc.data_ptr(), seq_lens.data_ptr(), positions.data_ptr(),
-        tree_mask.data_ptr(), block_tables.data_ptr(), S, T, mask_shape[1], H, Hkv, D, bs, NB,
-        table_shape[1], _DT[src], _DT[kv], scale, int(sliding_window), _a(sinks), _a(lse), k_scale,
-        v_scale, _a(k_scales), _a(v_scales), workspace.data_ptr(), nbytes, _on(dev, stream)),
-        "pa_tree_attention")
+    _check(_calls.tree_attention(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, positions,
+                                 tree_mask, block_tables, scale, sliding_window, workspace, stream,
+                                 sinks, lse, k_scale, v_scale, k_scales, v_scales),
+           "pa_tree_attention")
     return out
-
-
-def _pools(k_blocks, v_blocks):
-    if k_blocks.dim() != 4 or k_blocks.dtype not in _DT:
-        raise ValueError("pools must be [NB, b, Hkv, D]")
-    if v_blocks is not None and (k_blocks.shape != v_blocks.shape
-                                 or k_blocks.dtype != v_blocks.dtype):
-        raise ValueError("k_blocks and v_blocks must match")
-    return k_blocks.shape
 
 
 def pa_tree_commit(k_blocks, v_blocks, block_tables, context_lens, accepted, num_accepted,
@@ -714,94 +598,47 @@ def pa_tree_commit(k_blocks, v_blocks, block_tables, context_lens, accepted, num
     """Move the K and V rows of the accepted nodes (accepted [S, max_accepted], the first
     num_accepted[s] of a row, strictly increasing) of each sequence's tree, which begins at
     position context_lens[s], to its first positions."""
-    dev = torch.cuda.current_device()
-    _arrays(dev, k_blocks, v_blocks)
-    _ints(dev, block_tables, context_lens, accepted, num_accepted)
-    NB, bs, Hkv, D = _pools(k_blocks, v_blocks)
-    if accepted.dim() != 2 or block_tables.dim() != 2:
-        raise ValueError("accepted must be [S, max_accepted], block_tables [S, max_blocks]")
-    S, A = accepted.shape
-    if context_lens.numel() != S or num_accepted.numel() != S or block_tables.shape[0] != S:
-        raise ValueError("context_lens and num_accepted must be [S]")
-    _check(_lib.pa_tree_commit(_a(k_blocks), _a(v_blocks), _a(block_tables), _a(context_lens),
-                               _a(accepted), _a(num_accepted), S, A, Hkv, D, bs, NB,
-                               block_tables.shape[1], _DT[k_blocks.dtype], _on(dev, stream)),
-           "pa_tree_commit")
+    _check(_calls.tree_commit(k_blocks, v_blocks, block_tables, context_lens, accepted, num_accepted,
+                              stream), "pa_tree_commit")
 
 
 def pa_copy_blocks(k_blocks, v_blocks, block_pairs, stream=None):
     """Copy whole blocks of both pools (v_blocks may be None) for every (src, dst) of block_pairs
     [n, 2]; (-1, -1) is skipped."""
-    dev = torch.cuda.current_device()
-    _arrays(dev, k_blocks, v_blocks)
-    _ints(dev, block_pairs)
-    NB, bs, Hkv, D = _pools(k_blocks, v_blocks)
-    if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
-        raise ValueError("block_pairs must be [n, 2]")
-    _check(_lib.pa_copy_blocks(_a(k_blocks), _a(v_blocks), _a(block_pairs), block_pairs.shape[0],
-                               Hkv, D, bs, NB, _DT[k_blocks.dtype], _on(dev, stream)),
-           "pa_copy_blocks")
-
-
-def _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, *lists):
-    dev = torch.cuda.current_device()
-    _ints(dev, block_tables, seq_lens, ref_counts, free_list, free_count, *lists)
-    if block_tables.dim() != 2 or seq_lens.numel() != block_tables.shape[0]:
-        raise ValueError("block_tables must be [rows, max_blocks] and seq_lens [rows]")
-    if free_list.numel() != ref_counts.numel() or free_count.numel() != 1:
-        raise ValueError("ref_counts and free_list must be [num_blocks], free_count [1]")
-    if any(x.numel() != lists[0].numel() for x in lists):
-        raise ValueError("the lists must have one length")
-    return dev
+    _check(_calls.copy_blocks(k_blocks, v_blocks, block_pairs, stream), "pa_copy_blocks")
 
 
 def pa_fork_sequences(block_tables, seq_lens, parents, children, ref_counts, free_list, free_count,
                       block_size, block_pairs=None, stream=None):
     """Make row children[f] a copy of row parents[f] that shares its whole blocks; returns
     block_pairs [n, 2], the partly filled blocks to copy with pa_copy_blocks."""
-    dev = _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, parents, children)
-    n = parents.numel()
     if block_pairs is None:
-        block_pairs = _scratch(8 * n, dev, stream).view(torch.int32).view(n, 2)
-    _ints(dev, block_pairs)
-    if block_pairs.shape != (n, 2):
-        raise ValueError("block_pairs must be [n, 2]")
-    _check(_lib.pa_fork_sequences(_a(block_tables), _a(seq_lens), _a(parents), _a(children), n,
-                                  block_tables.shape[0], block_tables.shape[1], int(block_size),
-                                  _a(ref_counts), _a(free_list), _a(free_count),
-                                  ref_counts.numel(), _a(block_pairs), _on(dev, stream)),
-           "pa_fork_sequences")
+        # (from the pool of the call's stream: memory of another's may still be in use there)
+        with torch.cuda.stream(stream):
+            block_pairs = torch.empty(parents.numel(), 2, dtype=torch.int32,
+                                      device=block_tables.device)
+    _check(_calls.fork_sequences(block_tables, seq_lens, parents, children, ref_counts, free_list,
+                                 free_count, block_size, block_pairs, stream), "pa_fork_sequences")
     return block_pairs
 
 
 def pa_grow_sequences(block_tables, seq_lens, sequences, new_lens, ref_counts, free_list,
                       free_count, block_size, stream=None):
     """Lengthen the rows `sequences` to new_lens, taking the blocks they need."""
-    dev = _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, sequences,
-                       new_lens)
-    _check(_lib.pa_grow_sequences(_a(block_tables), _a(seq_lens), _a(sequences), _a(new_lens),
-                                  sequences.numel(), block_tables.shape[0], block_tables.shape[1],
-                                  int(block_size), _a(ref_counts), _a(free_list), _a(free_count),
-                                  ref_counts.numel(), _on(dev, stream)), "pa_grow_sequences")
+    _check(_calls.grow_sequences(block_tables, seq_lens, sequences, new_lens, ref_counts, free_list,
+                                 free_count, block_size, stream), "pa_grow_sequences")
 
 
 def pa_trim_sequences(block_tables, seq_lens, sequences, new_lens, ref_counts, free_list,
                       free_count, block_size, stream=None):
     """Shorten the rows `sequences` to new_lens, giving back the blocks behind."""
-    dev = _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, sequences,
-                       new_lens)
-    _check(_lib.pa_trim_sequences(_a(block_tables), _a(seq_lens), _a(sequences), _a(new_lens),
-                                  sequences.numel(), block_tables.shape[0], block_tables.shape[1],
-                                  int(block_size), _a(ref_counts), _a(free_list), _a(free_count),
-                                  ref_counts.numel(), _on(dev, stream)), "pa_trim_sequences")
+    _check(_calls.trim_sequences(block_tables, seq_lens, sequences, new_lens, ref_counts, free_list,
+                                 free_count, block_size, stream), "pa_trim_sequences")
 
 
 def pa_free_sequences(block_tables, seq_lens, sequences, ref_counts, free_list, free_count,
                       block_size, stream=None):
     """End the rows `sequences`: their blocks lose a reference each, and those without any go
     back to the free list in ascending order."""
-    dev = _page_arrays(block_tables, seq_lens, ref_counts, free_list, free_count, sequences)
-    _check(_lib.pa_free_sequences(_a(block_tables), _a(seq_lens), _a(sequences),
-                                  sequences.numel(), block_tables.shape[0], block_tables.shape[1],
-                                  int(block_size), _a(ref_counts), _a(free_list), _a(free_count),
-                                  ref_counts.numel(), _on(dev, stream)), "pa_free_sequences")
+    _check(_calls.free_sequences(block_tables, seq_lens, sequences, ref_counts, free_list,
+                                 free_count, block_size, stream), "pa_free_sequences")
