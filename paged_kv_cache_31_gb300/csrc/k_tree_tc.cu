@@ -71,7 +71,14 @@ struct Shape {
   static constexpr int kOffMisc = kOffBar + 40 * 8;
   // tensor-memory base, flags; e4m3: the rows' scale exponents of four Q tiles
   static constexpr int kOffExp = kOffMisc + 16;
-  static constexpr int kSmem = kOffExp + (FP8 ? 4 * 128 : 0);
+  static constexpr int kOffSeg = kOffExp + (FP8 ? 4 * 128 : 0);  // clusters: the CTA's TreeSegment
+  static constexpr int kSmem = kOffSeg + 64;
+  // clusters: a CTA's state in the ring's place, once that is used up: O, rows padded by 16 bytes
+  // (a warp's rows hit different banks), then (m, l)
+  static constexpr int kStateLd = D + 4;
+  static constexpr int kOffState = kOffKV;
+  static constexpr int kOffML = kOffState + 256 * kStateLd * 4;
+  static_assert(kOffML + 256 * 8 <= kOffX, "the state lies in the ring");
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
@@ -144,6 +151,26 @@ struct Ctx {
   int* status;
   uint64_t limit;
   bool work;  // false: an earlier error, nothing is done
+  const TreeSegment* own;  // clusters: the CTA's part of its cluster's item
+};
+
+// The segments of a CTA: its share's, or the one it has in its cluster (CL).
+template <bool CL>
+struct Walk {
+  TreeWalk w;
+  __device__ __forceinline__ Walk(const Ctx& c, const TreeParams& p) : w(p, blockIdx.x) {}
+  __device__ __forceinline__ bool next(const TreeParams& p, TreeSegment& g) { return w.next(p, g); }
+};
+template <>
+struct Walk<true> {
+  const TreeSegment* own;
+  __device__ __forceinline__ Walk(const Ctx& c, const TreeParams& p) : own(c.own) {}
+  __device__ __forceinline__ bool next(const TreeParams& p, TreeSegment& g) {
+    if (!own) return false;
+    g = *own;
+    own = nullptr;
+    return g.t1 > g.t0;
+  }
 };
 
 __device__ __forceinline__ bool wait_bar(const Ctx& c, int idx, uint32_t parity) {
@@ -234,7 +261,7 @@ __device__ __forceinline__ bool two_tiles(const TreeParams& p, const TreeSegment
 // Warp 0 brings K (kv = 0), warp 3 Q and V (kv = 1); both walk the whole share.  A block is one
 // box, issued by a lane of its own: a warp's TMA instructions go out one lane after the other,
 // and one warp issuing 32 half-size boxes per key tile was what bound this kernel.
-template <int D, bool FP8>
+template <int D, bool FP8, bool CL>
 __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* tkv,
                          const CUtensorMap* tq, int kv) {
   using S = Shape<D, FP8>;
@@ -243,7 +270,7 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
   Ring<FP8> r(p, kv);
   uint32_t issued = 0, nq = 0;  // this warp's stages; row tiles of Q (tile n uses buffer n % 2)
   bool ok = c.work;
-  TreeWalk walk(p, blockIdx.x);
+  Walk<CL> walk(c, p);
   TreeSegment g;
   while (ok && walk.next(p, g)) {
     const int32_t* row = p.m.block_tables + (int64_t)g.s * p.m.max_blocks;
@@ -301,7 +328,7 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
   __syncwarp();
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool CL>
 __device__ void s_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   using S = Shape<D, FP8>;
   // (f8f6f4's descriptor has zeros where e4m3 operands are named)
@@ -312,7 +339,7 @@ __device__ void s_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   uint32_t nq = 0, cnt[2] = {0, 0};  // row tiles used; tiles of each stream
   int turn = 0;                      // the stream whose turn it is
   if (!c.work) return;
-  TreeWalk walk(p, blockIdx.x);
+  Walk<CL> walk(c, p);
   TreeSegment g;
   while (walk.next(p, g)) {
     const bool two = two_tiles(p, g);
@@ -356,7 +383,7 @@ __device__ void s_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   }
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool CL>
 __device__ void pv_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   using S = Shape<D, FP8>;
   constexpr uint32_t kIdesc = idesc_f16kind(128, D, 1, FP8 ? 0 : 1);
@@ -367,7 +394,7 @@ __device__ void pv_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   uint32_t cnt[2] = {0, 0}, seg = 0;
   int turn = 0;
   if (!c.work) return;
-  TreeWalk walk(p, blockIdx.x);
+  Walk<CL> walk(c, p);
   TreeSegment g;
   for (; walk.next(p, g); ++seg) {
     const bool two = two_tiles(p, g);
@@ -514,14 +541,14 @@ __device__ __forceinline__ void split_q(uint8_t* tile, int8_t* exps, int w, int 
 }
 
 // Warps 12 to 15 split Q and widen V, a quarter of every tile each.  K is used as it is.
-template <int D>
+template <int D, bool CL>
 __device__ void converter(const Ctx& c, const TreeParams& p) {
   using S = Shape<D, true>;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 12;
   Ring<true> r(p, 1);
   uint32_t nq = 0, wide = 0;
   if (!c.work) return;
-  TreeWalk walk(p, blockIdx.x);
+  Walk<CL> walk(c, p);
   TreeSegment g;
   while (walk.next(p, g)) {
     const int tiles = two_tiles(p, g) ? 2 : 1;
@@ -632,8 +659,179 @@ __device__ __forceinline__ void state_taken(int par) {
   asm volatile("bar.sync %0, 256;" ::"r"(1 + par) : "memory");
 }
 
-// The streams' threads: warpgroup x (warps 4 + 4x ..), thread = row = tensor-memory lane.
+// ---- small calls: a cluster for each item -------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\t"
+      "barrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+// Address, in the cluster's shared window, of p's counterpart in CTA `rank`.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ uint32_t peer_load(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 peer_load2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_load4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// One warp: this CTA's part of its cluster's item.  An item that the batch does not have, or
+// whose sequence's numbers cannot be used as indices, has no rows and no tiles.
+__device__ __forceinline__ void plan_own(const TreeParams& p, TreeSegment* out, int lane) {
+  const VarlenMeta& m = p.m;
+  const int rank = blockIdx.x % p.cluster;
+  int u = blockIdx.x / p.cluster;
+  TreeSegment g;
+  g.kvh = u % m.num_kv_heads;
+  u /= m.num_kv_heads;
+  g.item = u % p.items;
+  g.s = u / p.items;
+  g.row0 = g.item * p.rows_per_item;
+  g.qs = m.query_start_loc[g.s];
+  const int qe = m.query_start_loc[g.s + 1];
+  g.n = m.seq_lens[g.s];
+  g.nodes = g.rows = g.kv0 = g.t0 = g.t1 = 0;
+  g.slot = p.cluster > 1 ? 0 : -1;
+  if (g.qs >= 0 && qe > g.qs && (int64_t)qe <= m.num_tokens && qe - g.qs <= 32 * (int64_t)p.mask_words &&
+      g.n >= qe - g.qs && ((int64_t)g.n + 15) / 16 <= m.max_blocks) {
+    g.nodes = qe - g.qs;
+    const int rows = g.nodes * m.group;
+    if (g.row0 < rows) {
+      g.rows = min(p.rows_per_item, rows - g.row0);
+      if (m.window > 0) {
+        int lo = INT_MAX;
+        for (int t = lane; t < g.nodes; t += 32) lo = min(lo, m.positions[g.qs + t]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) lo = min(lo, __shfl_xor_sync(kFull, lo, o));
+        g.kv0 = min(max(max(lo, 0) - m.window + 1, 0), g.n - g.nodes);
+        g.kv0 -= g.kv0 % 16;
+      }
+      const int tiles = (g.n - g.kv0 + kBN - 1) / kBN;
+      g.t0 = (int)((int64_t)tiles * rank / p.cluster);
+      g.t1 = (int)((int64_t)tiles * (rank + 1) / p.cluster);
+    }
+  }
+  if (lane == 0) *out = g;
+}
+
+// Whether this thread (of 256) finds the batch not valid; what k_tree_plan checks.
+__device__ __forceinline__ bool batch_refused(const TreeParams& p, int tid) {
+  const VarlenMeta& m = p.m;
+  bool bad = false;
+  for (int g = tid; g < m.num_kv_heads; g += 256) {
+    const float a = m.k_scales ? m.k_scales[g] : 1.f, b = m.v_scales ? m.v_scales[g] : 1.f;
+    bad |= !(a > 0.f && a <= 3.402823466e38f) || !(b > 0.f && b <= 3.402823466e38f);
+  }
+  for (int s = tid; s < m.num_seqs; s += 256) {
+    const int qs = m.query_start_loc[s], qe = m.query_start_loc[s + 1], n = m.seq_lens[s];
+    bad |= qs < 0 || qe < qs || (int64_t)qe > m.num_tokens || (s == 0 && qs != 0) ||
+           (s == m.num_seqs - 1 && (int64_t)qe != m.num_tokens);
+    if (qe > qs)
+      bad |= n < (int64_t)qe - qs || (int64_t)qe - qs > 32 * (int64_t)p.mask_words ||
+             ((int64_t)n + 15) / 16 > m.max_blocks;
+  }
+  if (m.window > 0)
+    for (int64_t t = tid; t < m.num_tokens; t += 256) bad |= m.positions[t] < 0;
+  const int per = (m.max_blocks + 31) / 32;  // 32 entries of a table row: a warp's
+  for (int i = tid >> 5; i < m.num_seqs * per; i += 8) {
+    const int s = i / per, e = i % per * 32 + (tid & 31);
+    const int qs = m.query_start_loc[s], qe = m.query_start_loc[s + 1], n = m.seq_lens[s];
+    if (qe <= qs || n < 1) continue;
+    if (e < (int)min(((int64_t)n + 15) / 16, (int64_t)m.max_blocks)) {
+      const int id = m.block_tables[(int64_t)s * m.max_blocks + e];
+      bad |= id < 0 || (int64_t)id >= m.num_blocks;
+    }
+  }
+  return bad;
+}
+
+// The eight softmax warps, after the cluster's barrier: the CTA's share of its item's rows, from
+// all CTAs' states in key order.
 template <int D, bool FP8>
+__device__ void cluster_merge(const Ctx& c, const TreeParams& p) {
+  using S = Shape<D, FP8>;
+  constexpr int E = D / 32;  // a lane's values of a row
+  const VarlenMeta& m = p.m;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 4, C = p.cluster;
+  const TreeSegment& g = *c.own;
+  // (a failed wait in any CTA, or a batch that is not valid: nothing is written)
+  const bool failed = lane < C && peer_load(peer_addr(const_cast<int*>(c.abort), lane)) != 0;
+  if (__any_sync(kFull, failed)) return;
+  const uint32_t ml = peer_addr(c.sm + S::kOffML, min(lane, C - 1));
+  const uint32_t o = smem_u32(c.sm + S::kOffState) + lane * E * 4;
+  for (int r = (int)cluster_rank() + C * warp; r < g.rows; r += 8 * C) {
+    float2 st = make_float2(-INFINITY, 0.f);
+    if (lane < C) st = peer_load2(ml + r * 8);
+    float M = st.x;
+#pragma unroll
+    for (int k = 1; k < 8; k <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, k));
+    const float w = st.x == -INFINITY ? 0.f : exp2f(st.x - M);
+    float L = w * st.y;
+#pragma unroll
+    for (int k = 1; k < 8; k <<= 1) L += __shfl_xor_sync(kFull, L, k);
+    M = __shfl_sync(kFull, M, 0);
+    L = __shfl_sync(kFull, L, 0);
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < C && __shfl_sync(kFull, w, k) > 0.f) {  // (a CTA without a tile left no row)
+        uint32_t a;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(o + r * S::kStateLd * 4), "r"(k));
+        if constexpr (E == 4) {
+          v[k] = peer_load4(a);
+        } else {
+          const float2 h = peer_load2(a);
+          v[k].x = h.x;
+          v[k].y = h.y;
+        }
+      }
+    }
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float wk = __shfl_sync(kFull, w, k);
+      acc[0] += wk * v[k].x;
+      acc[1] += wk * v[k].y;
+      acc[2] += wk * v[k].z;
+      acc[3] += wk * v[k].w;
+    }
+    const int R = g.row0 + r, tok = g.qs + R / m.group, h = g.kvh * m.group + R % m.group;
+    const float f = tree_finish(p, g.kvh, h, tok, M, L, lane == 0);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)tok * m.num_heads + h) * D + lane * E;
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(out) =
+          make_uint2(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f));
+    else
+      *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * f, acc[1] * f);
+  }
+}
+
+// The streams' threads: warpgroup x (warps 4 + 4x ..), thread = row = tensor-memory lane.
+template <int D, bool FP8, bool CL>
 __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, uint32_t stall) {
   using S = Shape<D, FP8>;
   const VarlenMeta& m = p.m;
@@ -648,7 +846,18 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
   int turn = 0;  // the stream whose turn it is
   bool bad = false;
   if (!c.work) return;
-  TreeWalk walk(p, blockIdx.x);
+  if constexpr (CL) {
+    // (every CTA finds the same; the flag ends the other roles' waits)
+    if (__any_sync(kFull, batch_refused(p, threadIdx.x - 128)) && lane == 0) {
+      record_error(p.status, PA_EINVAL);
+      *c.abort = 1;
+    }
+    asm volatile("bar.sync 3, 256;" ::: "memory");  // both streams' warps have looked
+    bad = __any_sync(kFull, *c.abort != 0);
+    if (c.own->t1 <= c.own->t0 && threadIdx.x - 128 < c.own->rows)
+      reinterpret_cast<float2*>(c.sm + S::kOffML)[threadIdx.x - 128] = make_float2(-INFINITY, 0.f);
+  }
+  Walk<CL> walk(c, p);
   TreeSegment g;
   for (; walk.next(p, g); ++seg) {
     const bool two = two_tiles(p, g);
@@ -791,6 +1000,9 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
       state_taken(par);
       bad |= bads[par * 4 + quad] != 0;  // (uniform across the warp)
     }
+    // (the state goes over the ring: the other stream's last product has to be done with it)
+    if (CL && two && !bad)
+      bad = !wait_all(c, B_PVDONE + (x ^ 1), ((x ? cnt[0] : cnt[1]) - 1) & 1);
     // (a failed role's rows must not be written)
     if (!bad && __all_sync(kFull, *c.abort == 0)) {
       tc_fence_after();
@@ -809,9 +1021,14 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
       __nv_bfloat16* out = nullptr;
       if (valid) {
         if (g.slot >= 0) {
-          const int64_t at = (int64_t)g.slot * p.rows_per_item + item_row;
-          p.part_ml[at] = make_float2(m_ref, l);
-          po = p.part_o + at * D;
+          if constexpr (CL) {
+            reinterpret_cast<float2*>(c.sm + S::kOffML)[item_row] = make_float2(m_ref, l);
+            po = reinterpret_cast<float*>(c.sm + S::kOffState) + item_row * S::kStateLd;
+          } else {
+            const int64_t at = (int64_t)g.slot * p.rows_per_item + item_row;
+            p.part_ml[at] = make_float2(m_ref, l);
+            po = p.part_o + at * D;
+          }
         } else {
           scale = tree_finish(p, g.kvh, h, tok, m_ref, l, true);
           out = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)tok * m.num_heads + h) * D;
@@ -857,7 +1074,7 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
   }
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool CL>
 __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     k_tree_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
               const __grid_constant__ CUtensorMap tv, const TreeParams p, uint64_t wait_limit,
@@ -867,6 +1084,8 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kOffMisc);
   int* flags = reinterpret_cast<int*>(sm + S::kOffMisc + 4);  // [0] skip, [1] abort
+  TreeSegment* own = reinterpret_cast<TreeSegment*>(sm + S::kOffSeg);
+  static_assert(sizeof(TreeSegment) <= 64, "kOffSeg");
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     flags[1] = 0;
@@ -895,7 +1114,7 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // everything above overlaps the planning kernel
+  // everything above overlaps the kernel ahead (shares: the planning kernel)
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -904,26 +1123,34 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     if (off) record_error(p.status, PA_ECUDA);
     flags[0] = off || status_set(p.status) ? 1 : 0;
   }
+  if (CL && warp == 2) plan_own(p, own, threadIdx.x & 31);
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
-  const Ctx c{sm, bar, reinterpret_cast<volatile int*>(flags + 1), p.status,
-              wait_limit, flags[0] == 0};
+  const Ctx c{sm,         bar,        reinterpret_cast<volatile int*>(flags + 1), p.status,
+              wait_limit, flags[0] == 0, own};
+  const bool joined = CL && p.cluster > 1;  // the cluster's CTAs join their states
+  // (a CTA that does nothing tells the others)
+  if (CL && !c.work && threadIdx.x == 0) flags[1] = 1;
 
   // register shares of the warps: bf16 4 x 72 + 8 x 216, e4m3 4 x 72 + 8 x 176 + 4 x 88
   static_assert(4 * 72 + 8 * 216 <= 12 * 168 && 4 * 72 + 8 * 176 + 4 * 88 <= 16 * 128, "registers");
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
-    if constexpr (FP8) converter<D>(c, p);
+    if constexpr (FP8) converter<D, CL>(c, p);
     __syncthreads();
+    if (joined) {
+      cluster_sync();
+      cluster_sync();
+    }
   } else if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
     if (warp == 0 || warp == 3) {
-      producer<D, FP8>(c, p, warp ? &tv : &tk, &tq, warp ? 1 : 0);
+      producer<D, FP8, CL>(c, p, warp ? &tv : &tk, &tq, warp ? 1 : 0);
     } else {
       if (warp == 1)
-        s_issuer<D, FP8>(c, p, tmem);
+        s_issuer<D, FP8, CL>(c, p, tmem);
       else
-        pv_issuer<D, FP8>(c, p, tmem);
+        pv_issuer<D, FP8, CL>(c, p, tmem);
       __syncwarp();
       // every MMA of this warp is done before the tensor memory goes (bounded)
       mma_commit(bar + B_FIN + (warp - 1));
@@ -932,33 +1159,63 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (joined) cluster_sync();
     if (warp == 1) {
       tc_fence_after();
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                    "r"(kTmemCols)
                    : "memory");
     }
+    if (joined) cluster_sync();
   } else {
     if constexpr (FP8)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 176;" ::: "memory");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
-    softmax_role<D, FP8>(c, p, tmem, stall);
+    softmax_role<D, FP8, CL>(c, p, tmem, stall);
     tc_fence_before();
     __syncthreads();
+    if (joined) {
+      cluster_sync();
+      cluster_merge<D, FP8>(c, p);
+      cluster_sync();  // every CTA stays until its state has been read
+    }
   }
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool CL>
 cudaError_t launch_as(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       const TreeParams& p, uint64_t limit, uint32_t stall, cudaStream_t stream) {
   using S = Shape<D, FP8>;
-  auto kern = k_tree_tc<D, FP8>;
+  auto kern = k_tree_tc<D, FP8, CL>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(p.grid), dim3(S::kThreads), S::kSmem, stream, tq, tk, tv, p, limit,
-                    stall);
+  if constexpr (!CL)
+    return launch_pdl(kern, dim3(p.grid), dim3(S::kThreads), S::kSmem, stream, tq, tk, tv, p, limit,
+                      stall);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p, limit, stall);
+}
+
+template <int D, bool FP8>
+cudaError_t launch_mode(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                        const TreeParams& p, uint64_t limit, uint32_t stall, cudaStream_t stream) {
+  return p.cluster ? launch_as<D, FP8, true>(tq, tk, tv, p, limit, stall, stream)
+                   : launch_as<D, FP8, false>(tq, tk, tv, p, limit, stall, stream);
 }
 
 }  // namespace
@@ -966,9 +1223,9 @@ cudaError_t launch_as(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
 cudaError_t launch_tree_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const TreeParams& p, bool fp8, uint64_t wait_limit, uint32_t stall,
                            cudaStream_t stream) {
-  if (fp8) return launch_as<128, true>(tq, tk, tv, p, wait_limit, stall, stream);
-  if (p.m.head_dim == 128) return launch_as<128, false>(tq, tk, tv, p, wait_limit, stall, stream);
-  return launch_as<64, false>(tq, tk, tv, p, wait_limit, stall, stream);
+  if (fp8) return launch_mode<128, true>(tq, tk, tv, p, wait_limit, stall, stream);
+  if (p.m.head_dim == 128) return launch_mode<128, false>(tq, tk, tv, p, wait_limit, stall, stream);
+  return launch_mode<64, false>(tq, tk, tv, p, wait_limit, stall, stream);
 }
 
 }  // namespace pa

@@ -132,6 +132,21 @@ static TreeLayout tree_tc_layout(int32_t num_seqs, int64_t num_tokens, int32_t g
                      kTreeTcKeys, kTreeTcGrid);
 }
 
+// CTAs of a cluster for each (sequence, kv head, item) of a small call, which then is one launch; 0:
+// the call takes the planned shares (three launches).  Both are right for any batch.  Clusters of
+// eight, four, two while about a wave of them covers the units (a GPC holds whole clusters only),
+// and no larger than the key tiles that a table can hold; not for long tables, whose tiles one
+// CTA of few would take one after the other.
+static int32_t tree_cluster(int32_t num_seqs, int32_t num_kv_heads, int32_t items, int64_t max_keys,
+                            int32_t max_blocks, int32_t sms) {
+  const int64_t units = (int64_t)num_seqs * num_kv_heads * items;
+  const int64_t tiles = (max_keys + kTreeTcKeys - 1) / kTreeTcKeys;
+  if (units > sms || (int64_t)num_seqs * max_blocks > kTreeSmallEntries) return 0;
+  int32_t c = 8;
+  while (c > 1 && (units * c > sms * 7 / 8 || c / 2 >= tiles)) c /= 2;
+  return (tiles + c - 1) / c <= kTreeSmallTiles ? c : 0;
+}
+
 size_t pa_tree_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads,
                                         int32_t num_kv_heads, int32_t head_dim,
                                         int32_t max_blocks_per_seq, int32_t block_size) {
@@ -240,6 +255,9 @@ pa_status pa_tree_attention(const void* q, const void* k_blocks, const void* v_b
     L = tree_tc_layout(num_seqs, num_tokens, m.group, num_kv_heads, head_dim, max_keys,
                        p.rows_per_item);
     L.grid = std::min(L.grid, d->sms);  // (a smaller grid uses less of each part of the workspace)
+    p.items = (int32_t)((most + p.rows_per_item - 1) / p.rows_per_item);
+    p.cluster = tree_cluster(num_seqs, num_kv_heads, p.items, max_keys, max_blocks_per_seq, d->sms);
+    if (p.cluster) L.grid = num_seqs * num_kv_heads * p.items * p.cluster;
   } else {
     p.tile_rows = p.rows_per_item = kTreeGenericRows;
     p.key_tile = kTreeGenericKeys;
@@ -263,12 +281,13 @@ pa_status pa_tree_attention(const void* q, const void* k_blocks, const void* v_b
                    pool_map_rows(&tv, v_blocks, num_blocks, num_kv_heads, head_dim));
     if (!ok) return PA_ECUDA;
   }
-  if (launch_tree_plan(p, stream) != cudaSuccess) return PA_ECUDA;
+  if (!p.cluster && launch_tree_plan(p, stream) != cudaSuccess) return PA_ECUDA;
   if (tc) {
     uint64_t limit;
     uint32_t stall;
     stall_hook(limit, stall);
     if (launch_tree_tc(tq, tk, tv, p, fp8, limit, stall, stream) != cudaSuccess) return PA_ECUDA;
+    if (p.cluster) return PA_OK;
   } else if (launch_tree_generic(p, kv_dtype, stream) != cudaSuccess) {
     return PA_ECUDA;
   }

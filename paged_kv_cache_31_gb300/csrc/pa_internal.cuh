@@ -611,7 +611,10 @@ struct TreeParams {
   float2* part_ml;  // [2 * grid, rows_per_item] running max (log2 units) and exp-sum
   float* part_o;    // [2 * grid, rows_per_item, head_dim] unnormalised outputs
   int* status;
-  int32_t q_bf16, out_vec;
+  int32_t q_bf16;
+  // Small calls: one cluster of `cluster` CTAs for each (sequence, kv head, item), items numbered
+  // 0 .. items - 1 in every sequence (0: the shares above).
+  int32_t cluster, items;
 };
 // The work of an item, in about hundredths of a microsecond (only the balance between the CTAs
 // depends on it): a key tile of one row tile takes about 1.5 us, a little more the more warps its
@@ -639,6 +642,10 @@ cudaError_t launch_tree_tc(const CUtensorMap& tq, const CUtensorMap& tk, const C
                            const TreeParams& p, bool fp8, uint64_t wait_limit, uint32_t stall,
                            cudaStream_t stream);
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t stream);
+// Small calls in one launch: each cluster plans its own item and every CTA checks the whole batch,
+// at most this many table entries of it.
+constexpr int64_t kTreeSmallEntries = 8192;
+constexpr int64_t kTreeSmallTiles = 8;  // key tiles of a CTA, at most
 
 // Status word and SM count of the current device, cached per context; null on a CUDA error.
 struct DeviceState {
