@@ -29,6 +29,12 @@
 // masked); warps 4..7 and 8..11: the streams' softmax and epilogue; warps 12..15 (e4m3
 // pools): widen Q, K and V in shared memory.
 //
+// Small calls (CL).  Instead of the planned shares, a cluster of 1 to 8 CTAs for each (sequence, kv
+// head, item): each CTA plans its own part from the sequence's numbers (an even run of the key
+// tiles), its softmax warps check the whole batch while the first tiles are on their way, and the
+// CTAs' states are joined in key order through distributed shared memory.  One launch instead of
+// three: a tree of 8 nodes over 700 positions takes 8.8 us instead of 14.2.
+//
 // What bounds it: up to 128 rows per kv head, the K / V bytes (a tile is 64 KB of bf16, 1.5 us of
 // an SM's share of the measured copy bandwidth, against 1.0 us of tensor time); with two row
 // tiles, the tensor cores (2.0 us a tile).
@@ -39,6 +45,7 @@
 // issuers wait (bounded) for their copies in flight and the MMA issuers for their MMAs before the
 // CTA gives its tensor memory back.
 #include <algorithm>
+#include <atomic>
 
 #include "k_tree.cuh"
 #include "pa_tcgen05.cuh"
@@ -164,11 +171,15 @@ struct Walk {
 template <>
 struct Walk<true> {
   const TreeSegment* own;
-  __device__ __forceinline__ Walk(const Ctx& c, const TreeParams& p) : own(c.own) {}
+  int left;
+  __device__ __forceinline__ Walk(const Ctx& c, const TreeParams& p) : own(c.own) {
+    // (not a constant to the compiler, which otherwise writes the roles' loops out several times)
+    asm volatile("mov.u32 %0, 1;" : "=r"(left));
+  }
   __device__ __forceinline__ bool next(const TreeParams& p, TreeSegment& g) {
-    if (!own) return false;
+    if (left == 0) return false;
+    --left;
     g = *own;
-    own = nullptr;
     return g.t1 > g.t0;
   }
 };
@@ -579,43 +590,48 @@ __device__ void converter(const Ctx& c, const TreeParams& p) {
   }
 }
 
-// Visible keys of one row in the 32 positions from key0 on.
-__device__ __forceinline__ uint32_t visible_word(const TreeParams& p, const TreeSegment& g, int tok,
-                                                 int pos, int key0) {
+// Visible keys of one row in a tile's 128 positions from key0 on, 32 to a word.
+__device__ __forceinline__ void visible_keys(const TreeParams& p, const TreeSegment& g, int tok,
+                                             int pos, int key0, uint32_t (&see)[4]) {
   const int ctx = g.n - g.nodes;
-  uint32_t w = 0;
-  if (key0 < ctx) {  // context positions from pos - window + 1 on
-    const int hi = min(32, ctx - key0);
-    w = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
-    if (p.m.window > 0) {
-      const int lo = pos - p.m.window + 1 - key0;
-      w = lo >= 32 ? 0u : lo > 0 ? w & (0xffffffffu << lo) : w;
-    }
-  }
   const int node0 = key0 - ctx;  // node of bit 0
-  if (node0 > -32 && node0 < g.nodes) {
-    const int32_t* row = p.mask + (int64_t)tok * p.mask_words;
-    uint32_t t;
-    if (node0 < 0) {
-      t = (uint32_t)row[0] << -node0;
-    } else {
-      const int i = node0 >> 5, s = node0 & 31;
-      const uint32_t a = (uint32_t)row[i], b = i + 1 < p.mask_words ? (uint32_t)row[i + 1] : 0u;
-      t = __funnelshift_r(a, b, s);
-    }
-    const int end = g.nodes - node0;  // bits from there on are past the tree
-    if (end < 32) t &= (1u << end) - 1u;
-    // Nodes too far behind pos, one by one, unless none can be: positions are not negative, and a
-    // first key kv0 > 0 says that the sequence's lowest one is at least kv0 + window - 1.
-    const int far = pos - p.m.window;
-    if (p.m.window > 0 && far >= 0 && !(g.kv0 > 0 && g.kv0 + p.m.window - 1 > far))
-      for (uint32_t m = t; m; m &= m - 1) {
-        const int i = __ffs(m) - 1;
-        if (p.m.positions[g.qs + node0 + i] <= far) t &= ~(1u << i);
-      }
-    w |= t;
+  // the row's words that hold these bits, all requested at once
+  uint32_t row[5];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
+    const int i = (node0 >> 5) + k;
+    row[k] = i >= 0 && 32 * i < g.nodes ? (uint32_t)p.mask[(int64_t)tok * p.mask_words + i] : 0u;
   }
-  return w;
+  const int far = pos - p.m.window;
+  // Nodes too far behind pos are looked for one by one, unless none can be: positions are not
+  // negative, and a first key kv0 > 0 says that the sequence's lowest one is at least
+  // kv0 + window - 1.
+  const bool look = p.m.window > 0 && far >= 0 && !(g.kv0 > 0 && g.kv0 + p.m.window - 1 > far);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int key = key0 + 32 * q, node = node0 + 32 * q;
+    uint32_t w = 0;
+    if (key < ctx) {  // context positions from pos - window + 1 on
+      const int hi = min(32, ctx - key);
+      w = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
+      if (p.m.window > 0) {
+        const int lo = far + 1 - key;
+        w = lo >= 32 ? 0u : lo > 0 ? w & (0xffffffffu << lo) : w;
+      }
+    }
+    uint32_t t = __funnelshift_r(row[q], row[q + 1], node0 & 31);
+    const int end = g.nodes - node;  // bits from there on are past the tree
+    if (end < 32) t = end > 0 ? t & ((1u << end) - 1u) : 0u;
+    see[q] = w | t;
+  }
+  if (!look) return;
+#pragma unroll 1
+  for (int i = max(0, -node0); i < kBN && node0 + i < g.nodes; ++i) {
+    const uint32_t bit = 1u << (i & 31);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (i >> 5 == q && (see[q] & bit) && p.m.positions[g.qs + node0 + i] <= far) see[q] &= ~bit;
+  }
 }
 
 // The weights p = 2^(s * sl + nb) of 32 keys (packed pairs), added to `sum` and written to
@@ -723,6 +739,7 @@ __device__ __forceinline__ void plan_own(const TreeParams& p, TreeSegment* out, 
       g.rows = min(p.rows_per_item, rows - g.row0);
       if (m.window > 0) {
         int lo = INT_MAX;
+    #pragma unroll 1
         for (int t = lane; t < g.nodes; t += 32) lo = min(lo, m.positions[g.qs + t]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) lo = min(lo, __shfl_xor_sync(kFull, lo, o));
@@ -741,10 +758,12 @@ __device__ __forceinline__ void plan_own(const TreeParams& p, TreeSegment* out, 
 __device__ __forceinline__ bool batch_refused(const TreeParams& p, int tid) {
   const VarlenMeta& m = p.m;
   bool bad = false;
+#pragma unroll 1
   for (int g = tid; g < m.num_kv_heads; g += 256) {
     const float a = m.k_scales ? m.k_scales[g] : 1.f, b = m.v_scales ? m.v_scales[g] : 1.f;
     bad |= !(a > 0.f && a <= 3.402823466e38f) || !(b > 0.f && b <= 3.402823466e38f);
   }
+#pragma unroll 1
   for (int s = tid; s < m.num_seqs; s += 256) {
     const int qs = m.query_start_loc[s], qe = m.query_start_loc[s + 1], n = m.seq_lens[s];
     bad |= qs < 0 || qe < qs || (int64_t)qe > m.num_tokens || (s == 0 && qs != 0) ||
@@ -754,8 +773,10 @@ __device__ __forceinline__ bool batch_refused(const TreeParams& p, int tid) {
              ((int64_t)n + 15) / 16 > m.max_blocks;
   }
   if (m.window > 0)
+#pragma unroll 1
     for (int64_t t = tid; t < m.num_tokens; t += 256) bad |= m.positions[t] < 0;
   const int per = (m.max_blocks + 31) / 32;  // 32 entries of a table row: a warp's
+#pragma unroll 1
   for (int i = tid >> 5; i < m.num_seqs * per; i += 8) {
     const int s = i / per, e = i % per * 32 + (tid & 31);
     const int qs = m.query_start_loc[s], qe = m.query_start_loc[s + 1], n = m.seq_lens[s];
@@ -780,27 +801,42 @@ __device__ void cluster_merge(const Ctx& c, const TreeParams& p) {
   // (a failed wait in any CTA, or a batch that is not valid: nothing is written)
   const bool failed = lane < C && peer_load(peer_addr(const_cast<int*>(c.abort), lane)) != 0;
   if (__any_sync(kFull, failed)) return;
-  const uint32_t ml = peer_addr(c.sm + S::kOffML, min(lane, C - 1));
+  // 8 / C rows at a time, so that eight loads are in flight whatever C: lane k < 8 has the (m, l)
+  // of row k / C from CTA k % C
+  const int lg = __ffs(C) - 1, low = C - 1, R = 8 >> lg, rank = (int)cluster_rank();
+  const uint32_t ml = peer_addr(c.sm + S::kOffML, lane & low);
   const uint32_t o = smem_u32(c.sm + S::kOffState) + lane * E * 4;
-  for (int r = (int)cluster_rank() + C * warp; r < g.rows; r += 8 * C) {
-    float2 st = make_float2(-INFINITY, 0.f);
-    if (lane < C) st = peer_load2(ml + r * 8);
+#pragma unroll 1
+  for (int i0 = R * warp; rank + C * i0 < g.rows; i0 += 8 * R) {  // rows rank + C i0, + C (i0 + 1) ..
+    const int mine = rank + C * (i0 + (lane >> lg));
+    const bool have = lane < 8 && mine < g.rows;
+    const float2 st = have ? peer_load2(ml + mine * 8) : make_float2(-INFINITY, 0.f);
     float M = st.x;
-#pragma unroll
-    for (int k = 1; k < 8; k <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, k));
+#pragma unroll 1
+    for (int k = 1; k < C; k <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, k));
     const float w = st.x == -INFINITY ? 0.f : exp2f(st.x - M);
     float L = w * st.y;
-#pragma unroll
-    for (int k = 1; k < 8; k <<= 1) L += __shfl_xor_sync(kFull, L, k);
-    M = __shfl_sync(kFull, M, 0);
-    L = __shfl_sync(kFull, L, 0);
+#pragma unroll 1
+    for (int k = 1; k < C; k <<= 1) L += __shfl_xor_sync(kFull, L, k);
+    float f = 0.f;
+    int to = -1;  // row of the output
+    if (have) {
+      const int n = g.row0 + mine, tok = g.qs + n / m.group, h = g.kvh * m.group + n % m.group;
+      f = tree_finish(p, g.kvh, h, tok, M, L, (lane & low) == 0);
+      to = tok * m.num_heads + h;
+    }
     float4 v[8];
+    float wk[8];
+    const uint32_t from = o + (rank + C * i0) * S::kStateLd * 4;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k < C && __shfl_sync(kFull, w, k) > 0.f) {  // (a CTA without a tile left no row)
+      wk[k] = __shfl_sync(kFull, w, k);
+      if (wk[k] > 0.f) {  // (a row past the item's, or a CTA without a tile, left nothing)
         uint32_t a;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(o + r * S::kStateLd * 4), "r"(k));
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(a)
+                     : "r"(from + (k >> lg << lg) * S::kStateLd * 4), "r"(k & low));
         if constexpr (E == 4) {
           v[k] = peer_load4(a);
         } else {
@@ -813,20 +849,23 @@ __device__ void cluster_merge(const Ctx& c, const TreeParams& p) {
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float wk = __shfl_sync(kFull, w, k);
-      acc[0] += wk * v[k].x;
-      acc[1] += wk * v[k].y;
-      acc[2] += wk * v[k].z;
-      acc[3] += wk * v[k].w;
+      acc[0] += wk[k] * v[k].x;
+      acc[1] += wk[k] * v[k].y;
+      acc[2] += wk[k] * v[k].z;
+      acc[3] += wk[k] * v[k].w;
+      if (((k + 1) & low) != 0) continue;  // not the row's last CTA
+      const float fk = __shfl_sync(kFull, f, k);
+      const int row = __shfl_sync(kFull, to, k);
+      if (row >= 0) {
+        const uint32_t lo = pack_bf16x2(acc[0] * fk, acc[1] * fk);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (int64_t)row * D + lane * E;
+        if constexpr (E == 4)
+          *reinterpret_cast<uint2*>(out) = make_uint2(lo, pack_bf16x2(acc[2] * fk, acc[3] * fk));
+        else
+          *reinterpret_cast<uint32_t*>(out) = lo;
+      }
+      acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
     }
-    const int R = g.row0 + r, tok = g.qs + R / m.group, h = g.kvh * m.group + R % m.group;
-    const float f = tree_finish(p, g.kvh, h, tok, M, L, lane == 0);
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)tok * m.num_heads + h) * D + lane * E;
-    if constexpr (E == 4)
-      *reinterpret_cast<uint2*>(out) =
-          make_uint2(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f));
-    else
-      *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * f, acc[1] * f);
   }
 }
 
@@ -887,14 +926,7 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
       // a tile that hides keys from some row: which ones, while S is still being computed
       const bool hides = !__all_sync(kFull, key0 >= free_lo && key0 + kBN <= ctx) && !idle;
       uint32_t see[4] = {0, 0, 0, 0};
-      if (hides) {
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t w = visible_word(p, g, tok, pos, key0 + 32 * q);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) see[e] = e == q ? w : see[e];
-        }
-      }
+      if (hides) visible_keys(p, g, tok, pos, key0, see);
       if (!bad)
         bad = !wait_all(c, stall ? B_NEVER : B_SFULL + x, stall ? 0u : n & 1);
       // the row of q was multiplied by 2^exp when it was split (known once its first S is)
@@ -1212,6 +1244,29 @@ cudaError_t launch_as(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
 }
 
 template <int D, bool FP8>
+int resident(int c) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(c);
+  cfg.blockDim = dim3(Shape<D, FP8>::kThreads);
+  cfg.dynamicSmemBytes = Shape<D, FP8>::kSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = c;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  auto kern = k_tree_tc<D, FP8, true>;
+  int n = 0;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Shape<D, FP8>::kSmem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+template <int D, bool FP8>
 cudaError_t launch_mode(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                         const TreeParams& p, uint64_t limit, uint32_t stall, cudaStream_t stream) {
   return p.cluster ? launch_as<D, FP8, true>(tq, tk, tv, p, limit, stall, stream)
@@ -1219,6 +1274,18 @@ cudaError_t launch_mode(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
 }
 
 }  // namespace
+
+int tree_clusters_resident(int device, bool fp8, int head_dim, int c) {
+  // [device][variant][cluster size 2, 4, 8]: number + 1, 0 while it is not known
+  static std::atomic<int> known[64][3][3];
+  const int variant = fp8 ? 2 : head_dim == 128, at = c == 2 ? 0 : c == 4 ? 1 : 2;
+  if (device < 0 || device >= 64) return 0;
+  const int k = known[device][variant][at].load(std::memory_order_relaxed);
+  if (k) return k - 1;
+  const int n = fp8 ? resident<128, true>(c) : variant ? resident<128, false>(c) : resident<64, false>(c);
+  known[device][variant][at].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
 
 cudaError_t launch_tree_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const TreeParams& p, bool fp8, uint64_t wait_limit, uint32_t stall,

@@ -132,19 +132,29 @@ static TreeLayout tree_tc_layout(int32_t num_seqs, int64_t num_tokens, int32_t g
                      kTreeTcKeys, kTreeTcGrid);
 }
 
-// CTAs of a cluster for each (sequence, kv head, item) of a small call, which then is one launch; 0:
-// the call takes the planned shares (three launches).  Both are right for any batch.  Clusters of
-// eight, four, two while about a wave of them covers the units (a GPC holds whole clusters only),
-// and no larger than the key tiles that a table can hold; not for long tables, whose tiles one
-// CTA of few would take one after the other.
-static int32_t tree_cluster(int32_t num_seqs, int32_t num_kv_heads, int32_t items, int64_t max_keys,
-                            int32_t max_blocks, int32_t sms) {
+// CTAs of a cluster for each (sequence, kv head, item of `wide` row tiles) of a small call, which
+// then is one launch; 0: the call takes the planned shares (three launches).  Both are right for
+// any batch.  The largest clusters that are all resident at once (a second wave costs more than a
+// larger cluster gives), no larger than the key tiles that a table can hold.  The slowest CTA's key
+// tiles decide: they may be as many as a CTA's even share of the batch (taken as 0.7 of what the
+// tables can hold: few sequences are as long as the longest) and the nine that the two other
+// launches are worth.  Measured (us, clusters / shares, bf16, 32 rows a kv head): 8 units of 5 tiles
+// 8.7 / 15.3, of 63 tiles 16.9 / 21.4; 128 units of 16 tiles 30.7 / 38.3, of 64 tiles 93 / 100.
+static int32_t tree_cluster(int32_t num_seqs, int32_t num_kv_heads, int32_t items, int32_t wide,
+                            int64_t max_keys, int32_t max_blocks, int32_t sms, bool fp8,
+                            int32_t head_dim) {
   const int64_t units = (int64_t)num_seqs * num_kv_heads * items;
   const int64_t tiles = (max_keys + kTreeTcKeys - 1) / kTreeTcKeys;
-  if (units > sms || (int64_t)num_seqs * max_blocks > kTreeSmallEntries) return 0;
+  int device = 0;
+  if (units > sms || (int64_t)num_seqs * max_blocks > kTreeSmallEntries ||
+      cudaGetDevice(&device) != cudaSuccess)
+    return 0;
   int32_t c = 8;
-  while (c > 1 && (units * c > sms * 7 / 8 || c / 2 >= tiles)) c /= 2;
-  return (tiles + c - 1) / c <= kTreeSmallTiles ? c : 0;
+  while (c > 1 && (c / 2 >= tiles || units * c > sms ||
+                   units > tree_clusters_resident(device, fp8, head_dim, c)))
+    c /= 2;
+  const int64_t most = (tiles + c - 1) / c * wide, share = units * wide * tiles / sms;
+  return most <= share * 7 / 10 + kTreeSmallTiles ? c : 0;
 }
 
 size_t pa_tree_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads,
@@ -250,14 +260,19 @@ pa_status pa_tree_attention(const void* q, const void* k_blocks, const void* v_b
     p.tile_rows = tree_tile_rows(m.group);
     p.tile_tokens = p.tile_rows / m.group;
     const int64_t most = std::min<int64_t>(32 * (int64_t)mask_words, num_tokens) * m.group;
-    p.rows_per_item = most > p.tile_rows ? 2 * p.tile_rows : p.tile_rows;
     p.key_tile = kTreeTcKeys;
+    // small calls: clusters, of items of one row tile (more of them, on more SMs) or else of two
+    const int32_t wide = most > p.tile_rows ? 2 : 1;
+    for (int32_t tiles = 1; tiles <= wide && !p.cluster; ++tiles) {
+      p.rows_per_item = tiles * p.tile_rows;
+      p.items = (int32_t)((most + p.rows_per_item - 1) / p.rows_per_item);
+      p.cluster = tree_cluster(num_seqs, num_kv_heads, p.items, tiles, max_keys, max_blocks_per_seq,
+                               d->sms, fp8, head_dim);
+    }
     L = tree_tc_layout(num_seqs, num_tokens, m.group, num_kv_heads, head_dim, max_keys,
                        p.rows_per_item);
-    L.grid = std::min(L.grid, d->sms);  // (a smaller grid uses less of each part of the workspace)
-    p.items = (int32_t)((most + p.rows_per_item - 1) / p.rows_per_item);
-    p.cluster = tree_cluster(num_seqs, num_kv_heads, p.items, max_keys, max_blocks_per_seq, d->sms);
-    if (p.cluster) L.grid = num_seqs * num_kv_heads * p.items * p.cluster;
+    L.grid = p.cluster ? num_seqs * num_kv_heads * p.items * p.cluster
+                       : std::min(L.grid, d->sms);  // (no more than the workspace has room for)
   } else {
     p.tile_rows = p.rows_per_item = kTreeGenericRows;
     p.key_tile = kTreeGenericKeys;

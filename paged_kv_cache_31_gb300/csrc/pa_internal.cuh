@@ -645,7 +645,8 @@ cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t stream);
 // Small calls in one launch: each cluster plans its own item and every CTA checks the whole batch,
 // at most this many table entries of it.
 constexpr int64_t kTreeSmallEntries = 8192;
-constexpr int64_t kTreeSmallTiles = 8;  // key tiles of a CTA, at most
+constexpr int64_t kTreeSmallTiles = 9;  // key tiles of a CTA beyond its even share, at most
+int tree_clusters_resident(int device, bool fp8, int head_dim, int c);  // c 2, 4 or 8; at once
 
 // Status word and SM count of the current device, cached per context; null on a CUDA error.
 struct DeviceState {
