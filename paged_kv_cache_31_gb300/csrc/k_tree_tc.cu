@@ -75,7 +75,7 @@ struct Shape {
   static constexpr int kOffX = FP8 ? kOffWide + 2 * kTileBytes : kOffKV + kStages * kTileBytes;
   static constexpr int kOffBad = kOffX + 2 * 128 * 8;          // [2][4] its warps' failed waits
   static constexpr int kOffBar = kOffBad + 2 * 4 * 4;
-  static constexpr int kOffMisc = kOffBar + 40 * 8;
+  static constexpr int kOffMisc = kOffBar + 48 * 8;
   // tensor-memory base, flags; e4m3: the rows' scale exponents of four Q tiles
   static constexpr int kOffExp = kOffMisc + 16;
   static constexpr int kOffSeg = kOffExp + (FP8 ? 4 * 128 : 0);  // clusters: the CTA's TreeSegment
@@ -98,8 +98,8 @@ enum : int {
   B_QEMPTY = B_QFULL + 2,          // its last S = Q K^T is done
   B_QCONV = B_QEMPTY + 2,          // e4m3: it has been split
   B_FULL = B_QCONV + 2,            // stage landed: K's copies, then V's (B_FULL + kMostStages + ..)
-  B_EMPTY = B_FULL + 2 * kMostStages,  // its copy has been used up
-  B_WIDE = B_EMPTY + kMostStages,  // e4m3: a V tile is ready as f16
+  B_EMPTY = B_FULL + 2 * kMostStages,  // its copy has been used up: K's copies, then V's
+  B_WIDE = B_EMPTY + 2 * kMostStages,  // e4m3: a V tile is ready as f16
   B_WFREE = B_WIDE + 2,            // e4m3: its P V is done
   B_SFULL = B_WFREE + 2,           // per stream: S is ready
   B_PFULL = B_SFULL + 2,           // P is written
@@ -109,7 +109,7 @@ enum : int {
   B_NEVER = B_FIN + 2,             // nothing arrives on it (the debug_stall test hook)
   kNumBars = B_NEVER + 1
 };
-static_assert(kNumBars <= 40, "barrier area");
+static_assert(kNumBars <= 48, "barrier area");
 
 constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t col_s(int x) { return (uint32_t)x * 128; }
@@ -209,15 +209,14 @@ __device__ __forceinline__ bool wait_all(const Ctx& c, int idx, uint32_t parity)
 // two row tiles, and K0 - K1 V0 K2 V1 K3 ... (K_t 2t, V_t 2t + 3; `ahead`) where none has: the
 // streams then work on two tiles at once, and tile t's V is needed after tile t + 1's K.  Copy n
 // uses stage n % kStages, so K and V take turns in a stage, and an operand's copies come to the
-// same stage every kStages tiles.  A parity tells neighbouring phases of a barrier apart, no more,
-// so each barrier has to be waited for in every phase, or be known to be near:
-//   - "landed" barriers are one set per operand, whose consumers wait for each phase;
-//   - a stage's "empty" barrier is completed by K's and V's consumers in turn and waited for by
-//     the other operand's producer.  A producer that waits for copy n + 5's consumption has sent
-//     copy n + 8 of its own, after copy n + 3 was used up, and that was after copy n was: QK of
-//     tile t + 3 follows PV of tile t + 1 (n V_t), and PV of tile t its QK (n K_t).  So the barrier
-//     has passed copy n's phase.
-// Where copy 1 does not exist its "empty" phase is completed at the start.
+// same stage every kStages tiles.
+//
+// A parity tells neighbouring phases of a barrier apart, no more, so every phase of a barrier is
+// waited for, in order, by the one that goes on by it: a stage's "landed" barriers are one set per
+// operand, and so are its "empty" ones.  K's producer waits for V's copies to leave a stage
+// and V's for K's (copy n for copy n - 5's).  (One "empty" barrier for both, its phases waited for in
+// turn by the two, let a producer mistake a phase two behind for the one before: a consumption
+// counts when its issuer comes to say so, which can be later than what depends on its products.)
 //
 // Over e4m3 pools each operand has a ring of code stages of its own (0 .. 2 K, 3 .. 5 V), half as
 // large.  V's codes are widened into one of two f16 tiles, and their stage is free as soon as they
@@ -227,38 +226,31 @@ __device__ __forceinline__ bool ring_ahead(const TreeParams& p) {
 }
 template <bool FP8>
 struct Ring {
-  uint32_t st, par;        // stage of this operand's current copy; the parity of its "empty" phase
-  uint32_t turn, par_own;  // tile t % kStages; the parity of its "landed" phase
+  static constexpr uint32_t kLen = FP8 ? kCodeStages : kStages;
+  uint32_t st;         // stage of this operand's current copy
+  uint32_t turn, par;  // tile t % kLen, and the parity of t / kLen: its visits to the stage
   __device__ __forceinline__ Ring(const TreeParams& p, int kv) {
     if constexpr (FP8)
       st = kv ? kCodeStages : 0;
     else
       st = kv ? (ring_ahead(p) ? 3 : 1) : 0;
-    par = turn = par_own = 0;
+    turn = par = 0;
   }
   __device__ __forceinline__ void next() {  // the next tile's copy of the same operand
     if constexpr (FP8) {
       ++st;
-      if (++turn == kCodeStages) {
-        st -= kCodeStages;
-        turn = 0;
-        par ^= 1;
-        par_own ^= 1;
-      }
     } else {
       st += 2;
-      if (st >= kStages) {
-        st -= kStages;
-        par ^= 1;
-      }
-      if (++turn == kStages) {
-        turn = 0;
-        par_own ^= 1;
-      }
+      if (st >= kStages) st -= kStages;
+    }
+    if (++turn == kLen) {
+      turn = 0;
+      par ^= 1;
+      if constexpr (FP8) st -= kCodeStages;
     }
   }
 };
-static_assert(kStages == 5, "the reasoning above");
+static_assert(kStages == 5, "copies n and n - 5 are of different operands");
 
 // Both streams take all key tiles of a segment with two row tiles.  With one row tile the streams
 // alternate, over segments too: the stream that does not take a segment's last tile begins the
@@ -279,6 +271,10 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
   const int lane = threadIdx.x & 31;
   uint64_t* full = c.bar + B_FULL + kv * kMostStages;
   Ring<FP8> r(p, kv);
+  // the stage's last copy is that of a tile `lag` before, of the other operand where they share
+  uint64_t* empty = c.bar + B_EMPTY + (FP8 ? kv : kv ^ 1) * kMostStages;
+  uint32_t lag = FP8 ? kCodeStages : kv ? (ring_ahead(p) ? 1 : 2) : (ring_ahead(p) ? 4 : 3);
+  uint32_t gone = 0, gone_par = 0;  // that tile % kLen, the parity of its visit
   uint32_t issued = 0, nq = 0;  // this warp's stages; row tiles of Q (tile n uses buffer n % 2)
   bool ok = c.work;
   Walk<CL> walk(c, p);
@@ -311,7 +307,7 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
       const int nb = b0 + 8 * (j + 1 - g.t0);
       if (j + 1 < g.t1) next = lane < 8 && nb < blocks ? row[nb] : -1;
       if (lane == 0) {
-        ok = wait_bar(c, B_EMPTY + r.st, r.par ^ 1);
+        if (issued >= lag) ok = wait_bar(c, (int)(empty - c.bar) + r.st, gone_par);
         if (ok) mbar_arrive_expect_tx(full + r.st, S::kStageBytes);
       }
       ok = __shfl_sync(kFull, (int)ok, 0);
@@ -323,6 +319,10 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
         else
           tma_load_5d(dst, tkv, 0, 0, 0, id >= 0 ? id * 2 : -2, g.kvh, full + r.st);
       }
+      if (issued >= lag && ++gone == Ring<FP8>::kLen) {
+        gone = 0;
+        gone_par ^= 1;
+      }
       ++issued;
       r.next();
     }
@@ -332,7 +332,7 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
   if (lane == 0) {
     Ring<FP8> d(p, kv);
     for (uint32_t k = 0; k < issued; ++k, d.next())
-      if (k + (FP8 ? kCodeStages : kStages) >= issued) mbar_wait(full + d.st, d.par_own, c.limit);
+      if (k + Ring<FP8>::kLen >= issued) mbar_wait(full + d.st, d.par, c.limit);
     for (uint32_t k = nq > 2 ? nq - 2 : 0; k < nq; ++k)
       mbar_wait(c.bar + B_QFULL + (k & 1), (k >> 1) & 1u, c.limit);
   }
@@ -355,7 +355,7 @@ __device__ void s_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
   while (walk.next(p, g)) {
     const bool two = two_tiles(p, g);
     for (int j = g.t0; j < g.t1; ++j) {
-      if (!wait_all(c, B_FULL + r.st, r.par_own)) return;
+      if (!wait_all(c, B_FULL + r.st, r.par)) return;
       const uint32_t kb = sm + S::kOffKV + r.st * S::kStageBytes;
 #pragma unroll 1
       for (int y = 0; y < (two ? 2 : 1); ++y) {
@@ -411,7 +411,7 @@ __device__ void pv_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
     const bool two = two_tiles(p, g);
     for (int j = g.t0; j < g.t1; ++j) {
       if (!(FP8 ? wait_all(c, B_WIDE + (wide & 1), (wide >> 1) & 1)
-                : wait_all(c, B_FULL + kMostStages + r.st, r.par_own)))
+                : wait_all(c, B_FULL + kMostStages + r.st, r.par)))
         return;
       uint8_t* v = c.sm + (FP8 ? S::kOffWide + (wide & 1) * S::kTileBytes
                                : S::kOffKV + r.st * S::kStageBytes);
@@ -456,7 +456,7 @@ __device__ void pv_issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
         if (x) ++cnt[1]; else ++cnt[0];
       }
       if (!two) turn ^= 1;
-      mma_commit(c.bar + (FP8 ? B_WFREE + (wide & 1) : B_EMPTY + r.st));
+      mma_commit(c.bar + (FP8 ? B_WFREE + (wide & 1) : B_EMPTY + kMostStages + r.st));
       __syncwarp();
       if constexpr (FP8)
         ++wide;
@@ -575,13 +575,13 @@ __device__ void converter(const Ctx& c, const TreeParams& p) {
     for (int j = g.t0; j < g.t1; ++j) {
       const uint32_t x = wide & 1;
       if (!wait_all(c, B_WFREE + x, ((wide >> 1) & 1) ^ 1)) return;
-      if (!wait_all(c, B_FULL + kMostStages + r.st, r.par_own)) return;
+      if (!wait_all(c, B_FULL + kMostStages + r.st, r.par)) return;
       widen_rows(c.sm + S::kOffKV + r.st * S::kStageBytes, c.sm + S::kOffWide + x * S::kTileBytes, w,
                  lane, g.n - (g.kv0 + j * kBN));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(c.bar + B_EMPTY + r.st);
+        mbar_arrive(c.bar + B_EMPTY + kMostStages + r.st);
         mbar_arrive(c.bar + B_WIDE + x);
       }
       ++wide;
@@ -669,9 +669,11 @@ __device__ __forceinline__ void weights32(uint32_t taddr, const uint32_t (&s)[32
 // Handing a stream's state over at a segment's end: the warpgroup that finishes first arrives and
 // goes on, the other waits for it.  Two barriers in turn.
 __device__ __forceinline__ void state_given(int par) {
+  __syncwarp();
   asm volatile("bar.arrive %0, 256;" ::"r"(1 + par) : "memory");
 }
 __device__ __forceinline__ void state_taken(int par) {
+  __syncwarp();
   asm volatile("bar.sync %0, 256;" ::"r"(1 + par) : "memory");
 }
 
@@ -891,6 +893,7 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
       record_error(p.status, PA_EINVAL);
       *c.abort = 1;
     }
+    __syncwarp();
     asm volatile("bar.sync 3, 256;" ::: "memory");  // both streams' warps have looked
     bad = __any_sync(kFull, *c.abort != 0);
     if (c.own->t1 <= c.own->t0 && threadIdx.x - 128 < c.own->rows)
@@ -1125,12 +1128,11 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
       uint32_t n = 1;
       if ((i >= B_QCONV && i < B_QCONV + 2) || (i >= B_WIDE && i < B_WIDE + 2)) n = 4;
       // e4m3: four warps read V's codes
-      if (FP8 && i >= B_EMPTY + kCodeStages && i < B_EMPTY + 2 * kCodeStages) n = 4;
+      if (FP8 && i >= B_EMPTY + kMostStages && i < B_EMPTY + 2 * kMostStages) n = 4;
       if (i >= B_PFULL && i < B_PFULL + 2) n = 4;
       if (i >= B_OFREE && i < B_OFREE + 2) n = 4;
       mbar_init(bar + i, n);
     }
-    if (!FP8 && ring_ahead(p)) mbar_arrive(bar + B_EMPTY + 1);
     prefetch_tmap(&tq);
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);

@@ -370,6 +370,29 @@ def test_streams_graphs_and_repeats(pa):
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("S,n,ctx", [(16, 8, 4000), (3, 40, 3000), (64, 4, 600)])
+def test_hundreds_of_calls(pa, S, n, ctx):
+    """Every one of many calls over all SMs gives the first one's bits: no wait runs out, no buffer
+    is taken before it is free, whatever the copies' and products' timing."""
+    for kv in (BF16, E4M3):
+        b = Batch([n] * S, [ctx - 3 * i for i in range(S)], 32, 8, 128, kv=kv, seed=28)
+        T = S * n
+        ws = torch.empty(pa.pa_tree_attention_workspace_size(S, T, 32, 8, 128, b.tables.shape[1], 16),
+                         dtype=torch.uint8, device=DEV)
+        want, _ = b.call(pa, lse=False, workspace=ws)
+        out = torch.empty_like(want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(20):
+                pa.pa_tree_attention(b.q, b.kb, b.vb, out, b.qsl, b.lens, b.pos, b.mask, b.tables,
+                                     b.scale, workspace=ws)
+        for _ in range(30):
+            out.zero_()
+            g.replay()
+            assert torch.equal(out, want)
+        assert pa.pa_device_status() == pa.PA_OK
+
+
 def test_unaligned_and_small_workspace(pa):
     b = Batch([5], [60], 8, 2, 128, seed=26)
     n = pa.pa_tree_attention_workspace_size(1, 5, 8, 2, 128, b.tables.shape[1], 16)
