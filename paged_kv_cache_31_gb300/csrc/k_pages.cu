@@ -3,7 +3,9 @@
 //
 // Copies (k_copy_blocks, k_tree_commit).  Pure data movement, bound by memory: a block of a
 // pool is contiguous (block_size * num_kv_heads * head_dim elements), a position's row is
-// num_kv_heads * head_dim of them.  16-byte accesses, several in flight per thread.
+// num_kv_heads * head_dim of them.  16-byte accesses, several in flight per thread.  Measured
+// (captured graph): 4096 pairs of 32-KB blocks in both pools 76.7 us, 7.0 TB/s, 1.05 of the copy
+// bandwidth; 7 pairs 1.8 us; the accepted rows of 1 tree of 24 nodes 3.0 us, of 256 of 64 5.3 us.
 //
 // Bookkeeping (k_pages).  A few hundred to some 10^5 integers: bound by the latency of its
 // dependent loads, not by bandwidth, so one cluster of eight CTAs does a whole call in one
@@ -13,7 +15,11 @@
 // whose last reference goes away is a bitmap spread over the CTAs' shared memory.  The blocks a
 // call takes or gives back are numbered by prefix sums, never by the order in which atomics
 // arrive, so equal inputs give equal tables and free lists.  Only the reference counts are
-// changed by atomics (integer additions, whose order does not matter).
+// changed by atomics (integer additions, whose order does not matter).  Measured (captured graph,
+// fork + grow + free): 4 children of a parent 17.5 us, 256 of 16 parents 43 us; a call's six or so
+// dependent loads and two or three cluster barriers are its 5.7 us, the 256 forks' reference counts
+// the rest.  Sixteen CTAs to the cluster measured 25.7 and 47.0 us where eight had 24.3 and 50.7
+// (dearer barriers, more loads in flight): not worth a cluster that needs a launch attribute.
 //
 // These kernels write block tables and lengths that a planning kernel behind them may read
 // before it waits for them (pa_varlen_forward's, launched with programmatic dependent launch),

@@ -19,7 +19,9 @@
 // has both sides of each pair in registers.  A CTA takes TOK tokens; their angles are computed
 // once into shared memory and serve all H + Hkv heads.  The items of a token (rotated units, copied
 // chunks and value chunks) are dealt to the threads in memory order; a thread takes its item through
-// the CTA's tokens, four in flight.
+// the CTA's tokens, four in flight.  Measured: 16381 tokens (32 + 2 x 8 heads of 128 out of one
+// fused product, half of each rotated, e4m3 pools) 65 us, 5.7 TB/s, 0.85 of the copy bandwidth; 64
+// tokens of the same heads 3.0 us in a captured graph, which is the launch and two dependent loads.
 #include <algorithm>
 
 #include "pa_internal.cuh"

@@ -12,7 +12,9 @@
 // Why split: a drafted step has few query rows and long contexts, so (sequence, kv head) items
 // alone do not fill the GPU evenly.  All items' key tiles are laid end to end and every CTA
 // takes an equal, contiguous share; the pieces of an item are merged afterwards in key order.
-// How a batch is cut depends on its lengths alone, so equal inputs give equal bits.
+// How a batch is cut depends on its lengths alone, so equal inputs give equal bits.  (Small calls
+// on the tensor cores need none of this: k_tree_tc.cu's clusters.)  Measured beside an attention
+// kernel of 118 us (64 sequences, 151 cuts of up to 128 rows): the plan 4.7 us, the merge 10 us.
 #include <algorithm>
 
 #include "k_tree.cuh"
@@ -197,7 +199,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(const TreeParams p) 
 // computes the scores of rows 4 rg .. 4 rg + 3 and keys c and c + 16, and dims 4c + 64i .. of the
 // same rows' outputs.  It is bound by shared-memory reads (a 16-byte read takes as long as 16 of
 // a warp's FMAs): 9 of them for the 64 FMAs per thread of four dims of Q K^T and one key of P V at
-// head size 128, against 18 when a thread had one row, eight keys and a quarter of the dims.
+// head size 128, against 18 when a thread had one row, eight keys and a quarter of the dims
+// (16 x 16 nodes x 4 heads over 2000 fp32 positions: 563 -> 299 us, 28 TFLOP/s).
 // Rows of the tiles are padded by four floats, so 16-byte reads of different rows hit different
 // banks.
 

@@ -12,8 +12,8 @@
 // row tiles gives each stream one, and both use the same key tiles: each K / V byte that reaches
 // shared memory serves 256 rows.  An item with one row tile gives its key tiles to the
 // streams in turn; the stream that takes the last one joins their states (m, l, O), while the
-// other goes on with the next item.  Either way one
-// stream's MMAs run while the other's exponentials do.
+// other goes on with the next item.  Either way one stream's MMAs run while the other's
+// exponentials do.
 //
 // Per key tile of a stream:  S = Q K^T (M 128, N 128, K = head size);  mask, running max (moved,
 // with O rescaled, only when it grows by more than 2^8), p = 2^(s - m);  P written over S;
@@ -23,11 +23,11 @@
 // power of two per row (exact down to 2^-9 of the row's largest element), two products for S.
 // (Widening K too made the conversions bound the kernel.)  Row sums add the fp32 weights.
 //
-// Roles.  warp 0: TMA of K, warp 3: of Q (a ring of two row tiles) and V; K and V alternate in a
-// ring of five 128-key stages; warp 1: tensor-memory owner, issues S = Q K^T; warp 2: issues
-// O += P V, and zeroes the V rows past the sequence's end (they may hold anything; K's are
-// masked); warps 4..7 and 8..11: the streams' softmax and epilogue; warps 12..15 (e4m3
-// pools): widen Q, K and V in shared memory.
+// Roles.  warp 0: TMA of K, warp 3: of Q (a ring of two row tiles) and V, into a ring of five
+// 128-key stages (bf16) or three stages of codes for each (e4m3); warp 1: tensor-memory owner,
+// issues S = Q K^T; warp 2: issues O += P V, and zeroes the V rows past the sequence's end (they may
+// hold anything; K's are masked); warps 4..7 and 8..11: the streams' softmax and epilogue; warps
+// 12..15 (e4m3 pools): split Q and widen V into one of two f16 tiles.
 //
 // Small calls (CL).  Instead of the planned shares, a cluster of 1 to 8 CTAs for each (sequence, kv
 // head, item): each CTA plans its own part from the sequence's numbers (an even run of the key
@@ -36,8 +36,18 @@
 // three: a tree of 8 nodes over 700 positions takes 8.8 us instead of 14.2.
 //
 // What bounds it: up to 128 rows per kv head, the K / V bytes (a tile is 64 KB of bf16, 1.5 us of
-// an SM's share of the measured copy bandwidth, against 1.0 us of tensor time); with two row
-// tiles, the tensor cores (2.0 us a tile).
+// an SM's share of the measured copy bandwidth, against 0.8 us of tensor time): 64 sequences of up
+// to 32 nodes x 4 heads over 512 to 4096 positions take 118 us, 5.3 TB/s, 0.79 of the copy
+// bandwidth.  With two row tiles, the tensor cores and the chain of a stream (its S has to wait for
+// the P V before it): 4 x 64 nodes x 8 heads over 65536 positions take 528 us, 1040 TFLOP/s of the
+// formulas' work, 1560 with both terms of P, 0.81 of the measured peak.  Over e4m3 pools (half the
+// bytes, V's widening on top) that chain, too: 48 x 16 nodes with a window take 95 us, 4.3 TB/s.
+//
+// Measured and left out: tiles of 64 keys with S and P double-buffered (Q is read twice as often:
+// 160 -> 209 us for the first case above); straight-line loops in any role (the code runs out of
+// the instruction cache); a pass over S saved by looking for larger scores 32 keys at a time, or
+// S loaded ahead (no change: the softmax is not what the chain waits for most); eight converter
+// warps, or widening by integer operations (no change, slower).
 //
 // Every mbarrier wait is bounded; one that runs out records PA_ETIMEOUT and raises an abort flag
 // that ends the other roles' waits.  A softmax warp whose wait fails goes through the rest of its
