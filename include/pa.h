@@ -592,9 +592,10 @@ size_t pa_tree_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, in
  * read only when there is a window.
  * Types, sinks, lse, k_scale / v_scale and k_scales / v_scales as in pa_varlen_forward_ex and
  * pa_varlen_forward_per_head (a per-head array needs a scalar of 1); kv_dtype PA_FP8_E4M3 reads
- * the codes' values times the scales.  Every cached V row of the sequences has to be finite (a
- * masked node's V enters the products with weight zero); K rows of masked keys, and rows at or
- * past seq_lens[s], may hold anything.
+ * the codes' values times the scales, and q has to be finite then (bf16 q: its elements count to
+ * 2^-17 of their row's largest, the softmax weights in f16).  Every cached V row of the sequences
+ * has to be finite (a masked node's V enters the products with weight zero); K rows of masked
+ * keys, and rows at or past seq_lens[s], may hold anything.
  * Validation, on the device before anything is written: query_start_loc starts at 0, never
  * decreases and ends at num_tokens; for a sequence with nodes n <= 32 * mask_words, n <=
  * seq_lens[s], its table covers seq_lens[s] positions with ids in [0, num_blocks), positions >= 0
@@ -604,7 +605,7 @@ size_t pa_tree_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, in
  * workspace: pa_tree_attention_workspace_size(...) bytes, 256-byte aligned, scratch of the caller
  * that calls which overlap on the device must not share.  The results of a call depend on its
  * inputs alone (no atomics on values); how a context is split, and so the last bits of a row,
- * depend on the lengths of the whole batch.
+ * depend on the sizes and the lengths of the whole batch.
  */
 pa_status pa_tree_attention(const void* q, const void* k_blocks, const void* v_blocks, void* out,
                             const int32_t* query_start_loc, const int32_t* seq_lens,

@@ -612,7 +612,7 @@ __device__ __forceinline__ void visible_keys(const TreeParams& p, const TreeSegm
     const int i = (node0 >> 5) + k;
     row[k] = i >= 0 && 32 * i < g.nodes ? (uint32_t)p.mask[(int64_t)tok * p.mask_words + i] : 0u;
   }
-  const int far = pos - p.m.window;
+  const int far = max(pos - p.m.window, -1);  // (not so low that a key's distance overflows)
   // Nodes too far behind pos are looked for one by one, unless none can be: positions are not
   // negative, and a first key kv0 > 0 says that the sequence's lowest one is at least
   // kv0 + window - 1.

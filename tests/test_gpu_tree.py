@@ -140,6 +140,18 @@ def test_windows(pa, window, kv):
     Batch([12, 40, 3], [300, 90, 0], 8, 2, 128, kv=kv, seed=window).check(pa, window=window)
 
 
+@pytest.mark.parametrize("kv", [BF16, E4M3, F32])
+def test_the_widest_windows_hide_nothing(pa, kv):
+    """A key's distance behind the window's edge must not leave 32 bits."""
+    src = F32 if kv == F32 else BF16
+    b = Batch([12, 40, 3], [300, 90, 0], 8, 2, 128, src=src, kv=kv, seed=29)
+    want, _ = b.check(pa)
+    b.pos.zero_()
+    for window in (2 ** 31 - 1, 2 ** 31 - 200, 2 ** 30):
+        out, _ = b.check(pa, window=window)
+        assert torch.equal(out, want)
+
+
 def test_long_context_many_pieces(pa):
     """One sequence over the whole GPU: every item is cut into many pieces."""
     Batch([7], [9001], 8, 1, 128, seed=1).check(pa)
@@ -368,6 +380,34 @@ def test_streams_graphs_and_repeats(pa):
     g.replay()
     want, _ = b.check(pa)
     assert torch.equal(out, want)
+
+
+def test_calls_on_two_streams_at_once(pa):
+    """Small and large calls, each stream with a workspace of its own."""
+    cases = [Batch([8], [700], 32, 8, 128, seed=30), Batch([30] * 6, [2500] * 6, 32, 8, 128, seed=31),
+             Batch([7] * 5, [400] * 5, 8, 2, 128, kv=E4M3, seed=32),
+             Batch([16] * 20, [900] * 20, 32, 8, 128, kv=E4M3, seed=33)]
+    want = [b.call(pa, lse=False)[0] for b in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for i in range(40):
+        for k, s in enumerate(streams):
+            j = (i + 2 * k + k * i) % 4
+            b = cases[j]
+            with torch.cuda.stream(s):
+                out = torch.empty_like(b.q)
+                if i % 2:  # the current stream, or given by name
+                    pa.pa_tree_attention(b.q, b.kb, b.vb, out, b.qsl, b.lens, b.pos, b.mask, b.tables,
+                                         b.scale)
+            if i % 2 == 0:
+                pa.pa_tree_attention(b.q, b.kb, b.vb, out, b.qsl, b.lens, b.pos, b.mask, b.tables,
+                                     b.scale, stream=s)
+            got[k].append((j, out))
+    torch.cuda.synchronize()
+    assert pa.pa_device_status() == pa.PA_OK
+    for j, out in got[0] + got[1]:
+        assert torch.equal(out, want[j])
 
 
 @pytest.mark.parametrize("S,n,ctx", [(16, 8, 4000), (3, 40, 3000), (64, 4, 600)])
