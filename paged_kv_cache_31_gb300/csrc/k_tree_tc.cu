@@ -37,11 +37,11 @@
 //
 // What bounds it: up to 128 rows per kv head, the K / V bytes (a tile is 64 KB of bf16, 1.5 us of
 // an SM's share of the measured copy bandwidth, against 0.8 us of tensor time): 64 sequences of up
-// to 32 nodes x 4 heads over 512 to 4096 positions take 118 us, 5.3 TB/s, 0.79 of the copy
+// to 32 nodes x 4 heads over 512 to 4096 positions take 118 us, 5.9 TB/s, 0.88 of the copy
 // bandwidth.  With two row tiles, the tensor cores and the chain of a stream (its S has to wait for
 // the P V before it): 4 x 64 nodes x 8 heads over 65536 positions take 528 us, 1040 TFLOP/s of the
 // formulas' work, 1560 with both terms of P, 0.81 of the measured peak.  Over e4m3 pools (half the
-// bytes, V's widening on top) that chain, too: 48 x 16 nodes with a window take 95 us, 4.3 TB/s.
+// bytes, V's widening on top) that chain, too: 48 x 16 nodes with a window take 92 us, 3.8 TB/s (52 us at the copy rate).
 //
 // Measured and left out: tiles of 64 keys with S and P double-buffered (Q is read twice as often:
 // 160 -> 209 us for the first case above); straight-line loops in any role (the code runs out of

@@ -119,9 +119,10 @@ bool pool_map_rows(CUtensorMap* map, const void* base, int64_t num_blocks, int h
 
 // TMA descriptor of an fp8 pool [num_blocks, 16, Hkv, 128] (one byte per element) seen as
 // the 3-D byte tensor (128, Hkv, num_blocks * 16): one 128 x 1 x 16 box is a whole K (or V)
-// block tile of one kv head, 2 KB, with the 128-byte swizzle.
+// block tile of one kv head, 2 KB, with the 128-byte swizzle.  one_head: L2 is not to fetch the
+// neighbouring head's 128 bytes with a row.
 bool pool_map_fp8(CUtensorMap* map, const void* base, int64_t num_blocks, int block_size,
-                  int hkv, int d) {
+                  int hkv, int d, bool one_head) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)hkv, (cuuint64_t)(num_blocks * block_size)};
@@ -130,7 +131,7 @@ bool pool_map_fp8(CUtensorMap* map, const void* base, int64_t num_blocks, int bl
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            one_head ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

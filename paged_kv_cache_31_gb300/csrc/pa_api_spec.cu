@@ -290,8 +290,10 @@ pa_status pa_tree_attention(const void* q, const void* k_blocks, const void* v_b
   if (tc) {
     const bool ok =
         query_map(&tq, q, num_tokens, num_heads, head_dim, m.group, p.tile_tokens) &&
-        (fp8 ? pool_map_fp8(&tk, k_blocks, num_blocks, 16, num_kv_heads, head_dim) &&
-                   pool_map_fp8(&tv, v_blocks, num_blocks, 16, num_kv_heads, head_dim)
+        // (the head beside it is read much later, or by another SM: fetched together, 48 x 16 nodes
+        // read 515 MB for 346 MB and took 107.8 us instead of 104.6)
+        (fp8 ? pool_map_fp8(&tk, k_blocks, num_blocks, 16, num_kv_heads, head_dim, true) &&
+                   pool_map_fp8(&tv, v_blocks, num_blocks, 16, num_kv_heads, head_dim, true)
              : pool_map_rows(&tk, k_blocks, num_blocks, num_kv_heads, head_dim) &&
                    pool_map_rows(&tv, v_blocks, num_blocks, num_kv_heads, head_dim));
     if (!ok) return PA_ECUDA;

@@ -659,7 +659,7 @@ const DeviceState* device_state();
 // tensor maps (false: the driver refused), waits and paths of the attention kernels; see pa_api.cu
 bool pool_map_rows(CUtensorMap* map, const void* base, int64_t num_blocks, int hkv, int d);
 bool pool_map_fp8(CUtensorMap* map, const void* base, int64_t num_blocks, int block_size,
-                  int hkv, int d);
+                  int hkv, int d, bool one_head = false);
 bool query_map(CUtensorMap* map, const void* q, int64_t num_tokens, int h, int d, int group,
                int tokens);
 void stall_hook(uint64_t& limit, uint32_t& stall);
