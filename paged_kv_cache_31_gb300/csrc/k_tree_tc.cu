@@ -972,11 +972,14 @@ __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, u
         if (hides) tmem_wait_st();
         // (the scale is positive on this path, so it commutes with the max)
         const float m_new = fmaxf(m_ref, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl);
-        const bool resc = m_new > m_ref + 8.f;
+        // (f16 weights are taken 2^7 times as large, up to 2^15: what rounds to a multiple of f16's
+        // smallest step is off by 2^-32 of the row's largest weight, not by 2^-25)
+        constexpr float kUp = FP8 ? 7.f : 0.f;
+        const bool resc = m_new > m_ref + (8.f + kUp);
         float alpha = 1.f;
         if (resc) {
-          alpha = fast_exp2(m_ref - m_new);  // 0 when nothing was visible before
-          m_ref = m_new;
+          alpha = fast_exp2(m_ref - (m_new - kUp));  // 0 when nothing was visible before
+          m_ref = m_new - kUp;
           l *= alpha;
         }
         const float nb = m_ref == -INFINITY ? 0.f : -m_ref;

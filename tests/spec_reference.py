@@ -65,13 +65,16 @@ def unpack_mask(mask, nodes):
 
 
 def tree_attention(q, kb, vb, qsl, lens, positions, mask, tables, scale, window=0, sinks=None,
-                   k_scales=None, v_scales=None, weight_u=2.0 ** -16, q_u=0.0):
+                   k_scales=None, v_scales=None, weight_u=2.0 ** -16, q_u=0.0,
+                   weight_min=0.0):
     """(out [T, H, D], lse [H, T], bound of out before its own rounding, bound of lse), 64 bits.
 
     k_scales, v_scales: per kv head (or None).  weight_u: the softmax weights' rounding where they
     enter the product with V (a bf16 pair 2^-16, f16 2^-11, fp32 less than either).  q_u: what q's
     elements may be off by, relative to their row's largest (0: q is used as it is; a pair of
-    e4m3 terms 2^-17: half of e4m3's smallest step, 2^-10, where the largest is at least 2^7)."""
+    e4m3 terms 2^-17: half of e4m3's smallest step, 2^-10, where the largest is at least 2^7).
+    weight_min: what a small weight is off by, relative to a sum of 1 (f16: half its smallest step,
+    2^-25, where the row's largest weight is at least 2^7: 2^-32)."""
     T, H, D = q.shape
     NB, bs, Hkv, _ = kb.shape
     G = H // Hkv
@@ -122,7 +125,7 @@ def tree_attention(q, kb, vb, qsl, lens, positions, mask, tables, scale, window=
             # for the product, and fp32 sums over L keys
             big = torch.where(see, x[:, :L].abs(), 0.0).amax(1, keepdim=True) + m.abs()
             e = 4 * d + 4 * big * U32 + 2.0 ** -20 + weight_u + 2 * L * U32
-            out_b[a:b, h] = (p @ Vn.abs()) * e
+            out_b[a:b, h] = (p @ Vn.abs()) * e + weight_min * (see.double() @ Vn.abs())
             lse_b[h, a:b] = (2 * d + 4 * big * U32 + 2.0 ** -20 + L * U32)[:, 0]
     lse_b += 4 * U32 * torch.nan_to_num(lse, neginf=0.0).abs()
     return out, lse, out_b, lse_b

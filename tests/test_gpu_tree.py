@@ -77,7 +77,8 @@ class Batch:
         want, wl, ob, lb = tree_attention(self.q, self.kb, self.vb, self.qsl, self.lens, self.pos,
                                           self.mask, self.tables, self.scale, window, sinks, ks,
                                           vs, weight_u=u,
-                                          q_u=2.0 ** -17 if self.kb.dtype == E4M3 else 0.0)
+                                          q_u=2.0 ** -17 if self.kb.dtype == E4M3 else 0.0,
+                                          weight_min=2.0 ** -32 if self.kb.dtype == E4M3 else 0.0)
         assert_within(out, want, ob + (want.abs() + ob) * OUT_U[self.q.dtype] + 2.0 ** -126, "out")
         assert_within(lse, wl, lb, "lse")
         kw = dict(window=window, sinks=sinks, k_scale=k_scale, v_scale=v_scale, k_scales=k_scales,
@@ -216,6 +217,23 @@ def test_uneven_queries_over_e4m3_pools(pa):
     b.check(pa, k_scale=2.0 ** -40)
     b.mask[9] = 0
     b.check(pa, window=3)
+
+
+def test_many_small_weights(pa):
+    """One key far above thousands whose weights are small but make up the whole output."""
+    for kv, gap in ((E4M3, 26.0), (E4M3, 30.0), (BF16, 30.0)):
+        S, ctx = 16, 1900
+        b = Batch([4] * S, [ctx] * S, 8, 8, 128, kv=kv, seed=34)
+        b.q[:] = 0.0
+        b.q[:, :, 0] = 1.0
+        b.kb[:, :, :, 0] = 0.0
+        b.vb[:] = 8.0
+        for s in range(S):
+            b.kb[b.tables[s, 3], 5, :, 0] = 32.0
+            b.vb[b.tables[s, 3], 5] = 0.0
+        b.scale = gap * 0.6931471805599453 / 32.0  # the other weights are 2^-gap of the largest
+        out, _ = b.check(pa)
+        assert abs(float(out[0, 0, 0]) / (ctx * 2.0 ** -gap * 8.0) - 1.0) < 2.0 ** -6
 
 
 def test_rows_that_see_nothing(pa):
