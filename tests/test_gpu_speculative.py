@@ -264,16 +264,19 @@ def _stalled_waits(ns):
 
 @pytest.mark.parametrize("kv", [BF16, E4M3])
 @pytest.mark.parametrize("nodes", [[5, 9, 2], [24, 40, 3]])
-def test_tree_attention_timeout_unwinds_and_the_device_stays_usable(pa, kv, nodes):
+@pytest.mark.parametrize("columns", [100, 1200])
+def test_tree_attention_timeout_unwinds_and_the_device_stays_usable(pa, kv, nodes, columns):
     """PA_DEBUG_STALL_NS points the softmax waits at a barrier that nothing signals, each wait
-    bounded at 20 ms: the status says so, nothing is written, the next call gives the same bits."""
+    bounded at 20 ms: the status says so, nothing is written, the next call gives the same bits
+    (short tables: clusters that join their states; long ones: planned shares)."""
     gen = torch.Generator().manual_seed(51)
     S, T, ctx, NB = len(nodes), sum(nodes), 1500, 330
     q = torch.randn(T, H, D, generator=gen).to(BF16).to(DEV)
     kb, vb = (torch.randn(NB, BLOCK, HKV, D, generator=gen).to(kv).to(DEV) for _ in range(2))
     qsl = _i32([sum(nodes[:i]) for i in range(S + 1)])
     lens = _i32([ctx + n for n in nodes])
-    tables = torch.randperm(NB, generator=gen)[:S * 100].int().view(S, 100).to(DEV)
+    tables = torch.zeros(S, columns, dtype=torch.int32, device=DEV)
+    tables[:, :100] = torch.randperm(NB, generator=gen)[:S * 100].int().view(S, 100).to(DEV)
     mask = torch.randint(-2 ** 31, 2 ** 31 - 1, (T, 2), generator=gen).int().to(DEV)
     pos = torch.zeros(T, dtype=torch.int32, device=DEV)
 

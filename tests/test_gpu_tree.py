@@ -329,9 +329,12 @@ def _bad(pa, b, change, **kw):
         getattr(b, k).copy_(v)
 
 
-@pytest.mark.parametrize("kv", [BF16, F32])
-def test_bad_metadata_writes_nothing(pa, kv):
+@pytest.mark.parametrize("kv,wide", [(BF16, False), (BF16, True), (E4M3, False), (E4M3, True),
+                                     (F32, False)])
+def test_bad_metadata_writes_nothing(pa, kv, wide):
     b = Batch([5, 40, 3], [60, 20, 0], 8, 2, 128, src=F32 if kv == F32 else BF16, kv=kv, seed=23)
+    if wide:  # (long tables: the planned shares)
+        b.tables = torch.cat([b.tables, b.tables.new_zeros(3, 1100)], 1).contiguous()
     NB = b.kb.shape[0]
 
     def put(name, at, value):
