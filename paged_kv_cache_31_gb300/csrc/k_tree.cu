@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "k_tree.cuh"
+#include "pa_tcgen05.cuh"
 
 namespace pa {
 namespace {
@@ -200,7 +201,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(const TreeParams p) 
 // same rows' outputs.  It is bound by shared-memory reads (a 16-byte read takes as long as 16 of
 // a warp's FMAs): 9 of them for the 64 FMAs per thread of four dims of Q K^T and one key of P V at
 // head size 128, against 18 when a thread had one row, eight keys and a quarter of the dims
-// (16 x 16 nodes x 4 heads over 2000 fp32 positions: 563 -> 299 us, 28 TFLOP/s).
+// (16 x 16 nodes x 4 heads over 2000 fp32 positions: 563 -> 299 us).  The arithmetic is packed, two
+// fp32 to an instruction, and the loops written out by eight: 275 us, 31 TFLOP/s.
 // Rows of the tiles are padded by four floats, so 16-byte reads of different rows hit different
 // banks.
 
@@ -296,13 +298,13 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
         *reinterpret_cast<float4*>(sq + (r0 + u * kStep) * LD + col) = a[u];
     }
     float mx[4], l[4];
-    float4 o[4][kDI];
+    ulonglong2 o[4][kDI];  // packed pairs of fp32
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       mx[k] = -INFINITY;
       l[k] = 0.f;
 #pragma unroll
-      for (int i = 0; i < kDI; ++i) o[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < kDI; ++i) o[k][i] = make_ulonglong2(0, 0);
     }
     const int32_t* trow = m.block_tables + (int64_t)sg.s * m.max_blocks;
     for (int j = sg.t0; j < sg.t1; ++j) {
@@ -332,21 +334,29 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
         }
       }
       __syncthreads();
-      float x[4][2] = {};
-#pragma unroll 2
+      uint64_t x2[4][2] = {};  // sums over even and over odd dims, two to a packed instruction
+#pragma unroll 8
       for (int d4 = 0; d4 < DP; d4 += 4) {
-        float4 b[2];
+        ulonglong2 b[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          b[i] = *reinterpret_cast<const float4*>(sk + (c + 16 * i) * LD + d4);
+          b[i] = *reinterpret_cast<const ulonglong2*>(sk + (c + 16 * i) * LD + d4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float4 a = *reinterpret_cast<const float4*>(sq + (rg + k) * LD + d4);
+          const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(sq + (rg + k) * LD + d4);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            x[k][i] += a.x * b[i].x + a.y * b[i].y + a.z * b[i].z + a.w * b[i].w;
+          for (int i = 0; i < 2; ++i) x2[k][i] = f2_fma(a.y, b[i].y, f2_fma(a.x, b[i].x, x2[k][i]));
         }
       }
+      float x[4][2];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float even, odd;
+          f2_unpack(x2[k][i], even, odd);
+          x[k][i] = even + odd;
+        }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -365,10 +375,8 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
         l[k] = l[k] * alpha + (x[k][0] + x[k][1]);  // this thread's keys; summed at the end
 #pragma unroll
         for (int i = 0; i < kDI; ++i) {
-          o[k][i].x *= alpha;
-          o[k][i].y *= alpha;
-          o[k][i].z *= alpha;
-          o[k][i].w *= alpha;
+          o[k][i].x = f2_mul(o[k][i].x, f2_pack(alpha, alpha));
+          o[k][i].y = f2_mul(o[k][i].y, f2_pack(alpha, alpha));
         }
       }
 #pragma unroll
@@ -376,19 +384,18 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
         *reinterpret_cast<float4*>(sp + (c + 16 * i) * kLDP + rg) =
             make_float4(x[0][i], x[1][i], x[2][i], x[3][i]);
       __syncwarp();  // a row's weights come from its own warp
-#pragma unroll 4
+#pragma unroll 8
       for (int kk = 0; kk < kBN; ++kk) {
         const float4 w4 = *reinterpret_cast<const float4*>(sp + kk * kLDP + rg);
-        const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+        const uint64_t w[4] = {f2_pack(w4.x, w4.x), f2_pack(w4.y, w4.y), f2_pack(w4.z, w4.z),
+                               f2_pack(w4.w, w4.w)};
 #pragma unroll
         for (int i = 0; i < kDI; ++i) {
-          const float4 b = *reinterpret_cast<const float4*>(sv + kk * LD + 4 * c + 64 * i);
+          const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(sv + kk * LD + 4 * c + 64 * i);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            o[k][i].x += w[k] * b.x;
-            o[k][i].y += w[k] * b.y;
-            o[k][i].z += w[k] * b.z;
-            o[k][i].w += w[k] * b.w;
+            o[k][i].x = f2_fma(w[k], b.x, o[k][i].x);
+            o[k][i].y = f2_fma(w[k], b.y, o[k][i].y);
           }
         }
       }
@@ -410,7 +417,9 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
       TQ* out = static_cast<TQ*>(p.out) + ((int64_t)tok[k] * m.num_heads + h) * D;
 #pragma unroll
       for (int i = 0; i < kDI; ++i) {
-        const float v[4] = {o[k][i].x, o[k][i].y, o[k][i].z, o[k][i].w};
+        float v[4];
+        f2_unpack(o[k][i].x, v[0], v[1]);
+        f2_unpack(o[k][i].y, v[2], v[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int d = 4 * c + 64 * i + e;
