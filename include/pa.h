@@ -588,8 +588,8 @@ size_t pa_tree_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, in
  *     tree_mask[t * mask_words + i / 32] is set (its ancestors and itself),
  * of which a sliding_window w > 0 leaves the keys with logical position > positions[t] - w (j for
  * a context position, positions[] of a node).  out = softmax(scale * q . K) V over those keys; a
- * token that sees no key gets 0 and lse -inf.  Bits of nodes >= n are ignored.  positions are
- * read only when there is a window.
+ * token that sees no key gets 0 and lse -inf; one with a score of NaN or +inf gets NaN in both.
+ * Bits of nodes >= n are ignored.  positions are read only when there is a window.
  * Types, sinks, lse, k_scale / v_scale and k_scales / v_scales as in pa_varlen_forward_ex and
  * pa_varlen_forward_per_head (a per-head array needs a scalar of 1); kv_dtype PA_FP8_E4M3 reads
  * the codes' values times the scales, and q has to be finite then (bf16 q: its elements count to

@@ -77,7 +77,9 @@ __device__ __forceinline__ bool tree_visible(const TreeParams& p, const TreeSegm
 
 // The factor that normalises a row's output, given its running max (log2 units) and exp-sum;
 // a sink (a virtual position with score sinks[h] and value zero) joins the sum, and the row's
-// lse is written when asked for.  A row that sees nothing gets 0 and lse -inf.
+// lse is written when asked for.  A row that sees nothing (its sum is 0) gets 0 and lse -inf; a
+// sum that is NaN (a score was NaN or +inf) makes the factor and the lse NaN, so that a row
+// spoiled by its inputs never looks like an empty one.
 __device__ __forceinline__ float tree_finish(const TreeParams& p, int kvh, int h, int tok, float mx,
                                              float l, bool write_lse) {
   const VarlenMeta& m = p.m;
@@ -90,8 +92,8 @@ __device__ __forceinline__ float tree_finish(const TreeParams& p, int kvh, int h
     mx = m2;
   }
   if (m.lse && write_lse)
-    m.lse[(int64_t)h * m.num_tokens + tok] = l > 0.f ? (mx + log2f(l)) * kLn2 : -INFINITY;
-  return l > 0.f ? a * head_scale(m.v_scales, kvh, m.v_scale) / l : 0.f;
+    m.lse[(int64_t)h * m.num_tokens + tok] = l == 0.f ? -INFINITY : (mx + log2f(l)) * kLn2;
+  return l == 0.f ? 0.f : a * head_scale(m.v_scales, kvh, m.v_scale) / l;
 }
 
 }  // namespace pa
