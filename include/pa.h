@@ -592,9 +592,9 @@ size_t pa_tree_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, in
  * Bits of nodes >= n are ignored.  positions are read only when there is a window.
  * Types, sinks, lse, k_scale / v_scale and k_scales / v_scales as in pa_varlen_forward_ex and
  * pa_varlen_forward_per_head (a per-head array needs a scalar of 1); kv_dtype PA_FP8_E4M3 reads
- * the codes' values times the scales, and q has to be finite then (bf16 q: its elements count to
- * 2^-17 of their row's largest, the softmax weights in f16).  Every cached V row of the sequences
- * has to be finite (a masked node's V enters the products with weight zero); K rows of masked
+ * the codes' values times the scales (bf16 q: its elements count to 2^-17 of their row's largest,
+ * a row with an infinity counts as NaN; the softmax weights in f16).  Every cached V row of the
+ * sequences has to be finite (a masked node's V enters the products with weight zero); K rows of masked
  * keys, and rows at or past seq_lens[s], may hold anything.
  * Validation, on the device before anything is written: query_start_loc starts at 0, never
  * decreases and ends at num_tokens; for a sequence with nodes n <= 32 * mask_words, n <=

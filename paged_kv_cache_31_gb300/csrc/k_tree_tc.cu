@@ -511,7 +511,8 @@ __device__ __forceinline__ void widen_rows(const uint8_t* codes, uint8_t* tile, 
 // in the first half's rows, lo in the second's (rows of 128 bytes, swizzled as they were).  With the
 // row times 2^s, its largest magnitude in [128, 256), hi is the nearest code and lo the rest: eight
 // significant bits in two of four, exactly, for elements down to 2^-9 of the row's largest (and to
-// 2^-17 of it below that).  Two lanes share a row, a dim half each.
+// 2^-17 of it below that).  NaN elements give NaN codes, an infinite one the whole row.  Two lanes
+// share a row, a dim half each.
 __device__ __forceinline__ void split_q(uint8_t* tile, int8_t* exps, int w, int lane) {
   constexpr int kHalf = 128 * 128;
 #pragma unroll 1
@@ -530,7 +531,8 @@ __device__ __forceinline__ void split_q(uint8_t* tile, int8_t* exps, int w, int 
     }
     m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
     const int exp = min(max(134 - (int)(__float_as_uint(m) >> 23), -120), 120);
-    const float up = __uint_as_float((uint32_t)(127 + exp) << 23);
+    // (e4m3 has no infinity to saturate to: a row that holds one becomes NaN as a whole)
+    const float up = m < INFINITY ? __uint_as_float((uint32_t)(127 + exp) << 23) : NAN;
     __syncwarp();  // both lanes of every row have loaded it
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

@@ -59,6 +59,19 @@ def test_an_infinity_in_q_is_not_an_empty_row(pa, form):
     assert pa.pa_device_status() == pa.PA_OK
 
 
+@pytest.mark.parametrize("form", ["one CTA", "cluster", "shares", "general"])
+def test_an_infinity_in_q_over_e4m3_pools(pa, form):
+    """The tensor cores' forms split q into e4m3 terms, which have no infinity."""
+    b = batch(form, E4M3, 53)
+    want = b.call(pa)
+    spoiled = torch.zeros(17, 32, dtype=torch.bool, device=DEV)
+    for t, h, d, x in ((0, 3, 64, float("inf")), (12, 30, 1, float("-inf"))):
+        b.q[t, h, d] = x
+        spoiled[t, h] = True
+    same_but(b.call(pa), want, spoiled)
+    assert pa.pa_device_status() == pa.PA_OK
+
+
 @pytest.mark.parametrize("kv", [BF16, E4M3])
 @pytest.mark.parametrize("form", ["one CTA", "cluster", "shares", "general"])
 def test_a_nan_in_a_visible_key(pa, form, kv):
