@@ -551,8 +551,9 @@ pa_status pa_rope_frequencies(int32_t rotary_dim, double base, const pa_rope_sca
  *             position).  Pair i of a head's first rotary_dim elements, (x_i, x_(i + rotary_dim/2))
  *             or (x_2i, x_(2i+1)) when interleaved, becomes
  *               attn_factor * (a cos t - b sin t, a sin t + b cos t),  t = position * inv_freq[i];
- *             elements from rotary_dim on are unchanged.  The angle is exact to 2^-25 half turns
- *             at any position (fp32 products lose it at far positions); arithmetic in fp32.
+ *             elements from rotary_dim on are unchanged.  The angle is off by less than 1.03 *
+ *             2^-25 half turns at any position, for frequencies below 2^53 (fp32 products lose it
+ *             at far positions); arithmetic in fp32.
  *   pools     as in pa_reshape_and_cache_ex: K stored as rotated value / scale, V as value / scale,
  *             rounded once to kv_dtype (e4m3 saturates), into row slot_mapping[t].  The scales are
  *             k_scale / v_scale, or k_scales / v_scales [num_kv_heads] DEVICE (NULL: the scalars;

@@ -9,10 +9,10 @@
 //
 // Angles.  In fp32 the product p * inv_freq is off by up to 2^-24 p radians: 0.06 at a million
 // positions.  Here each frequency becomes the fraction of a turn per position as a 64-bit
-// fixed-point number, once per CTA and in fp64 (fp64 is slow on this GPU: R / 2 values of five
-// operations), and a position's angle is one 64-bit integer product that wraps at whole turns,
-// exactly.  Its top 32 bits go to sincospif as a signed fraction of half a turn (off by at
-// most 2^-25 half turns).
+// fixed-point number (turn_per_position, once per CTA), and a position's angle is one 64-bit integer
+// product that wraps at whole turns, exactly: off by less than 2^-33 turns at the farthest.  Its top
+// 32 bits go to sincospif as a signed fraction of half a turn (off by at most 2^-25 half turns; the
+// dropped bits are less than 2^-31).
 //
 // What bounds it: memory.  Every element of q, k and v is read once and written once, 16 bytes
 // at a time; a rotated half-layout unit is the two 16-byte chunks of its pairs, so a thread
@@ -47,6 +47,23 @@ struct FastDiv {
     return (uint32_t)(((uint64_t)n * m) >> (31 + l));
   }
 };
+
+// The fraction of a turn that w radians are, times 2^64 and rounded down (towards zero for w < 0):
+// w = m 2^e with an integer m < 2^53, so it is bits 64 - e .. 127 - e of m times C = 2^128 / (2 pi).
+// (In fp64 even a product's one rounding is 2^-53 of w, which far positions multiply; and the integer
+// products are the faster ones here.)  |w| < 2^53, else 0.
+__device__ __forceinline__ uint64_t turn_per_position(double w) {
+  constexpr uint64_t kHigh = 0x28be60db9391054aull, kLow = 0x7f09d5f47d4d3770ull;  // C
+  const uint64_t bits = (uint64_t)__double_as_longlong(w);
+  const int field = (int)(bits >> 52) & 0x7ff;
+  const uint64_t m = (bits & 0xfffffffffffffull) | (field ? 1ull << 52 : 0ull);
+  const int s = 1075 - max(field, 1);  // -e: from the product's second word on
+  const uint64_t low = __umul64hi(m, kLow), mid = m * kHigh + low;
+  const uint64_t high = __umul64hi(m, kHigh) + (mid < low ? 1 : 0);
+  uint64_t t = 0;
+  if (s >= 0 && s < 128) t = s >= 64 ? high >> (s - 64) : s ? mid >> s | high << (64 - s) : mid;
+  return bits >> 63 ? 0 - t : t;
+}
 
 struct Geometry {
   uint32_t per_token;  // items of one token
@@ -142,10 +159,7 @@ __global__ void __launch_bounds__(kThreads)
   pdl_launch_dependents();
   if (threadIdx.x == 0) s_skip = status_set(p.status) ? 1 : 0;
   const int half = p.rotary_dim >> 1;
-  for (int i = threadIdx.x; i < half; i += kThreads) {
-    const double f = p.inv_freq[i] * 0.15915494309189533577;  // turns per position
-    s_turn[i] = (uint64_t)__double2ll_rn((f - rint(f)) * 18446744073709551616.0);
-  }
+  for (int i = threadIdx.x; i < half; i += kThreads) s_turn[i] = turn_per_position(p.inv_freq[i]);
   __syncthreads();
   if (s_skip) return;
   if constexpr (CHECKED) {
