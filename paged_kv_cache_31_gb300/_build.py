@@ -4,8 +4,9 @@ Each translation unit under csrc/ is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a`` and linked into
 ``paged_kv_cache_31_gb300/libpa.so`` (static CUDA runtime; the driver's tensor-map
 encoder is reached through cudaGetDriverEntryPointByVersion, so libcuda is not linked).
-csrc/pa_calls.cpp (host code over torch's C++ headers) becomes the Python module ``_calls.so``
-next to it, which is linked to libpa.so.
+csrc/pa_calls.cpp (host code over torch's C++ headers) becomes the Python module ``_calls`` next to
+it, which is linked to libpa.so.  Its file name holds the Python and torch that it was compiled
+for, so it is built anew, and no other one is loaded, after either has changed.
 """
 from __future__ import annotations
 
@@ -22,7 +23,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpa.so")
-CALLS = os.path.join(PKG, "_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]
@@ -39,16 +39,29 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps():
-    return sources() + [os.path.join(CSRC, "pa_calls.cpp")] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
-        os.path.join(INCLUDE, "pa.h")]
+def calls_path() -> str:
+    """The module _calls of this Python and torch."""
+    import torch
+
+    return os.path.join(PKG, f"_calls.{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}.so")
+
+
+def _newer(target: str, deps) -> bool:
+    return os.path.exists(target) and all(
+        os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
+
+
+def lib_up_to_date() -> bool:
+    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")]
+    return _newer(LIB, [*sources(), *headers, os.path.join(INCLUDE, "pa.h")])
+
+
+def calls_up_to_date() -> bool:
+    return _newer(calls_path(), [os.path.join(CSRC, "pa_calls.cpp"), os.path.join(INCLUDE, "pa.h")])
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return lib_up_to_date() and calls_up_to_date()
 
 
 def _compile_calls(nvcc: str) -> str:
@@ -71,22 +84,27 @@ def _compile_calls(nvcc: str) -> str:
 def _link_calls(obj: str) -> None:
     import torch
 
-    tmp = CALLS + f".tmp{os.getpid()}"
+    path = calls_path()
+    tmp = path + f".tmp{os.getpid()}"
     libs = ["-L", os.path.join(os.path.dirname(torch.__file__), "lib")]
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libpa.so", "-Wl,-rpath,$ORIGIN", *libs,
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
+    os.replace(tmp, path)
+    for f in os.listdir(PKG):  # those of another torch
+        if f.startswith("_calls") and f.endswith(".so") and f != os.path.basename(path):
+            os.remove(os.path.join(PKG, f))
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and up_to_date():
+    lib, calls = force or not lib_up_to_date(), force or not calls_up_to_date()
+    if not (lib or calls):
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
-    srcs = sources()
+    srcs = sources() if lib else []
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
@@ -100,16 +118,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
     workers = max(1, min(len(srcs) + 1, os.cpu_count() or 4))
     with concurrent.futures.ThreadPoolExecutor(max_workers=workers) as ex:
-        calls = ex.submit(_compile_calls, nvcc)
+        calls_obj = ex.submit(_compile_calls, nvcc) if calls else None
         objs = list(ex.map(compile_one, srcs))
-        calls = calls.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_calls(calls)
+        if lib:
+            tmp = LIB + f".tmp{os.getpid()}"
+            cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, LIB)
+        if calls:
+            _link_calls(calls_obj.result())
     return LIB
 
 

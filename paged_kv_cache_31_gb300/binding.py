@@ -5,16 +5,21 @@ checks their shapes / dtypes / contiguity, passes raw pointers and the current
 stream to the library, and raises ``PaError`` on a non-OK status.  It does no
 arithmetic of its own: every step of the path runs in the library's kernels.
 The speculative-decoding calls have their checks in the compiled module ``_calls``
-(csrc/pa_calls.cpp), as ctypes took longer than their kernels.
+(csrc/pa_calls.cpp), as ctypes took longer than their kernels; without that module, or with one
+built for another torch, they alone raise ImportError.
 Importing this module loads the library and raises if it has not been built
 (``python -c "import __graft_entry__ as g; g.build()"``); there is no fallback.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
+
+from . import _build
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpa.so")
@@ -24,7 +29,32 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _calls  # noqa: E402  (linked to libpa.so)
+
+
+class _NoCalls:
+    """In the module's place when it cannot be loaded."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the module _calls, which {name} needs, is not built for this Python and "
+                          f"torch ({self._why}); run __graft_entry__.build() first")
+
+
+def _load_calls():
+    path, name = _build.calls_path(), f"{__package__}._calls"
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    try:
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location(name, path, loader=loader))
+        loader.exec_module(module)
+    except ImportError as e:
+        return _NoCalls(e)
+    return module
+
+
+_calls = _load_calls()  # (linked to libpa.so)
 
 PA_OK, PA_EINVAL, PA_ESHAPE, PA_EUNSUPPORTED, PA_ECUDA, PA_ETIMEOUT = range(6)
 PA_F32, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
