@@ -579,6 +579,18 @@ size_t pa_tree_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, in
                                         int32_t num_kv_heads, int32_t head_dim,
                                         int32_t max_blocks_per_seq, int32_t block_size);
 
+/* pa_tree_attention_form -- how pa_tree_attention goes about a call of these sizes on the current
+ * device (tensors on 16-byte boundaries, a positive scale): *row_tiles 0: the general kernel, in
+ * three launches; 1 or 2: the tensor cores, items of that many tiles of query rows, *cluster CTAs
+ * to each in one launch, or (*cluster 0) shares of all items in three launches.  row_tiles and
+ * cluster are HOST pointers.  Sizes as there; without tokens PA_EINVAL.  It goes by the width of the
+ * table, not by the lengths (which are on the device): where a step is captured over tables as wide
+ * as the longest allowed sequence, short sequences take the shares, too. */
+pa_status pa_tree_attention_form(int32_t num_seqs, int64_t num_tokens, int32_t mask_words,
+                                 int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                 int32_t max_blocks_per_seq, int32_t block_size, pa_dtype q_dtype,
+                                 pa_dtype kv_dtype, int32_t* row_tiles, int32_t* cluster);
+
 /*
  * pa_tree_attention -- attention of trees of drafted tokens over the paged cache.  Sequence s has
  * n = query_start_loc[s + 1] - query_start_loc[s] nodes, cached as its LAST n positions: node i

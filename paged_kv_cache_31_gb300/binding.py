@@ -127,6 +127,8 @@ _SIGS = {
     "pa_rope_and_cache": ([_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
                            _i32, _i32, _f32, _i64, _i32, _i32, _i32, _i32, _i64, ctypes.c_int,
                            ctypes.c_int, _f32, _f32, _vp, _vp, _vp], ctypes.c_int),
+    "pa_tree_attention_form": ([_i32, _i64, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_int,
+                                ctypes.c_int, _vp, _vp], ctypes.c_int),
     "pa_tree_attention_workspace_size": ([_i32, _i64, _i32, _i32, _i32, _i32, _i32], _sz),
     "pa_tree_attention": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32,
                            _i32, _i32, _i32, _i64, _i32, ctypes.c_int, ctypes.c_int, _f32, _i32,
@@ -606,6 +608,20 @@ def pa_tree_attention_workspace_size(num_seqs, num_tokens, num_heads, num_kv_hea
                                      max_blocks_per_seq, block_size) -> int:
     return int(_lib.pa_tree_attention_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads,
                                                      head_dim, max_blocks_per_seq, block_size))
+
+
+def pa_tree_attention_form(num_seqs, num_tokens, mask_words, num_heads, num_kv_heads, head_dim,
+                           max_blocks_per_seq, block_size, q_dtype=torch.bfloat16,
+                           kv_dtype=torch.bfloat16):
+    """(row tiles of an item, CTAs of a cluster): how pa_tree_attention goes about a call of these
+    sizes.  (0, 0): the general kernel; (n, 0): planned shares, three launches; (n, c): clusters of
+    c CTAs, one launch."""
+    tiles, cluster = _i32(), _i32()
+    _check(_lib.pa_tree_attention_form(num_seqs, num_tokens, mask_words, num_heads, num_kv_heads,
+                                       head_dim, max_blocks_per_seq, block_size, _DT[q_dtype],
+                                       _DT[kv_dtype], ctypes.byref(tiles), ctypes.byref(cluster)),
+           "pa_tree_attention_form")
+    return tiles.value, cluster.value
 
 
 def pa_tree_attention(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, positions, tree_mask,

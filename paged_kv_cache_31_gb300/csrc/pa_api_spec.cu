@@ -157,6 +157,63 @@ static int32_t tree_cluster(int32_t num_seqs, int32_t num_kv_heads, int32_t item
   return most <= share * 7 / 10 + kTreeSmallTiles ? c : 0;
 }
 
+// Types and sizes that the tensor-core kernel takes: bf16 q over bf16 or e4m3 pools of 16-position
+// blocks, a group that fits a row tile.
+static bool tree_tc_takes(int32_t group, int32_t head_dim, int32_t block_size, pa_dtype q_dtype,
+                          pa_dtype kv_dtype) {
+  return q_dtype == PA_BF16 && block_size == 16 && group <= 128 &&
+         (kv_dtype == PA_FP8_E4M3 ? head_dim == 128
+                                  : kv_dtype == PA_BF16 && (head_dim == 64 || head_dim == 128));
+}
+
+// How a call on the tensor-core kernel goes: clusters, of items of one row tile (more of them, on
+// more SMs) or else of two, or (cluster 0) the planned shares.
+struct TreeForm {
+  int32_t row_tiles;       // of an item, at most
+  int32_t items, cluster;  // items of a (sequence, kv head), at most; CTAs to each
+};
+static TreeForm tree_tc_form(int32_t num_seqs, int64_t num_tokens, int32_t mask_words, int32_t group,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks, bool fp8,
+                             int32_t sms) {
+  const int64_t most = std::min<int64_t>(32 * (int64_t)mask_words, num_tokens) * group;
+  const int32_t tile = tree_tile_rows(group), wide = most > tile ? 2 : 1;
+  TreeForm f{0, 0, 0};
+  while (f.row_tiles < wide && !f.cluster) {
+    ++f.row_tiles;
+    f.items = (int32_t)((most + f.row_tiles * tile - 1) / (f.row_tiles * tile));
+    f.cluster = tree_cluster(num_seqs, num_kv_heads, f.items, f.row_tiles, (int64_t)max_blocks * 16,
+                             max_blocks, sms, fp8, head_dim);
+  }
+  return f;
+}
+
+pa_status pa_tree_attention_form(int32_t num_seqs, int64_t num_tokens, int32_t mask_words,
+                                 int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                 int32_t max_blocks_per_seq, int32_t block_size, pa_dtype q_dtype,
+                                 pa_dtype kv_dtype, int32_t* row_tiles, int32_t* cluster) {
+  if (num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
+      num_heads % num_kv_heads != 0)
+    return PA_ESHAPE;
+  if (!dtype_ok(q_dtype) || !pool_dtype_ok(kv_dtype) || head_dim > 256 ||
+      mask_words > kTreeMaxMaskWords || num_tokens > INT32_MAX / 2 ||
+      num_tokens * (num_heads / num_kv_heads) > INT32_MAX / 2 ||
+      (int64_t)max_blocks_per_seq * block_size > INT32_MAX - 1024)
+    return PA_EUNSUPPORTED;
+  if (num_seqs <= 0 || num_tokens <= 0 || mask_words <= 0 || max_blocks_per_seq < 0 || !row_tiles ||
+      !cluster)
+    return PA_EINVAL;
+  *row_tiles = *cluster = 0;
+  const int32_t group = num_heads / num_kv_heads;
+  if (!tree_tc_takes(group, head_dim, block_size, q_dtype, kv_dtype) || !tc_enabled()) return PA_OK;
+  const DeviceState* d = device_state();
+  if (!d) return PA_ECUDA;
+  const TreeForm f = tree_tc_form(num_seqs, num_tokens, mask_words, group, num_kv_heads, head_dim,
+                                  max_blocks_per_seq, kv_dtype == PA_FP8_E4M3, d->sms);
+  *row_tiles = f.row_tiles;
+  *cluster = f.cluster;
+  return PA_OK;
+}
+
 size_t pa_tree_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads,
                                         int32_t num_kv_heads, int32_t head_dim,
                                         int32_t max_blocks_per_seq, int32_t block_size) {
@@ -247,28 +304,21 @@ pa_status pa_tree_attention(const void* q, const void* k_blocks, const void* v_b
   p.q_bf16 = q_dtype == PA_BF16;
   const int64_t max_keys = (int64_t)max_blocks_per_seq * block_size;
   const bool fp8 = kv_dtype == PA_FP8_E4M3;
-  // the tensor-core kernel: bf16 q over bf16 or e4m3 pools of 16-position blocks, a group that
-  // fits a row tile, tensors aligned for TMA, and a positive scale (its row maxima are taken
-  // before the scale)
-  const bool tc = q_dtype == PA_BF16 && block_size == 16 && m.group <= 128 &&
-                  (fp8 ? head_dim == 128
-                       : kv_dtype == PA_BF16 && (head_dim == 64 || head_dim == 128)) &&
+  // the tensor-core kernel: its types and sizes, tensors aligned for TMA, and a positive scale (its
+  // row maxima are taken before the scale)
+  const bool tc = tree_tc_takes(m.group, head_dim, block_size, q_dtype, kv_dtype) &&
                   aligned(q, 16) && aligned(out, 16) && aligned(k_blocks, 16) &&
                   aligned(v_blocks, 16) && p.scale > 0.f && num_blocks > 0 && tc_enabled();
   TreeLayout L;
   if (tc) {
     p.tile_rows = tree_tile_rows(m.group);
     p.tile_tokens = p.tile_rows / m.group;
-    const int64_t most = std::min<int64_t>(32 * (int64_t)mask_words, num_tokens) * m.group;
     p.key_tile = kTreeTcKeys;
-    // small calls: clusters, of items of one row tile (more of them, on more SMs) or else of two
-    const int32_t wide = most > p.tile_rows ? 2 : 1;
-    for (int32_t tiles = 1; tiles <= wide && !p.cluster; ++tiles) {
-      p.rows_per_item = tiles * p.tile_rows;
-      p.items = (int32_t)((most + p.rows_per_item - 1) / p.rows_per_item);
-      p.cluster = tree_cluster(num_seqs, num_kv_heads, p.items, tiles, max_keys, max_blocks_per_seq,
-                               d->sms, fp8, head_dim);
-    }
+    const TreeForm f = tree_tc_form(num_seqs, num_tokens, mask_words, m.group, num_kv_heads, head_dim,
+                                    max_blocks_per_seq, fp8, d->sms);
+    p.rows_per_item = f.row_tiles * p.tile_rows;
+    p.items = f.items;
+    p.cluster = f.cluster;
     L = tree_tc_layout(num_seqs, num_tokens, m.group, num_kv_heads, head_dim, max_keys,
                        p.rows_per_item);
     L.grid = p.cluster ? num_seqs * num_kv_heads * p.items * p.cluster

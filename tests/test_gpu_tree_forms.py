@@ -1,5 +1,6 @@
 """pa_tree_attention in each of its forms (clusters of one and of several CTAs, planned shares, the
-general kernel): inputs that are not finite."""
+general kernel): which one a call takes, clusters over items of two row tiles, and inputs that are
+not finite."""
 import pytest
 import torch
 
@@ -15,12 +16,71 @@ def widen(b, columns):
     b.tables = t
 
 
-def batch(form, kv, seed):
-    ctx = [60, 31] if form == "one CTA" else [700, 300]
-    b = Batch([12, 5], ctx, 32, 8, 128, src=F32 if form == "general" else BF16, kv=kv, seed=seed)
-    if form == "shares":
+def form(pa, b):
+    """(row tiles of an item, CTAs of a cluster) that the batch's call takes."""
+    T, H, D = b.q.shape
+    return pa.pa_tree_attention_form(len(b.nodes), T, b.mask.shape[1], H, b.kb.shape[2], D,
+                                     b.tables.shape[1], b.bs, b.q.dtype, b.kb.dtype)
+
+
+def batch(pa, name, kv, seed):
+    ctx = [60, 31] if name == "one CTA" else [700, 300]
+    b = Batch([12, 5], ctx, 32, 8, 128, src=F32 if name == "general" else BF16, kv=kv, seed=seed)
+    if name == "shares":
         widen(b, 1100)
+    tiles, cluster = form(pa, b)
+    assert tiles == (0 if name == "general" else 1)
+    assert cluster == 1 if name == "one CTA" else cluster > 1 if name == "cluster" else cluster == 0
     return b
+
+
+@pytest.mark.parametrize("kv", [BF16, E4M3])
+@pytest.mark.parametrize("window", [0, 3, 700])
+def test_clusters_of_one_over_two_row_tiles(pa, kv, window):
+    """Ten trees of up to 40 nodes x 4 heads: 160 rows, 80 items of two row tiles, a CTA to each."""
+    b = Batch([40, 33, 1, 40, 32, 17, 40, 0, 39, 40], [530 - 50 * i for i in range(10)], 32, 8, 128,
+              kv=kv, seed=61)
+    assert form(pa, b) == (2, 1)
+    b.check(pa, window=window)
+
+
+@pytest.mark.parametrize("kv", [BF16, E4M3])
+@pytest.mark.parametrize("window", [0, 40, 700])
+def test_clusters_of_several_over_two_row_tiles(pa, kv, window):
+    """Trees of up to 160 nodes x 4 heads over up to 6400 positions, a cluster to each 256 rows.  The
+    last item of 160 and of 150 nodes has one row tile, 17 nodes are one; the third sequence's
+    clusters have CTAs without a key tile, with a window all have."""
+    b = Batch([160, 150, 90, 17], [6400, 900, 64, 3000], 4, 1, 128, kv=kv, seed=62)
+    widen(b, 418)
+    tiles, cluster = form(pa, b)
+    assert tiles == 2 and cluster > 1
+    b.check(pa, window=window)
+    b.mask[200:230] = 0  # rows that see only the context, and with a narrow window little of it
+    b.check(pa, window=window)
+
+
+def test_two_row_tiles_of_head_size_64(pa):
+    for nodes, ctx, H, Hkv in (([40] * 10, [500] * 10, 32, 8), ([160, 70, 33, 1], [6400, 10, 0, 90], 4, 1),
+                               ([30, 26, 25] * 4, [200, 31, 90] * 4, 40, 8)):
+        b = Batch(nodes, ctx, H, Hkv, 64, seed=63)
+        if ctx[0] == 6400:
+            widen(b, 418)
+        tiles, cluster = form(pa, b)
+        assert tiles == 2 and cluster >= 1
+        b.check(pa)
+        b.check(pa, window=100)
+
+
+def test_which_form(pa):
+    """The sizes alone decide: the width of the table, not the lengths."""
+    ask = pa.pa_tree_attention_form
+    assert ask(1, 8, 1, 32, 8, 128, 45, 16)[0] == 1 and ask(1, 8, 1, 32, 8, 128, 45, 16)[1] > 1
+    assert ask(1, 8, 1, 32, 8, 128, 8193, 16) == (1, 0)      # more entries than a CTA checks
+    assert ask(64, 1024, 1, 32, 8, 128, 258, 16) == (1, 0)   # more units than SMs
+    assert ask(4, 256, 2, 64, 8, 128, 4200, 16) == (2, 0)
+    assert ask(1, 8, 1, 32, 8, 128, 45, 32) == ask(1, 8, 1, 32, 8, 96, 45, 16) == (0, 0)
+    assert ask(1, 8, 1, 32, 8, 64, 45, 16, kv_dtype=E4M3) == (0, 0)
+    assert ask(1, 8, 1, 32, 8, 128, 45, 16, F32, BF16) == (0, 0)
 
 
 def same_but(got, want, spoiled):
@@ -33,10 +93,10 @@ def same_but(got, want, spoiled):
 
 
 @pytest.mark.parametrize("kv", [BF16, E4M3])
-@pytest.mark.parametrize("form", ["one CTA", "cluster", "shares", "general"])
-def test_a_nan_in_q_is_not_an_empty_row(pa, form, kv):
+@pytest.mark.parametrize("name", ["one CTA", "cluster", "shares", "general"])
+def test_a_nan_in_q_is_not_an_empty_row(pa, name, kv):
     """Every score of the row is NaN, so are its output and its lse; other rows do not notice."""
-    b = batch(form, kv, 50)
+    b = batch(pa, name, kv, 50)
     want = b.call(pa)
     spoiled = torch.zeros(17, 32, dtype=torch.bool, device=DEV)
     for t, h, d in ((2, 5, 17), (11, 31, 127), (13, 0, 0)):
@@ -46,10 +106,10 @@ def test_a_nan_in_q_is_not_an_empty_row(pa, form, kv):
     assert pa.pa_device_status() == pa.PA_OK
 
 
-@pytest.mark.parametrize("form", ["one CTA", "cluster", "shares", "general"])
-def test_an_infinity_in_q_is_not_an_empty_row(pa, form):
+@pytest.mark.parametrize("name", ["one CTA", "cluster", "shares", "general"])
+def test_an_infinity_in_q_is_not_an_empty_row(pa, name):
     """Some scores are +inf (the keys' elements have both signs), and inf - inf is NaN."""
-    b = batch(form, BF16, 51)
+    b = batch(pa, name, BF16, 51)
     want = b.call(pa)
     spoiled = torch.zeros(17, 32, dtype=torch.bool, device=DEV)
     for t, h, d, x in ((0, 3, 64, float("inf")), (12, 30, 1, float("-inf"))):
@@ -59,10 +119,10 @@ def test_an_infinity_in_q_is_not_an_empty_row(pa, form):
     assert pa.pa_device_status() == pa.PA_OK
 
 
-@pytest.mark.parametrize("form", ["one CTA", "cluster", "shares", "general"])
-def test_an_infinity_in_q_over_e4m3_pools(pa, form):
+@pytest.mark.parametrize("name", ["one CTA", "cluster", "shares", "general"])
+def test_an_infinity_in_q_over_e4m3_pools(pa, name):
     """The tensor cores' forms split q into e4m3 terms, which have no infinity."""
-    b = batch(form, E4M3, 53)
+    b = batch(pa, name, E4M3, 53)
     want = b.call(pa)
     spoiled = torch.zeros(17, 32, dtype=torch.bool, device=DEV)
     for t, h, d, x in ((0, 3, 64, float("inf")), (12, 30, 1, float("-inf"))):
@@ -73,11 +133,11 @@ def test_an_infinity_in_q_over_e4m3_pools(pa, form):
 
 
 @pytest.mark.parametrize("kv", [BF16, E4M3])
-@pytest.mark.parametrize("form", ["one CTA", "cluster", "shares", "general"])
-def test_a_nan_in_a_visible_key(pa, form, kv):
+@pytest.mark.parametrize("name", ["one CTA", "cluster", "shares", "general"])
+def test_a_nan_in_a_visible_key(pa, name, kv):
     """One key of one kv head: the rows that see it, and they alone, come out as NaN, whichever of
     the pieces of the context it lies in."""
-    b = batch(form, kv, 52)
+    b = batch(pa, name, kv, 52)
     want = b.call(pa)
     x = b.kb.float()
     x[b.tables[0, 1], 3, 2, 9] = float("nan")
