@@ -1,6 +1,6 @@
 """pa_tree_attention in each of its forms (clusters of one and of several CTAs, planned shares, the
-general kernel): which one a call takes, clusters over items of two row tiles, and inputs that are
-not finite."""
+general kernel): which one a call takes, clusters over items of two row tiles, many calls each with
+an output of its own, and inputs that are not finite."""
 import pytest
 import torch
 
@@ -145,4 +145,29 @@ def test_a_nan_in_a_visible_key(pa, name, kv):
     spoiled = torch.zeros(17, 32, dtype=torch.bool, device=DEV)
     spoiled[:12, 8:12] = True  # sequence 0, the four heads of kv head 2
     same_but(b.call(pa), want, spoiled)
+    assert pa.pa_device_status() == pa.PA_OK
+
+
+@pytest.mark.parametrize("kv", [BF16, E4M3])
+@pytest.mark.parametrize("S,n,ctx", [(16, 8, 4000), (3, 40, 3000), (64, 4, 600), (10, 40, 500)])
+def test_every_call_of_many_gives_the_same_bits(pa, S, n, ctx, kv):
+    """4000 calls in captured graphs, each with an output and an lse of its own, all of them compared.
+    (This finds what goes wrong once in some thousand calls, not what does once in 50 000.)"""
+    b = Batch([n] * S, [ctx - 3 * i for i in range(S)], 32, 8, 128, kv=kv, seed=28)
+    ws = torch.empty(pa.pa_tree_attention_workspace_size(S, S * n, 32, 8, 128, b.tables.shape[1], 16),
+                     dtype=torch.uint8, device=DEV)
+    out, lse = b.call(pa, workspace=ws)
+    outs, lses = (torch.empty(20, *x.shape, dtype=x.dtype, device=DEV) for x in (out, lse))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for o, ls in zip(outs, lses):
+            pa.pa_tree_attention(b.q, b.kb, b.vb, o, b.qsl, b.lens, b.pos, b.mask, b.tables, b.scale,
+                                 workspace=ws, lse=ls)
+    wrong = torch.zeros((), dtype=torch.int64, device=DEV)
+    for _ in range(200):
+        outs.zero_()
+        lses.zero_()
+        g.replay()
+        wrong += (outs != out).sum() + (lses != lse).sum()
+    assert int(wrong) == 0
     assert pa.pa_device_status() == pa.PA_OK
