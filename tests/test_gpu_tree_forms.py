@@ -1,10 +1,12 @@
 """pa_tree_attention in each of its forms (clusters of one and of several CTAs, planned shares, the
 general kernel): which one a call takes, clusters over items of two row tiles, many calls each with
-an output of its own, and inputs that are not finite."""
+an output of its own, the general kernel at its own bounds, tensors off a 16-byte boundary, and inputs
+that are not finite."""
 import pytest
 import torch
 
-from tests.test_gpu_tree import BF16, DEV, E4M3, F32, Batch, pa  # noqa: F401
+from tests.spec_reference import OUT_U, assert_within, tree_attention
+from tests.test_gpu_tree import BF16, DEV, E4M3, F32, RAGGED, Batch, pa  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -171,3 +173,54 @@ def test_every_call_of_many_gives_the_same_bits(pa, S, n, ctx, kv):
         wrong += (outs != out).sum() + (lses != lse).sum()
     assert int(wrong) == 0
     assert pa.pa_device_status() == pa.PA_OK
+
+
+def check_general(b, got, window=0):
+    """The bounds of fp32 weights and of q as it is: no bf16 pairs, no f16, no terms of e4m3."""
+    out, lse = got
+    want, wl, ob, lb = tree_attention(b.q, b.kb, b.vb, b.qsl, b.lens, b.pos, b.mask, b.tables, b.scale,
+                                      window, weight_u=2.0 ** -24)
+    assert_within(out, want, ob + (want.abs() + ob) * OUT_U[b.q.dtype] + 2.0 ** -126, "out")
+    assert_within(lse, wl, lb, "lse")
+
+
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("src,kv,D,bs", [
+    (F32, F32, 128, 16), (F32, F32, 64, 5), (F32, BF16, 64, 16), (F32, E4M3, 128, 16),
+    (BF16, F32, 128, 16), (BF16, BF16, 96, 16), (BF16, BF16, 128, 64), (BF16, E4M3, 64, 16),
+    (BF16, E4M3, 128, 32), (BF16, BF16, 256, 16), (F32, F32, 100, 16)])
+def test_the_general_kernel_keeps_32_bits(pa, src, kv, D, bs, window):
+    b = Batch(*RAGGED, 8, 2, D, src=src, kv=kv, bs=bs, seed=64)
+    assert form(pa, b) == (0, 0)
+    check_general(b, b.call(pa, window=window), window)
+
+
+def shifted(t):
+    """A copy that begins one element behind a 16-byte boundary."""
+    x = torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)[1:t.numel() + 1].view(t.shape)
+    assert x.data_ptr() % 16 != 0
+    return x.copy_(t)
+
+
+@pytest.mark.parametrize("kv", [BF16, E4M3])
+def test_one_tensor_off_a_boundary(pa, kv):
+    """Any of q, the pools and out by itself sends the call to the general kernel."""
+    b = Batch([9, 40, 1], [300, 17, 60], 8, 2, 128, kv=kv, seed=65)
+    first = None
+    for name in ("q", "kb", "vb", "out"):
+        keep = getattr(b, name, None)
+        out = torch.full_like(b.q, float("nan"))
+        if name == "out":
+            out = shifted(out)
+        else:
+            setattr(b, name, shifted(keep))
+        lse = torch.full((8, 50), float("nan"), device=DEV)
+        pa.pa_tree_attention(b.q, b.kb, b.vb, out, b.qsl, b.lens, b.pos, b.mask, b.tables, b.scale,
+                             lse=lse)
+        assert pa.pa_device_status() == pa.PA_OK
+        check_general(b, (out, lse))
+        first = first or (out.clone(), lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+        if name != "out":
+            setattr(b, name, keep)
+    b.check(pa)  # and all of them on boundaries, the tensor cores' kernel
