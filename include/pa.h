@@ -671,11 +671,14 @@ pa_status pa_copy_blocks(void* k_blocks, void* v_blocks, const int32_t* block_pa
  *   ref_counts   [num_blocks]: rows that hold each block;
  *   free_list    [num_blocks], free_count [1]: the ids of the blocks that nobody holds are
  *                free_list[0 .. *free_count - 1], each once (the caller sets this up).
- * Blocks are taken from the end of the free list.  Each call checks everything before it writes:
- * a row outside [0, num_rows), a written row listed twice, a length that is negative or beyond
- * the table, an id outside the pool, a held block without a reference, a free block with one, too
- * few free blocks, or a count outside [0, num_blocks] records PA_EINVAL and leaves every array as
- * it was.  num_rows <= 65536, num_blocks <= 2^23 and num_rows * max_blocks_per_seq < 2^31, else
+ * Blocks are taken from the end of the free list.  Each call checks everything that it uses before
+ * it writes: a row outside [0, num_rows), a written row listed twice, a length that is negative or
+ * beyond the table, an entry that it shares or lets go outside the pool or without a reference, a
+ * block taken from the free list that is outside the pool or has a reference, too few free blocks,
+ * or a count outside [0, num_blocks] records PA_EINVAL and leaves every array as it was.  Entries
+ * that stay as they are (all that a growing row holds, those in front of a trimmed row's end) and
+ * free blocks that are not taken are not looked at.  num_rows <= 65536, num_blocks <= 2^23 and
+ * num_rows * max_blocks_per_seq < 2^31, else
  * PA_EUNSUPPORTED.  Calls on the same arrays must not overlap on the device.
  *
  * pa_fork_sequences -- fork f makes row children[f] a copy of row parents[f]: whole blocks are
