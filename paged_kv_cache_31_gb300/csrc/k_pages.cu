@@ -17,8 +17,8 @@
 // arrive, so equal inputs give equal tables and free lists.  Only the reference counts are
 // changed by atomics (integer additions, whose order does not matter).  Measured (captured graph,
 // fork + grow + free): 4 children of a parent 17.5 us, 256 of 16 parents 43 us; a call's six or so
-// dependent loads and two or three cluster barriers are its 5.7 us, the 256 forks' reference counts
-// the rest.  Sixteen CTAs to the cluster measured 25.7 and 47.0 us where eight had 24.3 and 50.7
+// dependent loads and two or three cluster barriers are its 5.7 us, the 256 forks' (and their end's)
+// 10^5 table entries and the counts of their blocks the rest, 18 us each.  Sixteen CTAs to the cluster measured 25.7 and 47.0 us where eight had 24.3 and 50.7
 // (dearer barriers, more loads in flight): not worth a cluster that needs a launch attribute.
 //
 // These kernels write block tables and lengths that a planning kernel behind them may read

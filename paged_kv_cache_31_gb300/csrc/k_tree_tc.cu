@@ -33,15 +33,20 @@
 // head, item): each CTA plans its own part from the sequence's numbers (an even run of the key
 // tiles), its softmax warps check the whole batch while the first tiles are on their way, and the
 // CTAs' states are joined in key order through distributed shared memory.  One launch instead of
-// three: a tree of 8 nodes over 700 positions takes 9.2 us instead of 14.2.
+// three: a tree of 8 nodes over 700 positions takes 9.3 us instead of 16 (behind a table for 12 000
+// positions or more, which the rule for the form leaves to the shares).
 //
 // What bounds it: up to 128 rows per kv head, the K / V bytes (a tile is 64 KB of bf16, 1.5 us of
 // an SM's share of the measured copy bandwidth, against 0.8 us of tensor time): 64 sequences of up
 // to 32 nodes x 4 heads over 512 to 4096 positions take 118 us, 5.9 TB/s, 0.88 of the copy
 // bandwidth.  With two row tiles, the tensor cores and the chain of a stream (its S has to wait for
-// the P V before it): 4 x 64 nodes x 8 heads over 65536 positions take 528 us, 1040 TFLOP/s of the
-// formulas' work, 1560 with both terms of P, 0.81 of the measured peak.  Over e4m3 pools (half the
-// bytes, V's widening on top) that chain, too: 48 x 16 nodes with a window take 92 us, 3.8 TB/s (52 us at the copy rate).
+// the P V before it): 4 x 64 nodes x 8 heads over 65536 positions take 528 us at their best, 1040
+// TFLOP/s of the formulas' work, 1560 with both terms of P, 0.81 of the measured peak; at full power
+// the clock, and the time, depend on the box: up to 625 us.  Over e4m3 pools (half the bytes, V's
+// widening on top) that chain, too: 48 x 16 nodes with a window take 94 us, 3.8 TB/s (52 us at the
+// copy rate).  So does head size 64 (half the bytes over the same tiles): 64 sequences of up to 32
+// nodes x 4 heads, a call of 90 us for 43 at the copy rate.  Items of up to 64 rows leave half of
+// the lanes of S, P and O, and of the products, empty.
 //
 // Measured and left out: tiles of 64 keys with S and P double-buffered (Q is read twice as often:
 // 160 -> 209 us for the first case above); straight-line loops in any role (the code runs out of

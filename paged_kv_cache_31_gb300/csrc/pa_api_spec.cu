@@ -138,7 +138,10 @@ static TreeLayout tree_tc_layout(int32_t num_seqs, int64_t num_tokens, int32_t g
 // larger cluster gives), no larger than the key tiles that a table can hold.  The slowest CTA's key
 // tiles decide: they may be as many as a CTA's even share of the batch (taken as 0.7 of what the
 // tables can hold: few sequences are as long as the longest) and the nine that the two other
-// launches are worth.  Measured (us, clusters / shares, bf16, 32 rows a kv head): 8 units of 5 tiles
+// launches are worth.  The lengths are on the device, so the width of the table stands for them: one
+// sequence of 8 kv heads leaves the clusters behind a table for about 12 000 positions, 8 at 5 000,
+// 16 at 2 500, any call with more than kTreeSmallEntries entries, however short its sequences are (8
+// nodes over 700 positions: 9.3 / 15.9 us in a graph).  Measured (us, clusters / shares, bf16, 32 rows a kv head): 8 units of 5 tiles
 // 8.7 / 15.3, of 63 tiles 16.9 / 21.4; 128 units of 16 tiles 30.7 / 38.3, of 64 tiles 93 / 100.
 static int32_t tree_cluster(int32_t num_seqs, int32_t num_kv_heads, int32_t items, int32_t wide,
                             int64_t max_keys, int32_t max_blocks, int32_t sms, bool fp8,
