@@ -508,6 +508,10 @@ pa_status pa_gather_kv(const void* k_blocks, const void* v_blocks, void* k_out, 
  * pages of forked, growing, shortened and ended sequences are kept by pa_fork_sequences,
  * pa_grow_sequences, pa_trim_sequences and pa_free_sequences; pa_copy_blocks makes the copies
  * that forks ask for, in every layer's pools.
+ *
+ * Where a call is several launches, another stream's pa_device_status() may clear the error that the
+ * first one recorded before the next one reads it.  Such a call may then write those of its outputs
+ * whose indices are valid; nothing outside its arrays is read or written.
  */
 
 /* Long-context scalings of the rotary frequencies (pa_rope_frequencies). */

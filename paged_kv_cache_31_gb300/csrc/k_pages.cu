@@ -18,8 +18,13 @@
 // changed by atomics (integer additions, whose order does not matter).  Measured (captured graph,
 // fork + grow + free): 4 children of a parent 17.5 us, 256 of 16 parents 43 us; a call's six or so
 // dependent loads and two or three cluster barriers are its 5.7 us, the 256 forks' (and their end's)
-// 10^5 table entries and the counts of their blocks the rest, 18 us each.  Sixteen CTAs to the cluster measured 25.7 and 47.0 us where eight had 24.3 and 50.7
-// (dearer barriers, more loads in flight): not worth a cluster that needs a launch attribute.
+// 10^5 table entries and the counts of their blocks the rest, 18 us each.  Sixteen CTAs to the
+// cluster measured 25.7 and 47.0 us where eight had 24.3 and 50.7 (dearer barriers, more loads in
+// flight): not worth a cluster that needs a launch attribute.
+//
+// Lists too long for every CTA to check are checked by a kernel in front, which records what it finds
+// in the device's status word.  Another stream may read and clear that word in between, so the kernel
+// behind it does not rest its own bounds on it: it leaves out the entries that lie outside.
 //
 // These kernels write block tables and lengths that a planning kernel behind them may read
 // before it waits for them (pa_varlen_forward's, launched with programmatic dependent launch),
@@ -165,7 +170,7 @@ __global__ void __launch_bounds__(256)
   const int pi = blockIdx.x / chunks;
   const int64_t at = (int64_t)(blockIdx.x % chunks) * (256 * U) + threadIdx.x;
   const int2 pr = pairs[pi];
-  if (pr.x < 0) return;
+  if (pr.x < 0 || (!CHECKED && pair_bad(pr, num_blocks))) return;
   VEC* pool = blockIdx.y ? v_blocks : k_blocks;
   const VEC* src = pool + pr.x * units;
   VEC* dst = pool + pr.y * units;
@@ -195,21 +200,26 @@ cudaError_t copy_as(void* kb, void* vb, const int32_t* pairs, int64_t n, int64_t
 
 // ---- moving accepted rows together ------------------------------------------------------------
 
-// Entry e = (s, i) of the accepted lists: false when the call has to be refused.
+// Entry e = (s, i) of the accepted lists: false when the call has to be refused.  from, to: the
+// positions of the pool (block id * block_size + place) that it moves, when it has a node.
 __device__ __forceinline__ bool accepted_ok(const int32_t* tables, const int32_t* ctx,
                                             const int32_t* accepted, const int32_t* num_accepted,
                                             int s, int i, int max_accepted, int max_blocks,
-                                            int block_size, int64_t num_blocks) {
+                                            int block_size, int64_t num_blocks, int64_t& from,
+                                            int64_t& to) {
   const int na = num_accepted[s], c = ctx[s];
   if (na < 0 || na > max_accepted || c < 0) return false;
   if (i >= na) return true;
   const int32_t* list = accepted + (int64_t)s * max_accepted;
   const int a = list[i], before = i ? list[i - 1] : -1;
-  if (a <= before) return false;
-  const int64_t from = ((int64_t)c + a) / block_size, to = ((int64_t)c + i) / block_size;
-  if (from >= max_blocks) return false;  // (to <= from, as a >= i)
+  if (a <= before || a < i) return false;  // (a < i: some entry in front does not increase)
+  const int64_t p = (int64_t)c + a, q = (int64_t)c + i;
+  const int64_t pb = p / block_size, qb = q / block_size;
+  if (pb >= max_blocks) return false;  // (q <= p, as a >= i)
   const int32_t* row = tables + (int64_t)s * max_blocks;
-  const int32_t x = row[from], y = row[to];
+  const int32_t x = row[pb], y = row[qb];
+  from = (int64_t)x * block_size + (p - pb * block_size);
+  to = (int64_t)y * block_size + (q - qb * block_size);
   return x >= 0 && (int64_t)x < num_blocks && y >= 0 && (int64_t)y < num_blocks;
 }
 
@@ -222,10 +232,12 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
   pdl_launch_dependents();
   bool bad = false;
+  int64_t from, to;
   const int64_t n = (int64_t)num_seqs * max_accepted;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256)
     bad |= !accepted_ok(tables, ctx, accepted, num_accepted, (int)(e / max_accepted),
-                        (int)(e % max_accepted), max_accepted, max_blocks, block_size, num_blocks);
+                        (int)(e % max_accepted), max_accepted, max_blocks, block_size, num_blocks,
+                        from, to);
   if (__syncthreads_or(bad) && threadIdx.x == 0) record_error(status, PA_EINVAL);
 }
 
@@ -247,29 +259,28 @@ __global__ void __launch_bounds__(256)
   if (threadIdx.x == 0) s_skip = status_set(status) ? 1 : 0;
   __syncthreads();
   if (s_skip) return;
+  int64_t from, to;
   if constexpr (CHECKED) {
     bool bad = false;
     for (int e = threadIdx.x; e < num_seqs * max_accepted; e += 256)
       bad |= !accepted_ok(tables, ctx, accepted, num_accepted, e / max_accepted, e % max_accepted,
-                          max_accepted, max_blocks, block_size, num_blocks);
+                          max_accepted, max_blocks, block_size, num_blocks, from, to);
     if (__syncthreads_or(bad)) {
       if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_error(status, PA_EINVAL);
       return;
     }
   }
-  const int s = blockIdx.x, na = num_accepted[s], c = ctx[s];
+  const int s = blockIdx.x, na = min(num_accepted[s], max_accepted);
   const int64_t u = (int64_t)blockIdx.y * 256 + threadIdx.x;
   VEC* pool = u < row ? k_blocks + u : v_blocks + (u - row);
-  const int32_t* trow = tables + (int64_t)s * max_blocks;
   for (int i0 = 0; i0 < na; i0 += kRows) {
     const int m = min(kRows, na - i0);
     __syncthreads();  // the group before has been read
     if ((int)threadIdx.x < m) {
-      const int64_t from = (int64_t)c + accepted[(int64_t)s * max_accepted + i0 + threadIdx.x];
-      const int64_t to = (int64_t)c + i0 + threadIdx.x;
-      s_from[threadIdx.x] =
-          ((int64_t)trow[from / block_size] * block_size + from % block_size) * row;
-      s_to[threadIdx.x] = ((int64_t)trow[to / block_size] * block_size + to % block_size) * row;
+      const bool ok = accepted_ok(tables, ctx, accepted, num_accepted, s, i0 + threadIdx.x,
+                                  max_accepted, max_blocks, block_size, num_blocks, from, to);
+      s_from[threadIdx.x] = ok ? from * row : 0;  // (not ok: nothing is moved)
+      s_to[threadIdx.x] = ok ? to * row : 0;
     }
     __syncthreads();
     if (u >= 2 * row) continue;

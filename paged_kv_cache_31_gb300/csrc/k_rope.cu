@@ -175,7 +175,11 @@ __global__ void __launch_bounds__(kThreads)
   }
   const int64_t t0 = (int64_t)blockIdx.x * tok_per_cta;
   const int ntok = (int)min((int64_t)tok_per_cta, p.num_tokens - t0);
-  if ((int)threadIdx.x < ntok) s_slot[threadIdx.x] = p.slots[t0 + threadIdx.x];
+  if ((int)threadIdx.x < ntok) {
+    const int32_t s = p.slots[t0 + threadIdx.x];
+    // (not CHECKED: the status may have been cleared since the slots were found bad)
+    s_slot[threadIdx.x] = CHECKED || (s >= 0 && (int64_t)s < p.num_slots) ? s : -1;
+  }
   float* s_cos = s_trig;
   float* s_sin = s_trig + tok_per_cta * half;
   for (int a = threadIdx.x; a < ntok * half; a += kThreads) {
@@ -269,6 +273,7 @@ __global__ void __launch_bounds__(kThreads)
           if (two) store_chunk<SRC, VE>(p.q_out, at + half, b);
           continue;
         }
+        if (!CHECKED && s_slot[tk] < 0) continue;
         if (divide) {
 #pragma unroll
           for (int i = 0; i < VE; ++i) {

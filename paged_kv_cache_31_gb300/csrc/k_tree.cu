@@ -59,7 +59,10 @@ __device__ __forceinline__ int64_t item_weight(const TreeParams& p, int tiles, i
 
 // Block 0 plans; blocks 1 .. check the table entries of the sequences, one warp per 256 entries.
 // Everything is read after the wait for the kernels ahead, and nothing is written by the
-// attention kernel before this whole launch is done, so an error leaves the outputs untouched.
+// attention kernel before this whole launch is done, so an error leaves the outputs untouched.  (The
+// status word may be cleared by another stream before the kernels behind read it.  Their indices hold
+// all the same: a plan that failed is one of empty shares, and block ids are looked at again where
+// they are used, by the copies' tensor maps or the general kernel.)
 __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(const TreeParams p) {
   __shared__ int64_t s_warp[32];
   __shared__ int64_t s_cum[kCumShared + 1];
@@ -166,6 +169,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_tree_plan(const TreeParams p) 
   bad = __syncthreads_or(bad);
   if (bad) {
     if (tid == 0) record_error(p.status, PA_EINVAL);
+    for (int c = tid; c <= p.grid; c += kPlanThreads) p.starts[c] = make_int4(m.num_seqs, 0, 0, 0);
     return;
   }
   // where each CTA's share begins
@@ -310,10 +314,10 @@ __global__ void __launch_bounds__(128) k_tree_generic(const TreeParams p, const 
     for (int j = sg.t0; j < sg.t1; ++j) {
       const int key0 = sg.kv0 + j * kBN;
       if (tid < kBN) {
-        const int key = key0 + tid;
-        s_row[tid] = key < sg.n ? ((int64_t)trow[key / m.block_size] * m.block_size +
-                                   key % m.block_size) * m.num_kv_heads + sg.kvh
-                                : -1;
+        const int key = key0 + tid, id = key < sg.n ? trow[key / m.block_size] : -1;
+        s_row[tid] = id >= 0 && (int64_t)id < m.num_blocks
+                         ? ((int64_t)id * m.block_size + key % m.block_size) * m.num_kv_heads + sg.kvh
+                         : -1;
       }
       __syncthreads();  // (the tile before has been used, too)
       for (int k0 = tid / kCols; k0 < kBN; k0 += 4 * kStep) {
@@ -449,8 +453,7 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeParams p) {
   const VarlenMeta& m = p.m;
   const int b = blockIdx.x, lane = threadIdx.x & 31;
   // The plan is read before the wait: the attention kernel let this one start only after the
-  // planning kernel's end.  (After a failed plan there is anything in it: it is not used as an
-  // index before the status is known.)
+  // planning kernel's end.  (A plan that failed has empty shares: nothing is cut.)
   const int4 cut = __ldcg(&p.starts[b + 1]), from = __ldcg(&p.starts[b]);
   const bool in = cut.x >= 0 && cut.x < m.num_seqs;
   const int4 q = in ? __ldcg(&p.seqs[2 * cut.x]) : make_int4(0, 0, 0, 0);
