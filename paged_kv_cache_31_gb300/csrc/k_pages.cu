@@ -5,7 +5,7 @@
 // pool is contiguous (block_size * num_kv_heads * head_dim elements), a position's row is
 // num_kv_heads * head_dim of them.  16-byte accesses, several in flight per thread.  Measured
 // (captured graph): 4096 pairs of 32-KB blocks in both pools 76.7 us, 7.0 TB/s, 1.05 of the copy
-// bandwidth; 7 pairs 1.8 us; the accepted rows of 1 tree of 24 nodes 3.0 us, of 256 of 64 5.3 us.
+// bandwidth; 7 pairs 1.8 us; the accepted rows of 1 tree of 24 nodes 3.3 us, of 256 of 64 5.5 us.
 //
 // Bookkeeping (k_pages).  A few hundred to some 10^5 integers: bound by the latency of its
 // dependent loads, not by bandwidth, so one cluster of eight CTAs does a whole call in one
