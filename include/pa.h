@@ -725,6 +725,118 @@ pa_status pa_free_sequences(int32_t* block_tables, int32_t* seq_lens, const int3
                             int32_t block_size, int32_t* ref_counts, int32_t* free_list,
                             int32_t* free_count, int64_t num_blocks, cudaStream_t stream);
 
+/* ---- caches of bounded size ---------------------------------------------------------------
+ *
+ * Long sequences either see a window of the cache and its first tokens (pa_window_attention), or keep
+ * the keys that queries looked at: each step adds up the attention weight that every cached key
+ * receives (pa_attention_key_weights), and now and then those with the least of it are evicted
+ * (pa_evict_keys) and the pages behind the sequences' new ends given back (pa_trim_sequences).  Keys
+ * keep the rotary positions they were cached with; `positions` of these calls count cached keys, so
+ * after an eviction a new token lies at the sequence's new length.
+ *
+ * As above, another stream's pa_device_status() may clear a recorded error between the launches of a
+ * call: it may then write those of its outputs whose indices are valid, nothing outside its arrays.
+ */
+
+/* pa_window_attention_workspace_size -- bytes of device workspace pa_window_attention needs for these
+ * sizes. */
+size_t pa_window_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads,
+                                          int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t max_blocks_per_seq, int32_t block_size);
+
+/*
+ * pa_window_attention -- causal varlen paged attention behind a sliding window whose first tokens stay
+ * visible.  Token t of sequence s at position p = positions[t] attends to the keys j <= p with
+ *     j > p - sliding_window  or  j < first_tokens
+ * (sliding_window 0: all j <= p, whatever first_tokens).  One call serves any mix of prompt chunks and
+ * decoding tokens.  out = softmax(scale * q . K) V over those keys; a row with a score of NaN or +inf
+ * gets NaN in out and lse.  Types, sinks (logits, besides the first tokens), lse, k_scale / v_scale and
+ * k_scales / v_scales as in pa_varlen_forward_ex and pa_varlen_forward_per_head (a per-head array needs
+ * a scalar of 1); kv_dtype PA_FP8_E4M3 rounds as in pa_tree_attention.
+ * K rows of keys that a token does not see may hold anything.  So may V rows at or past seq_lens[s],
+ * and those of blocks between the first tokens' and the first that the sequence's tokens reach: these
+ * are not read, and their table entries not looked at (a server may have given them away).  All other V
+ * rows of the sequence have to be finite (an unseen one enters the products with weight zero).
+ * Validation, on the device before anything is written: query_start_loc starts at 0, never decreases
+ * and ends at num_tokens; for a sequence with tokens, seq_lens[s] >= 1, its table covers seq_lens[s]
+ * positions with ids in [0, num_blocks) where they are read, and its tokens' positions lie in
+ * [0, seq_lens[s]) and do not decrease; per-head scales finite and positive.  Failures record PA_EINVAL
+ * and leave out and lse untouched.  sliding_window and first_tokens >= 0 (PA_EINVAL).  A call without
+ * tokens does nothing.
+ * workspace: pa_window_attention_workspace_size(...) bytes, 256-byte aligned, scratch of the caller
+ * that calls which overlap on the device must not share.  The results depend on the inputs alone (no
+ * atomics on values); how keys are split, and so the last bits of a row, depend on the whole batch.
+ */
+pa_status pa_window_attention(const void* q, const void* k_blocks, const void* v_blocks, void* out,
+                              const int32_t* query_start_loc, const int32_t* seq_lens,
+                              const int32_t* positions, const int32_t* block_tables, int32_t num_seqs,
+                              int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                              int32_t max_blocks_per_seq, pa_dtype q_dtype, pa_dtype kv_dtype,
+                              float scale, int32_t sliding_window, int32_t first_tokens,
+                              const float* sinks, float* lse, float k_scale, float v_scale,
+                              const float* k_scales, const float* v_scales, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
+/* pa_attention_key_weights_workspace_size -- bytes of device workspace pa_attention_key_weights needs. */
+size_t pa_attention_key_weights_workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads,
+                                               int32_t num_kv_heads, int32_t head_dim,
+                                               int32_t max_blocks_per_seq, int32_t block_size);
+
+/*
+ * pa_attention_key_weights -- pa_window_attention that also adds up the attention weight of every key:
+ *     key_weights[s, g, j] += sum over tokens t of sequence s and heads h of kv head g's group of
+ *                             exp(scale * q[t, h] . K_j - lse[h, t])
+ * for the keys j that t sees.  observed_tokens > 0 counts each sequence's last so many tokens only
+ * (of a long prompt, say), 0 all of them.  key_weights [num_seqs, num_kv_heads, weights_len] fp32
+ * DEVICE; entries of keys that no counted token sees, and those at or past seq_lens[s], are left as
+ * they are.  A sequence with tokens and seq_lens[s] > weights_len is refused (PA_EINVAL recorded), and a
+ * refused call leaves key_weights untouched, too.  A row whose lse is NaN spoils the keys it sees.
+ * All other arguments, results and errors as pa_window_attention, and its workspace
+ * pa_attention_key_weights_workspace_size(...) bytes.
+ */
+pa_status pa_attention_key_weights(const void* q, const void* k_blocks, const void* v_blocks, void* out,
+                                   const int32_t* query_start_loc, const int32_t* seq_lens,
+                                   const int32_t* positions, const int32_t* block_tables,
+                                   float* key_weights, int64_t weights_len, int32_t observed_tokens,
+                                   int32_t num_seqs, int64_t num_tokens, int32_t num_heads,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                   int64_t num_blocks, int32_t max_blocks_per_seq, pa_dtype q_dtype,
+                                   pa_dtype kv_dtype, float scale, int32_t sliding_window,
+                                   int32_t first_tokens, const float* sinks, float* lse, float k_scale,
+                                   float v_scale, const float* k_scales, const float* v_scales,
+                                   void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* pa_evict_keys_workspace_size -- bytes of device workspace pa_evict_keys needs for these sizes. */
+size_t pa_evict_keys_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t max_blocks_per_seq,
+                                    int32_t block_size);
+
+/*
+ * pa_evict_keys -- cut every sequence with new_lens[s] < seq_lens[s] to new_lens[s] keys, each kv head
+ * its own.  With n = seq_lens[s], kept are the first f = min(keep_first, new_lens[s]) keys, the last
+ * r = min(keep_recent, new_lens[s] - f), and of the keys [f, n - r) the new_lens[s] - f - r with the
+ * largest key_weights[s, g, .] (ties: the lowest index; NaN counts as larger than any number;
+ * key_weights NULL: all are alike).  Kept keys below new_lens[s] - r stay in place, the other kept ones
+ * of [f, n - r) fill the places that become free there in ascending order, and the last r move up to
+ * [new_lens[s] - r, new_lens[s]).  K and V rows (bit-exact copies, pools of any kv_dtype; with per-block
+ * dequantisation factors only where the blocks' factors agree) and the weights move alike, and the
+ * weights of [new_lens[s], n) become 0, ready for new keys.  Lengths and tables stay: give the same
+ * new_lens to pa_trim_sequences.  Sequences with new_lens[s] >= n are left as they are.
+ * Checked before any row or weight is written: n and new_lens[s] not negative, the table covers n
+ * positions with ids in [0, num_blocks) (where keys are evicted), n <= weights_len (given weights):
+ * otherwise PA_EINVAL is recorded and nothing is written.  A block that is written belongs to one
+ * sequence only.  num_seqs and num_kv_heads <= 65535 and at most 524288 keys to a sequence (the smaller
+ * of the table's width and, given weights, weights_len), else PA_EUNSUPPORTED.
+ * workspace: pa_evict_keys_workspace_size(...) bytes, 256-byte aligned, scratch of the caller that calls
+ * which overlap on the device must not share.
+ */
+pa_status pa_evict_keys(void* k_blocks, void* v_blocks, const int32_t* block_tables,
+                        const int32_t* seq_lens, const int32_t* new_lens, float* key_weights,
+                        int64_t weights_len, int32_t keep_first, int32_t keep_recent, int32_t num_seqs,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                        int32_t max_blocks_per_seq, pa_dtype kv_dtype, void* workspace,
+                        size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -4,9 +4,9 @@ Each ``pa_*`` function takes torch tensors that live on the current CUDA device,
 checks their shapes / dtypes / contiguity, passes raw pointers and the current
 stream to the library, and raises ``PaError`` on a non-OK status.  It does no
 arithmetic of its own: every step of the path runs in the library's kernels.
-The speculative-decoding calls have their checks in the compiled module ``_calls``
-(csrc/pa_calls.cpp), as ctypes took longer than their kernels; without that module, or with one
-built for another torch, they alone raise ImportError.
+The speculative-decoding calls and those for bounded caches have their checks in the compiled
+module ``_calls`` (csrc/pa_calls.cpp), as ctypes took longer than their kernels; without that
+module, or with one built for another torch, they alone raise ImportError.
 Importing this module loads the library and raises if it has not been built
 (``python -c "import __graft_entry__ as g; g.build()"``); there is no fallback.
 """
@@ -145,6 +145,18 @@ _SIGS = {
                           ctypes.c_int),
     "pa_free_sequences": ([_vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _vp],
                           ctypes.c_int),
+    "pa_window_attention_workspace_size": ([_i32, _i64, _i32, _i32, _i32, _i32, _i32], _sz),
+    "pa_window_attention": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32,
+                             _i32, _i64, _i32, ctypes.c_int, ctypes.c_int, _f32, _i32, _i32, _vp,
+                             _vp, _f32, _f32, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "pa_attention_key_weights_workspace_size": ([_i32, _i64, _i32, _i32, _i32, _i32, _i32], _sz),
+    "pa_attention_key_weights": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32,
+                                  _i64, _i32, _i32, _i32, _i32, _i64, _i32, ctypes.c_int,
+                                  ctypes.c_int, _f32, _i32, _i32, _vp, _vp, _f32, _f32, _vp, _vp,
+                                  _vp, _sz, _vp], ctypes.c_int),
+    "pa_evict_keys_workspace_size": ([_i32, _i32, _i32, _i32], _sz),
+    "pa_evict_keys": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i64,
+                       _i32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -688,3 +700,61 @@ def pa_free_sequences(block_tables, seq_lens, sequences, ref_counts, free_list, 
     back to the free list in ascending order."""
     _check(_calls.free_sequences(block_tables, seq_lens, sequences, ref_counts, free_list,
                                  free_count, block_size, stream), "pa_free_sequences")
+
+
+# ---- caches of bounded size -----------------------------------------------------------------
+
+
+def pa_window_attention_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                                       max_blocks_per_seq, block_size) -> int:
+    return int(_lib.pa_window_attention_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads,
+                                                       head_dim, max_blocks_per_seq, block_size))
+
+
+def pa_window_attention(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, positions,
+                        block_tables, scale, sliding_window=0, first_tokens=0, workspace=None,
+                        stream=None, sinks=None, lse=None, k_scale=1.0, v_scale=1.0, k_scales=None,
+                        v_scales=None):
+    """Causal attention over the cache behind a sliding window (0: none) whose first_tokens stay
+    visible, for any mix of prompt chunks and decoding tokens.  The positions of a sequence's tokens
+    must not decrease.  sinks (logits), lse and scales as in pa_varlen_forward."""
+    _check(_calls.window_attention(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, positions,
+                                   block_tables, scale, sliding_window, first_tokens, workspace,
+                                   stream, sinks, lse, k_scale, v_scale, k_scales, v_scales),
+           "pa_window_attention")
+    return out
+
+
+def pa_attention_key_weights_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                                            max_blocks_per_seq, block_size) -> int:
+    return int(_lib.pa_attention_key_weights_workspace_size(
+        num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size))
+
+
+def pa_attention_key_weights(q, k_blocks, v_blocks, out, query_start_loc, seq_lens, positions,
+                             block_tables, key_weights, scale, observed_tokens=0, sliding_window=0,
+                             first_tokens=0, workspace=None, stream=None, sinks=None, lse=None,
+                             k_scale=1.0, v_scale=1.0, k_scales=None, v_scales=None):
+    """pa_window_attention that adds to key_weights (fp32 [num_seqs, num_kv_heads, length]) the
+    softmax weights that each cached key receives from the sequence's tokens (its last
+    observed_tokens, 0: all) and the heads of the kv head's group."""
+    _check(_calls.attention_key_weights(
+        q, k_blocks, v_blocks, out, query_start_loc, seq_lens, positions, block_tables, scale,
+        sliding_window, first_tokens, workspace, stream, sinks, lse, k_scale, v_scale, k_scales,
+        v_scales, key_weights, observed_tokens), "pa_attention_key_weights")
+    return out
+
+
+def pa_evict_keys_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq, block_size) -> int:
+    return int(_lib.pa_evict_keys_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq,
+                                                 block_size))
+
+
+def pa_evict_keys(k_blocks, v_blocks, block_tables, seq_lens, new_lens, key_weights=None,
+                  keep_first=0, keep_recent=0, workspace=None, stream=None):
+    """Cut the sequences to new_lens keys, each kv head its own: the first keep_first, the last
+    keep_recent, and those between with the largest key_weights (fp32 [S, num_kv_heads, length];
+    None: all alike).  K and V rows and the weights move together; lengths and tables stay (give
+    new_lens to pa_trim_sequences)."""
+    _check(_calls.evict_keys(k_blocks, v_blocks, block_tables, seq_lens, new_lens, key_weights,
+                             keep_first, keep_recent, workspace, stream), "pa_evict_keys")

@@ -1,0 +1,234 @@
+// k_window.cu -- causal attention over the paged cache behind a sliding window whose first tokens stay
+// visible: the planning kernel and the general kernel's launch (k_tree_generic.cuh; on the tensor cores
+// k_window_tc.cu).
+//
+// Math.  A token at position p sees key j when j <= p and (j > p - w or j < f): the window's w keys and
+// the sequence's first f.  Without a window (w = 0) it sees all j <= p.
+//
+// Layout of the work.  An item is one (sequence, kv head) and up to rows_per_item query rows.  With a
+// window, the blocks between the first tokens' and the first one that any of its rows reaches are left
+// out: the item's keys are counted without that gap, so its key tiles are full of visible keys.  (A
+// tile of 128 keys for the first tokens alone would cost a decoding token behind a window of 1024 an
+// eighth of its time.)  A sequence's positions do not decrease, so an item's keys follow from its first
+// and last token alone.
+// The items' tiles are laid end to end, weighted, and cut into equal shares, one contiguous range
+// per CTA; the pieces of a cut item are merged in key order (k_tree.cu).  Chunks of prompts and
+// decoding tokens lie in the same list, so some SMs stream keys while others compute.
+#include <algorithm>
+
+#include "k_tree_generic.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kCumShared = 2048;   // sequences whose prefix sums the planner keeps in shared memory
+constexpr int kCheckTokens = 1024;  // of one sequence, checked by a warp
+
+// Blocks of a sequence's table that its tokens read: [0, front) and [front + gap, its end).
+struct Keys {
+  int front, gap;
+};
+__device__ __forceinline__ Keys keys_from(const TreeParams& p, int lowest) {
+  const VarlenMeta& m = p.m;
+  const int front = (p.first + m.block_size - 1) / m.block_size;
+  const int lo = m.window > 0 ? max(lowest - m.window + 1, 0) / m.block_size : 0;
+  return Keys{front, max(lo - front, 0)};
+}
+
+// Block 0 plans; blocks 1 .. check the sequences' positions and table entries.  Everything is read
+// after the wait for the kernels ahead, and no output is written before this launch is done.  A plan
+// that failed is one of empty shares and of sequences without tokens, so the kernels behind do nothing
+// even where another stream has cleared the status word in between.
+__global__ void __launch_bounds__(kPlanThreads) k_window_plan(const TreeParams p) {
+  __shared__ int64_t s_warp[32];
+  __shared__ int64_t s_cum[kCumShared + 1];
+  __shared__ int s_base[kCumShared + 1];
+  const VarlenMeta& m = p.m;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+  bool bad = false;
+  if (blockIdx.x > 0) {
+    const int warps = (gridDim.x - 1) * (kPlanThreads / 32);
+    const int me = (blockIdx.x - 1) * (kPlanThreads / 32) + warp;
+    const int per = (m.max_blocks + 255) / 256;  // chunks of a table row
+    const int64_t chunks = (int64_t)m.num_seqs * per;
+    for (int64_t c = me; c < chunks; c += warps) {
+      const int s = (int)(c / per), e0 = (int)(c % per) * 256;
+      const int qs = m.query_start_loc[s], n = m.seq_lens[s];
+      if (m.query_start_loc[s + 1] <= qs || n < 1 || qs < 0 || qs >= m.num_tokens) continue;
+      const int64_t need = ((int64_t)n + m.block_size - 1) / m.block_size;
+      const int lim = (int)min(need, (int64_t)m.max_blocks);
+      if (e0 >= lim) continue;
+      const Keys k = keys_from(p, m.window > 0 ? m.positions[qs] : 0);
+      const int32_t* row = m.block_tables + (int64_t)s * m.max_blocks;
+      int id[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int e = e0 + lane + 32 * u;
+        id[u] = e < lim && (e < k.front || e >= k.front + k.gap) ? row[e] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) bad |= id[u] < 0 || (int64_t)id[u] >= m.num_blocks;
+    }
+    const int parts = (int)((m.num_tokens + kCheckTokens - 1) / kCheckTokens);
+    const int64_t units = (int64_t)m.num_seqs * parts;
+    for (int64_t c = me; c < units; c += warps) {
+      const int s = (int)(c / parts);
+      const int64_t t0 = (int64_t)m.query_start_loc[s] + c % parts * kCheckTokens;
+      const int64_t end = min(min((int64_t)m.query_start_loc[s + 1], t0 + kCheckTokens), m.num_tokens);
+      if (t0 < 0 || t0 >= end) continue;
+      const int n = m.seq_lens[s];
+      const bool more = t0 + kCheckTokens < m.query_start_loc[s + 1] && t0 + kCheckTokens < m.num_tokens;
+      for (int64_t t = t0 + lane; t < end; t += 32) {
+        const int pos = m.positions[t];
+        const int after = t + 1 < end || more ? m.positions[t + 1] : pos;
+        bad |= pos < 0 || pos >= n || after < pos;
+      }
+    }
+    if (__any_sync(kFull, bad) && lane == 0) record_error(p.status, PA_EINVAL);
+    return;
+  }
+
+  // per-head scales (each array may be missing)
+  for (int g = tid; g < m.num_kv_heads; g += kPlanThreads) {
+    const float a = m.k_scales ? m.k_scales[g] : 1.f, b = m.v_scales ? m.v_scales[g] : 1.f;
+    bad |= !(a > 0.f && a <= 3.402823466e38f) || !(b > 0.f && b <= 3.402823466e38f);
+  }
+  const bool shared = m.num_seqs <= kCumShared;
+  int64_t items = 0;
+  for (int s0 = 0; s0 < m.num_seqs; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    int qs = 0, q = 0, n = 0;
+    if (s < m.num_seqs) {
+      qs = m.query_start_loc[s];
+      const int qe = m.query_start_loc[s + 1];
+      bad |= qs < 0 || qe < qs || (int64_t)qe > m.num_tokens || (s == 0 && qs != 0) ||
+             (s == m.num_seqs - 1 && (int64_t)qe != m.num_tokens);
+      if (qs >= 0 && qe > qs && (int64_t)qe <= m.num_tokens) {
+        q = qe - qs;
+        n = m.seq_lens[s];
+        if (n < 1 || ((int64_t)n + m.block_size - 1) / m.block_size > m.max_blocks ||
+            (p.key_weights && (int64_t)n > p.weights_len)) {
+          bad = true;
+          q = 0;
+        }
+      }
+    }
+    const int rows = q * m.group, mine = (rows + p.rows_per_item - 1) / p.rows_per_item;
+    int64_t total;
+    const int64_t at = items + block_sum_scan(mine, s_warp, &total);
+    if (s < m.num_seqs) {
+      p.seqs[2 * s] = make_int4(qs, q, n, 0);
+      p.seqs[2 * s + 1] = make_int4(mine, (int)at, rows, 0);
+      if (shared) s_base[s] = (int)at;
+    }
+    items += total;
+  }
+  // (query_start_loc may be anything: a batch that is not valid has no items, however many it counts)
+  if (__syncthreads_or(bad)) items = 0;
+
+  // the items' keys and weights
+  int64_t base = 0;
+  for (int64_t i0 = 0; i0 < items; i0 += kPlanThreads) {
+    const int64_t i = i0 + tid;
+    int64_t weight = 0;
+    if (i < items) {
+      int lo = 0, hi = m.num_seqs;  // the last sequence whose first item is at most i: it has items
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((shared ? s_base[mid] : p.seqs[2 * mid + 1].y) <= i) lo = mid; else hi = mid;
+      }
+      const int4 q = p.seqs[2 * lo], w = p.seqs[2 * lo + 1];
+      const int row0 = (int)(i - w.y) * p.rows_per_item, rows = min(p.rows_per_item, w.z - row0);
+      const int a = m.positions[q.x + row0 / m.group];
+      const int b = m.positions[q.x + (row0 + rows - 1) / m.group];
+      bad |= a < 0 || b < a || b >= q.z;
+      const Keys k = keys_from(p, a);
+      const int end = min(max(b, a), q.z - 1) + 1 - k.gap * m.block_size;
+      const int tiles = max(1, (end + p.key_tile - 1) / p.key_tile);
+      p.item_keys[i] = make_int4(k.front, k.gap, tiles, 0);
+      weight = (int64_t)tree_weight(p, rows) * tiles + kTreeItemWeight;
+    }
+    int64_t total;
+    const int64_t at = base + block_sum_scan(weight, s_warp, &total);
+    if (i < items) p.item_cum[i] = at;
+    base += total;
+  }
+  if (tid == 0) p.item_cum[items] = base;
+  bad = __syncthreads_or(bad);  // (and the items' records can be read)
+  if (bad) {
+    if (tid == 0) record_error(p.status, PA_EINVAL);
+    for (int s = tid; s < m.num_seqs; s += kPlanThreads)
+      p.seqs[2 * s] = p.seqs[2 * s + 1] = make_int4(0, 0, 0, 0);
+    for (int c = tid; c <= p.grid; c += kPlanThreads) p.starts[c] = make_int4(m.num_seqs, 0, 0, 0);
+    return;
+  }
+  for (int s = tid; s <= m.num_seqs; s += kPlanThreads) {
+    const int64_t at = s < m.num_seqs ? p.item_cum[p.seqs[2 * s + 1].y] * m.num_kv_heads
+                                      : base * m.num_kv_heads;
+    if (shared) s_cum[s] = at; else p.cum[s] = at;
+  }
+  __syncthreads();
+  // where each CTA's share begins
+  base *= m.num_kv_heads;
+  for (int c = tid; c <= p.grid; c += kPlanThreads) {
+    int4 st = make_int4(m.num_seqs, 0, 0, 0);
+    if (c < p.grid && base > 0) {
+      const int64_t x = base / p.grid * c + base % p.grid * c / p.grid;  // floor(base c / grid)
+      int lo = 0, hi = m.num_seqs;  // the last sequence with cum <= x
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((shared ? s_cum[mid] : p.cum[mid]) <= x) lo = mid; else hi = mid;
+      }
+      const int64_t before = shared ? s_cum[lo] : p.cum[lo];
+      const int64_t per_head = ((shared ? s_cum[lo + 1] : p.cum[lo + 1]) - before) / m.num_kv_heads;
+      const int4 w = p.seqs[2 * lo + 1];
+      const int kvh = (int)((x - before) / per_head);
+      const int64_t r = (x - before) % per_head, cum0 = p.item_cum[w.y];
+      int it = 0, top = w.x;  // the last item with cum <= r
+      while (top - it > 1) {
+        const int mid = (it + top) >> 1;
+        if (p.item_cum[w.y + mid] - cum0 <= r) it = mid; else top = mid;
+      }
+      const int64_t in = max(r - (p.item_cum[w.y + it] - cum0) - kTreeItemWeight, (int64_t)0);
+      const int tw = tree_weight(p, min(p.rows_per_item, w.z - it * p.rows_per_item));
+      st = make_int4(lo, kvh, it, (int)min(in / tw, (int64_t)p.item_keys[w.y + it].z - 1));
+    }
+    p.starts[c] = st;
+  }
+}
+
+}  // namespace
+
+WindowLayout window_layout(int32_t num_seqs, int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                           int32_t head_dim, int64_t max_keys, int32_t rows_per_item, int32_t key_tile,
+                           int32_t max_grid, bool own_lse) {
+  auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  const int32_t group = num_heads / num_kv_heads;
+  const TreeLayout t = tree_layout(num_seqs, num_tokens, group, num_kv_heads, head_dim, max_keys,
+                                   rows_per_item, key_tile, max_grid);
+  const int64_t items = (num_tokens * group + rows_per_item - 1) / rows_per_item + num_seqs;
+  WindowLayout L;
+  L.tree = t;
+  L.items_off = t.bytes;
+  L.item_cum_off = L.items_off + up(16 * items);
+  L.lse_off = L.item_cum_off + up(8 * (items + 1));
+  L.bytes = L.lse_off + (own_lse ? up(4 * num_tokens * num_heads) : 0);
+  return L;
+}
+
+cudaError_t launch_window_plan(const TreeParams& p, cudaStream_t stream) {
+  // checks beside the planner: a warp per 256 table entries or 1024 tokens, at most 64 blocks
+  const int64_t chunks = (int64_t)p.m.num_seqs * ((p.m.max_blocks + 255) / 256 +
+                                                  (p.m.num_tokens + kCheckTokens - 1) / kCheckTokens);
+  const int blocks = (int)std::min<int64_t>((chunks + 31) / 32, 64);
+  return launch_pdl(k_window_plan, dim3(1 + blocks), dim3(kPlanThreads), 0, stream, p);
+}
+
+cudaError_t launch_window_generic(const TreeParams& p, pa_dtype kv, cudaStream_t stream) {
+  return generic_types<true>(p, kv, stream);
+}
+
+}  // namespace pa

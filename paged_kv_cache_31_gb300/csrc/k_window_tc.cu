@@ -1,0 +1,30 @@
+// k_window_tc.cu -- launches of the attention behind a window with first tokens on the tensor cores
+// (k_tree_tc.cuh, WIN).
+#include "k_tree_tc.cuh"
+
+namespace pa {
+namespace {
+
+template <int D, bool FP8>
+cudaError_t launch_as(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                      const TreeParams& p, uint64_t limit, uint32_t stall, cudaStream_t stream) {
+  using S = Shape<D, FP8>;
+  auto kern = k_tree_tc<D, FP8, kWindow>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(p.grid), dim3(S::kThreads), S::kSmem, stream, tq, tk, tv, p, limit,
+                    stall);
+}
+
+}  // namespace
+
+cudaError_t launch_window_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const TreeParams& p, bool fp8, uint64_t wait_limit, uint32_t stall,
+                             cudaStream_t stream) {
+  if (fp8) return launch_as<128, true>(tq, tk, tv, p, wait_limit, stall, stream);
+  if (p.m.head_dim == 128) return launch_as<128, false>(tq, tk, tv, p, wait_limit, stall, stream);
+  return launch_as<64, false>(tq, tk, tv, p, wait_limit, stall, stream);
+}
+
+}  // namespace pa

@@ -1,0 +1,282 @@
+// pa_api_bounded.cu -- the C ABI's calls for caches of bounded size: attention behind a window with
+// first tokens, the attention weights that keys receive, and the eviction of keys.  Argument checks,
+// path selection and launches only.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "pa_internal.cuh"
+
+using namespace pa;
+
+namespace {
+
+// Rows of one row tile of the tensor-core kernel: whole tokens, at most 128 rows.
+int32_t tile_rows(int32_t group) { return 128 / group * group; }
+
+bool tc_sizes(int32_t group, int32_t head_dim) {
+  return group <= 128 && (head_dim == 64 || head_dim == 128);
+}
+
+size_t workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                      int32_t head_dim, int32_t max_blocks, int32_t block_size, bool weights) {
+  if (num_seqs < 0 || num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
+      num_heads % num_kv_heads != 0 || head_dim <= 0 || max_blocks < 0 || block_size <= 0)
+    return 0;
+  const int64_t keys = (int64_t)max_blocks * block_size;
+  int64_t bytes = window_layout(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, keys,
+                                kTreeGenericRows, kTreeGenericKeys, kTreeGenericGrid, weights)
+                      .bytes;
+  const int32_t group = num_heads / num_kv_heads;
+  if (tc_sizes(group, head_dim))  // the tensor-core kernel may run
+    bytes = std::max(bytes, window_layout(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, keys,
+                                          2 * tile_rows(group), kTreeTcKeys, kTreeTcGrid, weights)
+                                .bytes);
+  return (size_t)bytes;
+}
+
+struct Call {
+  const void *q, *k_blocks, *v_blocks;
+  void* out;
+  const int32_t *query_start_loc, *seq_lens, *positions, *block_tables;
+  int32_t num_seqs;
+  int64_t num_tokens;
+  int32_t num_heads, num_kv_heads, head_dim, block_size;
+  int64_t num_blocks;
+  int32_t max_blocks;
+  pa_dtype q_dtype, kv_dtype;
+  float scale;
+  int32_t window, first;
+  const float* sinks;
+  float* lse;
+  float k_scale, v_scale;
+  const float *k_scales, *v_scales;
+  bool weighs;
+  float* key_weights;
+  int64_t weights_len;
+  int32_t observed;
+  void* workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+};
+
+pa_status attend(const Call& c) {
+  bool empty = false;  // no token: nothing to do, whatever the sequences
+  const int32_t check_seqs = c.num_tokens == 0 && c.num_seqs > 0 ? 0 : c.num_seqs;
+  const pa_status chk = varlen_check(c.q, c.k_blocks, c.v_blocks, c.out, c.query_start_loc, c.seq_lens,
+                                     c.positions, c.block_tables, check_seqs, c.num_tokens, c.num_heads,
+                                     c.num_kv_heads, c.head_dim, c.block_size, c.num_blocks,
+                                     c.max_blocks, c.q_dtype, c.kv_dtype, c.k_scale, c.v_scale, 0u,
+                                     &empty);
+  if (chk != PA_OK) return chk;
+  if ((c.k_scales && c.k_scale != 1.f) || (c.v_scales && c.v_scale != 1.f) || c.window < 0 ||
+      c.first < 0 || c.observed < 0 || c.weights_len < 0)
+    return PA_EINVAL;
+  if (empty) return PA_OK;
+  if (c.num_seqs == 0 || !std::isfinite(c.scale) || (c.weighs && !c.key_weights)) return PA_EINVAL;
+  const int32_t group = c.num_heads / c.num_kv_heads;
+  const int64_t max_keys = (int64_t)c.max_blocks * c.block_size;
+  // token * group rows of one sequence, and positions, are counted in 32 bits
+  if (c.num_tokens * group > INT32_MAX / 2 || max_keys > INT32_MAX - 1024) return PA_EUNSUPPORTED;
+  if (!c.workspace || !aligned(c.workspace, 256)) return PA_EINVAL;
+  if (c.workspace_bytes < workspace_size(c.num_seqs, c.num_tokens, c.num_heads, c.num_kv_heads,
+                                         c.head_dim, c.max_blocks, c.block_size, c.weighs))
+    return PA_EINVAL;
+  const DeviceState* d = device_state();
+  if (!d) return PA_ECUDA;
+
+  TreeParams p;
+  std::memset(&p, 0, sizeof p);
+  p.q = c.q;
+  p.k_blocks = c.k_blocks;
+  p.v_blocks = c.v_blocks;
+  p.out = c.out;
+  VarlenMeta& m = p.m;
+  m.query_start_loc = c.query_start_loc;
+  m.seq_lens = c.seq_lens;
+  m.positions = c.positions;
+  m.block_tables = c.block_tables;
+  m.num_seqs = c.num_seqs;
+  m.num_tokens = c.num_tokens;
+  m.num_heads = c.num_heads;
+  m.num_kv_heads = c.num_kv_heads;
+  m.group = group;
+  m.head_dim = c.head_dim;
+  m.block_size = c.block_size;
+  m.num_blocks = c.num_blocks;
+  m.max_blocks = c.max_blocks;
+  m.window = c.window;
+  m.sinks = c.sinks;
+  m.lse = c.lse;
+  m.v_scale = c.v_scale;
+  m.k_scales = c.k_scales;
+  m.v_scales = c.v_scales;
+  p.first = c.window > 0 ? (int32_t)std::min<int64_t>(c.first, max_keys) : 0;
+  p.scale = c.scale * c.k_scale;
+  p.status = d->status;
+  p.q_bf16 = c.q_dtype == PA_BF16;
+  p.key_weights = c.key_weights;
+  p.weights_len = c.weights_len;
+  p.observed = c.observed;
+  const bool fp8 = c.kv_dtype == PA_FP8_E4M3;
+  // the tensor-core kernel: its types and sizes, tensors aligned for TMA, and a positive scale (its
+  // row maxima are taken before the scale)
+  const bool tc = c.q_dtype == PA_BF16 && c.block_size == 16 && tc_sizes(group, c.head_dim) &&
+                  (fp8 ? c.head_dim == 128 : c.kv_dtype == PA_BF16) && aligned(c.q, 16) &&
+                  aligned(c.out, 16) && aligned(c.k_blocks, 16) && aligned(c.v_blocks, 16) &&
+                  p.scale > 0.f && c.num_blocks > 0 && tc_enabled();
+  WindowLayout L;
+  if (tc) {
+    p.tile_rows = tile_rows(group);
+    p.tile_tokens = p.tile_rows / group;
+    p.key_tile = kTreeTcKeys;
+    // items of one row tile when no sequence can have more rows, else of two
+    p.rows_per_item = c.num_tokens * group > p.tile_rows ? 2 * p.tile_rows : p.tile_rows;
+    L = window_layout(c.num_seqs, c.num_tokens, c.num_heads, c.num_kv_heads, c.head_dim, max_keys,
+                      p.rows_per_item, p.key_tile, kTreeTcGrid, c.weighs);
+    L.tree.grid = std::min(L.tree.grid, d->sms);
+  } else {
+    p.tile_rows = p.rows_per_item = kTreeGenericRows;
+    p.key_tile = kTreeGenericKeys;
+    L = window_layout(c.num_seqs, c.num_tokens, c.num_heads, c.num_kv_heads, c.head_dim, max_keys,
+                      p.rows_per_item, p.key_tile, kTreeGenericGrid, c.weighs);
+  }
+  p.grid = L.tree.grid;
+  uint8_t* ws = static_cast<uint8_t*>(c.workspace);
+  p.seqs = reinterpret_cast<int4*>(ws);
+  p.cum = reinterpret_cast<int64_t*>(ws + L.tree.cum_off);
+  p.starts = reinterpret_cast<int4*>(ws + L.tree.starts_off);
+  p.part_ml = reinterpret_cast<float2*>(ws + L.tree.ml_off);
+  p.part_o = reinterpret_cast<float*>(ws + L.tree.o_off);
+  p.item_keys = reinterpret_cast<int4*>(ws + L.items_off);
+  p.item_cum = reinterpret_cast<int64_t*>(ws + L.item_cum_off);
+  if (c.weighs && !m.lse) m.lse = reinterpret_cast<float*>(ws + L.lse_off);
+  CUtensorMap tq, tk, tv;
+  if (tc) {
+    const bool ok =
+        query_map(&tq, c.q, c.num_tokens, c.num_heads, c.head_dim, group, p.tile_tokens) &&
+        (fp8 ? pool_map_fp8(&tk, c.k_blocks, c.num_blocks, 16, c.num_kv_heads, c.head_dim, true) &&
+                   pool_map_fp8(&tv, c.v_blocks, c.num_blocks, 16, c.num_kv_heads, c.head_dim, true)
+             : pool_map_rows(&tk, c.k_blocks, c.num_blocks, c.num_kv_heads, c.head_dim) &&
+                   pool_map_rows(&tv, c.v_blocks, c.num_blocks, c.num_kv_heads, c.head_dim));
+    if (!ok) return PA_ECUDA;
+  }
+  if (launch_window_plan(p, c.stream) != cudaSuccess) return PA_ECUDA;
+  if (tc) {
+    uint64_t limit;
+    uint32_t stall;
+    stall_hook(limit, stall);
+    if (launch_window_tc(tq, tk, tv, p, fp8, limit, stall, c.stream) != cudaSuccess) return PA_ECUDA;
+  } else if (launch_window_generic(p, c.kv_dtype, c.stream) != cudaSuccess) {
+    return PA_ECUDA;
+  }
+  if (launch_tree_merge(p, c.stream) != cudaSuccess) return PA_ECUDA;
+  if (!c.weighs) return PA_OK;
+  return from_cuda(launch_key_weights_generic(p, c.kv_dtype, c.stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pa_window_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads,
+                                          int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t max_blocks_per_seq, int32_t block_size) {
+  return workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                        block_size, false);
+}
+
+pa_status pa_window_attention(const void* q, const void* k_blocks, const void* v_blocks, void* out,
+                              const int32_t* query_start_loc, const int32_t* seq_lens,
+                              const int32_t* positions, const int32_t* block_tables, int32_t num_seqs,
+                              int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                              int32_t max_blocks_per_seq, pa_dtype q_dtype, pa_dtype kv_dtype,
+                              float scale, int32_t sliding_window, int32_t first_tokens,
+                              const float* sinks, float* lse, float k_scale, float v_scale,
+                              const float* k_scales, const float* v_scales, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+  return attend(Call{q, k_blocks, v_blocks, out, query_start_loc, seq_lens, positions, block_tables,
+                     num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                     max_blocks_per_seq, q_dtype, kv_dtype, scale, sliding_window, first_tokens, sinks,
+                     lse, k_scale, v_scale, k_scales, v_scales, false, nullptr, 0, 0, workspace,
+                     workspace_bytes, stream});
+}
+
+size_t pa_attention_key_weights_workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads,
+                                               int32_t num_kv_heads, int32_t head_dim,
+                                               int32_t max_blocks_per_seq, int32_t block_size) {
+  return workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                        block_size, true);
+}
+
+pa_status pa_attention_key_weights(const void* q, const void* k_blocks, const void* v_blocks, void* out,
+                                   const int32_t* query_start_loc, const int32_t* seq_lens,
+                                   const int32_t* positions, const int32_t* block_tables,
+                                   float* key_weights, int64_t weights_len, int32_t observed_tokens,
+                                   int32_t num_seqs, int64_t num_tokens, int32_t num_heads,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                   int64_t num_blocks, int32_t max_blocks_per_seq, pa_dtype q_dtype,
+                                   pa_dtype kv_dtype, float scale, int32_t sliding_window,
+                                   int32_t first_tokens, const float* sinks, float* lse, float k_scale,
+                                   float v_scale, const float* k_scales, const float* v_scales,
+                                   void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return attend(Call{q, k_blocks, v_blocks, out, query_start_loc, seq_lens, positions, block_tables,
+                     num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                     max_blocks_per_seq, q_dtype, kv_dtype, scale, sliding_window, first_tokens, sinks,
+                     lse, k_scale, v_scale, k_scales, v_scales, true, key_weights, weights_len,
+                     observed_tokens, workspace, workspace_bytes, stream});
+}
+
+size_t pa_evict_keys_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t max_blocks_per_seq,
+                                    int32_t block_size) {
+  if (num_seqs < 0 || num_kv_heads <= 0 || max_blocks_per_seq < 0 || block_size <= 0) return 0;
+  return (size_t)evict_workspace(num_seqs, num_kv_heads, (int64_t)max_blocks_per_seq * block_size);
+}
+
+pa_status pa_evict_keys(void* k_blocks, void* v_blocks, const int32_t* block_tables,
+                        const int32_t* seq_lens, const int32_t* new_lens, float* key_weights,
+                        int64_t weights_len, int32_t keep_first, int32_t keep_recent, int32_t num_seqs,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                        int32_t max_blocks_per_seq, pa_dtype kv_dtype, void* workspace,
+                        size_t workspace_bytes, cudaStream_t stream) {
+  if (num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0) return PA_ESHAPE;
+  if (!pool_dtype_ok(kv_dtype)) return PA_EUNSUPPORTED;
+  if (num_seqs < 0 || num_blocks < 0 || max_blocks_per_seq < 0 || keep_first < 0 || keep_recent < 0 ||
+      weights_len < 0)
+    return PA_EINVAL;
+  const int64_t max_keys = (int64_t)max_blocks_per_seq * block_size;
+  const int64_t most = key_weights ? std::min(max_keys, weights_len) : max_keys;
+  if (num_seqs > 65535 || num_kv_heads > 65535 || max_keys > INT32_MAX - 1024 || most > kEvictMostKeys ||
+      (int64_t)head_dim * esize(kv_dtype) > (1 << 20))
+    return PA_EUNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  if (!k_blocks || !v_blocks || !block_tables || !seq_lens || !new_lens) return PA_EINVAL;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < pa_evict_keys_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq, block_size))
+    return PA_EINVAL;
+  const DeviceState* d = device_state();
+  if (!d) return PA_ECUDA;
+  EvictParams p{};
+  p.k_blocks = k_blocks;
+  p.v_blocks = v_blocks;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.new_lens = new_lens;
+  p.key_weights = key_weights;
+  p.weights_len = weights_len;
+  p.num_seqs = num_seqs;
+  p.keep_first = keep_first;
+  p.keep_recent = keep_recent;
+  p.num_kv_heads = num_kv_heads;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.row_bytes = (int64_t)head_dim * esize(kv_dtype);
+  p.moves = static_cast<int32_t*>(workspace);
+  p.moves_len = most;
+  p.status = d->status;
+  return from_cuda(launch_evict(p, d->sms, stream));
+}
+
+}  // extern "C"

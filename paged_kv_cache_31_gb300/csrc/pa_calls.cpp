@@ -1,5 +1,5 @@
 // pa_calls.cpp -- the Python module _calls: the checks and the argument passing of the
-// speculative-decoding calls over torch tensors (binding.py documents them and raises PaError).
+// speculative-decoding calls and of those for bounded caches over torch tensors (binding.py documents them and raises PaError).
 //
 // Why not ctypes, as for the calls around it: their kernels take 2 to 15 us at serving sizes, and
 // reading some ten tensors' properties and converting up to thirty arguments took 3 to 10 us of
@@ -7,8 +7,8 @@
 // captured graph).  Through this module the same checks take under a microsecond.
 //
 // Checks raise ValueError (TypeError for what is not a tensor or a number); the functions return
-// the library's status.  No call allocates but pa_tree_attention without a workspace, which takes
-// it from torch's allocator, from the pool of the stream that the call goes to.
+// the library's status.  Calls that are not given a workspace they need take it from torch's
+// allocator, from the pool of the stream that the call goes to; no other call allocates.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -138,6 +138,30 @@ struct Pools {
   }
 };
 
+// A call's workspace: the tensor given, or one of `size()` bytes.
+struct Workspace {
+  std::optional<at::Tensor> own;
+  void* ptr;
+  size_t bytes;
+  template <typename F>
+  Workspace(const Call& c, PyObject* o, F size) {
+    if (none(o)) {
+      bytes = size();
+      // memory of another stream's pool may still be in use by what that stream has queued
+      c10::cuda::OptionalCUDAStreamGuard guard;
+      if (c.given)
+        guard.reset_stream(c10::cuda::getStreamFromExternal(c.stream, (c10::DeviceIndex)c.dev));
+      own = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(
+                                            at::kCUDA, (c10::DeviceIndex)c.dev));
+      ptr = own->data_ptr();
+    } else {
+      const at::Tensor& t = c.array(o);
+      ptr = t.data_ptr();
+      bytes = t.nbytes();
+    }
+  }
+};
+
 // Elements between the tokens of [T, N, D] rows whose heads are contiguous.
 int64_t token_stride(const at::Tensor& t) {
   if ((t.stride(2) != 1 && t.size(2) > 1) || (t.stride(1) != t.size(2) && t.size(1) > 1))
@@ -222,26 +246,13 @@ pa_status tree_attention(Args a) {
   const int32_t window = integer(a[10]), words = int32(mask.size(1));
   const float *kss = c.head_scales(a[17], p.heads), *vss = c.head_scales(a[18], p.heads);
   const pa_dtype type = dtype(q);
-  std::optional<at::Tensor> own;
-  void* ws;
-  size_t bytes;
-  if (none(a[11])) {
-    bytes = pa_tree_attention_workspace_size(S, T, H, p.heads, p.dim, max_blocks, p.block);
-    // memory of another stream's pool may still be in use by what that stream has queued
-    c10::cuda::OptionalCUDAStreamGuard guard;
-    if (c.given) guard.reset_stream(c10::cuda::getStreamFromExternal(c.stream, (c10::DeviceIndex)c.dev));
-    own = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(
-                                          at::kCUDA, (c10::DeviceIndex)c.dev));
-    ws = own->data_ptr();
-  } else {
-    const at::Tensor& t = c.array(a[11]);
-    ws = t.data_ptr();
-    bytes = t.nbytes();
-  }
+  const Workspace ws(c, a[11], [&] {
+    return pa_tree_attention_workspace_size(S, T, H, p.heads, p.dim, max_blocks, p.block);
+  });
   Released r;
   return pa_tree_attention(q.data_ptr(), p.k, p.v, out.data_ptr(), qsl, lens, pos, mask_ptr,
                            table_ptr, S, T, words, H, p.heads, p.dim, p.block, p.blocks, max_blocks,
-                           type, p.type, scale, window, sinks, lse, ks, vs, kss, vss, ws, bytes,
+                           type, p.type, scale, window, sinks, lse, ks, vs, kss, vss, ws.ptr, ws.bytes,
                            c.stream);
 }
 
@@ -340,6 +351,86 @@ pa_status free_sequences(Args a) {
                            b.free_list, b.free_count, b.blocks, c.stream);
 }
 
+// pa_window_attention's arguments; with WEIGH pa_attention_key_weights', which has two more at the end.
+template <bool WEIGH>
+pa_status window_attention(Args a) {
+  const Call c(a[12]);
+  const at::Tensor &q = c.array(a[0]), &out = c.array(a[3]);
+  if (q.dim() != 3 || out.sizes() != q.sizes() || out.scalar_type() != q.scalar_type())
+    throw Bad{"q and out must be [T, H, D] of one dtype"};
+  const Pools p(c, a[1], a[2]);
+  const int64_t T = q.size(0);
+  const int32_t H = int32(q.size(1));
+  if (q.size(2) != p.dim) throw Bad{"head size differs between q and the pool"};
+  int64_t nq, nl, np;
+  const int32_t *qsl = c.ints(a[4], &nq), *lens = c.ints(a[5], &nl), *pos = c.ints(a[6], &np);
+  const at::Tensor& tables = c.array(a[7]);
+  const int32_t* table_ptr = c.ints(a[7]);
+  if (np != T) throw Bad{"positions must be [T]"};
+  const int32_t S = int32(nq - 1);
+  if (nl != S || tables.dim() != 2 || tables.size(0) != S)
+    throw Bad{"seq_lens must be [S] and block_tables [S, max_blocks]"};
+  const int32_t max_blocks = int32(tables.size(1));
+  const float scale = (float)number(a[8]), ks = (float)number(a[15]), vs = (float)number(a[16]);
+  const int32_t window = integer(a[9]), first = integer(a[10]);
+  const float* sinks = c.floats(a[13], H, -1, "sinks must be a contiguous fp32 [num_heads] tensor");
+  float* lse =
+      c.floats(a[14], H, T, "lse must be a contiguous fp32 [num_heads, num_tokens] tensor");
+  const float *kss = c.head_scales(a[17], p.heads), *vss = c.head_scales(a[18], p.heads);
+  const pa_dtype type = dtype(q);
+  if constexpr (WEIGH) {
+    const at::Tensor& w = c.array(a[19]);
+    if (w.scalar_type() != at::kFloat || w.dim() != 3 || w.size(0) != S || w.size(1) != p.heads)
+      throw Bad{"key_weights must be fp32 [num_seqs, num_kv_heads, length]"};
+    const int32_t observed = integer(a[20]);
+    float* wp = static_cast<float*>(w.data_ptr());
+    const int64_t len = w.size(2);
+    const Workspace ws(c, a[11], [&] {
+      return pa_attention_key_weights_workspace_size(S, T, H, p.heads, p.dim, max_blocks, p.block);
+    });
+    Released r;
+    return pa_attention_key_weights(q.data_ptr(), p.k, p.v, out.data_ptr(), qsl, lens, pos, table_ptr,
+                                    wp, len, observed, S, T, H, p.heads, p.dim, p.block, p.blocks,
+                                    max_blocks, type, p.type, scale, window, first, sinks, lse, ks, vs,
+                                    kss, vss, ws.ptr, ws.bytes, c.stream);
+  } else {
+    const Workspace ws(c, a[11], [&] {
+      return pa_window_attention_workspace_size(S, T, H, p.heads, p.dim, max_blocks, p.block);
+    });
+    Released r;
+    return pa_window_attention(q.data_ptr(), p.k, p.v, out.data_ptr(), qsl, lens, pos, table_ptr, S, T,
+                               H, p.heads, p.dim, p.block, p.blocks, max_blocks, type, p.type, scale,
+                               window, first, sinks, lse, ks, vs, kss, vss, ws.ptr, ws.bytes, c.stream);
+  }
+}
+
+pa_status evict_keys(Args a) {
+  const Call c(a[9]);
+  const Pools p(c, a[0], a[1]);
+  const at::Tensor& tables = c.array(a[2]);
+  int64_t nl, nn;
+  const int32_t *table_ptr = c.ints(a[2]), *lens = c.ints(a[3], &nl), *new_lens = c.ints(a[4], &nn);
+  if (tables.dim() != 2 || nl != tables.size(0) || nn != nl)
+    throw Bad{"block_tables must be [S, max_blocks], seq_lens and new_lens [S]"};
+  const int32_t S = int32(nl), max_blocks = int32(tables.size(1));
+  float* w = nullptr;
+  int64_t len = 0;
+  if (!none(a[5])) {
+    const at::Tensor& t = c.array(a[5]);
+    if (t.scalar_type() != at::kFloat || t.dim() != 3 || t.size(0) != S || t.size(1) != p.heads)
+      throw Bad{"key_weights must be fp32 [num_seqs, num_kv_heads, length]"};
+    w = static_cast<float*>(t.data_ptr());
+    len = t.size(2);
+  }
+  const int32_t first = integer(a[6]), recent = integer(a[7]);
+  const Workspace ws(c, a[8], [&] {
+    return pa_evict_keys_workspace_size(S, p.heads, max_blocks, p.block);
+  });
+  Released r;
+  return pa_evict_keys(p.k, p.v, table_ptr, lens, new_lens, w, len, first, recent, S, p.heads, p.dim,
+                       p.block, p.blocks, max_blocks, p.type, ws.ptr, ws.bytes, c.stream);
+}
+
 template <pa_status (*F)(Args), int N>
 PyObject* entry(PyObject*, Args args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -367,6 +458,9 @@ PyMethodDef kMethods[] = {
     method<tree_commit, 7>("tree_commit"),        method<copy_blocks, 4>("copy_blocks"),
     method<fork_sequences, 10>("fork_sequences"), method<grow_sequences, 9>("grow_sequences"),
     method<trim_sequences, 9>("trim_sequences"),  method<free_sequences, 8>("free_sequences"),
+    method<window_attention<false>, 19>("window_attention"),
+    method<window_attention<true>, 21>("attention_key_weights"),
+    method<evict_keys, 10>("evict_keys"),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, kMethods,

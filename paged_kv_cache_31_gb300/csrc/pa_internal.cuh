@@ -615,6 +615,16 @@ struct TreeParams {
   // Small calls: one cluster of `cluster` CTAs for each (sequence, kv head, item), items numbered
   // 0 .. items - 1 in every sequence (0: the shares above).
   int32_t cluster, items;
+  // Attention behind a window with first tokens (k_window.cu): m.window counts behind positions, no
+  // mask; seqs' second record is (items of a kv head, its first item's record, rows, 0).
+  int32_t first;     // positions that stay visible
+  int4* item_keys;  // [items of all sequences] (front blocks, gap in blocks behind them, key tiles, 0)
+  int64_t* item_cum;  // [items + 1] weight before the item, over all items of a kv head in order
+  // Attention weights that keys receive (k_key_weights.cu): [num_seqs, num_kv_heads, weights_len] that
+  // the weights are added to, of the last `observed` tokens of each sequence (null: none are).
+  float* key_weights;
+  int64_t weights_len;
+  int32_t observed;
 };
 // The work of an item, in about hundredths of a microsecond (only the balance between the CTAs
 // depends on it): a key tile of one row tile takes about 1.5 us, a little more the more warps its
@@ -649,6 +659,41 @@ cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t stream);
 constexpr int64_t kTreeSmallEntries = 8192;
 constexpr int64_t kTreeSmallTiles = 9;  // key tiles of a CTA beyond its even share, at most
 int tree_clusters_resident(int device, bool fp8, int head_dim, int c);  // c 2, 4 or 8; at once
+
+// Attention behind a window with first tokens, and the attention weights that keys receive.
+struct WindowLayout {
+  TreeLayout tree;
+  int64_t items_off, item_cum_off, lse_off, bytes;
+};
+WindowLayout window_layout(int32_t num_seqs, int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                           int32_t head_dim, int64_t max_keys, int32_t rows_per_item, int32_t key_tile,
+                           int32_t max_grid, bool own_lse);
+cudaError_t launch_window_plan(const TreeParams& p, cudaStream_t stream);
+cudaError_t launch_window_generic(const TreeParams& p, pa_dtype kv_dtype, cudaStream_t stream);
+cudaError_t launch_window_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const TreeParams& p, bool fp8, uint64_t wait_limit, uint32_t stall,
+                             cudaStream_t stream);
+// The weights of a batch whose plan and log-sum-exps (p.m.lse) are there.
+cudaError_t launch_key_weights_generic(const TreeParams& p, pa_dtype kv_dtype, cudaStream_t stream);
+
+struct EvictParams {
+  void* k_blocks;
+  void* v_blocks;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  float* key_weights;  // [num_seqs, num_kv_heads, weights_len], or null
+  int64_t weights_len;
+  int32_t num_seqs, keep_first, keep_recent, num_kv_heads, block_size, max_blocks;
+  int64_t num_blocks;
+  int64_t row_bytes;  // of one position and kv head
+  int32_t* moves;     // workspace: lists of up to moves_len fillers for each (sequence, kv head)
+  int64_t moves_len;  // most keys of a sequence
+  int* status;
+};
+constexpr int64_t kEvictMostKeys = 1 << 19;  // of a sequence: two bits each in shared memory
+int64_t evict_workspace(int32_t num_seqs, int32_t num_kv_heads, int64_t max_keys);
+cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream);
 
 // Status word and SM count of the current device, cached per context; null on a CUDA error.
 struct DeviceState {
