@@ -36,7 +36,151 @@ __device__ __forceinline__ Keys keys_from(const TreeParams& p, int lowest) {
   return Keys{front, max(lo - front, 0)};
 }
 
-// Block 0 plans; blocks 1 .. check the sequences' positions and table entries.  Everything is read
+// First token, tokens and length of sequence s; false (and no tokens) when they cannot be used.
+__device__ __forceinline__ bool sequence(const TreeParams& p, int s, int& qs, int& q, int& n) {
+  const VarlenMeta& m = p.m;
+  qs = m.query_start_loc[s];
+  const int qe = m.query_start_loc[s + 1];
+  q = n = 0;
+  bool ok = qs >= 0 && qe >= qs && (int64_t)qe <= m.num_tokens && (s > 0 || qs == 0) &&
+            (s < m.num_seqs - 1 || (int64_t)qe == m.num_tokens);
+  if (qs >= 0 && qe > qs && (int64_t)qe <= m.num_tokens) {
+    q = qe - qs;
+    n = m.seq_lens[s];
+    if (n < 1 || ((int64_t)n + m.block_size - 1) / m.block_size > m.max_blocks ||
+        (p.key_weights && (int64_t)n > p.weights_len)) {
+      ok = false;
+      q = 0;
+    }
+  }
+  return ok;
+}
+
+// The first of a sequence's tokens [a, b) at position `at` or later (b: none).  Mostly they are
+// consecutive: then it is found at once.
+__device__ __forceinline__ int token_from(const int32_t* pos, int a, int b, int64_t at) {
+  const int64_t guess = a + max(at - pos[a], (int64_t)0);
+  if (guess == a) return a;
+  if (guess < b && pos[guess] == at && pos[guess - 1] < at) return (int)guess;
+  while (a < b) {
+    const int mid = a + (b - a) / 2;
+    if (pos[mid] < at) a = mid + 1; else b = mid;
+  }
+  return a;
+}
+
+// The work of an item of the key weights, in about hundredths of a microsecond (only the balance
+// between the CTAs depends on it): its keys, and each row tile.
+constexpr int kWeightItem = 150, kWeightRowTile = 100;
+
+// One block: the plan of the key weights (k_weights_tc.cu).  It checks what it uses as an index and
+// leaves the errors to block 0, which finds the same; a batch that is not valid has no items.
+__device__ void plan_weights(const TreeParams& p, int64_t* s_warp, int64_t* s_cum, int* s_base) {
+  const VarlenMeta& m = p.m;
+  const int tid = threadIdx.x;
+  const bool shared = m.num_seqs <= kCumShared;
+  bool bad = false;
+  int64_t items = 0;
+  for (int s0 = 0; s0 < m.num_seqs; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    int qs = 0, q = 0, n = 0, mine = 0;
+    int4 first = make_int4(0, 0, 0, 0);
+    if (s < m.num_seqs) {
+      bad |= !sequence(p, s, qs, q, n);
+      if (q > 0) {
+        // the keys that counted tokens see: those of the first positions, and from lo to the last one
+        const int skip = p.observed > 0 ? max(0, q - p.observed) : 0;
+        const int low = m.positions[qs + skip], last = m.positions[qs + q - 1];
+        bad |= low < 0 || last < low || last >= n;
+        const int end = min(max(last, 0), n - 1) / kWeightKeys + 1;
+        const int lo = m.window > 0 ? max(min(low, n - 1) - m.window + 1, 0) / kWeightKeys : 0;
+        const int front = m.window > 0 ? min((p.first + kWeightKeys - 1) / kWeightKeys, end) : 0;
+        const int gap = max(lo - front, 0);
+        mine = max(end - gap, 0);
+        first = make_int4(0, 0, front, gap);
+        p.w.seqs[2 * s + 1] = make_int4(qs + skip, q - skip, n, 0);
+      }
+    }
+    int64_t total;
+    const int64_t at = items + block_sum_scan(mine, s_warp, &total);
+    if (s < m.num_seqs) {
+      p.w.seqs[2 * s] = make_int4((int)at, mine, first.z, first.w);
+      if (shared) s_base[s] = (int)at;
+    }
+    items += total;
+  }
+  if (__syncthreads_or(bad)) items = 0;
+  int64_t base = 0;
+  for (int64_t i0 = 0; i0 < items; i0 += kPlanThreads) {
+    const int64_t i = i0 + tid;
+    int64_t weight = 0;
+    if (i < items) {
+      int lo = 0, hi = m.num_seqs;  // the last sequence whose first item is at most i: it has items
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((shared ? s_base[mid] : p.w.seqs[2 * mid].x) <= i) lo = mid; else hi = mid;
+      }
+      const int4 r = p.w.seqs[2 * lo], t = p.w.seqs[2 * lo + 1];
+      int tile = (int)(i - r.x);
+      if (tile >= r.z) tile += r.w;
+      const int64_t key0 = (int64_t)tile * kWeightKeys;
+      // tokens that see one of the keys at least
+      const int a = token_from(m.positions, t.x, t.x + t.y, key0) - t.x;
+      int b = t.y;
+      if (m.window > 0 && key0 >= p.first)
+        b = token_from(m.positions, t.x, t.x + t.y, key0 + kWeightKeys - 1 + m.window) - t.x;
+      // (an item between the tokens' positions, where these skip, may be seen by none)
+      const int r0 = a / p.tile_tokens, r1 = max((b + p.tile_tokens - 1) / p.tile_tokens, r0 + 1);
+      p.w.items[i] = make_int4(tile, r0, r1, 0);
+      weight = kWeightItem + (int64_t)kWeightRowTile * (r1 - r0);
+    }
+    int64_t total;
+    const int64_t at = base + block_sum_scan(weight, s_warp, &total);
+    if (i < items) p.w.cum[i] = at;
+    base += total;
+  }
+  if (tid == 0) p.w.cum[items] = base;
+  __syncthreads();
+  if (items == 0) {
+    for (int s = tid; s < m.num_seqs; s += kPlanThreads) p.w.seqs[2 * s] = make_int4(0, 0, 0, 0);
+    for (int c = tid; c <= p.w.grid; c += kPlanThreads) p.w.starts[c] = make_int4(m.num_seqs, 0, 0, 0);
+    return;
+  }
+  for (int s = tid; shared && s <= m.num_seqs; s += kPlanThreads)
+    s_cum[s] = (s < m.num_seqs ? p.w.cum[p.w.seqs[2 * s].x] : base) * m.num_kv_heads;
+  __syncthreads();
+  base *= m.num_kv_heads;
+  for (int c = tid; c <= p.w.grid; c += kPlanThreads) {
+    int4 st = make_int4(m.num_seqs, 0, 0, 0);
+    if (c < p.w.grid) {
+      auto before = [&](int s) {
+        return shared ? s_cum[s]
+                      : (s < m.num_seqs ? p.w.cum[p.w.seqs[2 * s].x] * m.num_kv_heads : base);
+      };
+      const int64_t x = base / p.w.grid * c + base % p.w.grid * c / p.w.grid;  // floor(base c / grid)
+      int lo = 0, hi = m.num_seqs;  // the last sequence with no more weight before it
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (before(mid) <= x) lo = mid; else hi = mid;
+      }
+      const int64_t at = before(lo), per_head = (before(lo + 1) - at) / m.num_kv_heads;
+      const int4 r = p.w.seqs[2 * lo];
+      const int kvh = (int)((x - at) / per_head);
+      const int64_t rem = (x - at) % per_head, cum0 = p.w.cum[r.x];
+      int it = 0, top = r.y;
+      while (top - it > 1) {
+        const int mid = (it + top) >> 1;
+        if (p.w.cum[r.x + mid] - cum0 <= rem) it = mid; else top = mid;
+      }
+      const int4 w = p.w.items[r.x + it];
+      const int64_t in = max(rem - (p.w.cum[r.x + it] - cum0) - kWeightItem, (int64_t)0);
+      st = make_int4(lo, kvh, it, (int)min(w.y + in / kWeightRowTile, (int64_t)w.z - 1));
+    }
+    p.w.starts[c] = st;
+  }
+}
+
+// Block 0 plans (block 1 the key weights, where they are asked for); the blocks behind check the sequences' positions and table entries.  Everything is read
 // after the wait for the kernels ahead, and no output is written before this launch is done.  A plan
 // that failed is one of empty shares and of sequences without tokens, so the kernels behind do nothing
 // even where another stream has cleared the status word in between.
@@ -49,9 +193,14 @@ __global__ void __launch_bounds__(kPlanThreads) k_window_plan(const TreeParams p
   pdl_wait();
   pdl_launch_dependents();
   bool bad = false;
+  const int planners = p.w.grid > 0 ? 2 : 1;
+  if (blockIdx.x == 1 && planners == 2) {
+    plan_weights(p, s_warp, s_cum, s_base);
+    return;
+  }
   if (blockIdx.x > 0) {
-    const int warps = (gridDim.x - 1) * (kPlanThreads / 32);
-    const int me = (blockIdx.x - 1) * (kPlanThreads / 32) + warp;
+    const int warps = (gridDim.x - planners) * (kPlanThreads / 32);
+    const int me = (blockIdx.x - planners) * (kPlanThreads / 32) + warp;
     const int per = (m.max_blocks + 255) / 256;  // chunks of a table row
     const int64_t chunks = (int64_t)m.num_seqs * per;
     for (int64_t c = me; c < chunks; c += warps) {
@@ -101,21 +250,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_window_plan(const TreeParams p
   for (int s0 = 0; s0 < m.num_seqs; s0 += kPlanThreads) {
     const int s = s0 + tid;
     int qs = 0, q = 0, n = 0;
-    if (s < m.num_seqs) {
-      qs = m.query_start_loc[s];
-      const int qe = m.query_start_loc[s + 1];
-      bad |= qs < 0 || qe < qs || (int64_t)qe > m.num_tokens || (s == 0 && qs != 0) ||
-             (s == m.num_seqs - 1 && (int64_t)qe != m.num_tokens);
-      if (qs >= 0 && qe > qs && (int64_t)qe <= m.num_tokens) {
-        q = qe - qs;
-        n = m.seq_lens[s];
-        if (n < 1 || ((int64_t)n + m.block_size - 1) / m.block_size > m.max_blocks ||
-            (p.key_weights && (int64_t)n > p.weights_len)) {
-          bad = true;
-          q = 0;
-        }
-      }
-    }
+    if (s < m.num_seqs) bad |= !sequence(p, s, qs, q, n);
     const int rows = q * m.group, mine = (rows + p.rows_per_item - 1) / p.rows_per_item;
     int64_t total;
     const int64_t at = items + block_sum_scan(mine, s_warp, &total);
@@ -204,7 +339,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_window_plan(const TreeParams p
 
 WindowLayout window_layout(int32_t num_seqs, int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
                            int32_t head_dim, int64_t max_keys, int32_t rows_per_item, int32_t key_tile,
-                           int32_t max_grid, bool own_lse) {
+                           int32_t max_grid, bool weights) {
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   const int32_t group = num_heads / num_kv_heads;
   const TreeLayout t = tree_layout(num_seqs, num_tokens, group, num_kv_heads, head_dim, max_keys,
@@ -215,7 +350,14 @@ WindowLayout window_layout(int32_t num_seqs, int64_t num_tokens, int32_t num_hea
   L.items_off = t.bytes;
   L.item_cum_off = L.items_off + up(16 * items);
   L.lse_off = L.item_cum_off + up(8 * (items + 1));
-  L.bytes = L.lse_off + (own_lse ? up(4 * num_tokens * num_heads) : 0);
+  L.bytes = L.w_seqs_off = L.lse_off + (weights ? up(4 * num_tokens * num_heads) : 0);
+  if (!weights) return L;
+  const int64_t key_items = std::min<int64_t>(num_seqs, num_tokens) * ((max_keys + kWeightKeys - 1) / kWeightKeys);
+  L.w_items_off = L.w_seqs_off + up(32 * (int64_t)num_seqs);
+  L.w_cum_off = L.w_items_off + up(16 * key_items);
+  L.w_starts_off = L.w_cum_off + up(8 * (key_items + 1));
+  L.w_part_off = L.w_starts_off + up(16 * (kTreeTcGrid + 1));
+  L.bytes = L.w_part_off + up(8 * (int64_t)kTreeTcGrid * kWeightKeys);
   return L;
 }
 
@@ -224,7 +366,7 @@ cudaError_t launch_window_plan(const TreeParams& p, cudaStream_t stream) {
   const int64_t chunks = (int64_t)p.m.num_seqs * ((p.m.max_blocks + 255) / 256 +
                                                   (p.m.num_tokens + kCheckTokens - 1) / kCheckTokens);
   const int blocks = (int)std::min<int64_t>((chunks + 31) / 32, 64);
-  return launch_pdl(k_window_plan, dim3(1 + blocks), dim3(kPlanThreads), 0, stream, p);
+  return launch_pdl(k_window_plan, dim3((p.w.grid > 0 ? 2 : 1) + blocks), dim3(kPlanThreads), 0, stream, p);
 }
 
 cudaError_t launch_window_generic(const TreeParams& p, pa_dtype kv, cudaStream_t stream) {

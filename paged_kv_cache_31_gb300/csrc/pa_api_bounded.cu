@@ -151,6 +151,14 @@ pa_status attend(const Call& c) {
   p.item_keys = reinterpret_cast<int4*>(ws + L.items_off);
   p.item_cum = reinterpret_cast<int64_t*>(ws + L.item_cum_off);
   if (c.weighs && !m.lse) m.lse = reinterpret_cast<float*>(ws + L.lse_off);
+  if (c.weighs && tc) {
+    p.w.seqs = reinterpret_cast<int4*>(ws + L.w_seqs_off);
+    p.w.items = reinterpret_cast<int4*>(ws + L.w_items_off);
+    p.w.cum = reinterpret_cast<int64_t*>(ws + L.w_cum_off);
+    p.w.starts = reinterpret_cast<int4*>(ws + L.w_starts_off);
+    p.w.part = reinterpret_cast<float*>(ws + L.w_part_off);
+    p.w.grid = std::min(kTreeTcGrid, d->sms);
+  }
   CUtensorMap tq, tk, tv;
   if (tc) {
     const bool ok =
@@ -162,16 +170,17 @@ pa_status attend(const Call& c) {
     if (!ok) return PA_ECUDA;
   }
   if (launch_window_plan(p, c.stream) != cudaSuccess) return PA_ECUDA;
+  uint64_t limit;
+  uint32_t stall;
+  stall_hook(limit, stall);
   if (tc) {
-    uint64_t limit;
-    uint32_t stall;
-    stall_hook(limit, stall);
     if (launch_window_tc(tq, tk, tv, p, fp8, limit, stall, c.stream) != cudaSuccess) return PA_ECUDA;
   } else if (launch_window_generic(p, c.kv_dtype, c.stream) != cudaSuccess) {
     return PA_ECUDA;
   }
   if (launch_tree_merge(p, c.stream) != cudaSuccess) return PA_ECUDA;
   if (!c.weighs) return PA_OK;
+  if (p.w.grid > 0) return from_cuda(launch_weights_tc(tq, tk, p, fp8, limit, stall, c.stream));
   return from_cuda(launch_key_weights_generic(p, c.kv_dtype, c.stream));
 }
 

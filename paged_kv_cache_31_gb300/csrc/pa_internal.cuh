@@ -625,6 +625,17 @@ struct TreeParams {
   float* key_weights;
   int64_t weights_len;
   int32_t observed;
+  // Their plan for the tensor-core kernel (k_weights_tc.cu; grid 0: there is none): an item is kWeightKeys
+  // keys of one (sequence, kv head).
+  struct {
+    int4* seqs;    // [num_seqs, 2] (first item, items, front key tiles, gap in tiles behind them), (first counted
+                   // token, tokens, keys, 0)
+    int4* items;   // (key tile, first row tile, end, 0), of all sequences, once for all kv heads
+    int64_t* cum;  // [items + 1] weight before the item
+    int4* starts;  // [grid + 1] (sequence, kv head, item, row tile) where each CTA's share begins
+    float* part;   // [2 * grid, kWeightKeys] sums of cut items' pieces
+    int32_t grid;
+  } w;
 };
 // The work of an item, in about hundredths of a microsecond (only the balance between the CTAs
 // depends on it): a key tile of one row tile takes about 1.5 us, a little more the more warps its
@@ -663,11 +674,14 @@ int tree_clusters_resident(int device, bool fp8, int head_dim, int c);  // c 2, 
 // Attention behind a window with first tokens, and the attention weights that keys receive.
 struct WindowLayout {
   TreeLayout tree;
-  int64_t items_off, item_cum_off, lse_off, bytes;
+  int64_t items_off, item_cum_off, lse_off;
+  int64_t w_seqs_off, w_items_off, w_cum_off, w_starts_off, w_part_off;  // given weights
+  int64_t bytes;
 };
+constexpr int32_t kWeightKeys = 256;  // of an item of the weights' tensor-core kernel
 WindowLayout window_layout(int32_t num_seqs, int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
                            int32_t head_dim, int64_t max_keys, int32_t rows_per_item, int32_t key_tile,
-                           int32_t max_grid, bool own_lse);
+                           int32_t max_grid, bool weights);
 cudaError_t launch_window_plan(const TreeParams& p, cudaStream_t stream);
 cudaError_t launch_window_generic(const TreeParams& p, pa_dtype kv_dtype, cudaStream_t stream);
 cudaError_t launch_window_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -675,6 +689,8 @@ cudaError_t launch_window_tc(const CUtensorMap& tq, const CUtensorMap& tk, const
                              cudaStream_t stream);
 // The weights of a batch whose plan and log-sum-exps (p.m.lse) are there.
 cudaError_t launch_key_weights_generic(const TreeParams& p, pa_dtype kv_dtype, cudaStream_t stream);
+cudaError_t launch_weights_tc(const CUtensorMap& tq, const CUtensorMap& tk, const TreeParams& p, bool fp8,
+                              uint64_t wait_limit, uint32_t stall, cudaStream_t stream);
 
 struct EvictParams {
   void* k_blocks;
