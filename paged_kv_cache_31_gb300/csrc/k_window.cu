@@ -56,6 +56,76 @@ __device__ __forceinline__ bool sequence(const TreeParams& p, int s, int& qs, in
   return ok;
 }
 
+// Warp `me` of `warps`: the sequences' table entries that are read, and their positions; true when one
+// is bad.  (Sequences that cannot be used are found by sequence().)
+__device__ __forceinline__ bool bad_reads(const TreeParams& p, int me, int warps) {
+  const VarlenMeta& m = p.m;
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  const int per = (m.max_blocks + 255) / 256;  // chunks of a table row
+  const int64_t chunks = (int64_t)m.num_seqs * per;
+  for (int64_t c = me; c < chunks; c += warps) {
+    const int s = (int)(c / per), e0 = (int)(c % per) * 256;
+    const int qs = m.query_start_loc[s], n = m.seq_lens[s];
+    if (m.query_start_loc[s + 1] <= qs || n < 1 || qs < 0 || qs >= m.num_tokens) continue;
+    const int64_t need = ((int64_t)n + m.block_size - 1) / m.block_size;
+    const int lim = (int)min(need, (int64_t)m.max_blocks);
+    if (e0 >= lim) continue;
+    const Keys k = keys_from(p, m.window > 0 ? m.positions[qs] : 0);
+    const int32_t* row = m.block_tables + (int64_t)s * m.max_blocks;
+    int id[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int e = e0 + lane + 32 * u;
+      id[u] = e < lim && (e < k.front || e >= k.front + k.gap) ? row[e] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) bad |= id[u] < 0 || (int64_t)id[u] >= m.num_blocks;
+  }
+  const int parts = (int)((m.num_tokens + kCheckTokens - 1) / kCheckTokens);
+  const int64_t units = (int64_t)m.num_seqs * parts;
+  for (int64_t c = me; c < units; c += warps) {
+    const int s = (int)(c / parts);
+    const int64_t t0 = (int64_t)m.query_start_loc[s] + c % parts * kCheckTokens;
+    const int64_t end = min(min((int64_t)m.query_start_loc[s + 1], t0 + kCheckTokens), m.num_tokens);
+    if (t0 < 0 || t0 >= end) continue;
+    const int n = m.seq_lens[s];
+    const bool more = t0 + kCheckTokens < m.query_start_loc[s + 1] && t0 + kCheckTokens < m.num_tokens;
+    for (int64_t t = t0 + lane; t < end; t += 32) {
+      const int pos = m.positions[t];
+      const int after = t + 1 < end || more ? m.positions[t + 1] : pos;
+      bad |= pos < 0 || pos >= n || after < pos;
+    }
+  }
+  return bad;
+}
+
+// Per-head scales (each array may be missing).
+__device__ __forceinline__ bool bad_scales(const TreeParams& p, int tid, int threads) {
+  bool bad = false;
+  for (int g = tid; g < p.m.num_kv_heads; g += threads) {
+    const float a = p.m.k_scales ? p.m.k_scales[g] : 1.f, b = p.m.v_scales ? p.m.v_scales[g] : 1.f;
+    bad |= !(a > 0.f && a <= 3.402823466e38f) || !(b > 0.f && b <= 3.402823466e38f);
+  }
+  return bad;
+}
+
+// In front of k_window_decode, which starts once every block has waited for the work ahead and waits for
+// the end of this kernel before it writes.
+__global__ void __launch_bounds__(256) k_window_check(const TreeParams p) {
+  const VarlenMeta& m = p.m;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int at = blockIdx.x * 256 + threadIdx.x, threads = gridDim.x * 256;
+  bool bad = blockIdx.x == 0 && bad_scales(p, threadIdx.x, 256);
+  for (int s = at; s < m.num_seqs; s += threads) {
+    int qs, q, n;
+    bad |= !sequence(p, s, qs, q, n);
+  }
+  bad |= bad_reads(p, at >> 5, threads >> 5);
+  if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) record_error(p.status, PA_EINVAL);
+}
+
 // The first of a sequence's tokens [a, b) at position `at` or later (b: none).  Mostly they are
 // consecutive: then it is found at once.
 __device__ __forceinline__ int token_from(const int32_t* pos, int a, int b, int64_t at) {
@@ -200,51 +270,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_window_plan(const TreeParams p
   }
   if (blockIdx.x > 0) {
     const int warps = (gridDim.x - planners) * (kPlanThreads / 32);
-    const int me = (blockIdx.x - planners) * (kPlanThreads / 32) + warp;
-    const int per = (m.max_blocks + 255) / 256;  // chunks of a table row
-    const int64_t chunks = (int64_t)m.num_seqs * per;
-    for (int64_t c = me; c < chunks; c += warps) {
-      const int s = (int)(c / per), e0 = (int)(c % per) * 256;
-      const int qs = m.query_start_loc[s], n = m.seq_lens[s];
-      if (m.query_start_loc[s + 1] <= qs || n < 1 || qs < 0 || qs >= m.num_tokens) continue;
-      const int64_t need = ((int64_t)n + m.block_size - 1) / m.block_size;
-      const int lim = (int)min(need, (int64_t)m.max_blocks);
-      if (e0 >= lim) continue;
-      const Keys k = keys_from(p, m.window > 0 ? m.positions[qs] : 0);
-      const int32_t* row = m.block_tables + (int64_t)s * m.max_blocks;
-      int id[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int e = e0 + lane + 32 * u;
-        id[u] = e < lim && (e < k.front || e >= k.front + k.gap) ? row[e] : 0;
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) bad |= id[u] < 0 || (int64_t)id[u] >= m.num_blocks;
-    }
-    const int parts = (int)((m.num_tokens + kCheckTokens - 1) / kCheckTokens);
-    const int64_t units = (int64_t)m.num_seqs * parts;
-    for (int64_t c = me; c < units; c += warps) {
-      const int s = (int)(c / parts);
-      const int64_t t0 = (int64_t)m.query_start_loc[s] + c % parts * kCheckTokens;
-      const int64_t end = min(min((int64_t)m.query_start_loc[s + 1], t0 + kCheckTokens), m.num_tokens);
-      if (t0 < 0 || t0 >= end) continue;
-      const int n = m.seq_lens[s];
-      const bool more = t0 + kCheckTokens < m.query_start_loc[s + 1] && t0 + kCheckTokens < m.num_tokens;
-      for (int64_t t = t0 + lane; t < end; t += 32) {
-        const int pos = m.positions[t];
-        const int after = t + 1 < end || more ? m.positions[t + 1] : pos;
-        bad |= pos < 0 || pos >= n || after < pos;
-      }
-    }
-    if (__any_sync(kFull, bad) && lane == 0) record_error(p.status, PA_EINVAL);
+    bad = bad_reads(p, (blockIdx.x - planners) * (kPlanThreads / 32) + warp, warps);
+    if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(p.status, PA_EINVAL);
     return;
   }
 
-  // per-head scales (each array may be missing)
-  for (int g = tid; g < m.num_kv_heads; g += kPlanThreads) {
-    const float a = m.k_scales ? m.k_scales[g] : 1.f, b = m.v_scales ? m.v_scales[g] : 1.f;
-    bad |= !(a > 0.f && a <= 3.402823466e38f) || !(b > 0.f && b <= 3.402823466e38f);
-  }
+  bad = bad_scales(p, tid, kPlanThreads);
   const bool shared = m.num_seqs <= kCumShared;
   int64_t items = 0;
   for (int s0 = 0; s0 < m.num_seqs; s0 += kPlanThreads) {
@@ -367,6 +398,13 @@ cudaError_t launch_window_plan(const TreeParams& p, cudaStream_t stream) {
                                                   (p.m.num_tokens + kCheckTokens - 1) / kCheckTokens);
   const int blocks = (int)std::min<int64_t>((chunks + 31) / 32, 64);
   return launch_pdl(k_window_plan, dim3((p.w.grid > 0 ? 2 : 1) + blocks), dim3(kPlanThreads), 0, stream, p);
+}
+
+cudaError_t launch_window_check(const TreeParams& p, cudaStream_t stream) {
+  const int64_t units = (int64_t)p.m.num_seqs * ((p.m.max_blocks + 255) / 256 +
+                                                 (p.m.num_tokens + kCheckTokens - 1) / kCheckTokens);
+  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>((units + 7) / 8, 64));
+  return launch_pdl(k_window_check, dim3(blocks), dim3(256), 0, stream, p);
 }
 
 cudaError_t launch_window_generic(const TreeParams& p, pa_dtype kv, cudaStream_t stream) {

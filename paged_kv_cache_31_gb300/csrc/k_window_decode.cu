@@ -1,0 +1,773 @@
+// k_window_decode.cu -- attention behind a window with first tokens, and the attention weights that keys
+// receive, for batches of decoding tokens: bf16 queries over bf16 (head size 64 / 128) or e4m3 (128)
+// pools of 16-position blocks.
+//
+// Work.  A cluster of CTAs for each (sequence, kv head) shares the visible blocks (k_window.cu counts
+// them without the gap) in even, contiguous runs; a CTA's warps take the run's blocks in turn, each
+// through its own ring of TMA stages, so every key is read once.  The warps' and then the CTAs' softmax
+// states (m, l, O) are joined in fixed order, through shared memory and the cluster's.  The metadata are
+// checked by a kernel in front (k_window_check), beside which this one loads and computes already: it
+// waits for it before it writes, and bounds its own indices until then.  Two launches instead of the
+// three of a planned call, and no partial states in memory.
+//
+// Math.  As k_decode_mma.cu: S = Q K^T on the m16n8k16 warp MMA (bf16), rows = (token, head) pairs, an
+// online softmax over 16 keys at a time, P as a bf16 pair; e4m3 pools swap the operands, S^T = K Q^T and
+// O^T = V^T P^T in f16, with the codes widened in registers and the dimensions in a permuted order that
+// makes a lane's bytes contiguous.
+//
+// Weights.  exp(s - lse) needs a row's final log-sum-exp, so a CTA keeps the scores of its keys in shared
+// memory (16 KB: 1024 keys of 4 heads) until the states have been joined, and adds each key's sum to
+// memory then: K is read once, where a second pass over it would read half as many bytes again.  Keys
+// past that room are multiplied once more.  A key belongs to one thread: no atomics.
+//
+// What bounds it: the K / V bytes.
+#include <algorithm>
+
+#include "k_tree.cuh"
+
+namespace pa {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kBlk = 16;
+
+template <int D, bool FP8>
+struct Shape {
+  static constexpr int NW = FP8 ? 8 : 4;   // warps
+  static constexpr int NS = 3;             // stages of a warp's ring
+  static constexpr int TR = FP8 ? 8 : 16;  // query rows of a tile
+  static constexpr int kHalves = FP8 ? 1 : D / 64;
+  static constexpr int kTile = kHalves * kBlk * 128;  // a block's K (or V) of one kv head
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kNT = D / 8, kKS = D / 16;
+  static constexpr int kRing = NW * NS * kStage;
+  // scores of a CTA's keys, and the states that are joined (in the ring's place)
+  static constexpr int kScores = 15360;
+  static constexpr int kLd = D + 4;
+  static constexpr int kOffState = NW * 16 * kLd * 4;  // behind the warps' O: the CTA's
+  static_assert(kOffState + 16 * kLd * 4 <= kRing, "states lie in the ring");
+  static constexpr int kOffSmall = kRing;  // struct Small
+  static constexpr int kOffScores = kOffSmall + 1664;
+  static constexpr int smem(bool weigh) { return kOffScores + (weigh ? kScores : 0); }
+  static_assert(2 * (1024 + kOffScores + kScores) <= 228 * 1024, "two CTAs per SM");
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\t"
+      "barrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+__device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ uint32_t peer_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 peer_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Byte offset of 16-byte chunk `chunk` (along D) of row `row` of a block written by a 5-D box: 8-row
+// groups of (dim half, 8 rows of 128 bytes), 128-byte swizzle.
+template <int HALVES>
+__device__ __forceinline__ uint32_t tile_off(int row, int chunk) {
+  return (uint32_t)((row >> 3) * HALVES * 1024 + (chunk >> 3) * 1024 + (row & 7) * 128 +
+                    (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+template <int NW, int NS>
+struct Small {
+  uint64_t full[NW * NS + 1];  // the last: nothing arrives on it (the debug_stall test hook)
+  float2 warp_ml[NW][16];
+  float2 ml[16];  // the CTA's state, read by its cluster
+  float lse[16], norm[16];
+  int fail;
+};
+
+template <int D, bool FP8, bool WEIGH>
+__global__ void __launch_bounds__(Shape<D, FP8>::NW * 32, 2)
+    k_window_decode(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                    const TreeParams p, uint64_t limit, uint32_t stall) {
+  using S = Shape<D, FP8>;
+  constexpr int NW = S::NW, NS = S::NS, TR = S::TR, LD = S::kLd;
+  extern __shared__ __align__(1024) uint8_t ring[];
+  using Sm = Small<NW, NS>;
+  static_assert(sizeof(Sm) <= S::kOffScores - S::kOffSmall, "kOffScores");
+  Sm& sh = *reinterpret_cast<Sm*>(ring + S::kOffSmall);
+  float* scores = reinterpret_cast<float*>(ring + S::kOffScores);
+  float* mrg_o = reinterpret_cast<float*>(ring);
+  float* state = reinterpret_cast<float*>(ring + S::kOffState);
+  uint64_t* full = sh.full;
+  const VarlenMeta& m = p.m;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = p.cluster, rank = C > 1 ? (int)cluster_rank() : 0;
+  if (tid <= NW * NS) mbar_init(&full[tid], 1);
+  if (tid == 0) {
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+    // (the swizzled tiles need the alignment that the declaration asks for)
+    sh.fail = (smem_u32(ring) & 1023u) != 0;
+    if (sh.fail) record_error(p.status, PA_ECUDA);
+  }
+  fence_mbar_init();
+  __syncthreads();
+  // (the kernel in front lets this one start once it has waited for all work before it)
+  const int unit = blockIdx.x / C, s = unit / m.num_kv_heads, kvh = unit % m.num_kv_heads;
+  const int H = m.num_heads, G = m.group;
+  const int qs = m.query_start_loc[s], qe = m.query_start_loc[s + 1], n = m.seq_lens[s];
+  // numbers that cannot be used as indices: no rows (the check records the error)
+  const bool usable = qs >= 0 && qe >= qs && (int64_t)qe <= m.num_tokens && n >= 1 &&
+                      ((int64_t)n + kBlk - 1) / kBlk <= m.max_blocks &&
+                      (!WEIGH || (int64_t)n <= p.weights_len);
+  const int rows = usable && !sh.fail ? (qe - qs) * G : 0;
+  const int counted0 = WEIGH && p.observed > 0 ? max(0, qe - qs - p.observed) * G : 0;  // row
+  const int32_t* table = m.block_tables + (int64_t)s * m.max_blocks;
+  const float sl = p.scale * kLog2e;
+  uint32_t ring_pos = 0;
+  bool waited = false;
+
+  for (int row0 = 0; row0 < rows; row0 += TR) {
+    const int nrow = min(TR, rows - row0);
+    const int low = min(max(m.positions[qs + row0 / G], 0), n - 1);
+    const int high = min(max(m.positions[qs + (row0 + nrow - 1) / G], low), n - 1);
+    // the tile's blocks, counted without the gap, and this CTA's run of them
+    const int front = (p.first + kBlk - 1) / kBlk;
+    const int gap = m.window > 0 ? max(max(low - m.window + 1, 0) / kBlk - front, 0) : 0;
+    const int vn = n - gap * kBlk;
+    const int nblk = (high - gap * kBlk) / kBlk + 1;
+    const int run0 = (int)((int64_t)nblk * rank / C), run1 = (int)((int64_t)nblk * (rank + 1) / C);
+    const int count = run1 - run0;
+    const int mine = count > warp ? (count - warp + NW - 1) / NW : 0;  // blocks run0 + warp + NW x
+    auto pos_of = [&](int r) {  // counted without the gap; -1: no row
+      const int R = row0 + r;
+      return r < nrow ? min(max(m.positions[qs + R / G], 0), n - 1) - gap * kBlk : -1;
+    };
+
+    int win = -1, ids = 0;
+    auto block_id = [&](int x) -> int {  // whole warp
+      if ((x >> 5) != win) {
+        win = x >> 5;
+        const int i = (win << 5) + lane;
+        ids = -1;
+        if (i < mine) {
+          int b = run0 + warp + NW * i;
+          if (b >= front) b += gap;
+          ids = table[b];
+          if (ids < 0 || (int64_t)ids >= m.num_blocks) ids = -1;
+        }
+      }
+      return __shfl_sync(kFull, ids, x & 31);
+    };
+    auto issue = [&](int x, uint32_t at, bool with_v) {  // whole warp: its block x as copy `at`
+      const int id = block_id(x);
+      if (lane == 0) {
+        const uint32_t slot = at % NS;
+        uint64_t* bar = &full[warp * NS + slot];
+        uint8_t* dst = ring + (size_t)(warp * NS + slot) * S::kStage;
+        mbar_arrive_expect_tx(bar, with_v ? S::kStage : S::kTile);
+        // (an id outside the pool reads zeros from outside it)
+        if constexpr (FP8) {
+          tma_load_3d(dst, &tk, 0, kvh, id >= 0 ? id * kBlk : -kBlk, bar);
+          if (with_v) tma_load_3d(dst + S::kTile, &tv, 0, kvh, id >= 0 ? id * kBlk : -kBlk, bar);
+        } else {
+          tma_load_5d(dst, &tk, 0, 0, 0, id >= 0 ? id * 2 : -2, kvh, bar);
+          if (with_v) tma_load_5d(dst + S::kTile, &tv, 0, 0, 0, id >= 0 ? id * 2 : -2, kvh, bar);
+        }
+      }
+    };
+    int issued = 0;
+    for (; issued < min(mine, NS); ++issued) issue(issued, ring_pos + issued, true);
+
+    // scores to log2 units, of this lane's rows
+    float sk[2];
+    sk[0] = sk[1] = head_scale(m.k_scales, kvh, sl);
+    // ---- q fragments and the rows' visible keys
+    uint32_t qa[S::kKS][4];
+    int pos[2], lo[2];  // of this lane's rows: bf16 lane / 4 (+ 8), e4m3 2 (lane % 4) (+ 1)
+    {
+      const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = FP8 ? 2 * c + i : g + 8 * i;
+        pos[i] = pos_of(r);
+        lo[i] = m.window > 0 ? max(pos[i] - m.window, -1) + 1 : 0;
+      }
+      const int r0 = min(g, nrow - 1) + row0, r1 = min(g + 8, nrow - 1) + row0;
+      const uint32_t* q0 = reinterpret_cast<const uint32_t*>(
+          static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)(qs + r0 / G) * H + kvh * G + r0 % G) * D);
+      const uint32_t* q1 = reinterpret_cast<const uint32_t*>(
+          static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)(qs + r1 / G) * H + kvh * G + r1 % G) * D);
+      const bool v0 = g < nrow, v1 = g + 8 < nrow;
+      if constexpr (FP8) {
+        // dims 32c + 4kk + {0, 1} and {2, 3} of row g (the permuted order), as f16 with a power of two a
+        // row that brings its largest element to [2^14, 2^15): exact down to 2^-28 of that.  An infinity
+        // makes the whole row NaN.
+        uint2 w[8];
+        float big = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          w[kk] = v0 ? *reinterpret_cast<const uint2*>(q0 + 16 * c + 2 * kk) : make_uint2(0u, 0u);
+          big = fmaxf(big, fmaxf(fmaxf(fabsf(__uint_as_float(w[kk].x << 16)),
+                                       fabsf(__uint_as_float(w[kk].x & 0xffff0000u))),
+                                 fmaxf(fabsf(__uint_as_float(w[kk].y << 16)),
+                                       fabsf(__uint_as_float(w[kk].y & 0xffff0000u)))));
+        }
+        big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
+        const int up = min(max(141 - (int)(__float_as_uint(big) >> 23), -113), 120);
+        const float f = big < INFINITY ? __uint_as_float((uint32_t)(127 + up) << 23) : NAN;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          qa[kk][0] = pack_f16x2(__uint_as_float(w[kk].x << 16) * f, __uint_as_float(w[kk].x & 0xffff0000u) * f);
+          qa[kk][2] = pack_f16x2(__uint_as_float(w[kk].y << 16) * f, __uint_as_float(w[kk].y & 0xffff0000u) * f);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          sk[e] *= __uint_as_float((uint32_t)(127 - __shfl_sync(kFull, up, (2 * c + e) * 4)) << 23);
+      }
+#pragma unroll
+      for (int kk = 0; kk < S::kKS; ++kk) {
+        if constexpr (!FP8) {
+          qa[kk][0] = v0 ? q0[kk * 8 + c] : 0u;
+          qa[kk][1] = v1 ? q1[kk * 8 + c] : 0u;
+          qa[kk][2] = v0 ? q0[kk * 8 + 4 + c] : 0u;
+          qa[kk][3] = v1 ? q1[kk * 8 + 4 + c] : 0u;
+        }
+      }
+    }
+    // keys that every row sees: [.., all_hi), and from all_lo on (the first tokens apart)
+    const int all_hi = low - gap * kBlk + 1;
+    const int all_lo = m.window > 0 ? max(high - gap * kBlk - m.window, -1) + 1 : 0;
+    auto seen_by_all = [&](int key) {
+      return key + kBlk <= all_hi && (key >= all_lo || key + kBlk <= p.first);
+    };
+
+    // S of a block in log2 units: bf16 [key tile][row 2, key 2] of rows g, g + 8 and keys 2c + {0, 1}
+    // (+ 8); e4m3 in [0]: keys g (+ 8 in the upper two), rows 2c + {0, 1}
+    auto scores_of = [&](const uint8_t* kt, int key0, float (&sc)[2][4]) {
+      const uint32_t kbase = smem_u32(kt);
+      const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[0][i] = sc[1][i] = 0.f;
+      if constexpr (FP8) {
+        uint4 kw[2][2];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const int key = g + mt * 8;
+          kw[mt][0] = lds128(kbase + key * 128 + (((2 * c) ^ (key & 7)) << 4));
+          kw[mt][1] = lds128(kbase + key * 128 + (((2 * c + 1) ^ (key & 7)) << 4));
+        }
+#pragma unroll
+        for (int kk = 0; kk < S::kKS; ++kk) {  // (two accumulators: even and odd steps)
+          const uint4& k0 = kw[0][kk >> 2];
+          const uint4& k1 = kw[1][kk >> 2];
+          const int sel = kk & 3;
+          uint32_t a[4];
+          e4m3x4_to_f16(sel == 0 ? k0.x : sel == 1 ? k0.y : sel == 2 ? k0.z : k0.w, a[0], a[2]);
+          e4m3x4_to_f16(sel == 0 ? k1.x : sel == 1 ? k1.y : sel == 2 ? k1.z : k1.w, a[1], a[3]);
+          mma_f16_16816(sc[kk & 1], a, qa[kk][0], qa[kk][2]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[0][i] = (sc[0][i] + sc[1][i]) * sk[i & 1];
+        if (!seen_by_all(key0)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = key0 + g + 8 * (i >> 1), e = i & 1;
+            if (!(key <= pos[e] && (key >= lo[e] || key < p.first))) sc[0][i] = -INFINITY;
+          }
+        }
+      } else {
+        const int mi = lane >> 3, rr = lane & 7;
+        const int row = rr + ((mi >> 1) << 3);
+#pragma unroll
+        for (int kk = 0; kk < S::kKS; ++kk) {
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4(kbase + tile_off<S::kHalves>(row, kk * 2 + (mi & 1)), b0, b1, b2, b3);
+          mma_bf16_16816(sc[0], qa[kk], b0, b1);
+          mma_bf16_16816(sc[1], qa[kk], b2, b3);
+        }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[nt][i] *= sk[0];
+        if (!seen_by_all(key0)) {
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = key0 + 2 * c + 8 * nt + (i & 1), r = i >> 1;
+              if (!(key <= pos[r] && (key >= lo[r] || key < p.first))) sc[nt][i] = -INFINITY;
+            }
+        }
+      }
+    };
+
+    // ---- one pass over the keys
+    float mrow[2] = {-INFINITY, -INFINITY}, lrow[2] = {0.f, 0.f};
+    constexpr int NO = FP8 ? 8 : S::kNT;
+    float o[NO][4];
+#pragma unroll
+    for (int j = 0; j < NO; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    // room for the scores of the CTA's first `kept` blocks, [row][key]
+    // (rows 8 words apart in the banks)
+    const int ld = WEIGH ? S::kScores / 4 / nrow / 32 * 32 - 24 : 0;
+    const int kept = WEIGH ? min(count, ld / kBlk) : 0;
+    bool late = false;
+    for (int x = 0; x < mine; ++x) {
+      const uint32_t cnt = ring_pos + x, slot = cnt % NS;
+      if (!mbar_wait(&full[stall ? NW * NS : warp * NS + slot], stall ? 0u : (cnt / NS) & 1u, limit)) {
+        late = true;
+        break;
+      }
+      uint8_t* kt = ring + (size_t)(warp * NS + slot) * S::kStage;
+      uint8_t* vt = kt + S::kTile;
+      const int b = warp + NW * x, key0 = (run0 + b) * kBlk;
+      const int g = lane >> 2, c = lane & 3;
+      if (!FP8 && key0 + kBlk > vn) {
+        // V rows past the sequence's end hold anything: zeros, so that 0 x NaN does not show
+        const int first = vn - key0;
+        for (int i = lane; i < (kBlk - first) * S::kHalves * 8; i += 32) {
+          const int r = first + i / (S::kHalves * 8), ch = i % (S::kHalves * 8);
+          *reinterpret_cast<uint4*>(vt + tile_off<S::kHalves>(r, ch)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      float sc[2][4];
+      scores_of(kt, key0, sc);
+      if (WEIGH && b < kept) {
+        if constexpr (FP8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (2 * c + (i & 1) < nrow) scores[(2 * c + (i & 1)) * ld + b * kBlk + g + 8 * (i >> 1)] = sc[0][i];
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (g + 8 * r < nrow)
+                *reinterpret_cast<float2*>(scores + (g + 8 * r) * ld + b * kBlk + 8 * nt + 2 * c) =
+                    make_float2(sc[nt][2 * r], sc[nt][2 * r + 1]);
+        }
+      }
+      float alpha[2];
+      bool grew = false;  // a row's running maximum rose: its O needs the rescale (else alpha = 1)
+      if constexpr (FP8) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(sc[0][e], sc[0][2 + e]);
+          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+          const float mn = fmaxf(mrow[e], mx), base = mn == -INFINITY ? 0.f : mn;
+          alpha[e] = exp2f(mrow[e] - base);
+          grew |= mn > mrow[e];
+          mrow[e] = mn;
+          sc[0][e] = exp2f(sc[0][e] - base);
+          sc[0][2 + e] = exp2f(sc[0][2 + e] - base);
+          lrow[e] = lrow[e] * alpha[e] + (sc[0][e] + sc[0][2 + e]);
+        }
+        if (__any_sync(kFull, grew)) {
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            o[t][0] *= alpha[0];
+            o[t][1] *= alpha[1];
+            o[t][2] *= alpha[0];
+            o[t][3] *= alpha[1];
+          }
+        }
+        // (weights are taken 2^15 times as large, the row's largest so far just inside f16: what rounds
+        // to a multiple of f16's smallest step is off by 2^-40 of it)
+        constexpr float kUp = 32768.f;
+        const uint32_t pb0 = movmatrix_trans(pack_f16x2(sc[0][0] * kUp, sc[0][1] * kUp));
+        const uint32_t pb1 = movmatrix_trans(pack_f16x2(sc[0][2] * kUp, sc[0][3] * kUp));
+        const uint32_t vbase = smem_u32(vt);
+        const int lim = vn - key0;  // rows at or past it: zeros
+        uint4 vr[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 2 * c + (i & 1) + (i >> 1) * 8;
+          vr[i] = lds128(vbase + r * 128 + ((g ^ (r & 7)) << 4));
+          if (r >= lim) vr[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        const uint32_t ra[4] = {vr[0].x, vr[0].y, vr[0].z, vr[0].w};
+        const uint32_t rb[4] = {vr[1].x, vr[1].y, vr[1].z, vr[1].w};
+        const uint32_t rc[4] = {vr[2].x, vr[2].y, vr[2].z, vr[2].w};
+        const uint32_t rd[4] = {vr[3].x, vr[3].y, vr[3].z, vr[3].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t lo01 = __byte_perm(ra[i], rb[i], 0x5140), hi01 = __byte_perm(ra[i], rb[i], 0x7362);
+          const uint32_t lo89 = __byte_perm(rc[i], rd[i], 0x5140), hi89 = __byte_perm(rc[i], rd[i], 0x7362);
+          const uint32_t a0[4] = {e4m3x2_to_f16x2((uint16_t)(lo01 & 0xffffu)),
+                                  e4m3x2_to_f16x2((uint16_t)(lo01 >> 16)),
+                                  e4m3x2_to_f16x2((uint16_t)(lo89 & 0xffffu)),
+                                  e4m3x2_to_f16x2((uint16_t)(lo89 >> 16))};
+          const uint32_t a1[4] = {e4m3x2_to_f16x2((uint16_t)(hi01 & 0xffffu)),
+                                  e4m3x2_to_f16x2((uint16_t)(hi01 >> 16)),
+                                  e4m3x2_to_f16x2((uint16_t)(hi89 & 0xffffu)),
+                                  e4m3x2_to_f16x2((uint16_t)(hi89 >> 16))};
+          mma_f16_16816(o[2 * i], a0, pb0, pb1);
+          mma_f16_16816(o[2 * i + 1], a1, pb0, pb1);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float mx = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+          const float mn = fmaxf(mrow[r], mx), base = mn == -INFINITY ? 0.f : mn;
+          alpha[r] = exp2f(mrow[r] - base);
+          grew |= mn > mrow[r];
+          mrow[r] = mn;
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            sc[nt][2 * r] = exp2f(sc[nt][2 * r] - base);
+            sc[nt][2 * r + 1] = exp2f(sc[nt][2 * r + 1] - base);
+          }
+          lrow[r] = lrow[r] * alpha[r] + ((sc[0][2 * r] + sc[0][2 * r + 1]) + (sc[1][2 * r] + sc[1][2 * r + 1]));
+        }
+        uint32_t ph[4], pl[4];  // P as a bf16 pair: the weights keep 2^-17
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = sc[i >> 1][(i & 1) * 2], d = sc[i >> 1][(i & 1) * 2 + 1];
+          ph[i] = pack_bf16x2(a, d);
+          const float2 hv = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ph[i]));
+          pl[i] = pack_bf16x2(a - hv.x, d - hv.y);
+        }
+        if (__any_sync(kFull, grew)) {
+#pragma unroll
+          for (int j = 0; j < NO; ++j) {
+            o[j][0] *= alpha[0];
+            o[j][1] *= alpha[0];
+            o[j][2] *= alpha[1];
+            o[j][3] *= alpha[1];
+          }
+        }
+        const int mi = lane >> 3, rr = lane & 7;
+        const int row = rr + ((mi & 1) << 3);
+        const uint32_t vbase = smem_u32(vt);
+#pragma unroll
+        for (int dd = 0; dd < D / 16; ++dd) {
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4_trans(vbase + tile_off<S::kHalves>(row, dd * 2 + (mi >> 1)), b0, b1, b2, b3);
+          mma_bf16_16816(o[2 * dd], ph, b0, b1);
+          mma_bf16_16816(o[2 * dd + 1], ph, b2, b3);
+          mma_bf16_16816(o[2 * dd], pl, b0, b1);
+          mma_bf16_16816(o[2 * dd + 1], pl, b2, b3);
+        }
+      }
+      __syncwarp();
+      if (issued < mine) {
+        issue(issued, ring_pos + issued, true);
+        ++issued;
+      }
+    }
+    if (late) {
+      if (lane == 0) {
+        record_error(p.status, PA_ETIMEOUT);
+        atomicExch(&sh.fail, 1);
+      }
+      // wait (bounded) for this warp's copies still in flight
+      for (int x = max(0, issued - NS); x < issued; ++x)
+        mbar_wait(&full[warp * NS + (ring_pos + x) % NS], ((ring_pos + x) / NS) & 1u, 100000000ull);
+    }
+    ring_pos += issued;
+
+    // ---- the warps' states
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if constexpr (FP8) {
+        lrow[r] += __shfl_xor_sync(kFull, lrow[r], 4);
+        lrow[r] += __shfl_xor_sync(kFull, lrow[r], 8);
+        lrow[r] += __shfl_xor_sync(kFull, lrow[r], 16);
+      } else {
+        lrow[r] += __shfl_xor_sync(kFull, lrow[r], 1);
+        lrow[r] += __shfl_xor_sync(kFull, lrow[r], 2);
+      }
+    }
+    __syncthreads();  // every warp is done with its ring
+    {
+      float* ob = mrg_o + (size_t)warp * 16 * LD;
+      const int g = lane >> 2, c = lane & 3;
+      if constexpr (FP8) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 2 * c + e;
+          if (g == 0) sh.warp_ml[warp][row] = make_float2(mrow[e], lrow[e]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(ob + row * LD + 16 * g + 4 * i) =
+                make_float4(o[2 * i][e] * (1.f / 32768.f), o[2 * i][2 + e] * (1.f / 32768.f),
+                            o[2 * i + 1][e] * (1.f / 32768.f), o[2 * i + 1][2 + e] * (1.f / 32768.f));
+        }
+      } else {
+        if (c == 0) {
+          sh.warp_ml[warp][g] = make_float2(mrow[0], lrow[0]);
+          sh.warp_ml[warp][g + 8] = make_float2(mrow[1], lrow[1]);
+        }
+#pragma unroll
+        for (int j = 0; j < S::kNT; ++j) {
+          const int col = j * 8 + c * 2;
+          *reinterpret_cast<float2*>(ob + g * LD + col) = make_float2(o[j][0], o[j][1]);
+          *reinterpret_cast<float2*>(ob + (g + 8) * LD + col) = make_float2(o[j][2], o[j][3]);
+        }
+      }
+    }
+    if (!waited) {
+      // the check of the batch is complete; whatever follows on the stream may be prepared
+      pdl_wait();
+      pdl_launch_dependents();
+      if (tid == 0 && status_set(p.status)) atomicExch(&sh.fail, 1);
+      waited = true;
+    }
+    __syncthreads();
+    // (a row with scores of NaN keeps l NaN: a warp without a finite score has m -inf, and its factor 0
+    // makes 0 x NaN)
+    if (tid < nrow) {
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, sh.warp_ml[w][tid].x);
+      const float base = M == -INFINITY ? 0.f : M;
+      float L = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float f = exp2f(sh.warp_ml[w][tid].x - base);
+        L += f * sh.warp_ml[w][tid].y;
+        sh.warp_ml[w][tid].x = f;
+      }
+      sh.ml[tid] = make_float2(M, L);
+    }
+    __syncthreads();
+    for (int i = tid; i < nrow * (D / 4); i += NW * 32) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float f = sh.warp_ml[w][r].x;
+        const float4 v = *reinterpret_cast<const float4*>(mrg_o + ((size_t)w * 16 + r) * LD + d);
+        a.x += f * v.x;
+        a.y += f * v.y;
+        a.z += f * v.z;
+        a.w += f * v.w;
+      }
+      *reinterpret_cast<float4*>(state + r * LD + d) = a;
+    }
+    if (C > 1) cluster_sync(); else __syncthreads();
+
+    // ---- the cluster's
+    bool fail = sh.fail != 0;
+    if (C > 1) {
+      fail = lane < C && peer_u32(peer(&sh.fail, lane)) != 0;
+      fail = __any_sync(kFull, fail);
+    }
+    if (warp == 0 && lane < nrow) {
+      float M = -INFINITY;
+      for (int k = 0; k < C; ++k) M = fmaxf(M, C > 1 ? peer_f2(peer(&sh.ml[lane], k)).x : sh.ml[lane].x);
+      const float base = M == -INFINITY ? 0.f : M;
+      float L = 0.f;
+      for (int k = 0; k < C; ++k) {
+        const float2 t = C > 1 ? peer_f2(peer(&sh.ml[lane], k)) : sh.ml[lane];
+        L += exp2f(t.x - base) * t.y;
+      }
+      const int R = row0 + lane, t = qs + R / G, h = kvh * G + R % G;
+      // tree_finish takes the sink into the sum; the log-sum-exp with it, in log2 units, is the weights'
+      const float sink = m.sinks ? m.sinks[h] * kLog2e : -INFINITY;
+      float M2 = fmaxf(M, sink);
+      if (M2 == -INFINITY) M2 = 0.f;
+      const float total = L * exp2f(M - M2) + exp2f(sink - M2);
+      sh.lse[lane] = L == 0.f ? INFINITY : M2 + log2f(total);
+      sh.norm[lane] = tree_finish(p, kvh, h, t, M, L, rank == 0 && !fail);
+    }
+    __syncthreads();
+    if (!fail) {
+      const int items = nrow * (D / 4);
+      for (int i = items * rank / C + tid; i < items * (rank + 1) / C; i += NW * 32) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (C > 1) {
+          float M = -INFINITY;
+          for (int k = 0; k < C; ++k) M = fmaxf(M, peer_f2(peer(&sh.ml[r], k)).x);
+          const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+          for (int k = 0; k < C; ++k) {
+            const float f = exp2f(peer_f2(peer(&sh.ml[r], k)).x - base);
+            const float4 v = peer_f4(peer(state + r * LD + d, k));
+            a.x += f * v.x;
+            a.y += f * v.y;
+            a.z += f * v.z;
+            a.w += f * v.w;
+          }
+        } else {
+          a = *reinterpret_cast<const float4*>(state + r * LD + d);
+        }
+        const float f = sh.norm[r];
+        const int R = row0 + r;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) +
+                                  ((int64_t)(qs + R / G) * H + kvh * G + R % G) * D + d) =
+            make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+      }
+    }
+    if constexpr (WEIGH) {
+      float* w = p.key_weights + ((int64_t)s * m.num_kv_heads + kvh) * p.weights_len;
+      auto real = [&](int key) { return key >= front * kBlk ? key + gap * kBlk : key; };
+      // (through L2: another CTA of the cluster may have added to the same key for the rows before)
+      auto add = [&](int key, float v) {
+        if (v != 0.f && key < vn) __stcg(w + real(key), __ldcg(w + real(key)) + v);
+      };
+      const int r0 = max(0, counted0 - row0);
+      if (!fail)
+        for (int i = tid; i < kept * kBlk; i += NW * 32) {
+          float v = 0.f;
+          for (int r = r0; r < nrow; ++r) v += exp2f(scores[r * ld + i] - sh.lse[r]);
+          add(run0 * kBlk + i, v);
+        }
+      if ((nblk + C - 1) / C > ld / kBlk) {  // (one answer for the cluster)
+        // the blocks whose scores did not fit: K once more
+        fence_proxy_async_smem();
+        if (C > 1) cluster_sync(); else __syncthreads();  // (the states in the ring have been read)
+        const int x0 = kept > warp ? (kept - warp + NW - 1) / NW : 0;  // this warp's first
+        int sent = x0;
+        for (; sent < min(mine, x0 + NS); ++sent) issue(sent, ring_pos + sent - x0, false);
+        bool stop = fail;
+        for (int x = x0; x < mine && !stop; ++x) {
+          const uint32_t cnt = ring_pos + x - x0, slot = cnt % NS;
+          if (!mbar_wait(&full[warp * NS + slot], (cnt / NS) & 1u, limit)) {
+            if (lane == 0) {
+              record_error(p.status, PA_ETIMEOUT);
+              atomicExch(&sh.fail, 1);
+            }
+            break;
+          }
+          const int key0 = (run0 + warp + NW * x) * kBlk, g = lane >> 2, c = lane & 3;
+          float sc[2][4];
+          scores_of(ring + (size_t)(warp * NS + slot) * S::kStage, key0, sc);
+          __syncwarp();
+          if (sent < mine) {
+            issue(sent, ring_pos + sent - x0, false);
+            ++sent;
+          }
+          if constexpr (FP8) {
+            float v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              v[h] = 0.f;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int r = 2 * c + e;
+                if (r >= r0 && r < nrow) v[h] += exp2f(sc[0][2 * h + e] - sh.lse[r]);
+              }
+              v[h] += __shfl_xor_sync(kFull, v[h], 1);
+              v[h] += __shfl_xor_sync(kFull, v[h], 2);
+            }
+            if (c < 2) add(key0 + g + 8 * c, c ? v[1] : v[0]);
+          } else {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[i] = 0.f;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int r = g + 8 * h;
+                if (r >= r0 && r < nrow) v[i] += exp2f(sc[i >> 1][2 * h + (i & 1)] - sh.lse[r]);
+              }
+              v[i] += __shfl_xor_sync(kFull, v[i], 4);
+              v[i] += __shfl_xor_sync(kFull, v[i], 8);
+              v[i] += __shfl_xor_sync(kFull, v[i], 16);
+            }
+            // lanes 0 .. 3 of row group i have key 2c + (i & 1) + 8 (i >> 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (g == i) add(key0 + 2 * c + (i & 1) + 8 * (i >> 1), v[i]);
+          }
+        }
+        // (copies in flight when it stopped early)
+        for (int x = max(x0, sent - NS); x < sent; ++x)
+          mbar_wait(&full[warp * NS + (ring_pos + x - x0) % NS], ((ring_pos + x - x0) / NS) & 1u, 100000000ull);
+        ring_pos += sent - x0;
+      }
+    }
+    // the states have been read: the ring, or the CTA, may go
+    fence_proxy_async_smem();
+    if (C > 1) cluster_sync(); else __syncthreads();
+  }
+  if (!waited) {  // (a sequence without rows)
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+}
+
+template <int D, bool FP8, bool WEIGH>
+cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, uint64_t limit,
+                      uint32_t stall, cudaStream_t stream) {
+  using S = Shape<D, FP8>;
+  auto kern = k_window_decode<D, FP8, WEIGH>;
+  const int smem = (int)S::smem(WEIGH);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && p.cluster > 8)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.m.num_seqs * p.m.num_kv_heads * p.cluster));
+  cfg.blockDim = dim3(S::NW * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, tk, tv, p, limit, stall);
+}
+template <int D, bool FP8>
+cudaError_t launch_sum(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, uint64_t limit,
+                       uint32_t stall, cudaStream_t stream) {
+  return p.key_weights ? launch_as<D, FP8, true>(tk, tv, p, limit, stall, stream)
+                       : launch_as<D, FP8, false>(tk, tv, p, limit, stall, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_window_decode(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                                 bool fp8, uint64_t limit, uint32_t stall, cudaStream_t stream) {
+  if (fp8) return launch_sum<128, true>(tk, tv, p, limit, stall, stream);
+  if (p.m.head_dim == 128) return launch_sum<128, false>(tk, tv, p, limit, stall, stream);
+  return launch_sum<64, false>(tk, tv, p, limit, stall, stream);
+}
+
+}  // namespace pa

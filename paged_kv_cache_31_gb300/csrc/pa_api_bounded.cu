@@ -3,6 +3,7 @@
 // path selection and launches only.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 #include "pa_internal.cuh"
@@ -33,6 +34,14 @@ size_t workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads, i
                                           2 * tile_rows(group), kTreeTcKeys, kTreeTcGrid, weights)
                                 .bytes);
   return (size_t)bytes;
+}
+
+// CTAs of a cluster for each (sequence, kv head) of a batch of decoding tokens.
+int32_t decode_cluster(int64_t units, int64_t keys, int32_t sms) {
+  if (const char* v = std::getenv("PA_WD_C")) return std::atoi(v);
+  int32_t c = 16;
+  while (c > 1 && (units * c > 4 * sms || c * 64 > keys)) c /= 2;
+  return c;
 }
 
 struct Call {
@@ -125,6 +134,26 @@ pa_status attend(const Call& c) {
                   (fp8 ? c.head_dim == 128 : c.kv_dtype == PA_BF16) && aligned(c.q, 16) &&
                   aligned(c.out, 16) && aligned(c.k_blocks, 16) && aligned(c.v_blocks, 16) &&
                   p.scale > 0.f && c.num_blocks > 0 && tc_enabled();
+  // a batch of decoding tokens, or a few tokens of one sequence
+  const int64_t units = (int64_t)c.num_seqs * c.num_kv_heads;
+  const bool decode = tc && units < (1 << 24) &&
+                      (c.num_tokens <= c.num_seqs || (c.num_seqs == 1 && c.num_tokens * group <= 64));
+  if (decode) {
+    const int64_t keys = c.window > 0 ? std::min<int64_t>((int64_t)c.window + p.first, max_keys) : max_keys;
+    p.cluster = decode_cluster(units, keys, d->sms);
+    CUtensorMap tk, tv;
+    const bool ok =
+        fp8 ? pool_map_fp8(&tk, c.k_blocks, c.num_blocks, 16, c.num_kv_heads, c.head_dim, true) &&
+                  pool_map_fp8(&tv, c.v_blocks, c.num_blocks, 16, c.num_kv_heads, c.head_dim, true)
+            : pool_map_rows(&tk, c.k_blocks, c.num_blocks, c.num_kv_heads, c.head_dim) &&
+                  pool_map_rows(&tv, c.v_blocks, c.num_blocks, c.num_kv_heads, c.head_dim);
+    if (!ok) return PA_ECUDA;
+    uint64_t limit;
+    uint32_t stall;
+    stall_hook(limit, stall);
+    if (launch_window_check(p, c.stream) != cudaSuccess) return PA_ECUDA;
+    return from_cuda(launch_window_decode(tk, tv, p, fp8, limit, stall, c.stream));
+  }
   WindowLayout L;
   if (tc) {
     p.tile_rows = tile_rows(group);

@@ -683,6 +683,11 @@ WindowLayout window_layout(int32_t num_seqs, int64_t num_tokens, int32_t num_hea
                            int32_t head_dim, int64_t max_keys, int32_t rows_per_item, int32_t key_tile,
                            int32_t max_grid, bool weights);
 cudaError_t launch_window_plan(const TreeParams& p, cudaStream_t stream);
+// Batches of decoding tokens: the check in front, and a cluster of p.cluster CTAs for each (sequence, kv
+// head), with the key weights where p.key_weights is given.  tk, tv: the pools' block boxes.
+cudaError_t launch_window_check(const TreeParams& p, cudaStream_t stream);
+cudaError_t launch_window_decode(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                                 bool fp8, uint64_t limit, uint32_t stall, cudaStream_t stream);
 cudaError_t launch_window_generic(const TreeParams& p, pa_dtype kv_dtype, cudaStream_t stream);
 cudaError_t launch_window_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const TreeParams& p, bool fp8, uint64_t wait_limit, uint32_t stall,
