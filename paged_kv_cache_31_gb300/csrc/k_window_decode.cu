@@ -16,14 +16,23 @@
 // makes a lane's bytes contiguous.
 //
 // Weights.  exp(s - lse) needs a row's final log-sum-exp, so a CTA keeps the scores of its keys in shared
-// memory (16 KB: 1024 keys of 4 heads) until the states have been joined, and adds each key's sum to
-// memory then: K is read once, where a second pass over it would read half as many bytes again.  Keys
-// past that room are multiplied once more.  A key belongs to one thread: no atomics.
+// memory (15 KB: 936 keys of 4 heads) or, where they are more, in the workspace (they stay in L2) until
+// the states have been joined, and adds each key's sum to memory then: K is read once, where a second
+// pass over it would read half as many bytes again.  Keys past that room are multiplied once more.  One
+// thread adds to a key, so the order of the sums is fixed.
 //
-// What bounds it: the K / V bytes.
+// Where the scores lie in the workspace, K and V leave L2 first: left to itself L2 wrote the scores out
+// before they came back (64 sequences of 512 to 4096 keys: 22 MB written and 21 read beside 624 MB of K and
+// V, 109.6 us; so 101.2).
+//
+// What bounds it: the K / V bytes for large batches (64 sequences behind a window of 4096: 158 us, the
+// copy rate; 64 of 512 to 4096 keys with their weights 101 us, 0.93 of it), for small ones a chain of
+// latencies (metadata, table, keys, joins: 1 sequence, window 4096: 13.4 us), over e4m3 pools both (48
+// sequences, window 1024: 23.2 us for 15).
 #include <algorithm>
 
 #include "k_tree.cuh"
+#include "k_window.cuh"
 
 namespace pa {
 namespace {
@@ -31,9 +40,11 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBlk = 16;
 
-template <int D, bool FP8>
+// NARROW: half as many warps and four CTAs to an SM
+template <int D, bool FP8, bool NARROW>
 struct Shape {
-  static constexpr int NW = FP8 ? 8 : 4;   // warps
+  static constexpr int NW = (FP8 ? 8 : 4) / (NARROW ? 2 : 1);  // warps
+  static constexpr int kPerSm = NARROW ? 4 : 2;
   static constexpr int NS = 3;             // stages of a warp's ring
   static constexpr int TR = FP8 ? 8 : 16;  // query rows of a tile
   static constexpr int kHalves = FP8 ? 1 : D / 64;
@@ -42,14 +53,14 @@ struct Shape {
   static constexpr int kNT = D / 8, kKS = D / 16;
   static constexpr int kRing = NW * NS * kStage;
   // scores of a CTA's keys, and the states that are joined (in the ring's place)
-  static constexpr int kScores = 15360;
+  static constexpr int kScores = NARROW ? 0 : 15360;
   static constexpr int kLd = D + 4;
   static constexpr int kOffState = NW * 16 * kLd * 4;  // behind the warps' O: the CTA's
   static_assert(kOffState + 16 * kLd * 4 <= kRing, "states lie in the ring");
   static constexpr int kOffSmall = kRing;  // struct Small
   static constexpr int kOffScores = kOffSmall + 1664;
   static constexpr int smem(bool weigh) { return kOffScores + (weigh ? kScores : 0); }
-  static_assert(2 * (1024 + kOffScores + kScores) <= 228 * 1024, "two CTAs per SM");
+  static_assert(kPerSm * (1024 + kOffScores + kScores) <= 228 * 1024, "CTAs of an SM");
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -100,6 +111,29 @@ __device__ __forceinline__ float4 peer_f4(uint32_t addr) {
   return v;
 }
 
+// TMA loads whose lines leave L2 before others.
+__device__ __forceinline__ uint64_t evict_first() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                                        uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void load_5d(void* dst, const CUtensorMap* map, int32_t c3, int32_t c4,
+                                        uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c3), "r"(c4), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 // Byte offset of 16-byte chunk `chunk` (along D) of row `row` of a block written by a 5-D box: 8-row
 // groups of (dim half, 8 rows of 128 bytes), 128-byte swizzle.
 template <int HALVES>
@@ -113,21 +147,21 @@ struct Small {
   uint64_t full[NW * NS + 1];  // the last: nothing arrives on it (the debug_stall test hook)
   float2 warp_ml[NW][16];
   float2 ml[16];  // the CTA's state, read by its cluster
+  int seq;        // the sequence that is this CTA's
   float lse[16], norm[16];
   int fail;
 };
 
-template <int D, bool FP8, bool WEIGH>
-__global__ void __launch_bounds__(Shape<D, FP8>::NW * 32, 2)
+template <int D, bool FP8, bool WEIGH, bool NARROW>
+__global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, NARROW>::kPerSm)
     k_window_decode(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const TreeParams p, uint64_t limit, uint32_t stall) {
-  using S = Shape<D, FP8>;
+  using S = Shape<D, FP8, NARROW>;
   constexpr int NW = S::NW, NS = S::NS, TR = S::TR, LD = S::kLd;
   extern __shared__ __align__(1024) uint8_t ring[];
   using Sm = Small<NW, NS>;
   static_assert(sizeof(Sm) <= S::kOffScores - S::kOffSmall, "kOffScores");
   Sm& sh = *reinterpret_cast<Sm*>(ring + S::kOffSmall);
-  float* scores = reinterpret_cast<float*>(ring + S::kOffScores);
   float* mrg_o = reinterpret_cast<float*>(ring);
   float* state = reinterpret_cast<float*>(ring + S::kOffState);
   uint64_t* full = sh.full;
@@ -145,8 +179,28 @@ __global__ void __launch_bounds__(Shape<D, FP8>::NW * 32, 2)
   fence_mbar_init();
   __syncthreads();
   // (the kernel in front lets this one start once it has waited for all work before it)
-  const int unit = blockIdx.x / C, s = unit / m.num_kv_heads, kvh = unit % m.num_kv_heads;
+  bool waited = false;
+  const int unit = blockIdx.x / C, kvh = unit % m.num_kv_heads;
   const int H = m.num_heads, G = m.group;
+  int s = unit / m.num_kv_heads;
+  if (p.ordered) {
+    // more units than are resident at once: those with the most keys first (the s-th longest sequence)
+    int* keys = reinterpret_cast<int*>(ring);
+    auto seen = [&](int n) { return m.window > 0 ? min(n, (int)min((int64_t)m.window + p.first, (int64_t)INT_MAX)) : n; };
+    for (int i = tid; i < m.num_seqs; i += NW * 32) keys[i] = seen(m.seq_lens[i]);
+    __syncthreads();
+    for (int i = tid; i < m.num_seqs; i += NW * 32) {
+      const int mine = keys[i];
+      int before = 0;
+#pragma unroll 8
+      for (int j = 0; j < m.num_seqs; ++j) before += keys[j] > mine || (keys[j] == mine && j < i);
+      if (before == s) sh.seq = i;
+    }
+    __syncthreads();
+    s = sh.seq;
+    fence_proxy_async_smem();
+    __syncthreads();  // (the ring is free)
+  }
   const int qs = m.query_start_loc[s], qe = m.query_start_loc[s + 1], n = m.seq_lens[s];
   // numbers that cannot be used as indices: no rows (the check records the error)
   const bool usable = qs >= 0 && qe >= qs && (int64_t)qe <= m.num_tokens && n >= 1 &&
@@ -157,8 +211,7 @@ __global__ void __launch_bounds__(Shape<D, FP8>::NW * 32, 2)
   const int32_t* table = m.block_tables + (int64_t)s * m.max_blocks;
   const float sl = p.scale * kLog2e;
   uint32_t ring_pos = 0;
-  bool waited = false;
-
+  const uint64_t policy = evict_first();
   for (int row0 = 0; row0 < rows; row0 += TR) {
     const int nrow = min(TR, rows - row0);
     const int low = min(max(m.positions[qs + row0 / G], 0), n - 1);
@@ -199,7 +252,15 @@ __global__ void __launch_bounds__(Shape<D, FP8>::NW * 32, 2)
         uint8_t* dst = ring + (size_t)(warp * NS + slot) * S::kStage;
         mbar_arrive_expect_tx(bar, with_v ? S::kStage : S::kTile);
         // (an id outside the pool reads zeros from outside it)
-        if constexpr (FP8) {
+        if (WEIGH && p.ordered) {
+          if constexpr (FP8) {
+            load_3d(dst, &tk, 0, kvh, id >= 0 ? id * kBlk : -kBlk, bar, policy);
+            if (with_v) load_3d(dst + S::kTile, &tv, 0, kvh, id >= 0 ? id * kBlk : -kBlk, bar, policy);
+          } else {
+            load_5d(dst, &tk, id >= 0 ? id * 2 : -2, kvh, bar, policy);
+            if (with_v) load_5d(dst + S::kTile, &tv, id >= 0 ? id * 2 : -2, kvh, bar, policy);
+          }
+        } else if constexpr (FP8) {
           tma_load_3d(dst, &tk, 0, kvh, id >= 0 ? id * kBlk : -kBlk, bar);
           if (with_v) tma_load_3d(dst + S::kTile, &tv, 0, kvh, id >= 0 ? id * kBlk : -kBlk, bar);
         } else {
@@ -210,7 +271,6 @@ __global__ void __launch_bounds__(Shape<D, FP8>::NW * 32, 2)
     };
     int issued = 0;
     for (; issued < min(mine, NS); ++issued) issue(issued, ring_pos + issued, true);
-
     // scores to log2 units, of this lane's rows
     float sk[2];
     sk[0] = sk[1] = head_scale(m.k_scales, kvh, sl);
@@ -341,9 +401,15 @@ __global__ void __launch_bounds__(Shape<D, FP8>::NW * 32, 2)
     float o[NO][4];
 #pragma unroll
     for (int j = 0; j < NO; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    // room for the scores of the CTA's first `kept` blocks, [row][key]
-    // (rows 8 words apart in the banks)
-    const int ld = WEIGH ? S::kScores / 4 / nrow / 32 * 32 - 24 : 0;
+    // room for the scores of the CTA's first `kept` blocks, [row][key]: shared memory (rows 8 words apart
+    // in the banks) where all the cluster's fit, else the workspace
+    float* scores = reinterpret_cast<float*>(ring + S::kOffScores);
+    int ld = WEIGH && !NARROW ? S::kScores / 4 / nrow / 32 * 32 - 24 : 0;
+    const int most = (nblk + C - 1) / C;  // blocks of a CTA
+    if (WEIGH && most > ld / kBlk && p.w.room / nrow > ld) {
+      ld = p.w.room / nrow / 32 * 32;
+      scores = p.w.part + (int64_t)blockIdx.x * p.w.room;
+    }
     const int kept = WEIGH ? min(count, ld / kBlk) : 0;
     bool late = false;
     for (int x = 0; x < mine; ++x) {
@@ -550,9 +616,9 @@ __global__ void __launch_bounds__(Shape<D, FP8>::NW * 32, 2)
       // the check of the batch is complete; whatever follows on the stream may be prepared
       pdl_wait();
       pdl_launch_dependents();
-      if (tid == 0 && status_set(p.status)) atomicExch(&sh.fail, 1);
       waited = true;
     }
+    if (tid == 0 && row0 == 0 && status_set(p.status)) atomicExch(&sh.fail, 1);
     __syncthreads();
     // (a row with scores of NaN keeps l NaN: a warp without a finite score has m -inf, and its factor 0
     // makes 0 x NaN)
@@ -643,18 +709,54 @@ __global__ void __launch_bounds__(Shape<D, FP8>::NW * 32, 2)
     if constexpr (WEIGH) {
       float* w = p.key_weights + ((int64_t)s * m.num_kv_heads + kvh) * p.weights_len;
       auto real = [&](int key) { return key >= front * kBlk ? key + gap * kBlk : key; };
-      // (through L2: another CTA of the cluster may have added to the same key for the rows before)
+      // One thread adds to a key, a row tile after the other (another CTA's, perhaps, behind the cluster's
+      // barrier): atomic only so that L2 adds, and nobody waits for the sum that was there.
       auto add = [&](int key, float v) {
-        if (v != 0.f && key < vn) __stcg(w + real(key), __ldcg(w + real(key)) + v);
+        if (v != 0.f && key < vn) atomicAdd(w + real(key), v);
       };
       const int r0 = max(0, counted0 - row0);
+      constexpr int kU = 4;
       if (!fail)
-        for (int i = tid; i < kept * kBlk; i += NW * 32) {
-          float v = 0.f;
-          for (int r = r0; r < nrow; ++r) v += exp2f(scores[r * ld + i] - sh.lse[r]);
-          add(run0 * kBlk + i, v);
+        // four keys of one block to a step, kU steps' loads in flight
+        for (int i0 = tid; i0 < kept * 4; i0 += kU * NW * 32) {
+          float4 v[kU];
+          int at[kU];
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const int i = i0 + u * NW * 32, key = run0 * kBlk + 4 * i;
+            at[u] = i < kept * 4 ? real(key) : INT_MAX;
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          for (int r = r0; r < nrow; r += 4) {
+            float4 x[4][kU];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int u = 0; u < kU; ++u)
+                x[k][u] = at[u] < n && r + k < nrow
+                              ? *reinterpret_cast<const float4*>(scores + (r + k) * ld + 4 * (i0 + u * NW * 32))
+                              : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float l = sh.lse[min(r + k, nrow - 1)];
+#pragma unroll
+              for (int u = 0; u < kU; ++u) {
+                v[u].x += exp2f(x[k][u].x - l);
+                v[u].y += exp2f(x[k][u].y - l);
+                v[u].z += exp2f(x[k][u].z - l);
+                v[u].w += exp2f(x[k][u].w - l);
+              }
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const float y[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (at[u] < n - k && y[k] != 0.f) atomicAdd(w + at[u] + k, y[k]);
+          }
         }
-      if ((nblk + C - 1) / C > ld / kBlk) {  // (one answer for the cluster)
+      if (most > ld / kBlk) {  // (one answer for the cluster)
         // the blocks whose scores did not fit: K once more
         fence_proxy_async_smem();
         if (C > 1) cluster_sync(); else __syncthreads();  // (the states in the ring have been read)
@@ -729,11 +831,11 @@ __global__ void __launch_bounds__(Shape<D, FP8>::NW * 32, 2)
   }
 }
 
-template <int D, bool FP8, bool WEIGH>
+template <int D, bool FP8, bool WEIGH, bool NARROW>
 cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, uint64_t limit,
                       uint32_t stall, cudaStream_t stream) {
-  using S = Shape<D, FP8>;
-  auto kern = k_window_decode<D, FP8, WEIGH>;
+  using S = Shape<D, FP8, NARROW>;
+  auto kern = k_window_decode<D, FP8, WEIGH, NARROW>;
   const int smem = (int)S::smem(WEIGH);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess && p.cluster > 8)
@@ -757,8 +859,11 @@ cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const TreePa
 template <int D, bool FP8>
 cudaError_t launch_sum(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, uint64_t limit,
                        uint32_t stall, cudaStream_t stream) {
-  return p.key_weights ? launch_as<D, FP8, true>(tk, tv, p, limit, stall, stream)
-                       : launch_as<D, FP8, false>(tk, tv, p, limit, stall, stream);
+  if (p.narrow)
+    return p.key_weights ? launch_as<D, FP8, true, true>(tk, tv, p, limit, stall, stream)
+                         : launch_as<D, FP8, false, true>(tk, tv, p, limit, stall, stream);
+  return p.key_weights ? launch_as<D, FP8, true, false>(tk, tv, p, limit, stall, stream)
+                       : launch_as<D, FP8, false, false>(tk, tv, p, limit, stall, stream);
 }
 
 }  // namespace

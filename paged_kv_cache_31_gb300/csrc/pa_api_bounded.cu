@@ -3,7 +3,6 @@
 // path selection and launches only.
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 #include <cstring>
 
 #include "pa_internal.cuh"
@@ -17,6 +16,19 @@ int32_t tile_rows(int32_t group) { return 128 / group * group; }
 
 bool tc_sizes(int32_t group, int32_t head_dim) {
   return group <= 128 && (head_dim == 64 || head_dim == 128);
+}
+
+// Whether a batch is one of decoding tokens, or of a few tokens of one sequence (k_window_decode.cu).
+bool decodes(int32_t num_seqs, int64_t num_tokens, int32_t num_kv_heads, int32_t group) {
+  return (num_tokens <= num_seqs || (num_seqs == 1 && num_tokens * group <= 64)) &&
+         (int64_t)num_seqs * num_kv_heads < (1 << 24);
+}
+
+// Scores of a (sequence, kv head) that the workspace has room for: all keys of a token's heads, up to
+// 256 MB for the batch.
+int64_t score_room(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int64_t keys) {
+  const int64_t all = std::min(group, 16) * ((keys + 511) / 512 * 512);
+  return std::min(all, std::max<int64_t>((1 << 26) / ((int64_t)num_seqs * num_kv_heads), 2048)) / 512 * 512;
 }
 
 size_t workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
@@ -33,15 +45,39 @@ size_t workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads, i
     bytes = std::max(bytes, window_layout(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, keys,
                                           2 * tile_rows(group), kTreeTcKeys, kTreeTcGrid, weights)
                                 .bytes);
+  if (weights && num_seqs > 0 && decodes(num_seqs, num_tokens, num_kv_heads, group))
+    bytes = std::max(bytes, 4 * (int64_t)num_seqs * num_kv_heads *
+                                score_room(num_seqs, num_kv_heads, group, keys));
   return (size_t)bytes;
 }
 
-// CTAs of a cluster for each (sequence, kv head) of a batch of decoding tokens.
-int32_t decode_cluster(int64_t units, int64_t keys, int32_t sms) {
-  if (const char* v = std::getenv("PA_WD_C")) return std::atoi(v);
-  int32_t c = 16;
-  while (c > 1 && (units * c > 4 * sms || c * 64 > keys)) c /= 2;
-  return c;
+// How a batch of decoding tokens goes: CTAs of a cluster for each (sequence, kv head), their shape, and
+// whether the longest sequences come first.  keys: the most that a token can see (of the table's width
+// and the window; the lengths are on the device).
+struct DecodeForm {
+  int32_t cluster;
+  bool narrow, ordered;
+};
+// More CTAs to a unit read its keys sooner, but each costs some 5 us of latencies (metadata, first keys,
+// joins) in which it reads nothing.  Measured (us in a graph, bf16, 8 kv heads of 4 heads, lengths up to
+// the given one; CTAs to a unit): 1 sequence of 4096 1: 50, 4: 19.2, 16: 13.6; 8 sequences of 1024 1: 17.4,
+// 4: 11.4, 8: 18.1; 16 of 256 1: 9.4, 2: 10.5, 4: 16.6; 24 of 4096 1: 58, 2: 54, 4: 63; 16 of 16384
+// 1: 186, 4: 112, 8: 127; 48 of 16384 1: 319, 2: 288, 4: 312; 64 of 4096 1: 105, 2: 126.  Clusters of 16
+// only where they are all resident (2 sequences of 4096 8: 14.9, 16: 20.8).
+// Narrow CTAs (half the warps, four to an SM) where units are short or many: 64 sequences of 256 14.0
+// against 17.7 wide, 128 of 1024 65.8 / 76.2, e4m3 64 of 1024 19.8 / 24.4; but 64 of 4096 129 / 105.
+// Longest first where not all units are resident: 64 of 4096, ragged, 118 -> 98.
+DecodeForm decode_form(int64_t units, int32_t num_seqs, int64_t keys, int64_t key_bytes, int32_t sms) {
+  DecodeForm f{1, false, false};
+  while (f.cluster < 16) {
+    const int64_t ctas = units * 2 * f.cluster, each = keys / (2 * f.cluster);
+    const int64_t least = ctas <= sms ? 64 : ctas <= 2 * sms ? 256 : ctas <= 6 * sms ? 2048 : INT64_MAX;
+    if (each < least || (f.cluster == 8 && ctas > sms)) break;
+    f.cluster *= 2;
+  }
+  f.narrow = units > 2 * sms && (units >= 6 * sms || keys * key_bytes <= 384 * 1024);
+  f.ordered = f.cluster == 1 && units > (f.narrow ? 4 : 2) * sms && num_seqs <= 256;
+  return f;
 }
 
 struct Call {
@@ -136,11 +172,14 @@ pa_status attend(const Call& c) {
                   p.scale > 0.f && c.num_blocks > 0 && tc_enabled();
   // a batch of decoding tokens, or a few tokens of one sequence
   const int64_t units = (int64_t)c.num_seqs * c.num_kv_heads;
-  const bool decode = tc && units < (1 << 24) &&
-                      (c.num_tokens <= c.num_seqs || (c.num_seqs == 1 && c.num_tokens * group <= 64));
-  if (decode) {
+  if (tc && decodes(c.num_seqs, c.num_tokens, c.num_kv_heads, group)) {
     const int64_t keys = c.window > 0 ? std::min<int64_t>((int64_t)c.window + p.first, max_keys) : max_keys;
-    p.cluster = decode_cluster(units, keys, d->sms);
+    const DecodeForm f = decode_form(units, c.num_seqs, keys, 2 * c.head_dim * esize(c.kv_dtype), d->sms);
+    p.cluster = f.cluster;
+    p.narrow = f.narrow;
+    p.ordered = f.ordered;
+    p.w.part = static_cast<float*>(c.workspace);
+    p.w.room = (int32_t)(score_room(c.num_seqs, c.num_kv_heads, group, max_keys) / p.cluster);
     CUtensorMap tk, tv;
     const bool ok =
         fp8 ? pool_map_fp8(&tk, c.k_blocks, c.num_blocks, 16, c.num_kv_heads, c.head_dim, true) &&

@@ -618,6 +618,7 @@ struct TreeParams {
   // Attention behind a window with first tokens (k_window.cu): m.window counts behind positions, no
   // mask; seqs' second record is (items of a kv head, its first item's record, rows, 0).
   int32_t first;     // positions that stay visible
+  int32_t narrow, ordered;  // batches of decoding tokens: the CTAs' shape, longest sequences first
   int4* item_keys;  // [items of all sequences] (front blocks, gap in blocks behind them, key tiles, 0)
   int64_t* item_cum;  // [items + 1] weight before the item, over all items of a kv head in order
   // Attention weights that keys receive (k_key_weights.cu): [num_seqs, num_kv_heads, weights_len] that
@@ -633,8 +634,9 @@ struct TreeParams {
     int4* items;   // (key tile, first row tile, end, 0), of all sequences, once for all kv heads
     int64_t* cum;  // [items + 1] weight before the item
     int4* starts;  // [grid + 1] (sequence, kv head, item, row tile) where each CTA's share begins
-    float* part;   // [2 * grid, kWeightKeys] sums of cut items' pieces
-    int32_t grid;
+    float* part;   // [2 * grid, kWeightKeys] sums of cut items' pieces; batches of decoding tokens: scores,
+                   // `room` of them to a CTA
+    int32_t grid, room;
   } w;
 };
 // The work of an item, in about hundredths of a microsecond (only the balance between the CTAs
