@@ -324,6 +324,7 @@ pa_status pa_evict_keys(void* k_blocks, void* v_blocks, const int32_t* block_tab
     return PA_EINVAL;
   const int64_t max_keys = (int64_t)max_blocks_per_seq * block_size;
   const int64_t most = key_weights ? std::min(max_keys, weights_len) : max_keys;
+  if (num_blocks * block_size > INT32_MAX) return PA_EUNSUPPORTED;  // slots are int32
   if (num_seqs > 65535 || num_kv_heads > 65535 || max_keys > INT32_MAX - 1024 || most > kEvictMostKeys ||
       (int64_t)head_dim * esize(kv_dtype) > (1 << 20))
     return PA_EUNSUPPORTED;
@@ -347,6 +348,7 @@ pa_status pa_evict_keys(void* k_blocks, void* v_blocks, const int32_t* block_tab
   p.keep_recent = keep_recent;
   p.num_kv_heads = num_kv_heads;
   p.block_size = block_size;
+  p.block_shift = (block_size & (block_size - 1)) == 0 ? __builtin_ctz(block_size) : -1;
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.row_bytes = (int64_t)head_dim * esize(kv_dtype);

@@ -708,6 +708,7 @@ struct EvictParams {
   float* key_weights;  // [num_seqs, num_kv_heads, weights_len], or null
   int64_t weights_len;
   int32_t num_seqs, keep_first, keep_recent, num_kv_heads, block_size, max_blocks;
+  int32_t block_shift;  // of a block size that is a power of two, else -1
   int64_t num_blocks;
   int64_t row_bytes;  // of one position and kv head
   int32_t* moves;     // workspace: lists of up to moves_len fillers for each (sequence, kv head)
