@@ -6,16 +6,20 @@
 // order, and the last r rows move up behind them.  So a cache that is cut by a few keys moves its
 // recent rows and a few others, not everything behind the first evicted key.
 //
-// k_evict_select (one CTA per (sequence, kv head)): the m-th largest weight by histograms over 11, 11 and
-// 10 bits of its order-preserving integer form (the first covers exponent and two bits of the fraction, so
-// its bins seldom collide; bisection by two bits a step took 2.6 times as many instructions, which bound
-// it); then two bitmaps, of the larger keys and of the equal ones, whose prefix sums number the places and
-// the keys that fill them.
+// k_evict_check looks at all metadata.  Beside it k_evict, a CTA (or a small cluster) for each (sequence,
+// kv head), already selects; it waits for the check before it writes, and bounds its own indices.
 //
-// k_evict_move: pure data movement, bound by memory.  A sequence's moves in list order (the fillers,
-// then the recent rows, ascending) never write a row that a later one reads, so a CTA that moves its
-// part of every row - a slice of K's or of V's bytes, or the weights - needs only to read a batch of
-// rows before it writes the batch.  Slices are independent: no order between CTAs.
+// Selection.  The m-th largest weight by histograms over 11, 11 and 10 bits of its order-preserving integer
+// form (the first covers exponent and two bits of the fraction, so its bins seldom collide), or, as soon
+// as a bin holds no more keys than there are threads, by comparing each of these with all; then two
+// bitmaps, of the larger keys and of the equal ones, whose prefix sums number the places and the keys that
+// fill them.  (Bisection, two bits a step, took 2.6 times as many instructions and bound the selection.)
+//
+// Moves.  Pure data movement, bound by memory.  A sequence's moves in list order (the fillers, then the
+// recent rows, ascending) never write a row that a later one reads, so a CTA that moves its part of every
+// row needs only to have read a batch of rows before it writes the batch; it reads one batch ahead.  The
+// CTAs of a cluster take parts of the rows (of K's and V's together), each for itself: there is no order
+// between them but that the weights are moved when all have read them.
 #include <algorithm>
 
 #include "pa_internal.cuh"
@@ -24,9 +28,10 @@ namespace pa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kBins = 2048;
+constexpr int kBins = 2048;   // of the histogram
+constexpr int kMoves = 1024;  // whose places are looked up at a time
 
-// Larger weights have larger keys; both zeros the same, NaN the largest.
+// Larger weights have larger keys (none is 0); both zeros the same, NaN the largest.
 __device__ __forceinline__ uint32_t order_key(float w) {
   if (!(w == w)) return 0xffffffffu;
   const uint32_t b = __float_as_uint(w == 0.f ? 0.f : w);
@@ -45,216 +50,250 @@ __device__ __forceinline__ Plan evict_plan(const EvictParams& p, int s) {
   e.middle = e.to - e.first - e.recent;
   return e;
 }
-// Whether the sequence's numbers can be used as indices.
+// Whether the sequence's numbers cannot be used as indices.
 __device__ __forceinline__ bool evict_bad(const EvictParams& p, const Plan& e) {
   return e.n < 0 || e.to < 0 || ((int64_t)e.n + p.block_size - 1) / p.block_size > p.max_blocks ||
          (p.key_weights && e.n > p.weights_len);
 }
-__device__ __forceinline__ int64_t moves_at(const EvictParams& p, int64_t unit) {
-  return unit * (2 * p.moves_len + 2);
-}
 
-// Lists of a unit (sequence, kv head) in the workspace: the number of fillers, then from which index
-// each comes, then (from moves_len on) where it goes.
-// E > 0: a thread keeps the (ordered forms of the) weights of up to E keys in registers; 0: they are read
-// again in every pass.
-template <int NT, int E>
-__global__ void __launch_bounds__(NT) k_evict_select(const EvictParams p) {
-  extern __shared__ uint32_t s_bits[];  // larger keys, then equal ones, 32 to a word
-  __shared__ int s_hist[kBins];
-  __shared__ int3 s_found;  // bin, keys in larger ones, keys in it
-  __shared__ int s_warp[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// A warp per 256 table entries of a sequence.
+__global__ void __launch_bounds__(256) k_evict_check(const EvictParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int s = blockIdx.y, g = blockIdx.x;
-  const int64_t unit = (int64_t)s * p.num_kv_heads + g;
-  int32_t* list = p.moves + moves_at(p, unit);
-  const Plan e = evict_plan(p, s);
-  bool bad = evict_bad(p, e);
-  const float* w = p.key_weights ? p.key_weights + unit * p.weights_len + e.first : nullptr;
-  const int count = e.n - e.recent - e.first;  // keys between the first and the recent ones
-  uint32_t own[E > 0 ? E : 1];
-  if constexpr (E > 0) {
-    const bool any = !bad && e.to < e.n && w;
-#pragma unroll
-    for (int k = 0; k < E; ++k) {
-      const int i = tid + k * NT;
-      own[k] = any && i < count ? order_key(__ldg(w + i)) : 0u;
+  const int lane = threadIdx.x & 31, warps = gridDim.x * 8;
+  const int per = (p.max_blocks + 255) / 256 + 1;  // (one at least)
+  const int64_t chunks = (int64_t)p.num_seqs * per;
+  bool bad = false;
+  for (int64_t c = blockIdx.x * 8 + (threadIdx.x >> 5); c < chunks; c += warps) {
+    const int s = (int)(c / per), e0 = (int)(c % per) * 256;
+    const Plan e = evict_plan(p, s);
+    if (evict_bad(p, e)) {
+      bad = true;
+      continue;
     }
-  }
-  if (g == 0 && !bad && e.to < e.n) {  // the blocks that the sequence's rows lie in
+    if (e.to >= e.n) continue;
     const int need = (e.n + p.block_size - 1) / p.block_size;
-    for (int i = tid; i < need; i += NT) {
-      const int id = p.block_tables[(int64_t)s * p.max_blocks + i];
-      bad |= id < 0 || (int64_t)id >= p.num_blocks;
-    }
+    const int32_t* row = p.block_tables + (int64_t)s * p.max_blocks;
+    int id[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) id[u] = e0 + lane + 32 * u < need ? row[e0 + lane + 32 * u] : 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) bad |= id[u] < 0 || (int64_t)id[u] >= p.num_blocks;
   }
-  bad = __syncthreads_or(bad);
-  if (bad && tid == 0) record_error(p.status, PA_EINVAL);
-  if (bad || e.to >= e.n || e.middle == 0) {
-    if (tid == 0) list[0] = 0;
+  if (__any_sync(kFull, bad) && lane == 0) record_error(p.status, PA_EINVAL);
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// E > 0: sequences of at most NT * E keys; a thread keeps the ordered forms of E weights in registers, and
+// the list of fillers (from, to) lies in shared memory.  E = 0: weights are read again in every pass, and
+// the list lies in the workspace, written by the cluster's first CTA.
+template <typename T, int NT, int E>
+__global__ void __launch_bounds__(NT, 1024 / NT)
+    k_evict(const EvictParams p, int cluster, int row_words, int part_words) {
+  extern __shared__ __align__(16) uint8_t s_mem[];
+  __shared__ __align__(16) int s_work[kBins];  // histogram; then the moves' places, kMoves int2
+  static_assert(kMoves * 8 <= kBins * 4, "places");
+  __shared__ int s_warp[32];
+  __shared__ int3 s_found;  // bin, keys in larger ones, keys in it
+  __shared__ int s_left;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x % cluster, g = blockIdx.x / cluster, s = blockIdx.y;
+  const int64_t unit = (int64_t)s * p.num_kv_heads + g;
+  const Plan e = evict_plan(p, s);
+  if (evict_bad(p, e) || e.to >= e.n) {
+    pdl_wait();
+    pdl_launch_dependents();
     return;
   }
-  const int words = (count + 31) / 32;
-  auto key = [&](int i) { return w ? order_key(__ldg(w + i)) : 0u; };
-  // the middle-th largest key, 11, 11 and 10 bits at a time: the bin that holds it among the keys that
-  // agree with the bits found so far
-  uint32_t at = 0;
-  int need = e.middle;
+  // the list: from, then to, each up to half of the keys
+  uint16_t* near_list = reinterpret_cast<uint16_t*>(s_mem);
+  constexpr int kNear = NT * E / 2;
+  int32_t* far_list = p.moves + unit * p.moves_len;
+  const int far_to = (int)(p.moves_len / 2);
+  uint32_t* more = reinterpret_cast<uint32_t*>(s_mem + 4 * kNear);  // bitmaps: larger keys, then equal ones
+  int fillers = 0;
+
+  // ---- selection
+  if (e.middle > 0) {
+    const float* w = p.key_weights ? p.key_weights + unit * p.weights_len + e.first : nullptr;
+    const int count = e.n - e.recent - e.first;  // keys between the first and the recent ones
+    const int words = (count + 31) / 32;
+    uint32_t* same = more + words;
+    uint32_t own[E > 0 ? E : 1];
+    auto key = [&](int i) { return w ? order_key(w[i]) : 0u; };
+    if constexpr (E > 0) {
+#pragma unroll
+      for (int k = 0; k < E; ++k) own[k] = tid + k * NT < count ? key(tid + k * NT) : 0u;
+    }
+    auto each_key = [&](auto f) {  // (0: a key that is not there)
+      if constexpr (E > 0) {
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          if (own[k] != 0) f(own[k]);
+      } else {
+#pragma unroll 4
+        for (int i = tid; i < count; i += NT) f(key(i));
+      }
+    };
+    // the middle-th largest key: the bin that holds it among the keys that agree with the bits found so far
+    uint32_t at = 0;
+    int need = e.middle;
 #pragma unroll 1
-  for (int pass = 0; w && pass < 3; ++pass) {
-    const int bits = pass < 2 ? 11 : 10, shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    for (int i = tid; i < kBins; i += NT) s_hist[i] = 0;
-    __syncthreads();
-    auto count_key = [&](uint32_t k) {  // (0: a key that is not there)
-      if (k != 0 && (pass == 0 || k >> (shift + bits) == at >> (shift + bits)))
-        atomicAdd(&s_hist[(k >> shift) & ((1 << bits) - 1)], 1);
+    for (int pass = 0; w && pass < 3; ++pass) {
+      const int bits = pass < 2 ? 11 : 10, shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      for (int i = tid; i < kBins; i += NT) s_work[i] = 0;
+      if (tid == 0) s_left = 0;
+      __syncthreads();
+      each_key([&](uint32_t k) {
+        if (pass == 0 || k >> (shift + bits) == at >> (shift + bits))
+          atomicAdd(&s_work[(k >> shift) & ((1 << bits) - 1)], 1);
+      });
+      __syncthreads();
+      constexpr int kPer = kBins / NT;  // bins of a thread, from the highest down
+      int sum = 0, total;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) sum += s_work[kBins - 1 - (tid * kPer + k)];
+      int before = block_exclusive_scan(sum, s_warp, &total);
+      if (before < need && need <= before + sum) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int bin = kBins - 1 - (tid * kPer + k), n = s_work[bin];
+          if (before < need && need <= before + n) s_found = make_int3(bin, before, n);
+          before += n;
+        }
+      }
+      __syncthreads();
+      at |= (uint32_t)s_found.x << shift;
+      need -= s_found.y;
+      const int in = s_found.z;
+      if (need == in) break;  // all of the bin's keys are taken
+      if (in <= NT) {
+        // few are left: each is compared with all others
+        each_key([&](uint32_t k) {
+          if (k >> shift == at >> shift) s_work[atomicAdd(&s_left, 1)] = (int)k;
+        });
+        __syncthreads();
+        if (tid < in) {
+          const uint32_t mine = (uint32_t)s_work[tid];
+          int larger = 0, equal = 0;
+#pragma unroll 4
+          for (int i = 0; i < in; ++i) {
+            larger += (uint32_t)s_work[i] > mine;
+            equal += (uint32_t)s_work[i] == mine;
+          }
+          if (larger < need && need <= larger + equal) s_found.x = (int)mine;
+        }
+        __syncthreads();
+        at = (uint32_t)s_found.x;
+        break;
+      }
+      __syncthreads();
+    }
+    auto mark = [&](int i0, uint32_t k) {
+      const bool in = i0 + lane < count;
+      const uint32_t a = __ballot_sync(kFull, in && k > at);
+      const uint32_t b = __ballot_sync(kFull, in && k == at);
+      if (lane == 0) {
+        more[i0 >> 5] = a;
+        same[i0 >> 5] = b;
+      }
     };
     if constexpr (E > 0) {
 #pragma unroll
-      for (int k = 0; k < E; ++k) count_key(own[k]);
+      for (int k = 0; k < E; ++k)
+        if (warp * 32 + k * NT < count) mark(warp * 32 + k * NT, own[k]);
     } else {
-#pragma unroll 4
-      for (int i = tid; i < count; i += NT) count_key(key(i));
+      for (int i0 = warp * 32; i0 < count; i0 += NT) mark(i0, i0 + lane < count ? key(i0 + lane) : 0u);
     }
     __syncthreads();
-    constexpr int kPer = kBins / NT;  // bins of a thread, from the highest down
-    int sum = 0, total;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) sum += s_hist[kBins - 1 - (tid * kPer + k)];
-    int before = block_exclusive_scan(sum, s_warp, &total);
-    if (before < need && need <= before + sum) {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int bin = kBins - 1 - (tid * kPer + k), n = s_hist[bin];
-        if (before < need && need <= before + n) s_found = make_int3(bin, before, n);
-        before += n;
+    // a thread's words are consecutive, so prefix sums over threads number the keys in order
+    const int per = (words + NT - 1) / NT, w0 = min(words, tid * per), w1 = min(words, w0 + per);
+    int larger = 0, equal = 0;
+    for (int i = w0; i < w1; ++i) {
+      larger += __popc(more[i]);
+      equal += __popc(same[i]);
+    }
+    int all_larger, total;
+    block_exclusive_scan(larger, s_warp, &all_larger);
+    int ties = e.middle - all_larger - block_exclusive_scan(equal, s_warp, &total);  // left for this thread
+    int holes = 0, mine = 0;
+    for (int i = w0; i < w1; ++i) {
+      uint32_t b = same[i], kept = more[i];
+      if (ties >= __popc(b)) {
+        kept |= b;
+      } else {
+        for (int k = 0; k < ties; ++k) {
+          kept |= b & (0u - b);
+          b &= b - 1;
+        }
       }
+      ties = max(0, ties - __popc(same[i]));
+      const int in = e.middle - 32 * i;  // bits below it are places that stay
+      const uint32_t front = in >= 32 ? kFull : in <= 0 ? 0u : (1u << in) - 1u;
+      more[i] = kept & ~front;  // fillers
+      same[i] = ~kept & front;  // holes
+      mine += __popc(more[i]);
+      holes += __popc(same[i]);
     }
-    __syncthreads();
-    at |= (uint32_t)s_found.x << shift;
-    need -= s_found.y;
-    if (need == s_found.z) break;  // all of the bin's keys are taken
-    __syncthreads();
-  }
-  uint32_t* more = s_bits;
-  uint32_t* same = s_bits + words;
-  auto mark = [&](int i0, uint32_t k) {
-    const bool in = i0 + lane < count;
-    const uint32_t a = __ballot_sync(kFull, in && k > at);
-    const uint32_t b = __ballot_sync(kFull, in && k == at);
-    if (lane == 0) {
-      more[i0 >> 5] = a;
-      same[i0 >> 5] = b;
-    }
-  };
-  if constexpr (E > 0) {
-#pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (warp * 32 + k * NT < count) mark(warp * 32 + k * NT, own[k]);
-  } else {
-    for (int i0 = warp * 32; i0 < count; i0 += NT) mark(i0, i0 + lane < count ? key(i0 + lane) : 0u);
-  }
-  __syncthreads();
-  // a thread's words are consecutive, so prefix sums over threads number the keys in order
-  const int per = (words + NT - 1) / NT, w0 = min(words, tid * per), w1 = min(words, w0 + per);
-  int larger = 0, equal = 0;
-  for (int i = w0; i < w1; ++i) {
-    larger += __popc(more[i]);
-    equal += __popc(same[i]);
-  }
-  int total_larger, total;
-  block_exclusive_scan(larger, s_warp, &total_larger);
-  int ties = e.middle - total_larger - block_exclusive_scan(equal, s_warp, &total);  // left for this thread
-  int holes = 0, fillers = 0;
-  const int stay = e.middle;  // kept keys in front of this index of the middle stay where they are
-  for (int i = w0; i < w1; ++i) {
-    uint32_t b = same[i], kept = more[i];
-    if (ties >= __popc(b)) {
-      kept |= b;
-    } else {
-      for (int k = 0; k < ties; ++k) {
-        kept |= b & (0u - b);
-        b &= b - 1;
+    int f0 = block_exclusive_scan(mine, s_warp, &fillers);
+    int h0 = block_exclusive_scan(holes, s_warp, &total);
+    if (E > 0 || rank == 0)
+      for (int i = w0; i < w1; ++i) {
+        const int at0 = e.first + 32 * i - 1;
+        for (uint32_t b = more[i]; b; b &= b - 1, ++f0)
+          if constexpr (E > 0) near_list[f0] = (uint16_t)(at0 + __ffs(b)); else far_list[f0] = at0 + __ffs(b);
+        for (uint32_t b = same[i]; b; b &= b - 1, ++h0)
+          if constexpr (E > 0) near_list[kNear + h0] = (uint16_t)(at0 + __ffs(b)); else far_list[far_to + h0] = at0 + __ffs(b);
       }
-    }
-    ties = max(0, ties - __popc(same[i]));
-    const int in = stay - 32 * i;  // bits below it stay
-    const uint32_t front = in >= 32 ? kFull : in <= 0 ? 0u : (1u << in) - 1u;
-    more[i] = kept & ~front;  // fillers
-    same[i] = ~kept & front;  // holes
-    fillers += __popc(more[i]);
-    holes += __popc(same[i]);
+    __syncthreads();
   }
-  const int f0 = block_exclusive_scan(fillers, s_warp, &total);
-  int h0 = block_exclusive_scan(holes, s_warp, &total);
-  if (tid == 0) list[0] = total;
-  int32_t* from = list + 2 + f0;
-  int32_t* to = list + 2 + p.moves_len + h0;
-  for (int i = w0; i < w1; ++i) {
-    for (uint32_t b = more[i]; b; b &= b - 1) *from++ = e.first + 32 * i + __ffs(b) - 1;
-    for (uint32_t b = same[i]; b; b &= b - 1) *to++ = e.first + 32 * i + __ffs(b) - 1;
+  if (cluster > 1) {  // every CTA has read the weights, the list is there
+    cluster_arrive();
+    cluster_wait();
   }
-}
 
-// Move the weights of a unit, and zero those of the keys behind its new end.
-__device__ __forceinline__ void move_weights(const EvictParams& p, const Plan& e, int64_t unit,
-                                             const int32_t* list, int fillers) {
-  float* w = p.key_weights + unit * p.weights_len;
-  const int moves = fillers + e.recent;
-  for (int b = 0; b < moves; b += 4 * blockDim.x) {
-    float v[4];
-    int to[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = b + u * blockDim.x + threadIdx.x;
-      to[u] = -1;
-      if (i < moves) {
-        const int k = i - fillers;
-        v[u] = w[k < 0 ? list[2 + i] : e.n - e.recent + k];
-        to[u] = k < 0 ? list[2 + p.moves_len + i] : e.to - e.recent + k;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (to[u] >= 0) w[to[u]] = v[u];
-    __syncthreads();
-  }
-  for (int i = e.to + threadIdx.x; i < e.n; i += blockDim.x) w[i] = 0.f;
-}
-
-// blockIdx.x: a slice of `width` accesses of K's rows, then of V's, then (given weights) the weights.
-// Rows are read one batch ahead of the batch that is written, and the places of the batch after that are
-// looked up meanwhile, so reads are in flight all the time.
-template <typename T>
-__global__ void __launch_bounds__(256) k_evict_move(const EvictParams p, int slices, int width,
-                                                    int row_words) {
-  constexpr int U = 2;  // rows of a thread's batch
-  const int s = blockIdx.z, g = blockIdx.y;
+  // ---- moves, once the whole batch has been checked
   pdl_wait();
   pdl_launch_dependents();
   if (__syncthreads_or(status_set(p.status))) return;
-  const Plan e = evict_plan(p, s);
-  // (the status word may have been cleared by another stream in between)
-  if (evict_bad(p, e) || e.to >= e.n) return;
-  const int64_t unit = (int64_t)s * p.num_kv_heads + g;
-  const int32_t* list = p.moves + moves_at(p, unit);
-  const int fillers = __ldcg(list);
-  if (blockIdx.x == 2 * slices) {
-    move_weights(p, e, unit, list, fillers);
-    return;
-  }
-  T* pool = static_cast<T*>(blockIdx.x < slices ? p.k_blocks : p.v_blocks);
-  const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
-  const int moves = fillers + e.recent;
-  const int x = (blockIdx.x % slices) * width + threadIdx.x % width, lane = threadIdx.x / width;
-  const int step = blockDim.x / width;
-  const bool in = x < row_words && lane < step;
-  struct Places {
-    int from[U], to[U];  // slots, or -1
+  auto from = [&](int i) {  // of move i
+    const int k = i - fillers;
+    if (k >= 0) return e.n - e.recent + k;
+    if constexpr (E > 0) return (int)near_list[i]; else return __ldcg(far_list + i);
   };
+  auto to = [&](int i) {
+    const int k = i - fillers;
+    if (k >= 0) return e.to - e.recent + k;
+    if constexpr (E > 0) return (int)near_list[kNear + i]; else return __ldcg(far_list + far_to + i);
+  };
+  const int moves = fillers + e.recent;
+  if (p.key_weights && rank == cluster - 1) {
+    float* w = p.key_weights + unit * p.weights_len;
+    for (int b = 0; b < moves; b += 4 * NT) {
+      float v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = b + u * NT + tid;
+        if (i < moves) v[u] = w[from(i)];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = b + u * NT + tid;
+        if (i < moves) w[to(i)] = v[u];
+      }
+      __syncthreads();
+    }
+    for (int i = e.to + tid; i < e.n; i += NT) w[i] = 0.f;
+  }
+  const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
   auto slot = [&](int i) -> int {  // of index i, or -1
     int b, o;
     if (p.block_shift >= 0) {
@@ -268,94 +307,107 @@ __global__ void __launch_bounds__(256) k_evict_move(const EvictParams p, int sli
     if (id < 0 || (int64_t)id >= p.num_blocks) return -1;
     return id * p.block_size + o;
   };
-  T* mine = pool + (int64_t)g * row_words + x;
+  constexpr int U = 4;  // rows of a thread's batch
+  int2* places = reinterpret_cast<int2*>(s_work);  // slots (from, to); to -1: nothing is moved
   const int64_t stride = (int64_t)p.num_kv_heads * row_words;
-  auto places = [&](int b, Places& at) {
-    int i0[U], i1[U];
+  // this CTA's words of a row of K and of V laid end to end, up to NT at a time
+  const int x_end = min(2 * row_words, (rank + 1) * part_words);
+  for (int x0 = rank * part_words; x0 < x_end; x0 += NT) {
+    const int width = min(NT, x_end - x0), step = NT / width, batch = U * step;
+    const int x = x0 + tid % width, row = tid / width;
+    T* mine = x < row_words ? static_cast<T*>(p.k_blocks) + (int64_t)g * row_words + x
+                            : static_cast<T*>(p.v_blocks) + (int64_t)g * row_words + (x - row_words);
+    auto read = [&](int b, int here, T (&v)[U], int (&dst)[U]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = b + u * step + lane, k = i - fillers;
-      i0[u] = i1[u] = -1;
-      if (in && i < moves) {
-        // (the lists are read before their length is known)
-        const int a = i < p.moves_len ? __ldcg(list + 2 + i) : 0;
-        const int b = i < p.moves_len ? __ldcg(list + 2 + p.moves_len + i) : 0;
-        i0[u] = k < 0 ? a : e.n - e.recent + k;
-        i1[u] = k < 0 ? b : e.to - e.recent + k;
+      for (int u = 0; u < U; ++u) {
+        const int i = b + u * step + row;
+        const int2 a = row < step && i < here ? places[i] : make_int2(-1, -1);
+        dst[u] = a.y;
+        if (a.y >= 0) v[u] = mine[a.x * stride];
+      }
+    };
+    auto write = [&](const T (&v)[U], const int (&dst)[U]) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (dst[u] >= 0) mine[dst[u] * stride] = v[u];
+    };
+    for (int base = 0; base < moves; base += kMoves) {
+      const int here = min(kMoves, moves - base);
+      __syncthreads();  // the places before (or the histogram) have been used
+      for (int i = tid; i < here; i += NT) {
+        int2 a;
+        a.x = slot(from(base + i));
+        a.y = a.x >= 0 ? slot(to(base + i)) : -1;
+        places[i] = a;
+      }
+      __syncthreads();
+      T va[U], vb[U];
+      int ta[U], tb[U];
+      read(0, here, va, ta);
+      for (int i = 0; i < here; i += 2 * batch) {
+        read(i + batch, here, vb, tb);
+        __syncthreads();  // batch i has been read by all
+        write(va, ta);
+        read(i + 2 * batch, here, va, ta);
+        __syncthreads();
+        write(vb, tb);
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      at.from[u] = i0[u] >= 0 ? slot(i0[u]) : -1;
-      at.to[u] = i1[u] >= 0 && at.from[u] >= 0 ? slot(i1[u]) : -1;
-    }
-  };
-  auto read = [&](const Places& at, T (&v)[U]) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (at.to[u] >= 0) v[u] = mine[at.from[u] * stride];
-  };
-  auto write = [&](const Places& at, const T (&v)[U]) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (at.to[u] >= 0) mine[at.to[u] * stride] = v[u];
-  };
-  const int batch = U * step;
-  Places a, b;
-  T va[U], vb[U];
-  places(0, a);
-  read(a, va);
-  places(batch, b);
-  for (int i = 0; i < moves; i += 2 * batch) {
-    read(b, vb);
-    Places c;
-    places(i + 2 * batch, c);
-    __syncthreads();  // batch i has been read by all
-    write(a, va);
-    a = c;
-    read(a, va);
-    places(i + 3 * batch, c);
-    __syncthreads();
-    write(b, vb);
-    b = c;
   }
 }
 
-template <typename T>
-cudaError_t move_as(const EvictParams& p, cudaStream_t stream) {
+template <typename T, int NT, int E>
+cudaError_t evict_as(const EvictParams& p, int cluster, cudaStream_t stream) {
   const int row_words = (int)(p.row_bytes / sizeof(T));
-  // whole rows to a CTA, up to 256 accesses
-  const int width = std::min(row_words, 256), slices = (row_words + width - 1) / width;
-  const dim3 grid(2 * slices + (p.key_weights ? 1 : 0), p.num_kv_heads, p.num_seqs);
-  return launch_pdl(k_evict_move<T>, grid, dim3(256), 0, stream, p, slices, width, row_words);
+  const int part = (2 * row_words + cluster - 1) / cluster;
+  const int smem = (int)(2 * NT * E + (p.moves_len + 31) / 32 * 8);
+  auto kern = k_evict<T, NT, E>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster * p.num_kv_heads, p.num_seqs);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, p, cluster, row_words, part);
 }
 
-template <int NT, int E>
-cudaError_t select_as(const EvictParams& p, cudaStream_t stream) {
-  const size_t smem = (size_t)((p.moves_len + 31) / 32) * 8;
-  auto kern = k_evict_select<NT, E>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(p.num_kv_heads, p.num_seqs), dim3(NT), smem, stream, p);
+template <typename T>
+cudaError_t evict_keys(const EvictParams& p, int cluster, cudaStream_t stream) {
+  const int64_t keys = p.moves_len;  // at most
+  if (keys <= 2048) return evict_as<T, 256, 8>(p, cluster, stream);
+  if (keys <= 8192) return evict_as<T, 512, 16>(p, cluster, stream);
+  return evict_as<T, 1024, 0>(p, cluster, stream);
 }
 
 }  // namespace
 
 int64_t evict_workspace(int32_t num_seqs, int32_t num_kv_heads, int64_t max_keys) {
-  return (int64_t)num_seqs * num_kv_heads * (2 * max_keys + 2) * 4;
+  return (int64_t)num_seqs * num_kv_heads * max_keys * 4;
 }
 
 cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream) {
-  const int64_t keys = p.moves_len;  // at most
-  const cudaError_t e = keys <= 2048   ? select_as<256, 8>(p, stream)
-                        : keys <= 8192 ? select_as<1024, 8>(p, stream)
-                                       : select_as<1024, 0>(p, stream);
+  const int64_t chunks = (int64_t)p.num_seqs * ((p.max_blocks + 255) / 256 + 1);
+  const int blocks = (int)std::min<int64_t>((chunks + 7) / 8, 64);
+  const cudaError_t e = launch_pdl(k_evict_check, dim3(blocks), dim3(256), 0, stream, p);
   if (e != cudaSuccess) return e;
+  // few units: each to as many CTAs as are resident at once, which all select
+  const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads;
+  int cluster = 8;
+  while (cluster > 1 && units * cluster > 2 * num_sms) cluster /= 2;
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.k_blocks) | reinterpret_cast<uintptr_t>(p.v_blocks) |
                        (uintptr_t)p.row_bytes;
-  if (at % 16 == 0) return move_as<uint4>(p, stream);
-  if (at % 4 == 0) return move_as<uint32_t>(p, stream);
-  return move_as<uint8_t>(p, stream);
+  if (at % 16 == 0) return evict_keys<uint4>(p, cluster, stream);
+  if (at % 4 == 0) return evict_keys<uint32_t>(p, cluster, stream);
+  return evict_keys<uint8_t>(p, cluster, stream);
 }
 
 }  // namespace pa

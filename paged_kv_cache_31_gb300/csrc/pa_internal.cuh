@@ -711,7 +711,7 @@ struct EvictParams {
   int32_t block_shift;  // of a block size that is a power of two, else -1
   int64_t num_blocks;
   int64_t row_bytes;  // of one position and kv head
-  int32_t* moves;     // workspace: lists of up to moves_len fillers for each (sequence, kv head)
+  int32_t* moves;     // workspace: a list for each (sequence, kv head), moves_len words
   int64_t moves_len;  // most keys of a sequence
   int* status;
 };
