@@ -756,7 +756,8 @@ size_t pa_window_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, 
  * K rows of keys that a token does not see may hold anything.  So may V rows at or past seq_lens[s],
  * and those of blocks between the first tokens' and the first that the sequence's tokens reach: these
  * are not read, and their table entries not looked at (a server may have given them away).  All other V
- * rows of the sequence have to be finite (an unseen one enters the products with weight zero).
+ * rows of the sequence have to be finite (an unseen one enters the products with weight zero), their
+ * magnitudes, scaled, up to 2^100 (the sums before the division are fp32, of weights up to 2^8).
  * Validation, on the device before anything is written: query_start_loc starts at 0, never decreases
  * and ends at num_tokens; for a sequence with tokens, seq_lens[s] >= 1, its table covers seq_lens[s]
  * positions with ids in [0, num_blocks) where they are read, and its tokens' positions lie in

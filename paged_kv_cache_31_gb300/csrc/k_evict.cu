@@ -95,7 +95,7 @@ __device__ __forceinline__ void cluster_wait() {
 // the list of fillers (from, to) lies in shared memory.  E = 0: weights are read again in every pass, and
 // the list lies in the workspace, written by the cluster's first CTA.
 template <typename T, int NT, int E>
-__global__ void __launch_bounds__(NT, 1024 / NT)
+__global__ void __launch_bounds__(NT, (NT == 1024 ? 1 : 1536 / NT))
     k_evict(const EvictParams p, int cluster, int row_words, int part_words) {
   extern __shared__ __align__(16) uint8_t s_mem[];
   __shared__ __align__(16) int s_work[kBins];  // histogram; then the moves' places, kMoves int2
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
     if (id < 0 || (int64_t)id >= p.num_blocks) return -1;
     return id * p.block_size + o;
   };
-  constexpr int U = 4;  // rows of a thread's batch
+  constexpr int U = 2;  // rows of a thread's batch
   int2* places = reinterpret_cast<int2*>(s_work);  // slots (from, to); to -1: nothing is moved
   const int64_t stride = (int64_t)p.num_kv_heads * row_words;
   // this CTA's words of a row of K and of V laid end to end, up to NT at a time

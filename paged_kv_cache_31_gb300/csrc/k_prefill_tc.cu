@@ -251,9 +251,20 @@ __device__ __forceinline__ int item_of(const Ctx& c, int k) {
 
 struct Item {
   int s, kvh, qt, t0, n_tok, n, kv0, ntiles, nblk_vis;
+  // WIN: keys are counted without the gap of `gap` blocks behind the first `front` blocks (n, ntiles
+  // and nblk_vis, too; kv0 is 0)
+  int front, gap;
+  // table index of block b
+  template <bool WIN>
+  __device__ __forceinline__ int entry(int b) const {
+    return WIN && b >= front ? b + gap : b;
+  }
 };
 
-// Item idx = (256-row pair, kv head); this CTA of the pair takes the 128-row tile `rank`.
+// Item idx = (256-row pair, kv head); this CTA of the pair takes the 128-row tile `rank`.  WIN: an
+// attention behind a window with first tokens, whose plan (k_window.cu) gives an item's gap and the end
+// of its keys.
+template <bool WIN>
 __device__ __forceinline__ Item load_item(const TcParams& p, int idx, uint32_t rank) {
   const VarlenMeta& m = p.m;
   const int4 it = reinterpret_cast<const int4*>(p.plan + p.tc_off)[idx / m.num_kv_heads];
@@ -267,7 +278,15 @@ __device__ __forceinline__ Item load_item(const TcParams& p, int idx, uint32_t r
   r.n_tok = max(0, min(tpt, qe - r.t0));
   r.n = m.seq_lens[r.s];
   const int lo = it.z, hi = it.w;
-  r.kv0 = (lo / 16) * 16;
+  r.front = r.gap = 0;
+  if constexpr (WIN) {
+    r.front = (p.first + 15) / 16;
+    r.gap = lo;
+    r.n -= 16 * lo;
+    r.kv0 = 0;
+  } else {
+    r.kv0 = (lo / 16) * 16;
+  }
   r.ntiles = (hi - r.kv0 + kBN - 1) / kBN;
   r.nblk_vis = (hi + 15) / 16;  // logical blocks [kv0 / 16, nblk_vis) hold visible keys
   return r;
@@ -289,23 +308,23 @@ __device__ void drain_ring(const Ctx& c, int full, uint32_t nst, uint32_t issued
     mbar_wait(c.bar + full + k % nst, (k / nst) & 1u, c.limit);
 }
 
-template <bool FP8>
+template <bool FP8, bool WIN>
 __device__ void producer_loop(const Ctx& c, const TcParams& p, const CUtensorMap* tq,
                               const CUtensorMap* tkv, bool is_v, int n_items, uint32_t& kv,
                               uint32_t& q_issued);
 
-template <bool FP8>
+template <bool FP8, bool WIN>
 __device__ void producer(const Ctx& c, const TcParams& p, const CUtensorMap* tq,
                          const CUtensorMap* tkv, bool is_v, int n_items) {
   uint32_t kv = 0, q_issued = 0;  // K (or V) stage loads and Q loads issued
-  producer_loop<FP8>(c, p, tq, tkv, is_v, n_items, kv, q_issued);
+  producer_loop<FP8, WIN>(c, p, tq, tkv, is_v, n_items, kv, q_issued);
   // normally every issued copy has been consumed and these return at once
   drain_ring(c, is_v ? B_VFULL : B_KFULL, is_v ? kStagesV : kStagesK, kv);
   if (!is_v) drain_ring(c, B_QFULL, 2, q_issued);
   __syncwarp();
 }
 
-template <bool FP8>
+template <bool FP8, bool WIN>
 __device__ void producer_loop(const Ctx& c, const TcParams& p, const CUtensorMap* tq,
                               const CUtensorMap* tkv, bool is_v, int n_items, uint32_t& kv,
                               uint32_t& q_issued) {
@@ -316,7 +335,7 @@ __device__ void producer_loop(const Ctx& c, const TcParams& p, const CUtensorMap
   const uint32_t nst = is_v ? kStagesV : kStagesK;
   uint32_t it_cnt = 0;
   for (int idx; (idx = item_of(c, (int)it_cnt)) < n_items; ++it_cnt) {
-    const Item I = load_item(p, idx, c.rank);
+    const Item I = load_item<WIN>(p, idx, c.rank);
     const int32_t* row = m.block_tables + (int64_t)I.s * m.max_blocks;
     const int blk0 = I.kv0 / 16;
     if (!is_v) {
@@ -335,12 +354,12 @@ __device__ void producer_loop(const Ctx& c, const TcParams& p, const CUtensorMap
       if (!__shfl_sync(kFull, (int)qok, 0)) return;
       ++q_issued;
     }
-    int next_id = (lane < 8 && blk0 + lane < I.nblk_vis) ? row[blk0 + lane] : -1;
+    int next_id = (lane < 8 && blk0 + lane < I.nblk_vis) ? row[I.entry<WIN>(blk0 + lane)] : -1;
     for (int j = 0; j < I.ntiles; ++j, ++kv) {
       const int id = next_id;
       if (j + 1 < I.ntiles) {  // prefetch the next tile's block ids
         const int lb = blk0 + 8 * (j + 1) + lane;
-        next_id = (lane < 8 && lb < I.nblk_vis) ? row[lb] : -1;
+        next_id = (lane < 8 && lb < I.nblk_vis) ? row[I.entry<WIN>(lb)] : -1;
       }
       // lane 0 claims the stage; then lanes 0..7 issue one box each (a TMA fill probe moved
       // these 16-row boxes faster with several issuing lanes than with one)
@@ -386,7 +405,7 @@ __device__ void producer_loop(const Ctx& c, const TcParams& p, const CUtensorMap
 __device__ __forceinline__ uint32_t buf_of(uint32_t s) { return s % kSBufs; }
 __device__ __forceinline__ uint32_t use_par(uint32_t s) { return (s / kSBufs) & 1u; }
 
-template <bool FP8>
+template <bool FP8, bool WIN>
 __device__ void s_issuer(const Ctx& c, const TcParams& p, uint32_t tmem, int n_items) {
   const uint32_t sm = smem_u32(c.sm);
   const bool leader = c.rank == 0, fp8 = FP8;
@@ -397,7 +416,7 @@ __device__ void s_issuer(const Ctx& c, const TcParams& p, uint32_t tmem, int n_i
   const int qready = fp8 ? B_QCONV : B_QFULL, kready = fp8 ? B_KCONV : B_KFULL;
   uint32_t kv = 0, it_cnt = 0;
   for (int idx; (idx = item_of(c, (int)it_cnt)) < n_items; ++it_cnt) {
-    const Item I = load_item(p, idx, c.rank);
+    const Item I = load_item<WIN>(p, idx, c.rank);
     const uint32_t qb = it_cnt & 1u;
     if (!__all_sync(kFull, wait_bar(c, qready + qb, (it_cnt >> 1) & 1u))) return;
     if (!leader && (threadIdx.x & 31) == 0) arrive_leader(c.bar + B_QFULL + qb);
@@ -429,11 +448,12 @@ __device__ void s_issuer(const Ctx& c, const TcParams& p, uint32_t tmem, int n_i
 
 // The leader's whole warp runs the PV loop (lane 0 issues): O += P_j V_j once P_j is in
 // tensor memory and both CTAs' parts of V_j are f16.  The peer's warp has nothing to do.
+template <bool WIN>
 __device__ void pv_issuer(const Ctx& c, const TcParams& p, uint32_t tmem, int n_items) {
   if (c.rank != 0) return;
   uint32_t kv = 0, it_cnt = 0;
   for (int idx; (idx = item_of(c, (int)it_cnt)) < n_items; ++it_cnt) {
-    const Item I = load_item(p, idx, c.rank);
+    const Item I = load_item<WIN>(p, idx, c.rank);
     for (int j = 0; j < I.ntiles; ++j) {
       const uint32_t s = kv + j, st = s % kStagesV, b = buf_of(s);
       if (j == 0 && !__all_sync(kFull, wait_bar(c, B_OFREE, (it_cnt & 1u) ^ 1u))) return;
@@ -473,11 +493,12 @@ __device__ __forceinline__ uint32_t f16x2_poison(uint32_t acc, uint32_t h) {
 // on it stalls the warp on a memory barrier per stage, which measured 40% slower per call.
 // The stores are to this CTA's own shared memory, and fence.proxy.async (shared::cta) makes
 // them visible to the asynchronous proxy, through which the pair's MMAs read them.
+template <bool WIN>
 __device__ void v_converter(const Ctx& c, const TcParams& p, int n_items) {
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kFirstConvWarp;
   uint32_t kv = 0, it_cnt = 0;
   for (int idx; (idx = item_of(c, (int)it_cnt)) < n_items; ++it_cnt) {
-    const Item I = load_item(p, idx, c.rank);
+    const Item I = load_item<WIN>(p, idx, c.rank);
     uint32_t poison = 0;  // f16 pair; NaN once a widened value overflowed
     for (int j = 0; j < I.ntiles; ++j) {
       const uint32_t s = kv + j, st = s % kStagesV;
@@ -614,7 +635,7 @@ __device__ void fp8_converter(const Ctx& c, const TcParams& p, int n_items) {
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kFirstConvWarp;
   uint32_t kv = 0, it_cnt = 0;
   for (int idx; (idx = item_of(c, (int)it_cnt)) < n_items; ++it_cnt) {
-    const Item I = load_item(p, idx, c.rank);
+    const Item I = load_item<false>(p, idx, c.rank);
     FactorPipe<2> vf;  // PB: the V factors of blocks 2w, 2w + 1 of each tile
     float rref = 1.f;  // PB: 1 / the item's V reference
     bool out_of_range = false;  // PB: a ratio outside [kRatioMin, kRatioMax]
@@ -730,7 +751,7 @@ __device__ __forceinline__ void pair_sync(int quad) {
   asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
 }
 
-template <bool PB>
+template <bool PB, bool WIN>
 __device__ void softmax_role(const Ctx& c, const TcParams& p, uint32_t tmem, int n_items) {
   const VarlenMeta& m = p.m;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -747,7 +768,7 @@ __device__ void softmax_role(const Ctx& c, const TcParams& p, uint32_t tmem, int
   // dependent loads: the next item's is fetched while the current one's last P V runs
   Item In{};
   int pos_n = 0;
-  if (item_of(c, 0) < n_items) In = load_item(p, item_of(c, 0), c.rank);
+  if (item_of(c, 0) < n_items) In = load_item<WIN>(p, item_of(c, 0), c.rank);
   if (r / m.group < In.n_tok) pos_n = m.positions[In.t0 + r / m.group];
   for (int k = 0; item_of(c, k) < n_items; ++k) {
     const Item I = In;
@@ -757,9 +778,11 @@ __device__ void softmax_role(const Ctx& c, const TcParams& p, uint32_t tmem, int
     const int h = I.kvh * m.group + r % m.group;
     int start = 0, end = 0;
     if (valid) {
-      end = m.causal ? pos_n + 1 : I.n;
+      end = WIN ? pos_n + 1 - 16 * I.gap : m.causal ? pos_n + 1 : I.n;
       start = m.window > 0 ? max(0, end - m.window) : 0;
     }
+    // WIN: the first keys are visible, too, up to `end`
+    const int first = WIN && m.window > 0 ? min(p.first, end) : 0;
     float m_ref = -INFINITY, l = 0.f;
     const float sl = head_scale(m.k_scales, I.kvh, p.scale_log2);  // K = k_scales[g] * pool
     // PB: the K factors of this thread's four blocks (64 columns) in each tile, and the V
@@ -797,11 +820,17 @@ __device__ void softmax_role(const Ctx& c, const TcParams& p, uint32_t tmem, int
       // mask the raw scores (scale > 0 on this path, so the max commutes with it); an
       // invalid row has start == end == 0 and masks everything
       const int key0 = I.kv0 + j * kBN + col0;
-      if (!(key0 >= start && key0 + 64 <= end)) {
+      if (!(key0 >= start && key0 + 64 <= end) && !(WIN && key0 + 64 <= first)) {
         // visible columns of this thread: [a, b) within its 64
         const int a = start - key0, bnd = end - key0;
+        if constexpr (WIN) {
+          const int f = first - key0;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) x[i] = (i >= a && i < bnd) ? x[i] : -INFINITY;
+          for (int i = 0; i < 64; ++i) x[i] = ((i >= a && i < bnd) || i < f) ? x[i] : -INFINITY;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) x[i] = (i >= a && i < bnd) ? x[i] : -INFINITY;
+        }
       }
       float mx[8];
       float sq[4];  // PB: the score scale of each 16-column block, sl times its K factor
@@ -897,7 +926,7 @@ __device__ void softmax_role(const Ctx& c, const TcParams& p, uint32_t tmem, int
     }
 
     if (item_of(c, k + 1) < n_items) {
-      In = load_item(p, item_of(c, k + 1), c.rank);
+      In = load_item<WIN>(p, item_of(c, k + 1), c.rank);
       if (tl < In.n_tok) pos_n = m.positions[In.t0 + tl];
     }
     // epilogue: o = O / l, with l summed over both column halves; the pair's failure flags
@@ -916,6 +945,8 @@ __device__ void softmax_role(const Ctx& c, const TcParams& p, uint32_t tmem, int
     // an attention sink (TensorSharp ForwardWithSinks) is one more state to merge: max = the
     // sink logit, exp-sum = 1, weighted sum = 0
     float o_scale = 1.f;
+    // (WIN: a row whose sum is NaN comes out as NaN)
+    auto seen = [](float sum) { return WIN ? sum != 0.f : sum > 0.f; };
     {
       const float sk = m.sinks ? m.sinks[h] * kLog2e : -INFINITY;
       if (sk > -INFINITY) {
@@ -926,9 +957,10 @@ __device__ void softmax_role(const Ctx& c, const TcParams& p, uint32_t tmem, int
       }
     }
     if (m.lse && hf == 0 && valid)
-      m.lse[(int64_t)h * m.num_tokens + t] = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+      m.lse[(int64_t)h * m.num_tokens + t] =
+          seen(l) ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
     const float inv =
-        l > 0.f ? o_scale * head_scale(m.v_scales, I.kvh, m.v_scale) * vref / l : 0.f;
+        seen(l) ? o_scale * head_scale(m.v_scales, I.kvh, m.v_scale) * vref / l : 0.f;
     __nv_bfloat16* dst =
         reinterpret_cast<__nv_bfloat16*>(p.out) + ((int64_t)t * m.num_heads + h) * kD + col0;
     // rows start 256 bytes apart and halves at 0 / 128: 32-byte aligned when the output is
@@ -967,11 +999,12 @@ __device__ void softmax_role(const Ctx& c, const TcParams& p, uint32_t tmem, int
   }
 }
 
-template <bool FP8, bool PB>
+template <bool FP8, bool PB, bool WIN = false>
 __global__ void __launch_bounds__(kThreads, 1)
     k_tc_prefill(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const TcParams p) {
   static_assert(!PB || FP8, "per-block factors are for e4m3 pools");
+  static_assert(!WIN || !FP8, "windows with first tokens: bf16 pools");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~uintptr_t(1023));
@@ -1046,7 +1079,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (FP8)
       fp8_converter<PB>(c, p, n_items);
     else
-      v_converter(c, p, n_items);
+      v_converter<WIN>(c, p, n_items);
     tc_fence_before();
     cluster_sync();
   } else if (warp < 4) {
@@ -1055,14 +1088,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
     if (warp == 0) {
-      producer<FP8>(c, p, &tq, &tk, false, n_items);
+      producer<FP8, WIN>(c, p, &tq, &tk, false, n_items);
     } else if (warp == 2) {
-      producer<FP8>(c, p, &tq, &tv, true, n_items);
+      producer<FP8, WIN>(c, p, &tq, &tv, true, n_items);
     } else if (warp == 1 || warp == 3) {
       if (warp == 1)
-        s_issuer<FP8>(c, p, tmem, n_items);
+        s_issuer<FP8, WIN>(c, p, tmem, n_items);
       else
-        pv_issuer(c, p, tmem, n_items);
+        pv_issuer<WIN>(c, p, tmem, n_items);
       __syncwarp();
       // every MMA issued by either warp of the leader has completed before the tensor memory is
       // released
@@ -1089,7 +1122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 184;" ::: "memory");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 200;" ::: "memory");
-    softmax_role<PB>(c, p, tmem, n_items);
+    softmax_role<PB, WIN>(c, p, tmem, n_items);
     tc_fence_before();
     cluster_sync();
   }
@@ -1101,7 +1134,8 @@ cudaError_t launch_tc_prefill(const CUtensorMap& tq, const CUtensorMap& tk, cons
                               const TcParams& p, int grid, cudaStream_t stream) {
   if (grid < 2) grid = 2;
   // per-block factors: e4m3 pools only (the caller checks)
-  auto kern = !p.kv_fp8 ? k_tc_prefill<false, false>
+  auto kern = p.win ? k_tc_prefill<false, false, true>
+              : !p.kv_fp8 ? k_tc_prefill<false, false>
               : p.m.k_bscales ? k_tc_prefill<true, true> : k_tc_prefill<true, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;

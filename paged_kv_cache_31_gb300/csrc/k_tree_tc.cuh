@@ -1206,6 +1206,8 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     const bool off = (smem_u32(sm) & 1023u) != 0;
     if (off) record_error(p.status, PA_ECUDA);
     flags[0] = off || status_set(p.status) ? 1 : 0;
+    // (behind the prefill kernel: only where that left an item to do again)
+    if (MODE == kWindow && p.tc.plan && __ldcg(p.tc.plan + 3) == 0) flags[0] = 1;
   }
   if (CL && warp == 2) plan_own(p, own, threadIdx.x & 31);
   __syncthreads();

@@ -54,6 +54,80 @@ __device__ __forceinline__ int token_from(const int32_t* pos, int a, int b, int6
   return a;
 }
 
+// One block, for batches that go to the prefill kernel: its items, those of the most key tiles first (a
+// counting sort, eight buckets to an octave), and how many pairs of CTAs take them: the number that ends
+// both it and the decoding sequences beside it soonest.
+__device__ void plan_prefill(const TreeParams& p, int items, const int* s_base, int64_t* s_scratch) {
+  const VarlenMeta& m = p.m;
+  constexpr int kBuckets = 256;
+  __shared__ int s_at[kBuckets];
+  __shared__ unsigned long long s_tiles, s_keys;
+  __shared__ unsigned int s_best;
+  const int tid = threadIdx.x;
+  int* s_warp = reinterpret_cast<int*>(s_scratch);
+  auto bucket = [](int tiles) {  // 0: the most
+    return kBuckets - 1 - min((int)(__float_as_uint((float)tiles) >> 20) - (127 << 3), kBuckets - 1);
+  };
+  auto sequence_of = [&](int i) {
+    int lo = 0, hi = m.num_seqs;  // the last sequence whose first item is at most i: it has items
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((s_base ? s_base[mid] : p.seqs[2 * mid + 1].y) <= i) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+  if (tid < kBuckets) s_at[tid] = 0;
+  if (tid == 0) {
+    s_tiles = s_keys = 0;
+    s_best = ~0u;
+  }
+  __syncthreads();
+  unsigned long long tiles = 0, keys = 0;
+  for (int i = tid; i < items; i += kPlanThreads) {
+    const int s = sequence_of(i);
+    const int4 k = p.item_keys[i];
+    if (p.seqs[2 * s + 1].z > kWindowDecodeRows) {
+      tiles += k.z;
+      atomicAdd(&s_at[bucket(k.z)], 1);
+    } else {
+      keys += k.w;
+    }
+  }
+  if (tiles) atomicAdd(&s_tiles, tiles);
+  if (keys) atomicAdd(&s_keys, keys);
+  __syncthreads();
+  int total;
+  const int n = tid < kBuckets ? s_at[tid] : 0;
+  const int at = block_exclusive_scan(n, s_warp, &total);
+  if (tid < kBuckets) s_at[tid] = at;
+  __syncthreads();
+  int4* list = reinterpret_cast<int4*>(p.tc.plan + p.tc.items_off);
+  for (int i = tid; i < items; i += kPlanThreads) {
+    const int s = sequence_of(i);
+    if (p.seqs[2 * s + 1].z <= kWindowDecodeRows) continue;
+    const int4 k = p.item_keys[i];
+    const int to = atomicAdd(&s_at[bucket(k.z)], 1);
+    list[to] = make_int4(s, i - p.seqs[2 * s + 1].y, k.y, k.w);
+    p.tc.plan[p.tc.redo_off + to] = 0;
+  }
+  // k pairs: a key tile of 256 rows takes a pair 1.1 us; decoding sequences stream at the memory's rate
+  // on 80 SMs or more (the other pairs' SMs), and on all when the prefill items have ended
+  if (tid < p.tc.pairs) {
+    const int k = tid + 1, left = p.tc.num_sms - 2 * k;
+    const float prefill = (float)s_tiles * m.num_kv_heads * 1.1f / k;
+    const float stream = (float)s_keys * p.tc.decode_bytes_per_key / 6.7e6f;  // us on all SMs
+    const float rate = min(1.f, left / 80.f);  // while the prefill items run
+    const float time = prefill * rate >= stream ? prefill : prefill + (stream - prefill * rate);
+    atomicMin(&s_best, ((unsigned)min(time, 1e6f) << 8) | (unsigned)(p.tc.pairs - k));
+  }
+  __syncthreads();
+  if (tid == 0) {
+    p.tc.plan[1] = total;
+    p.tc.plan[3] = 0;
+    p.tc.plan[5] = p.tc.pairs - (int)(s_best & 255u);
+  }
+}
+
 // The work of an item of the key weights, in about hundredths of a microsecond (only the balance
 // between the CTAs depends on it): its keys, and each row tile.
 constexpr int kWeightItem = 150, kWeightRowTile = 100;
@@ -72,7 +146,8 @@ __device__ void plan_weights(const TreeParams& p, int64_t* s_warp, int64_t* s_cu
     int4 first = make_int4(0, 0, 0, 0);
     if (s < m.num_seqs) {
       bad |= !sequence(p, s, qs, q, n);
-      if (q > 0) {
+      // (the others' weights are added where they decode)
+      if (q > 0 && !(p.tc.plan && q * m.group <= kWindowDecodeRows)) {
         // the keys that counted tokens see: those of the first positions, and from lo to the last one
         const int skip = p.observed > 0 ? max(0, q - p.observed) : 0;
         const int low = m.positions[qs + skip], last = m.positions[qs + q - 1];
@@ -229,7 +304,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_window_plan(const TreeParams p
       const Keys k = keys_from(p, a);
       const int end = min(max(b, a), q.z - 1) + 1 - k.gap * m.block_size;
       const int tiles = max(1, (end + p.key_tile - 1) / p.key_tile);
-      p.item_keys[i] = make_int4(k.front, k.gap, tiles, 0);
+      p.item_keys[i] = make_int4(k.front, k.gap, tiles, max(end, 1));
       weight = (int64_t)tree_weight(p, rows) * tiles + kTreeItemWeight;
     }
     int64_t total;
@@ -239,6 +314,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_window_plan(const TreeParams p
   }
   if (tid == 0) p.item_cum[items] = base;
   bad = __syncthreads_or(bad);  // (and the items' records can be read)
+  if (p.tc.plan) plan_prefill(p, bad ? 0 : (int)items, shared ? s_base : nullptr, s_warp);
   if (bad) {
     if (tid == 0) record_error(p.status, PA_EINVAL);
     for (int s = tid; s < m.num_seqs; s += kPlanThreads)
@@ -295,7 +371,9 @@ WindowLayout window_layout(int32_t num_seqs, int64_t num_tokens, int32_t num_hea
   L.tree = t;
   L.items_off = t.bytes;
   L.item_cum_off = L.items_off + up(16 * items);
-  L.lse_off = L.item_cum_off + up(8 * (items + 1));
+  L.tc_off = L.item_cum_off + up(8 * (items + 1));
+  // header words, items, marks, list of marked items
+  L.lse_off = L.tc_off + up(4 * (kPlanHeaderWords + 6 * items));
   L.bytes = L.w_seqs_off = L.lse_off + (weights ? up(4 * num_tokens * num_heads) : 0);
   if (!weights) return L;
   const int64_t key_items = std::min<int64_t>(num_seqs, num_tokens) * ((max_keys + kWeightKeys - 1) / kWeightKeys);

@@ -206,7 +206,10 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
   const bool usable = qs >= 0 && qe >= qs && (int64_t)qe <= m.num_tokens && n >= 1 &&
                       ((int64_t)n + kBlk - 1) / kBlk <= m.max_blocks &&
                       (!WEIGH || (int64_t)n <= p.weights_len);
-  const int rows = usable && !sh.fail ? (qe - qs) * G : 0;
+  int rows = usable && !sh.fail ? (qe - qs) * G : 0;
+  // beside the prefill kernel: the sequences that it leaves; the plan was complete before it started
+  // (and left no tokens to a batch that is not valid)
+  if (p.after_tc && (rows > kWindowDecodeRows || p.seqs[2 * s].y == 0)) rows = 0;
   const int counted0 = WEIGH && p.observed > 0 ? max(0, qe - qs - p.observed) * G : 0;  // row
   const int32_t* table = m.block_tables + (int64_t)s * m.max_blocks;
   const float sl = p.scale * kLog2e;
@@ -612,7 +615,7 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
         }
       }
     }
-    if (!waited) {
+    if (!waited && !p.after_tc) {
       // the check of the batch is complete; whatever follows on the stream may be prepared
       pdl_wait();
       pdl_launch_dependents();
@@ -825,9 +828,11 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
     fence_proxy_async_smem();
     if (C > 1) cluster_sync(); else __syncthreads();
   }
-  if (!waited) {  // (a sequence without rows)
-    pdl_wait();
+  if (!waited) {
+    // a sequence without rows; beside the prefill kernel one CTA stays for it, so that what follows on
+    // the stream finds both done
     pdl_launch_dependents();
+    if (!p.after_tc || blockIdx.x == gridDim.x - 1) pdl_wait();
   }
 }
 

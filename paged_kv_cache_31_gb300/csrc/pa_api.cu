@@ -82,6 +82,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 // TMA descriptor of a bf16 pool [num_blocks, 16, Hkv, D] seen as the 3-D tensor
 // (D, Hkv, num_blocks * 16) with a 64 x 1 x 16 box and the 128-byte swizzle.
 bool pool_map(CUtensorMap* map, const void* base, int64_t num_blocks, int block_size, int hkv,
@@ -97,8 +99,6 @@ bool pool_map(CUtensorMap* map, const void* base, int64_t num_blocks, int block_
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-}  // namespace
 
 // TMA descriptor of a bf16 pool [num_blocks, 16, Hkv, D] seen as the 5-D tensor (64 dims of a half,
 // 8 rows, D / 64 halves, num_blocks * 2 groups of 8 rows, Hkv): a 64 x 8 x D/64 x 2 x 1 box is a

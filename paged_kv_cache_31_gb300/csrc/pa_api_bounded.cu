@@ -237,10 +237,56 @@ pa_status attend(const Call& c) {
                    pool_map_rows(&tv, c.v_blocks, c.num_blocks, c.num_kv_heads, c.head_dim));
     if (!ok) return PA_ECUDA;
   }
+  // many items of prompt chunks: the prefill kernel takes them (its pairs of CTAs do a fifth to a half
+  // more a second, but an item's keys are not cut, so there have to be more items than pairs)
+  const int64_t key_bytes = 2 * (int64_t)c.head_dim * esize(c.kv_dtype);
+  const bool prefill = tc && !fp8 && c.head_dim == 128 && 128 % group == 0 &&
+                       c.num_tokens * group / 256 * c.num_kv_heads >= 2 * d->sms && units < (1 << 24);
+  if (prefill) {
+    p.tc.plan = reinterpret_cast<int32_t*>(ws + L.tc_off);
+    const int64_t items = (c.num_tokens * group + 255) / 256 + c.num_seqs;
+    p.tc.items_off = kPlanHeaderWords;
+    p.tc.redo_off = p.tc.items_off + 4 * items;
+    p.tc.redo_list_off = p.tc.redo_off + items;
+    p.tc.num_sms = d->sms;
+    p.tc.pairs = d->sms / 2;
+    p.tc.decode_bytes_per_key = (float)(key_bytes * c.num_kv_heads);
+  }
   if (launch_window_plan(p, c.stream) != cudaSuccess) return PA_ECUDA;
   uint64_t limit;
   uint32_t stall;
   stall_hook(limit, stall);
+  if (prefill) {
+    CUtensorMap pk, pv;
+    if (!pool_map(&pk, c.k_blocks, c.num_blocks, 16, c.num_kv_heads, c.head_dim) ||
+        !pool_map(&pv, c.v_blocks, c.num_blocks, 16, c.num_kv_heads, c.head_dim))
+      return PA_ECUDA;
+    TcParams tp;
+    std::memset(&tp, 0, sizeof tp);
+    tp.out = c.out;
+    tp.m = m;
+    tp.plan = p.tc.plan;
+    tp.tc_off = p.tc.items_off;
+    tp.status = d->status;
+    tp.scale_log2 = p.scale * kLog2e;
+    tp.wait_limit_ns = limit;
+    tp.debug_stall = stall;
+    tp.win = 1;
+    tp.first = p.first;
+    tp.redo_flags = p.tc.plan + p.tc.redo_off;
+    tp.redo_list = p.tc.plan + p.tc.redo_list_off;
+    tp.redo_count = p.tc.plan + 3;
+    if (launch_tc_prefill(tq, pk, pv, tp, 2 * p.tc.pairs, c.stream) != cudaSuccess) return PA_ECUDA;
+    TreeParams dp = p;  // the decoding sequences
+    dp.after_tc = 1;
+    dp.w.room = 0;
+    const int64_t keys = c.window > 0 ? std::min<int64_t>((int64_t)c.window + p.first, max_keys) : max_keys;
+    const DecodeForm f = decode_form(units, c.num_seqs, keys, key_bytes, d->sms);
+    dp.cluster = f.cluster;
+    dp.narrow = f.narrow;
+    dp.ordered = f.ordered;
+    if (launch_window_decode(tk, tv, dp, fp8, limit, stall, c.stream) != cudaSuccess) return PA_ECUDA;
+  }
   if (tc) {
     if (launch_window_tc(tq, tk, tv, p, fp8, limit, stall, c.stream) != cudaSuccess) return PA_ECUDA;
   } else if (launch_window_generic(p, c.kv_dtype, c.stream) != cudaSuccess) {

@@ -442,6 +442,7 @@ struct TcParams {
   float scale_log2;
   uint64_t wait_limit_ns;
   uint32_t debug_stall;  // tests only: the softmax waits run out (PA_DEBUG_STALL_NS)
+  int32_t win, first;    // behind a window with first tokens (k_window.cu's plan), bf16 pools
   int32_t kv_fp8;        // e4m3 pools (tk: 128 x 1 x 16 byte boxes, tv: 64 x 1 x 16)
   // items whose V does not fit f16 (recomputed by the warp-MMA kernel afterwards): a flag per
   // 256-row item, the list of marked items and its length (all in the plan)
@@ -621,6 +622,16 @@ struct TreeParams {
   int32_t narrow, ordered;  // batches of decoding tokens: the CTAs' shape, longest sequences first
   int4* item_keys;  // [items of all sequences] (front blocks, gap in blocks behind them, key tiles, 0)
   int64_t* item_cum;  // [items + 1] weight before the item, over all items of a kv head in order
+  // Large batches of prompt chunks: sequences of more than kWindowDecodeRows rows go to the prefill kernel
+  // (k_prefill_tc.cu, plan as for that kernel: header words, items, marks, list of marked items), the
+  // others to k_window_decode; this kernel runs again over the batch when an item was marked.
+  struct {
+    int32_t* plan;  // null: no such batch
+    int64_t items_off, redo_off, redo_list_off;  // words
+    int32_t pairs, num_sms;
+    float decode_bytes_per_key;  // of a decode-class sequence, all kv heads
+  } tc;
+  int32_t after_tc;  // k_window_decode: it runs beside the prefill kernel
   // Attention weights that keys receive (k_key_weights.cu): [num_seqs, num_kv_heads, weights_len] that
   // the weights are added to, of the last `observed` tokens of each sequence (null: none are).
   float* key_weights;
@@ -676,10 +687,11 @@ int tree_clusters_resident(int device, bool fp8, int head_dim, int c);  // c 2, 
 // Attention behind a window with first tokens, and the attention weights that keys receive.
 struct WindowLayout {
   TreeLayout tree;
-  int64_t items_off, item_cum_off, lse_off;
+  int64_t items_off, item_cum_off, tc_off, lse_off;
   int64_t w_seqs_off, w_items_off, w_cum_off, w_starts_off, w_part_off;  // given weights
   int64_t bytes;
 };
+constexpr int32_t kWindowDecodeRows = 16;  // query rows of a kv head up to which a sequence decodes
 constexpr int32_t kWeightKeys = 256;  // of an item of the weights' tensor-core kernel
 WindowLayout window_layout(int32_t num_seqs, int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
                            int32_t head_dim, int64_t max_keys, int32_t rows_per_item, int32_t key_tile,
@@ -728,6 +740,7 @@ struct DeviceState {
 const DeviceState* device_state();
 
 // tensor maps (false: the driver refused), waits and paths of the attention kernels; see pa_api.cu
+bool pool_map(CUtensorMap* map, const void* base, int64_t num_blocks, int block_size, int hkv, int d);
 bool pool_map_rows(CUtensorMap* map, const void* base, int64_t num_blocks, int hkv, int d);
 bool pool_map_fp8(CUtensorMap* map, const void* base, int64_t num_blocks, int block_size,
                   int hkv, int d, bool one_head = false);

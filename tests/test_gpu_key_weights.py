@@ -4,7 +4,7 @@ import torch
 
 from tests import bounded_reference as ref
 from tests.spec_reference import U32, assert_within, stored
-from tests.test_gpu_window import BF16, BIG, E4M3, F32, MIXED, roundings
+from tests.test_gpu_window import BF16, BIG, CHUNKS, E4M3, F32, MIXED, roundings
 
 pytestmark = pytest.mark.gpu
 
@@ -17,7 +17,7 @@ def pa():
 
 
 def check(pa, b, observed=0, window=0, first=0, sinks=None, scales=(1.0, 1.0), lse=False, room=9,
-          per_head=None):
+          per_head=None, v_bits=0.0):
     L = int(b.lens.max()) + room
     ks = torch.full((b.Hkv,), scales[0]) if per_head is None else per_head[0].cpu()
     vs = torch.full((b.Hkv,), scales[1]) if per_head is None else per_head[1].cpu()
@@ -30,7 +30,7 @@ def check(pa, b, observed=0, window=0, first=0, sinks=None, scales=(1.0, 1.0), l
     pa.pa_attention_key_weights(*b.args(), w, b.scale, observed_tokens=observed, sliding_window=window,
                                 first_tokens=first, sinks=sinks, lse=b.lse if lse else None, **extra)
     assert pa.pa_device_status() == pa.PA_OK
-    y, bound = stored(want["out"], want["out_b"], b.out.dtype)
+    y, bound = stored(want["out"], want["out_b"] + v_bits, b.out.dtype)
     assert_within(b.out, y, bound, "out")
     if lse:
         assert_within(b.lse, want["lse"], want["lse_b"], "lse")
@@ -92,6 +92,14 @@ def test_long_chunk(pa, kv):
     b = ref.Batch([(1700, 900), (0, 1300), (2100, 1)], 8, 2, 128, kv=kv, seed=8)
     for observed in (0, 77):
         check(pa, b, observed, scales=(0.125, 0.25) if kv == E4M3 else (1.0, 1.0))
+
+
+@pytest.mark.parametrize("observed,window,first", [(0, 0, 0), (25, 0, 0), (0, 300, 4), (1, 64, 70)])
+def test_many_chunks(pa, observed, window, first):
+    """Enough rows for the prefill kernel, with decoding sequences beside it."""
+    b = ref.Batch(CHUNKS, 64, 8, 128, seed=observed)
+    b.poison_unread(window, first)
+    check(pa, b, observed, window, first, lse=observed == 25, v_bits=2.0 ** -25)
 
 
 @pytest.mark.parametrize("kv", [BF16, E4M3])

@@ -22,10 +22,15 @@ def roundings(b, tc=None):
     """What the kernels round softmax weights and q to (see spec_reference.tree_attention)."""
     if b.kb.dtype == E4M3 and b.q.dtype == BF16:
         return {"weight_u": 2.0 ** -11, "q_u": 2.0 ** -17, "weight_min": 2.0 ** -32}
+    if b.T * (b.H // b.Hkv) // 256 * b.Hkv >= 304:
+        # the prefill kernel: one f16 weight, at least 2^-8 for the row's largest (its reference may lie
+        # 8 powers of two above): below its normal range half its smallest step, 2^-25
+        return {"weight_u": 2.0 ** -11, "weight_min": 2.0 ** -25}
     return {"weight_u": 2.0 ** -16}
 
 
-def check(pa, b, window, first, sinks=None, scales=(1.0, 1.0), per_head=None, lse=True, **kw):
+def check(pa, b, window, first, sinks=None, scales=(1.0, 1.0), per_head=None, lse=True, v_bits=0.0,
+          **kw):
     ks = torch.full((b.Hkv,), scales[0]) if per_head is None else per_head[0].cpu()
     vs = torch.full((b.Hkv,), scales[1]) if per_head is None else per_head[1].cpu()
     want = ref.window_attention(b.q, b.kb, b.vb, b.qsl, b.lens, b.positions, b.tables, b.scale,
@@ -35,7 +40,8 @@ def check(pa, b, window, first, sinks=None, scales=(1.0, 1.0), per_head=None, ls
     pa.pa_window_attention(*b.args(), b.scale, sliding_window=window, first_tokens=first, sinks=sinks,
                            lse=b.lse if lse else None, **extra, **kw)
     assert pa.pa_device_status() == pa.PA_OK
-    y, bound = stored(want["out"], want["out_b"], b.out.dtype)
+    # v_bits: f16's rounding of V below its normal range (half its smallest step)
+    y, bound = stored(want["out"], want["out_b"] + v_bits, b.out.dtype)
     assert_within(b.out, y, bound, "out")
     if lse:
         assert_within(b.lse, want["lse"], want["lse_b"], "lse")
@@ -102,6 +108,30 @@ def test_long_chunk(pa):
     b = ref.Batch([(3000, 1500), (0, 700), (9000, 1), (2100, 1)], 8, 2, 128, seed=8)
     b.poison_unread(1024, 4)
     check(pa, b, 1024, 4)
+
+
+CHUNKS = [(300, 700), (0, 500), (1000, 1), (2000, 2), (40, 3), (900, 20), (7, 0), (0, 1)]
+
+
+@pytest.mark.parametrize("window,first", [(0, 0), (1, 1), (300, 4), (128, 130), (64, 0), (BIG, 7)])
+@pytest.mark.parametrize("H,Hkv", [(64, 8), (16, 16)])
+def test_many_chunks(pa, H, Hkv, window, first):
+    """Enough rows for the prefill kernel, with decoding sequences beside it."""
+    seqs = CHUNKS if H == 64 else [(c, 4 * n if n > 100 else n) for c, n in CHUNKS]
+    b = ref.Batch(seqs, H, Hkv, 128, seed=window % 91)
+    b.poison_unread(window, first)
+    sinks = torch.randn(H, device="cuda") if first == 4 else None
+    check(pa, b, window, first, sinks=sinks, v_bits=2.0 ** -25)
+
+
+def test_values_past_f16(pa):
+    """V values that f16 cannot hold: the items that meet them are done again.  (Values above 2^100 are
+    outside the call's domain: the sums before the division are fp32, weights up to 2^8 times V over all
+    keys, so 3e38 = 2^127.8 overflows there with the first such key.)"""
+    b = ref.Batch(CHUNKS, 64, 8, 128, seed=3)
+    b.vb.view(-1, 8, 128)[5::97, 3, 10] = 1e30
+    b.vb.view(-1, 8, 128)[7::89, 5, 100] = -1e6
+    check(pa, b, 200, 4)
 
 
 def test_no_window_is_causal_attention(pa):
