@@ -189,8 +189,7 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeParams p) {
   const int4 q = in ? __ldcg(&p.seqs[2 * cut.x]) : make_int4(0, 0, 0, 0);
   pdl_wait();
   pdl_launch_dependents();
-  // (one answer for the whole CTA; a window call behind the prefill kernel: nothing to do again)
-  if (__syncthreads_or(status_set(p.status) || (p.tc.plan && __ldcg(p.tc.plan + 3) == 0))) return;
+  if (__syncthreads_or(status_set(p.status))) return;  // (one answer for the whole CTA)
   if (!in || cut.w == 0) return;
   const bool same = from.x == cut.x && from.y == cut.y && from.z == cut.z;
   if (same && from.w > 0) return;  // a later cut of the item

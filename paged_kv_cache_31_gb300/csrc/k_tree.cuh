@@ -75,7 +75,7 @@ struct TreeWalk {
     if constexpr (WIN) {
       const int4 it = p.item_keys[w.y + at.z];
       tiles = it.z;
-      g.front = it.x;
+      g.front = p.front;
       g.gap = it.y;
     }
     const int t1 = last ? end.w : tiles;

@@ -178,8 +178,8 @@ struct Ctx {
 };
 
 // What the kernel is: tree attention by planned shares, by clusters (CL), or the attention behind a
-// window with first tokens, by planned shares (WIN).
-enum : int { kShares = 0, kClusters = 1, kWindow = 2 };
+// window with first tokens (WIN), by planned shares or of the items that the prefill kernel marked.
+enum : int { kShares = 0, kClusters = 1, kWindow = 2, kMarked = 3 };
 
 // The segments of a CTA: its share's, or the one it has in its cluster.
 template <int MODE>
@@ -187,6 +187,34 @@ struct Walk {
   TreeWalk<MODE == kWindow> w;
   __device__ __forceinline__ Walk(const Ctx& c, const TreeParams& p) : w(p, blockIdx.x) {}
   __device__ __forceinline__ bool next(const TreeParams& p, TreeSegment& g) { return w.next(p, g); }
+};
+// The items (of two row tiles, whole) that the prefill kernel marked, each for all kv heads.
+template <>
+struct Walk<kMarked> {
+  int at, end;
+  __device__ __forceinline__ Walk(const Ctx& c, const TreeParams& p)
+      : at(blockIdx.x), end(__ldcg(p.tc.plan + 3) * p.m.num_kv_heads) {}
+  __device__ __forceinline__ bool next(const TreeParams& p, TreeSegment& g) {
+    if (at >= end) return false;
+    const int item = __ldcg(p.tc.plan + p.tc.redo_list_off + at / p.m.num_kv_heads);
+    const int4 it = reinterpret_cast<const int4*>(p.tc.plan + p.tc.items_off)[item];
+    const int4 q = p.seqs[2 * it.x], w = p.seqs[2 * it.x + 1];
+    g.s = it.x;
+    g.kvh = at % p.m.num_kv_heads;
+    g.item = it.y;
+    g.row0 = it.y * p.rows_per_item;
+    g.rows = min(p.rows_per_item, w.z - g.row0);
+    g.qs = q.x;
+    g.nodes = q.y;
+    g.n = q.z - it.z * 16;
+    g.kv0 = g.t0 = 0;
+    g.t1 = (it.w + kBN - 1) / kBN;
+    g.slot = -1;
+    g.front = p.front;
+    g.gap = it.z;
+    at += gridDim.x;
+    return true;
+  }
 };
 template <>
 struct Walk<kClusters> {
@@ -304,7 +332,7 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
     const int blocks = (g.n + 15) / 16;
     const int b0 = g.kv0 / 16 + 8 * g.t0 + lane;
     auto entry = [&](int b) {  // of block b of the segment's keys
-      if (MODE == kWindow && b >= g.front) b += g.gap;
+      if (MODE >= kWindow && b >= g.front) b += g.gap;
       return row[b];
     };
     int next = lane < 8 && b0 < blocks ? entry(b0) : -1;
@@ -912,7 +940,7 @@ __device__ void cluster_merge(const Ctx& c, const TreeParams& p) {
 template <int D, bool FP8, int MODE>
 __device__ void softmax_role(const Ctx& c, const TreeParams& p, uint32_t tmem, uint32_t stall) {
   using S = Shape<D, FP8>;
-  constexpr bool CL = MODE == kClusters, WIN = MODE == kWindow;
+  constexpr bool CL = MODE == kClusters, WIN = MODE >= kWindow;
   const VarlenMeta& m = p.m;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 4;
   const int x = warp >> 2, quad = warp & 3;
@@ -1206,8 +1234,6 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     const bool off = (smem_u32(sm) & 1023u) != 0;
     if (off) record_error(p.status, PA_ECUDA);
     flags[0] = off || status_set(p.status) ? 1 : 0;
-    // (behind the prefill kernel: only where that left an item to do again)
-    if (MODE == kWindow && p.tc.plan && __ldcg(p.tc.plan + 3) == 0) flags[0] = 1;
   }
   if (CL && warp == 2) plan_own(p, own, threadIdx.x & 31);
   __syncthreads();

@@ -54,27 +54,19 @@ __device__ __forceinline__ int token_from(const int32_t* pos, int a, int b, int6
   return a;
 }
 
-// One block, for batches that go to the prefill kernel: its items, those of the most key tiles first (a
-// counting sort, eight buckets to an octave), and how many pairs of CTAs take them: the number that ends
-// both it and the decoding sequences beside it soonest.
-__device__ void plan_prefill(const TreeParams& p, int items, const int* s_base, int64_t* s_scratch) {
+// One block, for batches that go to the prefill kernel: its items, those of the most keys first (a counting
+// sort, sixteen buckets to an octave), and how many pairs of CTAs take them: the number that ends both it
+// and the decoding sequences beside it soonest.
+__device__ void plan_prefill(const TreeParams& p, int items, int64_t* s_scratch) {
   const VarlenMeta& m = p.m;
-  constexpr int kBuckets = 256;
+  constexpr int kBuckets = 512;
   __shared__ int s_at[kBuckets];
   __shared__ unsigned long long s_tiles, s_keys;
   __shared__ unsigned int s_best;
   const int tid = threadIdx.x;
   int* s_warp = reinterpret_cast<int*>(s_scratch);
-  auto bucket = [](int tiles) {  // 0: the most
-    return kBuckets - 1 - min((int)(__float_as_uint((float)tiles) >> 20) - (127 << 3), kBuckets - 1);
-  };
-  auto sequence_of = [&](int i) {
-    int lo = 0, hi = m.num_seqs;  // the last sequence whose first item is at most i: it has items
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((s_base ? s_base[mid] : p.seqs[2 * mid + 1].y) <= i) lo = mid; else hi = mid;
-    }
-    return lo;
+  auto bucket = [](int keys) {  // 0: the most (float bits from the exponent down to four of the fraction)
+    return kBuckets - 1 - ((int)(__float_as_uint((float)keys) >> 19) - (127 << 4));
   };
   if (tid < kBuckets) s_at[tid] = 0;
   if (tid == 0) {
@@ -84,11 +76,10 @@ __device__ void plan_prefill(const TreeParams& p, int items, const int* s_base, 
   __syncthreads();
   unsigned long long tiles = 0, keys = 0;
   for (int i = tid; i < items; i += kPlanThreads) {
-    const int s = sequence_of(i);
     const int4 k = p.item_keys[i];
-    if (p.seqs[2 * s + 1].z > kWindowDecodeRows) {
+    if (p.seqs[2 * k.x + 1].z > kWindowDecodeRows) {
       tiles += k.z;
-      atomicAdd(&s_at[bucket(k.z)], 1);
+      atomicAdd(&s_at[bucket(k.w)], 1);
     } else {
       keys += k.w;
     }
@@ -97,17 +88,15 @@ __device__ void plan_prefill(const TreeParams& p, int items, const int* s_base, 
   if (keys) atomicAdd(&s_keys, keys);
   __syncthreads();
   int total;
-  const int n = tid < kBuckets ? s_at[tid] : 0;
-  const int at = block_exclusive_scan(n, s_warp, &total);
+  const int at = block_exclusive_scan(tid < kBuckets ? s_at[tid] : 0, s_warp, &total);
   if (tid < kBuckets) s_at[tid] = at;
   __syncthreads();
   int4* list = reinterpret_cast<int4*>(p.tc.plan + p.tc.items_off);
   for (int i = tid; i < items; i += kPlanThreads) {
-    const int s = sequence_of(i);
-    if (p.seqs[2 * s + 1].z <= kWindowDecodeRows) continue;
-    const int4 k = p.item_keys[i];
-    const int to = atomicAdd(&s_at[bucket(k.z)], 1);
-    list[to] = make_int4(s, i - p.seqs[2 * s + 1].y, k.y, k.w);
+    const int4 k = p.item_keys[i], w = p.seqs[2 * k.x + 1];
+    if (w.z <= kWindowDecodeRows) continue;
+    const int to = atomicAdd(&s_at[bucket(k.w)], 1);
+    list[to] = make_int4(k.x, i - w.y, k.y, k.w);
     p.tc.plan[p.tc.redo_off + to] = 0;
   }
   // k pairs: a key tile of 256 rows takes a pair 1.1 us; decoding sequences stream at the memory's rate
@@ -154,7 +143,7 @@ __device__ void plan_weights(const TreeParams& p, int64_t* s_warp, int64_t* s_cu
         bad |= low < 0 || last < low || last >= n;
         const int end = min(max(last, 0), n - 1) / kWeightKeys + 1;
         const int lo = m.window > 0 ? max(min(low, n - 1) - m.window + 1, 0) / kWeightKeys : 0;
-        const int front = m.window > 0 ? min((p.first + kWeightKeys - 1) / kWeightKeys, end) : 0;
+        const int front = m.window > 0 ? min((int)(((int64_t)p.first + kWeightKeys - 1) / kWeightKeys), end) : 0;
         const int gap = max(lo - front, 0);
         mine = max(end - gap, 0);
         first = make_int4(0, 0, front, gap);
@@ -304,21 +293,27 @@ __global__ void __launch_bounds__(kPlanThreads) k_window_plan(const TreeParams p
       const Keys k = keys_from(p, a);
       const int end = min(max(b, a), q.z - 1) + 1 - k.gap * m.block_size;
       const int tiles = max(1, (end + p.key_tile - 1) / p.key_tile);
-      p.item_keys[i] = make_int4(k.front, k.gap, tiles, max(end, 1));
+      p.item_keys[i] = make_int4(lo, k.gap, tiles, max(end, 1));
       weight = (int64_t)tree_weight(p, rows) * tiles + kTreeItemWeight;
     }
+    if (p.tc.plan) continue;  // (no shares)
     int64_t total;
     const int64_t at = base + block_sum_scan(weight, s_warp, &total);
     if (i < items) p.item_cum[i] = at;
     base += total;
   }
-  if (tid == 0) p.item_cum[items] = base;
+  if (tid == 0 && !p.tc.plan) p.item_cum[items] = base;
   bad = __syncthreads_or(bad);  // (and the items' records can be read)
-  if (p.tc.plan) plan_prefill(p, bad ? 0 : (int)items, shared ? s_base : nullptr, s_warp);
   if (bad) {
     if (tid == 0) record_error(p.status, PA_EINVAL);
     for (int s = tid; s < m.num_seqs; s += kPlanThreads)
       p.seqs[2 * s] = p.seqs[2 * s + 1] = make_int4(0, 0, 0, 0);
+  }
+  if (p.tc.plan) {
+    plan_prefill(p, bad ? 0 : (int)items, s_warp);
+    return;
+  }
+  if (bad) {
     for (int c = tid; c <= p.grid; c += kPlanThreads) p.starts[c] = make_int4(m.num_seqs, 0, 0, 0);
     return;
   }

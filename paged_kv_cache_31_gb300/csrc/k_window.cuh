@@ -14,9 +14,8 @@ struct Keys {
 };
 __device__ __forceinline__ Keys keys_from(const TreeParams& p, int lowest) {
   const VarlenMeta& m = p.m;
-  const int front = (p.first + m.block_size - 1) / m.block_size;
   const int lo = m.window > 0 ? max(lowest - m.window + 1, 0) / m.block_size : 0;
-  return Keys{front, max(lo - front, 0)};
+  return Keys{p.front, max(lo - p.front, 0)};
 }
 
 // First token, tokens and length of sequence s; false (and no tokens) when they cannot be used.

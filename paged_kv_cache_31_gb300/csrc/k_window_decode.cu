@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
     const int low = min(max(m.positions[qs + row0 / G], 0), n - 1);
     const int high = min(max(m.positions[qs + (row0 + nrow - 1) / G], low), n - 1);
     // the tile's blocks, counted without the gap, and this CTA's run of them
-    const int front = (p.first + kBlk - 1) / kBlk;
+    const int front = p.front;
     const int gap = m.window > 0 ? max(max(low - m.window + 1, 0) / kBlk - front, 0) : 0;
     const int vn = n - gap * kBlk;
     const int nblk = (high - gap * kBlk) / kBlk + 1;

@@ -5,11 +5,11 @@
 namespace pa {
 namespace {
 
-template <int D, bool FP8>
+template <int D, bool FP8, int MODE = kWindow>
 cudaError_t launch_as(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       const TreeParams& p, uint64_t limit, uint32_t stall, cudaStream_t stream) {
   using S = Shape<D, FP8>;
-  auto kern = k_tree_tc<D, FP8, kWindow>;
+  auto kern = k_tree_tc<D, FP8, MODE>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
@@ -22,6 +22,7 @@ cudaError_t launch_as(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
 cudaError_t launch_window_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const TreeParams& p, bool fp8, uint64_t wait_limit, uint32_t stall,
                              cudaStream_t stream) {
+  if (p.tc.plan) return launch_as<128, false, kMarked>(tq, tk, tv, p, wait_limit, stall, stream);
   if (fp8) return launch_as<128, true>(tq, tk, tv, p, wait_limit, stall, stream);
   if (p.m.head_dim == 128) return launch_as<128, false>(tq, tk, tv, p, wait_limit, stall, stream);
   return launch_as<64, false>(tq, tk, tv, p, wait_limit, stall, stream);

@@ -157,6 +157,7 @@ pa_status attend(const Call& c) {
   m.k_scales = c.k_scales;
   m.v_scales = c.v_scales;
   p.first = c.window > 0 ? (int32_t)std::min<int64_t>(c.first, max_keys) : 0;
+  p.front = (int32_t)(((int64_t)p.first + c.block_size - 1) / c.block_size);
   p.scale = c.scale * c.k_scale;
   p.status = d->status;
   p.q_bf16 = c.q_dtype == PA_BF16;
@@ -292,7 +293,7 @@ pa_status attend(const Call& c) {
   } else if (launch_window_generic(p, c.kv_dtype, c.stream) != cudaSuccess) {
     return PA_ECUDA;
   }
-  if (launch_tree_merge(p, c.stream) != cudaSuccess) return PA_ECUDA;
+  if (!prefill && launch_tree_merge(p, c.stream) != cudaSuccess) return PA_ECUDA;
   if (!c.weighs) return PA_OK;
   if (p.w.grid > 0) return from_cuda(launch_weights_tc(tq, tk, p, fp8, limit, stall, c.stream));
   return from_cuda(launch_key_weights_generic(p, c.kv_dtype, c.stream));

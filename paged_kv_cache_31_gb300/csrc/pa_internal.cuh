@@ -618,13 +618,14 @@ struct TreeParams {
   int32_t cluster, items;
   // Attention behind a window with first tokens (k_window.cu): m.window counts behind positions, no
   // mask; seqs' second record is (items of a kv head, its first item's record, rows, 0).
-  int32_t first;     // positions that stay visible
+  int32_t first, front;  // positions that stay visible, and the blocks they lie in
   int32_t narrow, ordered;  // batches of decoding tokens: the CTAs' shape, longest sequences first
-  int4* item_keys;  // [items of all sequences] (front blocks, gap in blocks behind them, key tiles, 0)
+  int4* item_keys;  // [items of all sequences] (sequence, gap in blocks behind the front ones, key tiles, end of the
+                    // keys without it)
   int64_t* item_cum;  // [items + 1] weight before the item, over all items of a kv head in order
   // Large batches of prompt chunks: sequences of more than kWindowDecodeRows rows go to the prefill kernel
   // (k_prefill_tc.cu, plan as for that kernel: header words, items, marks, list of marked items), the
-  // others to k_window_decode; this kernel runs again over the batch when an item was marked.
+  // others to k_window_decode; the tree kernel does the items again that were marked.
   struct {
     int32_t* plan;  // null: no such batch
     int64_t items_off, redo_off, redo_list_off;  // words
