@@ -14,9 +14,11 @@
 // the pieces of a cut item leave partial sums, which k_weights_join adds in order.
 //
 // Roles.  warp 0: TMA of K (two stages of 256 keys) and Q (a ring of two row tiles); warp 1:
-// tensor-memory owner, issues S^T; warp 2: the rows' log-sum-exps and positions into a ring of four;
-// warps 4..7 and 8..11: 128 keys each, exponentials and sums, from two S^T buffers each; warps 12..15
-// (e4m3 pools): widen K to bf16, exactly, once an item.
+// tensor-memory owner, issues S^T; warps 2 and 3: the rows' log-sum-exps and positions into a ring of four;
+// warps 4..19: exponentials and sums, a warpgroup for 128 keys and 64 rows of a row tile each, from two S^T
+// buffers for each 128 keys (two warpgroups, of all rows, left the schedulers idle half of the time: 312 us
+// for a prompt of 8191 tokens, 8 x 4 heads); warps 20..23 (e4m3 pools): widen K to bf16, exactly, once an
+// item.
 //
 // What bounds it: a row tile's 32768 exponentials (2^x on the SFU and two packed fp32 instructions for
 // a pair) beside 1230 cycles of products.
@@ -38,7 +40,7 @@ struct Shape {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * 128 * 128;  // 128 rows of 16-bit values
   static constexpr int kCodes = 128 * 128;           // 128 keys of codes
-  static constexpr int kThreads = FP8 ? 512 : 384;
+  static constexpr int kThreads = FP8 ? 768 : 640;
   // K as it is multiplied: two stages of 256 keys (bf16, as the 5-D boxes write it), or one of widened
   // ones (dim half by dim half)
   static constexpr int kWide = FP8 ? 1 : 2;
@@ -49,7 +51,8 @@ struct Shape {
   static constexpr int kOffQ = kOffCodes + (FP8 ? 4 * kCodes : 0);
   static constexpr int kOffRow = kOffQ + 2 * kTile;  // [kLse][2][128]: -lse in log2 units, positions
   static constexpr int kOffInfo = kOffRow + kLse * 2 * kRows * 4;  // [kLse] int4
-  static constexpr int kOffBar = kOffInfo + kLse * 16;
+  static constexpr int kOffHalf = kOffInfo + kLse * 16;  // [key half][128]: sums of the second row halves
+  static constexpr int kOffBar = kOffHalf + 2 * 128 * 4;
   static constexpr int kOffMisc = kOffBar + 32 * 8;
   static constexpr int kSmem = kOffMisc + 16;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -66,7 +69,9 @@ enum : int {
   B_SFREE = B_SFULL + 4,
   B_LFULL = B_SFREE + 4,
   B_LFREE = B_LFULL + kLse,
-  B_FIN = B_LFREE + kLse,
+  B_HALF = B_LFREE + kLse,  // per key half: the second row half's sums are there
+  B_TAKEN = B_HALF + 2,     // they have been added
+  B_FIN = B_TAKEN + 2,
   B_NEVER = B_FIN + 1,  // nothing arrives on it (the debug_stall test hook)
   kNumBars = B_NEVER + 1
 };
@@ -291,53 +296,74 @@ __device__ void issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
 }
 
 // The rows' numbers: for column r of a row tile -lse in log2 units and its position (-1: no row), and
-// (lowest position, highest, rows) of the tile.
-__device__ void row_loader(const Ctx& c, const TreeParams& p, float* nl, int* pos, int4* info) {
+// (lowest position, highest, rows) of the tile.  Two warps take the tiles in turn, and a warp requests a
+// tile's before it stores those of the one before: one warp without either was what bound this kernel (a
+// load's latency to each row tile: 1.4 us a tile of 0.6 us).
+__device__ void row_loader(const Ctx& c, const TreeParams& p, int which, float* nl, int* pos, int4* info) {
   const VarlenMeta& m = p.m;
   const int lane = threadIdx.x & 31;
-  Ring<kLse> l;
-  uint32_t use = 0;
+  float a[4];
+  int b[4], cols = 0;
+  uint32_t tile = 0, held = 0;  // row tiles so far; the one whose numbers are held
+  bool have = false;
+  auto store = [&]() {
+    const uint32_t st = held % kLse, turn = held / kLse;
+    int lo = INT_MAX, hi = -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo = min(lo, b[i] >= 0 ? b[i] : INT_MAX);
+      hi = max(hi, b[i]);
+    }
+    lo = __reduce_min_sync(kFull, lo);
+    hi = __reduce_max_sync(kFull, hi);
+    if (turn > 0 && !wait_all(c, B_LFREE + st, (turn & 1) ^ 1)) return false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int col = lane + 32 * i;
+      // (a row without a finite score, lse -inf, gives no weight)
+      nl[st * 2 * kRows + col] = a[i] == -INFINITY ? -INFINITY : -a[i] * kLog2e;
+      pos[st * 2 * kRows + col] = b[i];
+    }
+    if (lane == 0) info[st] = make_int4(lo, hi, cols, 0);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.bar + B_LFULL + st);
+    return true;
+  };
   Walk walk(p, blockIdx.x);
   Piece g;
   while (walk.next(p, g)) {
-    for (int r = g.r0; r < g.r1; ++r, ++use) {
-      float a[4];
-      int b[4], lo = INT_MAX, hi = -1;
+    for (int r = g.r0; r < g.r1; ++r, ++tile) {
+      if ((int)(tile & 1) != which) continue;
+      float na[4];
+      int nb[4];
       const int first = r * p.tile_tokens;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int col = lane + 32 * i, t = first + col / m.group;
-        const bool have = col < p.tile_rows && t < g.tokens;
-        a[i] = have ? m.lse[(int64_t)(g.kvh * m.group + col % m.group) * m.num_tokens + g.qs + t] : 0.f;
-        b[i] = have ? m.positions[g.qs + t] : -1;
-        lo = min(lo, have ? b[i] : INT_MAX);
-        hi = max(hi, b[i]);
+        const bool in = col < p.tile_rows && t < g.tokens;
+        na[i] = in ? m.lse[(int64_t)(g.kvh * m.group + col % m.group) * m.num_tokens + g.qs + t] : 0.f;
+        nb[i] = in ? m.positions[g.qs + t] : -1;
       }
-      lo = __reduce_min_sync(kFull, lo);
-      hi = __reduce_max_sync(kFull, hi);
-      if (use >= kLse && !wait_all(c, B_LFREE + l.st, l.par ^ 1)) return;
+      if (have && !store()) return;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int col = lane + 32 * i;
-        // (a row without a finite score, lse -inf, gives no weight)
-        nl[l.st * 2 * kRows + col] = a[i] == -INFINITY ? -INFINITY : -a[i] * kLog2e;
-        pos[l.st * 2 * kRows + col] = b[i];
+        a[i] = na[i];
+        b[i] = nb[i];
       }
-      if (lane == 0)
-        info[l.st] = make_int4(lo, hi, min(p.tile_rows, (g.tokens - first) * m.group), 0);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(c.bar + B_LFULL + l.st);
-      l.next();
+      cols = min(p.tile_rows, (g.tokens - first) * m.group);
+      held = tile;
+      have = true;
     }
   }
+  if (have) store();
 }
 
-// Warps 12 to 15: codes to bf16 (exact), a quarter of the keys each; 128 keys at a time as in
+// Warps 20 to 23: codes to bf16 (exact), a quarter of the keys each; 128 keys at a time as in
 // k_tree_tc.cuh, dim half by dim half.
 template <int D>
 __device__ void widener(const Ctx& c, const TreeParams& p) {
   using S = Shape<D, true>;
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 12;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 20;
   Ring<2> k;
   Ring<1> wd;
   uint32_t use = 0;
@@ -382,15 +408,16 @@ __device__ void widener(const Ctx& c, const TreeParams& p) {
   }
 }
 
-// A warpgroup's 128 keys: thread = key.
+// A warpgroup's 128 keys and half of the rows: thread = key.
 template <int D, bool FP8>
 __device__ void summer(const Ctx& c, const TreeParams& p, uint32_t tmem, uint32_t stall, const float* nl,
-                       const int* pos, const int4* info) {
+                       const int* pos, const int4* info, float* sums) {
   const VarlenMeta& m = p.m;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 4, x = warp >> 2, quad = warp & 3;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 4, x = warp >> 3, quad = warp & 3;
+  const int half = (warp >> 2) & 1;  // of a row tile's columns
   const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + 2 * x * kRows;
   Ring<kLse> l;
-  uint32_t use = 0;
+  uint32_t use = 0, pieces = 0;  // row tiles and pieces of this key half so far
   Walk walk(p, blockIdx.x);
   Piece g;
   while (walk.next(p, g)) {
@@ -411,11 +438,11 @@ __device__ void summer(const Ctx& c, const TreeParams& p, uint32_t tmem, uint32_
         const float* tl = nl + l.st * 2 * kRows;
         const int* tp = pos + l.st * 2 * kRows;
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 2 * half; q < 2 * half + 2; ++q) {
           uint32_t v[32];
           tmem_ld32(lanes + buf * kRows + 32 * q, v);
           tmem_wait_ld(v);
-          if (q == 3) {  // the buffer has been read
+          if (q & 1) {  // this half of the buffer has been read
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(c.bar + B_SFREE + 2 * x + buf);
@@ -451,8 +478,25 @@ __device__ void summer(const Ctx& c, const TreeParams& p, uint32_t tmem, uint32_
     float a, b, d, e;
     f2_unpack(sum[0], a, b);
     f2_unpack(sum[1], d, e);
-    const float total = (a + b) + (d + e);
-    if (mine && key < g.key0 + g.keys && !*c.abort) {
+    float total = (a + b) + (d + e);
+    if (!mine) continue;
+    // the second half's sums go to the first
+    float* other = sums + 128 * x + 32 * quad + lane;
+    if (half) {
+      if (pieces >= 1 && !wait_all(c, B_TAKEN + x, (pieces & 1) ^ 1)) return;
+      *other = total;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c.bar + B_HALF + x);
+      ++pieces;
+      continue;
+    }
+    if (!wait_all(c, B_HALF + x, pieces & 1)) return;
+    const float add = *other;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.bar + B_TAKEN + x);
+    ++pieces;
+    total += add;
+    if (key < g.key0 + g.keys && !*c.abort) {
       if (g.slot >= 0) {
         p.w.part[(int64_t)g.slot * kKeys + key - g.key0] = total;
       } else if (total != 0.f) {
@@ -479,8 +523,9 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
       if ((FP8 && i >= B_KEMPTY && i < B_KEMPTY + 2) || i == B_WIDE) n = 4;
-      if (i >= B_SFREE && i < B_SFREE + 4) n = 4;
-      if (i >= B_LFREE && i < B_LFREE + kLse) n = 8;
+      if (i >= B_SFREE && i < B_SFREE + 4) n = 8;
+      if (i >= B_LFREE && i < B_LFREE + kLse) n = 16;
+      if (i >= B_HALF && i < B_TAKEN + 2) n = 4;
       mbar_init(bar + i, n);
     }
     prefetch_tmap(&tq);
@@ -520,12 +565,12 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
       commit(bar + B_FIN);
       if ((threadIdx.x & 31) == 0) mbar_wait(bar + B_FIN, 0, 1000000000ull);
       __syncwarp();
-    } else if (warp == 2) {
-      row_loader(c, p, nl, pos, info);
-    } else if (warp >= 12) {
+    } else if (warp == 2 || warp == 3) {
+      row_loader(c, p, warp - 2, nl, pos, info);
+    } else if (warp >= 20) {
       if constexpr (FP8) widener<D>(c, p);
     } else if (warp >= 4) {
-      summer<D, FP8>(c, p, tmem, stall, nl, pos, info);
+      summer<D, FP8>(c, p, tmem, stall, nl, pos, info, reinterpret_cast<float*>(sm + S::kOffHalf));
     }
   }
   tc_fence_before();
