@@ -40,12 +40,14 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBlk = 16;
 
-// NARROW: half as many warps and four CTAs to an SM
-template <int D, bool FP8, bool NARROW>
+// Shapes: two CTAs to an SM; kNarrow: half as many warps, four CTAs; kBroad (bf16): twice as many, one.
+enum : int { kPlain = 0, kNarrow = 1, kBroad = 2 };
+template <int D, bool FP8, int KIND>
 struct Shape {
-  static constexpr int NW = (FP8 ? 8 : 4) / (NARROW ? 2 : 1);  // warps
-  static constexpr int kPerSm = NARROW ? 4 : 2;
-  static constexpr int NS = 3;             // stages of a warp's ring
+  static constexpr bool NARROW = KIND == kNarrow;
+  static constexpr int NW = NARROW ? (FP8 ? 4 : 2) : FP8 || KIND == kBroad ? 8 : 4;  // warps
+  static constexpr int kPerSm = NARROW ? 4 : KIND == kBroad ? 1 : 2;
+  static constexpr int NS = KIND == kBroad ? 2 : 3;  // stages of a warp's ring
   static constexpr int TR = FP8 ? 8 : 16;  // query rows of a tile
   static constexpr int kHalves = FP8 ? 1 : D / 64;
   static constexpr int kTile = kHalves * kBlk * 128;  // a block's K (or V) of one kv head
@@ -53,12 +55,12 @@ struct Shape {
   static constexpr int kNT = D / 8, kKS = D / 16;
   static constexpr int kRing = NW * NS * kStage;
   // scores of a CTA's keys, and the states that are joined (in the ring's place)
-  static constexpr int kScores = NARROW ? 0 : 15360;
+  static constexpr int kScores = NARROW ? 0 : 14336;
   static constexpr int kLd = D + 4;
   static constexpr int kOffState = NW * 16 * kLd * 4;  // behind the warps' O: the CTA's
   static_assert(kOffState + 16 * kLd * 4 <= kRing, "states lie in the ring");
   static constexpr int kOffSmall = kRing;  // struct Small
-  static constexpr int kOffScores = kOffSmall + 1664;
+  static constexpr int kOffScores = kOffSmall + 2816;
   static constexpr int smem(bool weigh) { return kOffScores + (weigh ? kScores : 0); }
   static_assert(kPerSm * (1024 + kOffScores + kScores) <= 228 * 1024, "CTAs of an SM");
 };
@@ -80,12 +82,17 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
-  asm volatile(
-      "barrier.cluster.arrive.release.aligned;\n\t"
-      "barrier.cluster.wait.acquire.aligned;" ::
-          : "memory");
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
 }
 __device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
   uint32_t a;
@@ -149,14 +156,16 @@ struct Small {
   float2 ml[16];  // the CTA's state, read by its cluster
   int seq;        // the sequence that is this CTA's
   float lse[16], norm[16];
+  float factor[16][16];  // of each CTA's part of a row
   int fail;
 };
 
-template <int D, bool FP8, bool WEIGH, bool NARROW>
-__global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, NARROW>::kPerSm)
+template <int D, bool FP8, bool WEIGH, int KIND>
+__global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KIND>::kPerSm)
     k_window_decode(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const TreeParams p, uint64_t limit, uint32_t stall) {
-  using S = Shape<D, FP8, NARROW>;
+  using S = Shape<D, FP8, KIND>;
+  constexpr bool NARROW = S::NARROW;
   constexpr int NW = S::NW, NS = S::NS, TR = S::TR, LD = S::kLd;
   extern __shared__ __align__(1024) uint8_t ring[];
   using Sm = Small<NW, NS>;
@@ -168,6 +177,21 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
   const VarlenMeta& m = p.m;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = p.cluster, rank = C > 1 ? (int)cluster_rank() : 0;
+  const int unit = blockIdx.x / C, kvh = unit % m.num_kv_heads;
+  const int H = m.num_heads, G = m.group;
+  int s = unit / m.num_kv_heads;
+  // (the kernel in front lets this one start once it has waited for all work before it)
+  int qs = 0, qe = 0, n = 0, guess = 0;
+  auto numbers = [&]() {
+    qs = m.query_start_loc[s];
+    qe = m.query_start_loc[s + 1];
+    n = m.seq_lens[s];
+  };
+  if (!p.ordered) {
+    numbers();
+    // (mostly token s is sequence s's: its position is there when that is known)
+    guess = m.positions[min((int64_t)s, m.num_tokens - 1)];
+  }
   if (tid <= NW * NS) mbar_init(&full[tid], 1);
   if (tid == 0) {
     prefetch_tmap(&tk);
@@ -178,11 +202,7 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
   }
   fence_mbar_init();
   __syncthreads();
-  // (the kernel in front lets this one start once it has waited for all work before it)
   bool waited = false;
-  const int unit = blockIdx.x / C, kvh = unit % m.num_kv_heads;
-  const int H = m.num_heads, G = m.group;
-  int s = unit / m.num_kv_heads;
   if (p.ordered) {
     // more units than are resident at once: those with the most keys first (the s-th longest sequence)
     int* keys = reinterpret_cast<int*>(ring);
@@ -200,8 +220,8 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
     s = sh.seq;
     fence_proxy_async_smem();
     __syncthreads();  // (the ring is free)
+    numbers();
   }
-  const int qs = m.query_start_loc[s], qe = m.query_start_loc[s + 1], n = m.seq_lens[s];
   // numbers that cannot be used as indices: no rows (the check records the error)
   const bool usable = qs >= 0 && qe >= qs && (int64_t)qe <= m.num_tokens && n >= 1 &&
                       ((int64_t)n + kBlk - 1) / kBlk <= m.max_blocks &&
@@ -217,8 +237,35 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
   const uint64_t policy = evict_first();
   for (int row0 = 0; row0 < rows; row0 += TR) {
     const int nrow = min(TR, rows - row0);
-    const int low = min(max(m.positions[qs + row0 / G], 0), n - 1);
-    const int high = min(max(m.positions[qs + (row0 + nrow - 1) / G], low), n - 1);
+    // q's rows are requested first, their values are used last
+    uint32_t qa[S::kKS][4];
+    {
+      const int g = lane >> 2, c = lane & 3;
+      const int r0 = min(g, nrow - 1) + row0, r1 = min(g + 8, nrow - 1) + row0;
+      const uint32_t* q0 = reinterpret_cast<const uint32_t*>(
+          static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)(qs + r0 / G) * H + kvh * G + r0 % G) * D);
+      const uint32_t* q1 = reinterpret_cast<const uint32_t*>(
+          static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)(qs + r1 / G) * H + kvh * G + r1 % G) * D);
+      const bool v0 = g < nrow, v1 = g + 8 < nrow;
+#pragma unroll
+      for (int kk = 0; kk < S::kKS; ++kk) {
+        if constexpr (FP8) {  // dims 32c + 4kk + {0, 1} and {2, 3} of row g (the permuted order)
+          const uint2 w = v0 ? *reinterpret_cast<const uint2*>(q0 + 16 * c + 2 * kk) : make_uint2(0u, 0u);
+          qa[kk][0] = w.x;
+          qa[kk][2] = w.y;
+        } else {
+          qa[kk][0] = v0 ? q0[kk * 8 + c] : 0u;
+          qa[kk][1] = v1 ? q1[kk * 8 + c] : 0u;
+          qa[kk][2] = v0 ? q0[kk * 8 + 4 + c] : 0u;
+          qa[kk][3] = v1 ? q1[kk * 8 + 4 + c] : 0u;
+        }
+      }
+    }
+    auto position = [&](int t) {
+      return min(max(!p.ordered && qs + t == s ? guess : m.positions[qs + t], 0), n - 1);
+    };
+    const int low = position(row0 / G);
+    const int high = max(position((row0 + nrow - 1) / G), low);
     // the tile's blocks, counted without the gap, and this CTA's run of them
     const int front = p.front;
     const int gap = m.window > 0 ? max(max(low - m.window + 1, 0) / kBlk - front, 0) : 0;
@@ -229,7 +276,7 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
     const int mine = count > warp ? (count - warp + NW - 1) / NW : 0;  // blocks run0 + warp + NW x
     auto pos_of = [&](int r) {  // counted without the gap; -1: no row
       const int R = row0 + r;
-      return r < nrow ? min(max(m.positions[qs + R / G], 0), n - 1) - gap * kBlk : -1;
+      return r < nrow ? position(R / G) - gap * kBlk : -1;
     };
 
     int win = -1, ids = 0;
@@ -278,58 +325,35 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
     float sk[2];
     sk[0] = sk[1] = head_scale(m.k_scales, kvh, sl);
     // ---- q fragments and the rows' visible keys
-    uint32_t qa[S::kKS][4];
     int pos[2], lo[2];  // of this lane's rows: bf16 lane / 4 (+ 8), e4m3 2 (lane % 4) (+ 1)
-    {
-      const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = FP8 ? 2 * c + i : g + 8 * i;
-        pos[i] = pos_of(r);
-        lo[i] = m.window > 0 ? max(pos[i] - m.window, -1) + 1 : 0;
-      }
-      const int r0 = min(g, nrow - 1) + row0, r1 = min(g + 8, nrow - 1) + row0;
-      const uint32_t* q0 = reinterpret_cast<const uint32_t*>(
-          static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)(qs + r0 / G) * H + kvh * G + r0 % G) * D);
-      const uint32_t* q1 = reinterpret_cast<const uint32_t*>(
-          static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)(qs + r1 / G) * H + kvh * G + r1 % G) * D);
-      const bool v0 = g < nrow, v1 = g + 8 < nrow;
-      if constexpr (FP8) {
-        // dims 32c + 4kk + {0, 1} and {2, 3} of row g (the permuted order), as f16 with a power of two a
-        // row that brings its largest element to [2^14, 2^15): exact down to 2^-28 of that.  An infinity
-        // makes the whole row NaN.
-        uint2 w[8];
-        float big = 0.f;
+    for (int i = 0; i < 2; ++i) {
+      pos[i] = pos_of(FP8 ? 2 * (lane & 3) + i : (lane >> 2) + 8 * i);
+      lo[i] = m.window > 0 ? max(pos[i] - m.window, -1) + 1 : 0;
+    }
+    if constexpr (FP8) {
+      // f16 with a power of two a row that brings its largest element to [2^14, 2^15): exact down to
+      // 2^-28 of that.  An infinity makes the whole row NaN.
+      float big = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          w[kk] = v0 ? *reinterpret_cast<const uint2*>(q0 + 16 * c + 2 * kk) : make_uint2(0u, 0u);
-          big = fmaxf(big, fmaxf(fmaxf(fabsf(__uint_as_float(w[kk].x << 16)),
-                                       fabsf(__uint_as_float(w[kk].x & 0xffff0000u))),
-                                 fmaxf(fabsf(__uint_as_float(w[kk].y << 16)),
-                                       fabsf(__uint_as_float(w[kk].y & 0xffff0000u)))));
-        }
-        big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
-        const int up = min(max(141 - (int)(__float_as_uint(big) >> 23), -113), 120);
-        const float f = big < INFINITY ? __uint_as_float((uint32_t)(127 + up) << 23) : NAN;
+      for (int kk = 0; kk < 8; ++kk)
+        big = fmaxf(big, fmaxf(fmaxf(fabsf(__uint_as_float(qa[kk][0] << 16)),
+                                     fabsf(__uint_as_float(qa[kk][0] & 0xffff0000u))),
+                               fmaxf(fabsf(__uint_as_float(qa[kk][2] << 16)),
+                                     fabsf(__uint_as_float(qa[kk][2] & 0xffff0000u)))));
+      big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
+      const int up = min(max(141 - (int)(__float_as_uint(big) >> 23), -113), 120);
+      const float f = big < INFINITY ? __uint_as_float((uint32_t)(127 + up) << 23) : NAN;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          qa[kk][0] = pack_f16x2(__uint_as_float(w[kk].x << 16) * f, __uint_as_float(w[kk].x & 0xffff0000u) * f);
-          qa[kk][2] = pack_f16x2(__uint_as_float(w[kk].y << 16) * f, __uint_as_float(w[kk].y & 0xffff0000u) * f);
-        }
+      for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          sk[e] *= __uint_as_float((uint32_t)(127 - __shfl_sync(kFull, up, (2 * c + e) * 4)) << 23);
-      }
+        for (int i = 0; i < 4; i += 2)
+          qa[kk][i] = pack_f16x2(__uint_as_float(qa[kk][i] << 16) * f,
+                                 __uint_as_float(qa[kk][i] & 0xffff0000u) * f);
 #pragma unroll
-      for (int kk = 0; kk < S::kKS; ++kk) {
-        if constexpr (!FP8) {
-          qa[kk][0] = v0 ? q0[kk * 8 + c] : 0u;
-          qa[kk][1] = v1 ? q1[kk * 8 + c] : 0u;
-          qa[kk][2] = v0 ? q0[kk * 8 + 4 + c] : 0u;
-          qa[kk][3] = v1 ? q1[kk * 8 + 4 + c] : 0u;
-        }
-      }
+      for (int e = 0; e < 2; ++e)
+        sk[e] *= __uint_as_float((uint32_t)(127 - __shfl_sync(kFull, up, (2 * (lane & 3) + e) * 4)) << 23);
     }
     // keys that every row sees: [.., all_hi), and from all_lo on (the first tokens apart)
     const int all_hi = low - gap * kBlk + 1;
@@ -662,23 +686,30 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
       fail = lane < C && peer_u32(peer(&sh.fail, lane)) != 0;
       fail = __any_sync(kFull, fail);
     }
-    if (warp == 0 && lane < nrow) {
-      float M = -INFINITY;
-      for (int k = 0; k < C; ++k) M = fmaxf(M, C > 1 ? peer_f2(peer(&sh.ml[lane], k)).x : sh.ml[lane].x);
+    // a warp to a row, a lane to a CTA: all states of a row are requested at once
+    for (int r = warp; r < nrow; r += NW) {
+      const float2 st = lane >= C ? make_float2(-INFINITY, 0.f)
+                        : C > 1   ? peer_f2(peer(&sh.ml[r], lane))
+                                  : sh.ml[r];
+      float M = st.x;
+#pragma unroll
+      for (int k = 8; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, k));
       const float base = M == -INFINITY ? 0.f : M;
-      float L = 0.f;
-      for (int k = 0; k < C; ++k) {
-        const float2 t = C > 1 ? peer_f2(peer(&sh.ml[lane], k)) : sh.ml[lane];
-        L += exp2f(t.x - base) * t.y;
+      const float f = exp2f(st.x - base);
+      float L = f * st.y;
+#pragma unroll
+      for (int k = 8; k > 0; k >>= 1) L += __shfl_xor_sync(kFull, L, k);
+      if (lane < 16) sh.factor[r][lane] = f;
+      if (lane == 0) {
+        const int R = row0 + r, t = qs + R / G, h = kvh * G + R % G;
+        // tree_finish takes the sink into the sum; the log-sum-exp with it, in log2 units, is the weights'
+        const float sink = m.sinks ? m.sinks[h] * kLog2e : -INFINITY;
+        float M2 = fmaxf(M, sink);
+        if (M2 == -INFINITY) M2 = 0.f;
+        const float total = L * exp2f(M - M2) + exp2f(sink - M2);
+        sh.lse[r] = L == 0.f ? INFINITY : M2 + log2f(total);
+        sh.norm[r] = tree_finish(p, kvh, h, t, M, L, rank == 0 && !fail);
       }
-      const int R = row0 + lane, t = qs + R / G, h = kvh * G + R % G;
-      // tree_finish takes the sink into the sum; the log-sum-exp with it, in log2 units, is the weights'
-      const float sink = m.sinks ? m.sinks[h] * kLog2e : -INFINITY;
-      float M2 = fmaxf(M, sink);
-      if (M2 == -INFINITY) M2 = 0.f;
-      const float total = L * exp2f(M - M2) + exp2f(sink - M2);
-      sh.lse[lane] = L == 0.f ? INFINITY : M2 + log2f(total);
-      sh.norm[lane] = tree_finish(p, kvh, h, t, M, L, rank == 0 && !fail);
     }
     __syncthreads();
     if (!fail) {
@@ -687,17 +718,19 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
         const int r = i / (D / 4), d = i % (D / 4) * 4;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         if (C > 1) {
-          float M = -INFINITY;
-          for (int k = 0; k < C; ++k) M = fmaxf(M, peer_f2(peer(&sh.ml[r], k)).x);
-          const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-          for (int k = 0; k < C; ++k) {
-            const float f = exp2f(peer_f2(peer(&sh.ml[r], k)).x - base);
-            const float4 v = peer_f4(peer(state + r * LD + d, k));
-            a.x += f * v.x;
-            a.y += f * v.y;
-            a.z += f * v.z;
-            a.w += f * v.w;
+          for (int k0 = 0; k0 < C; k0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              v[k] = k0 + k < C ? peer_f4(peer(state + r * LD + d, k0 + k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float f = sh.factor[r][k0 + k];
+              a.x += f * v[k].x;
+              a.y += f * v[k].y;
+              a.z += f * v[k].z;
+              a.w += f * v[k].w;
+            }
           }
         } else {
           a = *reinterpret_cast<const float4*>(state + r * LD + d);
@@ -709,6 +742,10 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
             make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
       }
     }
+    // the states have been read
+    fence_proxy_async_smem();
+    if (C > 1) cluster_arrive();
+    bool reused = false;  // the ring: every CTA of the cluster has read the states
     if constexpr (WEIGH) {
       float* w = p.key_weights + ((int64_t)s * m.num_kv_heads + kvh) * p.weights_len;
       auto real = [&](int key) { return key >= front * kBlk ? key + gap * kBlk : key; };
@@ -761,8 +798,8 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
         }
       if (most > ld / kBlk) {  // (one answer for the cluster)
         // the blocks whose scores did not fit: K once more
-        fence_proxy_async_smem();
-        if (C > 1) cluster_sync(); else __syncthreads();  // (the states in the ring have been read)
+        if (C > 1) cluster_wait(); else __syncthreads();  // (the states in the ring have been read)
+        reused = true;
         const int x0 = kept > warp ? (kept - warp + NW - 1) / NW : 0;  // this warp's first
         int sent = x0;
         for (; sent < min(mine, x0 + NS); ++sent) issue(sent, ring_pos + sent - x0, false);
@@ -824,9 +861,12 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
         ring_pos += sent - x0;
       }
     }
-    // the states have been read: the ring, or the CTA, may go
-    fence_proxy_async_smem();
-    if (C > 1) cluster_sync(); else __syncthreads();
+    // the ring, or the CTA, may go when all have read
+    if (reused)
+      fence_proxy_async_smem();
+    else if (C > 1)
+      cluster_wait();
+    __syncthreads();
   }
   if (!waited) {
     // a sequence without rows; beside the prefill kernel one CTA stays for it, so that what follows on
@@ -836,11 +876,11 @@ __global__ void __launch_bounds__(Shape<D, FP8, NARROW>::NW * 32, Shape<D, FP8, 
   }
 }
 
-template <int D, bool FP8, bool WEIGH, bool NARROW>
+template <int D, bool FP8, bool WEIGH, int KIND>
 cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, uint64_t limit,
                       uint32_t stall, cudaStream_t stream) {
-  using S = Shape<D, FP8, NARROW>;
-  auto kern = k_window_decode<D, FP8, WEIGH, NARROW>;
+  using S = Shape<D, FP8, KIND>;
+  auto kern = k_window_decode<D, FP8, WEIGH, KIND>;
   const int smem = (int)S::smem(WEIGH);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess && p.cluster > 8)
@@ -864,11 +904,16 @@ cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const TreePa
 template <int D, bool FP8>
 cudaError_t launch_sum(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, uint64_t limit,
                        uint32_t stall, cudaStream_t stream) {
-  if (p.narrow)
-    return p.key_weights ? launch_as<D, FP8, true, true>(tk, tv, p, limit, stall, stream)
-                         : launch_as<D, FP8, false, true>(tk, tv, p, limit, stall, stream);
-  return p.key_weights ? launch_as<D, FP8, true, false>(tk, tv, p, limit, stall, stream)
-                       : launch_as<D, FP8, false, false>(tk, tv, p, limit, stall, stream);
+  const bool w = p.key_weights != nullptr;
+  if (p.shape == kNarrow)
+    return w ? launch_as<D, FP8, true, kNarrow>(tk, tv, p, limit, stall, stream)
+             : launch_as<D, FP8, false, kNarrow>(tk, tv, p, limit, stall, stream);
+  if constexpr (!FP8)
+    if (p.shape == kBroad)
+      return w ? launch_as<D, FP8, true, kBroad>(tk, tv, p, limit, stall, stream)
+               : launch_as<D, FP8, false, kBroad>(tk, tv, p, limit, stall, stream);
+  return w ? launch_as<D, FP8, true, kPlain>(tk, tv, p, limit, stall, stream)
+           : launch_as<D, FP8, false, kPlain>(tk, tv, p, limit, stall, stream);
 }
 
 }  // namespace

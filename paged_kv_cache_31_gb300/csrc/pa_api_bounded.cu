@@ -55,28 +55,31 @@ size_t workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads, i
 // whether the longest sequences come first.  keys: the most that a token can see (of the table's width
 // and the window; the lengths are on the device).
 struct DecodeForm {
-  int32_t cluster;
-  bool narrow, ordered;
+  int32_t cluster, shape;  // 1: narrow CTAs, 2: broad ones
+  bool ordered;
 };
-// More CTAs to a unit read its keys sooner, but each costs some 5 us of latencies (metadata, first keys,
+// More CTAs to a unit read its keys sooner, but each costs some 4 us of latencies (metadata, first keys,
 // joins) in which it reads nothing.  Measured (us in a graph, bf16, 8 kv heads of 4 heads, lengths up to
-// the given one; CTAs to a unit): 1 sequence of 4096 1: 50, 4: 19.2, 16: 13.6; 8 sequences of 1024 1: 17.4,
-// 4: 11.4, 8: 18.1; 16 of 256 1: 9.4, 2: 10.5, 4: 16.6; 24 of 4096 1: 58, 2: 54, 4: 63; 16 of 16384
-// 1: 186, 4: 112, 8: 127; 48 of 16384 1: 319, 2: 288, 4: 312; 64 of 4096 1: 105, 2: 126.  Clusters of 16
-// only where they are all resident (2 sequences of 4096 8: 14.9, 16: 20.8).
+// the given one; CTAs to a unit): 1 sequence of 2048 1: 27.8, 4: 12.4, 8: 9.4; of 16384 8: 28.8, 16: 20.7;
+// 4 of 4096 2: 29.4, 4: 18.0, 8: 13.6; 8 of 1024 1: 16.6, 4: 10.4, 8: 16.0; 16 of 8192 1: 95, 2: 76, 4: 76,
+// 8: 85; 24 of 4096 1: 58, 2: 54, 4: 63; 48 of 16384 1: 319, 2: 288, 4: 312; 64 of 4096 1: 105, 2: 126.
+// Clusters of 16 only over e4m3 pools and long contexts (1 sequence of 65536 8: 53.5, 16: 45.5; of 2048
+// 8.4 / 9.7), broad CTAs (bf16, twice the warps) where there are a few units: 1 of 16384 28.8 -> 20.3, but
+// 2 of 8192 20.2 / 25.3, as clusters of 8 broad CTAs find fewer places.
 // Narrow CTAs (half the warps, four to an SM) where units are short or many: 64 sequences of 256 14.0
-// against 17.7 wide, 128 of 1024 65.8 / 76.2, e4m3 64 of 1024 19.8 / 24.4; but 64 of 4096 129 / 105.
+// against 17.7, 128 of 1024 65.8 / 76.2, e4m3 64 of 1024 19.8 / 24.4; but 64 of 4096 129 / 105.
 // Longest first where not all units are resident: 64 of 4096, ragged, 118 -> 98.
-DecodeForm decode_form(int64_t units, int32_t num_seqs, int64_t keys, int64_t key_bytes, int32_t sms) {
-  DecodeForm f{1, false, false};
+DecodeForm decode_form(int64_t units, int32_t num_seqs, int64_t keys, int64_t key_bytes, bool fp8, int32_t sms) {
+  DecodeForm f{1, 0, false};
   while (f.cluster < 16) {
     const int64_t ctas = units * 2 * f.cluster, each = keys / (2 * f.cluster);
     const int64_t least = ctas <= sms ? 64 : ctas <= 2 * sms ? 256 : ctas <= 6 * sms ? 2048 : INT64_MAX;
-    if (each < least || (f.cluster == 8 && ctas > sms)) break;
+    if (each < least || (f.cluster == 8 && (!fp8 || ctas > sms || keys < 16384))) break;
     f.cluster *= 2;
   }
-  f.narrow = units > 2 * sms && (units >= 6 * sms || keys * key_bytes <= 384 * 1024);
-  f.ordered = f.cluster == 1 && units > (f.narrow ? 4 : 2) * sms && num_seqs <= 256;
+  if (units > 2 * sms && (units >= 6 * sms || keys * key_bytes <= 384 * 1024)) f.shape = 1;
+  if (!fp8 && f.cluster == 8 && units * 16 <= sms) f.shape = 2;
+  f.ordered = f.cluster == 1 && units > (f.shape == 1 ? 4 : 2) * sms && num_seqs <= 256;
   return f;
 }
 
@@ -175,9 +178,9 @@ pa_status attend(const Call& c) {
   const int64_t units = (int64_t)c.num_seqs * c.num_kv_heads;
   if (tc && decodes(c.num_seqs, c.num_tokens, c.num_kv_heads, group)) {
     const int64_t keys = c.window > 0 ? std::min<int64_t>((int64_t)c.window + p.first, max_keys) : max_keys;
-    const DecodeForm f = decode_form(units, c.num_seqs, keys, 2 * c.head_dim * esize(c.kv_dtype), d->sms);
+    const DecodeForm f = decode_form(units, c.num_seqs, keys, 2 * c.head_dim * esize(c.kv_dtype), fp8, d->sms);
     p.cluster = f.cluster;
-    p.narrow = f.narrow;
+    p.shape = f.shape;
     p.ordered = f.ordered;
     p.w.part = static_cast<float*>(c.workspace);
     p.w.room = (int32_t)(score_room(c.num_seqs, c.num_kv_heads, group, max_keys) / p.cluster);
@@ -282,9 +285,9 @@ pa_status attend(const Call& c) {
     dp.after_tc = 1;
     dp.w.room = 0;
     const int64_t keys = c.window > 0 ? std::min<int64_t>((int64_t)c.window + p.first, max_keys) : max_keys;
-    const DecodeForm f = decode_form(units, c.num_seqs, keys, key_bytes, d->sms);
+    const DecodeForm f = decode_form(units, c.num_seqs, keys, key_bytes, fp8, d->sms);
     dp.cluster = f.cluster;
-    dp.narrow = f.narrow;
+    dp.shape = f.shape;
     dp.ordered = f.ordered;
     if (launch_window_decode(tk, tv, dp, fp8, limit, stall, c.stream) != cudaSuccess) return PA_ECUDA;
   }

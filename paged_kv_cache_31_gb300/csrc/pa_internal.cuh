@@ -619,7 +619,8 @@ struct TreeParams {
   // Attention behind a window with first tokens (k_window.cu): m.window counts behind positions, no
   // mask; seqs' second record is (items of a kv head, its first item's record, rows, 0).
   int32_t first, front;  // positions that stay visible, and the blocks they lie in
-  int32_t narrow, ordered;  // batches of decoding tokens: the CTAs' shape, longest sequences first
+  // batches of decoding tokens: the CTAs' shape (0 two to an SM, 1 narrow, 2 broad), longest first
+  int32_t shape, ordered;
   int4* item_keys;  // [items of all sequences] (sequence, gap in blocks behind the front ones, key tiles, end of the
                     // keys without it)
   int64_t* item_cum;  // [items + 1] weight before the item, over all items of a kv head in order
