@@ -141,6 +141,12 @@ __device__ __forceinline__ void load_5d(void* dst, const CUtensorMap* map, int32
       : "memory");
 }
 
+// A key's weight in a row, of its score and the row's log-sum-exp in log2 units.  (A row of NaN leaves the
+// keys that it does not see, of score -inf, as they are.)
+__device__ __forceinline__ float weight(float score, float lse) {
+  return score == -INFINITY ? 0.f : exp2f(score - lse);
+}
+
 // Byte offset of 16-byte chunk `chunk` (along D) of row `row` of a block written by a 5-D box: 8-row
 // groups of (dim half, 8 rows of 128 bytes), 128-byte swizzle.
 template <int HALVES>
@@ -441,7 +447,9 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
     bool late = false;
     for (int x = 0; x < mine; ++x) {
       const uint32_t cnt = ring_pos + x, slot = cnt % NS;
-      if (!mbar_wait(&full[stall ? NW * NS : warp * NS + slot], stall ? 0u : (cnt / NS) & 1u, limit)) {
+      // (one answer for the warp: a lane's own wait may run out just before the copy lands)
+      if (!__all_sync(kFull, mbar_wait(&full[stall ? NW * NS : warp * NS + slot],
+                                       stall ? 0u : (cnt / NS) & 1u, limit))) {
         late = true;
         break;
       }
@@ -781,10 +789,10 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
               const float l = sh.lse[min(r + k, nrow - 1)];
 #pragma unroll
               for (int u = 0; u < kU; ++u) {
-                v[u].x += exp2f(x[k][u].x - l);
-                v[u].y += exp2f(x[k][u].y - l);
-                v[u].z += exp2f(x[k][u].z - l);
-                v[u].w += exp2f(x[k][u].w - l);
+                v[u].x += weight(x[k][u].x, l);
+                v[u].y += weight(x[k][u].y, l);
+                v[u].z += weight(x[k][u].z, l);
+                v[u].w += weight(x[k][u].w, l);
               }
             }
           }
@@ -806,7 +814,7 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
         bool stop = fail;
         for (int x = x0; x < mine && !stop; ++x) {
           const uint32_t cnt = ring_pos + x - x0, slot = cnt % NS;
-          if (!mbar_wait(&full[warp * NS + slot], (cnt / NS) & 1u, limit)) {
+          if (!__all_sync(kFull, mbar_wait(&full[warp * NS + slot], (cnt / NS) & 1u, limit))) {
             if (lane == 0) {
               record_error(p.status, PA_ETIMEOUT);
               atomicExch(&sh.fail, 1);
@@ -829,7 +837,7 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int r = 2 * c + e;
-                if (r >= r0 && r < nrow) v[h] += exp2f(sc[0][2 * h + e] - sh.lse[r]);
+                if (r >= r0 && r < nrow) v[h] += weight(sc[0][2 * h + e], sh.lse[r]);
               }
               v[h] += __shfl_xor_sync(kFull, v[h], 1);
               v[h] += __shfl_xor_sync(kFull, v[h], 2);
@@ -843,7 +851,7 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int r = g + 8 * h;
-                if (r >= r0 && r < nrow) v[i] += exp2f(sc[i >> 1][2 * h + (i & 1)] - sh.lse[r]);
+                if (r >= r0 && r < nrow) v[i] += weight(sc[i >> 1][2 * h + (i & 1)], sh.lse[r]);
               }
               v[i] += __shfl_xor_sync(kFull, v[i], 4);
               v[i] += __shfl_xor_sync(kFull, v[i], 8);
