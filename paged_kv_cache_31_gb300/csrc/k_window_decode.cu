@@ -30,6 +30,7 @@
 // latencies (metadata, table, keys, joins: 1 sequence, window 4096: 13.4 us), over e4m3 pools both (48
 // sequences, window 1024: 23.2 us for 15).
 #include <algorithm>
+#include <cfloat>
 
 #include "k_tree.cuh"
 #include "k_window.cuh"
@@ -139,12 +140,6 @@ __device__ __forceinline__ void load_5d(void* dst, const CUtensorMap* map, int32
       " [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c3), "r"(c4), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
-}
-
-// A key's weight in a row, of its score and the row's log-sum-exp in log2 units.  (A row of NaN leaves the
-// keys that it does not see, of score -inf, as they are.)
-__device__ __forceinline__ float weight(float score, float lse) {
-  return score == -INFINITY ? 0.f : exp2f(score - lse);
 }
 
 // Byte offset of 16-byte chunk `chunk` (along D) of row `row` of a block written by a 5-D box: 8-row
@@ -715,7 +710,10 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
         float M2 = fmaxf(M, sink);
         if (M2 == -INFINITY) M2 = 0.f;
         const float total = L * exp2f(M - M2) + exp2f(sink - M2);
-        sh.lse[r] = L == 0.f ? INFINITY : M2 + log2f(total);
+        // (a row without a finite score gives no weight; one of NaN infinite ones, which become NaN when they
+        // are added, but nothing to the keys that it does not see, of score -inf)
+        const float lse = L == 0.f ? INFINITY : M2 + log2f(total);
+        sh.lse[r] = lse == lse ? lse : -FLT_MAX;
         sh.norm[r] = tree_finish(p, kvh, h, t, M, L, rank == 0 && !fail);
       }
     }
@@ -760,7 +758,7 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
       // One thread adds to a key, a row tile after the other (another CTA's, perhaps, behind the cluster's
       // barrier): atomic only so that L2 adds, and nobody waits for the sum that was there.
       auto add = [&](int key, float v) {
-        if (v != 0.f && key < vn) atomicAdd(w + real(key), v);
+        if (v != 0.f && key < vn) atomicAdd(w + real(key), fmaf(v, 0.f, v));
       };
       const int r0 = max(0, counted0 - row0);
       constexpr int kU = 4;
@@ -789,10 +787,10 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
               const float l = sh.lse[min(r + k, nrow - 1)];
 #pragma unroll
               for (int u = 0; u < kU; ++u) {
-                v[u].x += weight(x[k][u].x, l);
-                v[u].y += weight(x[k][u].y, l);
-                v[u].z += weight(x[k][u].z, l);
-                v[u].w += weight(x[k][u].w, l);
+                v[u].x += exp2f(x[k][u].x - l);
+                v[u].y += exp2f(x[k][u].y - l);
+                v[u].z += exp2f(x[k][u].z - l);
+                v[u].w += exp2f(x[k][u].w - l);
               }
             }
           }
@@ -801,7 +799,7 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
             const float y[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (at[u] < n - k && y[k] != 0.f) atomicAdd(w + at[u] + k, y[k]);
+              if (at[u] < n - k && y[k] != 0.f) atomicAdd(w + at[u] + k, fmaf(y[k], 0.f, y[k]));
           }
         }
       if (most > ld / kBlk) {  // (one answer for the cluster)
@@ -837,7 +835,7 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int r = 2 * c + e;
-                if (r >= r0 && r < nrow) v[h] += weight(sc[0][2 * h + e], sh.lse[r]);
+                if (r >= r0 && r < nrow) v[h] += exp2f(sc[0][2 * h + e] - sh.lse[r]);
               }
               v[h] += __shfl_xor_sync(kFull, v[h], 1);
               v[h] += __shfl_xor_sync(kFull, v[h], 2);
@@ -851,7 +849,7 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int r = g + 8 * h;
-                if (r >= r0 && r < nrow) v[i] += weight(sc[i >> 1][2 * h + (i & 1)], sh.lse[r]);
+                if (r >= r0 && r < nrow) v[i] += exp2f(sc[i >> 1][2 * h + (i & 1)] - sh.lse[r]);
               }
               v[i] += __shfl_xor_sync(kFull, v[i], 4);
               v[i] += __shfl_xor_sync(kFull, v[i], 8);
