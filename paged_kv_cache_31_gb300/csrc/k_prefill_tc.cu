@@ -81,8 +81,14 @@ constexpr int kOffFlag = kOffTmem + 16;
 // wait flags of the item's end (a tile's failure travels in the row max slot as kBadMax)
 constexpr int kOffXchg = kOffFlag + 16;
 constexpr int kSmemBytes = kOffXchg + 2 * 2 * 128 * 4 + 1024;  // + slack to align the base
+// fp8 pools behind windows: [item % kQScales][row], what a row's scores are multiplied by.  An item's
+// factors are written when the scores of the item two before are done, so while the softmax may still be
+// four items behind (its three S buffers hold one-tile items, the fourth is the next).
+constexpr int kQScales = 8;
+constexpr int kOffQScale = kOffXchg + 2 * 2 * 128 * 4;
+constexpr int kSmemScaled = kSmemBytes + kQScales * 128 * 4;
 constexpr uint32_t kBadMax = 0x7fc0dea1u;  // a NaN that no arithmetic produces (canonical 7fffffff)
-static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+static_assert(kSmemScaled <= 232448, "shared memory of one CTA");
 constexpr int kSoftWarps = 8;   // two column halves x four lane quarters
 constexpr int kConvWarps = 4;   // V converters, a quarter of each V stage each
 constexpr int kThreads = 128 + kSoftWarps * 32 + kConvWarps * 32;
@@ -557,7 +563,7 @@ __device__ void v_converter(const Ctx& c, const TcParams& p, int n_items) {
 // Every byte a warp overwrites is one it loaded itself, so __syncwarp() orders the loads
 // before the stores and the four warps need no barrier between them.  Q (bf16 from TMA) is
 // widened to f16 in place once per item, a quarter per warp: exact in f16's normal range,
-// which is how the warp-MMA fp8 path takes q as well.
+// which is how the warp-MMA fp8 path takes q as well (WIN: with a power of two to each row).
 // Per-block factors (p.m.k_bscales / v_bscales, [num_blocks, num_kv_heads]).  The softmax
 // applies each block's K factor to its scores in fp32, exactly as the warp-MMA kernel does.
 // V: the converter multiplies the widened codes of each block by the ratio of its factor to
@@ -630,12 +636,43 @@ __device__ __forceinline__ float v_reference(const VarlenMeta& m, const int32_t*
   return b0 < I.nblk_vis ? m.v_bscales[(int64_t)trow[b0] * m.num_kv_heads + I.kvh] : 1.f;
 }
 
-template <bool PB>
+// Q's rows for WIN: f16 with a power of two a row that brings its largest element to [2^14, 2^15), exact
+// down to 2^-28 of that; the softmax takes the power back.  An infinity makes the whole row NaN.  Warp w
+// has rows 32 w .., a lane one of them (its 16-byte chunks in an order that spreads the lanes over the banks).
+__device__ __forceinline__ void scale_q_rows(const Ctx& c, uint32_t qb, uint32_t item, int w, int lane) {
+  const int row = 32 * w + lane;
+  uint8_t* at = c.sm + kOffQ + qb * kTile + row * 128;
+  auto chunk = [&](int i) {
+    return reinterpret_cast<uint4*>(at + (i >> 3) * kHalf + (((i & 7) ^ (row & 7)) << 4));
+  };
+  uint32_t big = 0;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const uint4 v = *chunk(i);
+    const uint32_t x = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    big = max(big, max(x & 0xffffu, x >> 16));
+  }
+  const int up = min(max(141 - (int)(big >> 7), -113), 120);
+  const float f = big < 0x7f80u ? __uint_as_float((uint32_t)(127 + up) << 23) : NAN;
+  auto half_of = [&](uint32_t x) {
+    return pack_f16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
+  };
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const uint4 v = *chunk(i);
+    *chunk(i) = make_uint4(half_of(v.x), half_of(v.y), half_of(v.z), half_of(v.w));
+  }
+  reinterpret_cast<float*>(c.sm + kOffQScale)[item % kQScales * 128 + row] =
+      __uint_as_float((uint32_t)(127 - up) << 23);
+}
+
+template <bool PB, bool WIN>
 __device__ void fp8_converter(const Ctx& c, const TcParams& p, int n_items) {
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kFirstConvWarp;
   uint32_t kv = 0, it_cnt = 0;
   for (int idx; (idx = item_of(c, (int)it_cnt)) < n_items; ++it_cnt) {
-    const Item I = load_item<false>(p, idx, c.rank);
+    const Item I = load_item<WIN>(p, idx, c.rank);
     FactorPipe<2> vf;  // PB: the V factors of blocks 2w, 2w + 1 of each tile
     float rref = 1.f;  // PB: 1 / the item's V reference
     bool out_of_range = false;  // PB: a ratio outside [kRatioMin, kRatioMax]
@@ -650,15 +687,19 @@ __device__ void fp8_converter(const Ctx& c, const TcParams& p, int n_items) {
     {  // Q: this warp's quarter of the 128 x 128 bf16 tile, 16 chunks of 16 bytes per lane
       const uint32_t qb = it_cnt & 1u;
       if (!__all_sync(kFull, wait_bar(c, B_QFULL + qb, (it_cnt >> 1) & 1u))) return;
-      uint4* q = reinterpret_cast<uint4*>(c.sm + kOffQ + qb * kTile) + w * (kTile / 16 / 4);
+      if constexpr (WIN) {
+        scale_q_rows(c, qb, it_cnt, w, lane);
+      } else {
+        uint4* q = reinterpret_cast<uint4*>(c.sm + kOffQ + qb * kTile) + w * (kTile / 16 / 4);
 #pragma unroll 4
-      for (int i = 0; i < kTile / 16 / 4 / 32; ++i) {
-        uint4 v = q[lane + 32 * i];
-        v.x = bf16x2_to_f16x2(v.x);
-        v.y = bf16x2_to_f16x2(v.y);
-        v.z = bf16x2_to_f16x2(v.z);
-        v.w = bf16x2_to_f16x2(v.w);
-        q[lane + 32 * i] = v;
+        for (int i = 0; i < kTile / 16 / 4 / 32; ++i) {
+          uint4 v = q[lane + 32 * i];
+          v.x = bf16x2_to_f16x2(v.x);
+          v.y = bf16x2_to_f16x2(v.y);
+          v.z = bf16x2_to_f16x2(v.z);
+          v.w = bf16x2_to_f16x2(v.w);
+          q[lane + 32 * i] = v;
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -751,7 +792,7 @@ __device__ __forceinline__ void pair_sync(int quad) {
   asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
 }
 
-template <bool PB, bool WIN>
+template <bool PB, bool WIN, bool SCALED>
 __device__ void softmax_role(const Ctx& c, const TcParams& p, uint32_t tmem, int n_items) {
   const VarlenMeta& m = p.m;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -784,7 +825,7 @@ __device__ void softmax_role(const Ctx& c, const TcParams& p, uint32_t tmem, int
     // WIN: the first keys are visible, too, up to `end`
     const int first = WIN && m.window > 0 ? min(p.first, end) : 0;
     float m_ref = -INFINITY, l = 0.f;
-    const float sl = head_scale(m.k_scales, I.kvh, p.scale_log2);  // K = k_scales[g] * pool
+    float sl = head_scale(m.k_scales, I.kvh, p.scale_log2);  // K = k_scales[g] * pool
     // PB: the K factors of this thread's four blocks (64 columns) in each tile, and the V
     // reference the converters divided the factors by
     FactorPipe<4> kf;
@@ -806,6 +847,9 @@ __device__ void softmax_role(const Ctx& c, const TcParams& p, uint32_t tmem, int
         bad = !__all_sync(kFull, p.debug_stall ? wait_bar(c, B_NEVER, 0u)
                                                : wait_bar(c, B_SFULL + b, use_par(s)));
       tc_fence_after();
+      // (Q's f16 rows, and so these factors, were there before the scores)
+      if (SCALED && j == 0)
+        sl *= reinterpret_cast<const float*>(c.sm + kOffQScale)[k % kQScales * 128 + r];
       // after a failed wait the values read here only travel to the exchange below, where
       // the pair leaves (a read of allocated tensor memory is defined, whatever it holds)
       float x[64];
@@ -1004,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_tc_prefill(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const TcParams p) {
   static_assert(!PB || FP8, "per-block factors are for e4m3 pools");
-  static_assert(!WIN || !FP8, "windows with first tokens: bf16 pools");
+  static_assert(!WIN || !PB, "windows with first tokens: no per-block factors");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~uintptr_t(1023));
@@ -1077,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
     if constexpr (FP8)
-      fp8_converter<PB>(c, p, n_items);
+      fp8_converter<PB, WIN>(c, p, n_items);
     else
       v_converter<WIN>(c, p, n_items);
     tc_fence_before();
@@ -1122,7 +1166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 184;" ::: "memory");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 200;" ::: "memory");
-    softmax_role<PB, WIN>(c, p, tmem, n_items);
+    softmax_role<PB, WIN, WIN && FP8>(c, p, tmem, n_items);
     tc_fence_before();
     cluster_sync();
   }
@@ -1134,16 +1178,18 @@ cudaError_t launch_tc_prefill(const CUtensorMap& tq, const CUtensorMap& tk, cons
                               const TcParams& p, int grid, cudaStream_t stream) {
   if (grid < 2) grid = 2;
   // per-block factors: e4m3 pools only (the caller checks)
-  auto kern = p.win ? k_tc_prefill<false, false, true>
+  auto kern = p.win && p.kv_fp8 ? k_tc_prefill<true, false, true>
+              : p.win     ? k_tc_prefill<false, false, true>
               : !p.kv_fp8 ? k_tc_prefill<false, false>
               : p.m.k_bscales ? k_tc_prefill<true, true> : k_tc_prefill<true, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  const int smem = p.win && p.kv_fp8 ? kSmemScaled : kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // pairs of CTAs (a cluster of two SMs) run the 2-SM MMAs
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(grid & ~1), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

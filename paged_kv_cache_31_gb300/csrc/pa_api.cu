@@ -135,8 +135,6 @@ bool pool_map_fp8(CUtensorMap* map, const void* base, int64_t num_blocks, int bl
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-namespace {
-
 // The same byte tensor with a 64 x 1 x 16 box and no swizzle: the 64 dims of one half of a
 // head size of 128 for one (block, kv head), 1 KB of plain 64-byte rows (the tcgen05 prefill
 // kernel's V part of a CTA).
@@ -153,8 +151,6 @@ bool pool_map_fp8_half(CUtensorMap* map, const void* base, int64_t num_blocks, i
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-}  // namespace
 
 // TMA descriptor of q [T, H, D] bf16 seen as the 3-D tensor (D, H, T): a 64 x G x `tokens` box
 // is the 64-dim half of a query tile whose rows are the G heads of one kv head for `tokens`

@@ -244,7 +244,7 @@ pa_status attend(const Call& c) {
   // many items of prompt chunks: the prefill kernel takes them (its pairs of CTAs do a fifth to a half
   // more a second, but an item's keys are not cut, so there have to be more items than pairs)
   const int64_t key_bytes = 2 * (int64_t)c.head_dim * esize(c.kv_dtype);
-  const bool prefill = tc && !fp8 && c.head_dim == 128 && 128 % group == 0 &&
+  const bool prefill = tc && c.head_dim == 128 && 128 % group == 0 &&
                        c.num_tokens * group / 256 * c.num_kv_heads >= 2 * d->sms && units < (1 << 24);
   if (prefill) {
     p.tc.plan = reinterpret_cast<int32_t*>(ws + L.tc_off);
@@ -262,9 +262,11 @@ pa_status attend(const Call& c) {
   stall_hook(limit, stall);
   if (prefill) {
     CUtensorMap pk, pv;
-    if (!pool_map(&pk, c.k_blocks, c.num_blocks, 16, c.num_kv_heads, c.head_dim) ||
-        !pool_map(&pv, c.v_blocks, c.num_blocks, 16, c.num_kv_heads, c.head_dim))
-      return PA_ECUDA;
+    const bool ok = fp8 ? pool_map_fp8(&pk, c.k_blocks, c.num_blocks, 16, c.num_kv_heads, c.head_dim) &&
+                              pool_map_fp8_half(&pv, c.v_blocks, c.num_blocks, 16, c.num_kv_heads, c.head_dim)
+                        : pool_map(&pk, c.k_blocks, c.num_blocks, 16, c.num_kv_heads, c.head_dim) &&
+                              pool_map(&pv, c.v_blocks, c.num_blocks, 16, c.num_kv_heads, c.head_dim);
+    if (!ok) return PA_ECUDA;
     TcParams tp;
     std::memset(&tp, 0, sizeof tp);
     tp.out = c.out;
@@ -276,6 +278,7 @@ pa_status attend(const Call& c) {
     tp.wait_limit_ns = limit;
     tp.debug_stall = stall;
     tp.win = 1;
+    tp.kv_fp8 = fp8;
     tp.first = p.first;
     tp.redo_flags = p.tc.plan + p.tc.redo_off;
     tp.redo_list = p.tc.plan + p.tc.redo_list_off;
@@ -291,9 +294,9 @@ pa_status attend(const Call& c) {
     dp.ordered = f.ordered;
     if (launch_window_decode(tk, tv, dp, fp8, limit, stall, c.stream) != cudaSuccess) return PA_ECUDA;
   }
-  if (tc) {
+  if (tc && !(prefill && fp8)) {  // (f16 holds every e4m3 value: no items to do again)
     if (launch_window_tc(tq, tk, tv, p, fp8, limit, stall, c.stream) != cudaSuccess) return PA_ECUDA;
-  } else if (launch_window_generic(p, c.kv_dtype, c.stream) != cudaSuccess) {
+  } else if (!tc && launch_window_generic(p, c.kv_dtype, c.stream) != cudaSuccess) {
     return PA_ECUDA;
   }
   if (!prefill && launch_tree_merge(p, c.stream) != cudaSuccess) return PA_ECUDA;

@@ -442,7 +442,7 @@ struct TcParams {
   float scale_log2;
   uint64_t wait_limit_ns;
   uint32_t debug_stall;  // tests only: the softmax waits run out (PA_DEBUG_STALL_NS)
-  int32_t win, first;    // behind a window with first tokens (k_window.cu's plan), bf16 pools
+  int32_t win, first;    // behind a window with first tokens (k_window.cu's plan)
   int32_t kv_fp8;        // e4m3 pools (tk: 128 x 1 x 16 byte boxes, tv: 64 x 1 x 16)
   // items whose V does not fit f16 (recomputed by the warp-MMA kernel afterwards): a flag per
   // 256-row item, the list of marked items and its length (all in the plan)
@@ -746,6 +746,8 @@ bool pool_map(CUtensorMap* map, const void* base, int64_t num_blocks, int block_
 bool pool_map_rows(CUtensorMap* map, const void* base, int64_t num_blocks, int hkv, int d);
 bool pool_map_fp8(CUtensorMap* map, const void* base, int64_t num_blocks, int block_size,
                   int hkv, int d, bool one_head = false);
+bool pool_map_fp8_half(CUtensorMap* map, const void* base, int64_t num_blocks, int block_size, int hkv,
+                       int d);
 bool query_map(CUtensorMap* map, const void* q, int64_t num_tokens, int h, int d, int group,
                int tokens);
 void stall_hook(uint64_t& limit, uint32_t& stall);

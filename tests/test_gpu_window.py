@@ -20,9 +20,13 @@ def pa():
 
 def roundings(b, tc=None):
     """What the kernels round softmax weights and q to (see spec_reference.tree_attention)."""
+    many = b.T * (b.H // b.Hkv) // 256 * b.Hkv >= 304  # (the prefill kernel)
     if b.kb.dtype == E4M3 and b.q.dtype == BF16:
+        if many:
+            # weights as below; q's f16 rows, their largest element in [2^14, 2^15), keep 2^-25
+            return {"weight_u": 2.0 ** -11, "weight_min": 2.0 ** -25, "q_u": 2.0 ** -39}
         return {"weight_u": 2.0 ** -11, "q_u": 2.0 ** -17, "weight_min": 2.0 ** -32}
-    if b.T * (b.H // b.Hkv) // 256 * b.Hkv >= 304:
+    if many:
         # the prefill kernel: one f16 weight, at least 2^-8 for the row's largest (its reference may lie
         # 8 powers of two above): below its normal range half its smallest step, 2^-25
         return {"weight_u": 2.0 ** -11, "weight_min": 2.0 ** -25}

@@ -83,6 +83,20 @@ def test_scores_past_the_room(pa, kv):
     weights_test.check(pa, b, scales=(0.125, 0.25) if kv == E4M3 else (1.0, 1.0))
 
 
+@pytest.mark.parametrize("window,first", [(0, 0), (1, 1), (300, 4), (128, 130), (2 ** 31 - 1, 7)])
+@pytest.mark.parametrize("H,Hkv", [(64, 8), (16, 16)])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -30, 2.0 ** 40])
+def test_many_chunks_over_e4m3(pa, H, Hkv, size, window, first):
+    """The prefill kernel over e4m3 pools, q of any magnitude."""
+    seqs = [(c, n if H == 64 or n <= 100 else 4 * n) for c, n in window_test.CHUNKS]
+    b = ref.Batch(seqs, H, Hkv, 128, kv=E4M3, seed=window % 91)
+    b.q *= size
+    b.q[::3] *= 2.0 ** -9  # rows of one tile
+    b.scale /= size
+    b.poison_unread(window, first)
+    both(pa, b, window, first, observed=30 if window == 300 else 0)
+
+
 def test_some_sequences_have_no_token(pa):
     """As many sequences as tokens, though one has them all and others none."""
     for seqs in ([(300, 1), (20, 0), (0, 1), (77, 2), (40, 0)], [(90, 0), (200, 5), (30, 0), (9, 0), (10, 0)]):
@@ -134,6 +148,7 @@ PATHS = {"decode": ([(900, 1), (300, 1), (2000, 1)], 8, 2, BF16),
          "decode e4m3": ([(900, 1), (300, 1), (2000, 1)], 8, 2, E4M3),
          "shares": ([(900, 40), (0, 100), (2000, 1)], 8, 2, BF16),
          "shares e4m3": ([(900, 40), (0, 100), (2000, 1)], 8, 2, E4M3),
+         "prefill e4m3": ([(300, 800), (0, 500), (1000, 1), (2000, 2)], 64, 8, E4M3),
          "prefill": ([(300, 800), (0, 500), (1000, 1), (2000, 2)], 64, 8, BF16)}
 
 
