@@ -6,22 +6,27 @@
 // final, so only S is computed again, a third of the attention's products over bf16 pools (which
 // multiplies V by both terms of P).  It is taken transposed, S^T = K Q^T: keys are the rows of the
 // accumulator, a key is a thread, and the sum over the queries stays in its registers: no exchange, no
-// atomics, one add to memory for a key in the end.
+// atomics, one add to memory for a key in the end.  -lse is added by the products, too: a row's, divided by
+// the scale, as three bf16 whose sum it is, times ones (each thread reading the rows' numbers from shared
+// memory kept that busy for a third of the time).
 //
-// Work.  An item is 256 keys of one (sequence, kv head), which stay in shared memory, against the row
+// Work.  An item is 256 keys of one (sequence, kv head), which stay in tensor memory, against the row
 // tiles (128 rows: whole tokens times the group's heads) that see any of them, which stream past.  The
 // items' row tiles, laid end to end with a weight for an item's keys, are cut evenly over one CTA per SM;
 // the pieces of a cut item leave partial sums, which k_weights_join adds in order.
 //
-// Roles.  warp 0: TMA of K (two stages of 256 keys) and Q (a ring of two row tiles); warp 1:
-// tensor-memory owner, issues S^T; warps 2 and 3: the rows' log-sum-exps and positions into a ring of four;
-// warps 4..19: exponentials and sums, a warpgroup for 128 keys and 64 rows of a row tile each, from two S^T
-// buffers for each 128 keys (two warpgroups, of all rows, left the schedulers idle half of the time: 312 us
-// for a prompt of 8191 tokens, 8 x 4 heads); warps 20..23 (e4m3 pools): widen K to bf16, exactly, once an
-// item.
+// Roles.  warp 0: TMA of K (256 keys) and Q (a ring of three row tiles); warp 1: tensor-memory owner,
+// issues S^T; warp 2: the rows' log-sum-exps into the ring and their positions; warps 4..19:
+// exponentials and sums, a warpgroup for 128 keys and 64 rows of a row tile each, from three S^T buffers
+// (two warpgroups, of all rows, left the schedulers idle half of the time); at an item's start they take
+// K from shared to tensor memory, e4m3 codes widened to bf16 exactly.
 //
-// What bounds it: a row tile's 32768 exponentials (2^x on the SFU and two packed fp32 instructions for
-// a pair) beside 1230 cycles of products.
+// What bounds it: a chain.  A row tile of a prompt of 8191 tokens (8 x 4 heads, 245 us in all) takes some
+// 2000 cycles, of which its products take 1150, its 32768 exponentials 1024 of the SFU and its instructions
+// 1200 of the schedulers; a warp waits for S^T, loads it and sums it in turn.  K from shared memory with
+// log-sum-exps read by each thread: 275 us, shared memory four fifths busy.  Tried without gain: two issuing
+// warps, a look at the next tile's waits between products (252), halves of a tile loaded while the halves
+// before are summed (311: the buffers are held longer).
 #include <algorithm>
 
 #include "k_tree.cuh"
@@ -33,58 +38,67 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kKeys = kWeightKeys;  // of an item
 constexpr int kRows = 128;          // of a row tile, at most
-constexpr int kLse = 4;             // ring of the rows' numbers
+constexpr int kPos = 8;             // ring of the rows' positions
+constexpr int kQueries = 3;         // ring of row tiles: queries and log-sum-exps
+constexpr int kSums = 3;            // S^T buffers (128 keys, a row tile) in tensor memory, then K
+constexpr uint32_t kColK = kSums * kRows;
 
 template <int D, bool FP8>
 struct Shape {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * 128 * 128;  // 128 rows of 16-bit values
-  static constexpr int kCodes = 128 * 128;           // 128 keys of codes
-  static constexpr int kThreads = FP8 ? 768 : 640;
-  // K as it is multiplied: two stages of 256 keys (bf16, as the 5-D boxes write it), or one of widened
-  // ones (dim half by dim half)
-  static constexpr int kWide = FP8 ? 1 : 2;
-  static constexpr int kRowGroup = FP8 ? 1024 : 1024 * kHalves;  // between 8-row groups
-  static constexpr int kDimHalf = FP8 ? 128 * 128 : 1024;        // between dim halves
+  static constexpr int kThreads = 640;
+  static constexpr int kHalf = FP8 ? 128 * 128 : kTile;  // of a stage: 128 keys as the pool has them
   static constexpr int kOffK = 0;
-  static constexpr int kOffCodes = kOffK + kWide * 2 * kTile;  // e4m3: two stages of 256 keys' codes
-  static constexpr int kOffQ = kOffCodes + (FP8 ? 4 * kCodes : 0);
-  static constexpr int kOffRow = kOffQ + 2 * kTile;  // [kLse][2][128]: -lse in log2 units, positions
-  static constexpr int kOffInfo = kOffRow + kLse * 2 * kRows * 4;  // [kLse] int4
-  static constexpr int kOffHalf = kOffInfo + kLse * 16;  // [key half][128]: sums of the second row halves
+  static constexpr int kOffQ = kOffK + 2 * kHalf;
+  // 128 rows of 64 bf16: 16 of a row for each of the ring's stages (its log-sum-exp), then K's ones
+  static constexpr int kOffLse = kOffQ + kQueries * kTile;
+  static_assert(kQueries == 3, "the stages and the ones fill a row");
+  static constexpr int kOffPos = kOffLse + 128 * 128;          // [kPos][128]
+  static constexpr int kOffInfo = kOffPos + kPos * kRows * 4;  // [kPos] int4
+  static constexpr int kOffHalf = kOffInfo + kPos * 16;  // [key half][128]: sums of the second row halves
   static constexpr int kOffBar = kOffHalf + 2 * 128 * 4;
-  static constexpr int kOffMisc = kOffBar + 32 * 8;
+  static constexpr int kOffMisc = kOffBar + 40 * 8;
   static constexpr int kSmem = kOffMisc + 16;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
 enum : int {
   B_KFULL = 0,              // K's keys (or codes) landed
-  B_KEMPTY = B_KFULL + 2,   // all products (or the widening) of the stage are done
-  B_WIDE = B_KEMPTY + 2,    // e4m3: K is widened
-  B_WFREE = B_WIDE + 1,     // e4m3: its products are done
-  B_QFULL = B_WFREE + 1,
-  B_QEMPTY = B_QFULL + 2,
-  B_SFULL = B_QEMPTY + 2,   // [key half][buffer]
-  B_SFREE = B_SFULL + 4,
-  B_LFULL = B_SFREE + 4,
-  B_LFREE = B_LFULL + kLse,
-  B_HALF = B_LFREE + kLse,  // per key half: the second row half's sums are there
+  B_KEMPTY = B_KFULL + 1,   // they have been read
+  B_KREADY = B_KEMPTY + 1,  // K is in tensor memory
+  B_KDONE = B_KREADY + 1,   // all its products are done
+  B_QFULL = B_KDONE + 1,        // a row tile's queries landed, its numbers are there
+  B_QEMPTY = B_QFULL + kQueries,
+  B_SFULL = B_QEMPTY + kQueries,
+  B_SFREE = B_SFULL + kSums,
+  B_PFREE = B_SFREE + kSums,    // positions have been read
+  B_HALF = B_PFREE + kPos,  // per key half: the second row half's sums are there
   B_TAKEN = B_HALF + 2,     // they have been added
   B_FIN = B_TAKEN + 2,
   B_NEVER = B_FIN + 1,  // nothing arrives on it (the debug_stall test hook)
   kNumBars = B_NEVER + 1
 };
-static_assert(kNumBars <= 32, "barrier area");
+static_assert(kNumBars <= 40, "barrier area");
 
 constexpr uint32_t kTmemCols = 512;
 
-__device__ __forceinline__ void mma(uint32_t elect, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                    uint32_t accumulate) {
+// Whole warp, in uniform control flow; lane 0 issues.
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred e, p;\n\tsetp.ne.u32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .u32 l;\n\t.reg .pred e, p;\n\tmov.u32 l, %%laneid;\n\tsetp.eq.u32 e, l, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elect)
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Same with A in tensor memory (row r in lane r, two values to a column).
+__device__ __forceinline__ void mma_ta(uint32_t d, uint32_t at, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .u32 l;\n\t.reg .pred e, p;\n\tmov.u32 l, %%laneid;\n\tsetp.eq.u32 e, l, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(at), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {  // whole warp; arrives once its MMAs are done
@@ -195,7 +209,8 @@ template <int D, bool FP8>
 __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* tk, const CUtensorMap* tq) {
   using S = Shape<D, FP8>;
   const int lane = threadIdx.x & 31;
-  Ring<2> k, q;
+  Ring<1> k;
+  Ring<kQueries> q;
   uint32_t nk = 0, nq = 0;  // stages issued
   bool ok = true;
   Walk walk(p, blockIdx.x);
@@ -211,24 +226,23 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
     }
     const int halves = g.keys > 128 ? 2 : 1;
     if (lane == 0) {
-      if (nk >= 2) ok = wait_bar(c, B_KEMPTY + k.st, k.par ^ 1);
-      if (ok) mbar_arrive_expect_tx(c.bar + B_KFULL + k.st, halves * (FP8 ? S::kCodes : S::kTile));
+      if (nk >= 1) ok = wait_bar(c, B_KEMPTY, k.par ^ 1);
+      if (ok) mbar_arrive_expect_tx(c.bar + B_KFULL, halves * S::kHalf);
     }
     ok = __shfl_sync(kFull, (int)ok, 0);
     if (!ok) break;
     if (lane < 8 * halves) {
       if constexpr (FP8)
-        tma_load_3d(c.sm + S::kOffCodes + k.st * 2 * S::kCodes + lane * 2048, tk, 0, g.kvh,
-                    id >= 0 ? id * 16 : -16, c.bar + B_KFULL + k.st);
+        tma_load_3d(c.sm + S::kOffK + lane * 2048, tk, 0, g.kvh, id >= 0 ? id * 16 : -16, c.bar + B_KFULL);
       else
-        tma_load_5d(c.sm + S::kOffK + k.st * 2 * S::kTile + lane * (S::kTile / 8), tk, 0, 0, 0,
-                    id >= 0 ? id * 2 : -2, g.kvh, c.bar + B_KFULL + k.st);
+        tma_load_5d(c.sm + S::kOffK + lane * (S::kTile / 8), tk, 0, 0, 0, id >= 0 ? id * 2 : -2, g.kvh,
+                    c.bar + B_KFULL);
     }
     ++nk;
     k.next();
     if (lane == 0) {
       for (int r = g.r0; ok && r < g.r1; ++r) {
-        if (nq >= 2) ok = wait_bar(c, B_QEMPTY + q.st, q.par ^ 1);
+        if (nq >= kQueries) ok = wait_bar(c, B_QEMPTY + q.st, q.par ^ 1);
         if (!ok) break;
         uint64_t* bar = c.bar + B_QFULL + q.st;
         mbar_arrive_expect_tx(bar, (uint32_t)p.tile_rows * 128 * S::kHalves);
@@ -244,242 +258,247 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
   }
   // the copies still in flight (after an abort; otherwise all have been consumed)
   if (lane == 0) {
-    for (uint32_t i = nk > 2 ? nk - 2 : 0; i < nk; ++i) mbar_wait(c.bar + B_KFULL + (i & 1), (i >> 1) & 1, c.limit);
-    for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) mbar_wait(c.bar + B_QFULL + (i & 1), (i >> 1) & 1, c.limit);
+    if (nk > 0) mbar_wait(c.bar + B_KFULL, (nk - 1) & 1, c.limit);
+    for (uint32_t i = nq > kQueries ? nq - kQueries : 0; i < nq; ++i)
+      mbar_wait(c.bar + B_QFULL + i % kQueries, i / kQueries & 1, c.limit);
   }
   __syncwarp();
 }
 
 template <int D, bool FP8>
-__device__ void issuer(const Ctx& c, const TreeParams& p, uint32_t tmem) {
+__device__ void issuer(const Ctx& c, const TreeParams& p, uint32_t tmem_base) {
   using S = Shape<D, FP8>;
   constexpr uint32_t kIdesc = idesc_f16kind(128, kRows, 0, 1);
-  const uint32_t sm = smem_u32(c.sm), elect = (threadIdx.x & 31) == 0;
-  Ring<2> k, q;
-  Ring<1> w;
-  uint32_t n[2] = {0, 0};  // tiles of each half so far
+  const uint32_t sm = smem_u32(c.sm);
+  Ring<1> k;
+  Ring<kQueries> q;
+  Ring<kSums> s;
+  uint32_t n = 0;  // S^T tiles so far
+  const uint32_t tmem = __shfl_sync(kFull, tmem_base, 0);
+  const uint64_t ones = sdesc(sm + S::kOffLse + kQueries * 32, 16, 1024);
   Walk walk(p, blockIdx.x);
   Piece g;
   while (walk.next(p, g)) {
-    const int halves = g.keys > 128 ? 2 : 1;
-    if (!(FP8 ? wait_all(c, B_WIDE, w.par) : wait_all(c, B_KFULL + k.st, k.par))) return;
-    const uint32_t kb = sm + S::kOffK + (FP8 ? 0 : k.st * 2 * S::kTile);
-    for (int r = g.r0; r < g.r1; ++r) {
+    // (one value for the warp, as the compiler can see: in control flow that it takes for divergent, an
+    // MMA's issue took 110 cycles instead of 65)
+    const int halves = __shfl_sync(kFull, g.keys > 128 ? 2 : 1, 0);
+    if (!wait_all(c, B_KREADY, k.par)) return;
+    for (int left = __shfl_sync(kFull, g.r1 - g.r0, 0); left > 0; --left) {
       if (!wait_all(c, B_QFULL + q.st, q.par)) return;
 #pragma unroll 1
-      for (int x = 0; x < halves; ++x) {
-        const uint32_t use = x ? n[1] : n[0], buf = use & 1;
-        if (use >= 2 && !wait_all(c, B_SFREE + 2 * x + buf, ((use >> 1) & 1) ^ 1)) return;
+      for (int x = 0; x < halves; ++x, ++n) {
+        if (n >= kSums && !wait_all(c, B_SFREE + s.st, s.par ^ 1)) return;
         tc_fence_after();
-        uint64_t kd = sdesc(kb + x * S::kTile, 16, S::kRowGroup);
-        uint64_t qd = sdesc(sm + S::kOffQ + q.st * S::kTile, 16, 1024);
-#pragma unroll 1
-        for (int h = 0; h < S::kHalves; ++h) {
+        const uint64_t qd = sdesc(sm + S::kOffQ + q.st * S::kTile, 16, 1024);
+        const uint32_t d = tmem + s.st * kRows, kt = tmem + kColK + x * (D / 2);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma(elect, tmem + (2 * x + buf) * kRows, kd + 2 * kk, qd + 2 * kk, kIdesc, (h | kk) ? 1u : 0u);
-          kd += S::kDimHalf / 16;
-          qd += 128 * 128 / 16;
-        }
-        commit(c.bar + B_SFULL + 2 * x + buf);
-        if (x) ++n[1]; else ++n[0];
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ta(d, kt + 8 * kk, qd + (kk >> 2) * (128 * 128 / 16) + 2 * (kk & 3), kIdesc, kk ? 1u : 0u);
+        // (last: one rounding at the log-sum-exp's magnitude)
+        mma(d, ones, sdesc(sm + S::kOffLse + q.st * 32, 16, 1024), kIdesc, 1u);
+        commit(c.bar + B_SFULL + s.st);
+        s.next();
       }
       commit(c.bar + B_QEMPTY + q.st);
       __syncwarp();
       q.next();
     }
-    commit(c.bar + (FP8 ? B_WFREE : B_KEMPTY + k.st));
+    commit(c.bar + B_KDONE);
     __syncwarp();
     k.next();
-    w.next();
   }
 }
 
-// The rows' numbers: for column r of a row tile -lse in log2 units and its position (-1: no row), and
-// (lowest position, highest, rows) of the tile.  Two warps take the tiles in turn, and a warp requests a
-// tile's before it stores those of the one before: one warp without either was what bound this kernel (a
-// load's latency to each row tile: 1.4 us a tile of 0.6 us).
-__device__ void row_loader(const Ctx& c, const TreeParams& p, int which, float* nl, int* pos, int4* info) {
+// The rows' numbers: for row r of a row tile -lse in the products' units, as three bf16 whose sum it is (for
+// the products with K's ones), and its position (-1: no row), and (lowest position, highest, rows) of the tile.  A tile's are
+// requested while the warp waits for the place of the one before (a load's latency to each row tile had
+// bound this kernel).
+__device__ void row_loader(const Ctx& c, const TreeParams& p, uint8_t* lse, int* pos, int4* info) {
   const VarlenMeta& m = p.m;
   const int lane = threadIdx.x & 31;
-  float a[4];
-  int b[4], cols = 0;
-  uint32_t tile = 0, held = 0;  // row tiles so far; the one whose numbers are held
-  bool have = false;
-  auto store = [&]() {
-    const uint32_t st = held % kLse, turn = held / kLse;
+  float a[4], scale = 1.f;  // scale: -1 over the kv head's
+  int b[4], cols = 0, token[4], head[4];  // of the lane's rows in a tile
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int col = lane + 32 * i;
+    token[i] = col < p.tile_rows ? col / m.group : INT_MAX / 2;
+    head[i] = col % m.group;
+  }
+  uint32_t tile = 0;  // row tiles so far
+  Ring<kQueries> q;
+  auto store = [&]() {  // the tile before
+    const uint32_t st = (tile - 1) % kPos, turn = (tile - 1) / kPos;
+    if (tile > kQueries && !wait_all(c, B_QEMPTY + q.st, q.par ^ 1)) return false;
+    if (turn > 0 && !wait_all(c, B_PFREE + st, (turn & 1) ^ 1)) return false;
     int lo = INT_MAX, hi = -1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const int col = lane + 32 * i;
       lo = min(lo, b[i] >= 0 ? b[i] : INT_MAX);
       hi = max(hi, b[i]);
+      // (a row without a finite score, lse -inf, gives no weight)
+      const float x = a[i] == -INFINITY ? -INFINITY : a[i] * scale;
+      const float x1 = __bfloat162float(__float2bfloat16_rn(x)), rest = fabsf(x1) < INFINITY ? x - x1 : 0.f;
+      const float x2 = __bfloat162float(__float2bfloat16_rn(rest));
+      *reinterpret_cast<uint2*>(lse + col * 128 + (((2 * q.st) ^ (col & 7)) << 4)) =
+          make_uint2(pack_bf16x2(x1, x2), pack_bf16x2(rest - x2, 0.f));
+      pos[st * kRows + col] = b[i];
     }
     lo = __reduce_min_sync(kFull, lo);
     hi = __reduce_max_sync(kFull, hi);
-    if (turn > 0 && !wait_all(c, B_LFREE + st, (turn & 1) ^ 1)) return false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int col = lane + 32 * i;
-      // (a row without a finite score, lse -inf, gives no weight)
-      nl[st * 2 * kRows + col] = a[i] == -INFINITY ? -INFINITY : -a[i] * kLog2e;
-      pos[st * 2 * kRows + col] = b[i];
-    }
     if (lane == 0) info[st] = make_int4(lo, hi, cols, 0);
+    fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar + B_LFULL + st);
+    if (lane == 0) mbar_arrive(c.bar + B_QFULL + q.st);
+    q.next();
     return true;
   };
   Walk walk(p, blockIdx.x);
   Piece g;
   while (walk.next(p, g)) {
+    const float of_head = -1.f / head_scale(m.k_scales, g.kvh, p.scale);
     for (int r = g.r0; r < g.r1; ++r, ++tile) {
-      if ((int)(tile & 1) != which) continue;
-      float na[4];
-      int nb[4];
+      if (tile > 0 && !store()) return;
       const int first = r * p.tile_tokens;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int col = lane + 32 * i, t = first + col / m.group;
-        const bool in = col < p.tile_rows && t < g.tokens;
-        na[i] = in ? m.lse[(int64_t)(g.kvh * m.group + col % m.group) * m.num_tokens + g.qs + t] : 0.f;
-        nb[i] = in ? m.positions[g.qs + t] : -1;
+        const int t = first + token[i];
+        const bool in = t < g.tokens;
+        a[i] = in ? m.lse[(int64_t)(g.kvh * m.group + head[i]) * m.num_tokens + g.qs + t] : 0.f;
+        b[i] = in ? m.positions[g.qs + t] : -1;
       }
-      if (have && !store()) return;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = na[i];
-        b[i] = nb[i];
-      }
+      scale = of_head;
       cols = min(p.tile_rows, (g.tokens - first) * m.group);
-      held = tile;
-      have = true;
     }
   }
-  if (have) store();
+  if (tile > 0) store();
 }
 
-// Warps 20 to 23: codes to bf16 (exact), a quarter of the keys each; 128 keys at a time as in
-// k_tree_tc.cuh, dim half by dim half.
-template <int D>
-__device__ void widener(const Ctx& c, const TreeParams& p) {
-  using S = Shape<D, true>;
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 20;
-  Ring<2> k;
-  Ring<1> wd;
-  uint32_t use = 0;
-  Walk walk(p, blockIdx.x);
-  Piece g;
-  for (; walk.next(p, g); ++use) {
-    const int halves = g.keys > 128 ? 2 : 1;
-    if (use >= 1 && !wait_all(c, B_WFREE, wd.par ^ 1)) return;
-    if (!wait_all(c, B_KFULL + k.st, k.par)) return;
-    for (int x = 0; x < halves; ++x) {
-      const uint8_t* codes = c.sm + S::kOffCodes + (2 * k.st + x) * S::kCodes;
-      uint8_t* tile = c.sm + S::kOffK + x * S::kTile;
-#pragma unroll 1
-      for (int i0 = 0; i0 < 8; ++i0) {
-        const int ch = lane + 32 * i0, r = 32 * w + (ch >> 3), sw = r & 7;
-        const uint4 src = *reinterpret_cast<const uint4*>(codes + 32 * w * 128 + ch * 16);
-        const int L = (ch & 7) ^ sw, h = L >> 2, c0 = 2 * (L & 3);
-        const uint32_t in[4] = {src.x, src.y, src.z, src.w};
-        uint32_t out[8];
+// 64 of a key's dims (half h) from a stage in shared memory, as pairs of bf16; codes are widened (exactly).
+template <int D, bool FP8>
+__device__ __forceinline__ void key_dims(const uint8_t* stage, int row, int h, uint32_t (&v)[32]) {
+  using S = Shape<D, FP8>;
+  const int sw = row & 7;
+  if constexpr (FP8) {
+    const uint8_t* at = stage + row * 128;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t a, b;
-          widen4(in[e], a, b);
-          const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
-          const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
-          out[2 * e] = pack_bf16x2(fa.x, fa.y);
-          out[2 * e + 1] = pack_bf16x2(fb.x, fb.y);
-        }
-        uint8_t* row = tile + h * 128 * 128 + r * 128;
-        *reinterpret_cast<uint4*>(row + ((c0 ^ sw) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
-        *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ sw) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
+    for (int i = 0; i < 4; ++i) {
+      const uint4 src = *reinterpret_cast<const uint4*>(at + (((4 * h + i) ^ sw) << 4));
+      const uint32_t in[4] = {src.x, src.y, src.z, src.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t lo, hi;
+        widen4(in[e], lo, hi);
+        const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+        const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+        v[8 * i + 2 * e] = pack_bf16x2(fl.x, fl.y);
+        v[8 * i + 2 * e + 1] = pack_bf16x2(fh.x, fh.y);
       }
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(c.bar + B_KEMPTY + k.st);
-      mbar_arrive(c.bar + B_WIDE);
+  } else {
+    const uint8_t* at = stage + (row >> 3) * 1024 * S::kHalves + h * 1024 + sw * 128;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 src = *reinterpret_cast<const uint4*>(at + ((i ^ sw) << 4));
+      v[4 * i] = src.x;
+      v[4 * i + 1] = src.y;
+      v[4 * i + 2] = src.z;
+      v[4 * i + 3] = src.w;
     }
-    k.next();
-    wd.next();
   }
 }
 
 // A warpgroup's 128 keys and half of the rows: thread = key.
 template <int D, bool FP8>
-__device__ void summer(const Ctx& c, const TreeParams& p, uint32_t tmem, uint32_t stall, const float* nl,
-                       const int* pos, const int4* info, float* sums) {
+__device__ void summer(const Ctx& c, const TreeParams& p, uint32_t tmem, uint32_t stall, const int* pos,
+                        const int4* info, float* sums) {
+  using S = Shape<D, FP8>;
   const VarlenMeta& m = p.m;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 4, x = warp >> 3, quad = warp & 3;
   const int half = (warp >> 2) & 1;  // of a row tile's columns
-  const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + 2 * x * kRows;
-  Ring<kLse> l;
-  uint32_t use = 0, pieces = 0;  // row tiles and pieces of this key half so far
+  const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+  Ring<1> k;
+  Ring<kPos> l;
+  Ring<kSums> s;
+  uint32_t pieces = 0;  // of this key half so far
+  bool first = true;
   Walk walk(p, blockIdx.x);
   Piece g;
   while (walk.next(p, g)) {
-    const bool mine = x == 0 || g.keys > 128;
+    const bool both = g.keys > 128, mine = x == 0 || both;
     const int low = g.key0 + 128 * x, key = low + 32 * quad + lane;
     const float sl = head_scale(m.k_scales, g.kvh, p.scale) * kLog2e;
     const uint64_t sl2 = f2_pack(sl, sl);
-    uint64_t sum[2] = {0, 0};
-    for (int r = g.r0; r < g.r1; ++r) {
-      if (!wait_all(c, B_LFULL + l.st, l.par)) return;
-      if (mine) {
-        const uint32_t buf = use & 1;
-        if (!wait_all(c, stall ? B_NEVER : B_SFULL + 2 * x + buf, stall ? 0u : (use >> 1) & 1)) return;
-        tc_fence_after();
-        const int4 t = info[l.st];
-        // every row of the tile sees all of the warpgroup's keys
-        const bool all = t.x >= low + 127 && (m.window <= 0 || low > t.y - m.window || low + 127 < p.first);
-        const float* tl = nl + l.st * 2 * kRows;
-        const int* tp = pos + l.st * 2 * kRows;
-#pragma unroll 1
-        for (int q = 2 * half; q < 2 * half + 2; ++q) {
-          uint32_t v[32];
-          tmem_ld32(lanes + buf * kRows + 32 * q, v);
-          tmem_wait_ld(v);
-          if (q & 1) {  // this half of the buffer has been read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(c.bar + B_SFREE + 2 * x + buf);
-          }
-          if (all && 32 * q + 32 <= t.z) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 n4 = *reinterpret_cast<const float4*>(tl + 32 * q + e);
-              float a, b;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2,
-                               f2_pack(n4.x, n4.y)), a, b);
-              sum[0] = f2_add(sum[0], f2_pack(fast_exp2(a), fast_exp2(b)));
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sl2,
-                               f2_pack(n4.z, n4.w)), a, b);
-              sum[1] = f2_add(sum[1], f2_pack(fast_exp2(a), fast_exp2(b)));
-            }
-          } else if (32 * q < t.z) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int ps = tp[32 * q + e];
-              const bool see = ps >= 0 && window_visible(p, ps, key);
-              const float a = see ? fast_exp2(fmaf(__uint_as_float(v[e]), sl, tl[32 * q + e])) : 0.f;
-              sum[0] = f2_add(sum[0], f2_pack(e & 1 ? 0.f : a, e & 1 ? a : 0.f));
-            }
-          }
-        }
-        ++use;
+    // K to tensor memory, where all of the item's products read it; each warp half of its keys' dims
+    if (!wait_all(c, B_KFULL, k.par)) return;
+    if (!first && !wait_all(c, B_KDONE, k.par ^ 1)) return;
+    if (mine && half < S::kHalves) {
+      uint32_t v[32];
+      key_dims<D, FP8>(c.sm + S::kOffK + x * S::kHalf, 32 * quad + lane, half, v);
+      tc_fence_after();
+      tmem_st32(lanes + kColK + x * (D / 2) + 32 * half, v);
+      tmem_wait_st();
+      tc_fence_before();
+    }
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(c.bar + B_KEMPTY);
+      mbar_arrive(c.bar + B_KREADY);
+    }
+    k.next();
+    first = false;
+    uint64_t sum[4] = {0, 0, 0, 0};
+    if (!mine) {  // (the first half's warps arrive for the second's)
+      for (int r = g.r0; r < g.r1; ++r) {
+        s.next();
+        l.next();
       }
+      continue;
+    }
+    for (int r = g.r0; r < g.r1; ++r) {
+      if (x) s.next();
+      // (the issuer has waited for the rows' numbers)
+      if (!wait_all(c, stall ? B_NEVER : B_SFULL + s.st, stall ? 0u : s.par)) return;
+      tc_fence_after();
+      uint32_t v[64];
+      tmem_ld64(lanes + s.st * kRows + 64 * half, v);
+      const int4 t = info[l.st];
+      // every row of the tile sees all of the warpgroup's keys
+      const bool all = t.x >= low + 127 && (m.window <= 0 || low > t.y - m.window || low + 127 < p.first);
+      const int* tp = pos + l.st * kRows + 64 * half;
+      tmem_wait_ld64(v);
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(c.bar + B_LFREE + l.st);
+      if (lane == 0) mbar_arrive(c.bar + B_SFREE + s.st);
+      if (all && t.z >= 64 * half + 64) {
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          float a, b;
+          f2_unpack(f2_mul(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2), a, b);
+          sum[(e >> 1) & 3] = f2_add(sum[(e >> 1) & 3], f2_pack(fast_exp2(a), fast_exp2(b)));
+        }
+      } else if (t.z > 64 * half) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+          const int ps = tp[e];
+          const bool see = ps >= 0 && window_visible(p, ps, key);
+          const float a = see ? fast_exp2(__uint_as_float(v[e]) * sl) : 0.f;
+          sum[e & 1] = f2_add(sum[e & 1], f2_pack(a, 0.f));
+        }
+      }
+      s.next();
+      if (!x && both) s.next();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(c.bar + B_PFREE + l.st);
+        if (!both) mbar_arrive(c.bar + B_PFREE + l.st);
+      }
       l.next();
     }
     float a, b, d, e;
-    f2_unpack(sum[0], a, b);
-    f2_unpack(sum[1], d, e);
+    f2_unpack(f2_add(sum[0], sum[1]), a, b);
+    f2_unpack(f2_add(sum[2], sum[3]), d, e);
     float total = (a + b) + (d + e);
-    if (!mine) continue;
     // the second half's sums go to the first
     float* other = sums + 128 * x + 32 * quad + lane;
     if (half) {
@@ -522,15 +541,22 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     flags[1] = 0;
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
-      if ((FP8 && i >= B_KEMPTY && i < B_KEMPTY + 2) || i == B_WIDE) n = 4;
-      if (i >= B_SFREE && i < B_SFREE + 4) n = 8;
-      if (i >= B_LFREE && i < B_LFREE + kLse) n = 16;
+      if (i == B_KEMPTY || i == B_KREADY) n = 16;
+      if (i >= B_SFREE && i < B_SFREE + kSums) n = 8;
+      if (i >= B_QFULL && i < B_QFULL + kQueries) n = 2;
+      if (i >= B_PFREE && i < B_PFREE + kPos) n = 16;
       if (i >= B_HALF && i < B_TAKEN + 2) n = 4;
       mbar_init(bar + i, n);
     }
     prefetch_tmap(&tq);
     prefetch_tmap(&tk);
   }
+  for (int i = threadIdx.x; i < 128 * 8; i += S::kThreads) {  // the rows of log-sum-exps and ones
+    const int chunk = (i & 7) ^ ((i >> 3) & 7);
+    *reinterpret_cast<uint4*>(sm + S::kOffLse + 16 * i) =
+        chunk == 2 * kQueries ? make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
   fence_mbar_init();
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -552,8 +578,7 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
   const Ctx c{sm, bar, reinterpret_cast<volatile int*>(flags + 1), p.status, wait_limit};
-  float* nl = reinterpret_cast<float*>(sm + S::kOffRow);
-  int* pos = reinterpret_cast<int*>(sm + S::kOffRow) + kRows;
+  int* pos = reinterpret_cast<int*>(sm + S::kOffPos);
   int4* info = reinterpret_cast<int4*>(sm + S::kOffInfo);
   if (flags[0] == 0) {
     if (warp == 0) {
@@ -565,12 +590,10 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
       commit(bar + B_FIN);
       if ((threadIdx.x & 31) == 0) mbar_wait(bar + B_FIN, 0, 1000000000ull);
       __syncwarp();
-    } else if (warp == 2 || warp == 3) {
-      row_loader(c, p, warp - 2, nl, pos, info);
-    } else if (warp >= 20) {
-      if constexpr (FP8) widener<D>(c, p);
+    } else if (warp == 2) {
+      row_loader(c, p, sm + S::kOffLse, pos, info);
     } else if (warp >= 4) {
-      summer<D, FP8>(c, p, tmem, stall, nl, pos, info, reinterpret_cast<float*>(sm + S::kOffHalf));
+      summer<D, FP8>(c, p, tmem, stall, pos, info, reinterpret_cast<float*>(sm + S::kOffHalf));
     }
   }
   tc_fence_before();
