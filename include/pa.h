@@ -752,7 +752,10 @@ size_t pa_window_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, 
  * decoding tokens.  out = softmax(scale * q . K) V over those keys; a row with a score of NaN or +inf
  * gets NaN in out and lse.  Types, sinks (logits, besides the first tokens), lse, k_scale / v_scale and
  * k_scales / v_scales as in pa_varlen_forward_ex and pa_varlen_forward_per_head (a per-head array needs
- * a scalar of 1); kv_dtype PA_FP8_E4M3 rounds as in pa_tree_attention.
+ * a scalar of 1).  bf16 q over e4m3 pools enters the products with 17 bits of its row's largest element
+ * or more (a row with an infinity comes out as NaN).  Softmax weights enter the products with V with 16
+ * bits, of large batches of prompt chunks, and over e4m3 pools, with 11 (f16); those batches' bf16 V as
+ * f16, exact from 2^-14 on and off by 2^-25 at most below.
  * K rows of keys that a token does not see may hold anything.  So may V rows at or past seq_lens[s],
  * and those of blocks between the first tokens' and the first that the sequence's tokens reach: these
  * are not read, and their table entries not looked at (a server may have given them away).  All other V
@@ -764,6 +767,8 @@ size_t pa_window_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, 
  * [0, seq_lens[s]) and do not decrease; per-head scales finite and positive.  Failures record PA_EINVAL
  * and leave out and lse untouched.  sliding_window and first_tokens >= 0 (PA_EINVAL).  A call without
  * tokens does nothing.
+ * A batch with num_tokens <= num_seqs is taken for one of decoding tokens: a prompt chunk among as many
+ * sequences without tokens is right, but slow (leave those sequences out).
  * workspace: pa_window_attention_workspace_size(...) bytes, 256-byte aligned, scratch of the caller
  * that calls which overlap on the device must not share.  The results depend on the inputs alone (no
  * atomics on values); how keys are split, and so the last bits of a row, depend on the whole batch.
@@ -792,7 +797,8 @@ size_t pa_attention_key_weights_workspace_size(int32_t num_seqs, int64_t num_tok
  * (of a long prompt, say), 0 all of them.  key_weights [num_seqs, num_kv_heads, weights_len] fp32
  * DEVICE; entries of keys that no counted token sees, and those at or past seq_lens[s], are left as
  * they are.  A sequence with tokens and seq_lens[s] > weights_len is refused (PA_EINVAL recorded), and a
- * refused call leaves key_weights untouched, too.  A row whose lse is NaN spoils the keys it sees.
+ * refused call leaves key_weights untouched, too.  A row whose lse is NaN spoils the keys it sees, and no
+ * others.  Weights below 2^-126 may count as 0; scale * k_scale >= 2^-100.
  * All other arguments, results and errors as pa_window_attention, and its workspace
  * pa_attention_key_weights_workspace_size(...) bytes.
  */
@@ -827,7 +833,8 @@ size_t pa_evict_keys_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int3
  * positions with ids in [0, num_blocks) (where keys are evicted), n <= weights_len (given weights):
  * otherwise PA_EINVAL is recorded and nothing is written.  A block that is written belongs to one
  * sequence only.  num_seqs and num_kv_heads <= 65535 and at most 524288 keys to a sequence (the smaller
- * of the table's width and, given weights, weights_len), else PA_EUNSUPPORTED.
+ * of the table's width and, given weights, weights_len), num_blocks * block_size < 2^31, else
+ * PA_EUNSUPPORTED.
  * workspace: pa_evict_keys_workspace_size(...) bytes, 256-byte aligned, scratch of the caller that calls
  * which overlap on the device must not share.
  */
