@@ -20,6 +20,11 @@
 // row needs only to have read a batch of rows before it writes the batch; it reads one batch ahead.  The
 // CTAs of a cluster take parts of the rows (of K's and V's together), each for itself: there is no order
 // between them but that the weights are moved when all have read them.
+//
+// What bounds it: memory, at 0.71 of the copy rate (rows of 256 bytes, read and written in places of their own:
+// half of 64 prompts of 2048 to 8192 keys, 720 MB, 147 to 152 us by the box; 256 sequences cut by 2 %, e4m3, 120 to
+// 129 us for 84); one
+// sequence a chain of latencies (metadata, weights, histogram, places, rows: 11.4 us).
 #include <algorithm>
 
 #include "pa_internal.cuh"
@@ -96,7 +101,7 @@ __device__ __forceinline__ void cluster_wait() {
 // the list lies in the workspace, written by the cluster's first CTA.
 template <typename T, int NT, int E>
 __global__ void __launch_bounds__(NT, (NT == 1024 ? 1 : 1536 / NT))
-    k_evict(const EvictParams p, int cluster, int row_words, int part_words) {
+    k_evict(const EvictParams p, int cluster, int row_words, int part_words, int ordered) {
   extern __shared__ __align__(16) uint8_t s_mem[];
   __shared__ __align__(16) int s_work[kBins];  // histogram; then the moves' places, kMoves int2
   static_assert(kMoves * 8 <= kBins * 4, "places");
@@ -104,7 +109,26 @@ __global__ void __launch_bounds__(NT, (NT == 1024 ? 1 : 1536 / NT))
   __shared__ int3 s_found;  // bin, keys in larger ones, keys in it
   __shared__ int s_left;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = blockIdx.x % cluster, g = blockIdx.x / cluster, s = blockIdx.y;
+  const int rank = blockIdx.x % cluster, g = blockIdx.x / cluster;
+  int s = blockIdx.y;
+  if (ordered) {  // the longest sequences come first, to a 64th of the most keys; those that are not cut last
+    const int n = tid < p.num_seqs ? p.seq_lens[tid] : 0;
+    const bool cut = tid < p.num_seqs && p.new_lens[tid] < n;
+    const int bin = !cut ? 64 : 63 - (int)(min((int64_t)max(n, 0), p.moves_len) * 63 / max(p.moves_len, (int64_t)1));
+    int total;
+    if (tid <= 64) s_work[tid] = 0;
+    __syncthreads();
+    if (tid < p.num_seqs) atomicAdd(&s_work[bin], 1);
+    __syncthreads();
+    const int here = tid <= 64 ? s_work[tid] : 0, before = block_exclusive_scan(here, s_warp, &total);
+    if (before <= s && s < before + here) s_found = make_int3(tid, s - before, 0);
+    __syncthreads();
+    const int mine = tid < p.num_seqs && bin == s_found.x, at = block_exclusive_scan(mine, s_warp, &total);
+    if (mine && at == s_found.y) s_left = tid;
+    __syncthreads();
+    s = s_left;
+    __syncthreads();  // (the words are used again)
+  }
   const int64_t unit = (int64_t)s * p.num_kv_heads + g;
   const Plan e = evict_plan(p, s);
   if (evict_bad(p, e) || e.to >= e.n) {
@@ -357,7 +381,7 @@ __global__ void __launch_bounds__(NT, (NT == 1024 ? 1 : 1536 / NT))
 }
 
 template <typename T, int NT, int E>
-cudaError_t evict_as(const EvictParams& p, int cluster, cudaStream_t stream) {
+cudaError_t evict_as(const EvictParams& p, int cluster, int num_sms, cudaStream_t stream) {
   const int row_words = (int)(p.row_bytes / sizeof(T));
   const int part = (2 * row_words + cluster - 1) / cluster;
   const int smem = (int)(2 * NT * E + (p.moves_len + 31) / 32 * 8);
@@ -377,15 +401,20 @@ cudaError_t evict_as(const EvictParams& p, int cluster, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, p, cluster, row_words, part);
+  // longest first where a second wave of CTAs is begun but not filled, so that it is of short sequences (half of
+  // 64 prompts of 2048 to 8192, 512 units for 456 places, 158 -> 147 us; of 80 212 -> 190; of 128, 2.2 waves,
+  // 297 either way, and 256 sequences of equal length 1.5 us more)
+  const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads, resident = num_sms * (NT == 1024 ? 1 : 1536 / NT);
+  const int ordered = cluster == 1 && units > resident && units < 2 * resident && p.num_seqs <= NT;
+  return cudaLaunchKernelEx(&cfg, kern, p, cluster, row_words, part, ordered);
 }
 
 template <typename T>
-cudaError_t evict_keys(const EvictParams& p, int cluster, cudaStream_t stream) {
+cudaError_t evict_keys(const EvictParams& p, int cluster, int num_sms, cudaStream_t stream) {
   const int64_t keys = p.moves_len;  // at most
-  if (keys <= 2048) return evict_as<T, 256, 8>(p, cluster, stream);
-  if (keys <= 8192) return evict_as<T, 512, 16>(p, cluster, stream);
-  return evict_as<T, 1024, 0>(p, cluster, stream);
+  if (keys <= 2048) return evict_as<T, 256, 8>(p, cluster, num_sms, stream);
+  if (keys <= 8192) return evict_as<T, 512, 16>(p, cluster, num_sms, stream);
+  return evict_as<T, 1024, 0>(p, cluster, num_sms, stream);
 }
 
 }  // namespace
@@ -405,9 +434,9 @@ cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream)
   while (cluster > 1 && units * cluster > 2 * num_sms) cluster /= 2;
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.k_blocks) | reinterpret_cast<uintptr_t>(p.v_blocks) |
                        (uintptr_t)p.row_bytes;
-  if (at % 16 == 0) return evict_keys<uint4>(p, cluster, stream);
-  if (at % 4 == 0) return evict_keys<uint32_t>(p, cluster, stream);
-  return evict_keys<uint8_t>(p, cluster, stream);
+  if (at % 16 == 0) return evict_keys<uint4>(p, cluster, num_sms, stream);
+  if (at % 4 == 0) return evict_keys<uint32_t>(p, cluster, num_sms, stream);
+  return evict_keys<uint8_t>(p, cluster, num_sms, stream);
 }
 
 }  // namespace pa

@@ -280,3 +280,15 @@ def test_python_refusals(pa):
         pa.pa_evict_keys(a["k_blocks"], a["v_blocks"], a["block_tables"], a["seq_lens"], a["seq_lens"],
                          keep_first=-1)
     assert pa.pa_device_status() == pa.PA_OK
+
+
+@pytest.mark.parametrize("S,longest", [(120, 1900), (70, 3500)])
+def test_evictions_longest_first(pa, S, longest):
+    """More (sequence, kv head) units than are resident at once, but not twice as many; some sequences stay."""
+    from tests.test_gpu_evict import Cache
+
+    g = torch.Generator().manual_seed(S)
+    lens = torch.randint(1, longest, (S,), generator=g).tolist()
+    lens[5] = 0
+    new = [n if i % 7 == 0 else n + 3 if i % 11 == 0 else n // 2 for i, n in enumerate(lens)]
+    Cache(lens, 8, 64, seed=S).check(pa, new, 4, 30)
