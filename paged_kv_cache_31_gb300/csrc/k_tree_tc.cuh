@@ -1,8 +1,9 @@
 // k_tree_tc.cuh -- tree attention on the 5th-generation tensor cores (tcgen05.mma, accumulators in
 // tensor memory), for bf16 queries over bf16 (head size 64 / 128) or e4m3 (128) pools of 16-position
-// blocks; k_tree_tc.cu launches it.  With WIN it is the attention behind a window with first tokens
+// blocks; k_tree_tc.cu launches it.  kWindow is the attention behind a window with first tokens
 // (k_window_tc.cu): the same kernel over items whose keys are counted without the gap between the
-// first tokens' blocks and the window's, every row's visible keys being two runs of them.
+// first tokens' blocks and the window's, every row's visible keys being two runs of them.  kMarked does
+// those items again that k_prefill_tc.cu marked, whole ones, a CTA each in turn.
 //
 // Work.  One CTA per SM walks its share of the items' key tiles (k_tree.cu, k_window.cu cut them).  An item is
 // one (sequence, kv head) and up to two tiles of query rows; a row tile is whole nodes times the
@@ -31,7 +32,7 @@
 // hold anything; K's are masked); warps 4..7 and 8..11: the streams' softmax and epilogue; warps
 // 12..15 (e4m3 pools): split Q and widen V into one of two f16 tiles.
 //
-// Small calls (CL).  Instead of the planned shares, a cluster of 1 to 8 CTAs for each (sequence, kv
+// Small calls (kClusters).  Instead of the planned shares, a cluster of 1 to 8 CTAs for each (sequence, kv
 // head, item): each CTA plans its own part from the sequence's numbers (an even run of the key
 // tiles), its softmax warps check the whole batch while the first tiles are on their way, and the
 // CTAs' states are joined in key order through distributed shared memory.  One launch instead of

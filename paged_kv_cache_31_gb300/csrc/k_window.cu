@@ -14,6 +14,9 @@
 // The items' tiles are laid end to end, weighted, and cut into equal shares, one contiguous range
 // per CTA; the pieces of a cut item are merged in key order (k_tree.cu).  Chunks of prompts and
 // decoding tokens lie in the same list, so some SMs stream keys while others compute.
+// Large batches of chunks go to the prefill kernel instead (k_prefill_tc.cu): whole items, the longest
+// first, on as many pairs of SMs as end together with the decoding sequences on the others
+// (k_window_decode.cu).  Batches of decoding tokens alone are not planned, only checked.
 #include <algorithm>
 
 #include "k_tree_generic.cuh"

@@ -16,7 +16,7 @@
 // makes a lane's bytes contiguous.
 //
 // Weights.  exp(s - lse) needs a row's final log-sum-exp, so a CTA keeps the scores of its keys in shared
-// memory (15 KB: 936 keys of 4 heads) or, where they are more, in the workspace (they stay in L2) until
+// memory (14 KB: 872 keys of 4 heads) or, where they are more, in the workspace (they stay in L2) until
 // the states have been joined, and adds each key's sum to memory then: K is read once, where a second
 // pass over it would read half as many bytes again.  Keys past that room are multiplied once more.  One
 // thread adds to a key, so the order of the sums is fixed.
@@ -27,8 +27,8 @@
 //
 // What bounds it: the K / V bytes for large batches (64 sequences behind a window of 4096: 158 us, the
 // copy rate; 64 of 512 to 4096 keys with their weights 101 us, 0.93 of it), for small ones a chain of
-// latencies (metadata, table, keys, joins: 1 sequence, window 4096: 13.4 us), over e4m3 pools both (48
-// sequences, window 1024: 23.2 us for 15).
+// latencies (metadata, table, keys, joins: 1 sequence, window 4096: 11.4 us), over e4m3 pools both (48
+// sequences, window 1024: 22.7 us for 15).
 #include <algorithm>
 #include <cfloat>
 

@@ -1,5 +1,7 @@
 // k_window_tc.cu -- launches of the attention behind a window with first tokens on the tensor cores
-// (k_tree_tc.cuh, WIN).
+// (k_tree_tc.cuh, kWindow and kMarked): batches of prompt chunks that are too small for k_prefill_tc.cu, of
+// head size 64 or of a group that 128 rows are no multiple of, cut into even shares (2 chunks of 300 and 500
+// tokens behind 1000 and 3000 positions, 32 + 8 heads: 60 us, e4m3 61), and the items it marked.
 #include "k_tree_tc.cuh"
 
 namespace pa {
