@@ -11,20 +11,21 @@
 //
 // Selection.  The m-th largest weight by histograms over 11, 11 and 10 bits of its order-preserving integer
 // form (the first covers exponent and two bits of the fraction, so its bins seldom collide), or, as soon
-// as a bin holds no more keys than there are threads, by comparing each of these with all; then two
+// as a bin holds 128 keys at most, by comparing each of these with all; then two
 // bitmaps, of the larger keys and of the equal ones, whose prefix sums number the places and the keys that
 // fill them.  (Bisection, two bits a step, took 2.6 times as many instructions and bound the selection.)
 //
 // Moves.  Pure data movement, bound by memory.  A sequence's moves in list order (the fillers, then the
 // recent rows, ascending) never write a row that a later one reads, so a CTA that moves its part of every
-// row needs only to have read a batch of rows before it writes the batch; it reads one batch ahead.  The
-// CTAs of a cluster take parts of the rows (of K's and V's together), each for itself: there is no order
-// between them but that the weights are moved when all have read them.
+// row needs only to have read a batch of rows before it writes the batch; it reads several batches ahead,
+// asynchronously, into shared memory.  The CTAs of a cluster take parts of the rows (of K's and V's
+// together), each for itself: there is no order between them but that the weights are moved when all have
+// read them.
 //
-// What bounds it: memory, at 0.71 of the copy rate (rows of 256 bytes, read and written in places of their own:
-// half of 64 prompts of 2048 to 8192 keys, 720 MB, 147 to 152 us by the box; 256 sequences cut by 2 %, e4m3, 120 to
-// 129 us for 84); one
-// sequence a chain of latencies (metadata, weights, histogram, places, rows: 11.4 us).
+// What bounds it: memory, at 0.74 of the copy rate (rows of 256 bytes, read and written in places of their own:
+// half of 64 prompts of 2048 to 8192 keys, 720 MB, 144 us, of which the first 16 select; 256 sequences cut by
+// 2 %, e4m3, 112 us for 76); one sequence a chain of latencies (metadata, weights, histogram, places, rows:
+// 10.9 us).
 #include <algorithm>
 
 #include "pa_internal.cuh"
@@ -96,12 +97,30 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// A word from global to the thread's own place in shared memory (4 bytes or more: asynchronously).
+template <typename T>
+__device__ __forceinline__ void copy_async(T* dst, const T* src) {
+  if constexpr (sizeof(T) == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else if constexpr (sizeof(T) == 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    *dst = *src;
+}
+
+// CTAs of an SM, and batches of rows (a word of each thread) on their way or landed: what shared memory holds.
+// (256 sequences of 1030 to 1060 keys, e4m3: 3 batches 133 us, 4 125, 5 118, 6 116, 7 114, 10 119; half of 64 prompts
+// by 512 threads: 3 159, 4 153, 6, three CTAs still, 152, 8 147; through registers, two rows a thread in two
+// batches, 128 and 148.)
+constexpr int per_sm(int nt) { return nt == 1024 ? 1 : nt == 512 ? 2 : 5; }
+constexpr int stages(int nt) { return nt == 1024 ? 4 : nt == 512 ? 8 : 7; }
+
 // E > 0: sequences of at most NT * E keys; a thread keeps the ordered forms of E weights in registers, and
 // the list of fillers (from, to) lies in shared memory.  E = 0: weights are read again in every pass, and
 // the list lies in the workspace, written by the cluster's first CTA.
 template <typename T, int NT, int E>
-__global__ void __launch_bounds__(NT, (NT == 1024 ? 1 : 1536 / NT))
-    k_evict(const EvictParams p, int cluster, int row_words, int part_words, int ordered) {
+__global__ void __launch_bounds__(NT, per_sm(NT))
+    k_evict(const EvictParams p, int cluster, int row_words, int part_words, int ordered, int ring_at) {
   extern __shared__ __align__(16) uint8_t s_mem[];
   __shared__ __align__(16) int s_work[kBins];  // histogram; then the moves' places, kMoves int2
   static_assert(kMoves * 8 <= kBins * 4, "places");
@@ -198,7 +217,7 @@ __global__ void __launch_bounds__(NT, (NT == 1024 ? 1 : 1536 / NT))
       need -= s_found.y;
       const int in = s_found.z;
       if (need == in) break;  // all of the bin's keys are taken
-      if (in <= NT) {
+      if (in <= min(NT, 128)) {
         // few are left: each is compared with all others
         each_key([&](uint32_t k) {
           if (k >> shift == at >> shift) s_work[atomicAdd(&s_left, 1)] = (int)k;
@@ -268,14 +287,31 @@ __global__ void __launch_bounds__(NT, (NT == 1024 ? 1 : 1536 / NT))
     }
     int f0 = block_exclusive_scan(mine, s_warp, &fillers);
     int h0 = block_exclusive_scan(holes, s_warp, &total);
-    if (E > 0 || rank == 0)
+    if constexpr (E > 0) {
+      // a warp to a word, a lane to a key (a thread that wrote its word's list key by key took 2 us)
+      int2* starts = reinterpret_cast<int2*>(s_work);
+      static_assert(NT * E / 32 * 8 <= kBins * 4, "starts");
+      for (int i = w0; i < w1; ++i) {
+        starts[i] = make_int2(f0, h0);
+        f0 += __popc(more[i]);
+        h0 += __popc(same[i]);
+      }
+      __syncthreads();
+      const uint32_t below = (1u << lane) - 1u;
+      for (int i = warp; i < words; i += NT / 32) {
+        const uint32_t b = more[i], c = same[i];
+        const int2 at = starts[i];
+        const uint16_t key = (uint16_t)(e.first + 32 * i + lane);
+        if (b >> lane & 1u) near_list[at.x + __popc(b & below)] = key;
+        if (c >> lane & 1u) near_list[kNear + at.y + __popc(c & below)] = key;
+      }
+    } else if (rank == 0) {
       for (int i = w0; i < w1; ++i) {
         const int at0 = e.first + 32 * i - 1;
-        for (uint32_t b = more[i]; b; b &= b - 1, ++f0)
-          if constexpr (E > 0) near_list[f0] = (uint16_t)(at0 + __ffs(b)); else far_list[f0] = at0 + __ffs(b);
-        for (uint32_t b = same[i]; b; b &= b - 1, ++h0)
-          if constexpr (E > 0) near_list[kNear + h0] = (uint16_t)(at0 + __ffs(b)); else far_list[far_to + h0] = at0 + __ffs(b);
+        for (uint32_t b = more[i]; b; b &= b - 1, ++f0) far_list[f0] = at0 + __ffs(b);
+        for (uint32_t b = same[i]; b; b &= b - 1, ++h0) far_list[far_to + h0] = at0 + __ffs(b);
       }
+    }
     __syncthreads();
   }
   if (cluster > 1) {  // every CTA has read the weights, the list is there
@@ -331,32 +367,19 @@ __global__ void __launch_bounds__(NT, (NT == 1024 ? 1 : 1536 / NT))
     if (id < 0 || (int64_t)id >= p.num_blocks) return -1;
     return id * p.block_size + o;
   };
-  constexpr int U = 2;  // rows of a thread's batch
+  constexpr int D = stages(NT);
+  T* ring = reinterpret_cast<T*>(s_mem + ring_at);  // [stage][thread]: what the thread itself reads and writes
   int2* places = reinterpret_cast<int2*>(s_work);  // slots (from, to); to -1: nothing is moved
   const int64_t stride = (int64_t)p.num_kv_heads * row_words;
   // this CTA's words of a row of K and of V laid end to end, up to NT at a time
   const int x_end = min(2 * row_words, (rank + 1) * part_words);
   for (int x0 = rank * part_words; x0 < x_end; x0 += NT) {
-    const int width = min(NT, x_end - x0), step = NT / width, batch = U * step;
+    const int width = min(NT, x_end - x0), step = NT / width;  // rows of a batch
     const int x = x0 + tid % width, row = tid / width;
     T* mine = x < row_words ? static_cast<T*>(p.k_blocks) + (int64_t)g * row_words + x
                             : static_cast<T*>(p.v_blocks) + (int64_t)g * row_words + (x - row_words);
-    auto read = [&](int b, int here, T (&v)[U], int (&dst)[U]) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = b + u * step + row;
-        const int2 a = row < step && i < here ? places[i] : make_int2(-1, -1);
-        dst[u] = a.y;
-        if (a.y >= 0) v[u] = mine[a.x * stride];
-      }
-    };
-    auto write = [&](const T (&v)[U], const int (&dst)[U]) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (dst[u] >= 0) mine[dst[u] * stride] = v[u];
-    };
     for (int base = 0; base < moves; base += kMoves) {
-      const int here = min(kMoves, moves - base);
+      const int here = min(kMoves, moves - base), batches = (here + step - 1) / step;
       __syncthreads();  // the places before (or the histogram) have been used
       for (int i = tid; i < here; i += NT) {
         int2 a;
@@ -365,17 +388,25 @@ __global__ void __launch_bounds__(NT, (NT == 1024 ? 1 : 1536 / NT))
         places[i] = a;
       }
       __syncthreads();
-      T va[U], vb[U];
-      int ta[U], tb[U];
-      read(0, here, va, ta);
-      for (int i = 0; i < here; i += 2 * batch) {
-        read(i + batch, here, vb, tb);
+      auto place = [&](int batch) {
+        const int i = batch * step + row;
+        return row < step && i < here ? places[i] : make_int2(-1, -1);
+      };
+      auto read = [&](int batch) {
+        const int2 a = place(batch);
+        if (a.y >= 0) copy_async(ring + batch % D * NT + tid, mine + a.x * stride);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll
+      for (int i = 0; i < D - 1; ++i) read(i);
+      for (int i = 0; i < batches; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory");
         __syncthreads();  // batch i has been read by all
-        write(va, ta);
-        read(i + 2 * batch, here, va, ta);
-        __syncthreads();
-        write(vb, tb);
+        const int2 a = place(i);
+        if (a.y >= 0) mine[a.y * stride] = ring[i % D * NT + tid];
+        read(i + D - 1);
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   }
 }
@@ -384,7 +415,8 @@ template <typename T, int NT, int E>
 cudaError_t evict_as(const EvictParams& p, int cluster, int num_sms, cudaStream_t stream) {
   const int row_words = (int)(p.row_bytes / sizeof(T));
   const int part = (2 * row_words + cluster - 1) / cluster;
-  const int smem = (int)(2 * NT * E + (p.moves_len + 31) / 32 * 8);
+  const int ring_at = (int)((2 * NT * E + (p.moves_len + 31) / 32 * 8 + 15) / 16 * 16);
+  const int smem = ring_at + stages(NT) * NT * (int)sizeof(T);
   auto kern = k_evict<T, NT, E>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -401,12 +433,12 @@ cudaError_t evict_as(const EvictParams& p, int cluster, int num_sms, cudaStream_
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  // longest first where a second wave of CTAs is begun but not filled, so that it is of short sequences (half of
-  // 64 prompts of 2048 to 8192, 512 units for 456 places, 158 -> 147 us; of 80 212 -> 190; of 128, 2.2 waves,
-  // 297 either way, and 256 sequences of equal length 1.5 us more)
-  const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads, resident = num_sms * (NT == 1024 ? 1 : 1536 / NT);
-  const int ordered = cluster == 1 && units > resident && units < 2 * resident && p.num_seqs <= NT;
-  return cudaLaunchKernelEx(&cfg, kern, p, cluster, row_words, part, ordered);
+  // longest first where the last of few waves of CTAs is not filled, so that it is of short sequences (half of 64
+  // prompts of 2048 to 8192, 512 units for 304 places, 156 -> 145 us; of 80 203 -> 197; of 128, 3.4 waves, 286
+  // and 290; of 24 of 9000 to 30000 290 -> 228; 256 sequences of equal length 1.5 us more)
+  const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads, resident = num_sms * per_sm(NT);
+  const int ordered = cluster == 1 && units > resident && 2 * units < 5 * resident && p.num_seqs <= NT;
+  return cudaLaunchKernelEx(&cfg, kern, p, cluster, row_words, part, ordered, ring_at);
 }
 
 template <typename T>
