@@ -767,6 +767,7 @@ size_t pa_window_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, 
  * [0, seq_lens[s]) and do not decrease; per-head scales finite and positive.  Failures record PA_EINVAL
  * and leave out and lse untouched.  sliding_window and first_tokens >= 0 (PA_EINVAL).  A call without
  * tokens does nothing.
+ * The outputs overlap no input and not one another.
  * A batch with num_tokens <= num_seqs is taken for one of decoding tokens: a prompt chunk among as many
  * sequences without tokens is right, but slow (leave those sequences out).
  * workspace: pa_window_attention_workspace_size(...) bytes, 256-byte aligned, scratch of the caller

@@ -292,3 +292,17 @@ def test_evictions_longest_first(pa, S, longest):
     lens[5] = 0
     new = [n if i % 7 == 0 else n + 3 if i % 11 == 0 else n // 2 for i, n in enumerate(lens)]
     Cache(lens, 8, 64, seed=S).check(pa, new, 4, 30)
+
+
+@pytest.mark.parametrize("D,bs", [(64, 16), (1, 16)])
+def test_eviction_with_the_most_keys(pa, D, bs):
+    """Tables and weights for 524288 keys: the largest lists and the least room beside them."""
+    from tests.test_gpu_evict import Cache
+
+    c = Cache([30000, 700], 1, D, bs=bs, seed=9)
+    tables = torch.full((2, 524288 // bs), -3, dtype=torch.int32, device="cuda")
+    tables[:, :c.tables.shape[1]] = c.tables
+    w = torch.zeros(2, 1, 524288, device="cuda")
+    w[:, :, :c.w.shape[2]] = c.w
+    c.tables, c.w = tables, w
+    c.check(pa, [17000, 600], 4, 500)
