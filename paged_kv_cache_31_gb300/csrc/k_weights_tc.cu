@@ -429,6 +429,8 @@ __device__ void summer(const Ctx& c, const TreeParams& p, uint32_t tmem, uint32_
     const int low = g.key0 + 128 * x, key = low + 32 * quad + lane;
     const float sl = head_scale(m.k_scales, g.kvh, p.scale) * kLog2e;
     const uint64_t sl2 = f2_pack(sl, sl);
+    // the last position that sees the key
+    const int last = m.window > 0 && key >= p.first ? (int)min((int64_t)key + m.window - 1, (int64_t)INT_MAX) : INT_MAX;
     // K to tensor memory, where all of the item's products read it; each warp half of its keys' dims
     if (!wait_all(c, B_KFULL, k.par)) return;
     if (!first && !wait_all(c, B_KDONE, k.par ^ 1)) return;
@@ -479,11 +481,13 @@ __device__ void summer(const Ctx& c, const TreeParams& p, uint32_t tmem, uint32_
         }
       } else if (t.z > 64 * half) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) {
-          const int ps = tp[e];
-          const bool see = ps >= 0 && window_visible(p, ps, key);
-          const float a = see ? fast_exp2(__uint_as_float(v[e]) * sl) : 0.f;
-          sum[e & 1] = f2_add(sum[e & 1], f2_pack(a, 0.f));
+        for (int e = 0; e < 64; e += 4) {
+          const int4 ps = *reinterpret_cast<const int4*>(tp + e);
+          auto one = [&](int at, int i) {  // (-1, no row, is below every key)
+            return at >= key && at <= last ? fast_exp2(__uint_as_float(v[e + i]) * sl) : 0.f;
+          };
+          sum[0] = f2_add(sum[0], f2_pack(one(ps.x, 0), one(ps.y, 1)));
+          sum[1] = f2_add(sum[1], f2_pack(one(ps.z, 2), one(ps.w, 3)));
         }
       }
       s.next();
