@@ -16,17 +16,17 @@
 // the pieces of a cut item leave partial sums, which k_weights_join adds in order.
 //
 // Roles.  warp 0: TMA of K (256 keys) and Q (a ring of three row tiles); warp 1: tensor-memory owner,
-// issues S^T; warp 2: the rows' log-sum-exps into the ring and their positions; warps 4..19:
-// exponentials and sums, a warpgroup for 128 keys and 64 rows of a row tile each, from three S^T buffers
-// (two warpgroups, of all rows, left the schedulers idle half of the time); at an item's start they take
-// K from shared to tensor memory, e4m3 codes widened to bf16 exactly.
+// issues S^T; warp 2: the rows' log-sum-exps into the ring and their positions; warps 4..19: exponentials
+// and sums, two warpgroups for 128 keys each, which take the row tiles in turn, from three S^T buffers (half of
+// every row tile to each: 9 us more; one warpgroup for 128 keys left the schedulers idle half of the time); at
+// an item's start they take K from shared to tensor memory, e4m3 codes widened to bf16 exactly.
 //
-// What bounds it: a chain.  A row tile of a prompt of 8191 tokens (8 x 4 heads, 245 us in all) takes some
-// 2000 cycles, of which its products take 1150, its 32768 exponentials 1024 of the SFU and its instructions
-// 1200 of the schedulers; a warp waits for S^T, loads it and sums it in turn.  K from shared memory with
-// log-sum-exps read by each thread: 275 us, shared memory four fifths busy.  Tried without gain: two issuing
-// warps, a look at the next tile's waits between products (252), halves of a tile loaded while the halves
-// before are summed (311: the buffers are held longer).
+// What bounds it: three buffers.  A row tile of a prompt of 8191 tokens (8 x 4 heads, 237 us in all) takes some
+// 1900 cycles, of which its products take 1150, its 32768 exponentials 1024 of the SFU and its instructions
+// 1100 of the schedulers; but a buffer is held by the products into it, a wait, and half of its sums.  K from
+// shared memory, a fourth buffer, with log-sum-exps read by each thread: 275 us, shared memory four fifths
+// busy.  Tried without gain: two issuing warps, a look at the next tile's waits between products, 32 columns
+// loaded while the 32 before are summed (311: the buffers are held longer).
 #include <algorithm>
 
 #include "k_tree.cuh"
@@ -56,7 +56,7 @@ struct Shape {
   static_assert(kQueries == 3, "the stages and the ones fill a row");
   static constexpr int kOffPos = kOffLse + 128 * 128;          // [kPos][128]
   static constexpr int kOffInfo = kOffPos + kPos * kRows * 4;  // [kPos] int4
-  static constexpr int kOffHalf = kOffInfo + kPos * 16;  // [key half][128]: sums of the second row halves
+  static constexpr int kOffHalf = kOffInfo + kPos * 16;  // [key half][128]: sums of the second warpgroups
   static constexpr int kOffBar = kOffHalf + 2 * 128 * 4;
   static constexpr int kOffMisc = kOffBar + 40 * 8;
   static constexpr int kSmem = kOffMisc + 16;
@@ -70,10 +70,10 @@ enum : int {
   B_KDONE = B_KREADY + 1,   // all its products are done
   B_QFULL = B_KDONE + 1,        // a row tile's queries landed, its numbers are there
   B_QEMPTY = B_QFULL + kQueries,
-  B_SFULL = B_QEMPTY + kQueries,
-  B_SFREE = B_SFULL + kSums,
+  B_SFULL = B_QEMPTY + kQueries,  // [key half][warpgroup][its tiles in turn]
+  B_SFREE = B_SFULL + 8,          // of a buffer
   B_PFREE = B_SFREE + kSums,    // positions have been read
-  B_HALF = B_PFREE + kPos,  // per key half: the second row half's sums are there
+  B_HALF = B_PFREE + kPos,  // per key half: the second warpgroup's sums are there
   B_TAKEN = B_HALF + 2,     // they have been added
   B_FIN = B_TAKEN + 2,
   B_NEVER = B_FIN + 1,  // nothing arrives on it (the debug_stall test hook)
@@ -265,6 +265,11 @@ __device__ void producer(const Ctx& c, const TreeParams& p, const CUtensorMap* t
   __syncwarp();
 }
 
+// Tile `tile` of a key half goes to warpgroup tile & 1 of the half, as its tile number tile / 2.
+__device__ __forceinline__ int sum_bar(int x, uint32_t tile) {
+  return B_SFULL + 4 * x + 2 * (tile & 1) + ((tile >> 1) & 1);
+}
+
 template <int D, bool FP8>
 __device__ void issuer(const Ctx& c, const TreeParams& p, uint32_t tmem_base) {
   using S = Shape<D, FP8>;
@@ -273,7 +278,7 @@ __device__ void issuer(const Ctx& c, const TreeParams& p, uint32_t tmem_base) {
   Ring<1> k;
   Ring<kQueries> q;
   Ring<kSums> s;
-  uint32_t n = 0;  // S^T tiles so far
+  uint32_t n = 0, tiles[2] = {0, 0};  // S^T tiles so far; of each key half
   const uint32_t tmem = __shfl_sync(kFull, tmem_base, 0);
   const uint64_t ones = sdesc(sm + S::kOffLse + kQueries * 32, 16, 1024);
   Walk walk(p, blockIdx.x);
@@ -296,7 +301,8 @@ __device__ void issuer(const Ctx& c, const TreeParams& p, uint32_t tmem_base) {
           mma_ta(d, kt + 8 * kk, qd + (kk >> 2) * (128 * 128 / 16) + 2 * (kk & 3), kIdesc, kk ? 1u : 0u);
         // (last: one rounding at the log-sum-exp's magnitude)
         mma(d, ones, sdesc(sm + S::kOffLse + q.st * 32, 16, 1024), kIdesc, 1u);
-        commit(c.bar + B_SFULL + s.st);
+        const uint32_t tile = x ? tiles[1]++ : tiles[0]++;
+        commit(c.bar + sum_bar(x, tile));
         s.next();
       }
       commit(c.bar + B_QEMPTY + q.st);
@@ -408,19 +414,19 @@ __device__ __forceinline__ void key_dims(const uint8_t* stage, int row, int h, u
   }
 }
 
-// A warpgroup's 128 keys and half of the rows: thread = key.
+// A warpgroup's 128 keys and every other row tile: thread = key.
 template <int D, bool FP8>
 __device__ void summer(const Ctx& c, const TreeParams& p, uint32_t tmem, uint32_t stall, const int* pos,
                         const int4* info, float* sums) {
   using S = Shape<D, FP8>;
   const VarlenMeta& m = p.m;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 4, x = warp >> 3, quad = warp & 3;
-  const int half = (warp >> 2) & 1;  // of a row tile's columns
+  const uint32_t half = (warp >> 2) & 1;  // warpgroup of the key half
   const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
   Ring<1> k;
   Ring<kPos> l;
   Ring<kSums> s;
-  uint32_t pieces = 0;  // of this key half so far
+  uint32_t pieces = 0, tile = 0;  // of this key half so far
   bool first = true;
   Walk walk(p, blockIdx.x);
   Piece g;
@@ -457,53 +463,60 @@ __device__ void summer(const Ctx& c, const TreeParams& p, uint32_t tmem, uint32_
       }
       continue;
     }
-    for (int r = g.r0; r < g.r1; ++r) {
+    for (int r = g.r0; r < g.r1; ++r, ++tile) {
       if (x) s.next();
-      // (the issuer has waited for the rows' numbers)
-      if (!wait_all(c, stall ? B_NEVER : B_SFULL + s.st, stall ? 0u : s.par)) return;
-      tc_fence_after();
-      uint32_t v[64];
-      tmem_ld64(lanes + s.st * kRows + 64 * half, v);
-      const int4 t = info[l.st];
-      // every row of the tile sees all of the warpgroup's keys
-      const bool all = t.x >= low + 127 && (m.window <= 0 || low > t.y - m.window || low + 127 < p.first);
-      const int* tp = pos + l.st * kRows + 64 * half;
-      tmem_wait_ld64(v);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(c.bar + B_SFREE + s.st);
-      if (all && t.z >= 64 * half + 64) {
+      if ((tile & 1) == half) {
+        // (the issuer has waited for the rows' numbers)
+        if (!wait_all(c, stall ? B_NEVER : sum_bar(x, tile), stall ? 0u : (tile >> 2) & 1)) return;
+        tc_fence_after();
+        const int4 t = info[l.st];
+        // every row of the tile sees all of the warpgroup's keys
+        const bool all = t.x >= low + 127 && (m.window <= 0 || low > t.y - m.window || low + 127 < p.first);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[64];
+          tmem_ld64(lanes + s.st * kRows + 64 * h, v);
+          const int* tp = pos + l.st * kRows + 64 * h;
+          tmem_wait_ld64(v);
+          if (h) {  // the buffer has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.bar + B_SFREE + s.st);
+          }
+          if (all && t.z >= 64 * h + 64) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          float a, b;
-          f2_unpack(f2_mul(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2), a, b);
-          sum[(e >> 1) & 3] = f2_add(sum[(e >> 1) & 3], f2_pack(fast_exp2(a), fast_exp2(b)));
+            for (int e = 0; e < 64; e += 2) {
+              float a, b;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2), a, b);
+              sum[(e >> 1) & 3] = f2_add(sum[(e >> 1) & 3], f2_pack(fast_exp2(a), fast_exp2(b)));
+            }
+          } else if (t.z > 64 * h) {
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+              const int4 ps = *reinterpret_cast<const int4*>(tp + e);
+              auto one = [&](int at, int i) {  // (-1, no row, is below every key)
+                return at >= key && at <= last ? fast_exp2(__uint_as_float(v[e + i]) * sl) : 0.f;
+              };
+              sum[0] = f2_add(sum[0], f2_pack(one(ps.x, 0), one(ps.y, 1)));
+              sum[1] = f2_add(sum[1], f2_pack(one(ps.z, 2), one(ps.w, 3)));
+            }
+          }
         }
-      } else if (t.z > 64 * half) {
-#pragma unroll
-        for (int e = 0; e < 64; e += 4) {
-          const int4 ps = *reinterpret_cast<const int4*>(tp + e);
-          auto one = [&](int at, int i) {  // (-1, no row, is below every key)
-            return at >= key && at <= last ? fast_exp2(__uint_as_float(v[e + i]) * sl) : 0.f;
-          };
-          sum[0] = f2_add(sum[0], f2_pack(one(ps.x, 0), one(ps.y, 1)));
-          sum[1] = f2_add(sum[1], f2_pack(one(ps.z, 2), one(ps.w, 3)));
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(c.bar + B_PFREE + l.st);
+          if (!both) mbar_arrive(c.bar + B_PFREE + l.st);
         }
       }
       s.next();
       if (!x && both) s.next();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(c.bar + B_PFREE + l.st);
-        if (!both) mbar_arrive(c.bar + B_PFREE + l.st);
-      }
       l.next();
     }
     float a, b, d, e;
     f2_unpack(f2_add(sum[0], sum[1]), a, b);
     f2_unpack(f2_add(sum[2], sum[3]), d, e);
     float total = (a + b) + (d + e);
-    // the second half's sums go to the first
+    // the second warpgroup's sums go to the first
     float* other = sums + 128 * x + 32 * quad + lane;
     if (half) {
       if (pieces >= 1 && !wait_all(c, B_TAKEN + x, (pieces & 1) ^ 1)) return;
@@ -546,9 +559,9 @@ __global__ void __launch_bounds__(Shape<D, FP8>::kThreads, 1)
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
       if (i == B_KEMPTY || i == B_KREADY) n = 16;
-      if (i >= B_SFREE && i < B_SFREE + kSums) n = 8;
+      if (i >= B_SFREE && i < B_SFREE + kSums) n = 4;
       if (i >= B_QFULL && i < B_QFULL + kQueries) n = 2;
-      if (i >= B_PFREE && i < B_PFREE + kPos) n = 16;
+      if (i >= B_PFREE && i < B_PFREE + kPos) n = 8;
       if (i >= B_HALF && i < B_TAKEN + 2) n = 4;
       mbar_init(bar + i, n);
     }
