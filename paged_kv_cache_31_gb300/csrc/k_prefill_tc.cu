@@ -1104,8 +1104,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   // everything above overlaps the planning kernel (programmatic dependent launch); the plan
   // and the status word are read only after it has finished
   pdl_wait();
-  if (threadIdx.x == 0) flags[0] = status_set(p.status) ? 1 : 0;
-  __syncthreads();
+  // another stream may clear the status word while the pair's CTAs read it (block ids are checked beside the
+  // plan, so items may be there): the leader reads it for both.  (A look before each item's output is written
+  // instead cost 1.5 % of a call behind a window.)
+  if (leader && threadIdx.x == 0) {
+    flags[0] = status_set(p.status) ? 1 : 0;
+    asm volatile(
+        "{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %0, 1;\n\t"
+        "st.shared::cluster.b32 [ra], %1;\n\t}" ::"r"(smem_u32(flags)), "r"(flags[0])
+        : "memory");
+  }
+  __syncwarp();
+  cluster_sync();
   pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   // the plan's number of working pairs: the others take no item and leave, and the warp-MMA
