@@ -284,15 +284,17 @@ pa_status attend(const Call& c) {
     tp.redo_list = p.tc.plan + p.tc.redo_list_off;
     tp.redo_count = p.tc.plan + 3;
     if (launch_tc_prefill(tq, pk, pv, tp, 2 * p.tc.pairs, c.stream) != cudaSuccess) return PA_ECUDA;
-    TreeParams dp = p;  // the decoding sequences
-    dp.after_tc = 1;
-    dp.w.room = 0;
-    const int64_t keys = c.window > 0 ? std::min<int64_t>((int64_t)c.window + p.first, max_keys) : max_keys;
-    const DecodeForm f = decode_form(units, c.num_seqs, keys, key_bytes, fp8, d->sms);
-    dp.cluster = f.cluster;
-    dp.shape = f.shape;
-    dp.ordered = f.ordered;
-    if (launch_window_decode(tk, tv, dp, fp8, limit, stall, c.stream) != cudaSuccess) return PA_ECUDA;
+    if (c.num_seqs > 1) {  // (one sequence has more rows than a decoding one)
+      TreeParams dp = p;  // the decoding sequences
+      dp.after_tc = 1;
+      dp.w.room = 0;
+      const int64_t keys = c.window > 0 ? std::min<int64_t>((int64_t)c.window + p.first, max_keys) : max_keys;
+      const DecodeForm f = decode_form(units, c.num_seqs, keys, key_bytes, fp8, d->sms);
+      dp.cluster = f.cluster;
+      dp.shape = f.shape;
+      dp.ordered = f.ordered;
+      if (launch_window_decode(tk, tv, dp, fp8, limit, stall, c.stream) != cudaSuccess) return PA_ECUDA;
+    }
   }
   if (tc && !(prefill && fp8)) {  // (f16 holds every e4m3 value: no items to do again)
     if (launch_window_tc(tq, tk, tv, p, fp8, limit, stall, c.stream) != cudaSuccess) return PA_ECUDA;

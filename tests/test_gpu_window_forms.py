@@ -97,6 +97,24 @@ def test_many_chunks_over_e4m3(pa, H, Hkv, size, window, first):
     both(pa, b, window, first, observed=30 if window == 300 else 0)
 
 
+@pytest.mark.parametrize("kv", [BF16, E4M3])
+@pytest.mark.parametrize("window,first", [(0, 0), (300, 20)])
+def test_one_long_chunk(pa, kv, window, first):
+    """The prefill kernel without decoding sequences beside it; calls one behind the other."""
+    b = ref.Batch([(90, 1300)], 64, 8, 128, kv=kv, seed=5)
+    b.poison_unread(window, first)
+    both(pa, b, window, first)
+    want = b.out.clone()
+    for _ in range(20):
+        b.out.zero_()
+        scale = 0.125 if kv == E4M3 else 1.0
+        for _ in range(2):
+            pa.pa_window_attention(*b.args(), b.scale, sliding_window=window, first_tokens=first,
+                                   k_scale=scale, v_scale=2 * scale if kv == E4M3 else 1.0)
+        assert torch.equal(b.out, want)
+    assert pa.pa_device_status() == pa.PA_OK
+
+
 def test_some_sequences_have_no_token(pa):
     """As many sequences as tokens, though one has them all and others none."""
     for seqs in ([(300, 1), (20, 0), (0, 1), (77, 2), (40, 0)], [(90, 0), (200, 5), (30, 0), (9, 0), (10, 0)]):
