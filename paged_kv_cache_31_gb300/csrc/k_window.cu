@@ -145,7 +145,7 @@ __device__ void plan_weights(const TreeParams& p, int64_t* s_warp, int64_t* s_cu
         const int low = m.positions[qs + skip], last = m.positions[qs + q - 1];
         bad |= low < 0 || last < low || last >= n;
         const int end = min(max(last, 0), n - 1) / kWeightKeys + 1;
-        const int lo = m.window > 0 ? max(min(low, n - 1) - m.window + 1, 0) / kWeightKeys : 0;
+        const int lo = m.window > 0 ? max(min(max(low, 0), n - 1) - m.window + 1, 0) / kWeightKeys : 0;
         const int front = m.window > 0 ? min((int)(((int64_t)p.first + kWeightKeys - 1) / kWeightKeys), end) : 0;
         const int gap = max(lo - front, 0);
         mine = max(end - gap, 0);
@@ -232,10 +232,11 @@ __device__ void plan_weights(const TreeParams& p, int64_t* s_warp, int64_t* s_cu
   }
 }
 
-// Block 0 plans (block 1 the key weights, where they are asked for); the blocks behind check the sequences' positions and table entries.  Everything is read
-// after the wait for the kernels ahead, and no output is written before this launch is done.  A plan
-// that failed is one of empty shares and of sequences without tokens, so the kernels behind do nothing
-// even where another stream has cleared the status word in between.
+// Block 0 plans (block 1 the key weights, where they are asked for); the blocks behind check the
+// sequences' positions and table entries.  Everything is read after the wait for the kernels ahead, and
+// no output is written before this launch is done.  A plan that failed is one of empty shares and of
+// sequences without tokens, so the kernels behind do nothing even where another stream has cleared the
+// status word in between.
 __global__ void __launch_bounds__(kPlanThreads) k_window_plan(const TreeParams p) {
   __shared__ int64_t s_warp[32];
   __shared__ int64_t s_cum[kCumShared + 1];

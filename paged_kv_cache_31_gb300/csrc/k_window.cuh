@@ -14,7 +14,7 @@ struct Keys {
 };
 __device__ __forceinline__ Keys keys_from(const TreeParams& p, int lowest) {
   const VarlenMeta& m = p.m;
-  const int lo = m.window > 0 ? max(lowest - m.window + 1, 0) / m.block_size : 0;
+  const int lo = m.window > 0 ? max(max(lowest, 0) - m.window + 1, 0) / m.block_size : 0;
   return Keys{p.front, max(lo - p.front, 0)};
 }
 

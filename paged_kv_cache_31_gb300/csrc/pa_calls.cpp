@@ -1,5 +1,6 @@
 // pa_calls.cpp -- the Python module _calls: the checks and the argument passing of the
-// speculative-decoding calls and of those for bounded caches over torch tensors (binding.py documents them and raises PaError).
+// speculative-decoding calls and of those for bounded caches over torch tensors (binding.py documents
+// them and raises PaError).
 //
 // Why not ctypes, as for the calls around it: their kernels take 2 to 15 us at serving sizes, and
 // reading some ten tensors' properties and converting up to thirty arguments took 3 to 10 us of

@@ -205,6 +205,26 @@ def test_timeouts_unwind_and_the_device_stays_usable(pa, path):
 
 
 @pytest.mark.parametrize("path", [*PATHS, "general"])
+@pytest.mark.parametrize("bad", [-2 ** 31, 2 ** 31 - 1])
+def test_farthest_positions_are_refused(pa, path, bad):
+    """Positions at both ends of int32 behind the widest windows: refused, with everything as it was."""
+    seqs, H, Hkv, kv = PATHS.get(path, ([(300, 1), (90, 30)], 8, 2, F32))
+    b = ref.Batch(seqs, H, Hkv, 128, src=F32 if path == "general" else BF16, kv=kv, seed=81)
+    w = torch.full((len(seqs), Hkv, int(b.lens.max())), 0.5, device="cuda")
+    fine = b.positions.clone()
+    for at in (0, -1):
+        b.positions.copy_(fine)
+        b.positions[at] = bad
+        for window, first in ((2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 1, 0), (1, 0)):
+            b.out.fill_(7.0)
+            pa.pa_window_attention(*b.args(), b.scale, sliding_window=window, first_tokens=first)
+            assert pa.pa_device_status() == pa.PA_EINVAL
+            pa.pa_attention_key_weights(*b.args(), w, b.scale, sliding_window=window, first_tokens=first)
+            assert pa.pa_device_status() == pa.PA_EINVAL
+            assert (b.out == 7.0).all() and (w == 0.5).all()
+
+
+@pytest.mark.parametrize("path", [*PATHS, "general"])
 @pytest.mark.parametrize("bad", ["table", "lens", "qsl", "positions"])
 def test_bad_batches_while_the_status_is_cleared(pa, path, bad):
     """Whatever the later launches then see, reads and writes stay inside the arrays.  Each array is a
