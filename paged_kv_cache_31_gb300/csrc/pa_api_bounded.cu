@@ -41,9 +41,10 @@ size_t workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_heads, i
                                 kTreeGenericRows, kTreeGenericKeys, kTreeGenericGrid, weights)
                       .bytes;
   const int32_t group = num_heads / num_kv_heads;
-  if (tc_sizes(group, head_dim))  // the tensor-core kernel may run
+  // the tensor-core kernel may run, with items of one row tile or of two (one: more items, more CTAs)
+  for (int tiles = 1; tiles <= 2 && tc_sizes(group, head_dim); ++tiles)
     bytes = std::max(bytes, window_layout(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, keys,
-                                          2 * tile_rows(group), kTreeTcKeys, kTreeTcGrid, weights)
+                                          tiles * tile_rows(group), kTreeTcKeys, kTreeTcGrid, weights)
                                 .bytes);
   if (weights && num_seqs > 0 && decodes(num_seqs, num_tokens, num_kv_heads, group))
     bytes = std::max(bytes, 4 * (int64_t)num_seqs * num_kv_heads *
@@ -213,6 +214,7 @@ pa_status attend(const Call& c) {
     L = window_layout(c.num_seqs, c.num_tokens, c.num_heads, c.num_kv_heads, c.head_dim, max_keys,
                       p.rows_per_item, p.key_tile, kTreeGenericGrid, c.weighs);
   }
+  if ((uint64_t)L.bytes > c.workspace_bytes) return PA_EINVAL;  // (workspace_size() covers every layout)
   p.grid = L.tree.grid;
   uint8_t* ws = static_cast<uint8_t*>(c.workspace);
   p.seqs = reinterpret_cast<int4*>(ws);
