@@ -833,10 +833,11 @@ size_t pa_evict_keys_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int3
  * new_lens to pa_trim_sequences.  Sequences with new_lens[s] >= n are left as they are.
  * Checked before any row or weight is written: n and new_lens[s] not negative, the table covers n
  * positions with ids in [0, num_blocks) (where keys are evicted), n <= weights_len (given weights):
- * otherwise PA_EINVAL is recorded and nothing is written.  A block that is written belongs to one
- * sequence only.  num_seqs and num_kv_heads <= 65535 and at most 524288 keys to a sequence (the smaller
- * of the table's width and, given weights, weights_len), num_blocks * block_size < 2^31, else
- * PA_EUNSUPPORTED.
+ * otherwise PA_EINVAL is recorded and nothing is written.  The call is whole: it goes by what this check
+ * found, an error recorded before it included, so errors that other streams record or clear meanwhile
+ * change nothing.  A block that is written belongs to one sequence only.  num_seqs and num_kv_heads <=
+ * 65535 and at most 524288 keys to a sequence (the smaller of the table's width and, given weights,
+ * weights_len), num_blocks * block_size < 2^31, else PA_EUNSUPPORTED.
  * workspace: pa_evict_keys_workspace_size(...) bytes, 256-byte aligned, scratch of the caller that calls
  * which overlap on the device must not share.
  */

@@ -7,7 +7,9 @@
 // recent rows and a few others, not everything behind the first evicted key.
 //
 // k_evict_check looks at all metadata.  Beside it k_evict, a CTA (or a small cluster) for each (sequence,
-// kv head), already selects; it waits for the check before it writes, and bounds its own indices.
+// kv head), already selects; it waits for the check before it writes, and bounds its own indices.  All go by
+// the check's answer, which lies in the workspace: the status word may change under the call (another stream
+// records an error, or clears one), and half of a cache that is cut in place could not be repaired.
 //
 // Selection.  The m-th largest weight by histograms over 11, 11 and 10 bits of its order-preserving integer
 // form (the first covers exponent and two bits of the fraction, so its bins seldom collide), or, as soon
@@ -62,7 +64,8 @@ __device__ __forceinline__ bool evict_bad(const EvictParams& p, const Plan& e) {
          (p.key_weights && e.n > p.weights_len);
 }
 
-// A warp per 256 table entries of a sequence.
+// A warp per 256 table entries of a sequence.  Each block's answer goes to verdict[block]; the first block's
+// says as well whether an error was recorded before the call.
 __global__ void __launch_bounds__(256) k_evict_check(const EvictParams p) {
   pdl_wait();
   pdl_launch_dependents();
@@ -70,6 +73,7 @@ __global__ void __launch_bounds__(256) k_evict_check(const EvictParams p) {
   const int per = (p.max_blocks + 255) / 256 + 1;  // (one at least)
   const int64_t chunks = (int64_t)p.num_seqs * per;
   bool bad = false;
+  const bool before = blockIdx.x == 0 && threadIdx.x == 0 && status_set(p.status);
   for (int64_t c = blockIdx.x * 8 + (threadIdx.x >> 5); c < chunks; c += warps) {
     const int s = (int)(c / per), e0 = (int)(c % per) * 256;
     const Plan e = evict_plan(p, s);
@@ -87,6 +91,8 @@ __global__ void __launch_bounds__(256) k_evict_check(const EvictParams p) {
     for (int u = 0; u < 8; ++u) bad |= id[u] < 0 || (int64_t)id[u] >= p.num_blocks;
   }
   if (__any_sync(kFull, bad) && lane == 0) record_error(p.status, PA_EINVAL);
+  const int stop = __syncthreads_or(bad || before);
+  if (threadIdx.x == 0) p.verdict[blockIdx.x] = stop;
 }
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -322,7 +328,7 @@ __global__ void __launch_bounds__(NT, per_sm(NT))
   // ---- moves, once the whole batch has been checked
   pdl_wait();
   pdl_launch_dependents();
-  if (__syncthreads_or(status_set(p.status))) return;
+  if (__syncthreads_or(tid < p.checkers && __ldcg(p.verdict + tid) != 0)) return;
   auto from = [&](int i) {  // of move i
     const int k = i - fillers;
     if (k >= 0) return e.n - e.recent + k;
@@ -452,13 +458,14 @@ cudaError_t evict_keys(const EvictParams& p, int cluster, int num_sms, cudaStrea
 }  // namespace
 
 int64_t evict_workspace(int32_t num_seqs, int32_t num_kv_heads, int64_t max_keys) {
-  return (int64_t)num_seqs * num_kv_heads * max_keys * 4;
+  return kEvictVerdict + (int64_t)num_seqs * num_kv_heads * max_keys * 4;
 }
 
-cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_evict(EvictParams p, int num_sms, cudaStream_t stream) {
   const int64_t chunks = (int64_t)p.num_seqs * ((p.max_blocks + 255) / 256 + 1);
-  const int blocks = (int)std::min<int64_t>((chunks + 7) / 8, 64);
-  const cudaError_t e = launch_pdl(k_evict_check, dim3(blocks), dim3(256), 0, stream, p);
+  p.checkers = (int)std::min<int64_t>((chunks + 7) / 8, 64);
+  static_assert(kEvictVerdict >= 64 * 4, "verdicts");
+  const cudaError_t e = launch_pdl(k_evict_check, dim3(p.checkers), dim3(256), 0, stream, p);
   if (e != cudaSuccess) return e;
   // few units: each to as many CTAs as are resident at once, which all select
   const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads;

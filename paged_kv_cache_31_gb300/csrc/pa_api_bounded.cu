@@ -409,7 +409,8 @@ pa_status pa_evict_keys(void* k_blocks, void* v_blocks, const int32_t* block_tab
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.row_bytes = (int64_t)head_dim * esize(kv_dtype);
-  p.moves = static_cast<int32_t*>(workspace);
+  p.verdict = static_cast<int32_t*>(workspace);
+  p.moves = p.verdict + kEvictVerdict / 4;
   p.moves_len = most;
   p.status = d->status;
   return from_cuda(launch_evict(p, d->sms, stream));
