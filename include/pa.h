@@ -816,7 +816,8 @@ pa_status pa_attention_key_weights(const void* q, const void* k_blocks, const vo
                                    float v_scale, const float* k_scales, const float* v_scales,
                                    void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
-/* pa_evict_keys_workspace_size -- bytes of device workspace pa_evict_keys needs for these sizes. */
+/* pa_evict_keys_workspace_size -- bytes of device workspace pa_evict_keys needs for these sizes: 4096, and
+ * where a table row covers more than 8192 positions a word for each (sequence, kv head, position). */
 size_t pa_evict_keys_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t max_blocks_per_seq,
                                     int32_t block_size);
 

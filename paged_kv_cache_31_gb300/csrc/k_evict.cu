@@ -38,6 +38,7 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBins = 2048;   // of the histogram
 constexpr int kMoves = 1024;  // whose places are looked up at a time
+constexpr int kNearKeys = 8192;  // of a sequence up to which the list lies in shared memory
 
 // Larger weights have larger keys (none is 0); both zeros the same, NaN the largest.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -451,14 +452,14 @@ template <typename T>
 cudaError_t evict_keys(const EvictParams& p, int cluster, int num_sms, cudaStream_t stream) {
   const int64_t keys = p.moves_len;  // at most
   if (keys <= 2048) return evict_as<T, 256, 8>(p, cluster, num_sms, stream);
-  if (keys <= 8192) return evict_as<T, 512, 16>(p, cluster, num_sms, stream);
+  if (keys <= kNearKeys) return evict_as<T, 512, kNearKeys / 512>(p, cluster, num_sms, stream);
   return evict_as<T, 1024, 0>(p, cluster, num_sms, stream);
 }
 
 }  // namespace
 
 int64_t evict_workspace(int32_t num_seqs, int32_t num_kv_heads, int64_t max_keys) {
-  return kEvictVerdict + (int64_t)num_seqs * num_kv_heads * max_keys * 4;
+  return kEvictVerdict + (max_keys > kNearKeys ? (int64_t)num_seqs * num_kv_heads * max_keys * 4 : 0);
 }
 
 cudaError_t launch_evict(EvictParams p, int num_sms, cudaStream_t stream) {

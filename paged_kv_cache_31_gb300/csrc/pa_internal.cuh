@@ -727,12 +727,13 @@ struct EvictParams {
   int64_t row_bytes;  // of one position and kv head
   int32_t* verdict;   // workspace: a word for each block of the check, not 0: nothing is written
   int32_t checkers;   // blocks of the check
-  int32_t* moves;     // workspace, behind the verdicts: a list for each (sequence, kv head), moves_len words
+  int32_t* moves;     // workspace, behind the verdicts, where shared memory cannot hold it: a list for each
+                      // (sequence, kv head), moves_len words
   int64_t moves_len;  // most keys of a sequence
   int* status;
 };
 constexpr int64_t kEvictMostKeys = 1 << 19;  // of a sequence: two bits each in shared memory
-constexpr int64_t kEvictVerdict = 256;  // bytes
+constexpr int64_t kEvictVerdict = 4096;  // bytes in front of the lists (a page)
 int64_t evict_workspace(int32_t num_seqs, int32_t num_kv_heads, int64_t max_keys);
 cudaError_t launch_evict(EvictParams p, int num_sms, cudaStream_t stream);
 

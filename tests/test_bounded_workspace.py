@@ -73,3 +73,12 @@ def test_more_tokens_or_sequences_never_need_less(b, weights):
             assert sizes == sorted(sizes), (H, Hkv, width, S)
         sizes = [size(S, 600, H, Hkv, 128, width, 16) for S in range(2, 40)]
         assert sizes == sorted(sizes), (H, Hkv, width)
+
+
+def test_eviction_lists(b):
+    """A list of moves lies in the workspace only where shared memory does not hold it."""
+    size = b.pa_evict_keys_workspace_size
+    for S, Hkv, width, bs in [(256, 8, 512, 16), (65535, 65535, 256, 32), (1, 1, 0, 16), (3, 2, 8192, 1)]:
+        assert size(S, Hkv, width, bs) == 4096
+    for S, Hkv, width, bs in [(256, 8, 513, 16), (2, 3, 8193, 1), (64, 8, 8192, 16)]:
+        assert size(S, Hkv, width, bs) == 4096 + 4 * S * Hkv * width * bs
