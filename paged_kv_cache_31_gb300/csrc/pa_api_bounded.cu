@@ -386,7 +386,10 @@ pa_status pa_evict_keys(void* k_blocks, void* v_blocks, const int32_t* block_tab
       (int64_t)head_dim * esize(kv_dtype) > (1 << 20))
     return PA_EUNSUPPORTED;
   if (num_seqs == 0) return PA_OK;
-  if (!k_blocks || !v_blocks || !block_tables || !seq_lens || !new_lens) return PA_EINVAL;
+  // (arrays without an element have no address: tables of no column, pools of no block)
+  if ((num_blocks > 0 && (!k_blocks || !v_blocks)) || (max_blocks_per_seq > 0 && !block_tables) || !seq_lens ||
+      !new_lens)
+    return PA_EINVAL;
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < pa_evict_keys_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq, block_size))
     return PA_EINVAL;

@@ -107,3 +107,18 @@ def test_eviction(pa, lens, width):
     assert ws.intact()
     with pytest.raises(pa.PaError):
         c.check(pa, [n // 4 for n in lens], workspace=ws.own[:-1])
+
+
+def test_eviction_of_empty_sequences(pa):
+    """Tables without a column: nothing to do, as in any other batch of sequences without keys."""
+    kb, vb = (torch.ones(3, 16, 2, 64, dtype=BF16, device="cuda") for _ in range(2))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    tables = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    pa.pa_evict_keys(kb, vb, tables, i32([0, 0]), i32([0, 0]))
+    assert pa.pa_device_status() == pa.PA_OK
+    none = kb[:0].contiguous()
+    pa.pa_evict_keys(none, none, tables, i32([0, 0]), i32([0, 0]), torch.zeros(2, 2, 0, device="cuda"))
+    assert pa.pa_device_status() == pa.PA_OK
+    pa.pa_evict_keys(kb, vb, tables, i32([0, 1]), i32([0, 0]))
+    assert pa.pa_device_status() == pa.PA_EINVAL
+    assert bool((kb == 1).all()) and bool((vb == 1).all())
