@@ -420,7 +420,9 @@ pa_status evict_keys(Args a) {
     const at::Tensor& t = c.array(a[5]);
     if (t.scalar_type() != at::kFloat || t.dim() != 3 || t.size(0) != S || t.size(1) != p.heads)
       throw Bad{"key_weights must be fp32 [num_seqs, num_kv_heads, length]"};
-    w = static_cast<float*>(t.data_ptr());
+    // (an array without an element has no address, and is not "no weights": its keys are refused)
+    static float empty;
+    w = t.numel() ? static_cast<float*>(t.data_ptr()) : &empty;
     len = t.size(2);
   }
   const int32_t first = integer(a[6]), recent = integer(a[7]);

@@ -122,3 +122,16 @@ def test_eviction_of_empty_sequences(pa):
     pa.pa_evict_keys(kb, vb, tables, i32([0, 1]), i32([0, 0]))
     assert pa.pa_device_status() == pa.PA_EINVAL
     assert bool((kb == 1).all()) and bool((vb == 1).all())
+
+
+def test_weights_of_no_column_are_not_none(pa):
+    from tests.test_gpu_evict import Cache
+
+    c = Cache([40, 20], 2, 64, seed=3)
+    before = c.kb.clone()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    args = (c.kb, c.vb, c.tables, i32([40, 20]), i32([30, 20]))
+    pa.pa_evict_keys(*args, c.w[:, :, :0].contiguous(), 0, 5)
+    assert pa.pa_device_status() == pa.PA_EINVAL  # 40 keys, 0 weights
+    assert torch.equal(c.kb.view(torch.uint8), before.view(torch.uint8))
+    c.check(pa, [30, 20], 0, 5, weights=False)
