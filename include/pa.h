@@ -754,8 +754,8 @@ size_t pa_window_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, 
  * k_scales / v_scales as in pa_varlen_forward_ex and pa_varlen_forward_per_head (a per-head array needs
  * a scalar of 1).  bf16 q over e4m3 pools enters the products with 17 bits of its row's largest element
  * or more (a row with an infinity comes out as NaN).  Softmax weights enter the products with V with 16
- * bits, of large batches of prompt chunks, and over e4m3 pools, with 11 (f16); those batches' bf16 V as
- * f16, exact from 2^-14 on and off by 2^-25 at most below.
+ * bits, of large batches of prompt chunks, and over e4m3 pools, with 11 (f16, or off by 2^-32 of the row's
+ * largest); those batches' bf16 V as f16, exact from 2^-14 on and off by 2^-25 at most below.
  * K rows of keys that a token does not see may hold anything.  So may V rows at or past seq_lens[s],
  * and those of blocks between the first tokens' and the first that the sequence's tokens reach: these
  * are not read, and their table entries not looked at (a server may have given them away).  All other V

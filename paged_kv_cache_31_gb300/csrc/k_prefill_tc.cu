@@ -51,8 +51,8 @@
 //
 // WIN: attention behind a window whose first tokens stay visible, for large batches of prompt chunks.
 // Keys are counted without the blocks between the first tokens' and the window's (k_window.cu plans the
-// items), so only block ids and masks differ; items with V that f16 cannot hold are done again by
-// k_tree_tc.cuh's kernel.  Measured (us a call): chunks of 257 to 2048 tokens with 58 decoding sequences
+// items), so only block ids, masks and the reference of the weights (kRefBelow) differ; items with V that f16
+// cannot hold are done again by k_tree_tc.cuh's kernel.  Measured (us a call): chunks of 257 to 2048 tokens with 58 decoding sequences
 // 547 (even shares on one-SM MMAs with exact V and two terms of P: 709), e4m3 prompts of 700 to 4096
 // with their weights 391 (408).
 //
@@ -94,6 +94,10 @@ constexpr int kSmemBytes = kOffXchg + 2 * 2 * 128 * 4 + 1024;  // + slack to ali
 constexpr int kQScales = 8;
 constexpr int kOffQScale = kOffXchg + 2 * 2 * 128 * 4;
 constexpr int kSmemScaled = kSmemBytes + kQScales * 128 * 4;
+// WIN: the reference that weights are taken from lies 7 powers of two below the maximum that set it, so f16
+// weights are at most 2^15, a row's largest at least 2^7, and what is rounded to a multiple of f16's smallest
+// step is off by 2^-32 of it (from the maximum itself 2^-25: thousands of weights of 2^-26 came out as zero).
+constexpr float kRefBelow = 7.f;
 constexpr uint32_t kBadMax = 0x7fc0dea1u;  // a NaN that no arithmetic produces (canonical 7fffffff)
 static_assert(kSmemScaled <= 232448, "shared memory of one CTA");
 constexpr int kSoftWarps = 8;   // two column halves x four lane quarters
@@ -914,15 +918,16 @@ __device__ void softmax_role(const Ctx& c, const TcParams& p, uint32_t tmem, int
       const bool leave = __any_sync(kFull, bad || __float_as_uint(other) == kBadMax);
       pair_sync(quad);  // both read before either writes again
       if (leave) return;
-      const float m_new = fmaxf(m_ref, mt);
-      const bool resc = m_new > m_ref + 8.f;
+      const float m_new = WIN ? mt - kRefBelow : fmaxf(m_ref, mt);
+      // (WIN: the difference is exact, so weights stay within f16 for scores of any magnitude)
+      const bool resc = WIN ? mt - m_ref > kRefBelow + 8.f : m_new > m_ref + 8.f;
       float alpha = 1.f;
       if (resc) {
         alpha = fast_exp2(m_ref - m_new);  // 0 when nothing was visible before
         m_ref = m_new;
         l *= alpha;
       }
-      // p = 2^(x * scale_log2 - m_ref) two at a time (p <= 2^8), the row sum of the fp32
+      // p = 2^(x * scale_log2 - m_ref) two at a time (p <= 2^8, WIN 2^15), the row sum of the fp32
       // weights, and p rounded to f16 for the P V MMAs
       const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
       const uint64_t sl2 = f2_pack(sl, sl), nb2 = f2_pack(nbase, nbase);

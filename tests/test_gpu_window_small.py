@@ -1,0 +1,64 @@
+"""Small softmax weights in every form of the attention behind a window: what f16 would round to nothing is
+kept."""
+import pytest
+import torch
+
+from tests import bounded_reference as ref
+from tests.spec_reference import assert_within, stored
+from tests.test_gpu_window import BF16, E4M3, pa  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+# (the prefill kernel; even shares; decoding clusters)
+FORMS = {"prefill": ([(90, 1300)], 64, 8), "prefill, mixed": ([(300, 700), (0, 600), (1000, 1), (40, 20)], 64, 8),
+         "shares": ([(700, 40), (0, 300)], 8, 2), "decode": ([(900, 1), (300, 1)], 8, 2)}
+
+
+def check(pa, b, want, v_scale=1.0):
+    pa.pa_window_attention(*b.args(), b.scale, sliding_window=b.window, first_tokens=b.first, lse=b.lse,
+                           v_scale=v_scale)
+    assert pa.pa_device_status() == pa.PA_OK
+    y, bound = stored(want["out"], want["out_b"], b.out.dtype)
+    assert_within(b.out, y, bound, "out")
+    assert_within(b.lse, want["lse"], want["lse_b"], "lse")
+
+
+def expected(b, **kw):
+    return ref.window_attention(b.q, b.kb, b.vb, b.qsl, b.lens, b.positions, b.tables, b.scale, b.window, b.first,
+                                **kw)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("kv", [BF16, E4M3])
+@pytest.mark.parametrize("window,first", [(0, 0), (400, 16)])
+def test_weights_of_2_to_the_minus_26(pa, form, kv, window, first):
+    """Position 0 takes nearly all of the weight and has V zero: the output is the sum of the others', each
+    2^-26 of it."""
+    seqs, H, Hkv = FORMS[form]
+    b = ref.Batch(seqs, H, Hkv, 128, kv=kv, seed=len(form))
+    b.window, b.first = window, first
+    b.q.fill_(1.0)
+    b.kb.view(torch.uint8).zero_()
+    for s, (c, n) in enumerate(seqs):
+        at = int(b.tables[s, 0])
+        b.kb[at, 0].fill_(1.625)  # 128 * 1.625 / sqrt(128) = 18.4: 2^26.5
+        b.vb.view(torch.uint8)[at, 0].zero_()
+    # f16 weights 2^-11 of their value and, below f16's normal range, half its smallest step, 2^-25, of a row
+    # whose largest weight is at least 2^7
+    want = expected(b, weight_u=2.0 ** -11, weight_min=2.0 ** -32)
+    assert float(want["out"].abs().max()) > 1e-7
+    check(pa, b, want)
+
+
+@pytest.mark.parametrize("kv", [BF16, E4M3])
+@pytest.mark.parametrize("size", [1.0, 30.0, 1000.0, 2.0 ** 20])
+def test_scores_of_any_magnitude(pa, kv, size):
+    """Maxima that rise from tile to tile by less than the reference follows, and by far more."""
+    b = ref.Batch([(700, 1300)], 64, 8, 128, kv=kv, seed=7)
+    b.window, b.first = 0, 0
+    b.q.fill_(1.0)
+    up = torch.arange(int(b.lens[0]), device="cuda")
+    rows = b.tables[0].long()[up // 16] * 16 + up % 16
+    level = (up // 128).float() * 0.11 * size / 16  # 128 * 0.11 / sqrt(128) / ln 2 = 1.8 a tile at size 16
+    b.kb.view(-1, 8, 128)[rows] = level.clamp(max=400.0)[:, None, None].expand(-1, 8, 128).to(kv)
+    check(pa, b, expected(b, weight_u=2.0 ** -11, weight_min=2.0 ** -32))
