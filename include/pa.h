@@ -755,7 +755,9 @@ size_t pa_window_attention_workspace_size(int32_t num_seqs, int64_t num_tokens, 
  * a scalar of 1).  bf16 q over e4m3 pools enters the products with 17 bits of its row's largest element
  * or more (a row with an infinity comes out as NaN).  Softmax weights enter the products with V with 16
  * bits, of large batches of prompt chunks, and over e4m3 pools, with 11 (f16, or off by 2^-32 of the row's
- * largest); those batches' bf16 V as f16, exact from 2^-14 on and off by 2^-25 at most below.
+ * largest); those batches' bf16 V as f16, exact from 2^-14 on and off by 2^-25 at most below,
+ * but as it is where no value of 2^-9 or more is found in a kv head of a sequence (8 values of the first row of
+ * each block that the sequence reads are looked at).
  * K rows of keys that a token does not see may hold anything.  So may V rows at or past seq_lens[s],
  * and those of blocks between the first tokens' and the first that the sequence's tokens reach: these
  * are not read, and their table entries not looked at (a server may have given them away).  All other V

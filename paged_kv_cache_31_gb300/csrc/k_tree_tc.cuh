@@ -189,19 +189,34 @@ struct Walk {
   __device__ __forceinline__ Walk(const Ctx& c, const TreeParams& p) : w(p, blockIdx.x) {}
   __device__ __forceinline__ bool next(const TreeParams& p, TreeSegment& g) { return w.next(p, g); }
 };
-// The items (of two row tiles, whole) that the prefill kernel marked, each for all kv heads.
+// The items (of two row tiles, whole) that the prefill kernel marked, each for all kv heads, and those of a
+// (sequence, kv head) whose values are small.
 template <>
 struct Walk<kMarked> {
   int at, end;
-  __device__ __forceinline__ Walk(const Ctx& c, const TreeParams& p)
-      : at(blockIdx.x), end(__ldcg(p.tc.plan + 3) * p.m.num_kv_heads) {}
+  // whole warp
+  __device__ __forceinline__ Walk(const Ctx& c, const TreeParams& p) : at(blockIdx.x), end(0) {
+    static_assert(kSmallBlocks == 64, "two words a lane");
+    const int32_t* any = p.tc.plan + p.tc.small_off + 2 * (threadIdx.x & 31);
+    const int marked = __ldcg(any) | __ldcg(any + 1) | __ldcg(p.tc.plan + 3);
+    const int items = __ldcg(p.tc.plan + 1);
+    if (__any_sync(kFull, marked != 0)) end = items * p.m.num_kv_heads;
+  }
   __device__ __forceinline__ bool next(const TreeParams& p, TreeSegment& g) {
-    if (at >= end) return false;
-    const int item = __ldcg(p.tc.plan + p.tc.redo_list_off + at / p.m.num_kv_heads);
-    const int4 it = reinterpret_cast<const int4*>(p.tc.plan + p.tc.items_off)[item];
+    int4 it;
+    int kvh;
+    for (;; at += gridDim.x) {
+      if (at >= end) return false;
+      const int item = at / p.m.num_kv_heads;
+      kvh = at - item * p.m.num_kv_heads;
+      it = reinterpret_cast<const int4*>(p.tc.plan + p.tc.items_off)[item];
+      if (__ldcg(p.tc.plan + p.tc.redo_off + item) |
+          __ldcg(p.tc.plan + p.tc.small_off + kSmallBlocks + (int64_t)it.x * p.m.num_kv_heads + kvh))
+        break;
+    }
     const int4 q = p.seqs[2 * it.x], w = p.seqs[2 * it.x + 1];
     g.s = it.x;
-    g.kvh = at % p.m.num_kv_heads;
+    g.kvh = kvh;
     g.item = it.y;
     g.row0 = it.y * p.rows_per_item;
     g.rows = min(p.rows_per_item, w.z - g.row0);

@@ -57,6 +57,44 @@ __device__ __forceinline__ int token_from(const int32_t* pos, int a, int b, int6
   return a;
 }
 
+// Warp `me` of `warps`, for batches that go to the prefill kernel: marks the (sequence, kv head)s in whose V no
+// value of 2^-9 or more is found.  That kernel holds V in f16, off by up to 2^-25 below 2^-14: 2^-16 of such a
+// value, but all of a V of 1e-8, so items of marked ones are done again with V as it is.  8 values of each of 32
+// rows at a time; mostly the first ones say so.  (A look by the prefill kernel's converters or producers, which
+// have the values at hand, took 2 to 6 % of a call.)  Returns whether it marked one.
+__device__ bool mark_small_values(const TreeParams& p, int me, int warps) {
+  const VarlenMeta& m = p.m;
+  const int lane = threadIdx.x & 31;
+  const int64_t units = (int64_t)m.num_seqs * m.num_kv_heads;
+  bool marked = false;
+  for (int64_t u = me; u < units; u += warps) {
+    const int s = (int)(u / m.num_kv_heads), g = (int)(u % m.num_kv_heads);
+    int qs, q, n;
+    sequence(p, s, qs, q, n);
+    if (q * m.group <= kWindowDecodeRows) continue;
+    const Keys k = keys_from(p, m.window > 0 ? m.positions[qs] : 0);
+    const int blocks = (int)(((int64_t)n + 15) / 16) - k.gap;
+    const int32_t* row = m.block_tables + (int64_t)s * m.max_blocks;
+    // 16 bytes of the first row of a block; the chunks of a block's row change with the lane
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_blocks) + (int64_t)g * m.head_dim +
+                             lane % (m.head_dim / 8) * 8;
+    bool found = false;
+    for (int b0 = 0; b0 < blocks && !found; b0 += 32) {
+      const int b = b0 + lane, id = b < blocks ? row[b < k.front ? b : b + k.gap] : -1;
+      uint32_t x = 0;
+      if (id >= 0 && (int64_t)id < m.num_blocks) {
+        const uint4 w = *reinterpret_cast<const uint4*>(v + (int64_t)id * 16 * m.num_kv_heads * m.head_dim);
+        x = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                     __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+      }
+      found = __any_sync(0xffffffffu, max(x & 0xffffu, x >> 16) >= 0x3b00u);  // (bf16 2^-9)
+    }
+    if (lane == 0) p.tc.plan[p.tc.small_off + kSmallBlocks + u] = !found;
+    marked |= !found;
+  }
+  return marked;
+}
+
 // One block, for batches that go to the prefill kernel: its items, those of the most keys first (a counting
 // sort, sixteen buckets to an octave), and how many pairs of CTAs take them: the number that ends both it
 // and the decoding sequences beside it soonest.
@@ -254,6 +292,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_window_plan(const TreeParams p
   if (blockIdx.x > 0) {
     const int warps = (gridDim.x - planners) * (kPlanThreads / 32);
     bad = bad_reads(p, (blockIdx.x - planners) * (kPlanThreads / 32) + warp, warps);
+    if (p.tc.small_off) {
+      const int block = blockIdx.x - planners, blocks = gridDim.x - planners;
+      const int any = __syncthreads_or(mark_small_values(p, block * (kPlanThreads / 32) + warp, warps));
+      if (tid < kSmallBlocks && tid % blocks == block) p.tc.plan[p.tc.small_off + tid] = any;
+    }
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(p.status, PA_EINVAL);
     return;
   }
@@ -371,8 +414,8 @@ WindowLayout window_layout(int32_t num_seqs, int64_t num_tokens, int32_t num_hea
   L.items_off = t.bytes;
   L.item_cum_off = L.items_off + up(16 * items);
   L.tc_off = L.item_cum_off + up(8 * (items + 1));
-  // header words, items, marks, list of marked items
-  L.lse_off = L.tc_off + up(4 * (kPlanHeaderWords + 6 * items));
+  // header words, items, marks, list of marked items, marks of small values
+  L.lse_off = L.tc_off + up(4 * (kPlanHeaderWords + 6 * items + kSmallBlocks + (int64_t)num_seqs * num_kv_heads));
   L.bytes = L.w_seqs_off = L.lse_off + (weights ? up(4 * num_tokens * num_heads) : 0);
   if (!weights) return L;
   const int64_t key_items = std::min<int64_t>(num_seqs, num_tokens) * ((max_keys + kWeightKeys - 1) / kWeightKeys);
@@ -388,6 +431,7 @@ cudaError_t launch_window_plan(const TreeParams& p, cudaStream_t stream) {
   // checks beside the planner: a warp per 256 table entries or 1024 tokens, at most 64 blocks
   const int64_t chunks = (int64_t)p.m.num_seqs * ((p.m.max_blocks + 255) / 256 +
                                                   (p.m.num_tokens + kCheckTokens - 1) / kCheckTokens);
+  static_assert(kSmallBlocks == 64, "a word for each of the blocks");
   const int blocks = (int)std::min<int64_t>((chunks + 31) / 32, 64);
   return launch_pdl(k_window_plan, dim3((p.w.grid > 0 ? 2 : 1) + blocks), dim3(kPlanThreads), 0, stream, p);
 }

@@ -254,6 +254,7 @@ pa_status attend(const Call& c) {
     p.tc.items_off = kPlanHeaderWords;
     p.tc.redo_off = p.tc.items_off + 4 * items;
     p.tc.redo_list_off = p.tc.redo_off + items;
+    p.tc.small_off = fp8 ? 0 : p.tc.redo_list_off + items;
     p.tc.num_sms = d->sms;
     p.tc.pairs = d->sms / 2;
     p.tc.decode_bytes_per_key = (float)(key_bytes * c.num_kv_heads);

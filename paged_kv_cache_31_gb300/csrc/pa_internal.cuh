@@ -626,10 +626,12 @@ struct TreeParams {
   int64_t* item_cum;  // [items + 1] weight before the item, over all items of a kv head in order
   // Large batches of prompt chunks: sequences of more than kWindowDecodeRows rows go to the prefill kernel
   // (k_prefill_tc.cu, plan as for that kernel: header words, items, marks, list of marked items), the
-  // others to k_window_decode; the tree kernel does the items again that were marked.
+  // others to k_window_decode; the tree kernel does the items again that were marked, and over bf16 pools those
+  // of a (sequence, kv head) whose values are small (small_off: kSmallBlocks words, one of which is set when any
+  // is, and a word for each; 0: none is).
   struct {
     int32_t* plan;  // null: no such batch
-    int64_t items_off, redo_off, redo_list_off;  // words
+    int64_t items_off, redo_off, redo_list_off, small_off;  // words
     int32_t pairs, num_sms;
     float decode_bytes_per_key;  // of a decode-class sequence, all kv heads
   } tc;
@@ -694,6 +696,7 @@ struct WindowLayout {
   int64_t bytes;
 };
 constexpr int32_t kWindowDecodeRows = 16;  // query rows of a kv head up to which a sequence decodes
+constexpr int32_t kSmallBlocks = 64;  // of the plan's launch, at most, that look for small values
 constexpr int32_t kWeightKeys = 256;  // of an item of the weights' tensor-core kernel
 WindowLayout window_layout(int32_t num_seqs, int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
                            int32_t head_dim, int64_t max_keys, int32_t rows_per_item, int32_t key_tile,

@@ -25,7 +25,7 @@ def planned_end(S, T, H, Hkv, D, keys, rows_per_item, key_tile, most_ctas, weigh
     end = up(32 * S) + up(8 * (S + 1)) + up(16 * (grid + 1))  # sequences, weights before them, shares
     end += up(2 * grid * rows_per_item * 8) + up(2 * grid * rows_per_item * D * 4)  # two states a CTA
     items = -(-rows // rows_per_item) + S
-    end += up(16 * items) + up(8 * (items + 1)) + up(4 * (16 + 6 * items))
+    end += up(16 * items) + up(8 * (items + 1)) + up(4 * (16 + 6 * items + 64 + S * Hkv))
     if weights:
         tiles = min(S, T) * -(-keys // 256)
         end += up(4 * T * H) + up(32 * S) + up(16 * tiles) + up(8 * (tiles + 1))

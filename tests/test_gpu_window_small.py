@@ -1,5 +1,5 @@
-"""Small softmax weights in every form of the attention behind a window: what f16 would round to nothing is
-kept."""
+"""Small softmax weights and small values of V in every form of the attention behind a window: what f16
+would round to nothing is kept."""
 import pytest
 import torch
 
@@ -61,4 +61,33 @@ def test_scores_of_any_magnitude(pa, kv, size):
     rows = b.tables[0].long()[up // 16] * 16 + up % 16
     level = (up // 128).float() * 0.11 * size / 16  # 128 * 0.11 / sqrt(128) / ln 2 = 1.8 a tile at size 16
     b.kb.view(-1, 8, 128)[rows] = level.clamp(max=400.0)[:, None, None].expand(-1, 8, 128).to(kv)
+    check(pa, b, expected(b, weight_u=2.0 ** -11, weight_min=2.0 ** -32))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("size", [2.0 ** -12, 1e-6, 1e-9, 1e-20, 1e-36])
+@pytest.mark.parametrize("heads", [slice(None), slice(3, 4)])
+def test_small_values(pa, form, size, heads):
+    """V all below 2^-9, or that of one kv head: as exact as V of any other size."""
+    seqs, H, Hkv = FORMS[form]
+    b = ref.Batch(seqs, H, Hkv, 128, seed=len(form))
+    b.window, b.first = 4, 2  # (few keys: nothing averages out)
+    b.vb[:, :, heads] = (b.vb[:, :, heads].float().clamp(-4, 4) * size).to(BF16)
+    check_bound = dict(weight_u=2.0 ** -11, weight_min=2.0 ** -32)
+    want = expected(b, **check_bound)
+    if heads != slice(None):  # (the other heads' own values below 2^-14 are off by 2^-25)
+        G = H // Hkv
+        other = [h for h in range(H) if h // G != 3]
+        want["out_b"][:, other] += 2.0 ** -25
+    check(pa, b, want)
+
+
+def test_a_prompt_of_few_values(pa):
+    """V of zeros but for a few places is exact in f16 or done again: parts of a tile without any value
+    are neither."""
+    b = ref.Batch([(0, 1300)], 64, 8, 128, seed=1)
+    b.window, b.first = 0, 0
+    b.vb.zero_()
+    b.vb[int(b.tables[0, 2]), 5, 3, 100] = 1e-7
+    b.vb[int(b.tables[0, 7]), 1, 4, 7] = 3.0
     check(pa, b, expected(b, weight_u=2.0 ** -11, weight_min=2.0 ** -32))
