@@ -804,7 +804,7 @@ size_t pa_attention_key_weights_workspace_size(int32_t num_seqs, int64_t num_tok
  * others.  Weights below 2^-126 may count as 0; scale * k_scale >= 2^-100.
  * All other arguments, results and errors as pa_window_attention, and its workspace
  * pa_attention_key_weights_workspace_size(...) bytes (for decoding tokens, whose scores wait there for the
- * log-sum-exps, up to 256 MB).
+ * log-sum-exps, up to 256 MB or 8 KB for each (sequence, kv head), whichever is more).
  */
 pa_status pa_attention_key_weights(const void* q, const void* k_blocks, const void* v_blocks, void* out,
                                    const int32_t* query_start_loc, const int32_t* seq_lens,

@@ -25,7 +25,7 @@ bool decodes(int32_t num_seqs, int64_t num_tokens, int32_t num_kv_heads, int32_t
 }
 
 // Scores of a (sequence, kv head) that the workspace has room for: all keys of a token's heads, up to
-// 256 MB for the batch.
+// 256 MB for the batch or, where that is more, 2048 (8 KB: 512 keys of 4 heads) for each.
 int64_t score_room(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int64_t keys) {
   const int64_t all = std::min(group, 16) * ((keys + 511) / 512 * 512);
   return std::min(all, std::max<int64_t>((1 << 26) / ((int64_t)num_seqs * num_kv_heads), 2048)) / 512 * 512;

@@ -82,3 +82,14 @@ def test_eviction_lists(b):
         assert size(S, Hkv, width, bs) == 4096
     for S, Hkv, width, bs in [(256, 8, 513, 16), (2, 3, 8193, 1), (64, 8, 8192, 16)]:
         assert size(S, Hkv, width, bs) == 4096 + 4 * S * Hkv * width * bs
+
+
+def test_scores_of_decoding_batches(b):
+    """They take 256 MB or 8 KB a (sequence, kv head), whichever is more, beside the planned calls' arrays."""
+    size, plain = b.pa_attention_key_weights_workspace_size, b.pa_window_attention_workspace_size
+    for S, (H, Hkv), width in itertools.product([1, 64, 4000, 16384, 100000], [(32, 8), (64, 64), (128, 1)],
+                                                [4, 256, 100000]):
+        got, units = size(S, S, H, Hkv, 128, width, 16), S * Hkv
+        tiles = S * -(-width * 16 // 256)  # (the plan of a batch with prompt chunks, which this is not)
+        planned = plain(S, S, H, Hkv, 128, width, 16) + 4 * S * H + 32 * S + 24 * tiles + 320000
+        assert got <= max(2 ** 28, 2 ** 13 * units, planned), (S, H, Hkv, width, got)
