@@ -159,6 +159,7 @@ struct Small {
   float lse[16], norm[16];
   float factor[16][16];  // of each CTA's part of a row
   int fail;
+  int nan;  // row0 + 1 of a tile with a row of NaN
 };
 
 template <int D, bool FP8, bool WEIGH, int KIND>
@@ -199,6 +200,7 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
     prefetch_tmap(&tv);
     // (the swizzled tiles need the alignment that the declaration asks for)
     sh.fail = (smem_u32(ring) & 1023u) != 0;
+    sh.nan = 0;
     if (sh.fail) record_error(p.status, PA_ECUDA);
   }
   fence_mbar_init();
@@ -714,6 +716,7 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
         // are added, but nothing to the keys that it does not see, of score -inf)
         const float lse = L == 0.f ? INFINITY : M2 + log2f(total);
         sh.lse[r] = lse == lse ? lse : -FLT_MAX;
+        if (WEIGH && lse != lse) sh.nan = row0 + 1;
         sh.norm[r] = tree_finish(p, kvh, h, t, M, L, rank == 0 && !fail);
       }
     }
@@ -866,6 +869,14 @@ __global__ void __launch_bounds__(Shape<D, FP8, KIND>::NW * 32, Shape<D, FP8, KI
           mbar_wait(&full[warp * NS + (ring_pos + x - x0) % NS], ((ring_pos + x - x0) / NS) & 1u, 100000000ull);
         ring_pos += sent - x0;
       }
+      // a row of NaN spoils all that it sees, keys of score -inf (q or K with an infinity) among them
+      if (sh.nan == row0 + 1 && !fail)
+        for (int r = r0; r < nrow; ++r) {
+          if (sh.lse[r] != -FLT_MAX) continue;
+          const int at = pos_of(r);
+          for (int key = run0 * kBlk + tid; key < min(run1 * kBlk, at + 1); key += NW * 32)
+            if (m.window <= 0 || key > at - m.window || key < p.first) atomicAdd(w + real(key), NAN);
+        }
     }
     // the ring, or the CTA, may go when all have read
     if (reused)
