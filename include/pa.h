@@ -735,7 +735,9 @@ pa_status pa_free_sequences(int32_t* block_tables, int32_t* seq_lens, const int3
  * after an eviction a new token lies at the sequence's new length.
  *
  * As above, another stream's pa_device_status() may clear a recorded error between the launches of a
- * call: it may then write those of its outputs whose indices are valid, nothing outside its arrays.
+ * call: it may then write those of its outputs whose indices are valid, nothing outside its arrays.  An
+ * error that is recorded while an attention call runs (another stream's, or a wait that runs out) may leave
+ * out, lse and the sums in key_weights written in part.  Neither holds of pa_evict_keys.
  */
 
 /* pa_window_attention_workspace_size -- bytes of device workspace pa_window_attention needs for these

@@ -24,10 +24,12 @@
 // together), each for itself: there is no order between them but that the weights are moved when all have
 // read them.
 //
-// What bounds it: memory, at 0.74 of the copy rate (rows of 256 bytes, read and written in places of their own:
-// half of 64 prompts of 2048 to 8192 keys, 720 MB, 144 us, of which the first 16 select; 256 sequences cut by
-// 2 %, e4m3, 112 us for 76); one sequence a chain of latencies (metadata, weights, histogram, places, rows:
-// 10.9 us).
+// What bounds it: memory, with rows of 256 bytes read and written in places of their own at 0.81 of the copy rate
+// (half of 64 prompts of 2048 to 8192 keys, 758 MB with the weights, 138 us, of which the first 16 select), of
+// 128 bytes at 0.77 (256 sequences cut by 2 %, e4m3, 571 MB, 109 us); one sequence a chain of latencies (metadata,
+// weights, histogram, places, rows: 9.7 us).  The form for more than 8192 keys reads the weights again in each pass,
+// one CTA to an SM: 16 prompts of 16384 keys cut to half 154 us for 85; tables and weights of 16384 columns alone
+// make the 256 sequences take it, and 217 us.
 #include <algorithm>
 
 #include "pa_internal.cuh"

@@ -53,8 +53,8 @@
 // Keys are counted without the blocks between the first tokens' and the window's (k_window.cu plans the
 // items), so only block ids, masks and the reference of the weights (kRefBelow) differ; items with V that f16
 // cannot hold, or not closely (k_window.cu looks for that), are done again by k_tree_tc.cuh's kernel.  Measured
-// (us a call): chunks of 257 to 2048 tokens with 58 decoding sequences 564 (even shares on one-SM MMAs with exact
-// V and two terms of P: 709), e4m3 prompts of 700 to 4096 with their weights 394 (408).
+// (us a call): chunks of 257 to 2048 tokens with 58 decoding sequences 549 (564 on another box; even shares on
+// one-SM MMAs with exact V and two terms of P: 709), e4m3 prompts of 700 to 4096 with their weights 395 (408).
 //
 // Every mbarrier wait is bounded; a wait that runs out records PA_ETIMEOUT, raises an abort
 // flag that makes the other roles unwind, and the CTA still frees its tensor memory.  Before

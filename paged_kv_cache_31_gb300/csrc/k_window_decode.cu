@@ -22,13 +22,13 @@
 // thread adds to a key, so the order of the sums is fixed.
 //
 // Where the scores lie in the workspace, K and V leave L2 first: left to itself L2 wrote the scores out
-// before they came back (64 sequences of 512 to 4096 keys: 22 MB written and 21 read beside 624 MB of K and
-// V, 109.6 us; so 101.2).
+// before they came back (64 sequences of 512 to 4096 keys, the same ones again: 22 MB written and 21 read beside
+// 624 MB of K and V, 109.6 us; so 102).
 //
-// What bounds it: the K / V bytes for large batches (64 sequences behind a window of 4096: 158 us, the
-// copy rate; 64 of 512 to 4096 keys with their weights 101 us, 0.93 of it), for small ones a chain of
-// latencies (metadata, table, keys, joins: 1 sequence, window 4096: 11.4 us), over e4m3 pools both (48
-// sequences, window 1024: 22.7 us for 15).
+// What bounds it: the K / V bytes for large batches (64 sequences behind a window of 4096, 1027 MB: 159 us, 0.95
+// of the copy rate; 64 of 512 to 4096 keys with their weights 104 us, 0.90 of it), for small ones a chain of
+// latencies (metadata, table, keys, joins: 1 sequence, window 4096: 11.7 us), over e4m3 pools both (48
+// sequences, window 1024: 24.7 us for 15, or 22.2 from L2 where the same 103 MB are read again).
 #include <algorithm>
 #include <cfloat>
 
